@@ -269,7 +269,7 @@ def _plain_train(s):
     a, b = s["ab"][:, :C].float(), s["ab"][:, C:].float()
     keep, d, beta = torch.sigmoid(-a), torch.sigmoid(a), torch.sigmoid(b)
     # the gradient of h_t: dy_t, and what the next token of the stream keeps of it
-    grad = s["dy"].float()
+    grad = s["dy"].float().clone()
     grad[last] += s["dh_final"][full]
     after = torch.cat([keep[1:], keep[:1]])
     after[last] = 0
