@@ -340,6 +340,127 @@ int la_prefill_segmented(const uint64_t *h_state_ptrs, const void *q, const void
                          int kda, int segments, int dtype, void *workspace,
                          size_t workspace_bytes, uint64_t stream);
 
+/* ---------------------------------------------------------------------------------------------
+ * Gated linear recurrence with one state per channel, and its backward pass:
+ *
+ *   d_t = sigmoid(a_t),  beta_t = sigmoid(b_t),  h_t = (1 - d_t) h_{t-1} + beta_t x_t,  y_t = h_t
+ *
+ * 1 - d = exp(-softplus(a)) and beta are the gates that la_gate_activations makes of the same rows
+ * a | b ("split_prefill.rs", prefill_phase1_proj_batched, "gates"); here they are computed on the way
+ * and never stored. It is the per-channel counterpart of the KDA state update above; the pages have
+ * no such layer.
+ *
+ * h_state_ptrs  DEVICE array of B device pointers; pointer s -> fp32 state [channels] of stream s,
+ *               16-byte aligned, read and advanced in place; no two streams share one. NULL: every
+ *               stream starts from zero and its final state is not kept.
+ * x             [total_tokens][x_stride] (dtype).
+ * ab            [total_tokens][ab_stride] (dtype): a in columns 0 .. channels-1, b in the next ones.
+ * y             [total_tokens][y_stride] (dtype; may not be x or ab).
+ * saved         NULL, or la_gated_scan_saved_bytes(...) bytes (16-byte aligned) that receive what
+ *               the backward pass needs besides x and ab: the state every few tokens, and the
+ *               states that the streams started from.
+ * cu_seqlens    DEVICE int32 [B + 1], or NULL for B streams of total_tokens / B tokens each
+ *               (total_tokens must then be a multiple of B). Unlike in the calls above one bad
+ *               offset stops the whole call: nothing but the workspace is written, and
+ *               la_device_status() reports LA_DEV_BAD_SEQLENS. A zero-length stream leaves its
+ *               state as it is.
+ * workspace     la_gated_scan_workspace_bytes(...) bytes (16-byte aligned), used by this call alone
+ *               until its work is done. It need not be initialised. Calls (and captured graphs) that
+ *               may overlap on the GPU need a workspace each; calls in stream order may share one.
+ * Gates of +-infinity are exact: a = -inf keeps the state, b = -inf adds nothing of a finite x.
+ * States and the scan are fp32; y is rounded once. LA_F32 or LA_BF16; channels and strides multiples
+ * of 16 bytes. Count rule: 1 <= total_tokens <= max_tokens.
+ * ------------------------------------------------------------------------------------------- */
+size_t la_gated_scan_workspace_bytes(int B, int total_tokens, int channels, int dtype);
+size_t la_gated_scan_saved_bytes(int B, int total_tokens, int channels, int dtype);
+int la_gated_scan(const uint64_t *h_state_ptrs, const void *x, const void *ab, void *y, void *saved,
+                  size_t saved_bytes, const int32_t *cu_seqlens, int B, int total_tokens,
+                  int max_tokens, int channels, int64_t x_stride, int64_t ab_stride,
+                  int64_t y_stride, int dtype, void *workspace, size_t workspace_bytes,
+                  uint64_t stream);
+
+/* Backward pass of la_gated_scan. With lam_t the gradient of h_t (dy_t and, but for a stream's last
+ * token, (1 - d_{t+1}) lam_{t+1}; there the gradient of the final state):
+ *   dx = lam beta,  da = -lam h_{t-1} d (1 - d),  db = lam x beta (1 - beta),  dh0 = (1 - d_1) lam_1.
+ * x, ab, cu_seqlens  as the forward call had them; saved as it left it (sizes and dtype the same).
+ * dy            [total_tokens][dy_stride] (dtype).
+ * dh_final_ptrs DEVICE array of B pointers to fp32 [channels] gradients of the final states (read),
+ *               or NULL for zero.
+ * dx            [total_tokens][dx_stride] (dtype), out. dab [total_tokens][dab_stride] (dtype; da and
+ *               db in the columns of a and b), out. Neither may be an input.
+ * dh0_ptrs      DEVICE array of B pointers to fp32 [channels] gradients of the initial states (out;
+ *               may be the buffers of dh_final_ptrs), or NULL. A zero-length stream's dh0 is its
+ *               dh_final.
+ * workspace, errors and counts as for la_gated_scan. The same inputs give the same bits. */
+int la_gated_scan_backward(const void *x, const void *ab, const void *saved, size_t saved_bytes,
+                           const void *dy, const uint64_t *dh_final_ptrs, void *dx, void *dab,
+                           const uint64_t *dh0_ptrs, const int32_t *cu_seqlens, int B,
+                           int total_tokens, int max_tokens, int channels, int64_t x_stride,
+                           int64_t ab_stride, int64_t dy_stride, int64_t dx_stride,
+                           int64_t dab_stride, int dtype, void *workspace, size_t workspace_bytes,
+                           uint64_t stream);
+
+/* One decode step of a gated recurrent layer: one new token for each of B streams through the causal
+ * conv1d + SiLU (as la_conv1d_silu_prefill; its window advances by one row) and one step of the
+ * recurrence above, in one launch. The conv output stays in fp32 on the way.
+ * conv_kernel 0: no convolution, x enters the recurrence as it is (conv_state_ptrs, conv_w and
+ * conv_bias are not read); 1..4 as for la_conv1d_silu_prefill.
+ * conv_state_ptrs, h_state_ptrs  DEVICE arrays of B pointers to [conv_kernel-1][channels] (dtype) and
+ * [channels] (fp32) states, 16-byte aligned, advanced in place; no two streams share one.
+ * x [B][x_stride], ab [B][ab_stride], y [B][y_stride] (y may not be x or ab).
+ * Count rule: 1 <= B <= max_streams. */
+int la_gated_scan_step(const uint64_t *conv_state_ptrs, const uint64_t *h_state_ptrs, const void *x,
+                       const void *ab, const void *conv_w, const void *conv_bias, int conv_kernel,
+                       void *y, int B, int max_streams, int channels, int64_t x_stride,
+                       int64_t ab_stride, int64_t y_stride, int dtype, uint64_t stream);
+
+/* ---------------------------------------------------------------------------------------------
+ * Backward pass of la_conv1d_silu_prefill[_varlen].
+ * conv_state_ptrs   DEVICE array of B pointers to the streams' conv states as they were BEFORE the
+ *                   forward call (which advances them in place: keep a copy). May be NULL when
+ *                   kernel == 1.
+ * x, w, bias        as in the forward call; dout [total_tokens][dout_stride] (dtype).
+ * dstate_final_ptrs DEVICE array of B pointers to [kernel-1][channels] (dtype) gradients of the
+ *                   states that the forward call left (read), or NULL for zero.
+ * dx                [total_tokens][dx_stride] (dtype), out; may not be x or dout.
+ * dw, dbias         fp32 [channels][kernel] and [channels], out (16-byte aligned); summed in a fixed
+ *                   order, so the same inputs give the same bits. dbias may be NULL.
+ * dstate_ptrs       DEVICE array of B pointers to [kernel-1][channels] (dtype) gradients of the
+ *                   initial states (out), or NULL; no buffer of dstate_final_ptrs.
+ * cu_seqlens, B     as for la_gated_scan (NULL: equal streams; a bad offset stops the whole call).
+ * workspace         la_conv1d_silu_backward_workspace_bytes(...) bytes (16-byte aligned).
+ * ------------------------------------------------------------------------------------------- */
+size_t la_conv1d_silu_backward_workspace_bytes(int B, int total_tokens, int channels, int kernel,
+                                               int dtype);
+int la_conv1d_silu_backward(const uint64_t *conv_state_ptrs, const void *x, const void *w,
+                            const void *bias, const void *dout, const uint64_t *dstate_final_ptrs,
+                            void *dx, float *dw, float *dbias, const uint64_t *dstate_ptrs,
+                            const int32_t *cu_seqlens, int B, int total_tokens, int max_tokens,
+                            int channels, int kernel, int64_t x_stride, int64_t dout_stride,
+                            int64_t dx_stride, int dtype, void *workspace, size_t workspace_bytes,
+                            uint64_t stream);
+
+/* ---------------------------------------------------------------------------------------------
+ * Projections of a few tokens with 4-bit weights: y[m][n] = sum_k x[m][k] W[n][k],
+ *   W[n][k] = scales[n][k / group] (q(n, k) - 8),   q(n, k) in 0..15.
+ * The decoding counterpart of la_gemm_bf16 ("split_prefill.rs", prefill_phase1_proj_batched).
+ * x, y    bf16 [M][ldx], [M][ldy]; x and ldx aligned to 16 bytes; y may not overlap x.
+ * q       [N][K/2] bytes, contiguous, 16-byte aligned: eight weights of a row to a little-endian
+ *         32-bit word, weight 2i in bits 4i..4i+3 and weight 2i+1 in bits 16+4i..16+4i+3.
+ * scales  bf16 [N][K/group], contiguous.
+ * group   32, 64 or 128; K a multiple of it. Sums are fp32, y is rounded once, and the order of the
+ *         sums does not depend on M: a row gives the same bits in any batch.
+ * Count rule: 1 <= M <= LA_W4_MAX_ROWS; N, K >= 1. */
+#define LA_W4_MAX_ROWS 32
+int la_w4_matvec(const void *x, const void *q, const void *scales, void *y, int M, int N, int K,
+                 int group, int64_t ldx, int64_t ldy, uint64_t stream);
+
+/* Lays a bf16 weight w [N][ldw] (K columns; finite values) out for la_w4_matvec: scale = the group's
+ * largest magnitude / 7, rounded to bf16; q = 8 + w / scale rounded to nearest (ties to even) and
+ * held to 0..15. A group of zeros has scale 0 and q = 8. */
+int la_w4_quantize(const void *w, void *q, void *scales, int N, int K, int group, int64_t ldw,
+                   uint64_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -22,12 +22,16 @@ __all__ = [
     "l2norm_heads",
     "prefill_workspace_bytes", "gdn_prefill_batched", "gdn_prefill_varlen",
     "gdn_prefill_varlen_noalloc", "kda_prefill",
+    "gated_scan", "gated_scan_backward", "gated_scan_step", "gated_scan_workspace_bytes",
+    "gated_scan_saved_bytes", "conv1d_silu_backward", "conv1d_silu_backward_workspace_bytes",
+    "w4_matvec", "w4_quantize", "LA_W4_MAX_ROWS",
     "pointer_array", "library_path",
 ]
 
 LA_OK, LA_ERR_ARG, LA_ERR_COUNT, LA_ERR_UNSUPPORTED, LA_ERR_CUDA = 0, 1, 2, 3, 4
 LA_F32, LA_BF16 = 0, 1
 LA_DEV_BAD_SEQLENS, LA_DEV_TIMEOUT = 1, 2
+LA_W4_MAX_ROWS = 32
 _CODES = {LA_ERR_ARG: "LA_ERR_ARG", LA_ERR_COUNT: "LA_ERR_COUNT",
           LA_ERR_UNSUPPORTED: "LA_ERR_UNSUPPORTED", LA_ERR_CUDA: "LA_ERR_CUDA"}
 
@@ -81,6 +85,22 @@ _SIGS = {
     "la_decode_workspace_bytes": ([_i32, _i32, _i32, _i32, _i32, _i32], _sz),
     "la_decode_step": ([_vp, _vp, _vp, _vp, _vp, _i32, _vp, _vp, _vp, _i32, _i32, _i32, _i32,
                         _i32, _i32, _i64, _f32, _f32, _i32, _i32, _vp, _sz, _u64], ctypes.c_int),
+    "la_gated_scan_workspace_bytes": ([_i32, _i32, _i32, _i32], _sz),
+    "la_gated_scan_saved_bytes": ([_i32, _i32, _i32, _i32], _sz),
+    "la_gated_scan": ([_vp, _vp, _vp, _vp, _vp, _sz, _vp, _i32, _i32, _i32, _i32, _i64, _i64,
+                       _i64, _i32, _vp, _sz, _u64], ctypes.c_int),
+    "la_gated_scan_backward": ([_vp, _vp, _vp, _sz, _vp, _vp, _vp, _vp, _vp, _vp, _i32, _i32,
+                                _i32, _i32, _i64, _i64, _i64, _i64, _i64, _i32, _vp, _sz, _u64],
+                               ctypes.c_int),
+    "la_gated_scan_step": ([_vp, _vp, _vp, _vp, _vp, _vp, _i32, _vp, _i32, _i32, _i32, _i64, _i64,
+                            _i64, _i32, _u64], ctypes.c_int),
+    "la_conv1d_silu_backward_workspace_bytes": ([_i32, _i32, _i32, _i32, _i32], _sz),
+    "la_conv1d_silu_backward": ([_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i32,
+                                 _i32, _i32, _i32, _i32, _i64, _i64, _i64, _i32, _vp, _sz, _u64],
+                                ctypes.c_int),
+    "la_w4_matvec": ([_vp, _vp, _vp, _vp, _i32, _i32, _i32, _i32, _i64, _i64, _u64],
+                     ctypes.c_int),
+    "la_w4_quantize": ([_vp, _vp, _vp, _i32, _i32, _i32, _i64, _u64], ctypes.c_int),
 }
 
 _lib = None
@@ -377,3 +397,202 @@ def prefill_segmented(h_state_ptrs, q, k, v, gate, beta, out, *, Hk, Hv, dk, dv,
         max_tokens if max_tokens is not None else total, Hk, Hv, dk, dv, _row_stride(q),
         _row_stride(k), _row_stride(v), float(scale), 1 if kda else 0, int(segments),
         _dtype_code(q), _ptr(workspace), ws_bytes, _stream(stream)))
+
+
+def _dtype_arg(dtype) -> int:
+    return dtype if isinstance(dtype, int) else (LA_BF16 if dtype == torch.bfloat16 else LA_F32)
+
+
+def _on_gpu(t) -> torch.device:
+    """The device of `t`, which has to be the current one: streams and launches are its own."""
+    if not t.is_cuda:
+        raise ValueError("expected CUDA tensors")
+    if t.device.index != torch.cuda.current_device():
+        raise ValueError(f"tensors on {t.device}, but the current device is "
+                         f"cuda:{torch.cuda.current_device()}: use torch.cuda.device(...)")
+    return t.device
+
+
+def _matrix(name, t, shape, dtype, device) -> int:
+    """Checks a matrix of dense rows; returns its row stride."""
+    if t.dtype != dtype:
+        raise TypeError(f"{name} is {t.dtype}, expected {dtype}")
+    if t.shape != shape or (t.stride(1) != 1 and shape[1] != 1) or t.device != device:
+        raise ValueError(f"{name}: {tuple(t.shape)} with strides {t.stride()} on {t.device}, "
+                         f"expected {tuple(shape)} with dense rows on {device}")
+    return t.stride(0) if shape[0] > 1 else max(t.stride(0), shape[1])
+
+
+def _dense(name, t, shape, dtype, device):
+    if t.dtype != dtype:
+        raise TypeError(f"{name} is {t.dtype}, expected {dtype}")
+    if t.shape != shape or not t.is_contiguous() or t.device != device:
+        raise ValueError(f"{name}: {tuple(t.shape)} on {t.device}, expected a contiguous "
+                         f"{tuple(shape)} on {device}")
+    return t.data_ptr()
+
+
+def _ptrs(name, t, B, device):
+    """The address of a device array of B pointers (pointer_array), or None."""
+    if t is None:
+        return None
+    if t.dtype not in (torch.int64, torch.uint64):
+        raise TypeError(f"{name} is {t.dtype}, expected the int64 of pointer_array")
+    if t.numel() != B or not t.is_contiguous() or t.device != device:
+        raise ValueError(f"{name}: {t.numel()} pointers on {t.device}, expected {B} on {device}")
+    return t.data_ptr()
+
+
+def _streams(cu_seqlens, B, device):
+    """(address of cu_seqlens or None, number of streams)."""
+    if cu_seqlens is None:
+        return None, 1 if B is None else B
+    n = cu_seqlens.shape[0] - 1
+    if B is not None and B != n:
+        raise ValueError(f"B = {B}, but cu_seqlens has {n} streams")
+    return _dense("cu_seqlens", cu_seqlens, (n + 1,), torch.int32, device), n
+
+
+def _room(name, t, device):
+    """(address, bytes) of a workspace or saved buffer, or (None, 0)."""
+    if t is None:
+        return None, 0
+    if not t.is_contiguous() or t.device != device:
+        raise ValueError(f"{name} must be contiguous and on {device}")
+    return t.data_ptr(), t.numel() * t.element_size()
+
+
+def gated_scan_workspace_bytes(B, total_tokens, channels, dtype) -> int:
+    """Bytes of workspace that gated_scan and gated_scan_backward need."""
+    return int(_load().la_gated_scan_workspace_bytes(B, total_tokens, channels, _dtype_arg(dtype)))
+
+
+def gated_scan_saved_bytes(B, total_tokens, channels, dtype) -> int:
+    """Bytes of the buffer that gated_scan fills for gated_scan_backward."""
+    return int(_load().la_gated_scan_saved_bytes(B, total_tokens, channels, _dtype_arg(dtype)))
+
+
+def gated_scan(h_state_ptrs, x, ab, y, cu_seqlens=None, *, B=None, saved=None, max_tokens=None,
+               workspace=None, stream=None) -> None:
+    """h_t = (1 - sigmoid(a_t)) h_{t-1} + sigmoid(b_t) x_t per channel, y_t = h_t.
+
+    x, y [t][C]; ab [t][2C] holds the gate rows a | b (as gate_activations takes them). Packed
+    streams (cu_seqlens, device int32 [B+1]) or, without cu_seqlens, B equal ones. h_state_ptrs:
+    pointer_array of B fp32 [C] states, advanced in place, or None (from zero, not kept). saved: a
+    buffer of gated_scan_saved_bytes(...) when gated_scan_backward is to follow."""
+    dev = _on_gpu(x)
+    T, C = x.shape
+    cu, B = _streams(cu_seqlens, B, dev)
+    sv, sv_bytes = _room("saved", saved, dev)
+    ws, ws_bytes = _room("workspace", workspace, dev)
+    _check(_load().la_gated_scan(
+        _ptrs("h_state_ptrs", h_state_ptrs, B, dev), x.data_ptr(), ab.data_ptr(), y.data_ptr(), sv,
+        sv_bytes, cu, B, T, T if max_tokens is None else max_tokens, C,
+        _matrix("x", x, (T, C), x.dtype, dev), _matrix("ab", ab, (T, 2 * C), x.dtype, dev),
+        _matrix("y", y, (T, C), x.dtype, dev), _dtype_code(x), ws, ws_bytes, _stream(stream)))
+
+
+def gated_scan_backward(x, ab, saved, dy, dx, dab, cu_seqlens=None, *, B=None, dh_final_ptrs=None,
+                        dh0_ptrs=None, max_tokens=None, workspace=None, stream=None) -> None:
+    """Gradients of gated_scan: dx [t][C] and dab [t][2C] from dy [t][C] and, where given, from the
+    gradients of the final states (dh_final_ptrs, B fp32 [C]; None: zero); the gradients of the
+    initial states go to dh0_ptrs (B fp32 [C]) where given. x, ab, cu_seqlens and B are those of the
+    forward call, saved what it left."""
+    dev = _on_gpu(x)
+    T, C = x.shape
+    cu, B = _streams(cu_seqlens, B, dev)
+    sv, sv_bytes = _room("saved", saved, dev)
+    ws, ws_bytes = _room("workspace", workspace, dev)
+    _check(_load().la_gated_scan_backward(
+        x.data_ptr(), ab.data_ptr(), sv, sv_bytes, dy.data_ptr(),
+        _ptrs("dh_final_ptrs", dh_final_ptrs, B, dev), dx.data_ptr(), dab.data_ptr(),
+        _ptrs("dh0_ptrs", dh0_ptrs, B, dev), cu, B, T, T if max_tokens is None else max_tokens, C,
+        _matrix("x", x, (T, C), x.dtype, dev), _matrix("ab", ab, (T, 2 * C), x.dtype, dev),
+        _matrix("dy", dy, (T, C), x.dtype, dev), _matrix("dx", dx, (T, C), x.dtype, dev),
+        _matrix("dab", dab, (T, 2 * C), x.dtype, dev), _dtype_code(x), ws, ws_bytes,
+        _stream(stream)))
+
+
+def gated_scan_step(h_state_ptrs, x, ab, y, *, conv_state_ptrs=None, conv_w=None, conv_bias=None,
+                    max_streams=None, stream=None) -> None:
+    """One token for each of B streams: conv1d + SiLU on the carried windows (with conv_w [C][K] and
+    conv_state_ptrs to [K-1][C]; without conv_w, x enters as it is), then one step of gated_scan.
+    x, y [B][C], ab [B][2C]; both states advance in place."""
+    dev = _on_gpu(x)
+    B, C = x.shape
+    K = 0
+    if conv_w is not None:
+        K = conv_w.shape[1]
+        _dense("conv_w", conv_w, (C, K), x.dtype, dev)
+        if conv_bias is not None:
+            _dense("conv_bias", conv_bias, (C,), x.dtype, dev)
+    _check(_load().la_gated_scan_step(
+        _ptrs("conv_state_ptrs", conv_state_ptrs, B, dev),
+        _ptrs("h_state_ptrs", h_state_ptrs, B, dev), x.data_ptr(), ab.data_ptr(), _ptr(conv_w),
+        _ptr(conv_bias), K, y.data_ptr(), B, B if max_streams is None else max_streams, C,
+        _matrix("x", x, (B, C), x.dtype, dev), _matrix("ab", ab, (B, 2 * C), x.dtype, dev),
+        _matrix("y", y, (B, C), x.dtype, dev), _dtype_code(x), _stream(stream)))
+
+
+def conv1d_silu_backward_workspace_bytes(B, total_tokens, channels, kernel, dtype) -> int:
+    """Bytes of workspace that conv1d_silu_backward needs."""
+    return int(_load().la_conv1d_silu_backward_workspace_bytes(B, total_tokens, channels, kernel,
+                                                               _dtype_arg(dtype)))
+
+
+def conv1d_silu_backward(conv_state_ptrs, x, w, dout, dx, dw, cu_seqlens=None, *, B=None, bias=None,
+                         dbias=None, dstate_final_ptrs=None, dstate_ptrs=None, max_tokens=None,
+                         workspace=None, stream=None) -> None:
+    """Gradients of conv1d_silu_prefill[_varlen]: dx [t][C] from dout [t][C], dw [C][K] and dbias [C]
+    in fp32, and the gradients of the initial windows (dstate_ptrs, where given).
+
+    conv_state_ptrs: the streams' [K-1][C] windows as they were before the forward call, which
+    advances them in place; dstate_final_ptrs: gradients of the windows it left (None: zero)."""
+    dev = _on_gpu(x)
+    T, C = x.shape
+    K = w.shape[1]
+    cu, B = _streams(cu_seqlens, B, dev)
+    ws, ws_bytes = _room("workspace", workspace, dev)
+    _check(_load().la_conv1d_silu_backward(
+        _ptrs("conv_state_ptrs", conv_state_ptrs, B, dev), x.data_ptr(),
+        _dense("w", w, (C, K), x.dtype, dev),
+        None if bias is None else _dense("bias", bias, (C,), x.dtype, dev), dout.data_ptr(),
+        _ptrs("dstate_final_ptrs", dstate_final_ptrs, B, dev), dx.data_ptr(),
+        _dense("dw", dw, (C, K), torch.float32, dev),
+        None if dbias is None else _dense("dbias", dbias, (C,), torch.float32, dev),
+        _ptrs("dstate_ptrs", dstate_ptrs, B, dev), cu, B, T, T if max_tokens is None else max_tokens,
+        C, K, _matrix("x", x, (T, C), x.dtype, dev), _matrix("dout", dout, (T, C), x.dtype, dev),
+        _matrix("dx", dx, (T, C), x.dtype, dev), _dtype_code(x), ws, ws_bytes, _stream(stream)))
+
+
+def w4_quantize(w, q=None, scales=None, *, group=128, stream=None):
+    """Lays a bf16 weight w [N][K] out for w4_matvec: (q uint8 [N][K/2], scales bf16 [N][K/group])."""
+    dev = _on_gpu(w)
+    N, K = w.shape
+    if q is None:
+        q = torch.empty(N, K // 2, dtype=torch.uint8, device=dev)
+    if scales is None:
+        scales = torch.empty(N, K // group, dtype=torch.bfloat16, device=dev)
+    _check(_load().la_w4_quantize(
+        w.data_ptr(), _dense("q", q, (N, K // 2), torch.uint8, dev),
+        _dense("scales", scales, (N, K // group), torch.bfloat16, dev), N, K, group,
+        _matrix("w", w, (N, K), torch.bfloat16, dev), _stream(stream)))
+    return q, scales
+
+
+def w4_matvec(x, q, scales, y=None, *, stream=None):
+    """y = x W^T for 1..LA_W4_MAX_ROWS bf16 rows x [M][K] and a weight that w4_quantize laid out
+    (q [N][K/2], scales [N][K/group]); y [M][N] bf16 (allocated when None). Returns y."""
+    dev = _on_gpu(x)
+    M, K = x.shape
+    N, groups = scales.shape
+    if groups == 0 or K % groups:
+        raise ValueError(f"{groups} scales for each {K} inputs")
+    if y is None:
+        y = torch.empty(M, N, dtype=torch.bfloat16, device=dev)
+    _check(_load().la_w4_matvec(
+        x.data_ptr(), _dense("q", q, (N, K // 2), torch.uint8, dev),
+        _dense("scales", scales, (N, groups), torch.bfloat16, dev), y.data_ptr(), M, N, K,
+        K // groups, _matrix("x", x, (M, K), torch.bfloat16, dev),
+        _matrix("y", y, (M, N), torch.bfloat16, dev), _stream(stream)))
+    return y

@@ -152,6 +152,51 @@ int conv_common(const void *x, const void *w, const void *bias, const void *out,
     return LA_OK;
 }
 
+int check_channels(int channels, int dtype) {
+    if (channels <= 0) return fail(LA_ERR_ARG, "channels must be positive (got %d)", channels);
+    if (channels % vec_elems(dtype))
+        return fail(LA_ERR_ARG, "channels (%d) is not a multiple of 16 bytes", channels);
+    return LA_OK;
+}
+
+// Counts, streams and channels of the calls over packed (cu_seqlens) or equal (NULL) streams.
+int packed_common(const int32_t *cu_seqlens, int B, int total_tokens, int max_tokens, int channels,
+                  int dtype, int *T_each) {
+    if (total_tokens <= 0 || total_tokens > max_tokens)
+        return fail(LA_ERR_COUNT, "call of %d tokens does not fit max_tokens %d", total_tokens,
+                    max_tokens);
+    LA_TRY(check_dtype(dtype));
+    if (B < 1) return fail(LA_ERR_ARG, "B must be >= 1 (got %d)", B);
+    if (!cu_seqlens && total_tokens % B)
+        return fail(LA_ERR_ARG, "cu_seqlens NULL: total_tokens (%d) is not a multiple of B (%d)",
+                    total_tokens, B);
+    *T_each = cu_seqlens ? 0 : total_tokens / B;
+    return check_channels(channels, dtype);
+}
+
+int check_bytes(size_t bytes, size_t need, const char *name) {
+    if (bytes < need)
+        return fail(LA_ERR_ARG, "%s of %zu bytes is below the %zu required", name, bytes, need);
+    return LA_OK;
+}
+
+int check_workspace(const void *workspace, size_t bytes, size_t need) {
+    LA_TRY(check_bytes(bytes, need, "workspace"));
+    if (need && (!workspace || !aligned16(workspace)))
+        return fail(LA_ERR_ARG, "workspace is NULL or not 16-byte aligned");
+    return LA_OK;
+}
+
+int w4_common(const void *q, const void *scales, int K, int group) {
+    if (group != 32 && group != 64 && group != 128)
+        return fail(LA_ERR_UNSUPPORTED, "group %d: compiled for 32, 64 and 128", group);
+    if (K % group) return fail(LA_ERR_ARG, "K (%d) is not a multiple of the group (%d)", K, group);
+    LA_TRY(check_act_ptr(q, "q"));
+    if (!scales || (reinterpret_cast<uintptr_t>(scales) & 1u))
+        return fail(LA_ERR_ARG, "scales is NULL or misaligned");
+    return LA_OK;
+}
+
 // Shared checks of the three recurrence calls.
 int rec_common(const uint64_t *h_state_ptrs, const void *q, const void *k, const void *v,
                const float *g, const float *beta, const void *out, int B, int Hk, int Hv,
@@ -664,6 +709,182 @@ int la_prefill_segmented(const uint64_t *h_state_ptrs, const void *q, const void
     LA_TRY(get_status(&a.status));
     a.wait_ns = wait_limit_ns();
     return launch_result([&] { return la::launch_segmented(a, segments, as_stream(stream)); }, "segmented scan launch");
+}
+
+size_t la_gated_scan_workspace_bytes(int B, int total_tokens, int channels, int dtype) {
+    if (B < 1 || total_tokens < 1 || channels < 1) return 0;
+    return la::gated_scan_workspace_bytes(B, total_tokens, channels, dtype);
+}
+
+size_t la_gated_scan_saved_bytes(int B, int total_tokens, int channels, int dtype) {
+    if (B < 1 || total_tokens < 1 || channels < 1) return 0;
+    return la::gated_scan_saved_bytes(B, total_tokens, channels, dtype);
+}
+
+int la_gated_scan(const uint64_t *h_state_ptrs, const void *x, const void *ab, void *y, void *saved,
+                  size_t saved_bytes, const int32_t *cu_seqlens, int B, int total_tokens,
+                  int max_tokens, int channels, int64_t x_stride, int64_t ab_stride,
+                  int64_t y_stride, int dtype, void *workspace, size_t workspace_bytes,
+                  uint64_t stream) {
+    int T_each = 0;
+    LA_TRY(packed_common(cu_seqlens, B, total_tokens, max_tokens, channels, dtype, &T_each));
+    LA_TRY(check_act_ptr(x, "x"));
+    LA_TRY(check_act_ptr(ab, "ab"));
+    LA_TRY(check_act_ptr(y, "y"));
+    LA_TRY(check_act_ptr(saved, "saved", true));
+    LA_TRY(check_stride(x_stride, channels, dtype, "x_stride"));
+    LA_TRY(check_stride(ab_stride, 2 * (int64_t)channels, dtype, "ab_stride"));
+    LA_TRY(check_stride(y_stride, channels, dtype, "y_stride"));
+    if (y == x || y == ab) return fail(LA_ERR_ARG, "y may not alias x or ab");
+    if (saved) LA_TRY(check_bytes(saved_bytes, la_gated_scan_saved_bytes(B, total_tokens, channels, dtype), "saved"));
+    LA_TRY(check_workspace(workspace, workspace_bytes,
+                           la_gated_scan_workspace_bytes(B, total_tokens, channels, dtype)));
+    la::GatedScanArgs a{};
+    a.h_ptrs = h_state_ptrs; a.x = x; a.ab = ab; a.y = y; a.saved = static_cast<float *>(saved);
+    a.cu = cu_seqlens; a.B = B; a.T_each = T_each; a.total = total_tokens; a.channels = channels;
+    a.x_stride = x_stride; a.ab_stride = ab_stride; a.y_stride = y_stride; a.dtype = dtype;
+    a.workspace = workspace;
+    LA_TRY(get_status(&a.status));
+    a.wait_ns = wait_limit_ns();
+    a.debug_stall = debug_stall();
+    return launch_result([&] { return la::launch_gated_scan(a, as_stream(stream)); }, "gated scan launch");
+}
+
+int la_gated_scan_backward(const void *x, const void *ab, const void *saved, size_t saved_bytes,
+                           const void *dy, const uint64_t *dh_final_ptrs, void *dx, void *dab,
+                           const uint64_t *dh0_ptrs, const int32_t *cu_seqlens, int B,
+                           int total_tokens, int max_tokens, int channels, int64_t x_stride,
+                           int64_t ab_stride, int64_t dy_stride, int64_t dx_stride,
+                           int64_t dab_stride, int dtype, void *workspace, size_t workspace_bytes,
+                           uint64_t stream) {
+    int T_each = 0;
+    LA_TRY(packed_common(cu_seqlens, B, total_tokens, max_tokens, channels, dtype, &T_each));
+    LA_TRY(check_act_ptr(x, "x"));
+    LA_TRY(check_act_ptr(ab, "ab"));
+    LA_TRY(check_act_ptr(saved, "saved"));
+    LA_TRY(check_act_ptr(dy, "dy"));
+    LA_TRY(check_act_ptr(dx, "dx"));
+    LA_TRY(check_act_ptr(dab, "dab"));
+    LA_TRY(check_stride(x_stride, channels, dtype, "x_stride"));
+    LA_TRY(check_stride(ab_stride, 2 * (int64_t)channels, dtype, "ab_stride"));
+    LA_TRY(check_stride(dy_stride, channels, dtype, "dy_stride"));
+    LA_TRY(check_stride(dx_stride, channels, dtype, "dx_stride"));
+    LA_TRY(check_stride(dab_stride, 2 * (int64_t)channels, dtype, "dab_stride"));
+    for (const void *out : {static_cast<const void *>(dx), static_cast<const void *>(dab)})
+        if (out == x || out == ab || out == dy || out == saved)
+            return fail(LA_ERR_ARG, "dx and dab may not alias an input");
+    if (dx == dab) return fail(LA_ERR_ARG, "dx may not alias dab");
+    LA_TRY(check_bytes(saved_bytes, la_gated_scan_saved_bytes(B, total_tokens, channels, dtype), "saved"));
+    LA_TRY(check_workspace(workspace, workspace_bytes,
+                           la_gated_scan_workspace_bytes(B, total_tokens, channels, dtype)));
+    la::GatedScanBwdArgs a{};
+    a.x = x; a.ab = ab; a.saved = static_cast<const float *>(saved); a.dy = dy;
+    a.dh_final_ptrs = dh_final_ptrs; a.dx = dx; a.dab = dab; a.dh0_ptrs = dh0_ptrs;
+    a.cu = cu_seqlens; a.B = B; a.T_each = T_each; a.total = total_tokens; a.channels = channels;
+    a.x_stride = x_stride; a.ab_stride = ab_stride; a.dy_stride = dy_stride;
+    a.dx_stride = dx_stride; a.dab_stride = dab_stride; a.dtype = dtype;
+    a.workspace = workspace;
+    LA_TRY(get_status(&a.status));
+    a.wait_ns = wait_limit_ns();
+    a.debug_stall = debug_stall();
+    return launch_result([&] { return la::launch_gated_scan_backward(a, as_stream(stream)); },
+                         "gated scan backward launch");
+}
+
+int la_gated_scan_step(const uint64_t *conv_state_ptrs, const uint64_t *h_state_ptrs, const void *x,
+                       const void *ab, const void *conv_w, const void *conv_bias, int conv_kernel,
+                       void *y, int B, int max_streams, int channels, int64_t x_stride,
+                       int64_t ab_stride, int64_t y_stride, int dtype, uint64_t stream) {
+    if (B < 1 || B > max_streams)
+        return fail(LA_ERR_COUNT, "decode step of %d streams does not fit max_streams %d", B,
+                    max_streams);
+    LA_TRY(check_dtype(dtype));
+    if (conv_kernel < 0 || conv_kernel > 4)
+        return fail(LA_ERR_UNSUPPORTED, "conv kernel %d outside the compiled 0..4", conv_kernel);
+    LA_TRY(check_channels(channels, dtype));
+    if (!h_state_ptrs) return fail(LA_ERR_ARG, "h_state_ptrs is NULL");
+    LA_TRY(check_act_ptr(x, "x"));
+    LA_TRY(check_act_ptr(ab, "ab"));
+    LA_TRY(check_act_ptr(y, "y"));
+    if (conv_kernel > 0) {
+        LA_TRY(check_act_ptr(conv_w, "conv_w"));
+        LA_TRY(check_act_ptr(conv_bias, "conv_bias", true));
+        if (conv_kernel > 1 && !conv_state_ptrs) return fail(LA_ERR_ARG, "conv_state_ptrs is NULL");
+    }
+    LA_TRY(check_stride(x_stride, channels, dtype, "x_stride"));
+    LA_TRY(check_stride(ab_stride, 2 * (int64_t)channels, dtype, "ab_stride"));
+    LA_TRY(check_stride(y_stride, channels, dtype, "y_stride"));
+    if (y == x || y == ab) return fail(LA_ERR_ARG, "y may not alias x or ab");
+    la::GatedStepArgs a{conv_state_ptrs, h_state_ptrs, x, ab, conv_w, conv_bias, conv_kernel, y, B,
+                        channels, x_stride, ab_stride, y_stride, dtype};
+    return launch_result([&] { return la::launch_gated_step(a, as_stream(stream)); }, "gated step launch");
+}
+
+size_t la_conv1d_silu_backward_workspace_bytes(int B, int total_tokens, int channels, int kernel,
+                                               int dtype) {
+    if (B < 1 || total_tokens < 1 || channels < 1 || kernel < 1) return 0;
+    return la::conv_backward_workspace_bytes(B, total_tokens, channels, kernel, dtype);
+}
+
+int la_conv1d_silu_backward(const uint64_t *conv_state_ptrs, const void *x, const void *w,
+                            const void *bias, const void *dout, const uint64_t *dstate_final_ptrs,
+                            void *dx, float *dw, float *dbias, const uint64_t *dstate_ptrs,
+                            const int32_t *cu_seqlens, int B, int total_tokens, int max_tokens,
+                            int channels, int kernel, int64_t x_stride, int64_t dout_stride,
+                            int64_t dx_stride, int dtype, void *workspace, size_t workspace_bytes,
+                            uint64_t stream) {
+    int T_each = 0;
+    LA_TRY(packed_common(cu_seqlens, B, total_tokens, max_tokens, channels, dtype, &T_each));
+    LA_TRY(conv_common(x, w, bias, dx, channels, kernel, x_stride, dx_stride, dtype));
+    LA_TRY(check_act_ptr(w, "w"));
+    LA_TRY(check_act_ptr(dout, "dout"));
+    LA_TRY(check_stride(dout_stride, channels, dtype, "dout_stride"));
+    LA_TRY(check_act_ptr(dw, "dw"));
+    LA_TRY(check_act_ptr(dbias, "dbias", true));
+    if (kernel > 1 && !conv_state_ptrs) return fail(LA_ERR_ARG, "conv_state_ptrs is NULL");
+    if (dx == dout) return fail(LA_ERR_ARG, "dx may not alias dout");
+    if (dstate_ptrs && dstate_ptrs == dstate_final_ptrs)
+        return fail(LA_ERR_ARG, "dstate_ptrs may not be dstate_final_ptrs");
+    LA_TRY(check_workspace(workspace, workspace_bytes,
+                           la_conv1d_silu_backward_workspace_bytes(B, total_tokens, channels, kernel, dtype)));
+    la::ConvBwdArgs a{};
+    a.state_ptrs = conv_state_ptrs; a.x = x; a.w = w; a.bias = bias; a.dout = dout;
+    a.dstate_final_ptrs = kernel > 1 ? dstate_final_ptrs : nullptr;
+    a.dx = dx; a.dw = dw; a.dbias = dbias;
+    a.dstate_ptrs = kernel > 1 ? dstate_ptrs : nullptr;
+    a.cu = cu_seqlens; a.B = B; a.T_each = T_each; a.total = total_tokens;
+    a.channels = channels; a.kernel = kernel;
+    a.x_stride = x_stride; a.dout_stride = dout_stride; a.dx_stride = dx_stride; a.dtype = dtype;
+    a.workspace = workspace;
+    LA_TRY(get_status(&a.status));
+    return launch_result([&] { return la::launch_conv1d_silu_backward(a, as_stream(stream)); },
+                         "conv1d_silu backward launch");
+}
+
+int la_w4_matvec(const void *x, const void *q, const void *scales, void *y, int M, int N, int K,
+                 int group, int64_t ldx, int64_t ldy, uint64_t stream) {
+    if (M < 1 || M > LA_W4_MAX_ROWS || N < 1 || K < 1)
+        return fail(LA_ERR_COUNT, "w4 matvec of %d rows x %d x %d (1..%d rows)", M, N, K, LA_W4_MAX_ROWS);
+    LA_TRY(w4_common(q, scales, K, group));
+    LA_TRY(check_act_ptr(x, "x"));
+    if (!y || (reinterpret_cast<uintptr_t>(y) & 1u)) return fail(LA_ERR_ARG, "y is NULL or misaligned");
+    LA_TRY(check_stride(ldx, K, LA_BF16, "ldx"));
+    if (ldy < N) return fail(LA_ERR_ARG, "ldy (%lld) is smaller than N (%d)", (long long)ldy, N);
+    const char *xb = static_cast<const char *>(x), *xe = xb + ((M - 1) * ldx + K) * 2;
+    const char *yb = static_cast<const char *>(y), *ye = yb + ((M - 1) * ldy + N) * 2;
+    if (xb < ye && yb < xe) return fail(LA_ERR_ARG, "y may not overlap x");
+    la::W4Args a{x, q, scales, y, M, N, K, group, ldx, ldy};
+    return launch_result([&] { return la::launch_w4_matvec(a, as_stream(stream)); }, "w4 matvec launch");
+}
+
+int la_w4_quantize(const void *w, void *q, void *scales, int N, int K, int group, int64_t ldw,
+                   uint64_t stream) {
+    if (N < 1 || K < 1) return fail(LA_ERR_COUNT, "w4 quantize of %d x %d", N, K);
+    LA_TRY(w4_common(q, scales, K, group));
+    LA_TRY(check_act_ptr(w, "w"));
+    LA_TRY(check_stride(ldw, K, LA_BF16, "ldw"));
+    la::W4QuantArgs a{w, q, scales, N, K, group, ldw};
+    return launch_result([&] { return la::launch_w4_quantize(a, as_stream(stream)); }, "w4 quantize launch");
 }
 
 }  // extern "C"

@@ -154,6 +154,92 @@ int segmented_plan_segments(int total, int requested);
 size_t segmented_workspace_bytes(int total, int Hv, int segments);
 cudaError_t launch_segmented(const RecArgs &a, int segments, cudaStream_t st);
 
+// Gated linear recurrence with one state per channel (gated_scan.cu): x [total][x_stride],
+// ab [total][ab_stride] (a in columns 0.., b from column `channels`), y [total][y_stride].
+struct GatedScanArgs {
+    const uint64_t *h_ptrs;  // B fp32 states [channels], in place; nullptr: from zero, not kept
+    const void *x, *ab;
+    void *y;
+    float *saved;  // states for the backward pass, or nullptr
+    const int32_t *cu;  // nullptr: B streams of T_each tokens
+    int B, T_each, total, channels;
+    int64_t x_stride, ab_stride, y_stride;
+    int dtype;
+    void *workspace;
+    int *status;
+    uint64_t wait_ns;  // limit of the kernel's bounded waits (0: the 2 s default)
+    int debug_stall;   // test knob: one wait for a tile that nobody publishes
+};
+struct GatedScanBwdArgs {
+    const void *x, *ab;
+    const float *saved;
+    const void *dy;
+    const uint64_t *dh_final_ptrs;  // gradients of the final states, or nullptr (zero)
+    void *dx, *dab;
+    const uint64_t *dh0_ptrs;  // gradients of the initial states (out), or nullptr
+    const int32_t *cu;
+    int B, T_each, total, channels;
+    int64_t x_stride, ab_stride, dy_stride, dx_stride, dab_stride;
+    int dtype;
+    void *workspace;
+    int *status;
+    uint64_t wait_ns;
+    int debug_stall;
+};
+size_t gated_scan_workspace_bytes(int B, int total, int channels, int dtype);
+size_t gated_scan_saved_bytes(int B, int total, int channels, int dtype);
+cudaError_t launch_gated_scan(const GatedScanArgs &a, cudaStream_t st);
+cudaError_t launch_gated_scan_backward(const GatedScanBwdArgs &a, cudaStream_t st);
+
+// One token per stream: conv1d + SiLU on the carried window (conv_kernel 0: none), then the
+// recurrence above (gated_step.cu).
+struct GatedStepArgs {
+    const uint64_t *conv_state_ptrs, *h_ptrs;
+    const void *x, *ab, *conv_w, *conv_bias;
+    int conv_kernel;
+    void *y;
+    int B, channels;
+    int64_t x_stride, ab_stride, y_stride;
+    int dtype;
+};
+cudaError_t launch_gated_step(const GatedStepArgs &a, cudaStream_t st);
+
+// Backward pass of conv1d + SiLU (conv1d_backward.cu).
+struct ConvBwdArgs {
+    const uint64_t *state_ptrs;  // B conv states as they were before the forward pass
+    const void *x, *w, *bias, *dout;
+    const uint64_t *dstate_final_ptrs;  // gradients of the states the forward pass left, or nullptr
+    void *dx;
+    float *dw, *dbias;            // dbias may be nullptr
+    const uint64_t *dstate_ptrs;  // gradients of state_ptrs' states (out), or nullptr
+    const int32_t *cu;
+    int B, T_each, total, channels, kernel;
+    int64_t x_stride, dout_stride, dx_stride;
+    int dtype;
+    void *workspace;
+    int *status;
+};
+size_t conv_backward_workspace_bytes(int B, int total, int channels, int kernel, int dtype);
+cudaError_t launch_conv1d_silu_backward(const ConvBwdArgs &a, cudaStream_t st);
+
+// Products of a few bf16 rows with 4-bit weights (w4.cu): y [M][ldy] = x [M][ldx] W^T,
+// W[n][k] = scales[n][k / group] (q(n, k) - 8); q [N][K / 2] in the layout of la_w4_quantize.
+constexpr int kW4MaxRows = 32;
+struct W4Args {
+    const void *x, *q, *scales;
+    void *y;
+    int M, N, K, group;
+    int64_t ldx, ldy;
+};
+cudaError_t launch_w4_matvec(const W4Args &a, cudaStream_t st);
+struct W4QuantArgs {
+    const void *w;
+    void *q, *scales;
+    int N, K, group;
+    int64_t ldw;
+};
+cudaError_t launch_w4_quantize(const W4QuantArgs &a, cudaStream_t st);
+
 // Encodes a 2-D tiled TMA map (a CUtensorMap, 64-byte aligned storage of 128 bytes) of a
 // row-major bf16 matrix [rows][cols] with row stride ld elements, boxes of box_rows x box_cols,
 // optional 128-byte swizzle; out-of-range elements of a box read as zero. False on failure.
