@@ -389,8 +389,7 @@ int la_gated_scan(const uint64_t *h_state_ptrs, const void *x, const void *ab, v
  * dx            [total_tokens][dx_stride] (dtype), out. dab [total_tokens][dab_stride] (dtype; da and
  *               db in the columns of a and b), out. Neither may be an input.
  * dh0_ptrs      DEVICE array of B pointers to fp32 [channels] gradients of the initial states (out;
- *               may be the buffers of dh_final_ptrs), or NULL. A zero-length stream's dh0 is its
- *               dh_final.
+ *               no buffer of dh_final_ptrs), or NULL. A zero-length stream's dh0 is its dh_final.
  * workspace, errors and counts as for la_gated_scan. The same inputs give the same bits. */
 int la_gated_scan_backward(const void *x, const void *ab, const void *saved, size_t saved_bytes,
                            const void *dy, const uint64_t *dh_final_ptrs, void *dx, void *dab,

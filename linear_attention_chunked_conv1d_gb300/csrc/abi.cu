@@ -774,6 +774,8 @@ int la_gated_scan_backward(const void *x, const void *ab, const void *saved, siz
         if (out == x || out == ab || out == dy || out == saved)
             return fail(LA_ERR_ARG, "dx and dab may not alias an input");
     if (dx == dab) return fail(LA_ERR_ARG, "dx may not alias dab");
+    if (dh0_ptrs && dh0_ptrs == dh_final_ptrs)
+        return fail(LA_ERR_ARG, "dh0_ptrs may not be dh_final_ptrs");
     LA_TRY(check_bytes(saved_bytes, la_gated_scan_saved_bytes(B, total_tokens, channels, dtype), "saved"));
     LA_TRY(check_workspace(workspace, workspace_bytes,
                            la_gated_scan_workspace_bytes(B, total_tokens, channels, dtype)));

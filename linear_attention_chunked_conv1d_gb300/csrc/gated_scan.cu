@@ -8,111 +8,809 @@
 // gradient of the stream's final state),
 //   lam_t = dy_t + m_{t+1},  m_t = (1 - d_t) lam_t,  dh_0 = m at the stream's first token,
 //   dx = lam beta,  db = lam x beta (1 - beta),  da = -lam h_{t-1} d (1 - d).
-// h_{t-1} is computed again from the states that the forward pass saved every kTile tokens.
+// h_{t-1} is computed again from the states that the forward pass saved.
+//
+// Both are HBM-bound: 4 activations a (token, channel) forward, 7 backward, a few tens of
+// instructions on them. One launch reads every input once, whatever the streams' lengths:
+//  - The packed rows are cut into tiles of L tokens x 32 channels, regardless of where streams meet.
+//    A tile maps the state (or, backward, the gradient m) that reaches it to the one that leaves it:
+//    h -> h - D h + H. D = 1 - prod (1 - d) is carried instead of the product, for the reason in
+//    gated.cuh. Where a stream starts inside the tile, what comes from before is dropped.
+//  - Tiles of a channel group are chained along the sequence. A block publishes its tile's (D, H) as
+//    soon as it has them, finds the nearest earlier tile whose outgoing state is known, and applies
+//    the maps in between to that state, oldest first. The state that leaves a tile is thus the same
+//    expression, evaluated in the same order, wherever that search ended: results do not depend on
+//    timing. Tiles are handed out in chain order by a counter, so a tile's predecessors are always
+//    done or running and no block waits for one that has not started; the waits are bounded.
+//  - Narrow, long tiles keep that search short: blocks at work / channel groups tiles of a chain are
+//    in flight at a time, 5 at 2048 channels (128-channel tiles of 64 tokens: 19, and the whole scan
+//    was bound by it).
+//  - Blocks are persistent. Tiles come by TMA into a ring in shared memory and are worked on in
+//    registers, so a tile's place in the ring is free again, and the next copy under way, while the
+//    tile waits for its state.
+#include <cuda.h>
+
 #include "gated.cuh"
 #include "launch.h"
+#include "tc.cuh"
 
 namespace la {
 
 namespace {
 
-constexpr int kTile = 64;       // tokens between two saved states (at packed positions 0, 64, ...)
-constexpr int kThreads = 128;   // channels per block
+constexpr int kWarps = 8;
+constexpr int kThreads = 32 * kWarps;
+constexpr int kLoader = 3;   // the warp that takes tiles and starts their copies
+constexpr int kWidth = 32;   // channels of a tile: 8 lanes of 4; the other 4 lanes' worth of a warp
+constexpr int kRuns = 4 * kWarps;  // is along the tokens, in runs of S
+constexpr uint64_t kWaitNs = 2000000000ull;
 
-struct Ctl {
-    int bad;  // an offset of cu_seqlens is out of order: no stream runs
+// Tokens of a run, and the ring's depth. What a thread keeps of a tile across the wait for its state
+// is 2 registers a (token, channel) forward and 3 to 5 backward; two blocks on an SM leave 128
+// registers a thread, which these fill. Two blocks' rings take 192 KB of shared memory.
+template <typename T, bool BWD> struct Shape {
+    static constexpr int kIn = BWD ? 4 : 3;                              // x, a, b (, dy)
+    static constexpr int S = sizeof(T) == 2 ? (BWD ? 4 : 8) : (BWD ? 2 : 4);
+    static constexpr int L = S * kRuns;
+    static constexpr int kPlane = L * kWidth * (int)sizeof(T);           // bytes of one input's tile
+    static constexpr int kStage = kIn * kPlane;                          // 48 KB forward, 32 KB backward
+    static constexpr int kStages = BWD ? 3 : 2;
+    // A slot is read until its tile is done, one tile longer than its copies are.
+    static constexpr int kSlots = kStages + 1;
 };
 
-__global__ void scan_init_kernel(const int32_t *cu, int B, int total, Ctl *ctl, int *status) {
+// Tokens between two saved states (at packed positions 0, kSave, 2 kSave, ...): the backward tile.
+template <typename T> constexpr int kSave = Shape<T, true>::L;
+
+// What lies in the workspace before the tiles' words.
+struct Ctl {
+    int bad;          // an offset of cu_seqlens is out of order: no stream runs
+    int abort;        // a wait ran out: every block leaves
+    unsigned ticket;  // tiles handed out
+    int pad;
+};
+
+// A word of the chains that nobody has written. No value is: arithmetic makes no NaN of this pattern.
+constexpr uint32_t kUnwritten = 0xffffffffu;
+
+struct Chain {
+    Ctl *ctl;
+    float *D, *H, *out;  // [tiles][groups][32]: the tile's map, the state that leaves it
+    int tiles, groups;
+};
+
+template <typename T, bool BWD> Chain make_chain(void *workspace, int total, int channels) {
+    Chain c;
+    c.tiles = (total + Shape<T, BWD>::L - 1) / Shape<T, BWD>::L;
+    c.groups = (channels + kWidth - 1) / kWidth;
+    const int64_t words = (int64_t)c.tiles * c.groups * kWidth;
+    c.ctl = static_cast<Ctl *>(workspace);
+    c.D = reinterpret_cast<float *>(c.ctl + 1);
+    c.H = c.D + words;
+    c.out = c.H + words;
+    return c;
+}
+
+template <typename T, bool BWD> size_t chain_bytes(int total, int channels) {
+    const Chain c = make_chain<T, BWD>(nullptr, total, channels);
+    return sizeof(Ctl) + (size_t)c.tiles * c.groups * kWidth * 12;
+}
+
+// Clears the chains; block 0 also looks at every offset.
+__global__ void chain_init_kernel(const int32_t *cu, int B, int total, Chain c, int *status) {
+    const int64_t quads = (int64_t)c.tiles * c.groups * kWidth * 3 / 4;
+    uint4 *p = reinterpret_cast<uint4 *>(c.D);
+    for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < quads; i += (int64_t)gridDim.x * blockDim.x)
+        p[i] = make_uint4(kUnwritten, kUnwritten, kUnwritten, kUnwritten);
+    if (blockIdx.x) return;
     int bad = 0;
-    if (threadIdx.x == 0) bad = cu[0] != 0 || cu[B] != total;
-    for (int s = threadIdx.x; s < B; s += blockDim.x) bad |= cu[s + 1] < cu[s];
+    if (cu) {
+        if (threadIdx.x == 0) bad = cu[0] != 0 || cu[B] != total;
+        for (int s = threadIdx.x; s < B; s += blockDim.x) bad |= cu[s + 1] < cu[s];
+    }
     bad = __syncthreads_or(bad);
     if (threadIdx.x == 0) {
-        ctl->bad = bad;
+        *c.ctl = Ctl{bad, 0, 0u, 0};
         if (bad) raise_status(status, LA_DEV_BAD_SEQLENS);
     }
 }
 
-template <typename T>
-__global__ void __launch_bounds__(kThreads) scan_kernel(const GatedScanArgs a, const Ctl *ctl) {
-    const int c = blockIdx.x * kThreads + threadIdx.x, s = blockIdx.y;
-    if (c >= a.channels || (a.cu && ctl->bad)) return;
-    const int t0 = a.cu ? a.cu[s] : s * a.T_each, t1 = a.cu ? a.cu[s + 1] : t0 + a.T_each;
-    const T *x = (const T *)a.x, *ab = (const T *)a.ab;
-    T *y = (T *)a.y;
-    float *h0 = a.h_ptrs ? reinterpret_cast<float *>(a.h_ptrs[s]) + c : nullptr;
-    float h = h0 ? *h0 : 0.f;
-    const int tiles = (a.total + kTile - 1) / kTile;
-    if (a.saved) a.saved[((int64_t)tiles + s) * a.channels + c] = h;
-    for (int t = t0; t < t1; ++t) {
-        if (a.saved && t % kTile == 0) a.saved[(int64_t)(t / kTile) * a.channels + c] = h;
-        float d, beta;
-        gates(to_f(ab[t * a.ab_stride + c]), to_f(ab[t * a.ab_stride + a.channels + c]), d, beta);
-        h = gated_update(h, d, beta * to_f(x[t * a.x_stride + c]));
-        y[t * a.y_stride + c] = from_f<T>(h);
+// Where the streams start and end in the packed rows.
+struct Streams {
+    const int32_t *cu;  // or nullptr: B streams of T_each tokens
+    int B, T_each, total;
+    __device__ __forceinline__ int start(int s) const { return cu ? cu[s] : s * T_each; }
+};
+
+// A tile in the ring: which one it is, and where in it streams start and end.
+template <int L> struct Slot {
+    static constexpr int S = L / kRuns;
+    int task;                               // tile * groups + group; -1: no more
+    uint32_t starts[L / 32], ends[L / 32];  // a bit for each token
+    // A bit for each run with a start (an end) in it. A start at the tile's first token and an end
+    // at its last are apart: there the state (gradient) that reaches the tile is the stream's own.
+    uint32_t run_starts, run_ends;
+    int start_id[L], end_id[L];             // the streams of the marked tokens
+
+    __device__ __forceinline__ bool first() const { return starts[0] & 1u; }
+    __device__ __forceinline__ bool last() const { return ends[L / 32 - 1] >> 31; }
+    // the marked tokens of a run, without those two
+    __device__ __forceinline__ uint32_t starts_of(int run) const { return bits(starts, run) & (run ? ~0u : ~1u); }
+    __device__ __forceinline__ uint32_t ends_of(int run) const {
+        return bits(ends, run) & (run < kRuns - 1 ? ~0u : ~(1u << (S - 1)));
     }
-    if (h0 && t1 > t0) *h0 = h;
+    static __device__ __forceinline__ uint32_t bits(const uint32_t *mask, int run) {
+        return mask[run * S / 32] >> (run * S % 32) & ((1u << S) - 1u);
+    }
+};
+
+// The whole warp fills in a slot for tokens t0 .. t0 + L - 1.
+template <int L> __device__ void find_streams(const Streams &st, int t0, int lane, Slot<L> *slot) {
+    // last stream that starts at or before t0: 32 probes a round
+    int lo = 0, hi = st.B;  // it is in [lo, hi)
+    while (hi - lo > 1) {
+        const int step = (hi - lo + 31) / 32, at = lo + lane * step;
+        const unsigned le = __ballot_sync(0xffffffffu, at < hi && st.start(at) <= t0);
+        const int last = 31 - __clz(le);  // lane 0's probe always holds
+        lo += last * step;
+        hi = min(hi, lo + step);
+    }
+    if (lane < L / 32) slot->starts[lane] = slot->ends[lane] = 0;
+    __syncwarp();
+    for (int s0 = lo; s0 < st.B; s0 += 32) {
+        const int s = s0 + lane;
+        int b = st.total, e = st.total;
+        if (s < st.B) {
+            b = st.start(s);
+            e = st.start(s + 1);
+            if (b < e) {  // an empty stream has no tokens to mark
+                if (b >= t0 && b < t0 + L) {
+                    atomicOr(&slot->starts[(b - t0) >> 5], 1u << ((b - t0) & 31));
+                    slot->start_id[b - t0] = s;
+                }
+                if (e > t0 && e <= t0 + L) {
+                    atomicOr(&slot->ends[(e - 1 - t0) >> 5], 1u << ((e - 1 - t0) & 31));
+                    slot->end_id[e - 1 - t0] = s;
+                }
+            }
+        }
+        if (__any_sync(0xffffffffu, b >= t0 + L || s >= st.B)) break;
+    }
+    __syncwarp();
+    const unsigned rs = __ballot_sync(0xffffffffu, slot->starts_of(lane) != 0);
+    const unsigned re = __ballot_sync(0xffffffffu, slot->ends_of(lane) != 0);
+    if (lane == 0) slot->run_starts = rs, slot->run_ends = re;
+    __syncwarp();
+}
+
+__device__ __forceinline__ void mbar_arrive(uint64_t *bar) {
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(tc::smem_u32(bar)) : "memory");
+}
+__device__ __forceinline__ float4 load4(const float *p) { return *reinterpret_cast<const float4 *>(p); }
+__device__ __forceinline__ void store4(float *p, const float4 &v) { *reinterpret_cast<float4 *>(p) = v; }
+__device__ __forceinline__ float4 zero4() { return make_float4(0.f, 0.f, 0.f, 0.f); }
+__device__ __forceinline__ float4 operator+(const float4 &a, const float4 &b) {
+    return make_float4(a.x + b.x, a.y + b.y, a.z + b.z, a.w + b.w);
+}
+__device__ __forceinline__ float4 keep(const float4 &d, const float4 &h) {  // (1 - d) h
+    return make_float4(fmaf(-d.x, h.x, h.x), fmaf(-d.y, h.y, h.y), fmaf(-d.z, h.z, h.z), fmaf(-d.w, h.w, h.w));
+}
+__device__ __forceinline__ float4 from_lane(const float4 &v, int lane) {
+    return make_float4(__shfl_sync(0xffffffffu, v.x, lane), __shfl_sync(0xffffffffu, v.y, lane),
+                       __shfl_sync(0xffffffffu, v.z, lane), __shfl_sync(0xffffffffu, v.w, lane));
+}
+
+// h -> h - D h + H of some tokens; `reset`: a stream starts among them, and what came before is
+// dropped (not multiplied by 0: it may be NaN).
+struct Map {
+    float4 D, H;
+    bool reset;
+    __device__ __forceinline__ float4 apply(const float4 &h) const { return reset ? H : keep(D, h) + H; }
+    // these tokens after those of `e`
+    __device__ __forceinline__ Map after(const Map &e) const {
+        if (reset) return *this;
+        return Map{e.D + keep(e.D, D), keep(D, e.H) + H, e.reset};  // 1 - (1 - D)(1 - d) = D + (1 - D) d
+    }
+};
+__device__ __forceinline__ Map from_lane(const Map &m, int lane) {
+    return Map{from_lane(m.D, lane), from_lane(m.H, lane), (bool)__shfl_sync(0xffffffffu, (int)m.reset, lane)};
+}
+
+// Joins the maps of a warp's four runs (in order of the tokens, or against it): what comes before
+// each run, and the warp's own.
+template <bool REV> __device__ __forceinline__ void join_runs(Map m, int lane, Map &before, Map &own) {
+    const int rank = REV ? 3 - lane / 8 : lane / 8;
+#pragma unroll
+    for (int n = 1; n < 4; n *= 2) {
+        const Map e = from_lane(m, (REV ? lane + 8 * n : lane - 8 * n) & 31);
+        if (rank >= n) m = m.after(e);
+    }
+    before = from_lane(m, (REV ? lane + 8 : lane - 8) & 31);
+    if (rank == 0) before = Map{zero4(), zero4(), false};
+    own = m;  // the last run's is the whole warp's
+}
+
+// Joins the warps' maps: what comes before this warp, and the tile's.
+template <bool REV>
+__device__ __forceinline__ void join_warps(const float (*D)[kWidth], const float (*H)[kWidth], uint32_t run_resets,
+                                           int warp, int quad, Map &before, Map &all) {
+    Map m{zero4(), zero4(), false};
+#pragma unroll
+    for (int r = 0; r < kWarps; ++r) {
+        const int w = REV ? kWarps - 1 - r : r;
+        if (w == warp) before = m;
+        m = Map{load4(&D[w][quad * 4]), load4(&H[w][quad * 4]), (run_resets >> (4 * w) & 15u) != 0}.after(m);
+    }
+    all = m;
+}
+
+__device__ __forceinline__ float4 load_relaxed(const float *p) {
+    float4 v;
+    asm volatile("ld.relaxed.gpu.global.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "l"(p) : "memory");
+    return v;
+}
+__device__ __forceinline__ void store_relaxed(float *p, const float4 &v) {
+    asm volatile("st.relaxed.gpu.global.v4.f32 [%0], {%1, %2, %3, %4};" ::"l"(p), "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w)
+                 : "memory");
+}
+__device__ __forceinline__ bool written(const float4 &v) {
+    return __float_as_uint(v.x) != kUnwritten && __float_as_uint(v.y) != kUnwritten &&
+           __float_as_uint(v.z) != kUnwritten && __float_as_uint(v.w) != kUnwritten;
+}
+__device__ __forceinline__ int load_abort(const Ctl *ctl) {
+    int v;
+    asm volatile("ld.relaxed.gpu.global.b32 %0, [%1];" : "=r"(v) : "l"(&ctl->abort) : "memory");
+    return v;
+}
+
+// Eight places of a chain, `top` and those before it: lane l has 4 channels (l % 8) of places
+// top - l / 8 and top - 4 - l / 8. The words themselves say whether they have been written, each by
+// itself, so there are no flags and no fences: one trip to L2 gives both.
+struct Window {
+    float4 D[2], H[2], out[2];
+    template <class Cell> __device__ __forceinline__ void load(const Chain &c, int top, Cell cell, int lane) {
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            const int p = top - 4 * u - lane / 8;
+            const float un = __uint_as_float(kUnwritten);
+            D[u] = H[u] = out[u] = make_float4(un, un, un, un);
+            if (p >= 0) {
+                const int64_t at = cell(p) * kWidth + lane % 8 * 4;
+                out[u] = load_relaxed(c.out + at);
+                D[u] = load_relaxed(c.D + at);
+                H[u] = load_relaxed(c.H + at);
+            }
+        }
+    }
+    // Bit n: place top - n is there (its state, or its map).
+    __device__ __forceinline__ unsigned states() const { return places(written(out[0]), written(out[1])); }
+    __device__ __forceinline__ unsigned maps() const {
+        return places(written(D[0]) && written(H[0]), written(D[1]) && written(H[1]));
+    }
+    static __device__ __forceinline__ unsigned places(bool v0, bool v1) {
+        const unsigned b0 = __ballot_sync(0xffffffffu, v0), b1 = __ballot_sync(0xffffffffu, v1);
+        unsigned r = 0;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) r |= (unsigned)((b0 >> 8 * j & 255u) == 255u) << j | (unsigned)((b1 >> 8 * j & 255u) == 255u) << (4 + j);
+        return r;
+    }
+    __device__ __forceinline__ float4 state(int n, int lane) const { return pick(out, n, lane); }
+    // h through places top - n + 1 .. top
+    __device__ __forceinline__ float4 apply(int n, float4 h, int lane) const {
+        for (int k = n - 1; k >= 0; --k) h = keep(pick(D, k, lane), h) + pick(H, k, lane);
+        return h;
+    }
+    static __device__ __forceinline__ float4 pick(const float4 (&v)[2], int n, int lane) {
+        return from_lane(n < 4 ? v[0] : v[1], n % 4 * 8 + lane % 8);
+    }
+};
+
+// What reaches the tile at place `at` > 0 of its chain, by one warp, 4 channels a lane. cell(place)
+// is a place's index. False: the wait ran out (with `stall` it is made to).
+template <class Cell>
+__device__ bool look_back(const Chain &c, int at, Cell cell, int lane, uint64_t wait_ns, bool stall, float4 &h) {
+    Window w;
+    int top = at - 1, n = 0;  // places top - n and later: the search's result
+    uint64_t t0 = 0;
+    for (uint32_t i = 0;; ++i) {
+        w.load(c, top, cell, lane);
+        const unsigned states = stall ? 0u : w.states(), maps = stall ? 0u : w.maps();
+        const unsigned nearer = states ? (states & -states) - 1 : 255u;
+        if ((maps & nearer) == nearer) {
+            if (states) {
+                n = __ffs(states) - 1;
+                break;
+            }
+            top -= 8;  // place 0 has a state and no map: the search never passes it
+            continue;
+        }
+        if ((i & 15) == 15) {
+            const uint64_t now = tc::globaltimer_ns();
+            if (!t0) t0 = now;
+            if (__any_sync(0xffffffffu, now - t0 > wait_ns || load_abort(c.ctl))) return false;
+        }
+    }
+    h = w.apply(n, w.state(n, lane), lane);
+    while (top < at - 1) {  // on to `at` through the windows that the search has seen
+        top += 8;
+        w.load(c, top, cell, lane);
+        h = w.apply(8, h, lane);
+    }
+    return true;
+}
+
+// One warp passes a tile on: publishes its map, waits for what reaches it (unless `known`), publishes
+// what leaves it. False: the wait ran out.
+template <class Cell>
+__device__ bool pass_on(const Chain &c, int place, Cell cell, int lane, const Map &m, bool known, uint64_t wait_ns,
+                        bool stall, float4 &in) {
+    const int64_t own = cell(place) * kWidth + lane * 4;
+    const bool publish = place < c.tiles - 1 && lane < 8;  // the last one's nobody reads
+    if (publish) {
+        if (m.reset) store_relaxed(c.out + own, m.H);  // does not depend on what comes
+        else if (!known) {
+            store_relaxed(c.D + own, m.D);
+            store_relaxed(c.H + own, m.H);
+        }
+    }
+    if (!known && !look_back(c, place, cell, lane, wait_ns, stall, in)) return false;
+    if (publish && !m.reset) store_relaxed(c.out + own, m.apply(in));
+    return true;
+}
+
+// Shared memory of a block, in front of its ring.
+template <int L, int STAGES> struct Shared {
+    uint64_t full[STAGES];
+    int failed;
+    Slot<L> slot[STAGES + 1];
+    alignas(16) float D[kWarps][kWidth], H[kWarps][kWidth];  // the warps' maps
+    alignas(16) float E[kWarps][kWidth], M[kWarps][kWidth];  // backward: those of the reverse scan
+    alignas(16) float in[kWidth];                            // what reaches the tile
+};
+
+template <class Sh> __device__ void init_shared(Sh *sh, int stages) {
+    for (int s = 0; s < stages; ++s) tc::mbar_init(&sh->full[s], 2);  // the copies and the slot
+    sh->failed = 0;
+    tc::fence_mbar_init();
+}
+
+// What the loading warp does, all its lanes together.
+template <typename T, bool BWD, class Sh> struct Loader {
+    using G = Shape<T, BWD>;
+    Sh *sh;
+    unsigned char *ring;
+    const CUtensorMap *x, *a, *b, *dy;
+    Streams streams;
+    Chain c;
+    uint32_t issued;  // tiles put into the ring, the end among them
+
+    // Takes the next tile of the chains, in their order (lane 0's answer counts).
+    __device__ __forceinline__ unsigned take(int lane) const {
+        return lane == 0 ? atomicAdd(&c.ctl->ticket, 1u) : 0u;
+    }
+    // Starts its copies into the ring's next place and fills in the slot.
+    __device__ void put(unsigned ticket, int lane) {
+        const uint32_t s = issued % G::kStages;
+        auto &slot = sh->slot[issued % G::kSlots];
+        ++issued;
+        ticket = __shfl_sync(0xffffffffu, ticket, 0);
+        if (ticket >= (unsigned)(c.tiles * c.groups)) {
+            if (lane == 0) {
+                slot.task = -1;
+                mbar_arrive(&sh->full[s]);
+                mbar_arrive(&sh->full[s]);
+            }
+            return;
+        }
+        const int place = (int)(ticket / c.groups), group = (int)(ticket % c.groups);
+        const int tile = BWD ? c.tiles - 1 - place : place;
+        if (lane == 0) {
+            tc::mbar_expect_tx(&sh->full[s], G::kStage);
+            const uint32_t to = tc::smem_u32(ring + s * G::kStage);
+            tc::tma_load_2d(to, x, group * kWidth, tile * G::L, &sh->full[s]);
+            tc::tma_load_2d(to + G::kPlane, a, group * kWidth, tile * G::L, &sh->full[s]);
+            tc::tma_load_2d(to + 2 * G::kPlane, b, group * kWidth, tile * G::L, &sh->full[s]);
+            if (BWD) tc::tma_load_2d(to + 3 * G::kPlane, dy, group * kWidth, tile * G::L, &sh->full[s]);
+        }
+        find_streams<G::L>(streams, tile * G::L, lane, &slot);
+        if (lane == 0) {
+            slot.task = tile * c.groups + group;
+            mbar_arrive(&sh->full[s]);
+        }
+    }
+    // A block that leaves early waits for the copies it has started; those up to number `it` have
+    // been waited for.
+    __device__ void drain(uint32_t it) {
+        for (++it; it < issued; ++it) tc::mbar_wait(&sh->full[it % G::kStages], (it / G::kStages) & 1u, kWaitNs, 100000u);
+    }
+};
+
+// The wait for a tile's state ran out: every block leaves.
+template <class Sh> __device__ __forceinline__ void give_up(Sh *sh, const Chain &c, int lane, int *status) {
+    if (lane == 0) {
+        atomicExch(&c.ctl->abort, 1);
+        raise_status(status, LA_DEV_TIMEOUT);
+    }
+    *(volatile int *)&sh->failed = 1;
 }
 
 template <typename T>
-__global__ void __launch_bounds__(kThreads)
-scan_backward_kernel(const GatedScanBwdArgs a, const Ctl *ctl) {
-    const int c = blockIdx.x * kThreads + threadIdx.x, s = blockIdx.y;
-    if (c >= a.channels || (a.cu && ctl->bad)) return;
-    const int t0 = a.cu ? a.cu[s] : s * a.T_each, t1 = a.cu ? a.cu[s + 1] : t0 + a.T_each;
-    const T *x = (const T *)a.x, *ab = (const T *)a.ab, *dy = (const T *)a.dy;
-    T *dx = (T *)a.dx, *dab = (T *)a.dab;
-    const int tiles = (a.total + kTile - 1) / kTile;
-    float m = a.dh_final_ptrs ? reinterpret_cast<const float *>(a.dh_final_ptrs[s])[c] : 0.f;
-    float before[kTile];
-    for (int end = t1; end > t0;) {
-        const int begin = max(t0, (end - 1) / kTile * kTile);
-        float h = a.saved[(begin == t0 ? (int64_t)tiles + s : (int64_t)(begin / kTile)) * a.channels + c];
-        for (int t = begin; t < end; ++t) {
-            before[t - begin] = h;
-            float d, beta;
-            gates(to_f(ab[t * a.ab_stride + c]), to_f(ab[t * a.ab_stride + a.channels + c]), d, beta);
-            h = gated_update(h, d, beta * to_f(x[t * a.x_stride + c]));
+__global__ void __launch_bounds__(kThreads, 2)
+scan_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_a,
+            const __grid_constant__ CUtensorMap map_b, const GatedScanArgs a, const Chain c) {
+    using G = Shape<T, false>;
+    using V = Vec4<T>;
+    constexpr int S = G::S, L = G::L, kPlane = G::kPlane / (int)sizeof(T);
+    using Sh = Shared<L, G::kStages>;
+    extern __shared__ __align__(128) unsigned char smem[];
+    Sh *sh = reinterpret_cast<Sh *>(smem);
+    unsigned char *ring = smem + (sizeof(Sh) + 127) / 128 * 128;
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, quad = lane % 8, run = warp * 4 + lane / 8;
+    if (threadIdx.x == 0) init_shared(sh, G::kStages);
+    __syncthreads();
+    if (c.ctl->bad) return;
+    Loader<T, false, Sh> loader{sh, ring, &map_x, &map_a, &map_b, nullptr, Streams{a.cu, a.B, a.T_each, a.total}, c, 0};
+    if (warp == kLoader)
+        for (int i = 0; i < G::kStages; ++i) loader.put(loader.take(lane), lane);
+    volatile int *failed = &sh->failed;
+    float *saved_initial = a.saved ? a.saved + (int64_t)((a.total + kSave<T> - 1) / kSave<T>) * a.channels : nullptr;
+    for (uint32_t it = 0;; ++it) {
+        const uint32_t s = it % G::kStages;
+        unsigned ticket = 0;
+        if (warp == kLoader) ticket = loader.take(lane);  // for the place that this tile leaves
+        const bool arrived = tc::mbar_wait(&sh->full[s], (it / G::kStages) & 1u, a.wait_ns + kWaitNs);
+        const Slot<L> &slot = sh->slot[it % G::kSlots];
+        const int task = arrived ? slot.task : 0;
+        if (task < 0) break;
+        if (!arrived) *failed = 1;
+        const int tile = task / c.groups, group = task % c.groups;
+        const int ch = group * kWidth + quad * 4, t0 = tile * L + run * S;
+        const bool live = ch < a.channels;
+        const uint32_t starts = slot.starts_of(run);
+
+        // this run's tokens from a state of zero: h, and how much is left of what comes before
+        float hl[S][4], A[S][4];
+        Map before_run, before_warp, all;
+        {
+            const T *in = reinterpret_cast<const T *>(ring + s * G::kStage) + run * S * kWidth + quad * 4;
+            float h[4] = {0.f, 0.f, 0.f, 0.f}, D[4] = {0.f, 0.f, 0.f, 0.f}, R[4] = {1.f, 1.f, 1.f, 1.f};
+#pragma unroll
+            for (int i = 0; i < S; ++i) {
+                float x[4], ga[4], gb[4];
+                V::load(in + i * kWidth, x);
+                V::load(in + i * kWidth + kPlane, ga);
+                V::load(in + i * kWidth + 2 * kPlane, gb);
+                if (starts >> i & 1u) {
+                    const int id = slot.start_id[run * S + i];
+                    float4 v = zero4();
+                    if (a.h_ptrs && live) v = load4(reinterpret_cast<const float *>(a.h_ptrs[id]) + ch);
+                    if (a.saved && live) {
+                        store4(saved_initial + (int64_t)id * a.channels + ch, v);
+                        if (i == 0 && t0 % kSave<T> == 0) store4(a.saved + (int64_t)(t0 / kSave<T>) * a.channels + ch, v);
+                    }
+                    h[0] = v.x, h[1] = v.y, h[2] = v.z, h[3] = v.w;
+                }
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    float d, beta;
+                    gates(ga[e], gb[e], d, beta);
+                    h[e] = fmaf(beta, x[e], fmaf(-d, h[e], h[e]));
+                    D[e] = fmaf(d, R[e], D[e]);
+                    R[e] = 1.f - D[e];
+                    hl[i][e] = h[e];
+                    A[i][e] = R[e];
+                }
+            }
+            Map own;
+            join_runs<false>(Map{make_float4(D[0], D[1], D[2], D[3]), make_float4(h[0], h[1], h[2], h[3]), starts != 0},
+                             lane, before_run, own);
+            if (lane >= 24) {
+                store4(&sh->D[warp][quad * 4], own.D);
+                store4(&sh->H[warp][quad * 4], own.H);
+            }
         }
-        for (int t = end - 1; t >= begin; --t) {
-            float d, beta;
-            gates(to_f(ab[t * a.ab_stride + c]), to_f(ab[t * a.ab_stride + a.channels + c]), d, beta);
-            const float lam = to_f(dy[t * a.dy_stride + c]) + m;
-            m = fmaf(-d, lam, lam);
-            dx[t * a.dx_stride + c] = from_f<T>(lam * beta);
-            dab[t * a.dab_stride + c] = from_f<T>(-lam * before[t - begin] * d * (1.f - d));
-            dab[t * a.dab_stride + a.channels + c] =
-                from_f<T>(lam * to_f(x[t * a.x_stride + c]) * beta * (1.f - beta));
+        __syncthreads();
+        if (*failed) {
+            if (warp == kLoader) loader.drain(it);
+            break;
         }
-        end = begin;
+        if (warp == kLoader) loader.put(ticket, lane);
+
+        join_warps<false>(sh->D, sh->H, slot.run_starts, warp, quad, before_warp, all);
+        if (warp == kWarps - 1) {
+            float4 h = zero4();
+            if (slot.first() && live) {
+                const int id = slot.start_id[0];
+                if (a.h_ptrs) h = load4(reinterpret_cast<const float *>(a.h_ptrs[id]) + ch);
+                if (a.saved && lane < 8) store4(saved_initial + (int64_t)id * a.channels + ch, h);
+            }
+            const auto cell = [&](int place) { return (int64_t)place * c.groups + group; };
+            if (!pass_on(c, tile, cell, lane, all, slot.first(), a.wait_ns, a.debug_stall != 0, h))
+                give_up(sh, c, lane, a.status);
+            if (lane < 8) store4(&sh->in[quad * 4], h);
+        }
+        __syncthreads();
+        if (*failed) {
+            if (warp == kLoader) loader.drain(it);
+            break;
+        }
+
+        // the state that reaches this run, then its tokens'
+        const float4 v = before_run.apply(before_warp.apply(load4(&sh->in[quad * 4])));
+        if (a.saved && live && !(starts & 1u) && t0 % kSave<T> == 0 && t0 < a.total)
+            store4(a.saved + (int64_t)(t0 / kSave<T>) * a.channels + ch, v);
+        const float hin[4] = {v.x, v.y, v.z, v.w};
+        const uint32_t ends = Slot<L>::bits(slot.ends, run);
+        T *yp = static_cast<T *>(a.y) + (int64_t)t0 * a.y_stride + ch;
+        bool fresh = false;  // a stream has started in this run
+#pragma unroll
+        for (int i = 0; i < S; ++i) {
+            if (starts >> i & 1u) fresh = true;
+            float y[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) y[e] = fresh ? hl[i][e] : fmaf(A[i][e], hin[e], hl[i][e]);
+            if (live && t0 + i < a.total) V::store(yp + i * a.y_stride, y);
+            if ((ends >> i & 1u) && a.h_ptrs && live)
+                Vec4<float>::store(reinterpret_cast<float *>(a.h_ptrs[slot.end_id[run * S + i]]) + ch, y);
+        }
     }
-    if (a.dh0_ptrs) reinterpret_cast<float *>(a.dh0_ptrs[s])[c] = m;
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kThreads, 2)
+scan_backward_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_a,
+                     const __grid_constant__ CUtensorMap map_b, const __grid_constant__ CUtensorMap map_dy,
+                     const GatedScanBwdArgs a, const Chain c) {
+    using G = Shape<T, true>;
+    using V = Vec4<T>;
+    constexpr int S = G::S, L = G::L, kPlane = G::kPlane / (int)sizeof(T);
+    using Sh = Shared<L, G::kStages>;
+    extern __shared__ __align__(128) unsigned char smem[];
+    Sh *sh = reinterpret_cast<Sh *>(smem);
+    unsigned char *ring = smem + (sizeof(Sh) + 127) / 128 * 128;
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, quad = lane % 8, run = warp * 4 + lane / 8;
+    if (threadIdx.x == 0) init_shared(sh, G::kStages);
+    __syncthreads();
+    if (c.ctl->bad) return;
+    Loader<T, true, Sh> loader{sh, ring, &map_x, &map_a, &map_b, &map_dy, Streams{a.cu, a.B, a.T_each, a.total}, c, 0};
+    if (warp == kLoader)
+        for (int i = 0; i < G::kStages; ++i) loader.put(loader.take(lane), lane);
+    volatile int *failed = &sh->failed;
+    const float *saved_initial = a.saved + (int64_t)c.tiles * a.channels;
+    if (a.cu && a.dh0_ptrs) {  // the gradient passes through an empty stream
+        for (int s = blockIdx.x; s < a.B; s += gridDim.x) {
+            if (a.cu[s] != a.cu[s + 1]) continue;
+            for (int i = threadIdx.x; i < a.channels; i += kThreads)
+                reinterpret_cast<float *>(a.dh0_ptrs[s])[i] =
+                    a.dh_final_ptrs ? reinterpret_cast<const float *>(a.dh_final_ptrs[s])[i] : 0.f;
+        }
+    }
+    for (uint32_t it = 0;; ++it) {
+        const uint32_t s = it % G::kStages;
+        unsigned ticket = 0;
+        if (warp == kLoader) ticket = loader.take(lane);
+        const bool arrived = tc::mbar_wait(&sh->full[s], (it / G::kStages) & 1u, a.wait_ns + kWaitNs);
+        const Slot<L> &slot = sh->slot[it % G::kSlots];
+        const int task = arrived ? slot.task : 0;
+        if (task < 0) break;
+        if (!arrived) *failed = 1;
+        const int tile = task / c.groups, group = task % c.groups;
+        const int ch = group * kWidth + quad * 4, t0 = tile * L + run * S;
+        const bool live = ch < a.channels;
+        float4 h_in = zero4();  // the state that reaches the tile
+        if (live) h_in = load4(a.saved + (int64_t)tile * a.channels + ch);
+        const uint32_t starts = slot.starts_of(run), ends = slot.ends_of(run);
+        const auto initial = [&](int i) {  // state of the stream that starts at this run's token i
+            return live ? load4(saved_initial + (int64_t)slot.start_id[run * S + i] * a.channels + ch) : zero4();
+        };
+        const auto final_gradient = [&](int at) {  // of the stream that ends at the tile's token `at`
+            return a.dh_final_ptrs && live ? load4(reinterpret_cast<const float *>(a.dh_final_ptrs[slot.end_id[at]]) + ch)
+                                           : zero4();
+        };
+
+        float d[S][4], beta[S][4];
+        typename V::Raw xr[S], dyr[S];
+        Map h_run, h_warp, m_run, m_warp, all;
+        {
+            const T *in = reinterpret_cast<const T *>(ring + s * G::kStage) + run * S * kWidth + quad * 4;
+            float h[4] = {0.f, 0.f, 0.f, 0.f}, m[4] = {0.f, 0.f, 0.f, 0.f}, D[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int i = 0; i < S; ++i) {
+                float x[4], ga[4], gb[4];
+                xr[i] = V::load_raw(in + i * kWidth);
+                V::load(in + i * kWidth + kPlane, ga);
+                V::load(in + i * kWidth + 2 * kPlane, gb);
+                dyr[i] = V::load_raw(in + i * kWidth + 3 * kPlane);
+                V::widen(xr[i], x);
+                if (starts >> i & 1u) {
+                    const float4 v = initial(i);
+                    h[0] = v.x, h[1] = v.y, h[2] = v.z, h[3] = v.w;
+                }
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    gates(ga[e], gb[e], d[i][e], beta[i][e]);
+                    h[e] = fmaf(beta[i][e], x[e], fmaf(-d[i][e], h[e], h[e]));
+                    D[e] = fmaf(d[i][e], 1.f - D[e], D[e]);
+                }
+            }
+#pragma unroll
+            for (int i = S - 1; i >= 0; --i) {
+                float dy[4];
+                V::widen(dyr[i], dy);
+                if (ends >> i & 1u) {
+                    const float4 v = final_gradient(run * S + i);
+                    m[0] = v.x, m[1] = v.y, m[2] = v.z, m[3] = v.w;
+                }
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float lam = dy[e] + m[e];
+                    m[e] = fmaf(-d[i][e], lam, lam);
+                }
+            }
+            const float4 Dv = make_float4(D[0], D[1], D[2], D[3]);
+            Map own;
+            join_runs<false>(Map{Dv, make_float4(h[0], h[1], h[2], h[3]), starts != 0}, lane, h_run, own);
+            if (lane >= 24) {
+                store4(&sh->D[warp][quad * 4], own.D);
+                store4(&sh->H[warp][quad * 4], own.H);
+            }
+            join_runs<true>(Map{Dv, make_float4(m[0], m[1], m[2], m[3]), ends != 0}, lane, m_run, own);
+            if (lane < 8) {
+                store4(&sh->E[warp][quad * 4], own.D);
+                store4(&sh->M[warp][quad * 4], own.H);
+            }
+        }
+        __syncthreads();
+        if (*failed) {
+            if (warp == kLoader) loader.drain(it);
+            break;
+        }
+        if (warp == kLoader) loader.put(ticket, lane);
+
+        join_warps<true>(sh->E, sh->M, slot.run_ends, warp, quad, m_warp, all);
+        if (warp == 0) {
+            float4 m = zero4();
+            if (slot.last()) m = final_gradient(L - 1);
+            const auto cell = [&](int place) { return (int64_t)(c.tiles - 1 - place) * c.groups + group; };
+            const int place = c.tiles - 1 - tile;
+            // behind the chain's first place there is nothing: the last stream ends in it
+            if (!pass_on(c, place, cell, lane, all, slot.last() || place == 0, a.wait_ns, a.debug_stall != 0, m))
+                give_up(sh, c, lane, a.status);
+            if (lane < 8) store4(&sh->in[quad * 4], m);
+        }
+        // meanwhile the others (and warp 0 after it) have the states before their tokens
+        join_warps<false>(sh->D, sh->H, slot.run_starts, warp, quad, h_warp, all);
+        float hp[S][4];
+        {
+            const float4 v = h_run.apply(h_warp.apply(h_in));
+            float h[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int i = 0; i < S; ++i) {
+                float x[4];
+                V::widen(xr[i], x);
+                if (starts >> i & 1u) {
+                    const float4 u = initial(i);
+                    h[0] = u.x, h[1] = u.y, h[2] = u.z, h[3] = u.w;
+                }
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    hp[i][e] = h[e];
+                    h[e] = fmaf(beta[i][e], x[e], fmaf(-d[i][e], h[e], h[e]));
+                }
+            }
+        }
+        __syncthreads();
+        if (*failed) {
+            if (warp == kLoader) loader.drain(it);
+            break;
+        }
+
+        const float4 v = m_run.apply(m_warp.apply(load4(&sh->in[quad * 4])));
+        float m[4] = {v.x, v.y, v.z, v.w};
+        const uint32_t all_starts = Slot<L>::bits(slot.starts, run);
+        T *dxp = static_cast<T *>(a.dx) + (int64_t)t0 * a.dx_stride + ch;
+        T *dap = static_cast<T *>(a.dab) + (int64_t)t0 * a.dab_stride + ch;
+#pragma unroll
+        for (int i = S - 1; i >= 0; --i) {
+            float x[4], dy[4], dx[4], da[4], db[4];
+            V::widen(xr[i], x);
+            V::widen(dyr[i], dy);
+            if (ends >> i & 1u) {
+                const float4 u = final_gradient(run * S + i);
+                m[0] = u.x, m[1] = u.y, m[2] = u.z, m[3] = u.w;
+            }
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const float lam = dy[e] + m[e], left = fmaf(-d[i][e], lam, lam);
+                dx[e] = lam * beta[i][e];
+                db[e] = dx[e] * x[e] * (1.f - beta[i][e]);
+                da[e] = -left * hp[i][e] * d[i][e];
+                m[e] = left;
+            }
+            if (live && t0 + i < a.total) {
+                V::store(dxp + i * a.dx_stride, dx);
+                V::store(dap + i * a.dab_stride, da);
+                V::store(dap + i * a.dab_stride + a.channels, db);
+            }
+            if ((all_starts >> i & 1u) && a.dh0_ptrs && live)
+                Vec4<float>::store(reinterpret_cast<float *>(a.dh0_ptrs[slot.start_id[run * S + i]]) + ch, m);
+        }
+    }
+}
+
+int device_sms() {
+    int dev = 0, n = 0;
+    cudaGetDevice(&dev);
+    cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
+    return n > 0 ? n : 148;
+}
+
+// Tensor map of one input's tiles, from its first channel.
+template <typename T, bool BWD>
+bool tile_map(CUtensorMap *map, const void *base, int total, int channels, int64_t ld) {
+    return make_map_2d(map, base, sizeof(T) == 2 ? LA_BF16 : LA_F32, total, channels, ld, kWidth, Shape<T, BWD>::L, false);
+}
+
+// Clears the chain, then starts as many blocks as fit (or as there are tiles).
+template <typename T, bool BWD, class Kernel, class Launch>
+cudaError_t start(Kernel kernel, const int32_t *cu, int B, int total, const Chain &c, int *status, cudaStream_t st,
+                  Launch launch) {
+    using G = Shape<T, BWD>;
+    const size_t smem = (sizeof(Shared<G::L, G::kStages>) + 127) / 128 * 128 + G::kStages * G::kStage;
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+    const int64_t cells = (int64_t)c.tiles * c.groups, clear = (cells * kWidth * 3 / 4 + 1023) / 1024;
+    const int sms = device_sms();
+    chain_init_kernel<<<(int)(clear < sms ? clear : sms), 1024, 0, st>>>(cu, B, total, c, status);
+    launch((int)(cells < 2 * sms ? cells : 2 * sms), smem);
+    return cudaGetLastError();
+}
+
+template <typename T> cudaError_t scan(const GatedScanArgs &a, cudaStream_t st) {
+    CUtensorMap x, ga, gb;
+    const T *ab = static_cast<const T *>(a.ab);
+    if (!tile_map<T, false>(&x, a.x, a.total, a.channels, a.x_stride) ||
+        !tile_map<T, false>(&ga, ab, a.total, a.channels, a.ab_stride) ||
+        !tile_map<T, false>(&gb, ab + a.channels, a.total, a.channels, a.ab_stride))
+        return cudaErrorInvalidValue;
+    const Chain c = make_chain<T, false>(a.workspace, a.total, a.channels);
+    return start<T, false>(scan_kernel<T>, a.cu, a.B, a.total, c, a.status, st, [&](int grid, size_t smem) {
+        scan_kernel<T><<<grid, kThreads, smem, st>>>(x, ga, gb, a, c);
+    });
+}
+
+template <typename T> cudaError_t backward(const GatedScanBwdArgs &a, cudaStream_t st) {
+    CUtensorMap x, ga, gb, dy;
+    const T *ab = static_cast<const T *>(a.ab);
+    if (!tile_map<T, true>(&x, a.x, a.total, a.channels, a.x_stride) ||
+        !tile_map<T, true>(&ga, ab, a.total, a.channels, a.ab_stride) ||
+        !tile_map<T, true>(&gb, ab + a.channels, a.total, a.channels, a.ab_stride) ||
+        !tile_map<T, true>(&dy, a.dy, a.total, a.channels, a.dy_stride))
+        return cudaErrorInvalidValue;
+    const Chain c = make_chain<T, true>(a.workspace, a.total, a.channels);
+    return start<T, true>(scan_backward_kernel<T>, a.cu, a.B, a.total, c, a.status, st, [&](int grid, size_t smem) {
+        scan_backward_kernel<T><<<grid, kThreads, smem, st>>>(x, ga, gb, dy, a, c);
+    });
 }
 
 }  // namespace
 
-size_t gated_scan_workspace_bytes(int, int, int, int) { return 16; }
-size_t gated_scan_saved_bytes(int B, int total, int channels, int) {
-    return (((size_t)total + kTile - 1) / kTile + B) * channels * sizeof(float);
+size_t gated_scan_workspace_bytes(int, int total, int channels, int dtype) {  // of either pass
+    return dtype == LA_BF16 ? chain_bytes<__nv_bfloat16, true>(total, channels) : chain_bytes<float, true>(total, channels);
+}
+
+size_t gated_scan_saved_bytes(int B, int total, int channels, int dtype) {
+    const int every = dtype == LA_BF16 ? kSave<__nv_bfloat16> : kSave<float>;
+    return (((size_t)total + every - 1) / every + B) * channels * sizeof(float);
 }
 
 cudaError_t launch_gated_scan(const GatedScanArgs &a, cudaStream_t st) {
-    Ctl *ctl = (Ctl *)a.workspace;
-    if (a.cu) scan_init_kernel<<<1, 1024, 0, st>>>(a.cu, a.B, a.total, ctl, a.status);
-    const dim3 grid((a.channels + kThreads - 1) / kThreads, a.B);
-    if (a.dtype == LA_BF16) scan_kernel<__nv_bfloat16><<<grid, kThreads, 0, st>>>(a, ctl);
-    else scan_kernel<float><<<grid, kThreads, 0, st>>>(a, ctl);
-    return cudaGetLastError();
+    return a.dtype == LA_BF16 ? scan<__nv_bfloat16>(a, st) : scan<float>(a, st);
 }
 
 cudaError_t launch_gated_scan_backward(const GatedScanBwdArgs &a, cudaStream_t st) {
-    Ctl *ctl = (Ctl *)a.workspace;
-    if (a.cu) scan_init_kernel<<<1, 1024, 0, st>>>(a.cu, a.B, a.total, ctl, a.status);
-    const dim3 grid((a.channels + kThreads - 1) / kThreads, a.B);
-    if (a.dtype == LA_BF16) scan_backward_kernel<__nv_bfloat16><<<grid, kThreads, 0, st>>>(a, ctl);
-    else scan_backward_kernel<float><<<grid, kThreads, 0, st>>>(a, ctl);
-    return cudaGetLastError();
+    return a.dtype == LA_BF16 ? backward<__nv_bfloat16>(a, st) : backward<float>(a, st);
 }
 
 }  // namespace la

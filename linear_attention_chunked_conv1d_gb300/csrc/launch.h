@@ -240,6 +240,9 @@ struct W4QuantArgs {
 };
 cudaError_t launch_w4_quantize(const W4QuantArgs &a, cudaStream_t st);
 
+// As make_map_bf16_2d below, for elements of either activation type (LA_F32, LA_BF16).
+bool make_map_2d(void *map, const void *base, int dtype, int64_t rows, int64_t cols, int64_t ld,
+                 uint32_t box_cols, uint32_t box_rows, bool swizzle128);
 // Encodes a 2-D tiled TMA map (a CUtensorMap, 64-byte aligned storage of 128 bytes) of a
 // row-major bf16 matrix [rows][cols] with row stride ld elements, boxes of box_rows x box_cols,
 // optional 128-byte swizzle; out-of-range elements of a box read as zero. False on failure.

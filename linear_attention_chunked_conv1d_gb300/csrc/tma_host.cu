@@ -5,6 +5,7 @@
 #include <mutex>
 
 #include "launch.h"
+#include "linattn.h"
 
 namespace la {
 
@@ -32,18 +33,24 @@ EncodeTiledFn encode_fn() {
 
 }  // namespace
 
-bool make_map_bf16_2d(void *map, const void *base, int64_t rows, int64_t cols, int64_t ld,
-                      uint32_t box_cols, uint32_t box_rows, bool swizzle128) {
+bool make_map_2d(void *map, const void *base, int dtype, int64_t rows, int64_t cols, int64_t ld,
+                 uint32_t box_cols, uint32_t box_rows, bool swizzle128) {
     EncodeTiledFn enc = encode_fn();
     if (!enc) return false;
     const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
-    const cuuint64_t strides[1] = {(cuuint64_t)ld * 2};
+    const cuuint64_t strides[1] = {(cuuint64_t)ld * (dtype == LA_BF16 ? 2 : 4)};
     const cuuint32_t box[2] = {box_cols, box_rows};
     const cuuint32_t estr[2] = {1, 1};
-    return enc(reinterpret_cast<CUtensorMap *>(map), CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2,
+    return enc(reinterpret_cast<CUtensorMap *>(map),
+               dtype == LA_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2,
                const_cast<void *>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
                swizzle128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+bool make_map_bf16_2d(void *map, const void *base, int64_t rows, int64_t cols, int64_t ld,
+                      uint32_t box_cols, uint32_t box_rows, bool swizzle128) {
+    return make_map_2d(map, base, LA_BF16, rows, cols, ld, box_cols, box_rows, swizzle128);
 }
 
 }  // namespace la

@@ -22,7 +22,7 @@ def scan(lib, **kw):
 
 
 def backward(lib, **kw):
-    a = dict(x=A, ab=2 * A, saved=5 * A, sb=1 << 24, dy=6 * A, fin=A, dx=7 * A, dab=8 * A, dh0=A, cu=A, B=2, T=40,
+    a = dict(x=A, ab=2 * A, saved=5 * A, sb=1 << 24, dy=6 * A, fin=A, dx=7 * A, dab=8 * A, dh0=2 * A, cu=A, B=2, T=40,
              maxt=40, C=64, xs=64, abs=128, dys=64, dxs=64, dabs=128, dtype=1, ws=4 * A, wsb=1 << 24)
     a.update(kw)
     return lib._load().la_gated_scan_backward(
@@ -94,6 +94,7 @@ def test_scan_backward(lib):
         for taken in (A, 2 * A, 5 * A, 6 * A):
             assert backward(lib, **{out: taken}) == ARG
     assert backward(lib, dab=7 * A) == ARG  # dx
+    assert backward(lib, dh0=A) == ARG  # dh_final
     assert backward(lib, dabs=64) == ARG and backward(lib, dys=60) == ARG and backward(lib, dxs=0) == ARG
 
 

@@ -213,12 +213,12 @@ def test_strided_views_leave_the_rest_alone(cuda, dtype):
     cu = cu_of(lengths, cuda)
     ws = workspace(la.gated_scan_workspace_bytes, 3, T, C, DT[dtype], dev=cuda)
     saved = workspace(la.gated_scan_saved_bytes, 3, T, C, DT[dtype], dev=cuda)
-    dfin = inp["dfinal"].to(cuda)  # dh0 goes to the buffers of dh_final
+    dfin, dh0 = inp["dfinal"].to(cuda), torch.empty(3, C, device=cuda)
     la.gated_scan(la.pointer_array(list(h)), x, ab, y, cu, saved=saved, workspace=ws)
     la.gated_scan_backward(x, ab, saved, inp["dy"].to(cuda), dx, dab, cu, dh_final_ptrs=la.pointer_array(list(dfin)),
-                           dh0_ptrs=la.pointer_array(list(dfin)), workspace=ws)
+                           dh0_ptrs=la.pointer_array(list(dh0)), workspace=ws)
     torch.cuda.synchronize()
-    for got, ref in zip((y, h, dx, dab, dfin), want):
+    for got, ref in zip((y, h, dx, dab, dh0), want):
         assert torch.equal(got, ref)
     out[1:T + 1, 8:C + 8] = out[1:T + 1, C + 16:2 * C + 16] = out[1:T + 1, 2 * C + 24:4 * C + 24] = 5.0
     assert torch.all(out == 5.0)
