@@ -14,9 +14,9 @@
 // instructions on them. One launch reads every input once, whatever the streams' lengths:
 //  - The packed rows are cut into tiles of L tokens x 32 channels, regardless of where streams meet.
 //    A tile maps the state (or, backward, the gradient m) that reaches it to the one that leaves it:
-//    h -> h - D h + H. D = 1 - prod (1 - d) is carried instead of the product, for the reason in
+//    h -> h + N h + H. N = prod (1 - d) - 1 is carried instead of the product, for the reason in
 //    gated.cuh. Where a stream starts inside the tile, what comes from before is dropped.
-//  - Tiles of a channel group are chained along the sequence. A block publishes its tile's (D, H) as
+//  - Tiles of a channel group are chained along the sequence. A block publishes its tile's (N, H) as
 //    soon as it has them, finds the nearest earlier tile whose outgoing state is known, and applies
 //    the maps in between to that state, oldest first. The state that leaves a tile is thus the same
 //    expression, evaluated in the same order, wherever that search ended: results do not depend on
@@ -28,7 +28,12 @@
 //  - Blocks are persistent. Tiles come by TMA into a ring in shared memory and are worked on in
 //    registers, so a tile's place in the ring is free again, and the next copy under way, while the
 //    tile waits for its state.
+//  - Instructions are the next bound after HBM, and of these the special function unit's: channels go
+//    in packed pairs, and tiles without a start or an end of a stream (all but one in each stream)
+//    take a path without tests for them.
 #include <cuda.h>
+
+#include <type_traits>
 
 #include "gated.cuh"
 #include "launch.h"
@@ -46,7 +51,7 @@ constexpr int kRuns = 4 * kWarps;  // is along the tokens, in runs of S
 constexpr uint64_t kWaitNs = 2000000000ull;
 
 // Tokens of a run, and the ring's depth. What a thread keeps of a tile across the wait for its state
-// is 2 registers a (token, channel) forward and 3 to 5 backward; two blocks on an SM leave 128
+// is 2 registers a (token, channel) forward and 4 to 5 backward; two blocks on an SM leave 128
 // registers a thread, which these fill. Two blocks' rings take 192 KB of shared memory.
 template <typename T, bool BWD> struct Shape {
     static constexpr int kIn = BWD ? 4 : 3;                              // x, a, b (, dy)
@@ -75,7 +80,7 @@ constexpr uint32_t kUnwritten = 0xffffffffu;
 
 struct Chain {
     Ctl *ctl;
-    float *D, *H, *out;  // [tiles][groups][32]: the tile's map, the state that leaves it
+    float *N, *H, *out;  // [tiles][groups][32]: the tile's map, the state that leaves it
     int tiles, groups;
 };
 
@@ -85,8 +90,8 @@ template <typename T, bool BWD> Chain make_chain(void *workspace, int total, int
     c.groups = (channels + kWidth - 1) / kWidth;
     const int64_t words = (int64_t)c.tiles * c.groups * kWidth;
     c.ctl = static_cast<Ctl *>(workspace);
-    c.D = reinterpret_cast<float *>(c.ctl + 1);
-    c.H = c.D + words;
+    c.N = reinterpret_cast<float *>(c.ctl + 1);
+    c.H = c.N + words;
     c.out = c.H + words;
     return c;
 }
@@ -99,7 +104,7 @@ template <typename T, bool BWD> size_t chain_bytes(int total, int channels) {
 // Clears the chains; block 0 also looks at every offset.
 __global__ void chain_init_kernel(const int32_t *cu, int B, int total, Chain c, int *status) {
     const int64_t quads = (int64_t)c.tiles * c.groups * kWidth * 3 / 4;
-    uint4 *p = reinterpret_cast<uint4 *>(c.D);
+    uint4 *p = reinterpret_cast<uint4 *>(c.N);
     for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < quads; i += (int64_t)gridDim.x * blockDim.x)
         p[i] = make_uint4(kUnwritten, kUnwritten, kUnwritten, kUnwritten);
     if (blockIdx.x) return;
@@ -130,6 +135,7 @@ template <int L> struct Slot {
     // A bit for each run with a start (an end) in it. A start at the tile's first token and an end
     // at its last are apart: there the state (gradient) that reaches the tile is the stream's own.
     uint32_t run_starts, run_ends;
+    bool marked;                            // some token is, or lies past the last one
     int start_id[L], end_id[L];             // the streams of the marked tokens
 
     __device__ __forceinline__ bool first() const { return starts[0] & 1u; }
@@ -179,84 +185,73 @@ template <int L> __device__ void find_streams(const Streams &st, int t0, int lan
     __syncwarp();
     const unsigned rs = __ballot_sync(0xffffffffu, slot->starts_of(lane) != 0);
     const unsigned re = __ballot_sync(0xffffffffu, slot->ends_of(lane) != 0);
-    if (lane == 0) slot->run_starts = rs, slot->run_ends = re;
+    const bool marked = __any_sync(0xffffffffu, lane < L / 32 && (slot->starts[lane] | slot->ends[lane]));
+    if (lane == 0) {
+        slot->run_starts = rs;
+        slot->run_ends = re;
+        slot->marked = marked || t0 + L > st.total;
+    }
     __syncwarp();
 }
 
 __device__ __forceinline__ void mbar_arrive(uint64_t *bar) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(tc::smem_u32(bar)) : "memory");
 }
-__device__ __forceinline__ float4 load4(const float *p) { return *reinterpret_cast<const float4 *>(p); }
-__device__ __forceinline__ void store4(float *p, const float4 &v) { *reinterpret_cast<float4 *>(p) = v; }
-__device__ __forceinline__ float4 zero4() { return make_float4(0.f, 0.f, 0.f, 0.f); }
-__device__ __forceinline__ float4 operator+(const float4 &a, const float4 &b) {
-    return make_float4(a.x + b.x, a.y + b.y, a.z + b.z, a.w + b.w);
-}
-__device__ __forceinline__ float4 keep(const float4 &d, const float4 &h) {  // (1 - d) h
-    return make_float4(fmaf(-d.x, h.x, h.x), fmaf(-d.y, h.y, h.y), fmaf(-d.z, h.z, h.z), fmaf(-d.w, h.w, h.w));
-}
-__device__ __forceinline__ float4 from_lane(const float4 &v, int lane) {
-    return make_float4(__shfl_sync(0xffffffffu, v.x, lane), __shfl_sync(0xffffffffu, v.y, lane),
-                       __shfl_sync(0xffffffffu, v.z, lane), __shfl_sync(0xffffffffu, v.w, lane));
+__device__ __forceinline__ F4 zero4() { return all4(0.f); }
+__device__ __forceinline__ F4 from_lane(const F4 &v, int lane) {
+    return F4{{__shfl_sync(0xffffffffu, v.p[0], lane), __shfl_sync(0xffffffffu, v.p[1], lane)}};
 }
 
-// h -> h - D h + H of some tokens; `reset`: a stream starts among them, and what came before is
-// dropped (not multiplied by 0: it may be NaN).
+// h -> h + N h + H of some tokens.
 struct Map {
-    float4 D, H;
-    bool reset;
-    __device__ __forceinline__ float4 apply(const float4 &h) const { return reset ? H : keep(D, h) + H; }
-    // these tokens after those of `e`
-    __device__ __forceinline__ Map after(const Map &e) const {
-        if (reset) return *this;
-        return Map{e.D + keep(e.D, D), keep(D, e.H) + H, e.reset};  // 1 - (1 - D)(1 - d) = D + (1 - D) d
-    }
+    F4 N, H;
+    __device__ __forceinline__ F4 apply(const F4 &h) const { return add4(left4(N, h), H); }
+    // these tokens after those of `e`: (1 + e.N)(1 + N) - 1 = e.N + N + e.N N
+    __device__ __forceinline__ Map after(const Map &e) const { return Map{fma4(N, e.N, add4(e.N, N)), apply(e.H)}; }
 };
-__device__ __forceinline__ Map from_lane(const Map &m, int lane) {
-    return Map{from_lane(m.D, lane), from_lane(m.H, lane), (bool)__shfl_sync(0xffffffffu, (int)m.reset, lane)};
-}
+__device__ __forceinline__ Map identity() { return Map{zero4(), zero4()}; }
 
-// Joins the maps of a warp's four runs (in order of the tokens, or against it): what comes before
-// each run, and the warp's own.
-template <bool REV> __device__ __forceinline__ void join_runs(Map m, int lane, Map &before, Map &own) {
-    const int rank = REV ? 3 - lane / 8 : lane / 8;
+// The first `last` of n maps (rows at a stride of kStep), joined in order of the tokens, or against it
+// (REV: row n - 1 first). A bit in `resets` says that a stream starts among a row's tokens: what comes
+// before it is dropped there, not multiplied by 0 (it may be NaN). kMarked: whether there may be any.
+template <bool REV, bool kMarked, int n, int kStep>
+__device__ __forceinline__ Map join(const float (*N)[kWidth], const float (*H)[kWidth], uint32_t resets, int last, int quad) {
+    Map m = identity();
 #pragma unroll
-    for (int n = 1; n < 4; n *= 2) {
-        const Map e = from_lane(m, (REV ? lane + 8 * n : lane - 8 * n) & 31);
-        if (rank >= n) m = m.after(e);
+    for (int k = 0; k < n; ++k) {
+        const int r = REV ? n - 1 - k : k;
+        if (k < last) {
+            const Map e{load_f4(&N[r * kStep][quad * 4]), load_f4(&H[r * kStep][quad * 4])};
+            m = kMarked && (resets >> r & 1u) ? Map{e.after(m).N, e.H} : e.after(m);
+        }
     }
-    before = from_lane(m, (REV ? lane + 8 : lane - 8) & 31);
-    if (rank == 0) before = Map{zero4(), zero4(), false};
-    own = m;  // the last run's is the whole warp's
+    return m;
 }
-
-// Joins the warps' maps: what comes before this warp, and the tile's.
-template <bool REV>
-__device__ __forceinline__ void join_warps(const float (*D)[kWidth], const float (*H)[kWidth], uint32_t run_resets,
-                                           int warp, int quad, Map &before, Map &all) {
-    Map m{zero4(), zero4(), false};
+// Whether there is a reset among the first `last` of n rows.
+template <bool REV, int n> __device__ __forceinline__ bool reset_before(uint32_t resets, int last) {
+    return resets & (REV ? ~0u << (n - last) : (1u << last) - 1u) & ((1u << n) - 1u);
+}
+// A bit for each warp with a bit among its four runs.
+__device__ __forceinline__ uint32_t by_warp(uint32_t runs) {
+    uint32_t r = 0;
 #pragma unroll
-    for (int r = 0; r < kWarps; ++r) {
-        const int w = REV ? kWarps - 1 - r : r;
-        if (w == warp) before = m;
-        m = Map{load4(&D[w][quad * 4]), load4(&H[w][quad * 4]), (run_resets >> (4 * w) & 15u) != 0}.after(m);
-    }
-    all = m;
+    for (int w = 0; w < kWarps; ++w) r |= (uint32_t)((runs >> 4 * w & 15u) != 0) << w;
+    return r;
 }
 
-__device__ __forceinline__ float4 load_relaxed(const float *p) {
-    float4 v;
-    asm volatile("ld.relaxed.gpu.global.v4.f32 {%0, %1, %2, %3}, [%4];"
-                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "l"(p) : "memory");
+__device__ __forceinline__ F4 load_relaxed(const float *p) {
+    F4 v;
+    asm volatile("ld.relaxed.gpu.global.v2.b64 {%0, %1}, [%2];" : "=l"(v.p[0]), "=l"(v.p[1]) : "l"(p) : "memory");
     return v;
 }
-__device__ __forceinline__ void store_relaxed(float *p, const float4 &v) {
-    asm volatile("st.relaxed.gpu.global.v4.f32 [%0], {%1, %2, %3, %4};" ::"l"(p), "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w)
-                 : "memory");
+__device__ __forceinline__ void store_relaxed(float *p, const F4 &v) {
+    asm volatile("st.relaxed.gpu.global.v2.b64 [%0], {%1, %2};" ::"l"(p), "l"(v.p[0]), "l"(v.p[1]) : "memory");
 }
-__device__ __forceinline__ bool written(const float4 &v) {
-    return __float_as_uint(v.x) != kUnwritten && __float_as_uint(v.y) != kUnwritten &&
-           __float_as_uint(v.z) != kUnwritten && __float_as_uint(v.w) != kUnwritten;
+__device__ __forceinline__ bool written(const F4 &v) {
+    float f[4];
+    unpack4(v, f);
+    return __float_as_uint(f[0]) != kUnwritten && __float_as_uint(f[1]) != kUnwritten &&
+           __float_as_uint(f[2]) != kUnwritten && __float_as_uint(f[3]) != kUnwritten;
 }
 __device__ __forceinline__ int load_abort(const Ctl *ctl) {
     int v;
@@ -268,17 +263,17 @@ __device__ __forceinline__ int load_abort(const Ctl *ctl) {
 // top - l / 8 and top - 4 - l / 8. The words themselves say whether they have been written, each by
 // itself, so there are no flags and no fences: one trip to L2 gives both.
 struct Window {
-    float4 D[2], H[2], out[2];
+    F4 N[2], H[2], out[2];
     template <class Cell> __device__ __forceinline__ void load(const Chain &c, int top, Cell cell, int lane) {
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
             const int p = top - 4 * u - lane / 8;
             const float un = __uint_as_float(kUnwritten);
-            D[u] = H[u] = out[u] = make_float4(un, un, un, un);
+            N[u] = H[u] = out[u] = all4(un);
             if (p >= 0) {
                 const int64_t at = cell(p) * kWidth + lane % 8 * 4;
                 out[u] = load_relaxed(c.out + at);
-                D[u] = load_relaxed(c.D + at);
+                N[u] = load_relaxed(c.N + at);
                 H[u] = load_relaxed(c.H + at);
             }
         }
@@ -286,7 +281,7 @@ struct Window {
     // Bit n: place top - n is there (its state, or its map).
     __device__ __forceinline__ unsigned states() const { return places(written(out[0]), written(out[1])); }
     __device__ __forceinline__ unsigned maps() const {
-        return places(written(D[0]) && written(H[0]), written(D[1]) && written(H[1]));
+        return places(written(N[0]) && written(H[0]), written(N[1]) && written(H[1]));
     }
     static __device__ __forceinline__ unsigned places(bool v0, bool v1) {
         const unsigned b0 = __ballot_sync(0xffffffffu, v0), b1 = __ballot_sync(0xffffffffu, v1);
@@ -295,13 +290,13 @@ struct Window {
         for (int j = 0; j < 4; ++j) r |= (unsigned)((b0 >> 8 * j & 255u) == 255u) << j | (unsigned)((b1 >> 8 * j & 255u) == 255u) << (4 + j);
         return r;
     }
-    __device__ __forceinline__ float4 state(int n, int lane) const { return pick(out, n, lane); }
+    __device__ __forceinline__ F4 state(int n, int lane) const { return pick(out, n, lane); }
     // h through places top - n + 1 .. top
-    __device__ __forceinline__ float4 apply(int n, float4 h, int lane) const {
-        for (int k = n - 1; k >= 0; --k) h = keep(pick(D, k, lane), h) + pick(H, k, lane);
+    __device__ __forceinline__ F4 apply(int n, F4 h, int lane) const {
+        for (int k = n - 1; k >= 0; --k) h = Map{pick(N, k, lane), pick(H, k, lane)}.apply(h);
         return h;
     }
-    static __device__ __forceinline__ float4 pick(const float4 (&v)[2], int n, int lane) {
+    static __device__ __forceinline__ F4 pick(const F4 (&v)[2], int n, int lane) {
         return from_lane(n < 4 ? v[0] : v[1], n % 4 * 8 + lane % 8);
     }
 };
@@ -309,7 +304,7 @@ struct Window {
 // What reaches the tile at place `at` > 0 of its chain, by one warp, 4 channels a lane. cell(place)
 // is a place's index. False: the wait ran out (with `stall` it is made to).
 template <class Cell>
-__device__ bool look_back(const Chain &c, int at, Cell cell, int lane, uint64_t wait_ns, bool stall, float4 &h) {
+__device__ bool look_back(const Chain &c, int at, Cell cell, int lane, uint64_t wait_ns, bool stall, F4 &h) {
     Window w;
     int top = at - 1, n = 0;  // places top - n and later: the search's result
     uint64_t t0 = 0;
@@ -340,33 +335,35 @@ __device__ bool look_back(const Chain &c, int at, Cell cell, int lane, uint64_t 
     return true;
 }
 
-// One warp passes a tile on: publishes its map, waits for what reaches it (unless `known`), publishes
-// what leaves it. False: the wait ran out.
+// One warp passes a tile on: publishes its map (`reset`: its H is what leaves it, whatever comes),
+// waits for what reaches it (unless `known`), publishes what leaves it. False: the wait ran out.
 template <class Cell>
-__device__ bool pass_on(const Chain &c, int place, Cell cell, int lane, const Map &m, bool known, uint64_t wait_ns,
-                        bool stall, float4 &in) {
+__device__ bool pass_on(const Chain &c, int place, Cell cell, int lane, const Map &m, bool reset, bool known,
+                        uint64_t wait_ns, bool stall, F4 &in) {
     const int64_t own = cell(place) * kWidth + lane * 4;
     const bool publish = place < c.tiles - 1 && lane < 8;  // the last one's nobody reads
     if (publish) {
-        if (m.reset) store_relaxed(c.out + own, m.H);  // does not depend on what comes
-        else if (!known) {
-            store_relaxed(c.D + own, m.D);
+        if (reset) {
+            store_relaxed(c.out + own, m.H);
+        } else if (!known) {
+            store_relaxed(c.N + own, m.N);
             store_relaxed(c.H + own, m.H);
         }
     }
     if (!known && !look_back(c, place, cell, lane, wait_ns, stall, in)) return false;
-    if (publish && !m.reset) store_relaxed(c.out + own, m.apply(in));
+    if (publish && !reset) store_relaxed(c.out + own, m.apply(in));
     return true;
 }
 
 // Shared memory of a block, in front of its ring.
-template <int L, int STAGES> struct Shared {
+template <int L, int STAGES, bool BWD> struct Shared {
     uint64_t full[STAGES];
     int failed;
     Slot<L> slot[STAGES + 1];
-    alignas(16) float D[kWarps][kWidth], H[kWarps][kWidth];  // the warps' maps
-    alignas(16) float E[kWarps][kWidth], M[kWarps][kWidth];  // backward: those of the reverse scan
-    alignas(16) float in[kWidth];                            // what reaches the tile
+    // the runs' maps: N and H, backward also M with N along the reverse scan; then, in the last row of
+    // each warp's four (of M: in the first), the warps'
+    alignas(16) float N[kRuns][kWidth], H[kRuns][kWidth], M[BWD ? kRuns : 1][kWidth];
+    alignas(16) float in[kWidth];  // what reaches the tile
 };
 
 template <class Sh> __device__ void init_shared(Sh *sh, int stages) {
@@ -442,11 +439,11 @@ scan_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ C
     using G = Shape<T, false>;
     using V = Vec4<T>;
     constexpr int S = G::S, L = G::L, kPlane = G::kPlane / (int)sizeof(T);
-    using Sh = Shared<L, G::kStages>;
+    using Sh = Shared<L, G::kStages, false>;
     extern __shared__ __align__(128) unsigned char smem[];
     Sh *sh = reinterpret_cast<Sh *>(smem);
     unsigned char *ring = smem + (sizeof(Sh) + 127) / 128 * 128;
-    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, quad = lane % 8, run = warp * 4 + lane / 8;
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, quad = lane % 8, rank = lane / 8, run = warp * 4 + rank;
     if (threadIdx.x == 0) init_shared(sh, G::kStages);
     __syncthreads();
     if (c.ctl->bad) return;
@@ -455,104 +452,118 @@ scan_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ C
         for (int i = 0; i < G::kStages; ++i) loader.put(loader.take(lane), lane);
     volatile int *failed = &sh->failed;
     float *saved_initial = a.saved ? a.saved + (int64_t)((a.total + kSave<T> - 1) / kSave<T>) * a.channels : nullptr;
-    for (uint32_t it = 0;; ++it) {
-        const uint32_t s = it % G::kStages;
-        unsigned ticket = 0;
-        if (warp == kLoader) ticket = loader.take(lane);  // for the place that this tile leaves
-        const bool arrived = tc::mbar_wait(&sh->full[s], (it / G::kStages) & 1u, a.wait_ns + kWaitNs);
-        const Slot<L> &slot = sh->slot[it % G::kSlots];
-        const int task = arrived ? slot.task : 0;
-        if (task < 0) break;
-        if (!arrived) *failed = 1;
-        const int tile = task / c.groups, group = task % c.groups;
+
+    // One tile of the ring, number `it`. False: the block leaves.
+    const auto tile_step = [&](auto is_marked, const Slot<L> &slot, uint32_t it, unsigned ticket) {
+        constexpr bool kMarked = decltype(is_marked)::value;
+        const int task = slot.task, tile = task / c.groups, group = task % c.groups;
         const int ch = group * kWidth + quad * 4, t0 = tile * L + run * S;
         const bool live = ch < a.channels;
-        const uint32_t starts = slot.starts_of(run);
+        const uint32_t starts = kMarked ? slot.starts_of(run) : 0u;
+        const uint32_t resets = kMarked ? slot.run_starts : 0u;
+        const bool first = kMarked && slot.first();
 
         // this run's tokens from a state of zero: h, and how much is left of what comes before
-        float hl[S][4], A[S][4];
-        Map before_run, before_warp, all;
-        {
-            const T *in = reinterpret_cast<const T *>(ring + s * G::kStage) + run * S * kWidth + quad * 4;
-            float h[4] = {0.f, 0.f, 0.f, 0.f}, D[4] = {0.f, 0.f, 0.f, 0.f}, R[4] = {1.f, 1.f, 1.f, 1.f};
+        F4 hl[S], A[S];
+        Map m;
+        const T *in = reinterpret_cast<const T *>(ring + it % G::kStages * G::kStage) + run * S * kWidth + quad * 4;
+        const auto run_tokens = [&](auto is_exact, float &lowest) {
+            constexpr bool kExact = decltype(is_exact)::value;
+            m = identity();
+            F4 R = all4(1.f);
 #pragma unroll
             for (int i = 0; i < S; ++i) {
-                float x[4], ga[4], gb[4];
-                V::load(in + i * kWidth, x);
-                V::load(in + i * kWidth + kPlane, ga);
-                V::load(in + i * kWidth + 2 * kPlane, gb);
-                if (starts >> i & 1u) {
+                if (kMarked && (starts >> i & 1u)) {
                     const int id = slot.start_id[run * S + i];
-                    float4 v = zero4();
-                    if (a.h_ptrs && live) v = load4(reinterpret_cast<const float *>(a.h_ptrs[id]) + ch);
+                    m.H = zero4();
+                    if (a.h_ptrs && live) m.H = load_f4(reinterpret_cast<const float *>(a.h_ptrs[id]) + ch);
                     if (a.saved && live) {
-                        store4(saved_initial + (int64_t)id * a.channels + ch, v);
-                        if (i == 0 && t0 % kSave<T> == 0) store4(a.saved + (int64_t)(t0 / kSave<T>) * a.channels + ch, v);
+                        store_f4(saved_initial + (int64_t)id * a.channels + ch, m.H);
+                        if (i == 0 && t0 % kSave<T> == 0) store_f4(a.saved + (int64_t)(t0 / kSave<T>) * a.channels + ch, m.H);
                     }
-                    h[0] = v.x, h[1] = v.y, h[2] = v.z, h[3] = v.w;
                 }
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    float d, beta;
-                    gates(ga[e], gb[e], d, beta);
-                    h[e] = fmaf(beta, x[e], fmaf(-d, h[e], h[e]));
-                    D[e] = fmaf(d, R[e], D[e]);
-                    R[e] = 1.f - D[e];
-                    hl[i][e] = h[e];
-                    A[i][e] = R[e];
-                }
+                F4 nd, beta;
+                gates4<kExact>(widen4<T>(V::load_raw(in + i * kWidth + kPlane)),
+                               widen4<T>(V::load_raw(in + i * kWidth + 2 * kPlane)), nd, beta, lowest);
+                m.H = fma4(beta, widen4<T>(V::load_raw(in + i * kWidth)), left4(nd, m.H));
+                m.N = fma4(nd, R, m.N);
+                R = add4(m.N, all4(1.f));
+                hl[i] = m.H;
+                A[i] = R;
             }
-            Map own;
-            join_runs<false>(Map{make_float4(D[0], D[1], D[2], D[3]), make_float4(h[0], h[1], h[2], h[3]), starts != 0},
-                             lane, before_run, own);
-            if (lane >= 24) {
-                store4(&sh->D[warp][quad * 4], own.D);
-                store4(&sh->H[warp][quad * 4], own.H);
-            }
+        };
+        float lowest = 0.f;
+        run_tokens(std::false_type{}, lowest);
+        if (!gates_in_range(lowest)) run_tokens(std::true_type{}, lowest);
+        store_f4(&sh->N[run][quad * 4], m.N);
+        store_f4(&sh->H[run][quad * 4], m.H);
+        __syncwarp();
+        const uint32_t own_resets = resets >> 4 * warp & 15u;
+        const Map before_run = join<false, kMarked, 4, 1>(&sh->N[warp * 4], &sh->H[warp * 4], own_resets, rank, quad);
+        if (rank == 3) {
+            const Map w = m.after(before_run);
+            store_f4(&sh->N[run][quad * 4], w.N);
+            store_f4(&sh->H[run][quad * 4], kMarked && (own_resets & 8u) ? m.H : w.H);
         }
         __syncthreads();
-        if (*failed) {
-            if (warp == kLoader) loader.drain(it);
-            break;
-        }
+        if (*failed) return false;
         if (warp == kLoader) loader.put(ticket, lane);
 
-        join_warps<false>(sh->D, sh->H, slot.run_starts, warp, quad, before_warp, all);
+        const uint32_t warp_resets = kMarked ? by_warp(resets) : 0u;
         if (warp == kWarps - 1) {
-            float4 h = zero4();
-            if (slot.first() && live) {
+            const Map all = join<false, kMarked, kWarps, 4>(&sh->N[3], &sh->H[3], warp_resets, kWarps, quad);
+            F4 h = zero4();
+            if (first && live) {
                 const int id = slot.start_id[0];
-                if (a.h_ptrs) h = load4(reinterpret_cast<const float *>(a.h_ptrs[id]) + ch);
-                if (a.saved && lane < 8) store4(saved_initial + (int64_t)id * a.channels + ch, h);
+                if (a.h_ptrs) h = load_f4(reinterpret_cast<const float *>(a.h_ptrs[id]) + ch);
+                if (a.saved && lane < 8) store_f4(saved_initial + (int64_t)id * a.channels + ch, h);
             }
             const auto cell = [&](int place) { return (int64_t)place * c.groups + group; };
-            if (!pass_on(c, tile, cell, lane, all, slot.first(), a.wait_ns, a.debug_stall != 0, h))
+            if (!pass_on(c, tile, cell, lane, all, resets != 0, first, a.wait_ns, a.debug_stall != 0, h))
                 give_up(sh, c, lane, a.status);
-            if (lane < 8) store4(&sh->in[quad * 4], h);
+            if (lane < 8) store_f4(&sh->in[quad * 4], h);
         }
+        const Map before_warp = join<false, kMarked, kWarps - 1, 4>(&sh->N[3], &sh->H[3], warp_resets, warp, quad);
         __syncthreads();
-        if (*failed) {
-            if (warp == kLoader) loader.drain(it);
-            break;
-        }
+        if (*failed) return false;
 
         // the state that reaches this run, then its tokens'
-        const float4 v = before_run.apply(before_warp.apply(load4(&sh->in[quad * 4])));
-        if (a.saved && live && !(starts & 1u) && t0 % kSave<T> == 0 && t0 < a.total)
-            store4(a.saved + (int64_t)(t0 / kSave<T>) * a.channels + ch, v);
-        const float hin[4] = {v.x, v.y, v.z, v.w};
-        const uint32_t ends = Slot<L>::bits(slot.ends, run);
+        F4 v = load_f4(&sh->in[quad * 4]);
+        v = reset_before<false, kWarps>(warp_resets, warp) ? before_warp.H : before_warp.apply(v);
+        v = reset_before<false, 4>(own_resets, rank) ? before_run.H : before_run.apply(v);
+        if (a.saved && live && t0 % kSave<T> == 0 && (!kMarked || (!(starts & 1u) && t0 < a.total)))
+            store_f4(a.saved + (int64_t)(t0 / kSave<T>) * a.channels + ch, v);
+        const uint32_t ends = kMarked ? Slot<L>::bits(slot.ends, run) : 0u;
         T *yp = static_cast<T *>(a.y) + (int64_t)t0 * a.y_stride + ch;
         bool fresh = false;  // a stream has started in this run
 #pragma unroll
         for (int i = 0; i < S; ++i) {
-            if (starts >> i & 1u) fresh = true;
-            float y[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) y[e] = fresh ? hl[i][e] : fmaf(A[i][e], hin[e], hl[i][e]);
-            if (live && t0 + i < a.total) V::store(yp + i * a.y_stride, y);
-            if ((ends >> i & 1u) && a.h_ptrs && live)
-                Vec4<float>::store(reinterpret_cast<float *>(a.h_ptrs[slot.end_id[run * S + i]]) + ch, y);
+            if (kMarked && (starts >> i & 1u)) fresh = true;
+            const F4 y = kMarked && fresh ? hl[i] : fma4(A[i], v, hl[i]);
+            if (live && (!kMarked || t0 + i < a.total)) store_act4<T>(yp, y);
+            yp += a.y_stride;
+            if (kMarked && (ends >> i & 1u) && a.h_ptrs && live)
+                store_f4(reinterpret_cast<float *>(a.h_ptrs[slot.end_id[run * S + i]]) + ch, y);
+        }
+        return true;
+    };
+
+    for (uint32_t it = 0;; ++it) {
+        unsigned ticket = 0;
+        if (warp == kLoader) ticket = loader.take(lane);  // for the place that this tile leaves
+        const bool arrived = tc::mbar_wait(&sh->full[it % G::kStages], (it / G::kStages) & 1u, a.wait_ns + kWaitNs);
+        const Slot<L> &slot = sh->slot[it % G::kSlots];
+        if (arrived && slot.task < 0) break;
+        if (!arrived) {  // nothing of the tile is used; the others leave at their first barrier
+            *failed = 1;
+            __syncthreads();
+        }
+        const bool ok = !arrived ? false
+                        : slot.marked ? tile_step(std::true_type{}, slot, it, ticket)
+                                      : tile_step(std::false_type{}, slot, it, ticket);
+        if (!ok) {
+            if (warp == kLoader) loader.drain(it);
+            break;
         }
     }
 }
@@ -565,11 +576,11 @@ scan_backward_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_con
     using G = Shape<T, true>;
     using V = Vec4<T>;
     constexpr int S = G::S, L = G::L, kPlane = G::kPlane / (int)sizeof(T);
-    using Sh = Shared<L, G::kStages>;
+    using Sh = Shared<L, G::kStages, true>;
     extern __shared__ __align__(128) unsigned char smem[];
     Sh *sh = reinterpret_cast<Sh *>(smem);
     unsigned char *ring = smem + (sizeof(Sh) + 127) / 128 * 128;
-    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, quad = lane % 8, run = warp * 4 + lane / 8;
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, quad = lane % 8, rank = lane / 8, run = warp * 4 + rank;
     if (threadIdx.x == 0) init_shared(sh, G::kStages);
     __syncthreads();
     if (c.ctl->bad) return;
@@ -586,155 +597,142 @@ scan_backward_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_con
                     a.dh_final_ptrs ? reinterpret_cast<const float *>(a.dh_final_ptrs[s])[i] : 0.f;
         }
     }
-    for (uint32_t it = 0;; ++it) {
-        const uint32_t s = it % G::kStages;
-        unsigned ticket = 0;
-        if (warp == kLoader) ticket = loader.take(lane);
-        const bool arrived = tc::mbar_wait(&sh->full[s], (it / G::kStages) & 1u, a.wait_ns + kWaitNs);
-        const Slot<L> &slot = sh->slot[it % G::kSlots];
-        const int task = arrived ? slot.task : 0;
-        if (task < 0) break;
-        if (!arrived) *failed = 1;
-        const int tile = task / c.groups, group = task % c.groups;
+
+    const auto tile_step = [&](auto is_marked, const Slot<L> &slot, uint32_t it, unsigned ticket) {
+        constexpr bool kMarked = decltype(is_marked)::value;
+        const int task = slot.task, tile = task / c.groups, group = task % c.groups;
         const int ch = group * kWidth + quad * 4, t0 = tile * L + run * S;
         const bool live = ch < a.channels;
-        float4 h_in = zero4();  // the state that reaches the tile
-        if (live) h_in = load4(a.saved + (int64_t)tile * a.channels + ch);
-        const uint32_t starts = slot.starts_of(run), ends = slot.ends_of(run);
+        F4 h_in = zero4();  // the state that reaches the tile
+        if (live) h_in = load_f4(a.saved + (int64_t)tile * a.channels + ch);
+        const uint32_t starts = kMarked ? slot.starts_of(run) : 0u, ends = kMarked ? slot.ends_of(run) : 0u;
+        const uint32_t resets = kMarked ? slot.run_starts : 0u, end_resets = kMarked ? slot.run_ends : 0u;
         const auto initial = [&](int i) {  // state of the stream that starts at this run's token i
-            return live ? load4(saved_initial + (int64_t)slot.start_id[run * S + i] * a.channels + ch) : zero4();
+            return live ? load_f4(saved_initial + (int64_t)slot.start_id[run * S + i] * a.channels + ch) : zero4();
         };
         const auto final_gradient = [&](int at) {  // of the stream that ends at the tile's token `at`
-            return a.dh_final_ptrs && live ? load4(reinterpret_cast<const float *>(a.dh_final_ptrs[slot.end_id[at]]) + ch)
+            return a.dh_final_ptrs && live ? load_f4(reinterpret_cast<const float *>(a.dh_final_ptrs[slot.end_id[at]]) + ch)
                                            : zero4();
         };
 
-        float d[S][4], beta[S][4];
+        F4 nd[S], beta[S];
         typename V::Raw xr[S], dyr[S];
-        Map h_run, h_warp, m_run, m_warp, all;
-        {
-            const T *in = reinterpret_cast<const T *>(ring + s * G::kStage) + run * S * kWidth + quad * 4;
-            float h[4] = {0.f, 0.f, 0.f, 0.f}, m[4] = {0.f, 0.f, 0.f, 0.f}, D[4] = {0.f, 0.f, 0.f, 0.f};
+        const T *in = reinterpret_cast<const T *>(ring + it % G::kStages * G::kStage) + run * S * kWidth + quad * 4;
+        float lowest = 0.f;
 #pragma unroll
-            for (int i = 0; i < S; ++i) {
-                float x[4], ga[4], gb[4];
-                xr[i] = V::load_raw(in + i * kWidth);
-                V::load(in + i * kWidth + kPlane, ga);
-                V::load(in + i * kWidth + 2 * kPlane, gb);
-                dyr[i] = V::load_raw(in + i * kWidth + 3 * kPlane);
-                V::widen(xr[i], x);
-                if (starts >> i & 1u) {
-                    const float4 v = initial(i);
-                    h[0] = v.x, h[1] = v.y, h[2] = v.z, h[3] = v.w;
-                }
+        for (int i = 0; i < S; ++i)
+            gates4<false>(widen4<T>(V::load_raw(in + i * kWidth + kPlane)),
+                          widen4<T>(V::load_raw(in + i * kWidth + 2 * kPlane)), nd[i], beta[i], lowest);
+        if (!gates_in_range(lowest)) {
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    gates(ga[e], gb[e], d[i][e], beta[i][e]);
-                    h[e] = fmaf(beta[i][e], x[e], fmaf(-d[i][e], h[e], h[e]));
-                    D[e] = fmaf(d[i][e], 1.f - D[e], D[e]);
-                }
-            }
-#pragma unroll
-            for (int i = S - 1; i >= 0; --i) {
-                float dy[4];
-                V::widen(dyr[i], dy);
-                if (ends >> i & 1u) {
-                    const float4 v = final_gradient(run * S + i);
-                    m[0] = v.x, m[1] = v.y, m[2] = v.z, m[3] = v.w;
-                }
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const float lam = dy[e] + m[e];
-                    m[e] = fmaf(-d[i][e], lam, lam);
-                }
-            }
-            const float4 Dv = make_float4(D[0], D[1], D[2], D[3]);
-            Map own;
-            join_runs<false>(Map{Dv, make_float4(h[0], h[1], h[2], h[3]), starts != 0}, lane, h_run, own);
-            if (lane >= 24) {
-                store4(&sh->D[warp][quad * 4], own.D);
-                store4(&sh->H[warp][quad * 4], own.H);
-            }
-            join_runs<true>(Map{Dv, make_float4(m[0], m[1], m[2], m[3]), ends != 0}, lane, m_run, own);
-            if (lane < 8) {
-                store4(&sh->E[warp][quad * 4], own.D);
-                store4(&sh->M[warp][quad * 4], own.H);
-            }
+            for (int i = 0; i < S; ++i)
+                gates4<true>(widen4<T>(V::load_raw(in + i * kWidth + kPlane)),
+                             widen4<T>(V::load_raw(in + i * kWidth + 2 * kPlane)), nd[i], beta[i], lowest);
         }
+        Map h = identity();  // of this run, forward; with m.H in place of h.H, along the reverse scan
+        F4 R = all4(1.f), m = zero4();
+#pragma unroll
+        for (int i = 0; i < S; ++i) {
+            xr[i] = V::load_raw(in + i * kWidth);
+            if (kMarked && (starts >> i & 1u)) h.H = initial(i);
+            h.H = fma4(beta[i], widen4<T>(xr[i]), left4(nd[i], h.H));
+            h.N = fma4(nd[i], R, h.N);
+            R = add4(h.N, all4(1.f));
+        }
+#pragma unroll
+        for (int i = S - 1; i >= 0; --i) {
+            dyr[i] = V::load_raw(in + i * kWidth + 3 * kPlane);
+            if (kMarked && (ends >> i & 1u)) m = final_gradient(run * S + i);
+            m = left4(nd[i], add4(widen4<T>(dyr[i]), m));
+        }
+        store_f4(&sh->N[run][quad * 4], h.N);
+        store_f4(&sh->H[run][quad * 4], h.H);
+        store_f4(&sh->M[run][quad * 4], m);
+        __syncwarp();
+        const uint32_t own_resets = resets >> 4 * warp & 15u, own_ends = end_resets >> 4 * warp & 15u;
+        const Map h_run = join<false, kMarked, 4, 1>(&sh->N[warp * 4], &sh->H[warp * 4], own_resets, rank, quad);
+        const Map m_run = join<true, kMarked, 4, 1>(&sh->N[warp * 4], &sh->M[warp * 4], own_ends, 3 - rank, quad);
+        __syncwarp();
+        if (rank == 3) {
+            const Map w = h.after(h_run);
+            store_f4(&sh->N[run][quad * 4], w.N);
+            store_f4(&sh->H[run][quad * 4], kMarked && (own_resets & 8u) ? h.H : w.H);
+        }
+        if (rank == 0) store_f4(&sh->M[run][quad * 4], kMarked && (own_ends & 1u) ? m : Map{h.N, m}.apply(m_run.H));
         __syncthreads();
-        if (*failed) {
-            if (warp == kLoader) loader.drain(it);
-            break;
-        }
+        if (*failed) return false;
         if (warp == kLoader) loader.put(ticket, lane);
 
-        join_warps<true>(sh->E, sh->M, slot.run_ends, warp, quad, m_warp, all);
+        const uint32_t warp_resets = kMarked ? by_warp(resets) : 0u, warp_ends = kMarked ? by_warp(end_resets) : 0u;
         if (warp == 0) {
-            float4 m = zero4();
-            if (slot.last()) m = final_gradient(L - 1);
+            const Map all = join<true, kMarked, kWarps, 4>(&sh->N[3], &sh->M[0], warp_ends, kWarps, quad);
+            const bool last = kMarked && slot.last();
+            F4 v = zero4();
+            if (last) v = final_gradient(L - 1);
             const auto cell = [&](int place) { return (int64_t)(c.tiles - 1 - place) * c.groups + group; };
             const int place = c.tiles - 1 - tile;
             // behind the chain's first place there is nothing: the last stream ends in it
-            if (!pass_on(c, place, cell, lane, all, slot.last() || place == 0, a.wait_ns, a.debug_stall != 0, m))
+            if (!pass_on(c, place, cell, lane, all, end_resets != 0, last || place == 0, a.wait_ns, a.debug_stall != 0, v))
                 give_up(sh, c, lane, a.status);
-            if (lane < 8) store4(&sh->in[quad * 4], m);
+            if (lane < 8) store_f4(&sh->in[quad * 4], v);
         }
+        const Map m_warp = join<true, kMarked, kWarps - 1, 4>(&sh->N[3 + 4], &sh->M[4], warp_ends >> 1, kWarps - 1 - warp, quad);
         // meanwhile the others (and warp 0 after it) have the states before their tokens
-        join_warps<false>(sh->D, sh->H, slot.run_starts, warp, quad, h_warp, all);
-        float hp[S][4];
+        const Map h_warp = join<false, kMarked, kWarps - 1, 4>(&sh->N[3], &sh->H[3], warp_resets, warp, quad);
+        F4 hp[S];
         {
-            const float4 v = h_run.apply(h_warp.apply(h_in));
-            float h[4] = {v.x, v.y, v.z, v.w};
+            F4 v = reset_before<false, kWarps>(warp_resets, warp) ? h_warp.H : h_warp.apply(h_in);
+            v = reset_before<false, 4>(own_resets, rank) ? h_run.H : h_run.apply(v);
 #pragma unroll
             for (int i = 0; i < S; ++i) {
-                float x[4];
-                V::widen(xr[i], x);
-                if (starts >> i & 1u) {
-                    const float4 u = initial(i);
-                    h[0] = u.x, h[1] = u.y, h[2] = u.z, h[3] = u.w;
-                }
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    hp[i][e] = h[e];
-                    h[e] = fmaf(beta[i][e], x[e], fmaf(-d[i][e], h[e], h[e]));
-                }
+                if (kMarked && (starts >> i & 1u)) v = initial(i);
+                hp[i] = v;
+                v = fma4(beta[i], widen4<T>(xr[i]), left4(nd[i], v));
             }
         }
         __syncthreads();
-        if (*failed) {
-            if (warp == kLoader) loader.drain(it);
-            break;
-        }
+        if (*failed) return false;
 
-        const float4 v = m_run.apply(m_warp.apply(load4(&sh->in[quad * 4])));
-        float m[4] = {v.x, v.y, v.z, v.w};
-        const uint32_t all_starts = Slot<L>::bits(slot.starts, run);
-        T *dxp = static_cast<T *>(a.dx) + (int64_t)t0 * a.dx_stride + ch;
-        T *dap = static_cast<T *>(a.dab) + (int64_t)t0 * a.dab_stride + ch;
+        F4 v = load_f4(&sh->in[quad * 4]);
+        v = reset_before<true, kWarps>(warp_ends, kWarps - 1 - warp) ? m_warp.H : m_warp.apply(v);
+        v = reset_before<true, 4>(own_ends, 3 - rank) ? m_run.H : m_run.apply(v);
+        const uint32_t all_starts = kMarked ? Slot<L>::bits(slot.starts, run) : 0u;
+        T *dxp = static_cast<T *>(a.dx) + (int64_t)(t0 + S - 1) * a.dx_stride + ch;
+        T *dap = static_cast<T *>(a.dab) + (int64_t)(t0 + S - 1) * a.dab_stride + ch;
 #pragma unroll
         for (int i = S - 1; i >= 0; --i) {
-            float x[4], dy[4], dx[4], da[4], db[4];
-            V::widen(xr[i], x);
-            V::widen(dyr[i], dy);
-            if (ends >> i & 1u) {
-                const float4 u = final_gradient(run * S + i);
-                m[0] = u.x, m[1] = u.y, m[2] = u.z, m[3] = u.w;
+            if (kMarked && (ends >> i & 1u)) v = final_gradient(run * S + i);
+            const F4 lam = add4(widen4<T>(dyr[i]), v), dx = mul4(lam, beta[i]);
+            v = left4(nd[i], lam);
+            if (live && (!kMarked || t0 + i < a.total)) {
+                store_act4<T>(dxp, dx);
+                store_act4<T>(dap, mul4(mul4(v, hp[i]), nd[i]));
+                store_act4<T>(dap + a.channels, mul4(mul4(dx, widen4<T>(xr[i])), fma4(beta[i], all4(-1.f), all4(1.f))));
             }
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const float lam = dy[e] + m[e], left = fmaf(-d[i][e], lam, lam);
-                dx[e] = lam * beta[i][e];
-                db[e] = dx[e] * x[e] * (1.f - beta[i][e]);
-                da[e] = -left * hp[i][e] * d[i][e];
-                m[e] = left;
-            }
-            if (live && t0 + i < a.total) {
-                V::store(dxp + i * a.dx_stride, dx);
-                V::store(dap + i * a.dab_stride, da);
-                V::store(dap + i * a.dab_stride + a.channels, db);
-            }
-            if ((all_starts >> i & 1u) && a.dh0_ptrs && live)
-                Vec4<float>::store(reinterpret_cast<float *>(a.dh0_ptrs[slot.start_id[run * S + i]]) + ch, m);
+            dxp -= a.dx_stride;
+            dap -= a.dab_stride;
+            if (kMarked && (all_starts >> i & 1u) && a.dh0_ptrs && live)
+                store_f4(reinterpret_cast<float *>(a.dh0_ptrs[slot.start_id[run * S + i]]) + ch, v);
+        }
+        return true;
+    };
+
+    for (uint32_t it = 0;; ++it) {
+        unsigned ticket = 0;
+        if (warp == kLoader) ticket = loader.take(lane);
+        const bool arrived = tc::mbar_wait(&sh->full[it % G::kStages], (it / G::kStages) & 1u, a.wait_ns + kWaitNs);
+        const Slot<L> &slot = sh->slot[it % G::kSlots];
+        if (arrived && slot.task < 0) break;
+        if (!arrived) {  // nothing of the tile is used; the others leave at their first barrier
+            *failed = 1;
+            __syncthreads();
+        }
+        const bool ok = !arrived ? false
+                        : slot.marked ? tile_step(std::true_type{}, slot, it, ticket)
+                                      : tile_step(std::false_type{}, slot, it, ticket);
+        if (!ok) {
+            if (warp == kLoader) loader.drain(it);
+            break;
         }
     }
 }
@@ -757,7 +755,7 @@ template <typename T, bool BWD, class Kernel, class Launch>
 cudaError_t start(Kernel kernel, const int32_t *cu, int B, int total, const Chain &c, int *status, cudaStream_t st,
                   Launch launch) {
     using G = Shape<T, BWD>;
-    const size_t smem = (sizeof(Shared<G::L, G::kStages>) + 127) / 128 * 128 + G::kStages * G::kStage;
+    const size_t smem = (sizeof(Shared<G::L, G::kStages, BWD>) + 127) / 128 * 128 + G::kStages * G::kStage;
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
     const int64_t cells = (int64_t)c.tiles * c.groups, clear = (cells * kWidth * 3 / 4 + 1023) / 1024;

@@ -47,12 +47,11 @@ __global__ void __launch_bounds__(kThreads) gated_step_kernel(const GatedStepArg
                 x[e] = silu(p[e]);
             }
         }
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            float d, beta;
-            gates(ga[e], gb[e], d, beta);
-            hv[e] = gated_update(hv[e], d, beta * x[e]);
-        }
+        F4 nd, beta;
+        float lowest = 0.f;
+        gates4<false>(pack4(ga), pack4(gb), nd, beta, lowest);
+        if (!gates_in_range(lowest)) gates4<true>(pack4(ga), pack4(gb), nd, beta, lowest);
+        unpack4(fma4(beta, pack4(x), left4(nd, pack4(hv))), hv);
         Vec4<float>::store(h, hv);
         V::store((T *)a.y + s * a.y_stride + c, hv);
     }
