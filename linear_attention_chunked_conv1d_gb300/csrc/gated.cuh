@@ -47,40 +47,24 @@ template <typename T> __device__ __forceinline__ void store_act4(T *p, const F4 
 // exp(-softplus(a)) is 1 + nd. The kernels carry d, which is exact to a few units in its last place
 // however small it is, and never the rounded 1 - d: h - d h keeps the time constant of a channel that
 // remembers thousands of tokens, where a decay rounded to 24 bits would be off by up to 2^-25 at every
-// token, the same way each time.
-// One reciprocal serves both gates (the special function unit is the scarce one: 3 instead of 4
-// operations a gate pair): with p = -(1 + e^-a), q = 1 + e^-b, r = 1 / (p q): -d = r q, beta = r p.
-// That holds while p q is in range (|a| and |b| together below 87); `lowest` gathers the least p q,
-// for gates_in_range to tell. kExact: a reciprocal for each gate, right for every value: infinite
-// gates give exactly 0 or 1.
-template <bool kExact>
-__device__ __forceinline__ void gates4(const F4 &a, const F4 &b, F4 &nd, F4 &beta, float &lowest) {
+// token, the same way each time. Infinite gates give exactly 0 or 1.
+// (One reciprocal of the product (1 + e^-a)(1 + e^-b) for both gates saves a special function but
+// needs a second way for gates beyond its range, and with it the scan's registers no longer sufficed:
+// 1.15 ms instead of 0.69 for 262,144 x 2048, the chains left out.)
+__device__ __forceinline__ void gates4(const F4 &a, const F4 &b, F4 &nd, F4 &beta) {
     const F4 l = all4(-kLog2e), one = all4(1.f), minus = all4(-1.f);
-    float ea[4], eb[4];
-    unpack4(mul4(a, l), ea);
-    unpack4(mul4(b, l), eb);
+    float p[4], q[4];
+    unpack4(mul4(a, l), p);
+    unpack4(mul4(b, l), q);
 #pragma unroll
-    for (int e = 0; e < 4; ++e) ea[e] = ex2_approx(ea[e]), eb[e] = ex2_approx(eb[e]);
-    const F4 p = fma4(pack4(ea), minus, minus), q = add4(pack4(eb), one);
-    float r[4];
-    if (kExact) {
-        float s[4];
-        unpack4(p, r);
-        unpack4(q, s);
+    for (int e = 0; e < 4; ++e) p[e] = ex2_approx(p[e]), q[e] = ex2_approx(q[e]);
+    unpack4(fma4(pack4(p), minus, minus), p);
+    unpack4(add4(pack4(q), one), q);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) r[e] = rcp_approx(r[e]), s[e] = rcp_approx(s[e]);
-        nd = pack4(r);
-        beta = pack4(s);
-    } else {
-        unpack4(mul4(p, q), r);
-        lowest = fminf(lowest, fminf(fminf(r[0], r[1]), fminf(r[2], r[3])));
-#pragma unroll
-        for (int e = 0; e < 4; ++e) r[e] = rcp_approx(r[e]);
-        nd = mul4(pack4(r), q);
-        beta = mul4(pack4(r), p);
-    }
+    for (int e = 0; e < 4; ++e) p[e] = rcp_approx(p[e]), q[e] = rcp_approx(q[e]);
+    nd = pack4(p);
+    beta = pack4(q);
 }
-__device__ __forceinline__ bool gates_in_range(float lowest) { return lowest > -0x1p126f; }
 
 // (1 - d) h, rounded once, so that a gate near 1 forgets a large state without its rounding errors
 // staying behind.

@@ -59,7 +59,8 @@ template <typename T, bool BWD> struct Shape {
     static constexpr int L = S * kRuns;
     static constexpr int kPlane = L * kWidth * (int)sizeof(T);           // bytes of one input's tile
     static constexpr int kStage = kIn * kPlane;                          // 48 KB forward, 32 KB backward
-    static constexpr int kStages = BWD ? 3 : 2;
+    static constexpr int kStages = 2;
+    static constexpr int kBlocks = 2;                                    // on an SM
     // A slot is read until its tile is done, one tile longer than its copies are.
     static constexpr int kSlots = kStages + 1;
 };
@@ -80,6 +81,7 @@ constexpr uint32_t kUnwritten = 0xffffffffu;
 
 struct Chain {
     Ctl *ctl;
+    int *first;          // [tiles]: the stream of the tile's first token; ~: tokens are marked (Slot)
     float *N, *H, *out;  // [tiles][groups][32]: the tile's map, the state that leaves it
     int tiles, groups;
 };
@@ -90,7 +92,8 @@ template <typename T, bool BWD> Chain make_chain(void *workspace, int total, int
     c.groups = (channels + kWidth - 1) / kWidth;
     const int64_t words = (int64_t)c.tiles * c.groups * kWidth;
     c.ctl = static_cast<Ctl *>(workspace);
-    c.N = reinterpret_cast<float *>(c.ctl + 1);
+    c.first = reinterpret_cast<int *>(c.ctl + 1);
+    c.N = reinterpret_cast<float *>(c.first + (c.tiles + 3) / 4 * 4);
     c.H = c.N + words;
     c.out = c.H + words;
     return c;
@@ -98,26 +101,7 @@ template <typename T, bool BWD> Chain make_chain(void *workspace, int total, int
 
 template <typename T, bool BWD> size_t chain_bytes(int total, int channels) {
     const Chain c = make_chain<T, BWD>(nullptr, total, channels);
-    return sizeof(Ctl) + (size_t)c.tiles * c.groups * kWidth * 12;
-}
-
-// Clears the chains; block 0 also looks at every offset.
-__global__ void chain_init_kernel(const int32_t *cu, int B, int total, Chain c, int *status) {
-    const int64_t quads = (int64_t)c.tiles * c.groups * kWidth * 3 / 4;
-    uint4 *p = reinterpret_cast<uint4 *>(c.N);
-    for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < quads; i += (int64_t)gridDim.x * blockDim.x)
-        p[i] = make_uint4(kUnwritten, kUnwritten, kUnwritten, kUnwritten);
-    if (blockIdx.x) return;
-    int bad = 0;
-    if (cu) {
-        if (threadIdx.x == 0) bad = cu[0] != 0 || cu[B] != total;
-        for (int s = threadIdx.x; s < B; s += blockDim.x) bad |= cu[s + 1] < cu[s];
-    }
-    bad = __syncthreads_or(bad);
-    if (threadIdx.x == 0) {
-        *c.ctl = Ctl{bad, 0, 0u, 0};
-        if (bad) raise_status(status, LA_DEV_BAD_SEQLENS);
-    }
+    return sizeof(Ctl) + (size_t)(c.tiles + 3) / 4 * 16 + (size_t)c.tiles * c.groups * kWidth * 12;
 }
 
 // Where the streams start and end in the packed rows.
@@ -127,16 +111,46 @@ struct Streams {
     __device__ __forceinline__ int start(int s) const { return cu ? cu[s] : s * T_each; }
 };
 
+// Clears the chains and looks up every tile's first stream; block 0 also looks at every offset.
+__global__ void chain_init_kernel(Streams st, int L, Chain c, int *status) {
+    const int64_t quads = (int64_t)c.tiles * c.groups * kWidth * 3 / 4;
+    const int64_t t = (int64_t)blockIdx.x * blockDim.x + threadIdx.x, step = (int64_t)gridDim.x * blockDim.x;
+    for (int64_t i = t; i < c.tiles; i += step) {
+        const int t0 = (int)i * L;
+        int lo = 0, hi = st.B;  // the last stream that starts at or before t0 is in [lo, hi)
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) / 2;
+            if (st.start(mid) <= t0) lo = mid; else hi = mid;
+        }
+        const bool whole = st.start(lo) < t0 && st.start(lo + 1) > t0 + L;  // inside one stream
+        c.first[i] = whole ? lo : ~lo;
+    }
+    uint4 *p = reinterpret_cast<uint4 *>(c.N);
+    for (int64_t i = t; i < quads; i += step) p[i] = make_uint4(kUnwritten, kUnwritten, kUnwritten, kUnwritten);
+    if (blockIdx.x) return;
+    int bad = 0;
+    if (st.cu) {
+        if (threadIdx.x == 0) bad = st.cu[0] != 0 || st.cu[st.B] != st.total;
+        for (int s = threadIdx.x; s < st.B; s += blockDim.x) bad |= st.cu[s + 1] < st.cu[s];
+    }
+    bad = __syncthreads_or(bad);
+    if (threadIdx.x == 0) {
+        *c.ctl = Ctl{bad, 0, 0u, 0};
+        if (bad) raise_status(status, LA_DEV_BAD_SEQLENS);
+    }
+}
+
 // A tile in the ring: which one it is, and where in it streams start and end.
 template <int L> struct Slot {
     static constexpr int S = L / kRuns;
     int task;                               // tile * groups + group; -1: no more
+    bool marked;                            // some token is (the last tile's last one always)
     uint32_t starts[L / 32], ends[L / 32];  // a bit for each token
     // A bit for each run with a start (an end) in it. A start at the tile's first token and an end
     // at its last are apart: there the state (gradient) that reaches the tile is the stream's own.
     uint32_t run_starts, run_ends;
-    bool marked;                            // some token is, or lies past the last one
-    int start_id[L], end_id[L];             // the streams of the marked tokens
+    int start_id[L];                        // the streams of the marked starts
+    int run_id[kRuns];                      // the stream of each run's first token
 
     __device__ __forceinline__ bool first() const { return starts[0] & 1u; }
     __device__ __forceinline__ bool last() const { return ends[L / 32 - 1] >> 31; }
@@ -148,19 +162,15 @@ template <int L> struct Slot {
     static __device__ __forceinline__ uint32_t bits(const uint32_t *mask, int run) {
         return mask[run * S / 32] >> (run * S % 32) & ((1u << S) - 1u);
     }
+    // the stream of a run's token i
+    __device__ __forceinline__ int id(int run, int i) const {
+        const uint32_t before = bits(starts, run) & ((2u << i) - 1u);
+        return before ? start_id[run * S + 31 - __clz(before)] : run_id[run];
+    }
 };
 
-// The whole warp fills in a slot for tokens t0 .. t0 + L - 1.
-template <int L> __device__ void find_streams(const Streams &st, int t0, int lane, Slot<L> *slot) {
-    // last stream that starts at or before t0: 32 probes a round
-    int lo = 0, hi = st.B;  // it is in [lo, hi)
-    while (hi - lo > 1) {
-        const int step = (hi - lo + 31) / 32, at = lo + lane * step;
-        const unsigned le = __ballot_sync(0xffffffffu, at < hi && st.start(at) <= t0);
-        const int last = 31 - __clz(le);  // lane 0's probe always holds
-        lo += last * step;
-        hi = min(hi, lo + step);
-    }
+// The whole warp marks the tokens t0 .. t0 + L - 1 of a slot; `lo` is the stream of the first one.
+template <int L> __device__ void mark_streams(const Streams &st, int lo, int t0, int lane, Slot<L> *slot) {
     if (lane < L / 32) slot->starts[lane] = slot->ends[lane] = 0;
     __syncwarp();
     for (int s0 = lo; s0 < st.B; s0 += 32) {
@@ -174,10 +184,7 @@ template <int L> __device__ void find_streams(const Streams &st, int t0, int lan
                     atomicOr(&slot->starts[(b - t0) >> 5], 1u << ((b - t0) & 31));
                     slot->start_id[b - t0] = s;
                 }
-                if (e > t0 && e <= t0 + L) {
-                    atomicOr(&slot->ends[(e - 1 - t0) >> 5], 1u << ((e - 1 - t0) & 31));
-                    slot->end_id[e - 1 - t0] = s;
-                }
+                if (e > t0 && e <= t0 + L) atomicOr(&slot->ends[(e - 1 - t0) >> 5], 1u << ((e - 1 - t0) & 31));
             }
         }
         if (__any_sync(0xffffffffu, b >= t0 + L || s >= st.B)) break;
@@ -185,12 +192,18 @@ template <int L> __device__ void find_streams(const Streams &st, int t0, int lan
     __syncwarp();
     const unsigned rs = __ballot_sync(0xffffffffu, slot->starts_of(lane) != 0);
     const unsigned re = __ballot_sync(0xffffffffu, slot->ends_of(lane) != 0);
-    const bool marked = __any_sync(0xffffffffu, lane < L / 32 && (slot->starts[lane] | slot->ends[lane]));
-    if (lane == 0) {
-        slot->run_starts = rs;
-        slot->run_ends = re;
-        slot->marked = marked || t0 + L > st.total;
+    if (lane == 0) slot->run_starts = rs, slot->run_ends = re;
+    static_assert(kRuns == 32, "a lane for each run");
+    const int at = lane * (L / kRuns);  // the run's first token: the last start at or before it
+    int id = lo;
+    for (int w = at / 32; w >= 0; --w) {
+        const uint32_t m = slot->starts[w] & (w == at / 32 ? (2u << at % 32) - 1u : ~0u);
+        if (m) {
+            id = slot->start_id[w * 32 + 31 - __clz(m)];
+            break;
+        }
     }
+    slot->run_id[lane] = id;
     __syncwarp();
 }
 
@@ -198,9 +211,6 @@ __device__ __forceinline__ void mbar_arrive(uint64_t *bar) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(tc::smem_u32(bar)) : "memory");
 }
 __device__ __forceinline__ F4 zero4() { return all4(0.f); }
-__device__ __forceinline__ F4 from_lane(const F4 &v, int lane) {
-    return F4{{__shfl_sync(0xffffffffu, v.p[0], lane), __shfl_sync(0xffffffffu, v.p[1], lane)}};
-}
 
 // h -> h + N h + H of some tokens.
 struct Map {
@@ -239,78 +249,86 @@ __device__ __forceinline__ uint32_t by_warp(uint32_t runs) {
     return r;
 }
 
-__device__ __forceinline__ F4 load_relaxed(const float *p) {
-    F4 v;
-    asm volatile("ld.relaxed.gpu.global.v2.b64 {%0, %1}, [%2];" : "=l"(v.p[0]), "=l"(v.p[1]) : "l"(p) : "memory");
-    return v;
+__device__ __forceinline__ void store_relaxed(float *p, float v) {
+    asm volatile("st.relaxed.gpu.global.f32 [%0], %1;" ::"l"(p), "f"(v) : "memory");
 }
-__device__ __forceinline__ void store_relaxed(float *p, const F4 &v) {
-    asm volatile("st.relaxed.gpu.global.v2.b64 [%0], {%1, %2};" ::"l"(p), "l"(v.p[0]), "l"(v.p[1]) : "memory");
-}
-__device__ __forceinline__ bool written(const F4 &v) {
-    float f[4];
-    unpack4(v, f);
-    return __float_as_uint(f[0]) != kUnwritten && __float_as_uint(f[1]) != kUnwritten &&
-           __float_as_uint(f[2]) != kUnwritten && __float_as_uint(f[3]) != kUnwritten;
-}
+__device__ __forceinline__ bool written(float v) { return __float_as_uint(v) != kUnwritten; }
 __device__ __forceinline__ int load_abort(const Ctl *ctl) {
     int v;
     asm volatile("ld.relaxed.gpu.global.b32 %0, [%1];" : "=r"(v) : "l"(&ctl->abort) : "memory");
     return v;
 }
 
-// Eight places of a chain, `top` and those before it: lane l has 4 channels (l % 8) of places
-// top - l / 8 and top - 4 - l / 8. The words themselves say whether they have been written, each by
-// itself, so there are no flags and no fences: one trip to L2 gives both.
+// Passing a tile's state on is the work of one warp, with one channel a lane: few registers, next to
+// those that hold its tokens.
+
+// The joined map of all warps of a tile (as join, for one channel).
+template <bool REV, bool kMarked>
+__device__ __forceinline__ void join_all(const float (*N)[kWidth], const float (*H)[kWidth], uint32_t resets, int lane,
+                                         float &n, float &h) {
+    n = h = 0.f;
+#pragma unroll
+    for (int k = 0; k < kWarps; ++k) {
+        const int r = REV ? kWarps - 1 - k : k;
+        const float en = N[r * 4][lane], eh = H[r * 4][lane];
+        n = fmaf(en, n, n + en);
+        h = kMarked && (resets >> r & 1u) ? eh : fmaf(en, h, h) + eh;
+    }
+}
+
+// Eight places of a chain in shared memory, `top` and those before it, as one warp finds them in L2.
+// The words themselves say whether they have been written, each by itself, so there are no flags and
+// no fences, and the copies can start before their answer is needed.
 struct Window {
-    F4 N[2], H[2], out[2];
-    template <class Cell> __device__ __forceinline__ void load(const Chain &c, int top, Cell cell, int lane) {
+    float N[8][kWidth], H[8][kWidth], out[8][kWidth];
+
+    template <class Cell> __device__ __forceinline__ void fetch(const Chain &c, int top, Cell cell, int lane) {
+        const int quad = lane % 8 * 4;
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
-            const int p = top - 4 * u - lane / 8;
-            const float un = __uint_as_float(kUnwritten);
-            N[u] = H[u] = out[u] = all4(un);
+            const int n = 4 * u + lane / 8, p = top - n;
             if (p >= 0) {
-                const int64_t at = cell(p) * kWidth + lane % 8 * 4;
-                out[u] = load_relaxed(c.out + at);
-                N[u] = load_relaxed(c.N + at);
-                H[u] = load_relaxed(c.H + at);
+                const int64_t at = cell(p) * kWidth + quad;
+                copy(&out[n][quad], c.out + at);
+                copy(&N[n][quad], c.N + at);
+                copy(&H[n][quad], c.H + at);
+            } else {
+                store_f4(&out[n][quad], all4(__uint_as_float(kUnwritten)));
+                store_f4(&N[n][quad], all4(__uint_as_float(kUnwritten)));
             }
         }
     }
-    // Bit n: place top - n is there (its state, or its map).
-    __device__ __forceinline__ unsigned states() const { return places(written(out[0]), written(out[1])); }
-    __device__ __forceinline__ unsigned maps() const {
-        return places(written(N[0]) && written(H[0]), written(N[1]) && written(H[1]));
+    static __device__ __forceinline__ void copy(float *to, const float *from) {
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(tc::smem_u32(to)), "l"(from) : "memory");
     }
-    static __device__ __forceinline__ unsigned places(bool v0, bool v1) {
-        const unsigned b0 = __ballot_sync(0xffffffffu, v0), b1 = __ballot_sync(0xffffffffu, v1);
-        unsigned r = 0;
+    // Waits for the copies. Bit n of the answer: place top - n has its state there; bit 8 + n: its map.
+    __device__ __forceinline__ unsigned look(int lane) const {
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        __syncwarp();
+        unsigned there = 0;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) r |= (unsigned)((b0 >> 8 * j & 255u) == 255u) << j | (unsigned)((b1 >> 8 * j & 255u) == 255u) << (4 + j);
-        return r;
+        for (int n = 0; n < 8; ++n) {
+            if (written(out[n][lane])) there |= 1u << n;
+            if (written(N[n][lane]) && written(H[n][lane])) there |= 256u << n;
+        }
+        return __reduce_and_sync(0xffffffffu, there);
     }
-    __device__ __forceinline__ F4 state(int n, int lane) const { return pick(out, n, lane); }
     // h through places top - n + 1 .. top
-    __device__ __forceinline__ F4 apply(int n, F4 h, int lane) const {
-        for (int k = n - 1; k >= 0; --k) h = Map{pick(N, k, lane), pick(H, k, lane)}.apply(h);
+    __device__ __forceinline__ float apply(int n, float h, int lane) const {
+        for (int k = n - 1; k >= 0; --k) h = fmaf(N[k][lane], h, h) + H[k][lane];
         return h;
-    }
-    static __device__ __forceinline__ F4 pick(const F4 (&v)[2], int n, int lane) {
-        return from_lane(n < 4 ? v[0] : v[1], n % 4 * 8 + lane % 8);
     }
 };
 
-// What reaches the tile at place `at` > 0 of its chain, by one warp, 4 channels a lane. cell(place)
-// is a place's index. False: the wait ran out (with `stall` it is made to).
+// What reaches the tile at place `at` > 0 of its chain. cell(place) is a place's index; `w` has been
+// told to fetch the places before `at`. False: the wait ran out (with `stall` it is made to).
 template <class Cell>
-__device__ bool look_back(const Chain &c, int at, Cell cell, int lane, uint64_t wait_ns, bool stall, F4 &h) {
-    Window w;
-    int top = at - 1, n = 0;  // places top - n and later: the search's result
+__device__ __forceinline__ bool look_back(Window &w, const Chain &c, int at, Cell cell, int lane, uint64_t wait_ns,
+                                          bool stall, float &h) {
+    int top = at - 1, n = 0;  // place top - n is the search's result
     uint64_t t0 = 0;
     for (uint32_t i = 0;; ++i) {
-        w.load(c, top, cell, lane);
-        const unsigned states = stall ? 0u : w.states(), maps = stall ? 0u : w.maps();
+        const unsigned there = stall ? 0u : w.look(lane), states = there & 255u, maps = there >> 8;
         const unsigned nearer = states ? (states & -states) - 1 : 255u;
         if ((maps & nearer) == nearer) {
             if (states) {
@@ -318,40 +336,42 @@ __device__ bool look_back(const Chain &c, int at, Cell cell, int lane, uint64_t 
                 break;
             }
             top -= 8;  // place 0 has a state and no map: the search never passes it
-            continue;
-        }
-        if ((i & 15) == 15) {
+        } else if ((i & 15) == 15) {
             const uint64_t now = tc::globaltimer_ns();
             if (!t0) t0 = now;
             if (__any_sync(0xffffffffu, now - t0 > wait_ns || load_abort(c.ctl))) return false;
         }
+        __syncwarp();
+        w.fetch(c, top, cell, lane);
     }
-    h = w.apply(n, w.state(n, lane), lane);
+    h = w.apply(n, w.out[n][lane], lane);
     while (top < at - 1) {  // on to `at` through the windows that the search has seen
         top += 8;
-        w.load(c, top, cell, lane);
+        __syncwarp();
+        w.fetch(c, top, cell, lane);
+        w.look(lane);
         h = w.apply(8, h, lane);
     }
     return true;
 }
 
-// One warp passes a tile on: publishes its map (`reset`: its H is what leaves it, whatever comes),
+// Publishes the map (n, h) of the tile at `place` (`reset`: its h is what leaves it, whatever comes),
 // waits for what reaches it (unless `known`), publishes what leaves it. False: the wait ran out.
 template <class Cell>
-__device__ bool pass_on(const Chain &c, int place, Cell cell, int lane, const Map &m, bool reset, bool known,
-                        uint64_t wait_ns, bool stall, F4 &in) {
-    const int64_t own = cell(place) * kWidth + lane * 4;
-    const bool publish = place < c.tiles - 1 && lane < 8;  // the last one's nobody reads
+__device__ __forceinline__ bool pass_on(Window &w, const Chain &c, int place, Cell cell, int lane, float n, float h,
+                                        bool reset, bool known, uint64_t wait_ns, bool stall, float &in) {
+    const int64_t own = cell(place) * kWidth + lane;
+    const bool publish = place < c.tiles - 1;  // the last one's nobody reads
     if (publish) {
         if (reset) {
-            store_relaxed(c.out + own, m.H);
+            store_relaxed(c.out + own, h);
         } else if (!known) {
-            store_relaxed(c.N + own, m.N);
-            store_relaxed(c.H + own, m.H);
+            store_relaxed(c.N + own, n);
+            store_relaxed(c.H + own, h);
         }
     }
-    if (!known && !look_back(c, place, cell, lane, wait_ns, stall, in)) return false;
-    if (publish && !reset) store_relaxed(c.out + own, m.apply(in));
+    if (!known && !look_back(w, c, place, cell, lane, wait_ns, stall, in)) return false;
+    if (publish && !reset) store_relaxed(c.out + own, fmaf(n, in, in) + h);
     return true;
 }
 
@@ -364,6 +384,7 @@ template <int L, int STAGES, bool BWD> struct Shared {
     // each warp's four (of M: in the first), the warps'
     alignas(16) float N[kRuns][kWidth], H[kRuns][kWidth], M[BWD ? kRuns : 1][kWidth];
     alignas(16) float in[kWidth];  // what reaches the tile
+    alignas(16) Window window;
 };
 
 template <class Sh> __device__ void init_shared(Sh *sh, int stages) {
@@ -382,17 +403,27 @@ template <typename T, bool BWD, class Sh> struct Loader {
     Chain c;
     uint32_t issued;  // tiles put into the ring, the end among them
 
-    // Takes the next tile of the chains, in their order (lane 0's answer counts).
-    __device__ __forceinline__ unsigned take(int lane) const {
-        return lane == 0 ? atomicAdd(&c.ctl->ticket, 1u) : 0u;
+    // Tiles are taken one ahead, and their first streams looked up, so that nothing waits for either.
+    unsigned ticket;  // taken, not yet put (lane 0's)
+    int first;        // of it
+
+    __device__ __forceinline__ int tile_of(unsigned t) const {
+        const int place = (int)(t / c.groups);
+        return BWD ? c.tiles - 1 - place : place;
     }
-    // Starts its copies into the ring's next place and fills in the slot.
-    __device__ void put(unsigned ticket, int lane) {
+    __device__ __forceinline__ unsigned tasks() const { return (unsigned)(c.tiles * c.groups); }
+    // Takes the next tile of the chains, in their order.
+    __device__ __forceinline__ unsigned take(int lane) const { return lane == 0 ? atomicAdd(&c.ctl->ticket, 1u) : 0u; }
+    __device__ __forceinline__ void look_up(int lane) {
+        first = lane == 0 && ticket < tasks() ? __ldg(&c.first[tile_of(ticket)]) : 0;
+    }
+    // Starts the copies of the tile last taken into the ring's next place and fills in the slot.
+    __device__ void put(int lane) {
         const uint32_t s = issued % G::kStages;
         auto &slot = sh->slot[issued % G::kSlots];
         ++issued;
-        ticket = __shfl_sync(0xffffffffu, ticket, 0);
-        if (ticket >= (unsigned)(c.tiles * c.groups)) {
+        const unsigned t = __shfl_sync(0xffffffffu, ticket, 0);
+        if (t >= tasks()) {
             if (lane == 0) {
                 slot.task = -1;
                 mbar_arrive(&sh->full[s]);
@@ -400,8 +431,7 @@ template <typename T, bool BWD, class Sh> struct Loader {
             }
             return;
         }
-        const int place = (int)(ticket / c.groups), group = (int)(ticket % c.groups);
-        const int tile = BWD ? c.tiles - 1 - place : place;
+        const int group = (int)(t % c.groups), tile = tile_of(t);
         if (lane == 0) {
             tc::mbar_expect_tx(&sh->full[s], G::kStage);
             const uint32_t to = tc::smem_u32(ring + s * G::kStage);
@@ -410,10 +440,22 @@ template <typename T, bool BWD, class Sh> struct Loader {
             tc::tma_load_2d(to + 2 * G::kPlane, b, group * kWidth, tile * G::L, &sh->full[s]);
             if (BWD) tc::tma_load_2d(to + 3 * G::kPlane, dy, group * kWidth, tile * G::L, &sh->full[s]);
         }
-        find_streams<G::L>(streams, tile * G::L, lane, &slot);
+        const int lo = __shfl_sync(0xffffffffu, first, 0);
+        if (lo < 0) mark_streams<G::L>(streams, ~lo, tile * G::L, lane, &slot);
         if (lane == 0) {
+            slot.marked = lo < 0;
             slot.task = tile * c.groups + group;
             mbar_arrive(&sh->full[s]);
+        }
+    }
+    // Fills the ring, and takes one tile more.
+    __device__ void begin(int lane) {
+        ticket = take(lane);
+        for (int i = 0; i < G::kStages; ++i) {
+            look_up(lane);
+            const unsigned next = take(lane);
+            put(lane);
+            ticket = next;
         }
     }
     // A block that leaves early waits for the copies it has started; those up to number `it` have
@@ -433,7 +475,7 @@ template <class Sh> __device__ __forceinline__ void give_up(Sh *sh, const Chain 
 }
 
 template <typename T>
-__global__ void __launch_bounds__(kThreads, 2)
+__global__ void __launch_bounds__(kThreads, Shape<T, false>::kBlocks)
 scan_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_a,
             const __grid_constant__ CUtensorMap map_b, const GatedScanArgs a, const Chain c) {
     using G = Shape<T, false>;
@@ -447,14 +489,13 @@ scan_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ C
     if (threadIdx.x == 0) init_shared(sh, G::kStages);
     __syncthreads();
     if (c.ctl->bad) return;
-    Loader<T, false, Sh> loader{sh, ring, &map_x, &map_a, &map_b, nullptr, Streams{a.cu, a.B, a.T_each, a.total}, c, 0};
-    if (warp == kLoader)
-        for (int i = 0; i < G::kStages; ++i) loader.put(loader.take(lane), lane);
+    Loader<T, false, Sh> loader{sh, ring, &map_x, &map_a, &map_b, nullptr, Streams{a.cu, a.B, a.T_each, a.total}, c, 0, 0, 0};
+    if (warp == kLoader) loader.begin(lane);
     volatile int *failed = &sh->failed;
     float *saved_initial = a.saved ? a.saved + (int64_t)((a.total + kSave<T> - 1) / kSave<T>) * a.channels : nullptr;
 
     // One tile of the ring, number `it`. False: the block leaves.
-    const auto tile_step = [&](auto is_marked, const Slot<L> &slot, uint32_t it, unsigned ticket) {
+    const auto tile_step = [&](auto is_marked, const Slot<L> &slot, uint32_t it, unsigned next) {
         constexpr bool kMarked = decltype(is_marked)::value;
         const int task = slot.task, tile = task / c.groups, group = task % c.groups;
         const int ch = group * kWidth + quad * 4, t0 = tile * L + run * S;
@@ -462,66 +503,64 @@ scan_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ C
         const uint32_t starts = kMarked ? slot.starts_of(run) : 0u;
         const uint32_t resets = kMarked ? slot.run_starts : 0u;
         const bool first = kMarked && slot.first();
+        const auto cell = [&](int place) { return (int64_t)place * c.groups + group; };
+        /*FETCH_A*/
 
         // this run's tokens from a state of zero: h, and how much is left of what comes before
         F4 hl[S], A[S];
-        Map m;
         const T *in = reinterpret_cast<const T *>(ring + it % G::kStages * G::kStage) + run * S * kWidth + quad * 4;
-        const auto run_tokens = [&](auto is_exact, float &lowest) {
-            constexpr bool kExact = decltype(is_exact)::value;
-            m = identity();
-            F4 R = all4(1.f);
+        Map m = identity();
+        F4 R = all4(1.f);
 #pragma unroll
-            for (int i = 0; i < S; ++i) {
-                if (kMarked && (starts >> i & 1u)) {
-                    const int id = slot.start_id[run * S + i];
-                    m.H = zero4();
-                    if (a.h_ptrs && live) m.H = load_f4(reinterpret_cast<const float *>(a.h_ptrs[id]) + ch);
-                    if (a.saved && live) {
-                        store_f4(saved_initial + (int64_t)id * a.channels + ch, m.H);
-                        if (i == 0 && t0 % kSave<T> == 0) store_f4(a.saved + (int64_t)(t0 / kSave<T>) * a.channels + ch, m.H);
-                    }
+        for (int i = 0; i < S; ++i) {
+            if (kMarked && (starts >> i & 1u)) {
+                const int id = slot.start_id[run * S + i];
+                m.H = zero4();
+                if (a.h_ptrs && live) m.H = load_f4(reinterpret_cast<const float *>(a.h_ptrs[id]) + ch);
+                if (a.saved && live) {
+                    store_f4(saved_initial + (int64_t)id * a.channels + ch, m.H);
+                    if (i == 0 && t0 % kSave<T> == 0) store_f4(a.saved + (int64_t)(t0 / kSave<T>) * a.channels + ch, m.H);
                 }
-                F4 nd, beta;
-                gates4<kExact>(widen4<T>(V::load_raw(in + i * kWidth + kPlane)),
-                               widen4<T>(V::load_raw(in + i * kWidth + 2 * kPlane)), nd, beta, lowest);
-                m.H = fma4(beta, widen4<T>(V::load_raw(in + i * kWidth)), left4(nd, m.H));
-                m.N = fma4(nd, R, m.N);
-                R = add4(m.N, all4(1.f));
-                hl[i] = m.H;
-                A[i] = R;
             }
-        };
-        float lowest = 0.f;
-        run_tokens(std::false_type{}, lowest);
-        if (!gates_in_range(lowest)) run_tokens(std::true_type{}, lowest);
+            F4 nd, beta;
+            gates4(widen4<T>(V::load_raw(in + i * kWidth + kPlane)), widen4<T>(V::load_raw(in + i * kWidth + 2 * kPlane)),
+                   nd, beta);
+            m.H = fma4(beta, widen4<T>(V::load_raw(in + i * kWidth)), left4(nd, m.H));
+            m.N = fma4(nd, R, m.N);
+            R = add4(m.N, all4(1.f));
+            hl[i] = m.H;
+            A[i] = R;
+        }
+        if (warp == kWarps - 1) sh->window.fetch(c, tile - 1, cell, lane);  // in good time for look_back
         store_f4(&sh->N[run][quad * 4], m.N);
         store_f4(&sh->H[run][quad * 4], m.H);
         __syncwarp();
         const uint32_t own_resets = resets >> 4 * warp & 15u;
-        const Map before_run = join<false, kMarked, 4, 1>(&sh->N[warp * 4], &sh->H[warp * 4], own_resets, rank, quad);
         if (rank == 3) {
-            const Map w = m.after(before_run);
+            const Map w = m.after(join<false, kMarked, 3, 1>(&sh->N[warp * 4], &sh->H[warp * 4], own_resets, 3, quad));
             store_f4(&sh->N[run][quad * 4], w.N);
             store_f4(&sh->H[run][quad * 4], kMarked && (own_resets & 8u) ? m.H : w.H);
         }
         __syncthreads();
         if (*failed) return false;
-        if (warp == kLoader) loader.put(ticket, lane);
+        if (warp == kLoader) {  // the place that this tile has left
+            loader.put(lane);
+            loader.ticket = next;
+        }
 
         const uint32_t warp_resets = kMarked ? by_warp(resets) : 0u;
         if (warp == kWarps - 1) {
-            const Map all = join<false, kMarked, kWarps, 4>(&sh->N[3], &sh->H[3], warp_resets, kWarps, quad);
-            F4 h = zero4();
-            if (first && live) {
+            float n, h, v = 0.f;
+            join_all<false, kMarked>(&sh->N[3], &sh->H[3], warp_resets, lane, n, h);
+            const int lane_ch = group * kWidth + lane;
+            if (first && lane_ch < a.channels) {
                 const int id = slot.start_id[0];
-                if (a.h_ptrs) h = load_f4(reinterpret_cast<const float *>(a.h_ptrs[id]) + ch);
-                if (a.saved && lane < 8) store_f4(saved_initial + (int64_t)id * a.channels + ch, h);
+                if (a.h_ptrs) v = reinterpret_cast<const float *>(a.h_ptrs[id])[lane_ch];
+                if (a.saved) saved_initial[(int64_t)id * a.channels + lane_ch] = v;
             }
-            const auto cell = [&](int place) { return (int64_t)place * c.groups + group; };
-            if (!pass_on(c, tile, cell, lane, all, resets != 0, first, a.wait_ns, a.debug_stall != 0, h))
+            if (!pass_on(sh->window, c, tile, cell, lane, n, h, resets != 0, first, a.wait_ns, a.debug_stall != 0, v))
                 give_up(sh, c, lane, a.status);
-            if (lane < 8) store_f4(&sh->in[quad * 4], h);
+            sh->in[lane] = v;
         }
         const Map before_warp = join<false, kMarked, kWarps - 1, 4>(&sh->N[3], &sh->H[3], warp_resets, warp, quad);
         __syncthreads();
@@ -530,6 +569,7 @@ scan_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ C
         // the state that reaches this run, then its tokens'
         F4 v = load_f4(&sh->in[quad * 4]);
         v = reset_before<false, kWarps>(warp_resets, warp) ? before_warp.H : before_warp.apply(v);
+        const Map before_run = join<false, kMarked, 3, 1>(&sh->N[warp * 4], &sh->H[warp * 4], own_resets, rank, quad);
         v = reset_before<false, 4>(own_resets, rank) ? before_run.H : before_run.apply(v);
         if (a.saved && live && t0 % kSave<T> == 0 && (!kMarked || (!(starts & 1u) && t0 < a.total)))
             store_f4(a.saved + (int64_t)(t0 / kSave<T>) * a.channels + ch, v);
@@ -543,14 +583,17 @@ scan_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ C
             if (live && (!kMarked || t0 + i < a.total)) store_act4<T>(yp, y);
             yp += a.y_stride;
             if (kMarked && (ends >> i & 1u) && a.h_ptrs && live)
-                store_f4(reinterpret_cast<float *>(a.h_ptrs[slot.end_id[run * S + i]]) + ch, y);
+                store_f4(reinterpret_cast<float *>(a.h_ptrs[slot.id(run, i)]) + ch, y);
         }
         return true;
     };
 
     for (uint32_t it = 0;; ++it) {
-        unsigned ticket = 0;
-        if (warp == kLoader) ticket = loader.take(lane);  // for the place that this tile leaves
+        unsigned next = 0;
+        if (warp == kLoader) {
+            loader.look_up(lane);
+            next = loader.take(lane);
+        }
         const bool arrived = tc::mbar_wait(&sh->full[it % G::kStages], (it / G::kStages) & 1u, a.wait_ns + kWaitNs);
         const Slot<L> &slot = sh->slot[it % G::kSlots];
         if (arrived && slot.task < 0) break;
@@ -559,8 +602,8 @@ scan_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ C
             __syncthreads();
         }
         const bool ok = !arrived ? false
-                        : slot.marked ? tile_step(std::true_type{}, slot, it, ticket)
-                                      : tile_step(std::false_type{}, slot, it, ticket);
+                        : slot.marked ? tile_step(std::true_type{}, slot, it, next)
+                                      : tile_step(std::false_type{}, slot, it, next);
         if (!ok) {
             if (warp == kLoader) loader.drain(it);
             break;
@@ -569,7 +612,7 @@ scan_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ C
 }
 
 template <typename T>
-__global__ void __launch_bounds__(kThreads, 2)
+__global__ void __launch_bounds__(kThreads, Shape<T, true>::kBlocks)
 scan_backward_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_a,
                      const __grid_constant__ CUtensorMap map_b, const __grid_constant__ CUtensorMap map_dy,
                      const GatedScanBwdArgs a, const Chain c) {
@@ -584,9 +627,8 @@ scan_backward_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_con
     if (threadIdx.x == 0) init_shared(sh, G::kStages);
     __syncthreads();
     if (c.ctl->bad) return;
-    Loader<T, true, Sh> loader{sh, ring, &map_x, &map_a, &map_b, &map_dy, Streams{a.cu, a.B, a.T_each, a.total}, c, 0};
-    if (warp == kLoader)
-        for (int i = 0; i < G::kStages; ++i) loader.put(loader.take(lane), lane);
+    Loader<T, true, Sh> loader{sh, ring, &map_x, &map_a, &map_b, &map_dy, Streams{a.cu, a.B, a.T_each, a.total}, c, 0, 0, 0};
+    if (warp == kLoader) loader.begin(lane);
     volatile int *failed = &sh->failed;
     const float *saved_initial = a.saved + (int64_t)c.tiles * a.channels;
     if (a.cu && a.dh0_ptrs) {  // the gradient passes through an empty stream
@@ -598,11 +640,14 @@ scan_backward_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_con
         }
     }
 
-    const auto tile_step = [&](auto is_marked, const Slot<L> &slot, uint32_t it, unsigned ticket) {
+    const auto tile_step = [&](auto is_marked, const Slot<L> &slot, uint32_t it, unsigned next) {
         constexpr bool kMarked = decltype(is_marked)::value;
         const int task = slot.task, tile = task / c.groups, group = task % c.groups;
         const int ch = group * kWidth + quad * 4, t0 = tile * L + run * S;
         const bool live = ch < a.channels;
+        const auto cell = [&](int place) { return (int64_t)(c.tiles - 1 - place) * c.groups + group; };
+        const int place = c.tiles - 1 - tile;
+        /*FETCH_A*/
         F4 h_in = zero4();  // the state that reaches the tile
         if (live) h_in = load_f4(a.saved + (int64_t)tile * a.channels + ch);
         const uint32_t starts = kMarked ? slot.starts_of(run) : 0u, ends = kMarked ? slot.ends_of(run) : 0u;
@@ -610,25 +655,18 @@ scan_backward_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_con
         const auto initial = [&](int i) {  // state of the stream that starts at this run's token i
             return live ? load_f4(saved_initial + (int64_t)slot.start_id[run * S + i] * a.channels + ch) : zero4();
         };
-        const auto final_gradient = [&](int at) {  // of the stream that ends at the tile's token `at`
-            return a.dh_final_ptrs && live ? load_f4(reinterpret_cast<const float *>(a.dh_final_ptrs[slot.end_id[at]]) + ch)
+        const auto final_gradient = [&](int i) {  // of the stream that ends at this run's token i
+            return a.dh_final_ptrs && live ? load_f4(reinterpret_cast<const float *>(a.dh_final_ptrs[slot.id(run, i)]) + ch)
                                            : zero4();
         };
 
         F4 nd[S], beta[S];
         typename V::Raw xr[S], dyr[S];
         const T *in = reinterpret_cast<const T *>(ring + it % G::kStages * G::kStage) + run * S * kWidth + quad * 4;
-        float lowest = 0.f;
 #pragma unroll
         for (int i = 0; i < S; ++i)
-            gates4<false>(widen4<T>(V::load_raw(in + i * kWidth + kPlane)),
-                          widen4<T>(V::load_raw(in + i * kWidth + 2 * kPlane)), nd[i], beta[i], lowest);
-        if (!gates_in_range(lowest)) {
-#pragma unroll
-            for (int i = 0; i < S; ++i)
-                gates4<true>(widen4<T>(V::load_raw(in + i * kWidth + kPlane)),
-                             widen4<T>(V::load_raw(in + i * kWidth + 2 * kPlane)), nd[i], beta[i], lowest);
-        }
+            gates4(widen4<T>(V::load_raw(in + i * kWidth + kPlane)), widen4<T>(V::load_raw(in + i * kWidth + 2 * kPlane)),
+                   nd[i], beta[i]);
         Map h = identity();  // of this run, forward; with m.H in place of h.H, along the reverse scan
         F4 R = all4(1.f), m = zero4();
 #pragma unroll
@@ -642,9 +680,10 @@ scan_backward_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_con
 #pragma unroll
         for (int i = S - 1; i >= 0; --i) {
             dyr[i] = V::load_raw(in + i * kWidth + 3 * kPlane);
-            if (kMarked && (ends >> i & 1u)) m = final_gradient(run * S + i);
+            if (kMarked && (ends >> i & 1u)) m = final_gradient(i);
             m = left4(nd[i], add4(widen4<T>(dyr[i]), m));
         }
+        if (warp == 0) sh->window.fetch(c, place - 1, cell, lane);  // in good time for look_back
         store_f4(&sh->N[run][quad * 4], h.N);
         store_f4(&sh->H[run][quad * 4], h.H);
         store_f4(&sh->M[run][quad * 4], m);
@@ -661,20 +700,24 @@ scan_backward_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_con
         if (rank == 0) store_f4(&sh->M[run][quad * 4], kMarked && (own_ends & 1u) ? m : Map{h.N, m}.apply(m_run.H));
         __syncthreads();
         if (*failed) return false;
-        if (warp == kLoader) loader.put(ticket, lane);
+        if (warp == kLoader) {  // the place that this tile has left
+            loader.put(lane);
+            loader.ticket = next;
+        }
 
         const uint32_t warp_resets = kMarked ? by_warp(resets) : 0u, warp_ends = kMarked ? by_warp(end_resets) : 0u;
         if (warp == 0) {
-            const Map all = join<true, kMarked, kWarps, 4>(&sh->N[3], &sh->M[0], warp_ends, kWarps, quad);
+            float n, h, v = 0.f;
+            join_all<true, kMarked>(&sh->N[3], &sh->M[0], warp_ends, lane, n, h);
+            const int lane_ch = group * kWidth + lane;
             const bool last = kMarked && slot.last();
-            F4 v = zero4();
-            if (last) v = final_gradient(L - 1);
-            const auto cell = [&](int place) { return (int64_t)(c.tiles - 1 - place) * c.groups + group; };
-            const int place = c.tiles - 1 - tile;
+            if (last && a.dh_final_ptrs && lane_ch < a.channels)
+                v = reinterpret_cast<const float *>(a.dh_final_ptrs[slot.id(kRuns - 1, S - 1)])[lane_ch];
             // behind the chain's first place there is nothing: the last stream ends in it
-            if (!pass_on(c, place, cell, lane, all, end_resets != 0, last || place == 0, a.wait_ns, a.debug_stall != 0, v))
+            if (!pass_on(sh->window, c, place, cell, lane, n, h, end_resets != 0, last || place == 0, a.wait_ns,
+                         a.debug_stall != 0, v))
                 give_up(sh, c, lane, a.status);
-            if (lane < 8) store_f4(&sh->in[quad * 4], v);
+            sh->in[lane] = v;
         }
         const Map m_warp = join<true, kMarked, kWarps - 1, 4>(&sh->N[3 + 4], &sh->M[4], warp_ends >> 1, kWarps - 1 - warp, quad);
         // meanwhile the others (and warp 0 after it) have the states before their tokens
@@ -701,7 +744,7 @@ scan_backward_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_con
         T *dap = static_cast<T *>(a.dab) + (int64_t)(t0 + S - 1) * a.dab_stride + ch;
 #pragma unroll
         for (int i = S - 1; i >= 0; --i) {
-            if (kMarked && (ends >> i & 1u)) v = final_gradient(run * S + i);
+            if (kMarked && (ends >> i & 1u)) v = final_gradient(i);
             const F4 lam = add4(widen4<T>(dyr[i]), v), dx = mul4(lam, beta[i]);
             v = left4(nd[i], lam);
             if (live && (!kMarked || t0 + i < a.total)) {
@@ -718,8 +761,11 @@ scan_backward_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_con
     };
 
     for (uint32_t it = 0;; ++it) {
-        unsigned ticket = 0;
-        if (warp == kLoader) ticket = loader.take(lane);
+        unsigned next = 0;
+        if (warp == kLoader) {
+            loader.look_up(lane);
+            next = loader.take(lane);
+        }
         const bool arrived = tc::mbar_wait(&sh->full[it % G::kStages], (it / G::kStages) & 1u, a.wait_ns + kWaitNs);
         const Slot<L> &slot = sh->slot[it % G::kSlots];
         if (arrived && slot.task < 0) break;
@@ -728,8 +774,8 @@ scan_backward_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_con
             __syncthreads();
         }
         const bool ok = !arrived ? false
-                        : slot.marked ? tile_step(std::true_type{}, slot, it, ticket)
-                                      : tile_step(std::false_type{}, slot, it, ticket);
+                        : slot.marked ? tile_step(std::true_type{}, slot, it, next)
+                                      : tile_step(std::false_type{}, slot, it, next);
         if (!ok) {
             if (warp == kLoader) loader.drain(it);
             break;
@@ -752,16 +798,18 @@ bool tile_map(CUtensorMap *map, const void *base, int total, int channels, int64
 
 // Clears the chain, then starts as many blocks as fit (or as there are tiles).
 template <typename T, bool BWD, class Kernel, class Launch>
-cudaError_t start(Kernel kernel, const int32_t *cu, int B, int total, const Chain &c, int *status, cudaStream_t st,
+cudaError_t start(Kernel kernel, const Streams &streams, const Chain &c, int *status, cudaStream_t st,
                   Launch launch) {
     using G = Shape<T, BWD>;
-    const size_t smem = (sizeof(Shared<G::L, G::kStages, BWD>) + 127) / 128 * 128 + G::kStages * G::kStage;
+    constexpr size_t smem = (sizeof(Shared<G::L, G::kStages, BWD>) + 127) / 128 * 128 + G::kStages * G::kStage;
+    static_assert(G::kBlocks * (smem + 1024) <= 228 * 1024, "the blocks of an SM share its 228 KB, 1 KB of it each their own");
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
     const int64_t cells = (int64_t)c.tiles * c.groups, clear = (cells * kWidth * 3 / 4 + 1023) / 1024;
     const int sms = device_sms();
-    chain_init_kernel<<<(int)(clear < sms ? clear : sms), 1024, 0, st>>>(cu, B, total, c, status);
-    launch((int)(cells < 2 * sms ? cells : 2 * sms), smem);
+    chain_init_kernel<<<(int)(clear < sms ? clear : sms), 1024, 0, st>>>(streams, G::L, c, status);
+    const int room = G::kBlocks * sms;
+    launch((int)(cells < room ? cells : room), smem);
     return cudaGetLastError();
 }
 
@@ -773,7 +821,7 @@ template <typename T> cudaError_t scan(const GatedScanArgs &a, cudaStream_t st) 
         !tile_map<T, false>(&gb, ab + a.channels, a.total, a.channels, a.ab_stride))
         return cudaErrorInvalidValue;
     const Chain c = make_chain<T, false>(a.workspace, a.total, a.channels);
-    return start<T, false>(scan_kernel<T>, a.cu, a.B, a.total, c, a.status, st, [&](int grid, size_t smem) {
+    return start<T, false>(scan_kernel<T>, Streams{a.cu, a.B, a.T_each, a.total}, c, a.status, st, [&](int grid, size_t smem) {
         scan_kernel<T><<<grid, kThreads, smem, st>>>(x, ga, gb, a, c);
     });
 }
@@ -787,7 +835,7 @@ template <typename T> cudaError_t backward(const GatedScanBwdArgs &a, cudaStream
         !tile_map<T, true>(&dy, a.dy, a.total, a.channels, a.dy_stride))
         return cudaErrorInvalidValue;
     const Chain c = make_chain<T, true>(a.workspace, a.total, a.channels);
-    return start<T, true>(scan_backward_kernel<T>, a.cu, a.B, a.total, c, a.status, st, [&](int grid, size_t smem) {
+    return start<T, true>(scan_backward_kernel<T>, Streams{a.cu, a.B, a.T_each, a.total}, c, a.status, st, [&](int grid, size_t smem) {
         scan_backward_kernel<T><<<grid, kThreads, smem, st>>>(x, ga, gb, dy, a, c);
     });
 }

@@ -48,9 +48,7 @@ __global__ void __launch_bounds__(kThreads) gated_step_kernel(const GatedStepArg
             }
         }
         F4 nd, beta;
-        float lowest = 0.f;
-        gates4<false>(pack4(ga), pack4(gb), nd, beta, lowest);
-        if (!gates_in_range(lowest)) gates4<true>(pack4(ga), pack4(gb), nd, beta, lowest);
+        gates4(pack4(ga), pack4(gb), nd, beta);
         unpack4(fma4(beta, pack4(x), left4(nd, pack4(hv))), hv);
         Vec4<float>::store(h, hv);
         V::store((T *)a.y + s * a.y_stride + c, hv);
