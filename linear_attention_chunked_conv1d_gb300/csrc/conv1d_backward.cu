@@ -6,11 +6,12 @@
 //   dw_j = sum_t dp_t xh[t + j],  dbias = sum_t dp_t;
 // a row that the window of the next call holds also takes that window's gradient.
 //
-// One thread has 4 channels of a run of consecutive tokens of one stream, with the last K rows of xh
-// and of dp in registers: x and dout are read once (plus K-1 rows on each side of a run), dx is
-// written once. p is computed again, never stored. The sums over tokens are kept per run in 32 bits
-// and joined run by run in a fixed order by a second kernel, so they come out the same every time.
-#include "common.cuh"
+// HBM-bound: x and dout are read once (plus K-1 rows on each side of a run), dx is written once; p is
+// computed again, never stored. One thread has 4 channels, in packed pairs, of a run of consecutive
+// tokens of one stream, with the last K rows of xh and of dp in registers; some rows are loaded
+// before the first of them is used. The sums over tokens are kept per run in 32 bits and joined run by
+// run in a fixed order by a second kernel, so they come out the same every time.
+#include "gated.cuh"
 #include "launch.h"
 
 namespace la {
@@ -18,144 +19,195 @@ namespace la {
 namespace {
 
 constexpr int kThreads = 128;
-constexpr int kRows = 64;  // tokens of a run
+// Rows in flight per thread: what the registers of four blocks on an SM hold.
+template <typename T> constexpr int kAheadOf = sizeof(T) == 2 ? 8 : 4;
 
-struct Ctl {
-    int bad;  // an offset of cu_seqlens is out of order: nothing is computed
+// Tokens of a run: long ones read and write less for what runs share (K-1 rows at each end, the sums),
+// short ones make more blocks. The longest that still makes ten blocks for each of 152 SMs (four are
+// resident; a fixed number of SMs, so that sums do not depend on the device). 16384 x 6144 bf16 in
+// eight streams: runs of 256 168 us, of 128 154 us (taken), of 64 168 us; 100003 x 8192 in 32: 256
+// 1.00 ms (taken), 128 1.06, 64 1.19.
+__host__ __device__ inline int run_rows(int B, int total, int channels) {
+    const int64_t cols = (channels / 4 + kThreads - 1) / kThreads;
+    for (int rows = 256; rows > 64; rows /= 2)
+        if ((total / rows + B) * cols >= 10 * 152) return rows;
+    return 64;
+}
+
+struct Runs {
+    const int32_t *cu;  // or nullptr: B streams of T_each tokens
+    int B, T_each, total, rows;
+    __device__ __forceinline__ int start(int s) const { return cu ? cu[s] : s * T_each; }
+    // First run of stream s: every stream, an empty one too, has at least one.
+    __device__ __forceinline__ int base(int s) const { return cu ? cu[s] / rows + s : s * ((T_each + rows - 1) / rows); }
+    __host__ __device__ int slots() const { return cu ? total / rows + B : B * ((T_each + rows - 1) / rows); }
+    // Every thread of the block looks at its share of the offsets.
+    __device__ bool bad() const {
+        int b = 0;
+        if (cu) {
+            if (threadIdx.x == 0) b = cu[0] != 0 || cu[B] != total;
+            for (int s = threadIdx.x; s < B; s += blockDim.x) b |= cu[s + 1] < cu[s];
+        }
+        return __syncthreads_or(b);
+    }
 };
 
-__global__ void conv_bwd_init_kernel(const int32_t *cu, int B, int total, Ctl *ctl, int *status) {
-    int bad = 0;
-    if (threadIdx.x == 0) bad = cu[0] != 0 || cu[B] != total;
-    for (int s = threadIdx.x; s < B; s += blockDim.x) bad |= cu[s + 1] < cu[s];
-    bad = __syncthreads_or(bad);
-    if (threadIdx.x == 0) {
-        ctl->bad = bad;
-        if (bad) raise_status(status, LA_DEV_BAD_SEQLENS);
-    }
-}
-
-// First run of stream s: every stream, an empty one too, has at least one.
-__device__ __forceinline__ int run_base(const ConvBwdArgs &a, int s) {
-    return a.cu ? a.cu[s] / kRows + s : s * ((a.T_each + kRows - 1) / kRows);
-}
-
-__host__ __device__ inline int run_slots(int B, int T_each, int total, bool varlen) {
-    return varlen ? total / kRows + B : B * ((T_each + kRows - 1) / kRows);
-}
-
 template <typename T, int K>
-__global__ void __launch_bounds__(kThreads) conv_bwd_kernel(const ConvBwdArgs a, const Ctl *ctl, float *part) {
+__global__ void __launch_bounds__(kThreads, 4) conv_bwd_kernel(const ConvBwdArgs a, const Runs runs, float *part) {
     using V = Vec4<T>;
+    constexpr int kAhead = kAheadOf<T>;
+    if (runs.bad()) {
+        if (threadIdx.x == 0) raise_status(a.status, LA_DEV_BAD_SEQLENS);
+        return;
+    }
     const int c = (blockIdx.y * kThreads + threadIdx.x) * 4;
-    if (c >= a.channels || (a.cu && ctl->bad)) return;
+    if (c >= a.channels) return;
     const int slot = blockIdx.x;
     int s = 0, hi = a.B - 1;
-    while (s < hi) {  // last s with run_base(s) <= slot
+    while (s < hi) {  // last s with base(s) <= slot
         const int mid = (s + hi + 1) >> 1;
-        if (run_base(a, mid) <= slot) s = mid; else hi = mid - 1;
+        if (runs.base(mid) <= slot) s = mid; else hi = mid - 1;
     }
-    const int sb = a.cu ? a.cu[s] : s * a.T_each, se = a.cu ? a.cu[s + 1] : sb + a.T_each;
-    const int len = se - sb, run = slot - run_base(a, s);
+    const int sb = runs.start(s), se = runs.start(s + 1), len = se - sb, run = slot - runs.base(s);
     const int64_t C = a.channels;
-    const int r0 = sb + run * kRows, r1 = min(r0 + kRows, se);
+    const int r0 = sb + run * runs.rows, r1 = min(r0 + runs.rows, se);
+    const T *fin = a.dstate_final_ptrs ? reinterpret_cast<const T *>(a.dstate_final_ptrs[s]) + c : nullptr;
+    T *dst = a.dstate_ptrs ? reinterpret_cast<T *>(a.dstate_ptrs[s]) + c : nullptr;
 
-    float w[K][4], bias[4] = {0.f, 0.f, 0.f, 0.f}, dw[K][4] = {}, db[4] = {};
-    float win[K][4] = {}, dpw[K][4] = {};  // rows t-K+1 .. t of xh, and dp of the same tokens
-    if (r0 < se) {
+    F4 dw[K], db = all4(0.f);
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-#pragma unroll
-            for (int j = 0; j < K; ++j) w[j][e] = to_f(((const T *)a.w)[(c + e) * K + j]);
-        if (a.bias) V::load((const T *)a.bias + c, bias);
-    }
-    const T *fin = a.dstate_final_ptrs ? reinterpret_cast<const T *>(a.dstate_final_ptrs[s]) : nullptr;
-    T *dst = a.dstate_ptrs ? reinterpret_cast<T *>(a.dstate_ptrs[s]) : nullptr;
+    for (int j = 0; j < K; ++j) dw[j] = all4(0.f);
     if (len == 0 && dst) {  // the window passes through an empty stream
 #pragma unroll
-        for (int m = 0; m < K - 1; ++m) {
-            float v[4] = {};
-            if (fin) V::load(fin + m * C + c, v);
-            V::store(dst + m * C + c, v);
-        }
+        for (int m = 0; m < K - 1; ++m)
+            store_act4<T>(dst + m * C, fin ? widen4<T>(V::load_raw(fin + m * C)) : all4(0.f));
     }
     if (r0 < se) {
+        F4 w[K], bias = all4(0.f), win[K], dpw[K];  // win, dpw: rows t-K+1 .. t of xh and of dp
+        {
+            float f[K][4];
 #pragma unroll
-        for (int m = 0; m < K - 1; ++m) {
-            if (run == 0) V::load(reinterpret_cast<const T *>(a.state_ptrs[s]) + m * C + c, win[m + 1]);
-            else V::load((const T *)a.x + (r0 - (K - 1) + m) * a.x_stride + c, win[m + 1]);
+            for (int e = 0; e < 4; ++e)
+#pragma unroll
+                for (int j = 0; j < K; ++j) f[j][e] = to_f(((const T *)a.w)[(c + e) * K + j]);
+#pragma unroll
+            for (int j = 0; j < K; ++j) w[j] = pack4(f[j]), win[j] = dpw[j] = all4(0.f);
+            if (a.bias) bias = widen4<T>(V::load_raw((const T *)a.bias + c));
         }
-        for (int t = r0; t < r1 + K - 1; ++t) {
-            float x[4] = {}, dout[4] = {};
-            if (t < se) {
-                V::load((const T *)a.x + t * a.x_stride + c, x);
-                V::load((const T *)a.dout + t * a.dout_stride + c, dout);
+#pragma unroll
+        for (int m = 0; m < K - 1; ++m)
+            win[m + 1] = widen4<T>(V::load_raw(run == 0 ? reinterpret_cast<const T *>(a.state_ptrs[s]) + m * C + c
+                                                        : (const T *)a.x + (r0 - (K - 1) + m) * a.x_stride + c));
+        const F4 one = all4(1.f), minus = all4(-1.f), l2e = all4(-kLog2e);
+
+        // Token t: its dp, its part of the sums, and the gradient of row t - (K-1), complete now.
+        const auto token = [&](const F4 &x, const F4 &dout) {
+#pragma unroll
+            for (int j = 0; j < K - 1; ++j) win[j] = win[j + 1], dpw[j] = dpw[j + 1];
+            win[K - 1] = x;
+            F4 p = bias;
+#pragma unroll
+            for (int j = 0; j < K; ++j) p = fma4(w[j], win[j], p);
+            float f[4];
+            unpack4(mul4(p, l2e), f);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) f[e] = ex2_approx(f[e]);
+            unpack4(add4(pack4(f), one), f);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) f[e] = rcp_approx(f[e]);
+            const F4 sg = pack4(f);
+            dpw[K - 1] = mul4(mul4(dout, sg), fma4(p, fma4(sg, minus, one), one));
+        };
+        const auto add = [&](const F4 &dp) {
+            db = add4(db, dp);
+#pragma unroll
+            for (int j = 0; j < K; ++j) dw[j] = fma4(dp, win[j], dw[j]);
+        };
+        const auto row = [&]() {
+            F4 g = mul4(w[K - 1], dpw[0]);
+#pragma unroll
+            for (int n = 1; n < K; ++n) g = fma4(w[K - 1 - n], dpw[n], g);
+            return g;
+        };
+
+        const T *xp = (const T *)a.x + r0 * a.x_stride + c, *dp = (const T *)a.dout + r0 * a.dout_stride + c;
+        T *dxp = (T *)a.dx + (r0 - (K - 1)) * a.dx_stride + c;
+        const int last = min(r1 + K - 1, se);  // tokens that the run's rows depend on
+        for (int t0 = r0; t0 < r1 + K - 1; t0 += kAhead) {
+            typename V::Raw xr[kAhead], dr[kAhead];
+            const bool whole = t0 >= r0 + K - 1 && t0 + kAhead <= r1;  // every row of these is the run's own
+#pragma unroll
+            for (int q = 0; q < kAhead; ++q) {
+                const bool there = whole || t0 + q < last;
+                xr[q] = there ? V::load_raw(xp + q * a.x_stride) : V::zero_raw();
+                dr[q] = there ? V::load_raw(dp + q * a.dout_stride) : V::zero_raw();
             }
-            float g[4];
+            xp += kAhead * a.x_stride;
+            dp += kAhead * a.dout_stride;
+            if (whole) {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-#pragma unroll
-                for (int j = 0; j < K - 1; ++j) {
-                    win[j][e] = win[j + 1][e];
-                    dpw[j][e] = dpw[j + 1][e];
+                for (int q = 0; q < kAhead; ++q) {
+                    token(widen4<T>(xr[q]), widen4<T>(dr[q]));
+                    add(dpw[K - 1]);
+                    store_act4<T>(dxp + q * a.dx_stride, row());
                 }
-                win[K - 1][e] = x[e];
-                float p = bias[e];
+            } else {
 #pragma unroll
-                for (int j = 0; j < K; ++j) p = fmaf(w[j][e], win[j][e], p);
-                const float sg = rcp_approx(1.f + ex2_approx(p * -kLog2e));
-                const float dp = t < se ? dout[e] * sg * fmaf(p, 1.f - sg, 1.f) : 0.f;
-                dpw[K - 1][e] = dp;
-                if (t < r1) {
-                    db[e] += dp;
-#pragma unroll
-                    for (int j = 0; j < K; ++j) dw[j][e] = fmaf(dp, win[j][e], dw[j][e]);
+                for (int q = 0; q < kAhead; ++q) {
+                    const int t = t0 + q, i = t - (K - 1);
+                    token(widen4<T>(xr[q]), widen4<T>(dr[q]));
+                    if (t >= last) dpw[K - 1] = all4(0.f);  // no such token (its dout is 0, its p need not be finite)
+                    if (t < r1) add(dpw[K - 1]);
+                    if ((i < r0 && run > 0) || i >= r1) continue;
+                    F4 g = row();
+                    const int m = i - sb + (K - 1) - len;  // its row in the window that the stream leaves
+                    if (m >= 0 && fin) g = add4(g, widen4<T>(V::load_raw(fin + m * C)));
+                    if (i >= sb) store_act4<T>(dxp + q * a.dx_stride, g);
+                    else if (dst) store_act4<T>(dst + (i - sb + K - 1) * C, g);
                 }
-                g[e] = 0.f;
-#pragma unroll
-                for (int n = 0; n < K; ++n) g[e] = fmaf(w[K - 1 - n][e], dpw[n][e], g[e]);
             }
-            const int i = t - (K - 1);  // the row whose gradient is complete now
-            if (i < r0 && run > 0) continue;
-            const int m = i - sb + (K - 1) - len;  // its row in the window that the stream leaves
-            if (m >= 0 && fin) {
-                float v[4];
-                V::load(fin + m * C + c, v);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) g[e] += v[e];
-            }
-            if (i >= sb) V::store((T *)a.dx + i * a.dx_stride + c, g);
-            else if (dst) V::store(dst + (i - sb + K - 1) * C + c, g);
+            dxp += kAhead * a.dx_stride;
         }
     }
     float *out = part + (int64_t)slot * (K + 1) * C + c;  // runs without tokens add zeros
 #pragma unroll
-    for (int j = 0; j < K; ++j) Vec4<float>::store(out + j * C, dw[j]);
-    Vec4<float>::store(out + K * C, db);
+    for (int j = 0; j < K; ++j) store_f4(out + j * C, dw[j]);
+    store_f4(out + K * C, db);
 }
 
-// Sum of the runs' parts: one thread per (tap or bias, channel).
-__global__ void conv_bwd_sum_kernel(const float *part, int slots, int K, int C, float *dw, float *dbias,
-                                    const Ctl *ctl) {
-    const int i = blockIdx.x * blockDim.x + threadIdx.x;
-    if (i >= (K + 1) * C || (ctl && ctl->bad)) return;
-    float v = 0.f;
-    for (int s = 0; s < slots; ++s) v += part[(int64_t)s * (K + 1) * C + i];
-    const int j = i / C, c = i % C;
-    if (j < K) dw[(int64_t)c * K + j] = v;
-    else if (dbias) dbias[c] = v;
+// Sums of the runs' parts. A block has 128 columns (of (K + 1) C) and eight groups of the runs; each
+// thread adds every eighth run of its four columns, then the groups are joined.
+constexpr int kGroups = 8;
+__global__ void __launch_bounds__(32 * kGroups)
+conv_bwd_sum_kernel(const float *part, const Runs runs, int K, int C, float *dw, float *dbias) {
+    __shared__ __align__(16) float sums[kGroups][128];
+    if (runs.bad()) return;
+    const int lane = threadIdx.x % 32, g = threadIdx.x / 32, width = (K + 1) * C, slots = runs.slots();
+    const int i = (blockIdx.x * 32 + lane) * 4;
+    F4 v = all4(0.f);
+    if (i < width) {
+#pragma unroll 4
+        for (int s = g; s < slots; s += kGroups) v = add4(v, load_f4(part + (int64_t)s * width + i));
+    }
+    store_f4(&sums[g][lane * 4], v);
+    __syncthreads();
+    const int col = blockIdx.x * 128 + threadIdx.x;
+    if (threadIdx.x >= 128 || col >= width) return;
+    float sum = 0.f;
+#pragma unroll
+    for (int k = 0; k < kGroups; ++k) sum += sums[k][threadIdx.x];
+    const int j = col / C, c = col % C;
+    if (j < K) dw[(int64_t)c * K + j] = sum;
+    else if (dbias) dbias[c] = sum;
 }
 
 template <typename T, int K>
 cudaError_t launch_t(const ConvBwdArgs &a, cudaStream_t st) {
-    Ctl *ctl = (Ctl *)a.workspace;
-    float *part = (float *)((char *)a.workspace + 16);
-    const int slots = run_slots(a.B, a.T_each, a.total, a.cu != nullptr);
-    if (a.cu) conv_bwd_init_kernel<<<1, 1024, 0, st>>>(a.cu, a.B, a.total, ctl, a.status);
-    const dim3 grid(slots, (a.channels / 4 + kThreads - 1) / kThreads);
-    conv_bwd_kernel<T, K><<<grid, kThreads, 0, st>>>(a, ctl, part);
-    conv_bwd_sum_kernel<<<((K + 1) * a.channels + 127) / 128, 128, 0, st>>>(
-        part, slots, K, a.channels, a.dw, a.dbias, a.cu ? ctl : nullptr);
+    const Runs runs{a.cu, a.B, a.T_each, a.total, run_rows(a.B, a.total, a.channels)};
+    float *part = static_cast<float *>(a.workspace);
+    const dim3 grid(runs.slots(), (a.channels / 4 + kThreads - 1) / kThreads);
+    conv_bwd_kernel<T, K><<<grid, kThreads, 0, st>>>(a, runs, part);
+    conv_bwd_sum_kernel<<<((K + 1) * a.channels + 127) / 128, 32 * kGroups, 0, st>>>(part, runs, K, a.channels, a.dw, a.dbias);
     return cudaGetLastError();
 }
 
@@ -173,8 +225,8 @@ cudaError_t launch_k(const ConvBwdArgs &a, cudaStream_t st) {
 }  // namespace
 
 size_t conv_backward_workspace_bytes(int B, int total, int channels, int kernel, int) {
-    // a run of a stream of equal lengths ends with it: no more runs than packed streams have
-    return 16 + ((size_t)total / kRows + B) * (kernel + 1) * channels * sizeof(float);
+    // streams of equal lengths have no more runs than packed ones
+    return ((size_t)total / run_rows(B, total, channels) + B) * (kernel + 1) * channels * sizeof(float);
 }
 
 cudaError_t launch_conv1d_silu_backward(const ConvBwdArgs &a, cudaStream_t st) {
