@@ -8,8 +8,9 @@
 //
 // HBM-bound: x and dout are read once (plus K-1 rows on each side of a run), dx is written once; p is
 // computed again, never stored. One thread has 4 channels, in packed pairs, of a run of consecutive
-// tokens of one stream, with the last K rows of xh and of dp in registers; some rows are loaded
-// before the first of them is used. The sums over tokens are kept per run in 32 bits and joined run by
+// tokens of one stream, with the last K rows of xh and of dp in registers. Rows come through a ring in
+// shared memory, each thread's its own (no barriers), two groups of rows ahead of the one at work: with
+// one group in registers instead, a third of the time went into waiting for it. The sums over tokens are kept per run in 32 bits and joined run by
 // run in a fixed order by a second kernel, so they come out the same every time.
 #include "gated.cuh"
 #include "launch.h"
@@ -19,8 +20,20 @@ namespace la {
 namespace {
 
 constexpr int kThreads = 128;
-// Rows in flight per thread: what the registers of four blocks on an SM hold.
-template <typename T> constexpr int kAheadOf = sizeof(T) == 2 ? 8 : 4;
+// Rows of a group, and groups of the ring: 48 KB a block, four blocks on an SM.
+template <typename T> constexpr int kGroupOf = 16 / sizeof(T);
+constexpr int kRing = 3;
+template <typename T> constexpr int kRingBytes = kRing * kGroupOf<T> * 2 * kThreads * 4 * (int)sizeof(T);
+
+// Four activations to shared memory, or zeros.
+template <typename T> __device__ __forceinline__ void copy_row(void *to, const T *from, bool there) {
+    const uint32_t dst = static_cast<uint32_t>(__cvta_generic_to_shared(to));
+    const int bytes = there ? 4 * (int)sizeof(T) : 0;
+    if constexpr (sizeof(T) == 2)
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(from), "r"(bytes) : "memory");
+    else
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(from), "r"(bytes) : "memory");
+}
 
 // Tokens of a run: long ones read and write less for what runs share (K-1 rows at each end, the sums),
 // short ones make more blocks. The longest that still makes ten blocks for each of 152 SMs (four are
@@ -55,7 +68,9 @@ struct Runs {
 template <typename T, int K>
 __global__ void __launch_bounds__(kThreads, 4) conv_bwd_kernel(const ConvBwdArgs a, const Runs runs, float *part) {
     using V = Vec4<T>;
-    constexpr int kAhead = kAheadOf<T>;
+    constexpr int kGroup = kGroupOf<T>;
+    extern __shared__ __align__(16) unsigned char smem[];
+    auto *ring = reinterpret_cast<typename V::Raw (*)[kGroup][2][kThreads]>(smem);  // [kRing]
     if (runs.bad()) {
         if (threadIdx.x == 0) raise_status(a.status, LA_DEV_BAD_SEQLENS);
         return;
@@ -130,43 +145,52 @@ __global__ void __launch_bounds__(kThreads, 4) conv_bwd_kernel(const ConvBwdArgs
             return g;
         };
 
-        const T *xp = (const T *)a.x + r0 * a.x_stride + c, *dp = (const T *)a.dout + r0 * a.dout_stride + c;
-        T *dxp = (T *)a.dx + (r0 - (K - 1)) * a.dx_stride + c;
         const int last = min(r1 + K - 1, se);  // tokens that the run's rows depend on
-        for (int t0 = r0; t0 < r1 + K - 1; t0 += kAhead) {
-            typename V::Raw xr[kAhead], dr[kAhead];
-            const bool whole = t0 >= r0 + K - 1 && t0 + kAhead <= r1;  // every row of these is the run's own
+        const int groups = (r1 + K - 1 - r0 + kGroup - 1) / kGroup;
+        const T *x0 = (const T *)a.x + r0 * a.x_stride + c, *d0 = (const T *)a.dout + r0 * a.dout_stride + c;
+        const auto fetch = [&](int g) {  // group g into the ring
+            if (g < groups) {
 #pragma unroll
-            for (int q = 0; q < kAhead; ++q) {
-                const bool there = whole || t0 + q < last;
-                xr[q] = there ? V::load_raw(xp + q * a.x_stride) : V::zero_raw();
-                dr[q] = there ? V::load_raw(dp + q * a.dout_stride) : V::zero_raw();
+                for (int q = 0; q < kGroup; ++q) {
+                    const int n = g * kGroup + q;
+                    const bool there = r0 + n < last;
+                    copy_row(&ring[g % kRing][q][0][threadIdx.x], there ? x0 + n * a.x_stride : x0, there);
+                    copy_row(&ring[g % kRing][q][1][threadIdx.x], there ? d0 + n * a.dout_stride : d0, there);
+                }
             }
-            xp += kAhead * a.x_stride;
-            dp += kAhead * a.dout_stride;
-            if (whole) {
+            asm volatile("cp.async.commit_group;" ::: "memory");
+        };
+        fetch(0);
+        fetch(1);
+        T *dxp = (T *)a.dx + (r0 - (K - 1)) * a.dx_stride + c;
+        for (int g = 0; g < groups; ++g) {
+            fetch(g + 2);
+            asm volatile("cp.async.wait_group 2;" ::: "memory");
+            const int t0 = r0 + g * kGroup;
+            const auto &rows = ring[g % kRing];
+            if (t0 >= r0 + K - 1 && t0 + kGroup <= r1) {  // every row of these is the run's own
 #pragma unroll
-                for (int q = 0; q < kAhead; ++q) {
-                    token(widen4<T>(xr[q]), widen4<T>(dr[q]));
+                for (int q = 0; q < kGroup; ++q) {
+                    token(widen4<T>(rows[q][0][threadIdx.x]), widen4<T>(rows[q][1][threadIdx.x]));
                     add(dpw[K - 1]);
                     store_act4<T>(dxp + q * a.dx_stride, row());
                 }
             } else {
 #pragma unroll
-                for (int q = 0; q < kAhead; ++q) {
+                for (int q = 0; q < kGroup; ++q) {
                     const int t = t0 + q, i = t - (K - 1);
-                    token(widen4<T>(xr[q]), widen4<T>(dr[q]));
+                    token(widen4<T>(rows[q][0][threadIdx.x]), widen4<T>(rows[q][1][threadIdx.x]));
                     if (t >= last) dpw[K - 1] = all4(0.f);  // no such token (its dout is 0, its p need not be finite)
                     if (t < r1) add(dpw[K - 1]);
                     if ((i < r0 && run > 0) || i >= r1) continue;
-                    F4 g = row();
+                    F4 grad = row();
                     const int m = i - sb + (K - 1) - len;  // its row in the window that the stream leaves
-                    if (m >= 0 && fin) g = add4(g, widen4<T>(V::load_raw(fin + m * C)));
-                    if (i >= sb) store_act4<T>(dxp + q * a.dx_stride, g);
-                    else if (dst) store_act4<T>(dst + (i - sb + K - 1) * C, g);
+                    if (m >= 0 && fin) grad = add4(grad, widen4<T>(V::load_raw(fin + m * C)));
+                    if (i >= sb) store_act4<T>(dxp + q * a.dx_stride, grad);
+                    else if (dst) store_act4<T>(dst + (i - sb + K - 1) * C, grad);
                 }
             }
-            dxp += kAhead * a.dx_stride;
+            dxp += kGroup * a.dx_stride;
         }
     }
     float *out = part + (int64_t)slot * (K + 1) * C + c;  // runs without tokens add zeros
@@ -206,7 +230,9 @@ cudaError_t launch_t(const ConvBwdArgs &a, cudaStream_t st) {
     const Runs runs{a.cu, a.B, a.T_each, a.total, run_rows(a.B, a.total, a.channels)};
     float *part = static_cast<float *>(a.workspace);
     const dim3 grid(runs.slots(), (a.channels / 4 + kThreads - 1) / kThreads);
-    conv_bwd_kernel<T, K><<<grid, kThreads, 0, st>>>(a, runs, part);
+    const cudaError_t e = cudaFuncSetAttribute(conv_bwd_kernel<T, K>, cudaFuncAttributeMaxDynamicSharedMemorySize, kRingBytes<T>);
+    if (e != cudaSuccess) return e;
+    conv_bwd_kernel<T, K><<<grid, kThreads, kRingBytes<T>, st>>>(a, runs, part);
     conv_bwd_sum_kernel<<<((K + 1) * a.channels + 127) / 128, 32 * kGroups, 0, st>>>(part, runs, K, a.channels, a.dw, a.dbias);
     return cudaGetLastError();
 }
