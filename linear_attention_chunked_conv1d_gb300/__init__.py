@@ -403,62 +403,78 @@ def _dtype_arg(dtype) -> int:
     return dtype if isinstance(dtype, int) else (LA_BF16 if dtype == torch.bfloat16 else LA_F32)
 
 
-def _on_gpu(t) -> torch.device:
-    """The device of `t`, which has to be the current one: streams and launches are its own."""
-    if not t.is_cuda:
+# The calls below may take no longer than their launch does, so their checks are kept to what costs
+# well under a microsecond each: devices are compared by their index.
+_current_device = torch._C._cuda_getDevice if hasattr(torch._C, "_cuda_getDevice") else None
+_current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _on_gpu(t) -> int:
+    """The device index of `t`, which has to be the current one: streams and launches are its own."""
+    dev = t.get_device()
+    if dev < 0:
         raise ValueError("expected CUDA tensors")
-    if t.device.index != torch.cuda.current_device():
-        raise ValueError(f"tensors on {t.device}, but the current device is "
-                         f"cuda:{torch.cuda.current_device()}: use torch.cuda.device(...)")
-    return t.device
+    cur = torch.cuda.current_device() if _current_device is None else _current_device()
+    if dev != cur:
+        raise ValueError(f"tensors on cuda:{dev}, but the current device is cuda:{cur}: use "
+                         "torch.cuda.device(...)")
+    return dev
 
 
-def _matrix(name, t, shape, dtype, device) -> int:
+def _stream_on(stream, dev) -> int:
+    return _current_stream(dev) if stream is None and _current_stream is not None else _stream(stream)
+
+
+def _matrix(name, t, rows, cols, dtype, dev) -> int:
     """Checks a matrix of dense rows; returns its row stride."""
     if t.dtype != dtype:
         raise TypeError(f"{name} is {t.dtype}, expected {dtype}")
-    if t.shape != shape or (t.stride(1) != 1 and shape[1] != 1) or t.device != device:
-        raise ValueError(f"{name}: {tuple(t.shape)} with strides {t.stride()} on {t.device}, "
-                         f"expected {tuple(shape)} with dense rows on {device}")
-    return t.stride(0) if shape[0] > 1 else max(t.stride(0), shape[1])
+    if t.shape == (rows, cols) and t.get_device() == dev:
+        s, inner = t.stride()
+        if inner == 1 or cols == 1:
+            return s if rows > 1 else max(s, cols)
+    raise ValueError(f"{name}: {tuple(t.shape)} with strides {t.stride()} on device {t.get_device()}, "
+                     f"expected {(rows, cols)} with dense rows on device {dev}")
 
 
-def _dense(name, t, shape, dtype, device):
+def _dense(name, t, shape, dtype, dev):
+    """The address of a contiguous tensor of this shape."""
     if t.dtype != dtype:
         raise TypeError(f"{name} is {t.dtype}, expected {dtype}")
-    if t.shape != shape or not t.is_contiguous() or t.device != device:
-        raise ValueError(f"{name}: {tuple(t.shape)} on {t.device}, expected a contiguous "
-                         f"{tuple(shape)} on {device}")
+    if t.shape != shape or not t.is_contiguous() or t.get_device() != dev:
+        raise ValueError(f"{name}: {tuple(t.shape)} on device {t.get_device()}, expected a "
+                         f"contiguous {tuple(shape)} on device {dev}")
     return t.data_ptr()
 
 
-def _ptrs(name, t, B, device):
+def _ptrs(name, t, B, dev):
     """The address of a device array of B pointers (pointer_array), or None."""
     if t is None:
         return None
-    if t.dtype not in (torch.int64, torch.uint64):
+    if t.dtype != torch.int64 and t.dtype != torch.uint64:
         raise TypeError(f"{name} is {t.dtype}, expected the int64 of pointer_array")
-    if t.numel() != B or not t.is_contiguous() or t.device != device:
-        raise ValueError(f"{name}: {t.numel()} pointers on {t.device}, expected {B} on {device}")
+    if t.numel() != B or not t.is_contiguous() or t.get_device() != dev:
+        raise ValueError(f"{name}: {t.numel()} pointers on device {t.get_device()}, expected {B} "
+                         f"on device {dev}")
     return t.data_ptr()
 
 
-def _streams(cu_seqlens, B, device):
+def _streams(cu_seqlens, B, dev):
     """(address of cu_seqlens or None, number of streams)."""
     if cu_seqlens is None:
         return None, 1 if B is None else B
     n = cu_seqlens.shape[0] - 1
     if B is not None and B != n:
         raise ValueError(f"B = {B}, but cu_seqlens has {n} streams")
-    return _dense("cu_seqlens", cu_seqlens, (n + 1,), torch.int32, device), n
+    return _dense("cu_seqlens", cu_seqlens, (n + 1,), torch.int32, dev), n
 
 
-def _room(name, t, device):
+def _room(name, t, dev):
     """(address, bytes) of a workspace or saved buffer, or (None, 0)."""
     if t is None:
         return None, 0
-    if not t.is_contiguous() or t.device != device:
-        raise ValueError(f"{name} must be contiguous and on {device}")
+    if not t.is_contiguous() or t.get_device() != dev:
+        raise ValueError(f"{name} must be contiguous and on device {dev}")
     return t.data_ptr(), t.numel() * t.element_size()
 
 
@@ -488,8 +504,8 @@ def gated_scan(h_state_ptrs, x, ab, y, cu_seqlens=None, *, B=None, saved=None, m
     _check(_load().la_gated_scan(
         _ptrs("h_state_ptrs", h_state_ptrs, B, dev), x.data_ptr(), ab.data_ptr(), y.data_ptr(), sv,
         sv_bytes, cu, B, T, T if max_tokens is None else max_tokens, C,
-        _matrix("x", x, (T, C), x.dtype, dev), _matrix("ab", ab, (T, 2 * C), x.dtype, dev),
-        _matrix("y", y, (T, C), x.dtype, dev), _dtype_code(x), ws, ws_bytes, _stream(stream)))
+        _matrix("x", x, T, C, x.dtype, dev), _matrix("ab", ab, T, 2 * C, x.dtype, dev),
+        _matrix("y", y, T, C, x.dtype, dev), _dtype_code(x), ws, ws_bytes, _stream_on(stream, dev)))
 
 
 def gated_scan_backward(x, ab, saved, dy, dx, dab, cu_seqlens=None, *, B=None, dh_final_ptrs=None,
@@ -507,10 +523,10 @@ def gated_scan_backward(x, ab, saved, dy, dx, dab, cu_seqlens=None, *, B=None, d
         x.data_ptr(), ab.data_ptr(), sv, sv_bytes, dy.data_ptr(),
         _ptrs("dh_final_ptrs", dh_final_ptrs, B, dev), dx.data_ptr(), dab.data_ptr(),
         _ptrs("dh0_ptrs", dh0_ptrs, B, dev), cu, B, T, T if max_tokens is None else max_tokens, C,
-        _matrix("x", x, (T, C), x.dtype, dev), _matrix("ab", ab, (T, 2 * C), x.dtype, dev),
-        _matrix("dy", dy, (T, C), x.dtype, dev), _matrix("dx", dx, (T, C), x.dtype, dev),
-        _matrix("dab", dab, (T, 2 * C), x.dtype, dev), _dtype_code(x), ws, ws_bytes,
-        _stream(stream)))
+        _matrix("x", x, T, C, x.dtype, dev), _matrix("ab", ab, T, 2 * C, x.dtype, dev),
+        _matrix("dy", dy, T, C, x.dtype, dev), _matrix("dx", dx, T, C, x.dtype, dev),
+        _matrix("dab", dab, T, 2 * C, x.dtype, dev), _dtype_code(x), ws, ws_bytes,
+        _stream_on(stream, dev)))
 
 
 def gated_scan_step(h_state_ptrs, x, ab, y, *, conv_state_ptrs=None, conv_w=None, conv_bias=None,
@@ -530,8 +546,8 @@ def gated_scan_step(h_state_ptrs, x, ab, y, *, conv_state_ptrs=None, conv_w=None
         _ptrs("conv_state_ptrs", conv_state_ptrs, B, dev),
         _ptrs("h_state_ptrs", h_state_ptrs, B, dev), x.data_ptr(), ab.data_ptr(), _ptr(conv_w),
         _ptr(conv_bias), K, y.data_ptr(), B, B if max_streams is None else max_streams, C,
-        _matrix("x", x, (B, C), x.dtype, dev), _matrix("ab", ab, (B, 2 * C), x.dtype, dev),
-        _matrix("y", y, (B, C), x.dtype, dev), _dtype_code(x), _stream(stream)))
+        _matrix("x", x, B, C, x.dtype, dev), _matrix("ab", ab, B, 2 * C, x.dtype, dev),
+        _matrix("y", y, B, C, x.dtype, dev), _dtype_code(x), _stream_on(stream, dev)))
 
 
 def conv1d_silu_backward_workspace_bytes(B, total_tokens, channels, kernel, dtype) -> int:
@@ -561,8 +577,8 @@ def conv1d_silu_backward(conv_state_ptrs, x, w, dout, dx, dw, cu_seqlens=None, *
         _dense("dw", dw, (C, K), torch.float32, dev),
         None if dbias is None else _dense("dbias", dbias, (C,), torch.float32, dev),
         _ptrs("dstate_ptrs", dstate_ptrs, B, dev), cu, B, T, T if max_tokens is None else max_tokens,
-        C, K, _matrix("x", x, (T, C), x.dtype, dev), _matrix("dout", dout, (T, C), x.dtype, dev),
-        _matrix("dx", dx, (T, C), x.dtype, dev), _dtype_code(x), ws, ws_bytes, _stream(stream)))
+        C, K, _matrix("x", x, T, C, x.dtype, dev), _matrix("dout", dout, T, C, x.dtype, dev),
+        _matrix("dx", dx, T, C, x.dtype, dev), _dtype_code(x), ws, ws_bytes, _stream_on(stream, dev)))
 
 
 def w4_quantize(w, q=None, scales=None, *, group=128, stream=None):
@@ -570,13 +586,13 @@ def w4_quantize(w, q=None, scales=None, *, group=128, stream=None):
     dev = _on_gpu(w)
     N, K = w.shape
     if q is None:
-        q = torch.empty(N, K // 2, dtype=torch.uint8, device=dev)
+        q = torch.empty(N, K // 2, dtype=torch.uint8, device=w.device)
     if scales is None:
-        scales = torch.empty(N, K // group, dtype=torch.bfloat16, device=dev)
+        scales = torch.empty(N, K // group, dtype=torch.bfloat16, device=w.device)
     _check(_load().la_w4_quantize(
         w.data_ptr(), _dense("q", q, (N, K // 2), torch.uint8, dev),
         _dense("scales", scales, (N, K // group), torch.bfloat16, dev), N, K, group,
-        _matrix("w", w, (N, K), torch.bfloat16, dev), _stream(stream)))
+        _matrix("w", w, N, K, torch.bfloat16, dev), _stream_on(stream, dev)))
     return q, scales
 
 
@@ -589,10 +605,10 @@ def w4_matvec(x, q, scales, y=None, *, stream=None):
     if groups == 0 or K % groups:
         raise ValueError(f"{groups} scales for each {K} inputs")
     if y is None:
-        y = torch.empty(M, N, dtype=torch.bfloat16, device=dev)
+        y = torch.empty(M, N, dtype=torch.bfloat16, device=x.device)
     _check(_load().la_w4_matvec(
         x.data_ptr(), _dense("q", q, (N, K // 2), torch.uint8, dev),
         _dense("scales", scales, (N, groups), torch.bfloat16, dev), y.data_ptr(), M, N, K,
-        K // groups, _matrix("x", x, (M, K), torch.bfloat16, dev),
-        _matrix("y", y, (M, N), torch.bfloat16, dev), _stream(stream)))
+        K // groups, _matrix("x", x, M, K, torch.bfloat16, dev),
+        _matrix("y", y, M, N, torch.bfloat16, dev), _stream_on(stream, dev)))
     return y

@@ -161,15 +161,17 @@ def test_binding_refuses_host_tensors(lib):
 
 def test_binding_checks(lib):
     """The helpers that look at every tensor, on host tensors (the device only has to agree)."""
-    dev = torch.device("cpu")
+    dev = -1  # as get_device says of the host
     t = torch.zeros(4, 8)
-    assert lib._matrix("t", t, (4, 8), torch.float32, dev) == 8
-    assert lib._matrix("t", torch.zeros(4, 24)[:, 8:16], (4, 8), torch.float32, dev) == 24
+    assert lib._matrix("t", t, 4, 8, torch.float32, dev) == 8
+    assert lib._matrix("t", torch.zeros(4, 24)[:, 8:16], 4, 8, torch.float32, dev) == 24
     for bad in (t.t(), torch.zeros(8, 4).t(), torch.zeros(3, 8), torch.zeros(4, 16)[:, ::2]):
         with pytest.raises(ValueError, match="name"):
-            lib._matrix("name", bad, (4, 8), torch.float32, dev)
+            lib._matrix("name", bad, 4, 8, torch.float32, dev)
+    with pytest.raises(ValueError, match="name"):
+        lib._matrix("name", t, 4, 8, torch.float32, 0)
     with pytest.raises(TypeError, match="name"):
-        lib._matrix("name", t, (4, 8), torch.bfloat16, dev)
+        lib._matrix("name", t, 4, 8, torch.bfloat16, dev)
     with pytest.raises(ValueError, match="name"):
         lib._dense("name", torch.zeros(4, 16)[:, :8], (4, 8), torch.float32, dev)
     with pytest.raises(ValueError, match="name"):
