@@ -446,7 +446,7 @@ int la_conv1d_silu_backward(const uint64_t *conv_state_ptrs, const void *x, cons
  * x, y    bf16 [M][ldx], [M][ldy]; x and ldx aligned to 16 bytes; y may not overlap x.
  * q       [N][K/2] bytes, contiguous, 16-byte aligned: eight weights of a row to a little-endian
  *         32-bit word, weight 2i in bits 4i..4i+3 and weight 2i+1 in bits 16+4i..16+4i+3.
- * scales  bf16 [N][K/group], contiguous.
+ * scales  bf16 [N][K/group], contiguous, 16-byte aligned.
  * group   32, 64 or 128; K a multiple of it. Sums are fp32, y is rounded once, and the order of the
  *         sums does not depend on M: a row gives the same bits in any batch.
  * Count rule: 1 <= M <= LA_W4_MAX_ROWS; N, K >= 1. */

@@ -192,9 +192,7 @@ int w4_common(const void *q, const void *scales, int K, int group) {
         return fail(LA_ERR_UNSUPPORTED, "group %d: compiled for 32, 64 and 128", group);
     if (K % group) return fail(LA_ERR_ARG, "K (%d) is not a multiple of the group (%d)", K, group);
     LA_TRY(check_act_ptr(q, "q"));
-    if (!scales || (reinterpret_cast<uintptr_t>(scales) & 1u))
-        return fail(LA_ERR_ARG, "scales is NULL or misaligned");
-    return LA_OK;
+    return check_act_ptr(scales, "scales");
 }
 
 // Shared checks of the three recurrence calls.

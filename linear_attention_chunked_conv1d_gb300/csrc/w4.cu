@@ -40,23 +40,34 @@ __global__ void w4_quantize_kernel(const W4QuantArgs a, int64_t words) {
     if (k8 % lanes == 0) ((__nv_bfloat16 *)a.scales)[n * (a.K / a.group) + k8 / lanes] = scale;
 }
 
-// The products: a tile of 128 outputs, 16 to a warp, over a share of the inputs that the blocks of a
-// cluster split. 128 inputs at a time go through a ring of asynchronous copies: the tile's weights (8
-// KB) and the rows' inputs, laid out so that a lane finds its part of an operand in 16 bytes. Weights
-// are the A operand of mma.m16n8k16, 16 outputs by 16 inputs, as exact bf16 integers -8 .. 7; the rows
-// are B. A lane's word of eight weights serves two mma: which inputs meet in one mma is free as long
-// as A and B agree, so word c of 32 inputs goes to the lanes with c = lane % 4 as it lies in memory.
-// Products and sums within a group are exact integers times bf16 in fp32; each group's sum is scaled
-// by its output's scale and added up in fp32. Blocks of a cluster leave their sums in shared memory
-// and each adds up a share of the outputs, in order of the blocks.
+// The products: a tile of 128 outputs over a share of the inputs that the blocks of a cluster split.
+// 256 inputs at a time go through a ring of asynchronous copies: the tile's weights (16 KB) and the
+// rows' inputs, laid out so that a lane finds its part of an operand in 16 bytes, and the scales (by
+// plain loads a stage ahead, these alone made 32 x 16384 x 8192 take 44 us). A warp has 32 of the
+// outputs and 128 of the inputs. Weights are the A operand of mma.m16n8k16, 16 outputs by 16 inputs,
+// as exact bf16 integers -8 .. 7; the rows are B. A lane's word of eight weights serves two mma: which
+// inputs meet in one mma is free as long as A and B agree, so word c of 32 inputs goes to the lanes
+// with c = lane % 4 as it lies in memory. Products and sums within a group are exact integers times
+// bf16 in fp32; each group's sum is scaled by its output's scale and added up in fp32. In the end every
+// block of the cluster gets all parts of its share of the outputs and adds them in a fixed order.
 constexpr int kThreads = 256;
-constexpr int kTile = 128;        // outputs of a block
-constexpr int kSeg = 128;         // inputs of a stage
-constexpr int kRowBytes = 64 + 16;  // a row's weights of a stage, padded: 8 rows x 4 lanes on 32 banks
-constexpr int kStages = 5;
+constexpr int kTile = 128;           // outputs of a block: four warps of 32
+constexpr int kSeg = 256;            // inputs of a stage: two warps of 128
+constexpr int kRowBytes = 128 + 16;  // a row's weights of a stage, padded: 8 rows x 4 lanes on 32 banks
+
+// Words that hold an output's scales of a stage: they may start in the middle of one.
+template <int G> constexpr int kScaleWords = kSeg / G / 2 + 1;
+// A stage: weights, inputs, scales.
+template <int NT> constexpr int kInputsAt = kTile * kRowBytes;
+template <int NT> constexpr int kScalesAt = kInputsAt<NT> + NT * 8 * kSeg * 2;
+template <int NT, int G> constexpr int kStageBytes = kScalesAt<NT> + kTile * kScaleWords<G> * 4;
+template <int NT> constexpr int kStages = NT == 1 ? 4 : 3;  // two blocks on an SM
 
 __device__ __forceinline__ void copy16(uint32_t to, const void *from, bool there) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(there ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void copy4(uint32_t to, const void *from, int bytes) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(to), "l"(from), "r"(bytes) : "memory");
 }
 __device__ __forceinline__ void mma_bf16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
     asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
@@ -70,136 +81,173 @@ __device__ __forceinline__ uint32_t weight_pair(uint32_t word, int i) {
     __nv_bfloat162 h = __hsub2(*reinterpret_cast<const __nv_bfloat162 *>(&v), __floats2bfloat162_rn(136.f, 136.f));
     return *reinterpret_cast<uint32_t *>(&h);
 }
-
-template <int NT> constexpr int kStageBytes = kTile * kRowBytes + NT * 2048;
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
 
 template <int NT, int G>  // 8 NT rows at most, groups of G inputs
 __global__ void __launch_bounds__(kThreads, 2) w4_matvec_kernel(const W4Args a, int segs_each) {
     extern __shared__ __align__(128) unsigned char smem[];
     const uint32_t sbase = static_cast<uint32_t>(__cvta_generic_to_shared(smem));
     const int t = threadIdx.x, warp = t / 32, lane = t % 32, g = lane / 4, c = lane % 4;
+    const int rows_at = warp % 4 * 32, half = warp / 4;
     uint32_t rank, blocks;
     asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
     asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(blocks));
     const int n0 = blockIdx.x / blocks * kTile;
     const int all = (a.K + kSeg - 1) / kSeg;
-    const int first = rank * segs_each, last = min(first + segs_each, all);
-    const unsigned char *q = static_cast<const unsigned char *>(a.q);
-    const __nv_bfloat16 *x = static_cast<const __nv_bfloat16 *>(a.x);
+    const int first = (int)rank * segs_each, last = min(first + segs_each, all);
 
+    // this thread's copies of a stage: 16 bytes of weights of rows t / 8, + 32, + 64, + 96 ..
+    const int kq = first * kSeg + t % 8 * 32;
+    const unsigned char *qp = static_cast<const unsigned char *>(a.q) + (int64_t)(n0 + t / 8) * (a.K / 2) + kq / 2;
+    const uint32_t q_to = t / 8 * kRowBytes + t % 8 * 16;
+    // .. and of inputs: 8 of them of row t / 32, + 8, ..
+    const int kx = first * kSeg + lane * 8;
+    const __nv_bfloat16 *xp = static_cast<const __nv_bfloat16 *>(a.x) + (int64_t)warp * a.ldx + kx;
+    const uint32_t x_to = kInputsAt<NT> + (lane / 4 * 32 + warp * 4 + lane % 4) * 16;
+    // .. and of scales, a word at a time
+    constexpr int kWords = kScaleWords<G>;
+    const int per_row = a.K / G;
+    const int64_t scales = (int64_t)a.N * per_row;
+    uint32_t at = sbase;
     const auto fetch = [&](int seg) {
         if (seg < last) {
-            const uint32_t to = sbase + seg % kStages * kStageBytes<NT>;
+            const int off = (seg - first) * kSeg;
 #pragma unroll
-            for (int i = 0; i < kTile * 4 / kThreads; ++i) {
-                const int r = (t + i * kThreads) / 4, part = t % 4, k = seg * kSeg + part * 32;
-                const bool there = n0 + r < a.N && k < a.K;
-                copy16(to + r * kRowBytes + part * 16, there ? q + (int64_t)(n0 + r) * (a.K / 2) + k / 2 : q, there);
+            for (int i = 0; i < 4; ++i) {
+                const bool there = n0 + t / 8 + i * 32 < a.N && kq + off < a.K;
+                copy16(at + q_to + i * 32 * kRowBytes, there ? qp + (int64_t)i * 32 * (a.K / 2) + off / 2 : a.q, there);
             }
 #pragma unroll
-            for (int i = 0; i < (NT * 128 + kThreads - 1) / kThreads; ++i) {
-                const int at = t + i * kThreads, m = at / 16, jc = at % 16, k = seg * kSeg + jc * 8;
-                const bool there = m < a.M && k < a.K;
-                if (NT * 128 >= kThreads || at < NT * 128)
-                    copy16(to + kTile * kRowBytes + ((m / 8 * 4 + jc / 4) * 32 + m % 8 * 4 + jc % 4) * 16,
-                           there ? x + m * a.ldx + k : x, there);
+            for (int n = 0; n < NT; ++n) {
+                const bool there = warp + n * 8 < a.M && kx + off < a.K;
+                copy16(at + x_to + n * 8 * kSeg * 2, there ? xp + n * 8 * a.ldx + off : a.x, there);
             }
+#pragma unroll
+            for (int i = 0; i < (kTile * kWords + kThreads - 1) / kThreads; ++i) {
+                const int w = t + i * kThreads, row = w / kWords;
+                if (kTile * kWords % kThreads && w >= kTile * kWords) break;
+                const int64_t from = (((int64_t)(n0 + row) * per_row + seg * (kSeg / G)) & ~int64_t(1)) + w % kWords * 2;
+                const int64_t left = scales - from;  // an odd last one is half a word
+                copy4(at + kScalesAt<NT> + w * 4, static_cast<const __nv_bfloat16 *>(a.scales) + (left > 0 ? from : 0),
+                      left > 1 ? 4 : left > 0 ? 2 : 0);
+            }
+            at = at == sbase + (kStages<NT> - 1) * kStageBytes<NT, G> ? sbase : at + kStageBytes<NT, G>;
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
     };
-    // the scales of this lane's two outputs in a stage
-    constexpr int kGroups = kSeg / G;
-    const int row0 = n0 + warp * 16 + g, per_row = a.K / G;
-    const __nv_bfloat16 *sc = static_cast<const __nv_bfloat16 *>(a.scales);
-    const auto scales = [&](int seg, float (&s)[2][kGroups]) {
+    // where a stage has the scales of this lane's four outputs
+    constexpr int kGroups = 128 / G;
+    int scale_at[4];
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
-#pragma unroll
-            for (int i = 0; i < kGroups; ++i) {
-                const int row = row0 + 8 * h, at = seg * kGroups + i;
-                s[h][i] = row < a.N && at < per_row && seg < last ? to_f(sc[(int64_t)row * per_row + at]) : 0.f;
-            }
-    };
+    for (int r = 0; r < 4; ++r) {
+        const int row = rows_at + g + 8 * r;
+        scale_at[r] = row * kWords * 2 + (int)((int64_t)(n0 + row) * per_row & 1) + half * kGroups;
+    }
 
-    float acc[NT][4] = {}, next[2][kGroups];
+    float acc[2][NT][4] = {};
 #pragma unroll
-    for (int s = 0; s < kStages - 1; ++s) fetch(first + s);
-    scales(first, next);
+    for (int s = 0; s < kStages<NT> - 1; ++s) fetch(first + s);
+    const unsigned char *st = smem;
     for (int seg = first; seg < last; ++seg) {
-        float s[2][kGroups];
-#pragma unroll
-        for (int i = 0; i < kGroups; ++i) s[0][i] = next[0][i], s[1][i] = next[1][i];
-        asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
+        asm volatile("cp.async.wait_group %0;" ::"n"(kStages<NT> - 2) : "memory");
         __syncthreads();  // this stage is here, and the one before it read by all
-        fetch(seg + kStages - 1);
-        scales(seg + 1, next);
-        const unsigned char *st = smem + seg % kStages * kStageBytes<NT>;
-        const uint32_t *w0 = reinterpret_cast<const uint32_t *>(st + (warp * 16 + g) * kRowBytes) + c;
-        const uint32_t *w1 = w0 + 8 * kRowBytes / 4;
-        const uint4 *xs = reinterpret_cast<const uint4 *>(st + kTile * kRowBytes) + lane;
-        float part[NT][4];
+        fetch(seg + kStages<NT> - 1);
+        const uint32_t *w = reinterpret_cast<const uint32_t *>(st + (rows_at + g) * kRowBytes + half * 64) + c;
+        const uint4 *xs = reinterpret_cast<const uint4 *>(st + kInputsAt<NT>) + half * 4 * 32 + lane;
+        // Inputs past K are zeros, but their scales are the next output's or nobody's.
+        const __nv_bfloat16 *sc = reinterpret_cast<const __nv_bfloat16 *>(st + kScalesAt<NT>);
+        const int groups_left = per_row - seg * (kSeg / G) - half * kGroups;
+        float part[2][NT][4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             if (j * 32 % G == 0) {
 #pragma unroll
-                for (int n = 0; n < NT; ++n) part[n][0] = part[n][1] = part[n][2] = part[n][3] = 0.f;
-            }
-            const uint32_t u0 = w0[j * 4], u1 = w1[j * 4];
-            const uint32_t A0[4] = {weight_pair(u0, 0), weight_pair(u1, 0), weight_pair(u0, 1), weight_pair(u1, 1)};
-            const uint32_t A1[4] = {weight_pair(u0, 2), weight_pair(u1, 2), weight_pair(u0, 3), weight_pair(u1, 3)};
-#pragma unroll
-            for (int n = 0; n < NT; ++n) {
-                const uint4 b = xs[(n * 4 + j) * 32];
-                mma_bf16(part[n], A0, b.x, b.y);
-                mma_bf16(part[n], A1, b.z, b.w);
-            }
-            if ((j + 1) * 32 % G == 0) {
-#pragma unroll
                 for (int n = 0; n < NT; ++n)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) acc[n][e] = fmaf(s[e / 2][j * 32 / G], part[n][e], acc[n][e]);
+                    for (int e = 0; e < 4; ++e) part[0][n][e] = part[1][n][e] = 0.f;
+            }
+            uint32_t A[2][2][4];  // [16 outputs][8 of 32 inputs' pairs]
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                const uint32_t u0 = w[(r * 16) * (kRowBytes / 4) + j * 4], u1 = w[(r * 16 + 8) * (kRowBytes / 4) + j * 4];
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    A[r][h][0] = weight_pair(u0, 2 * h);
+                    A[r][h][1] = weight_pair(u1, 2 * h);
+                    A[r][h][2] = weight_pair(u0, 2 * h + 1);
+                    A[r][h][3] = weight_pair(u1, 2 * h + 1);
+                }
+            }
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                const uint4 b = xs[n * (kSeg / 32 * 32) + j * 32];
+#pragma unroll
+                for (int r = 0; r < 2; ++r) {
+                    mma_bf16(part[r][n], A[r][0], b.x, b.y);
+                    mma_bf16(part[r][n], A[r][1], b.z, b.w);
+                }
+            }
+            if ((j + 1) * 32 % G == 0) {
+                const int i = j * 32 / G;
+                float s[4];
+#pragma unroll
+                for (int r = 0; r < 4; ++r) s[r] = i < groups_left ? to_f(sc[scale_at[r] + i]) : 0.f;
+#pragma unroll
+                for (int r = 0; r < 2; ++r)
+#pragma unroll
+                    for (int n = 0; n < NT; ++n)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) acc[r][n][e] = fmaf(s[2 * r + e / 2], part[r][n][e], acc[r][n][e]);
             }
         }
+        st = st == smem + (kStages<NT> - 1) * kStageBytes<NT, G> ? smem : st + kStageBytes<NT, G>;
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
-    __syncthreads();
-    // sums to shared memory: [8 NT rows][128 outputs]
-    float *sums = reinterpret_cast<float *>(smem);
+    // Every block has done with its ring: the parts go there, to the block whose share the output is in.
+    // [2 blocks][8 NT rows][share outputs]
+    cluster_sync();
+    const int share = kTile / (int)blocks, part_at = ((int)rank * 2 + half) * NT * 8;
 #pragma unroll
-    for (int n = 0; n < NT; ++n)
+    for (int r = 0; r < 2; ++r)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) sums[(n * 8 + 2 * c + e % 2) * kTile + warp * 16 + g + e / 2 * 8] = acc[n][e];
-    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-    // each block adds up a share of the outputs
-    const int share = kTile / (int)blocks;
-    for (int i = t; i < a.M * share; i += kThreads) {
-        const int m = i / share, r = (int)rank * share + i % share;
-        float v = 0.f;
-        for (uint32_t b = 0; b < blocks; ++b) {
-            uint32_t at;
-            float u;
-            asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(sbase + (m * kTile + r) * 4), "r"(b));
-            asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(u) : "r"(at) : "memory");
-            v += u;
+        for (int e = 0; e < 4; ++e) {
+            const int out = rows_at + r * 16 + g + e / 2 * 8;
+            uint32_t to;
+            asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(to) : "r"(sbase), "r"(out / share));
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                const int m = n * 8 + 2 * c + e % 2;
+                if (m < a.M)
+                    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(to + ((part_at + m) * share + out % share) * 4),
+                                 "f"(acc[r][n][e]) : "memory");
+            }
         }
-        if (n0 + r < a.N) static_cast<__nv_bfloat16 *>(a.y)[m * a.ldy + n0 + r] = __float2bfloat16_rn(v);
+    cluster_sync();
+    const float *sums = reinterpret_cast<const float *>(smem);
+    for (int i = t; i < a.M * share; i += kThreads) {
+        const int m = i / share, out = i % share, n = n0 + (int)rank * share + out;
+        float v = 0.f;
+        for (uint32_t b = 0; b < 2 * blocks; ++b) v += sums[(b * NT * 8 + m) * share + out];
+        if (n < a.N) static_cast<__nv_bfloat16 *>(a.y)[m * a.ldy + n] = __float2bfloat16_rn(v);
     }
-    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
-// Blocks that share a tile's inputs: as many (1, 2, 4 or 8) as it takes for a block and a half on each
-// of 152 SMs, while each still has four stages. By N and K alone, and a fixed number of SMs: a row's
+// Blocks that share a tile's inputs: as many (1, 2, 4 or 8) as still fit on 152 SMs, two on each less a
+// tenth for clusters that do not fill a group of SMs, while each still has two stages. By N and K alone, and a fixed number of SMs: a row's
 // sums do not depend on the batch or the device.
 int cluster_of(int N, int K) {
     const int tiles = (N + kTile - 1) / kTile, segs = (K + kSeg - 1) / kSeg;
     int blocks = 1;
-    while (blocks < 8 && tiles * blocks < 228 && segs >= 8 * blocks) blocks *= 2;
+    while (blocks < 8 && 2 * tiles * blocks <= 272 && segs >= 4 * blocks) blocks *= 2;
     return blocks;
 }
 
 template <int NT, int G> cudaError_t launch_t(const W4Args &a, cudaStream_t st) {
-    constexpr int smem = kStages * kStageBytes<NT>;
-    static_assert(smem >= NT * 8 * kTile * 4, "the sums take the ring's place");
+    constexpr int smem = kStages<NT> * kStageBytes<NT, G>;
+    static_assert(smem >= 16 * NT * 8 * kTile / 8 * 4, "the parts take the ring's place");
+    static_assert(2 * (smem + 1024) <= 228 * 1024, "two blocks on an SM");
     cudaError_t e = cudaFuncSetAttribute(w4_matvec_kernel<NT, G>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     const int blocks = cluster_of(a.N, a.K), segs = (a.K + kSeg - 1) / kSeg;

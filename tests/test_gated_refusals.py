@@ -123,6 +123,7 @@ def test_w4(lib):
     assert matvec(lib, g=48) == UNSUPPORTED and quantize(lib, g=256) == UNSUPPORTED
     assert matvec(lib, K=224, g=64) == ARG and quantize(lib, K=100, g=32) == ARG
     assert matvec(lib, x=A + 2) == ARG and matvec(lib, q=None) == ARG and matvec(lib, s=None) == ARG
+    assert matvec(lib, s=3 * A + 2) == ARG
     assert matvec(lib, ldx=128) == ARG and matvec(lib, ldy=9) == ARG and matvec(lib, ldx=260) == ARG
     assert matvec(lib, y=A + 64) == ARG  # overlaps x
     assert matvec(lib, y=4 * A + 1) == ARG
