@@ -12,7 +12,8 @@
 //
 // Both are HBM-bound: 4 activations a (token, channel) forward, 7 backward, a few tens of
 // instructions on them. One launch reads every input once, whatever the streams' lengths:
-//  - The packed rows are cut into tiles of L tokens x 32 channels, regardless of where streams meet.
+//  - The packed rows are cut into tiles of L tokens x 32 channels, regardless of where streams meet
+//    (but for the few sections below).
 //    A tile maps the state (or, backward, the gradient m) that reaches it to the one that leaves it:
 //    h -> h + N h + H. N = prod (1 - d) - 1 is carried instead of the product, for the reason in
 //    gated.cuh. Where a stream starts inside the tile, what comes from before is dropped.
@@ -22,9 +23,10 @@
 //    expression, evaluated in the same order, wherever that search ended: results do not depend on
 //    timing. Tiles are handed out in chain order by a counter, so a tile's predecessors are always
 //    done or running and no block waits for one that has not started; the waits are bounded.
-//  - Narrow, long tiles keep that search short: blocks at work / channel groups tiles of a chain are
-//    in flight at a time, 5 at 2048 channels (128-channel tiles of 64 tokens: 19, and the whole scan
-//    was bound by it).
+//  - Narrow, long tiles keep that search short: blocks at work / chains tiles of a chain are in flight
+//    at a time, 5 at 2048 channels (128-channel tiles of 64 tokens: 19, and the whole scan was bound by
+//    it). Several streams make more chains: the rows are cut into sections where a stream starts, each
+//    with tiles and chains of its own, as many as it takes for one tile of a chain in flight.
 //  - Blocks are persistent. Tiles come by TMA into a ring in shared memory and are worked on in
 //    registers, so a tile's place in the ring is free again, and the next copy under way, while the
 //    tile waits for its state.
@@ -65,15 +67,36 @@ template <typename T, bool BWD> struct Shape {
     static constexpr int kSlots = kStages + 1;
 };
 
-// Tokens between two saved states (at packed positions 0, kSave, 2 kSave, ...): the backward tile.
+// Tokens between two saved states, from the start of a section: the backward tile.
 template <typename T> constexpr int kSave = Shape<T, true>::L;
+
+constexpr int kMaxSections = 8;
+
+// Sections of a call: chains enough for the blocks of 152 SMs, and not more than streams. By sizes
+// alone, as the saved states follow them.
+inline int sections_of(int B, int channels) {
+    const int groups = (channels + kWidth - 1) / kWidth, wanted = (2 * 152 + groups - 1) / groups;
+    const int n = wanted < kMaxSections ? wanted : kMaxSections;
+    return n < B ? n : B;
+}
+// The most tiles (saved states) that total tokens in these sections can have.
+inline int64_t tiles_of(int total, int sections, int L) { return (int64_t)total / L + sections; }
 
 // What lies in the workspace before the tiles' words.
 struct Ctl {
     int bad;          // an offset of cu_seqlens is out of order: no stream runs
     int abort;        // a wait ran out: every block leaves
-    unsigned ticket;  // tiles handed out
-    int pad;
+    unsigned ticket;  // tiles handed out, of
+    unsigned tasks;   // tiles * groups
+};
+
+// A tile, by its place in the order of work.
+struct alignas(16) Tile {
+    int t0, count;  // its tokens
+    int id, place;  // in the chains' arrays and in its chain
+    int first;      // the stream of its first token; ~: some token is marked (Slot)
+    int saved;      // row of the saved state that reaches it
+    int pad[2];
 };
 
 // A word of the chains that nobody has written. No value is: arithmetic makes no NaN of this pattern.
@@ -81,27 +104,28 @@ constexpr uint32_t kUnwritten = 0xffffffffu;
 
 struct Chain {
     Ctl *ctl;
-    int *first;          // [tiles]: the stream of the tile's first token; ~: tokens are marked (Slot)
+    Tile *tile;          // [tiles]
     float *N, *H, *out;  // [tiles][groups][32]: the tile's map, the state that leaves it
-    int tiles, groups;
+    int tiles, groups, sections;  // tiles: the most there can be
 };
 
-template <typename T, bool BWD> Chain make_chain(void *workspace, int total, int channels) {
+template <typename T, bool BWD> Chain make_chain(void *workspace, int B, int total, int channels) {
     Chain c;
-    c.tiles = (total + Shape<T, BWD>::L - 1) / Shape<T, BWD>::L;
+    c.sections = sections_of(B, channels);
+    c.tiles = (int)tiles_of(total, c.sections, Shape<T, BWD>::L);
     c.groups = (channels + kWidth - 1) / kWidth;
     const int64_t words = (int64_t)c.tiles * c.groups * kWidth;
     c.ctl = static_cast<Ctl *>(workspace);
-    c.first = reinterpret_cast<int *>(c.ctl + 1);
-    c.N = reinterpret_cast<float *>(c.first + (c.tiles + 3) / 4 * 4);
+    c.tile = reinterpret_cast<Tile *>(c.ctl + 1);
+    c.N = reinterpret_cast<float *>(c.tile + c.tiles);
     c.H = c.N + words;
     c.out = c.H + words;
     return c;
 }
 
-template <typename T, bool BWD> size_t chain_bytes(int total, int channels) {
-    const Chain c = make_chain<T, BWD>(nullptr, total, channels);
-    return sizeof(Ctl) + (size_t)(c.tiles + 3) / 4 * 16 + (size_t)c.tiles * c.groups * kWidth * 12;
+template <typename T, bool BWD> size_t chain_bytes(int B, int total, int channels) {
+    const Chain c = make_chain<T, BWD>(nullptr, B, total, channels);
+    return sizeof(Ctl) + c.tiles * sizeof(Tile) + (size_t)c.tiles * c.groups * kWidth * 12;
 }
 
 // Where the streams start and end in the packed rows.
@@ -111,31 +135,81 @@ struct Streams {
     __device__ __forceinline__ int start(int s) const { return cu ? cu[s] : s * T_each; }
 };
 
-// Clears the chains and looks up every tile's first stream; block 0 also looks at every offset.
-__global__ void chain_init_kernel(Streams st, int L, Chain c, int *status) {
-    const int64_t quads = (int64_t)c.tiles * c.groups * kWidth * 3 / 4;
-    const int64_t t = (int64_t)blockIdx.x * blockDim.x + threadIdx.x, step = (int64_t)gridDim.x * blockDim.x;
-    for (int64_t i = t; i < c.tiles; i += step) {
-        const int t0 = (int)i * L;
+// Clears the chains and lays out the tiles in the order of work: the first of each section's chains
+// (the last one's, BWD), then the second ones, ...; block 0 also looks at every offset.
+template <bool BWD>
+__global__ void chain_init_kernel(Streams st, int L, int save, Chain c, int *status) {
+    // sections, longest first: where they start and end, their first tile's id and saved row
+    __shared__ int from[kMaxSections + 1], start[kMaxSections], end[kMaxSections], id[kMaxSections], row[kMaxSections];
+    const int K = c.sections, tid = threadIdx.x;
+    if (tid <= K) {  // at the first stream that starts at or after an even share
+        const int64_t share = (int64_t)st.total * tid / K;
+        int lo = 0, hi = st.B;  // it is in [lo, hi]
+        while (lo < hi) {
+            const int mid = (lo + hi) / 2;
+            if (st.start(mid) < share) lo = mid + 1; else hi = mid;
+        }
+        from[tid] = st.start(lo);
+    }
+    __syncthreads();
+    if (tid == 0) {
+        int tiles = 0, rows = 0;
+        for (int k = 0; k < K; ++k) {
+            const int len = from[k + 1] - from[k];
+            int at = k;
+            for (; at > 0 && end[at - 1] - start[at - 1] < len; --at)
+                start[at] = start[at - 1], end[at] = end[at - 1], id[at] = id[at - 1], row[at] = row[at - 1];
+            start[at] = from[k], end[at] = from[k + 1], id[at] = tiles, row[at] = rows;
+            tiles += (len + L - 1) / L;
+            rows += (len + save - 1) / save;
+        }
+    }
+    __syncthreads();
+    const int64_t t = (int64_t)blockIdx.x * blockDim.x + tid, step = (int64_t)gridDim.x * blockDim.x;
+    int tasks = 0;
+    for (int k = 0; k < K; ++k) tasks += (end[k] - start[k] + L - 1) / L;
+    for (int64_t o = t; o < c.tiles && o < tasks; o += step) {
+        // order `o`: `place` of section k, where the first j sections still have tiles
+        int rest = (int)o, place = 0, k = 0;
+        for (int j = K; j > 0; --j) {
+            const int upto = (end[j - 1] - start[j - 1] + L - 1) / L;
+            if (rest < j * (upto - place)) {
+                place += rest / j;
+                k = rest % j;
+                break;
+            }
+            rest -= j * (upto - place);
+            place = upto;
+        }
+        const int n = (end[k] - start[k] + L - 1) / L, i = BWD ? n - 1 - place : place;
+        Tile v;
+        v.t0 = start[k] + i * L;
+        v.count = min(L, end[k] - v.t0);
+        v.id = id[k] + i;
+        v.place = place;
+        v.saved = row[k] + i * (L / save);
         int lo = 0, hi = st.B;  // the last stream that starts at or before t0 is in [lo, hi)
         while (hi - lo > 1) {
             const int mid = (lo + hi) / 2;
-            if (st.start(mid) <= t0) lo = mid; else hi = mid;
+            if (st.start(mid) <= v.t0) lo = mid; else hi = mid;
         }
-        const bool whole = st.start(lo) < t0 && st.start(lo + 1) > t0 + L;  // inside one stream
-        c.first[i] = whole ? lo : ~lo;
+        const bool whole = st.start(lo) < v.t0 && st.start(lo + 1) > v.t0 + L;  // inside one stream
+        v.first = whole ? lo : ~lo;
+        v.pad[0] = v.pad[1] = 0;
+        c.tile[o] = v;
     }
+    const int64_t quads = (int64_t)c.tiles * c.groups * kWidth * 3 / 4;
     uint4 *p = reinterpret_cast<uint4 *>(c.N);
     for (int64_t i = t; i < quads; i += step) p[i] = make_uint4(kUnwritten, kUnwritten, kUnwritten, kUnwritten);
     if (blockIdx.x) return;
     int bad = 0;
     if (st.cu) {
-        if (threadIdx.x == 0) bad = st.cu[0] != 0 || st.cu[st.B] != st.total;
-        for (int s = threadIdx.x; s < st.B; s += blockDim.x) bad |= st.cu[s + 1] < st.cu[s];
+        if (tid == 0) bad = st.cu[0] != 0 || st.cu[st.B] != st.total;
+        for (int s = tid; s < st.B; s += blockDim.x) bad |= st.cu[s + 1] < st.cu[s];
     }
     bad = __syncthreads_or(bad);
-    if (threadIdx.x == 0) {
-        *c.ctl = Ctl{bad, 0, 0u, 0};
+    if (tid == 0) {
+        *c.ctl = Ctl{bad, 0, 0u, (unsigned)tasks * (unsigned)c.groups};
         if (bad) raise_status(status, LA_DEV_BAD_SEQLENS);
     }
 }
@@ -143,8 +217,9 @@ __global__ void chain_init_kernel(Streams st, int L, Chain c, int *status) {
 // A tile in the ring: which one it is, and where in it streams start and end.
 template <int L> struct Slot {
     static constexpr int S = L / kRuns;
-    int task;                               // tile * groups + group; -1: no more
-    bool marked;                            // some token is (the last tile's last one always)
+    int t0, count, id, place, saved;        // as Tile
+    int group;                              // of channels; -1: no more
+    bool marked;                            // some token is (a section's last one always)
     uint32_t starts[L / 32], ends[L / 32];  // a bit for each token
     // A bit for each run with a start (an end) in it. A start at the tile's first token and an end
     // at its last are apart: there the state (gradient) that reaches the tile is the stream's own.
@@ -163,14 +238,14 @@ template <int L> struct Slot {
         return mask[run * S / 32] >> (run * S % 32) & ((1u << S) - 1u);
     }
     // the stream of a run's token i
-    __device__ __forceinline__ int id(int run, int i) const {
+    __device__ __forceinline__ int stream(int run, int i) const {
         const uint32_t before = bits(starts, run) & ((2u << i) - 1u);
         return before ? start_id[run * S + 31 - __clz(before)] : run_id[run];
     }
 };
 
-// The whole warp marks the tokens t0 .. t0 + L - 1 of a slot; `lo` is the stream of the first one.
-template <int L> __device__ void mark_streams(const Streams &st, int lo, int t0, int lane, Slot<L> *slot) {
+// The whole warp marks the tokens t0 .. t0 + count - 1 of a slot; `lo` is the stream of the first one.
+template <int L> __device__ void mark_streams(const Streams &st, int lo, int t0, int count, int lane, Slot<L> *slot) {
     if (lane < L / 32) slot->starts[lane] = slot->ends[lane] = 0;
     __syncwarp();
     for (int s0 = lo; s0 < st.B; s0 += 32) {
@@ -180,14 +255,14 @@ template <int L> __device__ void mark_streams(const Streams &st, int lo, int t0,
             b = st.start(s);
             e = st.start(s + 1);
             if (b < e) {  // an empty stream has no tokens to mark
-                if (b >= t0 && b < t0 + L) {
+                if (b >= t0 && b < t0 + count) {
                     atomicOr(&slot->starts[(b - t0) >> 5], 1u << ((b - t0) & 31));
                     slot->start_id[b - t0] = s;
                 }
-                if (e > t0 && e <= t0 + L) atomicOr(&slot->ends[(e - 1 - t0) >> 5], 1u << ((e - 1 - t0) & 31));
+                if (e > t0 && e <= t0 + count) atomicOr(&slot->ends[(e - 1 - t0) >> 5], 1u << ((e - 1 - t0) & 31));
             }
         }
-        if (__any_sync(0xffffffffu, b >= t0 + L || s >= st.B)) break;
+        if (__any_sync(0xffffffffu, b >= t0 + count || s >= st.B)) break;
     }
     __syncwarp();
     const unsigned rs = __ballot_sync(0xffffffffu, slot->starts_of(lane) != 0);
@@ -361,17 +436,14 @@ template <class Cell>
 __device__ __forceinline__ bool pass_on(Window &w, const Chain &c, int place, Cell cell, int lane, float n, float h,
                                         bool reset, bool known, uint64_t wait_ns, bool stall, float &in) {
     const int64_t own = cell(place) * kWidth + lane;
-    const bool publish = place < c.tiles - 1;  // the last one's nobody reads
-    if (publish) {
-        if (reset) {
-            store_relaxed(c.out + own, h);
-        } else if (!known) {
-            store_relaxed(c.N + own, n);
-            store_relaxed(c.H + own, h);
-        }
+    if (reset) {
+        store_relaxed(c.out + own, h);
+    } else if (!known) {
+        store_relaxed(c.N + own, n);
+        store_relaxed(c.H + own, h);
     }
     if (!known && !look_back(w, c, place, cell, lane, wait_ns, stall, in)) return false;
-    if (publish && !reset) store_relaxed(c.out + own, fmaf(n, in, in) + h);
+    if (!reset) store_relaxed(c.out + own, fmaf(n, in, in) + h);
     return true;
 }
 
@@ -403,48 +475,46 @@ template <typename T, bool BWD, class Sh> struct Loader {
     Chain c;
     uint32_t issued;  // tiles put into the ring, the end among them
 
+    unsigned tasks;
     unsigned ticket;  // the tile last taken (lane 0's)
-    int first;        // its first stream
 
-    __device__ __forceinline__ int tile_of(unsigned t) const {
-        const int place = (int)(t / c.groups);
-        return BWD ? c.tiles - 1 - place : place;
-    }
-    __device__ __forceinline__ unsigned tasks() const { return (unsigned)(c.tiles * c.groups); }
     // Takes the next tile of the chains, in their order: late, for a tile taken early is one that its
     // successors wait for (taken one tile sooner, the 262,144 x 2048 scan took 1.00 ms instead of 0.96).
     __device__ __forceinline__ unsigned take(int lane) const { return lane == 0 ? atomicAdd(&c.ctl->ticket, 1u) : 0u; }
-    __device__ __forceinline__ void look_up(int lane) {
-        first = lane == 0 && ticket < tasks() ? __ldg(&c.first[tile_of(ticket)]) : 0;
-    }
     // Starts the copies of the tile last taken into the ring's next place and fills in the slot.
     __device__ void put(int lane) {
         const uint32_t s = issued % G::kStages;
         auto &slot = sh->slot[issued % G::kSlots];
         ++issued;
         const unsigned t = __shfl_sync(0xffffffffu, ticket, 0);
-        if (t >= tasks()) {
+        if (t >= tasks) {
             if (lane == 0) {
-                slot.task = -1;
+                slot.group = -1;
                 mbar_arrive(&sh->full[s]);
                 mbar_arrive(&sh->full[s]);
             }
             return;
         }
-        const int group = (int)(t % c.groups), tile = tile_of(t);
+        const int group = (int)(t % c.groups);
+        const int4 *tile = reinterpret_cast<const int4 *>(c.tile + t / c.groups);
+        const int4 u = tile[0], v = tile[1];  // t0, count, id, place; first, saved
         if (lane == 0) {
             tc::mbar_expect_tx(&sh->full[s], G::kStage);
             const uint32_t to = tc::smem_u32(ring + s * G::kStage);
-            tc::tma_load_2d(to, x, group * kWidth, tile * G::L, &sh->full[s]);
-            tc::tma_load_2d(to + G::kPlane, a, group * kWidth, tile * G::L, &sh->full[s]);
-            tc::tma_load_2d(to + 2 * G::kPlane, b, group * kWidth, tile * G::L, &sh->full[s]);
-            if (BWD) tc::tma_load_2d(to + 3 * G::kPlane, dy, group * kWidth, tile * G::L, &sh->full[s]);
+            tc::tma_load_2d(to, x, group * kWidth, u.x, &sh->full[s]);
+            tc::tma_load_2d(to + G::kPlane, a, group * kWidth, u.x, &sh->full[s]);
+            tc::tma_load_2d(to + 2 * G::kPlane, b, group * kWidth, u.x, &sh->full[s]);
+            if (BWD) tc::tma_load_2d(to + 3 * G::kPlane, dy, group * kWidth, u.x, &sh->full[s]);
         }
-        const int lo = __shfl_sync(0xffffffffu, first, 0);
-        if (lo < 0) mark_streams<G::L>(streams, ~lo, tile * G::L, lane, &slot);
+        if (v.x < 0) mark_streams<G::L>(streams, ~v.x, u.x, u.y, lane, &slot);
         if (lane == 0) {
-            slot.marked = lo < 0;
-            slot.task = tile * c.groups + group;
+            slot.t0 = u.x;
+            slot.count = u.y;
+            slot.id = u.z;
+            slot.place = u.w;
+            slot.saved = v.y;
+            slot.group = group;
+            slot.marked = v.x < 0;
             mbar_arrive(&sh->full[s]);
         }
     }
@@ -452,7 +522,6 @@ template <typename T, bool BWD, class Sh> struct Loader {
     __device__ void begin(int lane) {
         for (int i = 0; i < G::kStages; ++i) {
             ticket = take(lane);
-            look_up(lane);
             put(lane);
 
         }
@@ -488,22 +557,21 @@ scan_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ C
     if (threadIdx.x == 0) init_shared(sh, G::kStages);
     __syncthreads();
     if (c.ctl->bad) return;
-    Loader<T, false, Sh> loader{sh, ring, &map_x, &map_a, &map_b, nullptr, Streams{a.cu, a.B, a.T_each, a.total}, c, 0, 0, 0};
+    Loader<T, false, Sh> loader{sh, ring, &map_x, &map_a, &map_b, nullptr, Streams{a.cu, a.B, a.T_each, a.total}, c, 0, c.ctl->tasks, 0};
     if (warp == kLoader) loader.begin(lane);
     volatile int *failed = &sh->failed;
-    float *saved_initial = a.saved ? a.saved + (int64_t)((a.total + kSave<T> - 1) / kSave<T>) * a.channels : nullptr;
+    float *saved_initial = a.saved ? a.saved + a.saved_rows * a.channels : nullptr;
 
     // One tile of the ring, number `it`. False: the block leaves.
     const auto tile_step = [&](auto is_marked, const Slot<L> &slot, uint32_t it) {
         constexpr bool kMarked = decltype(is_marked)::value;
-        const int task = slot.task, tile = task / c.groups, group = task % c.groups;
-        const int ch = group * kWidth + quad * 4, t0 = tile * L + run * S;
+        const int group = slot.group, place = slot.place, chain = slot.id - place;
+        const int ch = group * kWidth + quad * 4;
         const bool live = ch < a.channels;
         const uint32_t starts = kMarked ? slot.starts_of(run) : 0u;
         const uint32_t resets = kMarked ? slot.run_starts : 0u;
         const bool first = kMarked && slot.first();
-        const auto cell = [&](int place) { return (int64_t)place * c.groups + group; };
-        /*FETCH_A*/
+        const auto cell = [&](int p) { return (int64_t)(chain + p) * c.groups + group; };
 
         // this run's tokens from a state of zero: h, and how much is left of what comes before
         F4 hl[S], A[S];
@@ -518,7 +586,8 @@ scan_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ C
                 if (a.h_ptrs && live) m.H = load_f4(reinterpret_cast<const float *>(a.h_ptrs[id]) + ch);
                 if (a.saved && live) {
                     store_f4(saved_initial + (int64_t)id * a.channels + ch, m.H);
-                    if (i == 0 && t0 % kSave<T> == 0) store_f4(a.saved + (int64_t)(t0 / kSave<T>) * a.channels + ch, m.H);
+                    if (i == 0 && run * S % kSave<T> == 0)
+                        store_f4(a.saved + (int64_t)(slot.saved + run * S / kSave<T>) * a.channels + ch, m.H);
                 }
             }
             F4 nd, beta;
@@ -530,7 +599,7 @@ scan_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ C
             hl[i] = m.H;
             A[i] = R;
         }
-        if (warp == kWarps - 1) sh->window.fetch(c, tile - 1, cell, lane);  // in good time for look_back
+        if (warp == kWarps - 1) sh->window.fetch(c, place - 1, cell, lane);  // in good time for look_back
         store_f4(&sh->N[run][quad * 4], m.N);
         store_f4(&sh->H[run][quad * 4], m.H);
         __syncwarp();
@@ -543,7 +612,6 @@ scan_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ C
         __syncthreads();
         if (*failed) return false;
         if (warp == kLoader) {
-            loader.look_up(lane);
             loader.put(lane);
         }
 
@@ -557,7 +625,7 @@ scan_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ C
                 if (a.h_ptrs) v = reinterpret_cast<const float *>(a.h_ptrs[id])[lane_ch];
                 if (a.saved) saved_initial[(int64_t)id * a.channels + lane_ch] = v;
             }
-            if (!pass_on(sh->window, c, tile, cell, lane, n, h, resets != 0, first, a.wait_ns, a.debug_stall != 0, v))
+            if (!pass_on(sh->window, c, place, cell, lane, n, h, resets != 0, first, a.wait_ns, a.debug_stall != 0, v))
                 give_up(sh, c, lane, a.status);
             sh->in[lane] = v;
         }
@@ -570,19 +638,20 @@ scan_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ C
         v = reset_before<false, kWarps>(warp_resets, warp) ? before_warp.H : before_warp.apply(v);
         const Map before_run = join<false, kMarked, 3, 1>(&sh->N[warp * 4], &sh->H[warp * 4], own_resets, rank, quad);
         v = reset_before<false, 4>(own_resets, rank) ? before_run.H : before_run.apply(v);
-        if (a.saved && live && t0 % kSave<T> == 0 && (!kMarked || (!(starts & 1u) && t0 < a.total)))
-            store_f4(a.saved + (int64_t)(t0 / kSave<T>) * a.channels + ch, v);
+        const int count = kMarked ? slot.count - run * S : S;  // tokens of this run (or more)
+        if (a.saved && live && run * S % kSave<T> == 0 && (!kMarked || (!(starts & 1u) && count > 0)))
+            store_f4(a.saved + (int64_t)(slot.saved + run * S / kSave<T>) * a.channels + ch, v);
         const uint32_t ends = kMarked ? Slot<L>::bits(slot.ends, run) : 0u;
-        T *yp = static_cast<T *>(a.y) + (int64_t)t0 * a.y_stride + ch;
+        T *yp = static_cast<T *>(a.y) + (int64_t)(slot.t0 + run * S) * a.y_stride + ch;
         bool fresh = false;  // a stream has started in this run
 #pragma unroll
         for (int i = 0; i < S; ++i) {
             if (kMarked && (starts >> i & 1u)) fresh = true;
             const F4 y = kMarked && fresh ? hl[i] : fma4(A[i], v, hl[i]);
-            if (live && (!kMarked || t0 + i < a.total)) store_act4<T>(yp, y);
+            if (live && (!kMarked || i < count)) store_act4<T>(yp, y);
             yp += a.y_stride;
             if (kMarked && (ends >> i & 1u) && a.h_ptrs && live)
-                store_f4(reinterpret_cast<float *>(a.h_ptrs[slot.id(run, i)]) + ch, y);
+                store_f4(reinterpret_cast<float *>(a.h_ptrs[slot.stream(run, i)]) + ch, y);
         }
         return true;
     };
@@ -591,7 +660,7 @@ scan_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ C
         if (warp == kLoader) loader.ticket = loader.take(lane);  // for the place that this tile leaves
         const bool arrived = tc::mbar_wait(&sh->full[it % G::kStages], (it / G::kStages) & 1u, a.wait_ns + kWaitNs);
         const Slot<L> &slot = sh->slot[it % G::kSlots];
-        if (arrived && slot.task < 0) break;
+        if (arrived && slot.group < 0) break;
         if (!arrived) {  // nothing of the tile is used; the others leave at their first barrier
             *failed = 1;
             __syncthreads();
@@ -622,10 +691,10 @@ scan_backward_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_con
     if (threadIdx.x == 0) init_shared(sh, G::kStages);
     __syncthreads();
     if (c.ctl->bad) return;
-    Loader<T, true, Sh> loader{sh, ring, &map_x, &map_a, &map_b, &map_dy, Streams{a.cu, a.B, a.T_each, a.total}, c, 0, 0, 0};
+    Loader<T, true, Sh> loader{sh, ring, &map_x, &map_a, &map_b, &map_dy, Streams{a.cu, a.B, a.T_each, a.total}, c, 0, c.ctl->tasks, 0};
     if (warp == kLoader) loader.begin(lane);
     volatile int *failed = &sh->failed;
-    const float *saved_initial = a.saved + (int64_t)c.tiles * a.channels;
+    const float *saved_initial = a.saved + (int64_t)c.tiles * a.channels;  // a tile for each saved row
     if (a.cu && a.dh0_ptrs) {  // the gradient passes through an empty stream
         for (int s = blockIdx.x; s < a.B; s += gridDim.x) {
             if (a.cu[s] != a.cu[s + 1]) continue;
@@ -637,21 +706,19 @@ scan_backward_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_con
 
     const auto tile_step = [&](auto is_marked, const Slot<L> &slot, uint32_t it) {
         constexpr bool kMarked = decltype(is_marked)::value;
-        const int task = slot.task, tile = task / c.groups, group = task % c.groups;
-        const int ch = group * kWidth + quad * 4, t0 = tile * L + run * S;
+        const int group = slot.group, place = slot.place, chain = slot.id + place;
+        const int ch = group * kWidth + quad * 4;
         const bool live = ch < a.channels;
-        const auto cell = [&](int place) { return (int64_t)(c.tiles - 1 - place) * c.groups + group; };
-        const int place = c.tiles - 1 - tile;
-        /*FETCH_A*/
+        const auto cell = [&](int p) { return (int64_t)(chain - p) * c.groups + group; };
         F4 h_in = zero4();  // the state that reaches the tile
-        if (live) h_in = load_f4(a.saved + (int64_t)tile * a.channels + ch);
+        if (live) h_in = load_f4(a.saved + (int64_t)slot.id * a.channels + ch);
         const uint32_t starts = kMarked ? slot.starts_of(run) : 0u, ends = kMarked ? slot.ends_of(run) : 0u;
         const uint32_t resets = kMarked ? slot.run_starts : 0u, end_resets = kMarked ? slot.run_ends : 0u;
         const auto initial = [&](int i) {  // state of the stream that starts at this run's token i
             return live ? load_f4(saved_initial + (int64_t)slot.start_id[run * S + i] * a.channels + ch) : zero4();
         };
         const auto final_gradient = [&](int i) {  // of the stream that ends at this run's token i
-            return a.dh_final_ptrs && live ? load_f4(reinterpret_cast<const float *>(a.dh_final_ptrs[slot.id(run, i)]) + ch)
+            return a.dh_final_ptrs && live ? load_f4(reinterpret_cast<const float *>(a.dh_final_ptrs[slot.stream(run, i)]) + ch)
                                            : zero4();
         };
 
@@ -696,7 +763,6 @@ scan_backward_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_con
         __syncthreads();
         if (*failed) return false;
         if (warp == kLoader) {
-            loader.look_up(lane);
             loader.put(lane);
         }
 
@@ -707,8 +773,8 @@ scan_backward_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_con
             const int lane_ch = group * kWidth + lane;
             const bool last = kMarked && slot.last();
             if (last && a.dh_final_ptrs && lane_ch < a.channels)
-                v = reinterpret_cast<const float *>(a.dh_final_ptrs[slot.id(kRuns - 1, S - 1)])[lane_ch];
-            // behind the chain's first place there is nothing: the last stream ends in it
+                v = reinterpret_cast<const float *>(a.dh_final_ptrs[slot.stream(kRuns - 1, S - 1)])[lane_ch];
+            // behind a chain's first place there is nothing: a stream ends in it
             if (!pass_on(sh->window, c, place, cell, lane, n, h, end_resets != 0, last || place == 0, a.wait_ns,
                          a.debug_stall != 0, v))
                 give_up(sh, c, lane, a.status);
@@ -735,14 +801,15 @@ scan_backward_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_con
         v = reset_before<true, kWarps>(warp_ends, kWarps - 1 - warp) ? m_warp.H : m_warp.apply(v);
         v = reset_before<true, 4>(own_ends, 3 - rank) ? m_run.H : m_run.apply(v);
         const uint32_t all_starts = kMarked ? Slot<L>::bits(slot.starts, run) : 0u;
-        T *dxp = static_cast<T *>(a.dx) + (int64_t)(t0 + S - 1) * a.dx_stride + ch;
-        T *dap = static_cast<T *>(a.dab) + (int64_t)(t0 + S - 1) * a.dab_stride + ch;
+        const int count = kMarked ? slot.count - run * S : S;
+        T *dxp = static_cast<T *>(a.dx) + (int64_t)(slot.t0 + run * S + S - 1) * a.dx_stride + ch;
+        T *dap = static_cast<T *>(a.dab) + (int64_t)(slot.t0 + run * S + S - 1) * a.dab_stride + ch;
 #pragma unroll
         for (int i = S - 1; i >= 0; --i) {
             if (kMarked && (ends >> i & 1u)) v = final_gradient(i);
             const F4 lam = add4(widen4<T>(dyr[i]), v), dx = mul4(lam, beta[i]);
             v = left4(nd[i], lam);
-            if (live && (!kMarked || t0 + i < a.total)) {
+            if (live && (!kMarked || i < count)) {
                 store_act4<T>(dxp, dx);
                 store_act4<T>(dap, mul4(mul4(v, hp[i]), nd[i]));
                 store_act4<T>(dap + a.channels, mul4(mul4(dx, widen4<T>(xr[i])), fma4(beta[i], all4(-1.f), all4(1.f))));
@@ -759,7 +826,7 @@ scan_backward_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_con
         if (warp == kLoader) loader.ticket = loader.take(lane);  // for the place that this tile leaves
         const bool arrived = tc::mbar_wait(&sh->full[it % G::kStages], (it / G::kStages) & 1u, a.wait_ns + kWaitNs);
         const Slot<L> &slot = sh->slot[it % G::kSlots];
-        if (arrived && slot.task < 0) break;
+        if (arrived && slot.group < 0) break;
         if (!arrived) {  // nothing of the tile is used; the others leave at their first barrier
             *failed = 1;
             __syncthreads();
@@ -798,20 +865,21 @@ cudaError_t start(Kernel kernel, const Streams &streams, const Chain &c, int *st
     if (e != cudaSuccess) return e;
     const int64_t cells = (int64_t)c.tiles * c.groups, clear = (cells * kWidth * 3 / 4 + 1023) / 1024;
     const int sms = device_sms();
-    chain_init_kernel<<<(int)(clear < sms ? clear : sms), 1024, 0, st>>>(streams, G::L, c, status);
+    chain_init_kernel<BWD><<<(int)(clear < sms ? clear : sms), 1024, 0, st>>>(streams, G::L, kSave<T>, c, status);
     const int room = G::kBlocks * sms;
     launch((int)(cells < room ? cells : room), smem);
     return cudaGetLastError();
 }
 
-template <typename T> cudaError_t scan(const GatedScanArgs &a, cudaStream_t st) {
+template <typename T> cudaError_t scan(GatedScanArgs a, cudaStream_t st) {
     CUtensorMap x, ga, gb;
     const T *ab = static_cast<const T *>(a.ab);
     if (!tile_map<T, false>(&x, a.x, a.total, a.channels, a.x_stride) ||
         !tile_map<T, false>(&ga, ab, a.total, a.channels, a.ab_stride) ||
         !tile_map<T, false>(&gb, ab + a.channels, a.total, a.channels, a.ab_stride))
         return cudaErrorInvalidValue;
-    const Chain c = make_chain<T, false>(a.workspace, a.total, a.channels);
+    a.saved_rows = tiles_of(a.total, sections_of(a.B, a.channels), kSave<T>);
+    const Chain c = make_chain<T, false>(a.workspace, a.B, a.total, a.channels);
     return start<T, false>(scan_kernel<T>, Streams{a.cu, a.B, a.T_each, a.total}, c, a.status, st, [&](int grid, size_t smem) {
         scan_kernel<T><<<grid, kThreads, smem, st>>>(x, ga, gb, a, c);
     });
@@ -825,7 +893,7 @@ template <typename T> cudaError_t backward(const GatedScanBwdArgs &a, cudaStream
         !tile_map<T, true>(&gb, ab + a.channels, a.total, a.channels, a.ab_stride) ||
         !tile_map<T, true>(&dy, a.dy, a.total, a.channels, a.dy_stride))
         return cudaErrorInvalidValue;
-    const Chain c = make_chain<T, true>(a.workspace, a.total, a.channels);
+    const Chain c = make_chain<T, true>(a.workspace, a.B, a.total, a.channels);
     return start<T, true>(scan_backward_kernel<T>, Streams{a.cu, a.B, a.T_each, a.total}, c, a.status, st, [&](int grid, size_t smem) {
         scan_backward_kernel<T><<<grid, kThreads, smem, st>>>(x, ga, gb, dy, a, c);
     });
@@ -833,13 +901,14 @@ template <typename T> cudaError_t backward(const GatedScanBwdArgs &a, cudaStream
 
 }  // namespace
 
-size_t gated_scan_workspace_bytes(int, int total, int channels, int dtype) {  // of either pass
-    return dtype == LA_BF16 ? chain_bytes<__nv_bfloat16, true>(total, channels) : chain_bytes<float, true>(total, channels);
+size_t gated_scan_workspace_bytes(int B, int total, int channels, int dtype) {  // of either pass
+    return dtype == LA_BF16 ? chain_bytes<__nv_bfloat16, true>(B, total, channels)
+                            : chain_bytes<float, true>(B, total, channels);
 }
 
 size_t gated_scan_saved_bytes(int B, int total, int channels, int dtype) {
     const int every = dtype == LA_BF16 ? kSave<__nv_bfloat16> : kSave<float>;
-    return (((size_t)total + every - 1) / every + B) * channels * sizeof(float);
+    return ((size_t)tiles_of(total, sections_of(B, channels), every) + B) * channels * sizeof(float);
 }
 
 cudaError_t launch_gated_scan(const GatedScanArgs &a, cudaStream_t st) {

@@ -161,6 +161,7 @@ struct GatedScanArgs {
     const void *x, *ab;
     void *y;
     float *saved;  // states for the backward pass, or nullptr
+    int64_t saved_rows;  // rows of it before the initial states' (set by the launch)
     const int32_t *cu;  // nullptr: B streams of T_each tokens
     int B, T_each, total, channels;
     int64_t x_stride, ab_stride, y_stride;
