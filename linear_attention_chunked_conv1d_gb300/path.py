@@ -19,11 +19,13 @@ import math
 
 import torch
 
-from . import (conv1d_silu_l2_prefill, conv1d_silu_prefill, conv1d_silu_prefill_varlen,
-               decode_step, decode_workspace_bytes, gate_activations, gdn_prefill_batched,
-               gdn_prefill_varlen, gemm_bf16, kda_prefill, l2norm_heads, pointer_array,
-               prefill_front, prefill_segmented, prefill_segmented_workspace_bytes,
-               prefill_workspace_bytes, rmsnorm_rows)
+from . import (conv1d_silu_backward, conv1d_silu_backward_workspace_bytes, conv1d_silu_l2_prefill,
+               conv1d_silu_prefill, conv1d_silu_prefill_varlen, decode_step,
+               decode_workspace_bytes, gate_activations, gated_scan, gated_scan_backward,
+               gated_scan_saved_bytes, gated_scan_step, gated_scan_workspace_bytes,
+               gdn_prefill_batched, gdn_prefill_varlen, gemm_bf16, kda_prefill, l2norm_heads,
+               pointer_array, prefill_front, prefill_segmented, prefill_segmented_workspace_bytes,
+               prefill_workspace_bytes, rmsnorm_rows, w4_matvec)
 
 
 class PrefillPass:
@@ -152,12 +154,25 @@ class DecodeStep:
         return self.out
 
 
+def project(y, w, out=None, stream=None):
+    """y W^T for a linear layer's weight: bf16 [out][in], or the (q, scales) of w4_quantize (then at
+    most LA_W4_MAX_ROWS rows)."""
+    if isinstance(w, tuple):
+        return w4_matvec(y, *w, out, stream=stream)
+    return gemm_bf16(y, w, out, stream=stream)
+
+
+def _outputs(w) -> int:
+    return (w[0] if isinstance(w, tuple) else w).shape[0]
+
+
 class Phase1:
     """Phase 1 of a layer over the stacked hidden rows ("split_prefill.rs",
     prefill_phase1_proj_batched: norm, QKVZ, gates), through the library:
     rmsnorm_rows -> three projection GEMMs (q|k|v, z, gate pre-activations a|b) -> gate
-    activations. Weights are the caller's ([out][in] bf16); outputs are device tensors:
-    x [t][cd] (the conv input), z [t][Hv*dv], g (fp32 [t][Hv] or [t][Hv*dk]), beta [t][Hv]."""
+    activations. Weights are the caller's ([out][in] bf16, or the 4-bit (q, scales) of w4_quantize
+    for the few rows of a decode step); outputs are device tensors: x [t][cd] (the conv input),
+    z [t][Hv*dv], g (fp32 [t][Hv] or [t][Hv*dk]), beta [t][Hv]."""
 
     def __init__(self, wl, norm_w, w_qkv, w_z, w_ab, *, eps=1e-6):
         self.wl, self.norm_w, self.w_qkv, self.w_z, self.w_ab, self.eps = (
@@ -166,11 +181,11 @@ class Phase1:
 
     def run(self, hidden, stream=None):
         y = rmsnorm_rows(hidden, self.norm_w, eps=self.eps, stream=stream)
-        x = gemm_bf16(y, self.w_qkv, stream=stream)
-        z = gemm_bf16(y, self.w_z, stream=stream)
-        n_ab = self.w_ab.shape[0]  # rows padded to 16 bytes (the GEMM's output stride rule)
+        x = project(y, self.w_qkv, stream=stream)
+        z = project(y, self.w_z, stream=stream)
+        n_ab = _outputs(self.w_ab)  # rows padded to 16 bytes (the GEMM's output stride rule)
         ab = torch.empty(y.shape[0], (n_ab + 7) // 8 * 8, dtype=y.dtype, device=y.device)[:, :n_ab]
-        gemm_bf16(y, self.w_ab, ab, stream=stream)
+        project(y, self.w_ab, ab, stream=stream)
         g, beta = gate_activations(ab, self.na, stream=stream)
         return dict(y=y, x=x, z=z, ab=ab, g=g, beta=beta)
 
@@ -237,3 +252,85 @@ class StreamedPrefill:
         """Make the compute stream wait for the last copies back (then record on it)."""
         self.compute.wait_event(self.drained[0])
         self.compute.wait_event(self.drained[1])
+
+
+class GatedPass:
+    """Repeated passes of a gated recurrent layer (one state per channel) over one packed batch:
+    conv1d + SiLU over the carried windows, then the gated scan from the carried states.
+
+    `inputs` holds device tensors: x [T][C] (before the conv) and ab [T][2C] (gate rows a | b),
+    conv_w [C][K], conv_bias [C] or None, conv_state [B][K-1][C], h [B][C] (fp32), cu_seqlens.
+    forward() advances both states; with train=True it also keeps what backward() needs: the
+    conv states as they were, and the scan's saved states."""
+
+    def __init__(self, inputs: dict, *, train: bool = False):
+        self.inp, self.train = inputs, train
+        x, h, conv_state = inputs["x"], inputs["h"], inputs["conv_state"]
+        (T, C), B, dev = x.shape, h.shape[0], x.device
+        K = inputs["conv_w"].shape[1]
+        self.u, self.y = torch.empty_like(x), torch.empty_like(x)
+        self.h_ptrs = pointer_array(list(h))
+        self.conv_ptrs = pointer_array(list(conv_state)) if K > 1 else None
+        room = lambda n: torch.empty(n, dtype=torch.uint8, device=dev)  # noqa: E731
+        self.workspace = room(gated_scan_workspace_bytes(B, T, C, x.dtype))
+        if train:
+            self.saved = room(gated_scan_saved_bytes(B, T, C, x.dtype))
+            self.conv_workspace = room(conv1d_silu_backward_workspace_bytes(B, T, C, K, x.dtype))
+            self.conv_start = torch.empty_like(conv_state)
+            self.conv_start_ptrs = pointer_array(list(self.conv_start)) if K > 1 else None
+            self.grads = dict(x=torch.empty_like(x), ab=torch.empty_like(inputs["ab"]),
+                              conv_w=torch.empty(C, K, device=dev), conv_bias=torch.empty(C, device=dev),
+                              conv_state=torch.empty_like(conv_state), h=torch.empty_like(h))
+            self.du = torch.empty_like(x)
+            self.dh_ptrs = pointer_array(list(self.grads["h"]))
+            self.dconv_ptrs = pointer_array(list(self.grads["conv_state"])) if K > 1 else None
+
+    def forward(self, stream=None):
+        inp = self.inp
+        if self.train:
+            with torch.cuda.stream(stream):
+                self.conv_start.copy_(inp["conv_state"])
+        conv1d_silu_prefill_varlen(self.conv_ptrs, inp["x"], inp["conv_w"], self.u, inp["cu_seqlens"],
+                                   bias=inp["conv_bias"], stream=stream)
+        gated_scan(self.h_ptrs, self.u, inp["ab"], self.y, inp["cu_seqlens"],
+                   saved=self.saved if self.train else None, workspace=self.workspace, stream=stream)
+        return self.y
+
+    def backward(self, dy, *, dh_final_ptrs=None, dconv_final_ptrs=None, stream=None):
+        """Gradients of the last forward(), by the names of `inputs`; of the states that it left,
+        where given (pointer arrays, as gated_scan_backward and conv1d_silu_backward take them)."""
+        inp, g = self.inp, self.grads
+        gated_scan_backward(self.u, inp["ab"], self.saved, dy, self.du, g["ab"], inp["cu_seqlens"],
+                            dh_final_ptrs=dh_final_ptrs, dh0_ptrs=self.dh_ptrs,
+                            workspace=self.workspace, stream=stream)
+        bias = inp["conv_bias"]
+        conv1d_silu_backward(self.conv_start_ptrs, inp["x"], inp["conv_w"], self.du, g["x"], g["conv_w"],
+                             inp["cu_seqlens"], bias=bias, dbias=None if bias is None else g["conv_bias"],
+                             dstate_final_ptrs=dconv_final_ptrs, dstate_ptrs=self.dconv_ptrs,
+                             workspace=self.conv_workspace, stream=stream)
+        return g
+
+
+class GatedDecode:
+    """Decode steps of a gated recurrent layer for B streams (one token each): row RMSNorm, one
+    projection to x | a | b (3C outputs; bf16 weight or the 4-bit (q, scales) of w4_quantize),
+    conv1d + SiLU and the gated recurrence on the carried states, the projection back (w_out)."""
+
+    def __init__(self, norm_w, w_in, w_out, conv_w, conv_bias, conv_state, h, *, eps=1e-6):
+        self.norm_w, self.w_in, self.w_out, self.eps = norm_w, w_in, w_out, eps
+        self.conv_w, self.conv_bias = conv_w, conv_bias
+        self.B, self.C = h.shape
+        dev, bf16 = h.device, torch.bfloat16
+        self.conv_ptrs = pointer_array(list(conv_state)) if conv_w.shape[1] > 1 else None
+        self.h_ptrs = pointer_array(list(h))
+        self.rows = torch.empty(self.B, 3 * self.C, dtype=bf16, device=dev)
+        self.y = torch.empty(self.B, self.C, dtype=bf16, device=dev)
+        self.out = torch.empty(self.B, _outputs(w_out), dtype=bf16, device=dev)
+
+    def run(self, hidden, stream=None):
+        n = rmsnorm_rows(hidden, self.norm_w, eps=self.eps, stream=stream)
+        project(n, self.w_in, self.rows, stream=stream)
+        gated_scan_step(self.h_ptrs, self.rows[:, :self.C], self.rows[:, self.C:], self.y,
+                        conv_state_ptrs=self.conv_ptrs, conv_w=self.conv_w, conv_bias=self.conv_bias,
+                        stream=stream)
+        return project(self.y, self.w_out, self.out, stream=stream)

@@ -1,0 +1,207 @@
+"""The gated recurrent layer's operators together, as they are used: a training pass of conv1d + SiLU and
+the scan against automatic differentiation in 64 bits, a decode loop with 4-bit projections against the
+calls one by one and against the plain layer, and phase 1 with 4-bit weights."""
+import numpy as np
+import pytest
+import torch
+
+import linear_attention_chunked_conv1d_gb300 as la
+from linear_attention_chunked_conv1d_gb300.inputs import WORKLOADS
+from linear_attention_chunked_conv1d_gb300.path import GatedDecode, GatedPass, Phase1
+from tests.helpers import f64
+
+pytestmark = pytest.mark.gpu
+
+
+def layer64(x, ab, conv_w, conv_bias, conv_state, h, lengths):
+    """The plain layer in 64 bits, differentiable: y, the windows and the states it leaves."""
+    K, C = conv_w.shape[1], x.shape[1]
+    ys, windows, states, t0 = [], [], [], 0
+    for s, n in enumerate(lengths):
+        rows = torch.cat([conv_state[s], x[t0:t0 + n]])
+        state = h[s]
+        for t in range(n):
+            p = conv_bias + (rows[t:t + K] * conv_w.t()).sum(0)
+            u = p * torch.sigmoid(p)
+            a, b = ab[t0 + t, :C], ab[t0 + t, C:]
+            state = (1 - torch.sigmoid(a)) * state + torch.sigmoid(b) * u
+            ys.append(state)
+        windows.append(rows[n:])
+        states.append(state)
+        t0 += n
+    return torch.stack(ys), torch.stack(windows), torch.stack(states)
+
+
+def test_training_pass(cuda):
+    """Every gradient, of a loss over y and the states left behind. Gates within 4 keep the memory under
+    60 tokens; each of the three kernels is off by a few 2^-20 of its own operands (their own tests),
+    which the sums over tokens average: 2^-15 of a gradient's largest value is a factor of ten more."""
+    lengths, C, K = [70, 0, 1, 33, 130], 40, 4
+    T, B = sum(lengths), len(lengths)
+    g = torch.Generator().manual_seed(1)
+    r = lambda *s: torch.randn(*s, generator=g)  # noqa: E731
+    host = dict(x=r(T, C), ab=r(T, 2 * C).clamp(-4, 4), conv_w=0.5 * r(C, K), conv_bias=r(C),
+                conv_state=r(B, K - 1, C), h=r(B, C))
+    dy, dwindow, dstate = r(T, C), r(B, K - 1, C), r(B, C)
+    v = {n: u.double().requires_grad_() for n, u in host.items()}
+    y, windows, states = layer64(**v, lengths=lengths)
+    ((y * dy).sum() + (windows * dwindow).sum() + (states * dstate).sum()).backward()
+
+    inp = {n: u.to(cuda) for n, u in host.items()}
+    inp["cu_seqlens"] = torch.tensor(np.concatenate([[0], np.cumsum(lengths)]), dtype=torch.int32, device=cuda)
+    p = GatedPass(inp, train=True)
+    for _ in range(2):  # a second step from the same states gives the same
+        for n in ("conv_state", "h"):
+            inp[n].copy_(host[n])
+        got_y = p.forward()
+        dw, ds = dwindow.to(cuda), dstate.to(cuda)
+        grads = p.backward(dy.to(cuda), dh_final_ptrs=la.pointer_array(list(ds)),
+                           dconv_final_ptrs=la.pointer_array(list(dw)))
+        torch.cuda.synchronize()
+        assert la.device_status() == 0
+        for got, want in ((got_y, y), (inp["h"], states), (inp["conv_state"], windows)):
+            want = want.detach().numpy()
+            assert np.max(np.abs(f64(got) - want)) <= 2.0 ** -15 * np.max(np.abs(want))
+        for n, got in grads.items():
+            want = v[n].grad.numpy()
+            assert np.max(np.abs(f64(got) - want)) <= 2.0 ** -15 * np.max(np.abs(want)), n
+
+
+def test_training_pass_in_two_pieces_matches_one(cuda):
+    """Truncating nothing: the gradients of the states that the second piece started from, handed to the
+    first piece as those of the states it left, give the whole sequence's gradients."""
+    C, K, T, cut = 24, 4, 300, 111
+    g = torch.Generator().manual_seed(2)
+    r = lambda *s: torch.randn(*s, generator=g)  # noqa: E731
+    host = dict(x=r(T, C), ab=r(T, 2 * C).clamp(-4, 4), conv_w=0.5 * r(C, K), conv_bias=r(C),
+                conv_state=r(1, K - 1, C), h=r(1, C))
+    dy = r(T, C).to(cuda)
+
+    def a_pass(lo, hi, conv_state, h):
+        inp = {n: u.to(cuda) for n, u in host.items()}
+        inp.update(x=inp["x"][lo:hi], ab=inp["ab"][lo:hi], conv_state=conv_state.clone(), h=h.clone(),
+                   cu_seqlens=torch.tensor([0, hi - lo], dtype=torch.int32, device=cuda))
+        p = GatedPass(inp, train=True)
+        p.forward()
+        return p, inp
+
+    whole, _ = a_pass(0, T, host["conv_state"].to(cuda), host["h"].to(cuda))
+    want = {n: u.clone() for n, u in whole.backward(dy).items()}
+    one, inp = a_pass(0, cut, host["conv_state"].to(cuda), host["h"].to(cuda))
+    two, _ = a_pass(cut, T, inp["conv_state"], inp["h"])
+    g2 = two.backward(dy[cut:])
+    g1 = one.backward(dy[:cut], dh_final_ptrs=la.pointer_array(list(g2["h"])),
+                      dconv_final_ptrs=la.pointer_array(list(g2["conv_state"])))
+    torch.cuda.synchronize()
+    for n in ("x", "ab"):
+        got = torch.cat([g1[n], g2[n]])
+        assert float((got - want[n]).abs().max()) <= 2.0 ** -15 * float(want[n].abs().max()), n
+    for n in ("conv_w", "conv_bias"):
+        assert float((g1[n] + g2[n] - want[n]).abs().max()) <= 2.0 ** -15 * float(want[n].abs().max()), n
+    for n in ("h", "conv_state"):
+        assert float((g1[n] - want[n]).abs().max()) <= 2.0 ** -15 * float(want[n].abs().max()), n
+
+
+@pytest.mark.parametrize("B", [1, 5, 32])
+def test_decode_loop(cuda, B):
+    """Prompts through GatedPass, then tokens through GatedDecode with 4-bit projections: the states are
+    the plain layer's, fed with the rows that the projection gave."""
+    C, D, K, steps = 96, 256, 4, 3
+    g = torch.Generator().manual_seed(3 + B)
+    r = lambda *s: torch.randn(*s, generator=g).to(torch.bfloat16).to(cuda)  # noqa: E731
+    norm_w, conv_w, bias = r(D), (0.5 * r(C, K)).contiguous(), r(C)
+    w_in = la.w4_quantize((r(3 * C, D) / D ** 0.5).contiguous(), group=64)
+    w_out = la.w4_quantize((r(D, C) / C ** 0.5).contiguous(), group=32)
+    lengths = [7 + 3 * (s % 4) for s in range(B)]
+    T = sum(lengths)
+    inp = dict(x=r(T, C), ab=r(T, 2 * C), conv_w=conv_w, conv_bias=bias, conv_state=r(B, K - 1, C),
+               h=torch.randn(B, C, generator=g).to(cuda),
+               cu_seqlens=torch.tensor(np.concatenate([[0], np.cumsum(lengths)]), dtype=torch.int32, device=cuda))
+    GatedPass(inp).forward()
+    state, win = f64(inp["h"]), f64(inp["conv_state"])
+    layer = GatedDecode(norm_w, w_in, w_out, conv_w, bias, inp["conv_state"], inp["h"])
+    for t in range(steps):
+        out = layer.run(r(B, D))
+        torch.cuda.synchronize()
+        x, ab = f64(layer.rows[:, :C]), f64(layer.rows[:, C:])
+        xh = np.concatenate([win, x[:, None]], 1)
+        p = f64(bias) + np.einsum("bkc,ck->bc", xh, f64(conv_w))
+        keep, beta = 1 / (1 + np.exp(ab[:, :C])), 1 / (1 + np.exp(-ab[:, C:]))
+        state, win = keep * state + beta * p / (1 + np.exp(-p)), xh[:, 1:]
+        # three steps, each under 2^-19 of its operands (those of the conv: up to 10)
+        assert np.max(np.abs(f64(inp["h"]) - state) / np.maximum(np.abs(state), 1.0)) <= 2.0 ** -14
+        assert np.array_equal(f64(inp["conv_state"]), win)
+        assert np.all(np.abs(f64(layer.y) - state) <= 2.0 ** -8 * np.abs(state) + 2.0 ** -13)
+        assert out.shape == (B, D) and bool(torch.isfinite(out).all())
+
+
+def test_decode_path_object(cuda):
+    """GatedDecode.run against the calls one by one, for 4-bit and for bf16 weights."""
+    B, C, D, K = 6, 128, 256, 3
+    g = torch.Generator().manual_seed(9)
+    r = lambda *s: torch.randn(*s, generator=g).to(torch.bfloat16).to(cuda)  # noqa: E731
+    norm_w, conv_w, bias = r(D), (0.5 * r(C, K)).contiguous(), r(C)
+    dense_in, dense_out = (r(3 * C, D) / D ** 0.5).contiguous(), (r(D, C) / C ** 0.5).contiguous()
+    for w_in, w_out in (((la.w4_quantize(dense_in)), (la.w4_quantize(dense_out))), (dense_in, dense_out)):
+        window, h = r(B, K - 1, C), torch.randn(B, C, generator=g).to(cuda)
+        window2, h2 = window.clone(), h.clone()
+        layer = GatedDecode(norm_w, w_in, w_out, conv_w, bias, window, h)
+        for _ in range(3):
+            hidden = r(B, D)
+            got = layer.run(hidden).clone()
+            mul = la.w4_matvec if isinstance(w_in, tuple) else (lambda v, w: la.gemm_bf16(v, w))
+            args = (lambda w: w) if isinstance(w_in, tuple) else (lambda w: (w,))
+            rows = mul(la.rmsnorm_rows(hidden, norm_w), *args(w_in))
+            y = torch.empty(B, C, dtype=torch.bfloat16, device=cuda)
+            la.gated_scan_step(la.pointer_array(list(h2)), rows[:, :C], rows[:, C:], y, conv_w=conv_w, conv_bias=bias,
+                               conv_state_ptrs=la.pointer_array(list(window2)))
+            want = mul(y, *args(w_out))
+            torch.cuda.synchronize()
+            assert torch.equal(got, want) and torch.equal(h, h2) and torch.equal(window, window2)
+
+
+def test_phase1_with_4_bit_weights(cuda):
+    """Phase 1 of a decode step: every output against the 64-bit products of its own stage's inputs."""
+    wl = WORKLOADS["gdn_varlen_32_hk16_hv32_d128"].replace(B=4, Hk=1, Hv=2)
+    D, t = 256, 4
+    g = torch.Generator().manual_seed(10)
+    r = lambda *s: torch.randn(*s, generator=g).to(torch.bfloat16).to(cuda)  # noqa: E731
+    dense = [(r(n, D) / D ** 0.5).contiguous() for n in (wl.cd, wl.Hv * wl.d, 2 * wl.Hv)]
+    w = [la.w4_quantize(v, group=32) for v in dense]
+    norm_w, hidden = r(D), r(t, D)
+    out = Phase1(wl, norm_w, *w).run(hidden)
+    torch.cuda.synchronize()
+    assert torch.equal(out["x"], la.w4_matvec(out["y"], *w[0])) and torch.equal(out["z"], la.w4_matvec(out["y"], *w[1]))
+    assert torch.equal(out["ab"], la.w4_matvec(out["y"], *w[2]))
+    a, b = f64(out["ab"][:, :wl.Hv]), f64(out["ab"][:, wl.Hv:])
+    assert np.max(np.abs(f64(out["g"]) + np.logaddexp(0, a))) <= 1e-5
+    assert np.max(np.abs(f64(out["beta"]) - 1 / (1 + np.exp(-b)))) <= 1e-6
+    assert out["x"].shape == (t, wl.cd) and out["z"].shape == (t, wl.Hv * wl.d)
+
+
+def test_scan_wait_runs_out_then_next_call_is_correct(cuda, monkeypatch):
+    """With LA_DEBUG_STALL=1 a tile's search of its chain finds nothing; after LA_WAIT_LIMIT_NS the call
+    gives up, every block leaves, the status says so, and the next call runs."""
+    T, C = 3000, 64
+    g = torch.Generator().manual_seed(11)
+    x, ab = torch.randn(T, C, generator=g).to(cuda), torch.randn(T, 2 * C, generator=g).to(cuda)
+    ws = torch.empty(la.gated_scan_workspace_bytes(1, T, C, x.dtype), dtype=torch.uint8, device=cuda)
+    saved = torch.empty(la.gated_scan_saved_bytes(1, T, C, x.dtype), dtype=torch.uint8, device=cuda)
+    y, dx, dab = torch.empty_like(x), torch.empty_like(x), torch.empty_like(ab)
+
+    def call():
+        la.gated_scan(None, x, ab, y, saved=saved, workspace=ws)
+        first = la.device_status()
+        la.gated_scan_backward(x, ab, saved, x, dx, dab, workspace=ws)
+        return first, la.device_status()
+
+    assert call() == (0, 0)
+    want = [v.clone() for v in (y, dx, dab)]
+    monkeypatch.setenv("LA_DEBUG_STALL", "1")
+    monkeypatch.setenv("LA_WAIT_LIMIT_NS", "1000000")
+    assert call() == (la.LA_DEV_TIMEOUT, la.LA_DEV_TIMEOUT)
+    monkeypatch.delenv("LA_DEBUG_STALL")
+    monkeypatch.delenv("LA_WAIT_LIMIT_NS")
+    assert call() == (0, 0)
+    for u, v in zip((y, dx, dab), want):
+        assert torch.equal(u, v)
