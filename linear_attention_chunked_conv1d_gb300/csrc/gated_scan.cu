@@ -53,15 +53,18 @@ constexpr int kRuns = 4 * kWarps;  // is along the tokens, in runs of S
 constexpr uint64_t kWaitNs = 2000000000ull;
 
 // Tokens of a run, and the ring's depth. What a thread keeps of a tile across the wait for its state
-// is 2 registers a (token, channel) forward and 4 to 5 backward; two blocks on an SM leave 128
-// registers a thread, which these fill. Two blocks' rings take 192 KB of shared memory.
+// is 2 registers a (token, channel) forward and 4 (bf16) or 5 (fp32) backward; two blocks on an SM leave
+// 128 registers a thread, which these fill: half of these runs takes half again as long. A tile's place
+// in the ring is free, and its next copy under way, half way through the tile: backward one place is
+// enough (a second one only takes tiles earlier than needed: 8 x 2048 x 4096 bf16, both passes, 357 us
+// instead of 350), forward two are better by 5%.
 template <typename T, bool BWD> struct Shape {
     static constexpr int kIn = BWD ? 4 : 3;                              // x, a, b (, dy)
-    static constexpr int S = sizeof(T) == 2 ? (BWD ? 4 : 8) : (BWD ? 2 : 4);
+    static constexpr int S = sizeof(T) == 2 && !BWD ? 8 : 4;
     static constexpr int L = S * kRuns;
     static constexpr int kPlane = L * kWidth * (int)sizeof(T);           // bytes of one input's tile
-    static constexpr int kStage = kIn * kPlane;                          // 48 KB forward, 32 KB backward
-    static constexpr int kStages = 2;
+    static constexpr int kStage = kIn * kPlane;                          // 48 KB; backward 32 (bf16), 64 (fp32)
+    static constexpr int kStages = BWD ? 1 : 2;
     static constexpr int kBlocks = 2;                                    // on an SM
     // A slot is read until its tile is done, one tile longer than its copies are.
     static constexpr int kSlots = kStages + 1;

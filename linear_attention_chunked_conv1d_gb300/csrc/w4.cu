@@ -41,15 +41,14 @@ __global__ void w4_quantize_kernel(const W4QuantArgs a, int64_t words) {
 }
 
 // The products: a tile of 128 outputs over a share of the inputs that the blocks of a cluster split.
-// 256 inputs at a time go through a ring of asynchronous copies: the tile's weights (16 KB) and the
-// rows' inputs, laid out so that a lane finds its part of an operand in 16 bytes, and the scales (by
-// plain loads a stage ahead, these alone made 32 x 16384 x 8192 take 44 us). A warp has 32 of the
-// outputs and 128 of the inputs. Weights are the A operand of mma.m16n8k16, 16 outputs by 16 inputs,
-// as exact bf16 integers -8 .. 7; the rows are B. A lane's word of eight weights serves two mma: which
+// 256 inputs at a time go through a ring of asynchronous copies: the tile's weights (16 KB), the rows'
+// inputs, laid out so that a lane finds its part of an operand in 16 bytes, and the scales. A warp has
+// 32 of the outputs and 128 of the inputs. Weights are the A operand of mma.m16n8k16, 16 outputs by 16
+// inputs, as exact bf16 numbers; the rows are B. A lane's word of eight weights serves two mma: which
 // inputs meet in one mma is free as long as A and B agree, so word c of 32 inputs goes to the lanes
-// with c = lane % 4 as it lies in memory. Products and sums within a group are exact integers times
-// bf16 in fp32; each group's sum is scaled by its output's scale and added up in fp32. In the end every
-// block of the cluster gets all parts of its share of the outputs and adds them in a fixed order.
+// with c = lane % 4 as it lies in memory. Products are exact in fp32; a group's sum is scaled by its
+// output's scale and added to the others in fp32. In the end every block of the cluster gets all parts
+// of its share of the outputs and adds them in a fixed order.
 constexpr int kThreads = 256;
 constexpr int kTile = 128;           // outputs of a block: four warps of 32
 constexpr int kSeg = 256;            // inputs of a stage: two warps of 128
@@ -74,12 +73,23 @@ __device__ __forceinline__ void mma_bf16(float (&d)[4], const uint32_t (&a)[4], 
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-// Weights 2i and 2i + 1 of a word as bf16: 128 + q is exact in bf16 (0x4300 | q), and so is its
-// difference to 136.
-__device__ __forceinline__ uint32_t weight_pair(uint32_t word, int i) {
-    const uint32_t v = (word >> (4 * i) & 0x000f000fu) | 0x43004300u;
-    __nv_bfloat162 h = __hsub2(*reinterpret_cast<const __nv_bfloat162 *>(&v), __floats2bfloat162_rn(136.f, 136.f));
-    return *reinterpret_cast<uint32_t *>(&h);
+// Pairs of weights (2i, 2i + 1) of a word as bf16, times 2^-6. A nibble in the low half of a bf16 pattern
+// is a subnormal (bit 7 is the exponent's last, and the least normal numbers go on in the subnormals'
+// steps): q 2^-133 in bits 0-3, q 2^-129 in bits 4-7. One multiply-add makes (q - 8) 2^-6 of either,
+// exactly; the sums take the 2^6.
+__device__ __forceinline__ uint32_t to_weight(uint32_t v, uint32_t mul) {
+    const uint32_t minus = 0xbe00be00u;  // -8 2^-6
+    uint32_t r;
+    asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(v), "r"(mul), "r"(minus));
+    return r;
+}
+__device__ __forceinline__ void weights_of(uint32_t word, uint32_t (&v)[4]) {
+    constexpr uint32_t lo = 0x7f007f00u, hi = 0x7d007d00u;  // 2^127, 2^123
+    const uint32_t up = word >> 8;
+    v[0] = to_weight(word & 0x000f000fu, lo);
+    v[1] = to_weight(word & 0x00f000f0u, hi);
+    v[2] = to_weight(up & 0x000f000fu, lo);
+    v[3] = to_weight(up & 0x00f000f0u, hi);
 }
 __device__ __forceinline__ void cluster_sync() {
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
@@ -171,13 +181,15 @@ __global__ void __launch_bounds__(kThreads, 2) w4_matvec_kernel(const W4Args a, 
             uint32_t A[2][2][4];  // [16 outputs][8 of 32 inputs' pairs]
 #pragma unroll
             for (int r = 0; r < 2; ++r) {
-                const uint32_t u0 = w[(r * 16) * (kRowBytes / 4) + j * 4], u1 = w[(r * 16 + 8) * (kRowBytes / 4) + j * 4];
+                uint32_t u[4], v[4];
+                weights_of(w[r * 16 * (kRowBytes / 4) + j * 4], u);
+                weights_of(w[(r * 16 + 8) * (kRowBytes / 4) + j * 4], v);
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    A[r][h][0] = weight_pair(u0, 2 * h);
-                    A[r][h][1] = weight_pair(u1, 2 * h);
-                    A[r][h][2] = weight_pair(u0, 2 * h + 1);
-                    A[r][h][3] = weight_pair(u1, 2 * h + 1);
+                    A[r][h][0] = u[2 * h];
+                    A[r][h][1] = v[2 * h];
+                    A[r][h][2] = u[2 * h + 1];
+                    A[r][h][3] = v[2 * h + 1];
                 }
             }
 #pragma unroll
@@ -221,7 +233,7 @@ __global__ void __launch_bounds__(kThreads, 2) w4_matvec_kernel(const W4Args a, 
                 const int m = n * 8 + 2 * c + e % 2;
                 if (m < a.M)
                     asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(to + ((part_at + m) * share + out % share) * 4),
-                                 "f"(acc[r][n][e]) : "memory");
+                                 "f"(acc[r][n][e] * 64.f) : "memory");
             }
         }
     cluster_sync();
