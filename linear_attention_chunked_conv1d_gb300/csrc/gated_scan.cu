@@ -77,7 +77,8 @@ constexpr int kMaxSections = 8;
 
 // Sections of a call: chains enough for the blocks of 152 SMs, and not more than streams. By sizes
 // alone, as the saved states follow them.
-inline int sections_of(int B, int channels) {
+template <typename T> int sections_of(int B, int total, int channels) {
+    if (total <= Shape<T, false>::L) return 1;
     const int groups = (channels + kWidth - 1) / kWidth, wanted = (2 * 152 + groups - 1) / groups;
     const int n = wanted < kMaxSections ? wanted : kMaxSections;
     return n < B ? n : B;
@@ -110,13 +111,17 @@ struct Chain {
     Tile *tile;          // [tiles]
     float *N, *H, *out;  // [tiles][groups][32]: the tile's map, the state that leaves it
     int tiles, groups, sections;  // tiles: the most there can be
+    // All tokens fit in one tile: nothing is chained, and a block for each group does without the
+    // kernel that lays the chains out (100 tokens x 768 fp32: 9.7 us on the device with it, 4.8 without).
+    bool single;
 };
 
 template <typename T, bool BWD> Chain make_chain(void *workspace, int B, int total, int channels) {
     Chain c;
-    c.sections = sections_of(B, channels);
+    c.sections = sections_of<T>(B, total, channels);
     c.tiles = (int)tiles_of(total, c.sections, Shape<T, BWD>::L);
     c.groups = (channels + kWidth - 1) / kWidth;
+    c.single = total <= Shape<T, BWD>::L;
     const int64_t words = (int64_t)c.tiles * c.groups * kWidth;
     c.ctl = static_cast<Ctl *>(workspace);
     c.tile = reinterpret_cast<Tile *>(c.ctl + 1);
@@ -136,6 +141,15 @@ struct Streams {
     const int32_t *cu;  // or nullptr: B streams of T_each tokens
     int B, T_each, total;
     __device__ __forceinline__ int start(int s) const { return cu ? cu[s] : s * T_each; }
+    // Whether an offset is out of order; every thread of the block looks at its share.
+    __device__ __forceinline__ bool bad() const {
+        int b = 0;
+        if (cu) {
+            if (threadIdx.x == 0) b = cu[0] != 0 || cu[B] != total;
+            for (int s = threadIdx.x; s < B; s += blockDim.x) b |= cu[s + 1] < cu[s];
+        }
+        return __syncthreads_or(b);
+    }
 };
 
 // Clears the chains and lays out the tiles in the order of work: the first of each section's chains
@@ -205,12 +219,7 @@ __global__ void chain_init_kernel(Streams st, int L, int save, Chain c, int *sta
     uint4 *p = reinterpret_cast<uint4 *>(c.N);
     for (int64_t i = t; i < quads; i += step) p[i] = make_uint4(kUnwritten, kUnwritten, kUnwritten, kUnwritten);
     if (blockIdx.x) return;
-    int bad = 0;
-    if (st.cu) {
-        if (tid == 0) bad = st.cu[0] != 0 || st.cu[st.B] != st.total;
-        for (int s = tid; s < st.B; s += blockDim.x) bad |= st.cu[s + 1] < st.cu[s];
-    }
-    bad = __syncthreads_or(bad);
+    const bool bad = st.bad();
     if (tid == 0) {
         *c.ctl = Ctl{bad, 0, 0u, (unsigned)tasks * (unsigned)c.groups};
         if (bad) raise_status(status, LA_DEV_BAD_SEQLENS);
@@ -469,7 +478,7 @@ template <class Sh> __device__ void init_shared(Sh *sh, int stages) {
 }
 
 // What the loading warp does, all its lanes together.
-template <typename T, bool BWD, class Sh> struct Loader {
+template <typename T, bool BWD, bool kSingle, class Sh> struct Loader {
     using G = Shape<T, BWD>;
     Sh *sh;
     unsigned char *ring;
@@ -483,24 +492,30 @@ template <typename T, bool BWD, class Sh> struct Loader {
 
     // Takes the next tile of the chains, in their order: late, for a tile taken early is one that its
     // successors wait for (taken one tile sooner, the 262,144 x 2048 scan took 1.00 ms instead of 0.96).
-    __device__ __forceinline__ unsigned take(int lane) const { return lane == 0 ? atomicAdd(&c.ctl->ticket, 1u) : 0u; }
-    // Starts the copies of the tile last taken into the ring's next place and fills in the slot.
+    __device__ __forceinline__ void take(int lane) {
+        if (lane == 0 && !kSingle) ticket = atomicAdd(&c.ctl->ticket, 1u);
+    }
+    // The tile last taken into the ring's next place, or the end.
     __device__ void put(int lane) {
+        const unsigned t = __shfl_sync(0xffffffffu, ticket, 0);
+        if (t < tasks) {
+            const int4 *tile = reinterpret_cast<const int4 *>(c.tile + t / c.groups);
+            put_tile(tile[0], tile[1], (int)(t % c.groups), lane);
+            return;
+        }
+        if (lane == 0) {
+            sh->slot[issued % G::kSlots].group = -1;
+            mbar_arrive(&sh->full[issued % G::kStages]);
+            mbar_arrive(&sh->full[issued % G::kStages]);
+        }
+        ++issued;
+    }
+    // Starts a tile's copies into the ring's next place and fills in its slot. u: t0, count, id, place;
+    // v: first, saved.
+    __device__ void put_tile(const int4 &u, const int4 &v, int group, int lane) {
         const uint32_t s = issued % G::kStages;
         auto &slot = sh->slot[issued % G::kSlots];
         ++issued;
-        const unsigned t = __shfl_sync(0xffffffffu, ticket, 0);
-        if (t >= tasks) {
-            if (lane == 0) {
-                slot.group = -1;
-                mbar_arrive(&sh->full[s]);
-                mbar_arrive(&sh->full[s]);
-            }
-            return;
-        }
-        const int group = (int)(t % c.groups);
-        const int4 *tile = reinterpret_cast<const int4 *>(c.tile + t / c.groups);
-        const int4 u = tile[0], v = tile[1];  // t0, count, id, place; first, saved
         if (lane == 0) {
             tc::mbar_expect_tx(&sh->full[s], G::kStage);
             const uint32_t to = tc::smem_u32(ring + s * G::kStage);
@@ -523,10 +538,16 @@ template <typename T, bool BWD, class Sh> struct Loader {
     }
     // Fills the ring.
     __device__ void begin(int lane) {
-        for (int i = 0; i < G::kStages; ++i) {
-            ticket = take(lane);
+        int n = 0;
+        if (kSingle) {  // the first stream that has tokens starts at the first one
+            int first = 0;
+            while (streams.start(first + 1) == 0) ++first;
+            put_tile(make_int4(0, streams.total, 0, 0), make_int4(~first, 0, 0, 0), blockIdx.x, lane);
+            n = 1;
+        }
+        for (; n < G::kStages; ++n) {  // one at a time: a second tile taken with the first is late for its chain
+            take(lane);
             put(lane);
-
         }
     }
     // A block that leaves early waits for the copies it has started; those up to number `it` have
@@ -545,7 +566,7 @@ template <class Sh> __device__ __forceinline__ void give_up(Sh *sh, const Chain 
     *(volatile int *)&sh->failed = 1;
 }
 
-template <typename T>
+template <typename T, bool kSingle>
 __global__ void __launch_bounds__(kThreads, Shape<T, false>::kBlocks)
 scan_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_a,
             const __grid_constant__ CUtensorMap map_b, const GatedScanArgs a, const Chain c) {
@@ -559,8 +580,12 @@ scan_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ C
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, quad = lane % 8, rank = lane / 8, run = warp * 4 + rank;
     if (threadIdx.x == 0) init_shared(sh, G::kStages);
     __syncthreads();
-    if (c.ctl->bad) return;
-    Loader<T, false, Sh> loader{sh, ring, &map_x, &map_a, &map_b, nullptr, Streams{a.cu, a.B, a.T_each, a.total}, c, 0, c.ctl->tasks, 0};
+    const Streams streams{a.cu, a.B, a.T_each, a.total};
+    if (kSingle ? streams.bad() : c.ctl->bad != 0) {
+        if (kSingle && threadIdx.x == 0) raise_status(a.status, LA_DEV_BAD_SEQLENS);
+        return;
+    }
+    Loader<T, false, kSingle, Sh> loader{sh, ring, &map_x, &map_a, &map_b, nullptr, streams, c, 0, kSingle ? 0u : c.ctl->tasks, 0};
     if (warp == kLoader) loader.begin(lane);
     volatile int *failed = &sh->failed;
     float *saved_initial = a.saved ? a.saved + a.saved_rows * a.channels : nullptr;
@@ -660,7 +685,7 @@ scan_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ C
     };
 
     for (uint32_t it = 0;; ++it) {
-        if (warp == kLoader) loader.ticket = loader.take(lane);  // for the place that this tile leaves
+        if (warp == kLoader) loader.take(lane);  // for the place that this tile leaves
         const bool arrived = tc::mbar_wait(&sh->full[it % G::kStages], (it / G::kStages) & 1u, a.wait_ns + kWaitNs);
         const Slot<L> &slot = sh->slot[it % G::kSlots];
         if (arrived && slot.group < 0) break;
@@ -678,7 +703,7 @@ scan_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ C
     }
 }
 
-template <typename T>
+template <typename T, bool kSingle>
 __global__ void __launch_bounds__(kThreads, Shape<T, true>::kBlocks)
 scan_backward_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_a,
                      const __grid_constant__ CUtensorMap map_b, const __grid_constant__ CUtensorMap map_dy,
@@ -693,8 +718,12 @@ scan_backward_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_con
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, quad = lane % 8, rank = lane / 8, run = warp * 4 + rank;
     if (threadIdx.x == 0) init_shared(sh, G::kStages);
     __syncthreads();
-    if (c.ctl->bad) return;
-    Loader<T, true, Sh> loader{sh, ring, &map_x, &map_a, &map_b, &map_dy, Streams{a.cu, a.B, a.T_each, a.total}, c, 0, c.ctl->tasks, 0};
+    const Streams streams{a.cu, a.B, a.T_each, a.total};
+    if (kSingle ? streams.bad() : c.ctl->bad != 0) {
+        if (kSingle && threadIdx.x == 0) raise_status(a.status, LA_DEV_BAD_SEQLENS);
+        return;
+    }
+    Loader<T, true, kSingle, Sh> loader{sh, ring, &map_x, &map_a, &map_b, &map_dy, streams, c, 0, kSingle ? 0u : c.ctl->tasks, 0};
     if (warp == kLoader) loader.begin(lane);
     volatile int *failed = &sh->failed;
     const float *saved_initial = a.saved + (int64_t)c.tiles * a.channels;  // a tile for each saved row
@@ -826,7 +855,7 @@ scan_backward_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_con
     };
 
     for (uint32_t it = 0;; ++it) {
-        if (warp == kLoader) loader.ticket = loader.take(lane);  // for the place that this tile leaves
+        if (warp == kLoader) loader.take(lane);  // for the place that this tile leaves
         const bool arrived = tc::mbar_wait(&sh->full[it % G::kStages], (it / G::kStages) & 1u, a.wait_ns + kWaitNs);
         const Slot<L> &slot = sh->slot[it % G::kSlots];
         if (arrived && slot.group < 0) break;
@@ -866,6 +895,10 @@ cudaError_t start(Kernel kernel, const Streams &streams, const Chain &c, int *st
     static_assert(G::kBlocks * (smem + 1024) <= 228 * 1024, "the blocks of an SM share its 228 KB, 1 KB of it each their own");
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
+    if (c.single) {
+        launch(c.groups, smem);
+        return cudaGetLastError();
+    }
     const int64_t cells = (int64_t)c.tiles * c.groups, clear = (cells * kWidth * 3 / 4 + 1023) / 1024;
     const int sms = device_sms();
     chain_init_kernel<BWD><<<(int)(clear < sms ? clear : sms), 1024, 0, st>>>(streams, G::L, kSave<T>, c, status);
@@ -881,10 +914,11 @@ template <typename T> cudaError_t scan(GatedScanArgs a, cudaStream_t st) {
         !tile_map<T, false>(&ga, ab, a.total, a.channels, a.ab_stride) ||
         !tile_map<T, false>(&gb, ab + a.channels, a.total, a.channels, a.ab_stride))
         return cudaErrorInvalidValue;
-    a.saved_rows = tiles_of(a.total, sections_of(a.B, a.channels), kSave<T>);
+    a.saved_rows = tiles_of(a.total, sections_of<T>(a.B, a.total, a.channels), kSave<T>);
     const Chain c = make_chain<T, false>(a.workspace, a.B, a.total, a.channels);
-    return start<T, false>(scan_kernel<T>, Streams{a.cu, a.B, a.T_each, a.total}, c, a.status, st, [&](int grid, size_t smem) {
-        scan_kernel<T><<<grid, kThreads, smem, st>>>(x, ga, gb, a, c);
+    const auto kernel = c.single ? scan_kernel<T, true> : scan_kernel<T, false>;
+    return start<T, false>(kernel, Streams{a.cu, a.B, a.T_each, a.total}, c, a.status, st, [&](int grid, size_t smem) {
+        kernel<<<grid, kThreads, smem, st>>>(x, ga, gb, a, c);
     });
 }
 
@@ -897,8 +931,9 @@ template <typename T> cudaError_t backward(const GatedScanBwdArgs &a, cudaStream
         !tile_map<T, true>(&dy, a.dy, a.total, a.channels, a.dy_stride))
         return cudaErrorInvalidValue;
     const Chain c = make_chain<T, true>(a.workspace, a.B, a.total, a.channels);
-    return start<T, true>(scan_backward_kernel<T>, Streams{a.cu, a.B, a.T_each, a.total}, c, a.status, st, [&](int grid, size_t smem) {
-        scan_backward_kernel<T><<<grid, kThreads, smem, st>>>(x, ga, gb, dy, a, c);
+    const auto kernel = c.single ? scan_backward_kernel<T, true> : scan_backward_kernel<T, false>;
+    return start<T, true>(kernel, Streams{a.cu, a.B, a.T_each, a.total}, c, a.status, st, [&](int grid, size_t smem) {
+        kernel<<<grid, kThreads, smem, st>>>(x, ga, gb, dy, a, c);
     });
 }
 
@@ -910,8 +945,10 @@ size_t gated_scan_workspace_bytes(int B, int total, int channels, int dtype) {  
 }
 
 size_t gated_scan_saved_bytes(int B, int total, int channels, int dtype) {
-    const int every = dtype == LA_BF16 ? kSave<__nv_bfloat16> : kSave<float>;
-    return ((size_t)tiles_of(total, sections_of(B, channels), every) + B) * channels * sizeof(float);
+    const int64_t rows = dtype == LA_BF16
+                             ? tiles_of(total, sections_of<__nv_bfloat16>(B, total, channels), kSave<__nv_bfloat16>)
+                             : tiles_of(total, sections_of<float>(B, total, channels), kSave<float>);
+    return ((size_t)rows + B) * channels * sizeof(float);
 }
 
 cudaError_t launch_gated_scan(const GatedScanArgs &a, cudaStream_t st) {

@@ -117,6 +117,7 @@ def gpu_pass(cuda, inp, lengths, *, packed=True, states=True, grads=True):
 
 
 LENGTHS = {
+    "empty first": [0, 0, 5], "between the tiles": [0, 150, 0, 1, 100], "a tile": [100, 156], "over a tile": [100, 157],
     "one": [1], "two": [2], "short": [37], "tile": [64], "tile+1": [65], "batch": [100, 100, 100],
     "ones": [1] * 70, "ragged": [0, 1, 63, 64, 65, 0, 0, 130, 7, 0], "long": [5000], "mixed": [3, 1900, 0, 1, 700, 64],
 }
