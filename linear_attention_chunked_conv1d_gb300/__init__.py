@@ -405,7 +405,7 @@ def _dtype_arg(dtype) -> int:
 
 # The calls below may take no longer than their launch does, so their checks are kept to what costs
 # well under a microsecond each: devices are compared by their index.
-_current_device = torch._C._cuda_getDevice if hasattr(torch._C, "_cuda_getDevice") else None
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 _current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
@@ -414,7 +414,7 @@ def _on_gpu(t) -> int:
     dev = t.get_device()
     if dev < 0:
         raise ValueError("expected CUDA tensors")
-    cur = torch.cuda.current_device() if _current_device is None else _current_device()
+    cur = _current_device()
     if dev != cur:
         raise ValueError(f"tensors on cuda:{dev}, but the current device is cuda:{cur}: use "
                          "torch.cuda.device(...)")
@@ -534,20 +534,47 @@ def gated_scan_step(h_state_ptrs, x, ab, y, *, conv_state_ptrs=None, conv_w=None
     """One token for each of B streams: conv1d + SiLU on the carried windows (with conv_w [C][K] and
     conv_state_ptrs to [K-1][C]; without conv_w, x enters as it is), then one step of gated_scan.
     x, y [B][C], ab [B][2C]; both states advance in place."""
-    dev = _on_gpu(x)
+    dt, dev = x.dtype, x.get_device()
     B, C = x.shape
-    K = 0
-    if conv_w is not None:
-        K = conv_w.shape[1]
-        _dense("conv_w", conv_w, (C, K), x.dtype, dev)
-        if conv_bias is not None:
-            _dense("conv_bias", conv_bias, (C,), x.dtype, dev)
+    K = 0 if conv_w is None else conv_w.shape[1]
+    (xs, x1), (gs, g1), (ys, y1) = x.stride(), ab.stride(), y.stride()
+    # A decode step is as long as its launch: one look at everything, and only where something is
+    # unusual the checks that say what.
+    if not (dev >= 0 and dev == _current_device() and ab.dtype is dt and y.dtype is dt
+            and ab.shape == (B, 2 * C) and y.shape == (B, C) and x1 == g1 == y1 == 1
+            and ab.get_device() == dev and y.get_device() == dev
+            and h_state_ptrs is not None and h_state_ptrs.dtype is torch.int64
+            and h_state_ptrs.numel() == B and h_state_ptrs.get_device() == dev
+            and h_state_ptrs.is_contiguous()
+            and (K == 0 or (conv_w.dtype is dt and conv_w.shape[0] == C and conv_w.is_contiguous()
+                            and conv_w.get_device() == dev
+                            and (K == 1 or (conv_state_ptrs is not None
+                                            and conv_state_ptrs.dtype is torch.int64
+                                            and conv_state_ptrs.numel() == B
+                                            and conv_state_ptrs.get_device() == dev
+                                            and conv_state_ptrs.is_contiguous()))
+                            and (conv_bias is None or (conv_bias.dtype is dt
+                                                       and conv_bias.shape == (C,)
+                                                       and conv_bias.is_contiguous()
+                                                       and conv_bias.get_device() == dev))))):
+        _on_gpu(x)
+        for name, m, cols in (("x", x, C), ("ab", ab, 2 * C), ("y", y, C)):
+            _matrix(name, m, B, cols, dt, dev)
+        _ptrs("h_state_ptrs", h_state_ptrs, B, dev)
+        _ptrs("conv_state_ptrs", conv_state_ptrs, B, dev)
+        if conv_w is not None:
+            _dense("conv_w", conv_w, (C, K), dt, dev)
+            if conv_bias is not None:
+                _dense("conv_bias", conv_bias, (C,), dt, dev)
+    if B == 1:  # a single row's stride says nothing
+        xs, gs, ys = C, 2 * C, C
     _check(_load().la_gated_scan_step(
-        _ptrs("conv_state_ptrs", conv_state_ptrs, B, dev),
-        _ptrs("h_state_ptrs", h_state_ptrs, B, dev), x.data_ptr(), ab.data_ptr(), _ptr(conv_w),
-        _ptr(conv_bias), K, y.data_ptr(), B, B if max_streams is None else max_streams, C,
-        _matrix("x", x, B, C, x.dtype, dev), _matrix("ab", ab, B, 2 * C, x.dtype, dev),
-        _matrix("y", y, B, C, x.dtype, dev), _dtype_code(x), _stream_on(stream, dev)))
+        None if conv_state_ptrs is None else conv_state_ptrs.data_ptr(),
+        None if h_state_ptrs is None else h_state_ptrs.data_ptr(), x.data_ptr(), ab.data_ptr(),
+        None if conv_w is None else conv_w.data_ptr(),
+        None if conv_bias is None else conv_bias.data_ptr(), K, y.data_ptr(), B,
+        B if max_streams is None else max_streams, C, xs, gs, ys, _dtype_code(x),
+        _stream_on(stream, dev)))
 
 
 def conv1d_silu_backward_workspace_bytes(B, total_tokens, channels, kernel, dtype) -> int:
@@ -599,16 +626,26 @@ def w4_quantize(w, q=None, scales=None, *, group=128, stream=None):
 def w4_matvec(x, q, scales, y=None, *, stream=None):
     """y = x W^T for 1..LA_W4_MAX_ROWS bf16 rows x [M][K] and a weight that w4_quantize laid out
     (q [N][K/2], scales [N][K/group]); y [M][N] bf16 (allocated when None). Returns y."""
-    dev = _on_gpu(x)
+    dev = x.get_device()
     M, K = x.shape
     N, groups = scales.shape
     if groups == 0 or K % groups:
         raise ValueError(f"{groups} scales for each {K} inputs")
     if y is None:
         y = torch.empty(M, N, dtype=torch.bfloat16, device=x.device)
-    _check(_load().la_w4_matvec(
-        x.data_ptr(), _dense("q", q, (N, K // 2), torch.uint8, dev),
-        _dense("scales", scales, (N, groups), torch.bfloat16, dev), y.data_ptr(), M, N, K,
-        K // groups, _matrix("x", x, M, K, torch.bfloat16, dev),
-        _matrix("y", y, M, N, torch.bfloat16, dev), _stream_on(stream, dev)))
+    (xs, x1), (ys, y1) = x.stride(), y.stride()
+    if not (dev >= 0 and dev == _current_device() and x.dtype is torch.bfloat16
+            and y.dtype is torch.bfloat16 and scales.dtype is torch.bfloat16
+            and q.dtype is torch.uint8 and q.shape == (N, K // 2) and y.shape == (M, N)
+            and x1 == y1 == 1 and q.get_device() == dev and scales.get_device() == dev
+            and y.get_device() == dev and q.is_contiguous() and scales.is_contiguous()):
+        _on_gpu(x)  # what is unusual, and whether it is wrong
+        _matrix("x", x, M, K, torch.bfloat16, dev)
+        _matrix("y", y, M, N, torch.bfloat16, dev)
+        _dense("q", q, (N, K // 2), torch.uint8, dev)
+        _dense("scales", scales, (N, groups), torch.bfloat16, dev)
+    if M == 1:
+        xs, ys = K, N
+    _check(_load().la_w4_matvec(x.data_ptr(), q.data_ptr(), scales.data_ptr(), y.data_ptr(), M, N, K,
+                                K // groups, xs, ys, _stream_on(stream, dev)))
     return y

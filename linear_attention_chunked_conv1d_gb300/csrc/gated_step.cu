@@ -27,23 +27,21 @@ __global__ void __launch_bounds__(kThreads) gated_step_kernel(const GatedStepArg
         V::load((const T *)a.ab + s * a.ab_stride + c, ga);
         V::load((const T *)a.ab + s * a.ab_stride + a.channels + c, gb);
         if constexpr (K > 0) {
-            float win[K][4], w[4][K], p[4] = {0.f, 0.f, 0.f, 0.f};
+            float win[K][4], w[4 * K], p[4] = {0.f, 0.f, 0.f, 0.f};  // w: four channels' taps, as they lie
             T *st = K > 1 ? reinterpret_cast<T *>(a.conv_state_ptrs[s]) + c : nullptr;
 #pragma unroll
             for (int m = 0; m < K - 1; ++m) V::load(st + (int64_t)m * a.channels, win[m]);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                win[K - 1][e] = x[e];
+            for (int j = 0; j < K; ++j) V::load((const T *)a.conv_w + (int64_t)c * K + 4 * j, w + 4 * j);
 #pragma unroll
-                for (int j = 0; j < K; ++j) w[e][j] = to_f(((const T *)a.conv_w)[(int64_t)(c + e) * K + j]);
-            }
+            for (int e = 0; e < 4; ++e) win[K - 1][e] = x[e];
             if (a.conv_bias) V::load((const T *)a.conv_bias + c, p);
 #pragma unroll
             for (int m = 0; m < K - 1; ++m) V::store(st + (int64_t)m * a.channels, win[m + 1]);
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
 #pragma unroll
-                for (int j = 0; j < K; ++j) p[e] = fmaf(w[e][j], win[j][e], p[e]);
+                for (int j = 0; j < K; ++j) p[e] = fmaf(w[e * K + j], win[j][e], p[e]);
                 x[e] = silu(p[e]);
             }
         }

@@ -205,3 +205,48 @@ def test_scan_wait_runs_out_then_next_call_is_correct(cuda, monkeypatch):
     assert call() == (0, 0)
     for u, v in zip((y, dx, dab), want):
         assert torch.equal(u, v)
+
+
+def test_binding_refuses_what_does_not_fit(cuda):
+    """Shapes, types and layouts that the calls cannot take raise before anything runs."""
+    B, C, K = 3, 16, 4
+    bf = dict(dtype=torch.bfloat16, device=cuda)
+    x, ab, y = torch.zeros(B, C, **bf), torch.zeros(B, 2 * C, **bf), torch.full((B, C), 5.0, **bf)
+    h, win = torch.zeros(B, C, device=cuda), torch.zeros(B, K - 1, C, **bf)
+    hp, wp = la.pointer_array(list(h)), la.pointer_array(list(win))
+    w, bias = torch.zeros(C, K, **bf), torch.zeros(C, **bf)
+    step = lambda *a, **kw: la.gated_scan_step(*a, **{**dict(conv_state_ptrs=wp, conv_w=w, conv_bias=bias), **kw})  # noqa: E731
+    for args, kw, kind, match in (
+            ((hp, x, ab[:, :C], y), {}, ValueError, "ab"), ((hp, x, ab.float(), y), {}, TypeError, "ab"),
+            ((hp, x, ab, y[:2]), {}, ValueError, "y"), ((hp[:2], x, ab, y), {}, ValueError, "h_state_ptrs"),
+            ((hp, x.t().contiguous().t(), ab, y), {}, ValueError, "x"), ((hp.float(), x, ab, y), {}, TypeError, "h_state"),
+            ((hp, x, ab, y), dict(conv_w=w[:8]), ValueError, "conv_w"), ((hp, x, ab, y), dict(conv_w=w.float()), TypeError, "conv_w"),
+            ((hp, x, ab, y), dict(conv_bias=bias[:8]), ValueError, "conv_bias"),
+            ((hp, x, ab, y), dict(conv_state_ptrs=wp[:1]), ValueError, "conv_state_ptrs"),
+            ((hp, x, ab, y), dict(conv_state_ptrs=None), la.LinAttnError, "conv_state_ptrs"),
+            ((None, x, ab, y), {}, la.LinAttnError, "h_state_ptrs"),
+            ((hp, x, ab, y), dict(max_streams=2), la.LinAttnError, "max_streams"),
+            ((hp.cpu(), x, ab, y), {}, ValueError, "h_state_ptrs"), ((hp, x, ab, x), {}, la.LinAttnError, "alias")):
+        with pytest.raises(kind, match=match):
+            step(*args, **kw)
+    v, q, s = torch.zeros(2, 64, **bf), torch.zeros(8, 32, dtype=torch.uint8, device=cuda), torch.zeros(8, 2, **bf)
+    for args, kind, match in (((v.float(), q, s), TypeError, "x"), ((v, q[:4], s), ValueError, "q"), ((v, q.int(), s), TypeError, "q"),
+                              ((v, q, s[:, :0]), ValueError, "scales"), ((v, q, s, torch.zeros(2, 7, **bf)), ValueError, "y"),
+                              ((v, q, s, torch.zeros(8, 2, **bf).t()), ValueError, "y"), ((v, q, s.float()), TypeError, "scales"),
+                              ((torch.zeros(33, 64, **bf), q, s), la.LinAttnError, "rows")):
+        with pytest.raises(kind, match=match):
+            la.w4_matvec(*args)
+    T = 20
+    x, ab, y = torch.zeros(T, C, **bf), torch.zeros(T, 2 * C, **bf), torch.full((T, C), 5.0, **bf)
+    cu = torch.tensor([0, 5, T], dtype=torch.int32, device=cuda)
+    ws = torch.empty(la.gated_scan_workspace_bytes(2, T, C, x.dtype), dtype=torch.uint8, device=cuda)
+    for args, kw, kind, match in (
+            ((None, x, ab, y, cu.long()), {}, TypeError, "cu_seqlens"), ((None, x, ab, y, cu), dict(B=3), ValueError, "B = 3"),
+            ((hp, x, ab, y, cu), {}, ValueError, "h_state_ptrs"), ((None, x, ab, y, cu), dict(workspace=None), la.LinAttnError, "workspace"),
+            ((None, x, ab, y, cu), dict(workspace=ws[:8]), la.LinAttnError, "workspace"),
+            ((None, x, ab, y, cu), dict(saved=ws[:8]), la.LinAttnError, "saved"), ((None, x, ab[:10], y, cu), {}, ValueError, "ab"),
+            ((None, x, ab, y, None), dict(B=3), la.LinAttnError, "multiple")):
+        with pytest.raises(kind, match=match):
+            la.gated_scan(*args, **{**dict(workspace=ws), **kw})
+    torch.cuda.synchronize()
+    assert torch.all(y == 5.0) and la.device_status() == 0
