@@ -367,9 +367,11 @@ int la_prefill_segmented(const uint64_t *h_state_ptrs, const void *q, const void
  * workspace     la_gated_scan_workspace_bytes(...) bytes (16-byte aligned), used by this call alone
  *               until its work is done. It need not be initialised. Calls (and captured graphs) that
  *               may overlap on the GPU need a workspace each; calls in stream order may share one.
- * Gates of +-infinity are exact: a = -inf keeps the state, b = -inf adds nothing of a finite x.
+ * Gates of +-infinity are exact: a = -inf keeps a finite state, a = +inf drops it, b = -inf adds
+ * nothing of a finite x. An infinite or NaN state, x or NaN gate makes its channel NaN or infinite
+ * from there to the stream's end, and no other stream or channel.
  * States and the scan are fp32; y is rounded once. LA_F32 or LA_BF16; channels and strides multiples
- * of 16 bytes. Count rule: 1 <= total_tokens <= max_tokens.
+ * of 16 bytes. Count rule: 1 <= total_tokens <= max_tokens, and at most 2^31 - 1024.
  * ------------------------------------------------------------------------------------------- */
 size_t la_gated_scan_workspace_bytes(int B, int total_tokens, int channels, int dtype);
 size_t la_gated_scan_saved_bytes(int B, int total_tokens, int channels, int dtype);
@@ -426,7 +428,8 @@ int la_gated_scan_step(const uint64_t *conv_state_ptrs, const uint64_t *h_state_
  *                   order, so the same inputs give the same bits. dbias may be NULL.
  * dstate_ptrs       DEVICE array of B pointers to [kernel-1][channels] (dtype) gradients of the
  *                   initial states (out), or NULL; no buffer of dstate_final_ptrs.
- * cu_seqlens, B     as for la_gated_scan (NULL: equal streams; a bad offset stops the whole call).
+ * cu_seqlens, B     as for la_gated_scan (NULL: equal streams; a bad offset stops the whole call), and
+ *                   counts too.
  * workspace         la_conv1d_silu_backward_workspace_bytes(...) bytes (16-byte aligned).
  * ------------------------------------------------------------------------------------------- */
 size_t la_conv1d_silu_backward_workspace_bytes(int B, int total_tokens, int channels, int kernel,
@@ -449,7 +452,7 @@ int la_conv1d_silu_backward(const uint64_t *conv_state_ptrs, const void *x, cons
  * scales  bf16 [N][K/group], contiguous, 16-byte aligned.
  * group   32, 64 or 128; K a multiple of it. Sums are fp32, y is rounded once, and the order of the
  *         sums does not depend on M: a row gives the same bits in any batch.
- * Count rule: 1 <= M <= LA_W4_MAX_ROWS; N, K >= 1. */
+ * Count rule: 1 <= M <= LA_W4_MAX_ROWS; 1 <= N, K <= 2^31 - 1024. */
 #define LA_W4_MAX_ROWS 32
 int la_w4_matvec(const void *x, const void *q, const void *scales, void *y, int M, int N, int K,
                  int group, int64_t ldx, int64_t ldy, uint64_t stream);

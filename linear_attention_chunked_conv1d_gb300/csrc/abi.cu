@@ -5,6 +5,7 @@
 // of prefill_with_pad_fill); "split_prefill.rs" returns an error from calls a layer cannot run
 // (prefill_gdn_full_batched's default) — here LA_ERR_UNSUPPORTED for dims outside the compiled
 // instances.
+#include <climits>
 #include <cstdarg>
 #include <cstdio>
 #include <cstdlib>
@@ -159,12 +160,17 @@ int check_channels(int channels, int dtype) {
     return LA_OK;
 }
 
+// The kernels of the calls below add up to a tile to a token's, output's or input's 32-bit number.
+constexpr int kMaxCount = INT_MAX - 1023;
+
 // Counts, streams and channels of the calls over packed (cu_seqlens) or equal (NULL) streams.
 int packed_common(const int32_t *cu_seqlens, int B, int total_tokens, int max_tokens, int channels,
                   int dtype, int *T_each) {
     if (total_tokens <= 0 || total_tokens > max_tokens)
         return fail(LA_ERR_COUNT, "call of %d tokens does not fit max_tokens %d", total_tokens,
                     max_tokens);
+    if (total_tokens > kMaxCount)
+        return fail(LA_ERR_COUNT, "call of %d tokens: the most are %d", total_tokens, kMaxCount);
     LA_TRY(check_dtype(dtype));
     if (B < 1) return fail(LA_ERR_ARG, "B must be >= 1 (got %d)", B);
     if (!cu_seqlens && total_tokens % B)
@@ -863,8 +869,9 @@ int la_conv1d_silu_backward(const uint64_t *conv_state_ptrs, const void *x, cons
 
 int la_w4_matvec(const void *x, const void *q, const void *scales, void *y, int M, int N, int K,
                  int group, int64_t ldx, int64_t ldy, uint64_t stream) {
-    if (M < 1 || M > LA_W4_MAX_ROWS || N < 1 || K < 1)
-        return fail(LA_ERR_COUNT, "w4 matvec of %d rows x %d x %d (1..%d rows)", M, N, K, LA_W4_MAX_ROWS);
+    if (M < 1 || M > LA_W4_MAX_ROWS || N < 1 || K < 1 || N > kMaxCount || K > kMaxCount)
+        return fail(LA_ERR_COUNT, "w4 matvec of %d rows x %d x %d (1..%d rows, N and K up to %d)", M, N, K,
+                    LA_W4_MAX_ROWS, kMaxCount);
     LA_TRY(w4_common(q, scales, K, group));
     LA_TRY(check_act_ptr(x, "x"));
     if (!y || (reinterpret_cast<uintptr_t>(y) & 1u)) return fail(LA_ERR_ARG, "y is NULL or misaligned");

@@ -66,6 +66,11 @@ def test_packed_calls(lib, call):
     assert call(lib, T=0) == COUNT and call(lib, T=-1) == COUNT
     assert call(lib, T=41) == COUNT
     assert "max_tokens" in lib.last_error()
+    most = 2 ** 31 - 1024  # the kernels add a tile's tokens to a token's number
+    assert call(lib, T=most + 1, maxt=2 ** 31 - 1, wsb=2 ** 62, sb=2 ** 62) == COUNT
+    assert str(most) in lib.last_error()
+    assert call(lib, T=2 ** 31 - 1, maxt=2 ** 31 - 1, wsb=2 ** 62, sb=2 ** 62) == COUNT
+    assert call(lib, T=most, maxt=most, C=8, xs=8, wsb=8) == ARG
     assert call(lib, dtype=2) == ARG
     assert call(lib, B=0) == ARG
     assert call(lib, cu=None, B=3) == ARG  # 40 tokens are not 3 equal streams
@@ -120,6 +125,7 @@ def test_conv_backward(lib):
 def test_w4(lib):
     assert matvec(lib, M=0) == COUNT and matvec(lib, M=33) == COUNT and matvec(lib, N=0) == COUNT
     assert lib.LA_W4_MAX_ROWS == 32
+    assert matvec(lib, N=2 ** 31 - 1023, ldy=2 ** 31) == COUNT and matvec(lib, K=2 ** 31 - 512, ldx=2 ** 31) == COUNT
     assert matvec(lib, g=48) == UNSUPPORTED and quantize(lib, g=256) == UNSUPPORTED
     assert matvec(lib, K=224, g=64) == ARG and quantize(lib, K=100, g=32) == ARG
     assert matvec(lib, x=A + 2) == ARG and matvec(lib, q=None) == ARG and matvec(lib, s=None) == ARG
