@@ -459,6 +459,11 @@ __device__ __forceinline__ bool pass_on(Window &w, const Chain &c, int place, Ce
     return true;
 }
 
+// Why a block leaves: a warp's wait for the tile ran out, told at the tile's first barrier, or the wait for
+// its state, told at the second. Two values, so that a warp that is late to look behind one barrier does
+// not take what was written after it for that barrier's answer, and leave while others wait at the next.
+enum { kNoTile = 1, kNoState = 2 };
+
 // Shared memory of a block, in front of its ring.
 template <int L, int STAGES, bool BWD> struct Shared {
     uint64_t full[STAGES];
@@ -563,7 +568,7 @@ template <class Sh> __device__ __forceinline__ void give_up(Sh *sh, const Chain 
         atomicExch(&c.ctl->abort, 1);
         raise_status(status, LA_DEV_TIMEOUT);
     }
-    *(volatile int *)&sh->failed = 1;
+    *(volatile int *)&sh->failed = kNoState;
 }
 
 template <typename T, bool kSingle>
@@ -638,10 +643,8 @@ scan_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ C
             store_f4(&sh->H[run][quad * 4], kMarked && (own_resets & 8u) ? m.H : w.H);
         }
         __syncthreads();
-        if (*failed) return false;
-        if (warp == kLoader) {
-            loader.put(lane);
-        }
+        if (*failed == kNoTile) return false;
+        if (warp == kLoader) loader.put(lane);
 
         const uint32_t warp_resets = kMarked ? by_warp(resets) : 0u;
         if (warp == kWarps - 1) {
@@ -659,7 +662,7 @@ scan_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ C
         }
         const Map before_warp = join<false, kMarked, kWarps - 1, 4>(&sh->N[3], &sh->H[3], warp_resets, warp, quad);
         __syncthreads();
-        if (*failed) return false;
+        if (*failed == kNoState) return false;
 
         // the state that reaches this run, then its tokens'
         F4 v = load_f4(&sh->in[quad * 4]);
@@ -690,7 +693,7 @@ scan_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ C
         const Slot<L> &slot = sh->slot[it % G::kSlots];
         if (arrived && slot.group < 0) break;
         if (!arrived) {  // nothing of the tile is used; the others leave at their first barrier
-            *failed = 1;
+            *failed = kNoTile;
             __syncthreads();
         }
         const bool ok = !arrived ? false
@@ -793,10 +796,8 @@ scan_backward_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_con
         }
         if (rank == 0) store_f4(&sh->M[run][quad * 4], kMarked && (own_ends & 1u) ? m : Map{h.N, m}.apply(m_run.H));
         __syncthreads();
-        if (*failed) return false;
-        if (warp == kLoader) {
-            loader.put(lane);
-        }
+        if (*failed == kNoTile) return false;
+        if (warp == kLoader) loader.put(lane);
 
         const uint32_t warp_resets = kMarked ? by_warp(resets) : 0u, warp_ends = kMarked ? by_warp(end_resets) : 0u;
         if (warp == 0) {
@@ -827,7 +828,7 @@ scan_backward_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_con
             }
         }
         __syncthreads();
-        if (*failed) return false;
+        if (*failed == kNoState) return false;
 
         F4 v = load_f4(&sh->in[quad * 4]);
         v = reset_before<true, kWarps>(warp_ends, kWarps - 1 - warp) ? m_warp.H : m_warp.apply(v);
@@ -860,7 +861,7 @@ scan_backward_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_con
         const Slot<L> &slot = sh->slot[it % G::kSlots];
         if (arrived && slot.group < 0) break;
         if (!arrived) {  // nothing of the tile is used; the others leave at their first barrier
-            *failed = 1;
+            *failed = kNoTile;
             __syncthreads();
         }
         const bool ok = !arrived ? false
