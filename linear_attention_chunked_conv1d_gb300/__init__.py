@@ -432,9 +432,16 @@ def _matrix(name, t, rows, cols, dtype, dev) -> int:
     if t.shape == (rows, cols) and t.get_device() == dev:
         s, inner = t.stride()
         if inner == 1 or cols == 1:
-            return s if rows > 1 else max(s, cols)
+            return s if rows > 1 else cols  # a single row's stride says nothing
     raise ValueError(f"{name}: {tuple(t.shape)} with strides {t.stride()} on device {t.get_device()}, "
                      f"expected {(rows, cols)} with dense rows on device {dev}")
+
+
+def _on_stream(stream):
+    """The context in which what a call allocates belongs to the stream that it runs on."""
+    if isinstance(stream, int):
+        stream = torch.cuda.ExternalStream(stream)
+    return torch.cuda.stream(stream)
 
 
 def _dense(name, t, shape, dtype, dev):
@@ -612,10 +619,13 @@ def w4_quantize(w, q=None, scales=None, *, group=128, stream=None):
     """Lays a bf16 weight w [N][K] out for w4_matvec: (q uint8 [N][K/2], scales bf16 [N][K/group])."""
     dev = _on_gpu(w)
     N, K = w.shape
-    if q is None:
-        q = torch.empty(N, K // 2, dtype=torch.uint8, device=w.device)
-    if scales is None:
-        scales = torch.empty(N, K // group, dtype=torch.bfloat16, device=w.device)
+    if group <= 0 or K % group:
+        raise ValueError(f"groups of {group} for {K} inputs")
+    with _on_stream(stream):
+        if q is None:
+            q = torch.empty(N, K // 2, dtype=torch.uint8, device=w.device)
+        if scales is None:
+            scales = torch.empty(N, K // group, dtype=torch.bfloat16, device=w.device)
     _check(_load().la_w4_quantize(
         w.data_ptr(), _dense("q", q, (N, K // 2), torch.uint8, dev),
         _dense("scales", scales, (N, K // group), torch.bfloat16, dev), N, K, group,
@@ -632,7 +642,11 @@ def w4_matvec(x, q, scales, y=None, *, stream=None):
     if groups == 0 or K % groups:
         raise ValueError(f"{groups} scales for each {K} inputs")
     if y is None:
-        y = torch.empty(M, N, dtype=torch.bfloat16, device=x.device)
+        if stream is None:
+            y = torch.empty(M, N, dtype=torch.bfloat16, device=x.device)
+        else:
+            with _on_stream(stream):
+                y = torch.empty(M, N, dtype=torch.bfloat16, device=x.device)
     (xs, x1), (ys, y1) = x.stride(), y.stride()
     if not (dev >= 0 and dev == _current_device() and x.dtype is torch.bfloat16
             and y.dtype is torch.bfloat16 and scales.dtype is torch.bfloat16

@@ -25,7 +25,7 @@ from . import (conv1d_silu_backward, conv1d_silu_backward_workspace_bytes, conv1
                gated_scan_saved_bytes, gated_scan_step, gated_scan_workspace_bytes,
                gdn_prefill_batched, gdn_prefill_varlen, gemm_bf16, kda_prefill, l2norm_heads,
                pointer_array, prefill_front, prefill_segmented, prefill_segmented_workspace_bytes,
-               prefill_workspace_bytes, rmsnorm_rows, w4_matvec)
+               prefill_workspace_bytes, rmsnorm_rows, w4_matvec, _on_stream)
 
 
 class PrefillPass:
@@ -259,9 +259,11 @@ class GatedPass:
     conv1d + SiLU over the carried windows, then the gated scan from the carried states.
 
     `inputs` holds device tensors: x [T][C] (before the conv) and ab [T][2C] (gate rows a | b),
-    conv_w [C][K], conv_bias [C] or None, conv_state [B][K-1][C], h [B][C] (fp32), cu_seqlens.
+    conv_w [C][K], conv_bias [C] or None, conv_state [B][K-1][C], h [B][C] (fp32, both contiguous),
+    cu_seqlens.
     forward() advances both states; with train=True it also keeps what backward() needs: the
-    conv states as they were, and the scan's saved states."""
+    conv states as they were, and the scan's saved states. Outputs and gradients are the pass's own
+    tensors, written again by the next call."""
 
     def __init__(self, inputs: dict, *, train: bool = False):
         self.inp, self.train = inputs, train
@@ -279,8 +281,10 @@ class GatedPass:
             self.conv_start = torch.empty_like(conv_state)
             self.conv_start_ptrs = pointer_array(list(self.conv_start)) if K > 1 else None
             self.grads = dict(x=torch.empty_like(x), ab=torch.empty_like(inputs["ab"]),
-                              conv_w=torch.empty(C, K, device=dev), conv_bias=torch.empty(C, device=dev),
+                              conv_w=torch.empty(C, K, device=dev), conv_bias=None,
                               conv_state=torch.empty_like(conv_state), h=torch.empty_like(h))
+            if inputs["conv_bias"] is not None:
+                self.grads["conv_bias"] = torch.empty(C, device=dev)
             self.du = torch.empty_like(x)
             self.dh_ptrs = pointer_array(list(self.grads["h"]))
             self.dconv_ptrs = pointer_array(list(self.grads["conv_state"])) if K > 1 else None
@@ -288,7 +292,7 @@ class GatedPass:
     def forward(self, stream=None):
         inp = self.inp
         if self.train:
-            with torch.cuda.stream(stream):
+            with _on_stream(stream):
                 self.conv_start.copy_(inp["conv_state"])
         conv1d_silu_prefill_varlen(self.conv_ptrs, inp["x"], inp["conv_w"], self.u, inp["cu_seqlens"],
                                    bias=inp["conv_bias"], stream=stream)
@@ -297,15 +301,17 @@ class GatedPass:
         return self.y
 
     def backward(self, dy, *, dh_final_ptrs=None, dconv_final_ptrs=None, stream=None):
-        """Gradients of the last forward(), by the names of `inputs`; of the states that it left,
-        where given (pointer arrays, as gated_scan_backward and conv1d_silu_backward take them)."""
+        """Gradients of the last forward(), by the names of `inputs` (conv_bias: None without one).
+        dh_final_ptrs, dconv_final_ptrs: gradients of the states that it left (pointer arrays, as
+        gated_scan_backward and conv1d_silu_backward take them)."""
+        if not self.train:
+            raise RuntimeError("backward() needs GatedPass(..., train=True)")
         inp, g = self.inp, self.grads
         gated_scan_backward(self.u, inp["ab"], self.saved, dy, self.du, g["ab"], inp["cu_seqlens"],
                             dh_final_ptrs=dh_final_ptrs, dh0_ptrs=self.dh_ptrs,
                             workspace=self.workspace, stream=stream)
-        bias = inp["conv_bias"]
         conv1d_silu_backward(self.conv_start_ptrs, inp["x"], inp["conv_w"], self.du, g["x"], g["conv_w"],
-                             inp["cu_seqlens"], bias=bias, dbias=None if bias is None else g["conv_bias"],
+                             inp["cu_seqlens"], bias=inp["conv_bias"], dbias=g["conv_bias"],
                              dstate_final_ptrs=dconv_final_ptrs, dstate_ptrs=self.dconv_ptrs,
                              workspace=self.conv_workspace, stream=stream)
         return g
@@ -323,13 +329,14 @@ class GatedDecode:
         dev, bf16 = h.device, torch.bfloat16
         self.conv_ptrs = pointer_array(list(conv_state)) if conv_w.shape[1] > 1 else None
         self.h_ptrs = pointer_array(list(h))
+        self.normed = torch.empty(self.B, norm_w.numel(), dtype=bf16, device=dev)
         self.rows = torch.empty(self.B, 3 * self.C, dtype=bf16, device=dev)
         self.y = torch.empty(self.B, self.C, dtype=bf16, device=dev)
         self.out = torch.empty(self.B, _outputs(w_out), dtype=bf16, device=dev)
 
     def run(self, hidden, stream=None):
-        n = rmsnorm_rows(hidden, self.norm_w, eps=self.eps, stream=stream)
-        project(n, self.w_in, self.rows, stream=stream)
+        rmsnorm_rows(hidden, self.norm_w, self.normed, eps=self.eps, stream=stream)
+        project(self.normed, self.w_in, self.rows, stream=stream)
         gated_scan_step(self.h_ptrs, self.rows[:, :self.C], self.rows[:, self.C:], self.y,
                         conv_state_ptrs=self.conv_ptrs, conv_w=self.conv_w, conv_bias=self.conv_bias,
                         stream=stream)

@@ -250,3 +250,93 @@ def test_binding_refuses_what_does_not_fit(cuda):
             la.gated_scan(*args, **{**dict(workspace=ws), **kw})
     torch.cuda.synchronize()
     assert torch.all(y == 5.0) and la.device_status() == 0
+
+
+@pytest.mark.parametrize("K", [1, 4])
+@pytest.mark.parametrize("raw", [False, True])
+def test_pass_on_a_stream_and_without_bias(cuda, K, raw):
+    """GatedPass on a stream of the caller's (torch's object or its raw handle), its first kernel held back
+    by work of that stream, gives what it gives on the current one; without a bias there is no gradient of it."""
+    lengths, C = [70, 0, 131], 32
+    T, B = sum(lengths), len(lengths)
+    g = torch.Generator().manual_seed(20)
+    r = lambda *s: torch.randn(*s, generator=g).to(cuda)  # noqa: E731
+    inp = dict(x=r(T, C), ab=r(T, 2 * C), conv_w=0.5 * r(C, K), conv_bias=None, conv_state=r(B, K - 1, C), h=r(B, C),
+               cu_seqlens=torch.tensor(np.concatenate([[0], np.cumsum(lengths)]), dtype=torch.int32, device=cuda))
+    start = inp["conv_state"].clone(), inp["h"].clone()
+    dy = r(T, C)
+    p = GatedPass(inp, train=True)
+    want = p.forward().clone(), {n: u if u is None else u.clone() for n, u in p.backward(dy).items()}, inp["h"].clone()
+    assert want[1]["conv_bias"] is None
+    for n, u in zip(("conv_state", "h"), start):
+        inp[n].zero_()
+    p = GatedPass(inp, train=True)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        busy = torch.randn(4096, 4096, device=cuda)
+        for _ in range(8):
+            busy = (busy @ busy).clamp(-1, 1)
+        for n, u in zip(("conv_state", "h"), start):
+            inp[n].copy_(u)
+    stream = side.cuda_stream if raw else side
+    y = p.forward(stream=stream)
+    grads = p.backward(dy, stream=stream)
+    side.synchronize()
+    assert la.device_status(side) == 0
+    assert torch.equal(y, want[0]) and torch.equal(inp["h"], want[2])
+    for n, u in grads.items():
+        assert (u is None and want[1][n] is None) or torch.equal(u, want[1][n]), n
+    with pytest.raises(RuntimeError, match="train"):
+        GatedPass(inp).backward(dy)
+
+
+@pytest.mark.parametrize("raw", [False, True])
+def test_products_allocate_on_the_stream_they_run_on(cuda, raw):
+    """A result that is allocated for a side stream does not take memory that work of the current stream
+    may still write to: the block that the current stream has just freed is not the result's."""
+    N, K = 512, 256
+    g = torch.Generator().manual_seed(21)
+    w = torch.randn(N, K, generator=g).to(torch.bfloat16).to(cuda)
+    x = torch.randn(4, K, generator=g).to(torch.bfloat16).to(cuda)
+    want_q, want_s = la.w4_quantize(w)
+    want = la.w4_matvec(x, want_q, want_s)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    stream = side.cuda_stream if raw else side
+    freed = [torch.empty(n, dtype=torch.uint8, device=cuda) for n in (N * K // 2, N * K // 128 * 2, 4 * N * 2)]
+    places = {u.data_ptr() for u in freed}
+    del freed
+    q, s = la.w4_quantize(w, stream=stream)
+    y = la.w4_matvec(x, q, s, stream=stream)
+    side.synchronize()
+    assert not places & {q.data_ptr(), s.data_ptr(), y.data_ptr()}
+    assert torch.equal(q, want_q) and torch.equal(s, want_s) and torch.equal(y, want)
+
+
+def test_a_single_row_may_come_from_a_matrix_of_any_width(cuda):
+    """One token of a wider matrix whose row stride is no multiple of 16 bytes: the stride says nothing."""
+    C, wide = 64, 259
+    g = torch.Generator().manual_seed(22)
+    r = lambda *s: torch.randn(*s, generator=g).to(torch.bfloat16).to(cuda)  # noqa: E731
+    x, ab, dy = r(3, wide)[:1, :C], r(3, wide)[:1, :2 * C], r(3, wide)[:1, :C]
+    w = r(C, 4)
+    outs = []
+    for f in (lambda v: v, lambda v: v.contiguous()):
+        y, dx, dab = torch.empty_like(x), torch.empty(1, C, device=cuda, dtype=x.dtype), torch.empty(1, 2 * C, device=cuda, dtype=x.dtype)
+        ws = torch.empty(la.gated_scan_workspace_bytes(1, 1, C, x.dtype), dtype=torch.uint8, device=cuda)
+        saved = torch.empty(la.gated_scan_saved_bytes(1, 1, C, x.dtype), dtype=torch.uint8, device=cuda)
+        la.gated_scan(None, f(x), f(ab), y, saved=saved, workspace=ws)
+        la.gated_scan_backward(f(x), f(ab), saved, f(dy), dx, dab, workspace=ws)
+        dw, dcx = torch.empty(C, 4, device=cuda), torch.empty_like(dx)
+        cws = torch.empty(la.conv1d_silu_backward_workspace_bytes(1, 1, C, 4, x.dtype), dtype=torch.uint8, device=cuda)
+        window = torch.zeros(1, 3, C, device=cuda, dtype=x.dtype)
+        la.conv1d_silu_backward(la.pointer_array(list(window)), f(x), w, f(dy), dcx, dw, workspace=cws)
+        q, s = la.w4_quantize(r(3, wide)[:1, :C] * 0 + 1, group=32)
+        outs.append((y, dx, dab, dcx, dw, la.w4_matvec(f(x), q, s)))
+    torch.cuda.synchronize()
+    assert la.device_status() == 0
+    for u, v in zip(*outs):
+        assert torch.equal(u, v)
+    with pytest.raises(ValueError, match="groups of 0"):
+        la.w4_quantize(w, group=0)
