@@ -4,7 +4,9 @@
 // a prefill leaves. The conv output stays in 32 bits on its way to the recurrence (it is not stored).
 //
 // HBM-bound: every state element is read and written once. One thread has 4 channels of one stream;
-// all its loads are issued before the first is used.
+// all its loads are issued before the first is used. On the device, bf16 with K = 4: one stream of 2048
+// channels 1.4 us (a launch and one trip to memory), 256 x 4096 4.3 us (30 MB, partly in L2). A thread's taps
+// lie next to each other and come in K loads of 8 bytes: with one load a tap it was 6.8 us.
 #include "gated.cuh"
 #include "launch.h"
 

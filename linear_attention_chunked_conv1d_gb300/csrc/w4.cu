@@ -247,8 +247,8 @@ __global__ void __launch_bounds__(kThreads, 2) w4_matvec_kernel(const W4Args a, 
 }
 
 // Blocks that share a tile's inputs: as many (1, 2, 4 or 8) as still fit on 152 SMs, two on each less a
-// tenth for clusters that do not fill a group of SMs, while each still has two stages. By N and K alone, and a fixed number of SMs: a row's
-// sums do not depend on the batch or the device.
+// tenth for clusters that do not fill a group of SMs, while each still has two stages. By N and K alone,
+// and a fixed number of SMs: a row's sums do not depend on the batch or the device.
 int cluster_of(int N, int K) {
     const int tiles = (N + kTile - 1) / kTile, segs = (K + kSeg - 1) / kSeg;
     int blocks = 1;
