@@ -73,6 +73,12 @@ __device__ __forceinline__ void mma_bf16(float (&d)[4], const uint32_t (&a)[4], 
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
+// The same, onto zeros.
+__device__ __forceinline__ void mma_bf16_0(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %10, %10, %10};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
+}
 // Pairs of weights (2i, 2i + 1) of a word as bf16, times 2^-6. A nibble in the low half of a bf16 pattern
 // is a subnormal (bit 7 is the exponent's last, and the least normal numbers go on in the subnormals'
 // steps): q 2^-133 in bits 0-3, q 2^-129 in bits 4-7. One multiply-add makes (q - 8) 2^-6 of either,
@@ -108,41 +114,54 @@ __global__ void __launch_bounds__(kThreads, 2) w4_matvec_kernel(const W4Args a, 
     const int all = (a.K + kSeg - 1) / kSeg;
     const int first = (int)rank * segs_each, last = min(first + segs_each, all);
 
-    // this thread's copies of a stage: 16 bytes of weights of rows t / 8, + 32, + 64, + 96 ..
-    const int kq = first * kSeg + t % 8 * 32;
-    const unsigned char *qp = static_cast<const unsigned char *>(a.q) + (int64_t)(n0 + t / 8) * (a.K / 2) + kq / 2;
+    // this thread's copies of a stage: 16 bytes of weights of rows t / 8, + 32, + 64, + 96 (past the last
+    // output the last one's: nobody looks at what becomes of them) ..
+    int left = a.K - first * kSeg;  // inputs from the stage's first one on
+    const unsigned char *qp[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        qp[i] = static_cast<const unsigned char *>(a.q) + (int64_t)min(n0 + t / 8 + i * 32, a.N - 1) * (a.K / 2) +
+                (first * kSeg + t % 8 * 32) / 2;
     const uint32_t q_to = t / 8 * kRowBytes + t % 8 * 16;
-    // .. and of inputs: 8 of them of row t / 32, + 8, ..
-    const int kx = first * kSeg + lane * 8;
-    const __nv_bfloat16 *xp = static_cast<const __nv_bfloat16 *>(a.x) + (int64_t)warp * a.ldx + kx;
+    // .. and of inputs: 8 of them of row t / 32, + 8, .. (rows past the last one stay what they are) ..
+    const __nv_bfloat16 *xp = static_cast<const __nv_bfloat16 *>(a.x) + (int64_t)warp * a.ldx + first * kSeg + lane * 8;
     const uint32_t x_to = kInputsAt<NT> + (lane / 4 * 32 + warp * 4 + lane % 4) * 16;
     // .. and of scales, a word at a time
     constexpr int kWords = kScaleWords<G>;
+    constexpr int kScaleCopies = (kTile * kWords + kThreads - 1) / kThreads;
     const int per_row = a.K / G;
-    const int64_t scales = (int64_t)a.N * per_row;
+    const __nv_bfloat16 *sp[kScaleCopies];
+    const __nv_bfloat16 *const sp_end = static_cast<const __nv_bfloat16 *>(a.scales) + (int64_t)a.N * per_row;
+#pragma unroll
+    for (int i = 0; i < kScaleCopies; ++i) {
+        const int w = t + i * kThreads;
+        sp[i] = static_cast<const __nv_bfloat16 *>(a.scales) +
+                (((int64_t)(n0 + w / kWords) * per_row + first * (kSeg / G)) & ~int64_t(1)) + w % kWords * 2;
+    }
     uint32_t at = sbase;
     const auto fetch = [&](int seg) {
         if (seg < last) {
-            const int off = (seg - first) * kSeg;
+            // Only a row's last stage may end inside: what lies past K is zeros. (Of the inputs: a weight is
+            // finite whatever its bits are.)
+            const bool q_there = t % 8 * 32 < left, x_there = lane * 8 < left;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const bool there = n0 + t / 8 + i * 32 < a.N && kq + off < a.K;
-                copy16(at + q_to + i * 32 * kRowBytes, there ? qp + (int64_t)i * 32 * (a.K / 2) + off / 2 : a.q, there);
+                copy16(at + q_to + i * 32 * kRowBytes, q_there ? qp[i] : a.q, q_there);
+                qp[i] += kSeg / 2;
             }
 #pragma unroll
-            for (int n = 0; n < NT; ++n) {
-                const bool there = warp + n * 8 < a.M && kx + off < a.K;
-                copy16(at + x_to + n * 8 * kSeg * 2, there ? xp + n * 8 * a.ldx + off : a.x, there);
-            }
+            for (int n = 0; n < NT; ++n)
+                if (warp + n * 8 < a.M) copy16(at + x_to + n * 8 * kSeg * 2, x_there ? xp + n * 8 * a.ldx : a.x, x_there);
+            xp += kSeg;
 #pragma unroll
-            for (int i = 0; i < (kTile * kWords + kThreads - 1) / kThreads; ++i) {
-                const int w = t + i * kThreads, row = w / kWords;
-                if (kTile * kWords % kThreads && w >= kTile * kWords) break;
-                const int64_t from = (((int64_t)(n0 + row) * per_row + seg * (kSeg / G)) & ~int64_t(1)) + w % kWords * 2;
-                const int64_t left = scales - from;  // an odd last one is half a word
-                copy4(at + kScalesAt<NT> + w * 4, static_cast<const __nv_bfloat16 *>(a.scales) + (left > 0 ? from : 0),
-                      left > 1 ? 4 : left > 0 ? 2 : 0);
+            for (int i = 0; i < kScaleCopies; ++i) {
+                if (kTile * kWords % kThreads && t + i * kThreads >= kTile * kWords) break;
+                // an odd last one is half a word
+                copy4(at + kScalesAt<NT> + (t + i * kThreads) * 4, sp[i] < sp_end ? sp[i] : a.scales,
+                      sp[i] + 1 < sp_end ? 4 : sp[i] < sp_end ? 2 : 0);
+                sp[i] += kSeg / G;
             }
+            left -= kSeg;
             at = at == sbase + (kStages<NT> - 1) * kStageBytes<NT, G> ? sbase : at + kStageBytes<NT, G>;
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
@@ -172,12 +191,6 @@ __global__ void __launch_bounds__(kThreads, 2) w4_matvec_kernel(const W4Args a, 
         float part[2][NT][4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            if (j * 32 % G == 0) {
-#pragma unroll
-                for (int n = 0; n < NT; ++n)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) part[0][n][e] = part[1][n][e] = 0.f;
-            }
             uint32_t A[2][2][4];  // [16 outputs][8 of 32 inputs' pairs]
 #pragma unroll
             for (int r = 0; r < 2; ++r) {
@@ -197,7 +210,8 @@ __global__ void __launch_bounds__(kThreads, 2) w4_matvec_kernel(const W4Args a, 
                 const uint4 b = xs[n * (kSeg / 32 * 32) + j * 32];
 #pragma unroll
                 for (int r = 0; r < 2; ++r) {
-                    mma_bf16(part[r][n], A[r][0], b.x, b.y);
+                    if (j * 32 % G == 0) mma_bf16_0(part[r][n], A[r][0], b.x, b.y);
+                    else mma_bf16(part[r][n], A[r][0], b.x, b.y);
                     mma_bf16(part[r][n], A[r][1], b.z, b.w);
                 }
             }
