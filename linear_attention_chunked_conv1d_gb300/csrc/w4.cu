@@ -47,8 +47,12 @@ __global__ void w4_quantize_kernel(const W4QuantArgs a, int64_t words) {
 // inputs, as exact bf16 numbers; the rows are B. A lane's word of eight weights serves two mma: which
 // inputs meet in one mma is free as long as A and B agree, so word c of 32 inputs goes to the lanes
 // with c = lane % 4 as it lies in memory. Products are exact in fp32; a group's sum is scaled by its
-// output's scale and added to the others in fp32. In the end every block of the cluster gets all parts
-// of its share of the outputs and adds them in a fixed order.
+// output's scale and added to the others in fp32. In the end every block of the cluster gets the parts of
+// its share of the outputs and adds them in a fixed order. (Each warp's sums by themselves, 4 bytes a store,
+// took 1.4 us longer at 32 x 16384 x 8192, 3 us at 32 x 4096 x 8192.)
+// Measured on the device: 1 x 8192 x 2048 4.6 us (of that 3.6 without the products: the launch, one trip to
+// HBM, two cluster barriers); 1 x 16384 x 8192 20.5 us, 3.4 TB/s (loads alone 14.2, products alone 14.5: with
+// 16 warps on an SM neither hides the other), 16 rows 28 us, 32 rows 38 us (22 and 32).
 constexpr int kThreads = 256;
 constexpr int kTile = 128;           // outputs of a block: four warps of 32
 constexpr int kSeg = 256;            // inputs of a stage: two warps of 128
@@ -97,9 +101,8 @@ __device__ __forceinline__ void weights_of(uint32_t word, uint32_t (&v)[4]) {
     v[2] = to_weight(up & 0x000f000fu, lo);
     v[3] = to_weight(up & 0x00f000f0u, hi);
 }
-__device__ __forceinline__ void cluster_sync() {
-    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 
 template <int NT, int G>  // 8 NT rows at most, groups of G inputs
 __global__ void __launch_bounds__(kThreads, 2) w4_matvec_kernel(const W4Args a, int segs_each) {
@@ -231,31 +234,45 @@ __global__ void __launch_bounds__(kThreads, 2) w4_matvec_kernel(const W4Args a, 
         st = st == smem + (kStages<NT> - 1) * kStageBytes<NT, G> ? smem : st + kStageBytes<NT, G>;
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
-    // Every block has done with its ring: the parts go there, to the block whose share the output is in.
-    // [2 blocks][8 NT rows][share outputs]
-    cluster_sync();
-    const int share = kTile / (int)blocks, part_at = ((int)rank * 2 + half) * NT * 8;
+    // The ring is free. The warps with the second half of a stage's inputs hand their sums to those with the
+    // first, these theirs to the block whose share the output is in, 8 bytes a store.
+    __syncthreads();
+    cluster_arrive();
+    constexpr int kPitch = NT * 8 + 2;  // of an output's rows
+    float *parts = reinterpret_cast<float *>(smem), *hand = parts + kTile * kPitch + t % 128;
+    if (half)
 #pragma unroll
-    for (int r = 0; r < 2; ++r)
+        for (int r = 0; r < 2; ++r)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const int out = rows_at + r * 16 + g + e / 2 * 8;
-            uint32_t to;
-            asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(to) : "r"(sbase), "r"(out / share));
+            for (int n = 0; n < NT; ++n)
 #pragma unroll
-            for (int n = 0; n < NT; ++n) {
-                const int m = n * 8 + 2 * c + e % 2;
-                if (m < a.M)
-                    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(to + ((part_at + m) * share + out % share) * 4),
-                                 "f"(acc[r][n][e] * 64.f) : "memory");
+                for (int e = 0; e < 4; ++e) hand[((r * NT + n) * 4 + e) * 128] = acc[r][n][e];
+    __syncthreads();
+    cluster_wait();  // every block's ring is
+    const int share = kTile / (int)blocks;
+    if (!half)
+#pragma unroll
+        for (int r = 0; r < 2; ++r)
+#pragma unroll
+            for (int e = 0; e < 4; e += 2) {
+                const int out = rows_at + r * 16 + g + e / 2 * 8;
+                uint32_t to;
+                asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(to) : "r"(sbase), "r"(out / share));
+                to += (((int)rank * share + out % share) * kPitch + 2 * c) * 4;
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                    const float *other = hand + ((r * NT + n) * 4 + e) * 128;
+                    if (n * 8 + 2 * c < a.M)
+                        asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(to + n * 32),
+                                     "f"((acc[r][n][e] + other[0]) * 64.f), "f"((acc[r][n][e + 1] + other[128]) * 64.f) : "memory");
+                }
             }
-        }
-    cluster_sync();
-    const float *sums = reinterpret_cast<const float *>(smem);
+    cluster_arrive();
+    cluster_wait();
     for (int i = t; i < a.M * share; i += kThreads) {
         const int m = i / share, out = i % share, n = n0 + (int)rank * share + out;
         float v = 0.f;
-        for (uint32_t b = 0; b < 2 * blocks; ++b) v += sums[(b * NT * 8 + m) * share + out];
+        for (uint32_t b = 0; b < blocks; ++b) v += parts[((int)b * share + out) * kPitch + m];
         if (n < a.N) static_cast<__nv_bfloat16 *>(a.y)[m * a.ldy + n] = __float2bfloat16_rn(v);
     }
 }
@@ -272,7 +289,7 @@ int cluster_of(int N, int K) {
 
 template <int NT, int G> cudaError_t launch_t(const W4Args &a, cudaStream_t st) {
     constexpr int smem = kStages<NT> * kStageBytes<NT, G>;
-    static_assert(smem >= 16 * NT * 8 * kTile / 8 * 4, "the parts take the ring's place");
+    static_assert(smem >= kTile * (NT * 8 + 2) * 4 + 128 * NT * 8 * 4, "what is handed on takes the ring's place");
     static_assert(2 * (smem + 1024) <= 228 * 1024, "two blocks on an SM");
     cudaError_t e = cudaFuncSetAttribute(w4_matvec_kernel<NT, G>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
