@@ -503,16 +503,45 @@ def gated_scan(h_state_ptrs, x, ab, y, cu_seqlens=None, *, B=None, saved=None, m
     streams (cu_seqlens, device int32 [B+1]) or, without cu_seqlens, B equal ones. h_state_ptrs:
     pointer_array of B fp32 [C] states, advanced in place, or None (from zero, not kept). saved: a
     buffer of gated_scan_saved_bytes(...) when gated_scan_backward is to follow."""
-    dev = _on_gpu(x)
+    dt, dev = x.dtype, x.get_device()
     T, C = x.shape
-    cu, B = _streams(cu_seqlens, B, dev)
-    sv, sv_bytes = _room("saved", saved, dev)
-    ws, ws_bytes = _room("workspace", workspace, dev)
+    (xs, x1), (gs, g1), (ys, y1) = x.stride(), ab.stride(), y.stride()
+    if cu_seqlens is not None:
+        n = cu_seqlens.shape[0] - 1
+    else:
+        n = 1 if B is None else B
+    # As in gated_scan_step: a scan of a few tokens is as long as its launch.
+    if not (dev >= 0 and dev == _current_device() and ab.dtype is dt and y.dtype is dt
+            and ab.shape == (T, 2 * C) and y.shape == (T, C) and x1 == g1 == y1 == 1
+            and ab.get_device() == dev and y.get_device() == dev
+            and (cu_seqlens is None or (cu_seqlens.dtype is torch.int32 and (B is None or B == n)
+                                        and cu_seqlens.dim() == 1 and cu_seqlens.is_contiguous()
+                                        and cu_seqlens.get_device() == dev))
+            and (h_state_ptrs is None or (h_state_ptrs.dtype is torch.int64
+                                          and h_state_ptrs.numel() == n
+                                          and h_state_ptrs.get_device() == dev
+                                          and h_state_ptrs.is_contiguous()))
+            and workspace is not None and workspace.is_contiguous()
+            and workspace.get_device() == dev
+            and (saved is None or (saved.is_contiguous() and saved.get_device() == dev))):
+        _on_gpu(x)
+        _streams(cu_seqlens, B, dev)
+        for name, m, cols in (("x", x, C), ("ab", ab, 2 * C), ("y", y, C)):
+            _matrix(name, m, T, cols, dt, dev)
+        _ptrs("h_state_ptrs", h_state_ptrs, n, dev)
+        _room("saved", saved, dev)
+        _room("workspace", workspace, dev)
+    if T == 1:  # a single row's stride says nothing
+        xs, gs, ys = C, 2 * C, C
     _check(_load().la_gated_scan(
-        _ptrs("h_state_ptrs", h_state_ptrs, B, dev), x.data_ptr(), ab.data_ptr(), y.data_ptr(), sv,
-        sv_bytes, cu, B, T, T if max_tokens is None else max_tokens, C,
-        _matrix("x", x, T, C, x.dtype, dev), _matrix("ab", ab, T, 2 * C, x.dtype, dev),
-        _matrix("y", y, T, C, x.dtype, dev), _dtype_code(x), ws, ws_bytes, _stream_on(stream, dev)))
+        None if h_state_ptrs is None else h_state_ptrs.data_ptr(), x.data_ptr(), ab.data_ptr(),
+        y.data_ptr(), None if saved is None else saved.data_ptr(),
+        0 if saved is None else saved.numel() * saved.element_size(),
+        None if cu_seqlens is None else cu_seqlens.data_ptr(), n, T,
+        T if max_tokens is None else max_tokens, C, xs, gs, ys, _dtype_code(x),
+        None if workspace is None else workspace.data_ptr(),
+        0 if workspace is None else workspace.numel() * workspace.element_size(),
+        _stream_on(stream, dev)))
 
 
 def gated_scan_backward(x, ab, saved, dy, dx, dab, cu_seqlens=None, *, B=None, dh_final_ptrs=None,
