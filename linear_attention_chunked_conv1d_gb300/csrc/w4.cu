@@ -55,6 +55,8 @@ __global__ void w4_quantize_kernel(const W4QuantArgs a, int64_t words) {
 // 16 warps on an SM neither hides the other), 16 rows 28 us, 32 rows 38 us (22 and 32).
 constexpr int kThreads = 256;
 constexpr int kTile = 128;           // outputs of a block: four warps of 32
+constexpr int kMaxBlocks = 8;        // of a cluster
+constexpr int kParts = kTile + kMaxBlocks;  // places for the parts: a share is rounded up
 constexpr int kSeg = 256;            // inputs of a stage: two warps of 128
 constexpr int kRowBytes = 128 + 16;  // a row's weights of a stage, padded: 8 rows x 4 lanes on 32 banks
 
@@ -239,7 +241,7 @@ __global__ void __launch_bounds__(kThreads, 2) w4_matvec_kernel(const W4Args a, 
     __syncthreads();
     cluster_arrive();
     constexpr int kPitch = NT * 8 + 2;  // of an output's rows
-    float *parts = reinterpret_cast<float *>(smem), *hand = parts + kTile * kPitch + t % 128;
+    float *parts = reinterpret_cast<float *>(smem), *hand = parts + kParts * kPitch + t % 128;
     if (half)
 #pragma unroll
         for (int r = 0; r < 2; ++r)
@@ -249,7 +251,7 @@ __global__ void __launch_bounds__(kThreads, 2) w4_matvec_kernel(const W4Args a, 
                 for (int e = 0; e < 4; ++e) hand[((r * NT + n) * 4 + e) * 128] = acc[r][n][e];
     __syncthreads();
     cluster_wait();  // every block's ring is
-    const int share = kTile / (int)blocks;
+    const int share = (kTile + (int)blocks - 1) / (int)blocks;
     if (!half)
 #pragma unroll
         for (int r = 0; r < 2; ++r)
@@ -273,23 +275,25 @@ __global__ void __launch_bounds__(kThreads, 2) w4_matvec_kernel(const W4Args a, 
         const int m = i / share, out = i % share, n = n0 + (int)rank * share + out;
         float v = 0.f;
         for (uint32_t b = 0; b < blocks; ++b) v += parts[((int)b * share + out) * kPitch + m];
-        if (n < a.N) static_cast<__nv_bfloat16 *>(a.y)[m * a.ldy + n] = __float2bfloat16_rn(v);
+        if (n < a.N && (int)rank * share + out < kTile) static_cast<__nv_bfloat16 *>(a.y)[m * a.ldy + n] = __float2bfloat16_rn(v);
     }
 }
 
-// Blocks that share a tile's inputs: as many (1, 2, 4 or 8) as still fit on 152 SMs, two on each less a
-// tenth for clusters that do not fill a group of SMs, while each still has two stages. By N and K alone,
-// and a fixed number of SMs: a row's sums do not depend on the batch or the device.
+// Blocks that share a tile's inputs: as few as make their shares as short as they can be while each still
+// has two stages and all fit on 152 SMs, two on each less a tenth for clusters that do not fill a group of
+// SMs. By N and K alone, and a fixed number of SMs: a row's sums do not depend on the batch or the device.
 int cluster_of(int N, int K) {
     const int tiles = (N + kTile - 1) / kTile, segs = (K + kSeg - 1) / kSeg;
-    int blocks = 1;
-    while (blocks < 8 && 2 * tiles * blocks <= 272 && segs >= 4 * blocks) blocks *= 2;
-    return blocks;
+    int most = 272 / tiles;
+    most = most < 1 ? 1 : most > kMaxBlocks ? kMaxBlocks : most;
+    int each = (segs + most - 1) / most;
+    each = each < 2 ? 2 : each;
+    return (segs + each - 1) / each;
 }
 
 template <int NT, int G> cudaError_t launch_t(const W4Args &a, cudaStream_t st) {
     constexpr int smem = kStages<NT> * kStageBytes<NT, G>;
-    static_assert(smem >= kTile * (NT * 8 + 2) * 4 + 128 * NT * 8 * 4, "what is handed on takes the ring's place");
+    static_assert(smem >= kParts * (NT * 8 + 2) * 4 + 128 * NT * 8 * 4, "what is handed on takes the ring's place");
     static_assert(2 * (smem + 1024) <= 228 * 1024, "two blocks on an SM");
     cudaError_t e = cudaFuncSetAttribute(w4_matvec_kernel<NT, G>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;

@@ -158,3 +158,16 @@ def test_graph_replay(cuda):
         g.replay()
         torch.cuda.synchronize()
         check(y, x, q, s)
+
+
+@pytest.mark.parametrize("N,K", [(16000, 512), (16000, 1024), (11450, 1536), (8000, 2016), (6900, 2560), (5700, 2816), (4850, 3584),
+                                 (3001, 8096)])
+def test_every_way_to_split_the_inputs(cuda, N, K):
+    """One to eight blocks share an output's inputs, some of them fewer than the others and with a share of
+    the outputs that does not divide the tile; a row's bits are the same in a batch of 32 and of 3."""
+    x, q, s = product(cuda, 32, N, K, 32, seed=N)
+    y = la.w4_matvec(x, q, s)
+    few = la.w4_matvec(x[5:8], q, s)
+    torch.cuda.synchronize()
+    check(y, x, q, s)
+    assert torch.equal(y[5:8], few)
