@@ -39,6 +39,7 @@
 
 #include "gated.cuh"
 #include "launch.h"
+#include "overlap.cuh"
 #include "tc.cuh"
 
 namespace la {
@@ -159,6 +160,7 @@ __global__ void chain_init_kernel(Streams st, int L, int save, Chain c, int *sta
     // sections, longest first: where they start and end, their first tile's id and saved row
     __shared__ int from[kMaxSections + 1], start[kMaxSections], end[kMaxSections], id[kMaxSections], row[kMaxSections];
     const int K = c.sections, tid = threadIdx.x;
+    wait_for_previous();
     if (tid <= K) {  // at the first stream that starts at or after an even share
         const int64_t share = (int64_t)st.total * tid / K;
         int lo = 0, hi = st.B;  // it is in [lo, hi]
@@ -585,6 +587,7 @@ scan_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ C
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, quad = lane % 8, rank = lane / 8, run = warp * 4 + rank;
     if (threadIdx.x == 0) init_shared(sh, G::kStages);
     __syncthreads();
+    wait_for_previous();
     const Streams streams{a.cu, a.B, a.T_each, a.total};
     if (kSingle ? streams.bad() : c.ctl->bad != 0) {
         if (kSingle && threadIdx.x == 0) raise_status(a.status, LA_DEV_BAD_SEQLENS);
@@ -721,6 +724,7 @@ scan_backward_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_con
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, quad = lane % 8, rank = lane / 8, run = warp * 4 + rank;
     if (threadIdx.x == 0) init_shared(sh, G::kStages);
     __syncthreads();
+    wait_for_previous();
     const Streams streams{a.cu, a.B, a.T_each, a.total};
     if (kSingle ? streams.bad() : c.ctl->bad != 0) {
         if (kSingle && threadIdx.x == 0) raise_status(a.status, LA_DEV_BAD_SEQLENS);
@@ -894,18 +898,16 @@ cudaError_t start(Kernel kernel, const Streams &streams, const Chain &c, int *st
     using G = Shape<T, BWD>;
     constexpr size_t smem = (sizeof(Shared<G::L, G::kStages, BWD>) + 127) / 128 * 128 + G::kStages * G::kStage;
     static_assert(G::kBlocks * (smem + 1024) <= 228 * 1024, "the blocks of an SM share its 228 KB, 1 KB of it each their own");
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
-    if (c.single) {
-        launch(c.groups, smem);
-        return cudaGetLastError();
-    }
+    if (c.single) return launch(c.groups, smem);
     const int64_t cells = (int64_t)c.tiles * c.groups, clear = (cells * kWidth * 3 / 4 + 1023) / 1024;
     const int sms = device_sms();
-    chain_init_kernel<BWD><<<(int)(clear < sms ? clear : sms), 1024, 0, st>>>(streams, G::L, kSave<T>, c, status);
+    e = launch_overlapped(chain_init_kernel<BWD>, dim3((int)(clear < sms ? clear : sms)), dim3(1024), 0, 0, st, streams, G::L, kSave<T>,
+                          c, status);
+    if (e != cudaSuccess) return e;
     const int room = G::kBlocks * sms;
-    launch((int)(cells < room ? cells : room), smem);
-    return cudaGetLastError();
+    return launch((int)(cells < room ? cells : room), smem);
 }
 
 template <typename T> cudaError_t scan(GatedScanArgs a, cudaStream_t st) {
@@ -919,7 +921,7 @@ template <typename T> cudaError_t scan(GatedScanArgs a, cudaStream_t st) {
     const Chain c = make_chain<T, false>(a.workspace, a.B, a.total, a.channels);
     const auto kernel = c.single ? scan_kernel<T, true> : scan_kernel<T, false>;
     return start<T, false>(kernel, Streams{a.cu, a.B, a.T_each, a.total}, c, a.status, st, [&](int grid, size_t smem) {
-        kernel<<<grid, kThreads, smem, st>>>(x, ga, gb, a, c);
+        return launch_overlapped(kernel, dim3(grid), dim3(kThreads), smem, 0, st, x, ga, gb, a, c);
     });
 }
 
@@ -934,7 +936,7 @@ template <typename T> cudaError_t backward(const GatedScanBwdArgs &a, cudaStream
     const Chain c = make_chain<T, true>(a.workspace, a.B, a.total, a.channels);
     const auto kernel = c.single ? scan_backward_kernel<T, true> : scan_backward_kernel<T, false>;
     return start<T, true>(kernel, Streams{a.cu, a.B, a.T_each, a.total}, c, a.status, st, [&](int grid, size_t smem) {
-        kernel<<<grid, kThreads, smem, st>>>(x, ga, gb, dy, a, c);
+        return launch_overlapped(kernel, dim3(grid), dim3(kThreads), smem, 0, st, x, ga, gb, dy, a, c);
     });
 }
 

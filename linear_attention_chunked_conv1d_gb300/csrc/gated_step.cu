@@ -9,6 +9,7 @@
 // lie next to each other and come in K loads of 8 bytes: with one load a tap it was 6.8 us.
 #include "gated.cuh"
 #include "launch.h"
+#include "overlap.cuh"
 
 namespace la {
 
@@ -20,6 +21,7 @@ template <typename T, int K>  // K = 0: no conv, x enters the recurrence as it i
 __global__ void __launch_bounds__(kThreads) gated_step_kernel(const GatedStepArgs a) {
     using V = Vec4<T>;
     const int c = (blockIdx.x * kThreads + threadIdx.x) * 4;
+    wait_for_previous();
     if (c >= a.channels) return;
     for (int s = blockIdx.y; s < a.B; s += gridDim.y) {
         float *h = reinterpret_cast<float *>(a.h_ptrs[s]) + c;
@@ -59,14 +61,13 @@ template <typename T>
 cudaError_t launch_t(const GatedStepArgs &a, cudaStream_t st) {
     const dim3 grid((a.channels / 4 + kThreads - 1) / kThreads, a.B < 65535 ? a.B : 65535);
     switch (a.conv_kernel) {
-        case 0: gated_step_kernel<T, 0><<<grid, kThreads, 0, st>>>(a); break;
-        case 1: gated_step_kernel<T, 1><<<grid, kThreads, 0, st>>>(a); break;
-        case 2: gated_step_kernel<T, 2><<<grid, kThreads, 0, st>>>(a); break;
-        case 3: gated_step_kernel<T, 3><<<grid, kThreads, 0, st>>>(a); break;
-        case 4: gated_step_kernel<T, 4><<<grid, kThreads, 0, st>>>(a); break;
-        default: return cudaErrorInvalidValue;
+        case 0: return launch_overlapped(gated_step_kernel<T, 0>, grid, dim3(kThreads), 0, 0, st, a);
+        case 1: return launch_overlapped(gated_step_kernel<T, 1>, grid, dim3(kThreads), 0, 0, st, a);
+        case 2: return launch_overlapped(gated_step_kernel<T, 2>, grid, dim3(kThreads), 0, 0, st, a);
+        case 3: return launch_overlapped(gated_step_kernel<T, 3>, grid, dim3(kThreads), 0, 0, st, a);
+        case 4: return launch_overlapped(gated_step_kernel<T, 4>, grid, dim3(kThreads), 0, 0, st, a);
     }
-    return cudaGetLastError();
+    return cudaErrorInvalidValue;
 }
 
 }  // namespace

@@ -8,6 +8,7 @@
 // pair (2i, 2i + 1) in the two halves of a word.
 #include "common.cuh"
 #include "launch.h"
+#include "overlap.cuh"
 
 namespace la {
 
@@ -181,6 +182,7 @@ __global__ void __launch_bounds__(kThreads, 2) w4_matvec_kernel(const W4Args a, 
     }
 
     float acc[2][NT][4] = {};
+    wait_for_previous();
 #pragma unroll
     for (int s = 0; s < kStages<NT> - 1; ++s) fetch(first + s);
     const unsigned char *st = smem;
@@ -298,18 +300,8 @@ template <int NT, int G> cudaError_t launch_t(const W4Args &a, cudaStream_t st) 
     cudaError_t e = cudaFuncSetAttribute(w4_matvec_kernel<NT, G>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     const int blocks = cluster_of(a.N, a.K), segs = (a.K + kSeg - 1) / kSeg;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((a.N + kTile - 1) / kTile * blocks);
-    cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = st;
-    cudaLaunchAttribute attr;
-    attr.id = cudaLaunchAttributeClusterDimension;
-    attr.val.clusterDim.x = blocks;
-    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, w4_matvec_kernel<NT, G>, a, (segs + blocks - 1) / blocks);
+    return launch_overlapped(w4_matvec_kernel<NT, G>, dim3((a.N + kTile - 1) / kTile * blocks), dim3(kThreads), smem, blocks, st, a,
+                             (segs + blocks - 1) / blocks);
 }
 template <int NT> cudaError_t launch_g(const W4Args &a, cudaStream_t st) {
     return a.group == 32 ? launch_t<NT, 32>(a, st) : a.group == 64 ? launch_t<NT, 64>(a, st) : launch_t<NT, 128>(a, st);

@@ -340,3 +340,79 @@ def test_a_single_row_may_come_from_a_matrix_of_any_width(cuda):
         assert torch.equal(u, v)
     with pytest.raises(ValueError, match="groups of 0"):
         la.w4_quantize(w, group=0)
+
+
+def test_calls_next_to_copies_fills_and_another_stream(cuda):
+    """Launches overlap the end of the kernel before them, and wait for it: whatever stands before a call in
+    its stream (a copy, a fill, another call, the event of another stream), it reads what that wrote and
+    writes only then. Eager and in a captured graph, many times over, bit for bit as with a wait of the host
+    after every call."""
+    C, K, T, lengths = 256, 4, 700, [300, 0, 400]
+    g = torch.Generator().manual_seed(23)
+    r = lambda *s: torch.randn(*s, generator=g).to(torch.bfloat16).to(cuda)  # noqa: E731
+    x0, ab0, dy0, w, rows0 = r(T, C), r(T, 2 * C), r(T, C), r(C, K), r(3, C)
+    qs = [la.w4_quantize((r(n, C) / 16).contiguous(), group=64) for n in (3 * C, C)]
+    h0, win0 = torch.randn(3, C, generator=g).to(cuda), r(3, K - 1, C)
+    cu = torch.tensor(np.concatenate([[0], np.cumsum(lengths)]), dtype=torch.int32, device=cuda)
+    x, ab, dy, rows = (torch.empty_like(v) for v in (x0, ab0, dy0, rows0))
+    h, win = torch.empty_like(h0), torch.empty_like(win0)
+    hp, wp = la.pointer_array(list(h)), la.pointer_array(list(win))
+    e = lambda *s, dtype=torch.bfloat16: torch.empty(*s, dtype=dtype, device=cuda)  # noqa: E731
+    y, dx, dab, dcx, dw = e(T, C), e(T, C), e(T, 2 * C), e(T, C), e(C, K, dtype=torch.float32)
+    step, tri, back = e(3, C), e(3, 3 * C), e(3, C)
+    ws, ws2 = e(la.gated_scan_workspace_bytes(3, T, C, x.dtype), dtype=torch.uint8), e(1 << 20, dtype=torch.uint8)
+    saved = e(la.gated_scan_saved_bytes(3, T, C, x.dtype), dtype=torch.uint8)
+    assert la.conv1d_silu_backward_workspace_bytes(3, T, C, K, x.dtype) <= ws2.numel()
+    total = torch.zeros((), device=cuda)
+    side = torch.cuda.Stream()
+
+    def work(wait):
+        main = torch.cuda.current_stream()
+        for a, b in ((x, x0), (ab, ab0), (dy, dy0), (h, h0), (win, win0)):
+            a.copy_(b)
+        wait()
+        la.gated_scan(hp, x, ab, y, cu, saved=saved, workspace=ws)
+        wait()
+        side.wait_stream(main)
+        with torch.cuda.stream(side):
+            rows.copy_(rows0)
+            la.w4_matvec(rows, *qs[0], tri)
+            wait()
+            la.gated_scan_step(hp, tri[:, :C], tri[:, C:], step, conv_state_ptrs=wp, conv_w=w)
+            wait()
+            la.w4_matvec(step, *qs[1], back)
+            wait()
+            back.mul_(2)
+        x.zero_()  # the scan has read it; the backward pass gets it back
+        x.copy_(x0)
+        la.gated_scan_backward(x, ab, saved, dy, dx, dab, cu, workspace=ws)
+        wait()
+        main.wait_stream(side)
+        la.conv1d_silu_backward(wp, x, w, dx, dcx, dw, cu, workspace=ws2)
+        wait()
+        dx.add_(back[0])
+        la.w4_matvec(dx[:3], *qs[1], step)
+        total.add_(step.float().sum() + dcx.float().sum() + dw.sum())
+
+    outs = (y, dx, dab, dcx, dw, step, tri, back, h, win)
+    work(torch.cuda.synchronize)
+    torch.cuda.synchronize()
+    want = [v.clone() for v in outs]
+    assert all(bool(torch.isfinite(v).all()) for v in want)
+    for v in outs:
+        v.zero_()
+    for _ in range(20):
+        work(lambda: None)
+    torch.cuda.synchronize()
+    for u, v in zip(outs, want):
+        assert torch.equal(u, v)
+        u.zero_()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        work(lambda: None)
+    for _ in range(20):
+        graph.replay()
+    torch.cuda.synchronize()
+    assert la.device_status() == 0
+    for u, v in zip(outs, want):
+        assert torch.equal(u, v)
