@@ -40,8 +40,8 @@ template <typename T> __device__ __forceinline__ void copy_row(void *to, const T
 // Tokens of a run: long ones read and write less for what runs share (K-1 rows at each end, the sums),
 // short ones make more blocks. The longest that still makes ten blocks for each of 152 SMs (four are
 // resident; a fixed number of SMs, so that sums do not depend on the device). 16384 x 6144 bf16 in
-// eight streams: runs of 256 140 us, of 128 136 us (taken), of 64 146 us; 100003 x 8192 in 32: 256
-// 0.87 ms (taken), 128 0.92, 64 1.04.
+// eight streams: runs of 256 135 us, of 128 131 us (taken), of 64 140 us; 100003 x 8192 in 32: 256
+// 0.87 ms (taken), 128 0.91, 64 1.03.
 __host__ __device__ inline int run_rows(int B, int total, int channels) {
     const int64_t cols = (channels / 4 + kThreads - 1) / kThreads;
     for (int rows = 256; rows > 64; rows /= 2)

@@ -51,9 +51,9 @@ __global__ void w4_quantize_kernel(const W4QuantArgs a, int64_t words) {
 // output's scale and added to the others in fp32. In the end every block of the cluster gets the parts of
 // its share of the outputs and adds them in a fixed order. (Each warp's sums by themselves, 4 bytes a store,
 // took 1.4 us longer at 32 x 16384 x 8192, 3 us at 32 x 4096 x 8192.)
-// Measured on the device: 1 x 8192 x 2048 4.6 us (of that 3.6 without the products: the launch, one trip to
-// HBM, two cluster barriers); 1 x 16384 x 8192 20.5 us, 3.4 TB/s (loads alone 14.2, products alone 14.5: with
-// 16 warps on an SM neither hides the other), 16 rows 28 us, 32 rows 38 us (22 and 32).
+// Measured on the device: 1 x 8192 x 2048 4.3 us (3.2 of it without the products: the launch, one trip to
+// HBM, two cluster barriers); 1 x 16384 x 8192 20.1 us, 3.5 TB/s (loads alone 13.7, products alone 14.0: with
+// 16 warps on an SM neither hides the other), 32 rows 38 us (21 and 30).
 constexpr int kThreads = 256;
 constexpr int kTile = 128;           // outputs of a block: four warps of 32
 constexpr int kMaxBlocks = 8;        // of a cluster
