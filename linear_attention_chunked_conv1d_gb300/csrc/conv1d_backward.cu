@@ -12,7 +12,7 @@
 // shared memory, each thread's its own (no barriers), two groups of rows ahead of the one at work: with
 // one group in registers instead, a third of the time went into waiting for it. The sums over tokens are
 // kept per run in 32 bits and joined run by run in a fixed order by a second kernel, so they come out the
-// same every time. 100003 x 8192 bf16 in 32 streams, K = 4: 0.87 ms, 5.6 TB/s of what has to move.
+// same every time. 100003 x 8192 bf16 in 32 streams, K = 4: 0.86 ms, 5.7 TB/s of what has to move.
 #include "gated.cuh"
 #include "launch.h"
 #include "overlap.cuh"
@@ -38,15 +38,18 @@ template <typename T> __device__ __forceinline__ void copy_row(void *to, const T
 }
 
 // Tokens of a run: long ones read and write less for what runs share (K-1 rows at each end, the sums),
-// short ones make more blocks. The longest that still makes ten blocks for each of 152 SMs (four are
-// resident; a fixed number of SMs, so that sums do not depend on the device). 16384 x 6144 bf16 in
-// eight streams: runs of 256 135 us, of 128 131 us (taken), of 64 140 us; 100003 x 8192 in 32: 256
-// 0.87 ms (taken), 128 0.91, 64 1.03.
+// short ones make more blocks. The longest that still makes 1000 blocks (152 SMs have 608 at a time; a
+// fixed number of SMs, so that sums do not depend on the device). bf16, K = 4, runs of 384, 256, 192, 128
+// and 64 (*: taken), us:
+//   16384 x 6144, 8 streams    134  135 *126  131  140
+//   16384 x 4096, 8 streams    104   95  102  *93  101
+//   65536 x 2048, 32 streams   188 *173  175  180  205
+//   100003 x 8192, 32 streams *860  869  887  912 1028
 __host__ __device__ inline int run_rows(int B, int total, int channels) {
     const int64_t cols = (channels / 4 + kThreads - 1) / kThreads;
-    for (int rows = 256; rows > 64; rows /= 2)
-        if ((total / rows + B) * cols >= 10 * 152) return rows;
-    return 64;
+    const auto blocks = [&](int rows) { return (total / rows + B) * cols; };
+    return blocks(384) >= 1000 ? 384 : blocks(256) >= 1000 ? 256 : blocks(192) >= 1000 ? 192 : blocks(128) >= 1000 ? 128
+           : blocks(96) >= 1000 ? 96 : 64;
 }
 
 struct Runs {

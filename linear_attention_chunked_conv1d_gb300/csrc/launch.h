@@ -168,8 +168,8 @@ struct GatedScanArgs {
     int dtype;
     void *workspace;
     int *status;
-    uint64_t wait_ns;  // limit of the kernel's bounded waits (0: the 2 s default)
-    int debug_stall;   // test knob: one wait for a tile that nobody publishes
+    uint64_t wait_ns;  // limit of the wait for a tile's state
+    int debug_stall;   // test knob: the search of a tile's chain finds nothing
 };
 struct GatedScanBwdArgs {
     const void *x, *ab;
@@ -225,7 +225,6 @@ cudaError_t launch_conv1d_silu_backward(const ConvBwdArgs &a, cudaStream_t st);
 
 // Products of a few bf16 rows with 4-bit weights (w4.cu): y [M][ldy] = x [M][ldx] W^T,
 // W[n][k] = scales[n][k / group] (q(n, k) - 8); q [N][K / 2] in the layout of la_w4_quantize.
-constexpr int kW4MaxRows = 32;
 struct W4Args {
     const void *x, *q, *scales;
     void *y;

@@ -235,3 +235,17 @@ def test_graph_replay(cuda):
         torch.cuda.synchronize()
         for u, v in zip((dx, dw, db, dwin), gpu_pass(cuda, inp, lengths)):
             assert torch.equal(u, v)
+
+
+@pytest.mark.parametrize("B", [1003, 990, 979])
+def test_long_runs_of_tokens_and_many_empty_streams(cuda, B):
+    """The runs' length follows the call's sizes: 384 tokens with 1003 streams, 192 with 990, 96 with 979.
+    Streams that end just before, at and after such a run's end, among empty ones."""
+    lengths = [0] * B
+    for at, n in ((0, 95), (3, 96), (4, 97), (200, 191), (201, 193), (500, 383), (777, 385), (B - 1, 770)):
+        lengths[at] = n
+    assert sum(lengths) == 2210
+    inp = make(lengths, 8, 4, "f32", seed=B)
+    ref = reference(*(f64(inp[n]) for n in ("window", "x", "w", "bias", "dout", "dfinal")), lengths)
+    for got, want in zip(gpu_pass(cuda, inp, lengths), ref):
+        close(got, *want)
