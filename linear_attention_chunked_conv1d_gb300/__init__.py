@@ -439,8 +439,10 @@ def _matrix(name, t, rows, cols, dtype, dev) -> int:
 
 def _on_stream(stream):
     """The context in which what a call allocates belongs to the stream that it runs on."""
-    if isinstance(stream, int):
-        stream = torch.cuda.ExternalStream(stream)
+    if stream is not None and not isinstance(stream, torch.cuda.Stream):
+        handle = _stream(stream)
+        # 0 is the default stream; torch would make a new one of it
+        stream = torch.cuda.ExternalStream(handle) if handle else torch.cuda.default_stream()
     return torch.cuda.stream(stream)
 
 

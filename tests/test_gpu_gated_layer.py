@@ -416,3 +416,33 @@ def test_calls_next_to_copies_fills_and_another_stream(cuda):
     assert la.device_status() == 0
     for u, v in zip(outs, want):
         assert torch.equal(u, v)
+
+
+def test_handle_zero_is_the_default_stream(cuda):
+    """stream=0 from within another stream: the pass's copy of the windows and its kernels come after what the
+    default stream holds, and what the products allocate is that stream's."""
+    T, C, K = 50, 32, 4
+    g = torch.Generator().manual_seed(24)
+    r = lambda *s: torch.randn(*s, generator=g).to(cuda)  # noqa: E731
+    start = r(1, K - 1, C)
+    inp = dict(x=r(T, C), ab=r(T, 2 * C), conv_w=r(C, K), conv_bias=None, conv_state=torch.zeros_like(start),
+               h=torch.zeros(1, C, device=cuda), cu_seqlens=torch.tensor([0, T], dtype=torch.int32, device=cuda))
+    p = GatedPass(inp, train=True)
+    w = la.w4_quantize(torch.randn(256, 256, generator=g).to(torch.bfloat16).to(cuda))
+    x4 = torch.randn(4, 256, generator=g).to(torch.bfloat16).to(cuda)
+    want = la.w4_matvec(x4, *w)
+    busy = r(4096, 4096)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    assert torch.cuda.current_stream() == torch.cuda.default_stream()
+    for _ in range(8):
+        busy = (busy @ busy).clamp(-1, 1)
+    inp["conv_state"].copy_(start)
+    freed = torch.empty(4 * 256 * 2, dtype=torch.uint8, device=cuda)
+    place = freed.data_ptr()
+    del freed
+    with torch.cuda.stream(side):
+        p.forward(stream=0)
+        y = la.w4_matvec(x4, *w, stream=0)
+    torch.cuda.synchronize()
+    assert torch.equal(p.conv_start, start) and y.data_ptr() == place and torch.equal(y, want)
