@@ -412,14 +412,16 @@ struct Window {
 };
 
 // What reaches the tile at place `at` > 0 of its chain. cell(place) is a place's index; `w` has been
-// told to fetch the places before `at`. False: the wait ran out (with `stall` it is made to).
+// told to fetch the places before `at`. False: the wait ran out (with `stall` it is made to). Every copy
+// into the window has been waited for when it returns: such copies have no order among themselves, so one
+// of this tile's must not be under way when the next tile's begin.
 template <class Cell>
 __device__ __forceinline__ bool look_back(Window &w, const Chain &c, int at, Cell cell, int lane, uint64_t wait_ns,
                                           bool stall, float &h) {
     int top = at - 1, n = 0;  // place top - n is the search's result
     uint64_t t0 = 0;
     for (uint32_t i = 0;; ++i) {
-        const unsigned there = stall ? 0u : w.look(lane), states = there & 255u, maps = there >> 8;
+        const unsigned seen = w.look(lane), there = stall ? 0u : seen, states = there & 255u, maps = there >> 8;
         const unsigned nearer = states ? (states & -states) - 1 : 255u;
         if ((maps & nearer) == nearer) {
             if (states) {
@@ -447,7 +449,8 @@ __device__ __forceinline__ bool look_back(Window &w, const Chain &c, int at, Cel
 }
 
 // Publishes the map (n, h) of the tile at `place` (`reset`: its h is what leaves it, whatever comes),
-// waits for what reaches it (unless `known`), publishes what leaves it. False: the wait ran out.
+// waits for what reaches it (unless `known`: then the window has not been told to fetch anything, as nobody
+// would wait for it), publishes what leaves it. False: the wait ran out.
 template <class Cell>
 __device__ __forceinline__ bool pass_on(Window &w, const Chain &c, int place, Cell cell, int lane, float n, float h,
                                         bool reset, bool known, uint64_t wait_ns, bool stall, float &in) {
@@ -637,7 +640,7 @@ scan_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ C
             hl[i] = m.H;
             A[i] = R;
         }
-        if (warp == kWarps - 1) sh->window.fetch(c, place - 1, cell, lane);  // in good time for look_back
+        if (warp == kWarps - 1 && !first) sh->window.fetch(c, place - 1, cell, lane);  // in good time for look_back
         store_f4(&sh->N[run][quad * 4], m.N);
         store_f4(&sh->H[run][quad * 4], m.H);
         __syncwarp();
@@ -755,6 +758,8 @@ scan_backward_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_con
         if (live) h_in = load_f4(a.saved + (int64_t)slot.id * a.channels + ch);
         const uint32_t starts = kMarked ? slot.starts_of(run) : 0u, ends = kMarked ? slot.ends_of(run) : 0u;
         const uint32_t resets = kMarked ? slot.run_starts : 0u, end_resets = kMarked ? slot.run_ends : 0u;
+        // behind a chain's first place there is nothing: a stream ends in it
+        const bool last = kMarked && slot.last(), known = last || place == 0;
         const auto initial = [&](int i) {  // state of the stream that starts at this run's token i
             return live ? load_f4(saved_initial + (int64_t)slot.start_id[run * S + i] * a.channels + ch) : zero4();
         };
@@ -786,7 +791,7 @@ scan_backward_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_con
             if (kMarked && (ends >> i & 1u)) m = final_gradient(i);
             m = left4(nd[i], add4(widen4<T>(dyr[i]), m));
         }
-        if (warp == 0) sh->window.fetch(c, place - 1, cell, lane);  // in good time for look_back
+        if (warp == 0 && !known) sh->window.fetch(c, place - 1, cell, lane);  // in good time for look_back
         store_f4(&sh->N[run][quad * 4], h.N);
         store_f4(&sh->H[run][quad * 4], h.H);
         store_f4(&sh->M[run][quad * 4], m);
@@ -810,12 +815,9 @@ scan_backward_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_con
             float n, h, v = 0.f;
             join_all<true, kMarked>(&sh->N[3], &sh->M[0], warp_ends, lane, n, h);
             const int lane_ch = group * kWidth + lane;
-            const bool last = kMarked && slot.last();
             if (last && a.dh_final_ptrs && lane_ch < a.channels)
                 v = reinterpret_cast<const float *>(a.dh_final_ptrs[slot.stream(kRuns - 1, S - 1)])[lane_ch];
-            // behind a chain's first place there is nothing: a stream ends in it
-            if (!pass_on(sh->window, c, place, cell, lane, n, h, end_resets != 0, last || place == 0, a.wait_ns,
-                         a.debug_stall != 0, v))
+            if (!pass_on(sh->window, c, place, cell, lane, n, h, end_resets != 0, known, a.wait_ns, a.debug_stall != 0, v))
                 give_up(sh, c, lane, a.status);
             sh->in[lane] = v;
         }

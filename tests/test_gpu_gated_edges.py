@@ -1,0 +1,79 @@
+"""The gated recurrence where streams start and end on the edges of the kernels' tiles (256 tokens forward in
+bf16, 128 in fp32 and backward), inside a chain of tiles: such a tile's incoming state is known without a
+search of its chain, and what it leaves is published without a map. There are more streams than sections of
+the rows (at most 8), so that chains go on over such an edge. Against the 64-bit form, with the running
+bounds of test_gpu_gated_scan."""
+import numpy as np
+import pytest
+import torch
+
+from tests.helpers import f64
+from tests.test_gpu_gated_scan import backward, close, forward, gpu_pass, make
+
+pytestmark = pytest.mark.gpu
+
+EDGES = {
+    "24 of 256": [256] * 24,
+    "12 of 512": [512] * 12,
+    "30 of 128": [128] * 30,
+    "one off": [256, 255, 257, 128, 127, 129, 256, 0, 1, 255, 384, 128, 512, 0, 256, 257, 255, 640, 127, 129, 256, 128, 128],
+    "one token over": [256, 257, 256, 255, 513, 511, 256, 1, 255, 256, 128, 129, 127, 256] * 2,
+}
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("name,C", [(n, c) for n in EDGES for c in (8, 72)] + [("12 of 512", 2056)])
+def test_streams_that_meet_on_tile_edges(cuda, name, C, dtype):
+    lengths = EDGES[name]
+    inp = make(lengths, C, dtype, seed=40 + C + len(lengths), slow=6.0)
+    x, ab, dy = (f64(inp[n]) for n in ("x", "ab", "dy"))
+    a, b = ab[:, :C], ab[:, C:]
+    y_r, before, fin, err, err_b, fin_err = forward(x, a, b, f64(inp["h"]), lengths)
+    dx_r, dab_r, dh0_r = backward(x, a, b, before, err_b, dy, f64(inp["dfinal"]), lengths)
+    outs = [gpu_pass(cuda, inp, lengths)]
+    if len(set(lengths)) == 1:
+        outs.append(gpu_pass(cuda, inp, lengths, packed=False))
+    for y, h, dx, dab, dh0 in outs:
+        close(y, y_r, err, dtype)
+        close(h, fin, fin_err)
+        close(dx, *dx_r, dtype)
+        close(dab, *dab_r, dtype)
+        close(dh0, *dh0_r)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_edges_repeat_bit_for_bit(cuda, dtype):
+    """8 equal streams of a training batch, eight tiles each: the same bits every time."""
+    lengths = [2048] * 8
+    inp = make(lengths, 2048, dtype, seed=41, slow=6.0)
+    first = gpu_pass(cuda, inp, lengths, packed=False)
+    for _ in range(5):
+        for u, v in zip(first, gpu_pass(cuda, inp, lengths, packed=False)):
+            assert torch.equal(u, v)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_gates_that_are_nan_stay_in_their_stream(cuda, dtype):
+    """NaN and infinite gates, on both sides of tile edges and inside tiles, reach no other stream or channel."""
+    lengths, C = [256, 30, 226, 256, 0, 64, 320, 128, 128, 5, 256, 512], 24
+    inp = make(lengths, C, dtype, seed=42)
+    clean = gpu_pass(cuda, inp, lengths)
+    ends = np.cumsum([0] + lengths)
+    bad, inf = {0, 3, 5, 8, 10}, float("inf")
+    for s in bad:
+        ab = inp["ab"][ends[s]:ends[s + 1]]
+        ab[:, :8] = ab[:, C:C + 8] = float("nan")
+        ab[::2, 8:16], ab[1::2, C + 8:C + 16] = inf, -inf
+    got = gpu_pass(cuda, inp, lengths)
+    for s in range(len(lengths)):
+        rows, chans = slice(ends[s], ends[s + 1]), slice(16, C) if s in bad else slice(0, C)
+        for i in (0, 2):
+            assert torch.equal(got[i][rows, chans], clean[i][rows, chans]), (s, i)
+        for half in (0, C):
+            part = slice(chans.start + half, chans.stop + half)
+            assert torch.equal(got[3][rows, part], clean[3][rows, part]), s
+        for i in (1, 4):
+            assert torch.equal(got[i][s, chans], clean[i][s, chans]), (s, i)
+        if s in bad:
+            assert bool(torch.isnan(got[0][rows, :8]).all())
+            assert bool(torch.isfinite(got[0][rows, 8:16]).all())
