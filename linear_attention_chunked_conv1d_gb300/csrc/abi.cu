@@ -243,6 +243,11 @@ int debug_stall() {
     const char *v = getenv("LA_DEBUG_STALL");
     return v && !strcmp(v, "1") ? 1 : 0;
 }
+// The gated scan's: 1, a tile's search of its chain finds nothing; 2, a tile counts as not arrived.
+int debug_stall_scan() {
+    const char *v = getenv("LA_DEBUG_STALL");
+    return v && !strcmp(v, "2") ? 2 : debug_stall();
+}
 
 int run_recurrence(la::RecArgs &a, cudaStream_t st) {
     LA_TRY(get_status(&a.status));
@@ -750,7 +755,7 @@ int la_gated_scan(const uint64_t *h_state_ptrs, const void *x, const void *ab, v
     a.workspace = workspace;
     LA_TRY(get_status(&a.status));
     a.wait_ns = wait_limit_ns();
-    a.debug_stall = debug_stall();
+    a.debug_stall = debug_stall_scan();
     return launch_result([&] { return la::launch_gated_scan(a, as_stream(stream)); }, "gated scan launch");
 }
 
@@ -792,7 +797,7 @@ int la_gated_scan_backward(const void *x, const void *ab, const void *saved, siz
     a.workspace = workspace;
     LA_TRY(get_status(&a.status));
     a.wait_ns = wait_limit_ns();
-    a.debug_stall = debug_stall();
+    a.debug_stall = debug_stall_scan();
     return launch_result([&] { return la::launch_gated_scan_backward(a, as_stream(stream)); },
                          "gated scan backward launch");
 }

@@ -569,13 +569,13 @@ template <typename T, bool BWD, bool kSingle, class Sh> struct Loader {
     }
 };
 
-// The wait for a tile's state ran out: every block leaves.
-template <class Sh> __device__ __forceinline__ void give_up(Sh *sh, const Chain &c, int lane, int *status) {
+// A wait ran out (why: kNoTile, kNoState): the status says so, every block leaves.
+template <class Sh> __device__ __forceinline__ void give_up(Sh *sh, const Chain &c, int why, int lane, int *status) {
     if (lane == 0) {
         atomicExch(&c.ctl->abort, 1);
         raise_status(status, LA_DEV_TIMEOUT);
     }
-    *(volatile int *)&sh->failed = kNoState;
+    *(volatile int *)&sh->failed = why;
 }
 
 template <typename T, bool kSingle>
@@ -664,8 +664,8 @@ scan_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ C
                 if (a.h_ptrs) v = reinterpret_cast<const float *>(a.h_ptrs[id])[lane_ch];
                 if (a.saved) saved_initial[(int64_t)id * a.channels + lane_ch] = v;
             }
-            if (!pass_on(sh->window, c, place, cell, lane, n, h, resets != 0, first, a.wait_ns, a.debug_stall != 0, v))
-                give_up(sh, c, lane, a.status);
+            if (!pass_on(sh->window, c, place, cell, lane, n, h, resets != 0, first, a.wait_ns, a.debug_stall == 1, v))
+                give_up(sh, c, kNoState, lane, a.status);
             sh->in[lane] = v;
         }
         const Map before_warp = join<false, kMarked, kWarps - 1, 4>(&sh->N[3], &sh->H[3], warp_resets, warp, quad);
@@ -697,11 +697,13 @@ scan_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ C
 
     for (uint32_t it = 0;; ++it) {
         if (warp == kLoader) loader.take(lane);  // for the place that this tile leaves
-        const bool arrived = tc::mbar_wait(&sh->full[it % G::kStages], (it / G::kStages) & 1u, a.wait_ns + kWaitNs);
+        // one answer for the warp, whose lanes work together from here on
+        const bool arrived = __all_sync(0xffffffffu, tc::mbar_wait(&sh->full[it % G::kStages], (it / G::kStages) & 1u,
+                                                                   a.wait_ns + kWaitNs) && a.debug_stall != 2);
         const Slot<L> &slot = sh->slot[it % G::kSlots];
         if (arrived && slot.group < 0) break;
         if (!arrived) {  // nothing of the tile is used; the others leave at their first barrier
-            *failed = kNoTile;
+            give_up(sh, c, kNoTile, lane, a.status);
             __syncthreads();
         }
         const bool ok = !arrived ? false
@@ -817,8 +819,8 @@ scan_backward_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_con
             const int lane_ch = group * kWidth + lane;
             if (last && a.dh_final_ptrs && lane_ch < a.channels)
                 v = reinterpret_cast<const float *>(a.dh_final_ptrs[slot.stream(kRuns - 1, S - 1)])[lane_ch];
-            if (!pass_on(sh->window, c, place, cell, lane, n, h, end_resets != 0, known, a.wait_ns, a.debug_stall != 0, v))
-                give_up(sh, c, lane, a.status);
+            if (!pass_on(sh->window, c, place, cell, lane, n, h, end_resets != 0, known, a.wait_ns, a.debug_stall == 1, v))
+                give_up(sh, c, kNoState, lane, a.status);
             sh->in[lane] = v;
         }
         const Map m_warp = join<true, kMarked, kWarps - 1, 4>(&sh->N[3 + 4], &sh->M[4], warp_ends >> 1, kWarps - 1 - warp, quad);
@@ -865,11 +867,13 @@ scan_backward_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_con
 
     for (uint32_t it = 0;; ++it) {
         if (warp == kLoader) loader.take(lane);  // for the place that this tile leaves
-        const bool arrived = tc::mbar_wait(&sh->full[it % G::kStages], (it / G::kStages) & 1u, a.wait_ns + kWaitNs);
+        // one answer for the warp, whose lanes work together from here on
+        const bool arrived = __all_sync(0xffffffffu, tc::mbar_wait(&sh->full[it % G::kStages], (it / G::kStages) & 1u,
+                                                                   a.wait_ns + kWaitNs) && a.debug_stall != 2);
         const Slot<L> &slot = sh->slot[it % G::kSlots];
         if (arrived && slot.group < 0) break;
         if (!arrived) {  // nothing of the tile is used; the others leave at their first barrier
-            *failed = kNoTile;
+            give_up(sh, c, kNoTile, lane, a.status);
             __syncthreads();
         }
         const bool ok = !arrived ? false

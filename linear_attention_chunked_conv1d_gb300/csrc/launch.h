@@ -169,7 +169,7 @@ struct GatedScanArgs {
     void *workspace;
     int *status;
     uint64_t wait_ns;  // limit of the wait for a tile's state
-    int debug_stall;   // test knob: the search of a tile's chain finds nothing
+    int debug_stall;   // test knob: 1, the search of a tile's chain finds nothing; 2, a tile counts as not arrived
 };
 struct GatedScanBwdArgs {
     const void *x, *ab;
