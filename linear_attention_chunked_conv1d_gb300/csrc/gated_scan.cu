@@ -562,10 +562,10 @@ template <typename T, bool BWD, bool kSingle, class Sh> struct Loader {
             put(lane);
         }
     }
-    // A block that leaves early waits for the copies it has started; those up to number `it` have
-    // been waited for.
+    // A block that leaves early waits (with a limit) for the copies it has started; those before number `it`
+    // have been waited for.
     __device__ void drain(uint32_t it) {
-        for (++it; it < issued; ++it) tc::mbar_wait(&sh->full[it % G::kStages], (it / G::kStages) & 1u, kWaitNs, 100000u);
+        for (; it < issued; ++it) tc::mbar_wait(&sh->full[it % G::kStages], (it / G::kStages) & 1u, kWaitNs, 100000u);
     }
 };
 
@@ -709,8 +709,9 @@ scan_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ C
         const bool ok = !arrived ? false
                         : slot.marked ? tile_step(std::true_type{}, slot, it)
                                       : tile_step(std::false_type{}, slot, it);
-        if (!ok) {
-            if (warp == kLoader) loader.drain(it);
+        if (!ok) {  // no copy into shared memory, of the ring or of the window, outlives the block
+            if (warp == kLoader) loader.drain(arrived ? it + 1 : it);
+            asm volatile("cp.async.wait_all;" ::: "memory");
             break;
         }
     }
@@ -879,8 +880,9 @@ scan_backward_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_con
         const bool ok = !arrived ? false
                         : slot.marked ? tile_step(std::true_type{}, slot, it)
                                       : tile_step(std::false_type{}, slot, it);
-        if (!ok) {
-            if (warp == kLoader) loader.drain(it);
+        if (!ok) {  // no copy into shared memory, of the ring or of the window, outlives the block
+            if (warp == kLoader) loader.drain(arrived ? it + 1 : it);
+            asm volatile("cp.async.wait_all;" ::: "memory");
             break;
         }
     }

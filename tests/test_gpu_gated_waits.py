@@ -37,3 +37,28 @@ def test_a_tile_that_does_not_arrive_is_reported(cuda, monkeypatch, T, dtype):
     assert (forward(), backward()) == (0, 0)
     for u, v in zip((y, dx, dab), want):
         assert torch.equal(u, v)
+
+
+@pytest.mark.parametrize("stall", ["1", "2"])
+def test_blocks_that_leave_disturb_nobody(cuda, monkeypatch, stall):
+    """Calls that give up early, right next to calls that do not, on two streams: shared memory that a leaving
+    block has copies under way into may be another block's next. The calls that run give their own bits."""
+    T, C = 3000, 256
+    g = torch.Generator().manual_seed(50)
+    x, ab = torch.randn(T, C, generator=g).to(cuda), torch.randn(T, 2 * C, generator=g).to(cuda)
+    ws = [torch.empty(la.gated_scan_workspace_bytes(1, T, C, x.dtype), dtype=torch.uint8, device=cuda) for _ in range(2)]
+    y, left = torch.empty_like(x), torch.empty_like(x)
+    side = torch.cuda.Stream()
+    la.gated_scan(None, x, ab, y, workspace=ws[0])
+    torch.cuda.synchronize()
+    want = y.clone()
+    monkeypatch.setenv("LA_WAIT_LIMIT_NS", "1000000")
+    for _ in range(5):
+        monkeypatch.setenv("LA_DEBUG_STALL", stall)
+        la.gated_scan(None, x, ab, left, workspace=ws[1], stream=side)
+        monkeypatch.delenv("LA_DEBUG_STALL")
+        y.zero_()
+        la.gated_scan(None, x, ab, y, workspace=ws[0])
+        torch.cuda.synchronize()
+        assert torch.equal(y, want)
+    assert la.device_status() == la.LA_DEV_TIMEOUT
