@@ -15,8 +15,10 @@
 //  - The packed rows are cut into tiles of L tokens x 32 channels, regardless of where streams meet
 //    (but for the few sections below).
 //    A tile maps the state (or, backward, the gradient m) that reaches it to the one that leaves it:
-//    h -> h + N h + H. N = prod (1 - d) - 1 is carried instead of the product, for the reason in
-//    gated.cuh. Where a stream starts inside the tile, what comes from before is dropped.
+//    h -> K h + H with K = prod (1 - d). Where a stream starts inside the tile, what comes from before
+//    is dropped. K is a product of its factors, right to its own last places however small it gets:
+//    what a channel forgets is gone. Of a K above 1/2 the difference from 1, N = K - 1, is kept beside
+//    it, for the reason in gated.cuh, and it is what the tiles of a chain pass on (word_of).
 //  - Tiles of a channel group are chained along the sequence. A block publishes its tile's (N, H) as
 //    soon as it has them, finds the nearest earlier tile whose outgoing state is known, and applies
 //    the maps in between to that state, oldest first. The state that leaves a tile is thus the same
@@ -112,7 +114,7 @@ constexpr uint32_t kUnwritten = 0xffffffffu;
 struct Chain {
     Ctl *ctl;
     Tile *tile;          // [tiles]
-    float *N, *H, *out;  // [tiles][groups][32]: the tile's map, the state that leaves it
+    float *N, *H, *out;  // [tiles][groups][32]: the tile's map (N: word_of), the state that leaves it
     int tiles, groups, sections;  // tiles: the most there can be
     // All tokens fit in one tile: nothing is chained, and a block for each group does without the
     // kernel that lays the chains out (100 tokens x 768 fp32: 9.7 us on the device with it, 4.4 without).
@@ -303,27 +305,57 @@ __device__ __forceinline__ void mbar_arrive(uint64_t *bar) {
 }
 __device__ __forceinline__ F4 zero4() { return all4(0.f); }
 
-// h -> h + N h + H of some tokens.
+// h -> K h + H of some tokens.
 struct Map {
-    F4 N, H;
-    __device__ __forceinline__ F4 apply(const F4 &h) const { return add4(left4(N, h), H); }
-    // these tokens after those of `e`: (1 + e.N)(1 + N) - 1 = e.N + N + e.N N
-    __device__ __forceinline__ Map after(const Map &e) const { return Map{fma4(N, e.N, add4(e.N, N)), apply(e.H)}; }
+    F4 K, H;
+    __device__ __forceinline__ F4 apply(const F4 &h) const { return fma4(K, h, H); }
+    // these tokens after those of `e`
+    __device__ __forceinline__ Map after(const Map &e) const { return Map{mul4(K, e.K), apply(e.H)}; }
 };
-__device__ __forceinline__ Map identity() { return Map{zero4(), zero4()}; }
+__device__ __forceinline__ Map identity() { return Map{all4(1.f), zero4()}; }
+
+// What a run's tokens leave of a state, K = R or 1 + N: R is rounded at every token, which for slow
+// channels goes the same way each time, N's terms all have one sign.
+__device__ __forceinline__ F4 left_of_run(const F4 &N, const F4 &R) {
+    float n[4], r[4];
+    unpack4(N, n);
+    unpack4(R, r);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) r[e] = r[e] > 0.5f ? 1.f + n[e] : r[e];
+    return pack4(r);
+}
+// N of a warp's four runs (ranks), from each lane's: (1 + a)(1 + b) - 1 = a (1 + b) + b.
+__device__ __forceinline__ F4 join_ranks(F4 N) {
+#pragma unroll
+    for (int off = 8; off < 32; off *= 2) {
+        float f[4];
+        unpack4(N, f);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) f[e] = __shfl_xor_sync(0xffffffffu, f[e], off);
+        const F4 other = pack4(f);
+        N = fma4(N, add4(other, all4(1.f)), other);
+    }
+    return N;
+}
+
+// The word by which a tile's K is passed on: N (its sign is set: -0 says that all is kept) where K > 1/2,
+// else K itself (its sign is not).
+__device__ __forceinline__ float word_of(float N, float K) { return K > 0.5f ? N : K; }
+// K h of a word
+__device__ __forceinline__ float left_by(float word, float h) { return fmaf(word, h, __float_as_int(word) < 0 ? h : 0.f); }
 
 // The first `last` of n maps (rows at a stride of kStep), joined in order of the tokens, or against it
 // (REV: row n - 1 first). A bit in `resets` says that a stream starts among a row's tokens: what comes
 // before it is dropped there, not multiplied by 0 (it may be NaN). kMarked: whether there may be any.
 template <bool REV, bool kMarked, int n, int kStep>
-__device__ __forceinline__ Map join(const float (*N)[kWidth], const float (*H)[kWidth], uint32_t resets, int last, int quad) {
+__device__ __forceinline__ Map join(const float (*K)[kWidth], const float (*H)[kWidth], uint32_t resets, int last, int quad) {
     Map m = identity();
 #pragma unroll
     for (int k = 0; k < n; ++k) {
         const int r = REV ? n - 1 - k : k;
         if (k < last) {
-            const Map e{load_f4(&N[r * kStep][quad * 4]), load_f4(&H[r * kStep][quad * 4])};
-            m = kMarked && (resets >> r & 1u) ? Map{e.after(m).N, e.H} : e.after(m);
+            const Map e{load_f4(&K[r * kStep][quad * 4]), load_f4(&H[r * kStep][quad * 4])};
+            m = kMarked && (resets >> r & 1u) ? Map{e.after(m).K, e.H} : e.after(m);
         }
     }
     return m;
@@ -353,18 +385,20 @@ __device__ __forceinline__ int load_abort(const Ctl *ctl) {
 // Passing a tile's state on is the work of one warp, with one channel a lane: few registers, next to
 // those that hold its tokens.
 
-// The joined map of all warps of a tile (as join, for one channel).
-template <bool REV, bool kMarked>
-__device__ __forceinline__ void join_all(const float (*N)[kWidth], const float (*H)[kWidth], uint32_t resets, int lane,
-                                         float &n, float &h) {
-    n = h = 0.f;
+// The joined map of all warps of a tile (as join, for one channel), its K as a word.
+template <bool REV, bool kMarked, class Sh>
+__device__ __forceinline__ void join_all(const Sh *sh, const float (*H)[kWidth], uint32_t resets, int lane, float &word, float &h) {
+    float n = -0.f, k = 1.f;
+    h = 0.f;
 #pragma unroll
-    for (int k = 0; k < kWarps; ++k) {
-        const int r = REV ? kWarps - 1 - k : k;
-        const float en = N[r * 4][lane], eh = H[r * 4][lane];
-        n = fmaf(en, n, n + en);
-        h = kMarked && (resets >> r & 1u) ? eh : fmaf(en, h, h) + eh;
+    for (int j = 0; j < kWarps; ++j) {
+        const int r = REV ? kWarps - 1 - j : j;
+        const float en = sh->N[r][lane], ek = sh->K[r * 4 + 3][lane], eh = H[r * 4][lane];
+        n = fmaf(n, 1.f + en, en);
+        k *= ek;
+        h = kMarked && (resets >> r & 1u) ? eh : fmaf(ek, h, eh);
     }
+    word = word_of(n, k);
 }
 
 // Eight places of a chain in shared memory, `top` and those before it, as one warp finds them in L2.
@@ -406,7 +440,7 @@ struct Window {
     }
     // h through places top - n + 1 .. top
     __device__ __forceinline__ float apply(int n, float h, int lane) const {
-        for (int k = n - 1; k >= 0; --k) h = fmaf(N[k][lane], h, h) + H[k][lane];
+        for (int k = n - 1; k >= 0; --k) h = left_by(N[k][lane], h) + H[k][lane];
         return h;
     }
 };
@@ -448,7 +482,7 @@ __device__ __forceinline__ bool look_back(Window &w, const Chain &c, int at, Cel
     return true;
 }
 
-// Publishes the map (n, h) of the tile at `place` (`reset`: its h is what leaves it, whatever comes),
+// Publishes the map (n: the word of its K, h) of the tile at `place` (`reset`: its h is what leaves it, whatever comes),
 // waits for what reaches it (unless `known`: then the window has not been told to fetch anything, as nobody
 // would wait for it), publishes what leaves it. False: the wait ran out.
 template <class Cell>
@@ -462,7 +496,7 @@ __device__ __forceinline__ bool pass_on(Window &w, const Chain &c, int place, Ce
         store_relaxed(c.H + own, h);
     }
     if (!known && !look_back(w, c, place, cell, lane, wait_ns, stall, in)) return false;
-    if (!reset) store_relaxed(c.out + own, fmaf(n, in, in) + h);
+    if (!reset) store_relaxed(c.out + own, left_by(n, in) + h);
     return true;
 }
 
@@ -476,9 +510,10 @@ template <int L, int STAGES, bool BWD> struct Shared {
     uint64_t full[STAGES];
     int failed;
     Slot<L> slot[STAGES + 1];
-    // the runs' maps: N and H, backward also M with N along the reverse scan; then, in the last row of
+    // the runs' maps: K and H, backward also M with K along the reverse scan; then, in the last row of
     // each warp's four (of M: in the first), the warps'
-    alignas(16) float N[kRuns][kWidth], H[kRuns][kWidth], M[BWD ? kRuns : 1][kWidth];
+    alignas(16) float K[kRuns][kWidth], H[kRuns][kWidth], M[BWD ? kRuns : 1][kWidth];
+    alignas(16) float N[kWarps][kWidth];  // the warps' K - 1
     alignas(16) float in[kWidth];  // what reaches the tile
     alignas(16) Window window;
 };
@@ -618,7 +653,7 @@ scan_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ C
         F4 hl[S], A[S];
         const T *in = reinterpret_cast<const T *>(ring + it % G::kStages * G::kStage) + run * S * kWidth + quad * 4;
         Map m = identity();
-        F4 R = all4(1.f);
+        F4 N = all4(-0.f);
 #pragma unroll
         for (int i = 0; i < S; ++i) {
             if (kMarked && (starts >> i & 1u)) {
@@ -635,19 +670,22 @@ scan_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ C
             gates4(widen4<T>(V::load_raw(in + i * kWidth + kPlane)), widen4<T>(V::load_raw(in + i * kWidth + 2 * kPlane)),
                    nd, beta);
             m.H = fma4(beta, widen4<T>(V::load_raw(in + i * kWidth)), left4(nd, m.H));
-            m.N = fma4(nd, R, m.N);
-            R = add4(m.N, all4(1.f));
+            N = fma4(nd, m.K, N);
+            m.K = left4(nd, m.K);
             hl[i] = m.H;
-            A[i] = R;
+            A[i] = m.K;
         }
+        m.K = left_of_run(N, m.K);
         if (warp == kWarps - 1 && !first) sh->window.fetch(c, place - 1, cell, lane);  // in good time for look_back
-        store_f4(&sh->N[run][quad * 4], m.N);
+        store_f4(&sh->K[run][quad * 4], m.K);
         store_f4(&sh->H[run][quad * 4], m.H);
+        N = join_ranks(N);
         __syncwarp();
         const uint32_t own_resets = resets >> 4 * warp & 15u;
         if (rank == 3) {
-            const Map w = m.after(join<false, kMarked, 3, 1>(&sh->N[warp * 4], &sh->H[warp * 4], own_resets, 3, quad));
-            store_f4(&sh->N[run][quad * 4], w.N);
+            const Map w = m.after(join<false, kMarked, 3, 1>(&sh->K[warp * 4], &sh->H[warp * 4], own_resets, 3, quad));
+            store_f4(&sh->N[warp][quad * 4], N);
+            store_f4(&sh->K[run][quad * 4], w.K);
             store_f4(&sh->H[run][quad * 4], kMarked && (own_resets & 8u) ? m.H : w.H);
         }
         __syncthreads();
@@ -657,7 +695,7 @@ scan_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ C
         const uint32_t warp_resets = kMarked ? by_warp(resets) : 0u;
         if (warp == kWarps - 1) {
             float n, h, v = 0.f;
-            join_all<false, kMarked>(&sh->N[3], &sh->H[3], warp_resets, lane, n, h);
+            join_all<false, kMarked>(sh, &sh->H[3], warp_resets, lane, n, h);
             const int lane_ch = group * kWidth + lane;
             if (first && lane_ch < a.channels) {
                 const int id = slot.start_id[0];
@@ -668,14 +706,14 @@ scan_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ C
                 give_up(sh, c, kNoState, lane, a.status);
             sh->in[lane] = v;
         }
-        const Map before_warp = join<false, kMarked, kWarps - 1, 4>(&sh->N[3], &sh->H[3], warp_resets, warp, quad);
+        const Map before_warp = join<false, kMarked, kWarps - 1, 4>(&sh->K[3], &sh->H[3], warp_resets, warp, quad);
         __syncthreads();
         if (*failed == kNoState) return false;
 
         // the state that reaches this run, then its tokens'
         F4 v = load_f4(&sh->in[quad * 4]);
         v = reset_before<false, kWarps>(warp_resets, warp) ? before_warp.H : before_warp.apply(v);
-        const Map before_run = join<false, kMarked, 3, 1>(&sh->N[warp * 4], &sh->H[warp * 4], own_resets, rank, quad);
+        const Map before_run = join<false, kMarked, 3, 1>(&sh->K[warp * 4], &sh->H[warp * 4], own_resets, rank, quad);
         v = reset_before<false, 4>(own_resets, rank) ? before_run.H : before_run.apply(v);
         const int count = kMarked ? slot.count - run * S : S;  // tokens of this run (or more)
         if (a.saved && live && run * S % kSave<T> == 0 && (!kMarked || (!(starts & 1u) && count > 0)))
@@ -778,16 +816,17 @@ scan_backward_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_con
         for (int i = 0; i < S; ++i)
             gates4(widen4<T>(V::load_raw(in + i * kWidth + kPlane)), widen4<T>(V::load_raw(in + i * kWidth + 2 * kPlane)),
                    nd[i], beta[i]);
-        Map h = identity();  // of this run, forward; with m.H in place of h.H, along the reverse scan
-        F4 R = all4(1.f), m = zero4();
+        Map h = identity();  // of this run, forward; with m in place of h.H, along the reverse scan
+        F4 N = all4(-0.f), m = zero4();
 #pragma unroll
         for (int i = 0; i < S; ++i) {
             xr[i] = V::load_raw(in + i * kWidth);
             if (kMarked && (starts >> i & 1u)) h.H = initial(i);
             h.H = fma4(beta[i], widen4<T>(xr[i]), left4(nd[i], h.H));
-            h.N = fma4(nd[i], R, h.N);
-            R = add4(h.N, all4(1.f));
+            N = fma4(nd[i], h.K, N);
+            h.K = left4(nd[i], h.K);
         }
+        h.K = left_of_run(N, h.K);
 #pragma unroll
         for (int i = S - 1; i >= 0; --i) {
             dyr[i] = V::load_raw(in + i * kWidth + 3 * kPlane);
@@ -795,20 +834,22 @@ scan_backward_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_con
             m = left4(nd[i], add4(widen4<T>(dyr[i]), m));
         }
         if (warp == 0 && !known) sh->window.fetch(c, place - 1, cell, lane);  // in good time for look_back
-        store_f4(&sh->N[run][quad * 4], h.N);
+        store_f4(&sh->K[run][quad * 4], h.K);
         store_f4(&sh->H[run][quad * 4], h.H);
         store_f4(&sh->M[run][quad * 4], m);
+        N = join_ranks(N);
         __syncwarp();
         const uint32_t own_resets = resets >> 4 * warp & 15u, own_ends = end_resets >> 4 * warp & 15u;
-        const Map h_run = join<false, kMarked, 4, 1>(&sh->N[warp * 4], &sh->H[warp * 4], own_resets, rank, quad);
-        const Map m_run = join<true, kMarked, 4, 1>(&sh->N[warp * 4], &sh->M[warp * 4], own_ends, 3 - rank, quad);
+        const Map h_run = join<false, kMarked, 4, 1>(&sh->K[warp * 4], &sh->H[warp * 4], own_resets, rank, quad);
+        const Map m_run = join<true, kMarked, 4, 1>(&sh->K[warp * 4], &sh->M[warp * 4], own_ends, 3 - rank, quad);
         __syncwarp();
         if (rank == 3) {
             const Map w = h.after(h_run);
-            store_f4(&sh->N[run][quad * 4], w.N);
+            store_f4(&sh->N[warp][quad * 4], N);
+            store_f4(&sh->K[run][quad * 4], w.K);
             store_f4(&sh->H[run][quad * 4], kMarked && (own_resets & 8u) ? h.H : w.H);
         }
-        if (rank == 0) store_f4(&sh->M[run][quad * 4], kMarked && (own_ends & 1u) ? m : Map{h.N, m}.apply(m_run.H));
+        if (rank == 0) store_f4(&sh->M[run][quad * 4], kMarked && (own_ends & 1u) ? m : Map{h.K, m}.apply(m_run.H));
         __syncthreads();
         if (*failed == kNoTile) return false;
         if (warp == kLoader) loader.put(lane);
@@ -816,7 +857,7 @@ scan_backward_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_con
         const uint32_t warp_resets = kMarked ? by_warp(resets) : 0u, warp_ends = kMarked ? by_warp(end_resets) : 0u;
         if (warp == 0) {
             float n, h, v = 0.f;
-            join_all<true, kMarked>(&sh->N[3], &sh->M[0], warp_ends, lane, n, h);
+            join_all<true, kMarked>(sh, &sh->M[0], warp_ends, lane, n, h);
             const int lane_ch = group * kWidth + lane;
             if (last && a.dh_final_ptrs && lane_ch < a.channels)
                 v = reinterpret_cast<const float *>(a.dh_final_ptrs[slot.stream(kRuns - 1, S - 1)])[lane_ch];
@@ -824,9 +865,9 @@ scan_backward_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_con
                 give_up(sh, c, kNoState, lane, a.status);
             sh->in[lane] = v;
         }
-        const Map m_warp = join<true, kMarked, kWarps - 1, 4>(&sh->N[3 + 4], &sh->M[4], warp_ends >> 1, kWarps - 1 - warp, quad);
+        const Map m_warp = join<true, kMarked, kWarps - 1, 4>(&sh->K[3 + 4], &sh->M[4], warp_ends >> 1, kWarps - 1 - warp, quad);
         // meanwhile the others (and warp 0 after it) have the states before their tokens
-        const Map h_warp = join<false, kMarked, kWarps - 1, 4>(&sh->N[3], &sh->H[3], warp_resets, warp, quad);
+        const Map h_warp = join<false, kMarked, kWarps - 1, 4>(&sh->K[3], &sh->H[3], warp_resets, warp, quad);
         F4 hp[S];
         {
             F4 v = reset_before<false, kWarps>(warp_resets, warp) ? h_warp.H : h_warp.apply(h_in);
