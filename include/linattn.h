@@ -367,6 +367,9 @@ int la_prefill_segmented(const uint64_t *h_state_ptrs, const void *q, const void
  * workspace     la_gated_scan_workspace_bytes(...) bytes (16-byte aligned), used by this call alone
  *               until its work is done. It need not be initialised. Calls (and captured graphs) that
  *               may overlap on the GPU need a workspace each; calls in stream order may share one.
+ * Decay, 1 - decay, beta and 1 - beta are each right relative to themselves, however near 0 or 1 a
+ * gate is (to about 2^-21 + |gate| 2^-23 of the smaller one; below 2^-126 it counts as 0), here and
+ * in the calls below: what a state loses and a gate's gradient keep their own last places.
  * Gates of +-infinity are exact: a = -inf keeps a finite state, a = +inf drops it, b = -inf adds
  * nothing of a finite x. An infinite or NaN state, x or NaN gate makes its channel NaN or infinite
  * from there to the stream's end, and no other stream or channel.

@@ -43,31 +43,71 @@ template <typename T> __device__ __forceinline__ void store_act4(T *p, const F4 
     Vec4<T>::store(p, f);
 }
 
-// The gates of four channels: nd = -d = -sigmoid(a) and beta = sigmoid(b). The decay
-// exp(-softplus(a)) is 1 + nd. The kernels carry d, which is exact to a few units in its last place
-// however small it is, and never the rounded 1 - d: h - d h keeps the time constant of a channel that
-// remembers thousands of tokens, where a decay rounded to 24 bits would be off by up to 2^-25 at every
-// token, the same way each time. Infinite gates give exactly 0 or 1.
-// (One reciprocal of the product (1 + e^-a)(1 + e^-b) for both gates saves a special function but
-// needs a second way for gates beyond its range, and with it the scan's registers no longer sufficed:
-// 1.15 ms instead of 0.69 for 262,144 x 2048, the chains left out.)
-__device__ __forceinline__ void gates4(const F4 &a, const F4 &b, F4 &nd, F4 &beta) {
-    const F4 l = all4(-kLog2e), one = all4(1.f), minus = all4(-1.f);
-    float p[4], q[4];
-    unpack4(mul4(a, l), p);
-    unpack4(mul4(b, l), q);
+// The decay 1 - d = sigmoid(-a) = exp(-softplus(a)) of four channels, by its smaller side. With t = a log2 e,
+//   small = 2^-|t| / (1 + 2^-|t|) in 0 .. 1/2,  side = t < 0 ? -small : small,  neg = t < 0 ? 1 : 0,
+// the decay neg + side and d = (1 - neg) - side are both right to their own last places: the one is small, the
+// other 1 - small, rounded once. (From d = sigmoid(a) alone 1 - d is off by 2^-25: by 0.3% of it at a = 10, by
+// all of it at 17.) Relative to small the error is that of the argument's rounding, |a| 2^-23 at most, and 2^-21
+// of the hardware exponential and reciprocal and three roundings; below 2^-126 (|a| > 87.3) it is flushed to 0.
+// Infinite gates give exactly 0 and 1.
+// The rounded decay is what the few tokens of a run go by. Where tokens follow each other without end, a
+// channel that remembers thousands of them would be off by up to 2^-25 at every one, the same way each time:
+// there h goes on as left4, h - d h (or (1 - d) h), rounded once.
+// kMark: a negative side has 2^-149 more, so that neg_of finds it again when small is 0. (Next to 1 it is nothing;
+// d is then 2^-149, not 0.)
+template <bool kMark> __device__ __forceinline__ F4 decay4(const F4 &a, F4 &neg) {
+    const F4 one = all4(1.f);
+    float f[4], n[4], e[4];
+    unpack4(fma4(a, all4(kLog2e), all4(0.f)), f);  // + 0: -0 counts as 0 below, too
 #pragma unroll
-    for (int e = 0; e < 4; ++e) p[e] = ex2_approx(p[e]), q[e] = ex2_approx(q[e]);
-    unpack4(fma4(pack4(p), minus, minus), p);
-    unpack4(add4(pack4(q), one), q);
+    for (int i = 0; i < 4; ++i) e[i] = ex2_approx(-fabsf(f[i])), n[i] = f[i] < 0.f ? 1.f : 0.f;
+    neg = pack4(n);
+    const F4 E = pack4(e);
+    unpack4(add4(E, one), f);
 #pragma unroll
-    for (int e = 0; e < 4; ++e) p[e] = rcp_approx(p[e]), q[e] = rcp_approx(q[e]);
-    nd = pack4(p);
-    beta = pack4(q);
+    for (int i = 0; i < 4; ++i) f[i] = rcp_approx(f[i]);
+    const F4 small = mul4(E, pack4(f)), sign = fma4(neg, all4(-2.f), one);
+    return kMark ? fma4(small, sign, mul4(neg, all4(-0x1p-149f))) : mul4(small, sign);
 }
+// neg of a marked side; the decay, -d and what is left of h.
+__device__ __forceinline__ F4 neg_of(const F4 &side) {
+    float f[4];
+    unpack4(side, f);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) f[i] = f[i] < 0.f ? 1.f : 0.f;
+    return pack4(f);
+}
+__device__ __forceinline__ F4 decay_of(const F4 &side, const F4 &neg) { return add4(neg, side); }
+__device__ __forceinline__ F4 minus_d_of(const F4 &side, const F4 &neg) { return add4(add4(neg, all4(-1.f)), side); }
+__device__ __forceinline__ F4 left4(const F4 &side, const F4 &neg, const F4 &h) { return fma4(side, h, mul4(neg, h)); }
 
-// (1 - d) h, rounded once, so that a gate near 1 forgets a large state without its rounding errors
-// staying behind.
-__device__ __forceinline__ F4 left4(const F4 &nd, const F4 &h) { return fma4(nd, h, h); }
+// The input gate beta = sigmoid(b) = 1 / (1 + q) with q = e^-b, and 1 - beta = q beta: a product, which is right
+// relative to itself for either sign of b. q is held to 2^127, where beta is flushed to 0 and the product is 0,
+// not NaN: it is only ever a factor next to beta. min.NaN passes a NaN on.
+__device__ __forceinline__ F4 input_exp4(const F4 &b) {
+    float q[4];
+    unpack4(mul4(b, all4(-kLog2e)), q);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        q[e] = ex2_approx(q[e]);
+        asm("min.NaN.f32 %0, %0, 0f7f000000;" : "+f"(q[e]));
+    }
+    return pack4(q);
+}
+__device__ __forceinline__ F4 input_of(const F4 &q) {
+    float f[4];
+    unpack4(add4(q, all4(1.f)), f);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) f[e] = rcp_approx(f[e]);
+    return pack4(f);
+}
+// beta where 1 - beta is not needed.
+__device__ __forceinline__ F4 input4(const F4 &b) {
+    float q[4];
+    unpack4(mul4(b, all4(-kLog2e)), q);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) q[e] = ex2_approx(q[e]);
+    return input_of(pack4(q));
+}
 
 }  // namespace la

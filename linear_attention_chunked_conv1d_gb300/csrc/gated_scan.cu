@@ -17,7 +17,7 @@
 //    A tile maps the state (or, backward, the gradient m) that reaches it to the one that leaves it:
 //    h -> K h + H with K = prod (1 - d). Where a stream starts inside the tile, what comes from before
 //    is dropped. K is a product of its factors, right to its own last places however small it gets:
-//    what a channel forgets is gone. Of a K above 1/2 the difference from 1, N = K - 1, is kept beside
+//    what a channel forgets is gone. Of a K above 3/4 the difference from 1, N = K - 1, is kept beside
 //    it, for the reason in gated.cuh, and it is what the tiles of a chain pass on (word_of).
 //  - Tiles of a channel group are chained along the sequence. A block publishes its tile's (N, H) as
 //    soon as it has them, finds the nearest earlier tile whose outgoing state is known, and applies
@@ -58,7 +58,7 @@ constexpr int kRuns = 4 * kWarps;  // is along the tokens, in runs of S
 constexpr uint64_t kWaitNs = 2000000000ull;
 
 // Tokens of a run, and the ring's depth. What a thread keeps of a tile across the wait for its state
-// is 2 registers a (token, channel) forward and 4 (bf16) or 5 (fp32) backward; two blocks on an SM leave
+// is 2 registers a (token, channel) forward and 4.5 (bf16) or 5 (fp32) backward; two blocks on an SM leave
 // 128 registers a thread, which these fill: half of these runs takes half again as long. A tile's place
 // in the ring is free, and its next copy under way, half way through the tile: backward one place is
 // enough (a second one only takes tiles earlier than needed: 8 x 2048 x 4096 bf16, both passes, 2%
@@ -315,13 +315,15 @@ struct Map {
 __device__ __forceinline__ Map identity() { return Map{all4(1.f), zero4()}; }
 
 // What a run's tokens leave of a state, K = R or 1 + N: R is rounded at every token, which for slow
-// channels goes the same way each time, N's terms all have one sign.
+// channels goes the same way each time, N's terms all have one sign. N is there only where every decay of
+// the run is above 1/2 (decay4), so that it is looked at only where K is well above it.
+constexpr float kSlow = 0.75f;
 __device__ __forceinline__ F4 left_of_run(const F4 &N, const F4 &R) {
     float n[4], r[4];
     unpack4(N, n);
     unpack4(R, r);
 #pragma unroll
-    for (int e = 0; e < 4; ++e) r[e] = r[e] > 0.5f ? 1.f + n[e] : r[e];
+    for (int e = 0; e < 4; ++e) r[e] = r[e] > kSlow ? 1.f + n[e] : r[e];
     return pack4(r);
 }
 // N of a warp's four runs (ranks), from each lane's: (1 + a)(1 + b) - 1 = a (1 + b) + b.
@@ -338,9 +340,9 @@ __device__ __forceinline__ F4 join_ranks(F4 N) {
     return N;
 }
 
-// The word by which a tile's K is passed on: N (its sign is set: -0 says that all is kept) where K > 1/2,
-// else K itself (its sign is not).
-__device__ __forceinline__ float word_of(float N, float K) { return K > 0.5f ? N : K; }
+// The word by which a tile's K is passed on: N (its sign is set: -0 says that all is kept) where K is above
+// kSlow, else K itself (its sign is not).
+__device__ __forceinline__ float word_of(float N, float K) { return K > kSlow ? N : K; }
 // K h of a word
 __device__ __forceinline__ float left_by(float word, float h) { return fmaf(word, h, __float_as_int(word) < 0 ? h : 0.f); }
 
@@ -666,12 +668,12 @@ scan_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ C
                         store_f4(a.saved + (int64_t)(slot.saved + run * S / kSave<T>) * a.channels + ch, m.H);
                 }
             }
-            F4 nd, beta;
-            gates4(widen4<T>(V::load_raw(in + i * kWidth + kPlane)), widen4<T>(V::load_raw(in + i * kWidth + 2 * kPlane)),
-                   nd, beta);
-            m.H = fma4(beta, widen4<T>(V::load_raw(in + i * kWidth)), left4(nd, m.H));
-            N = fma4(nd, m.K, N);
-            m.K = left4(nd, m.K);
+            F4 neg;
+            const F4 side = decay4<false>(widen4<T>(V::load_raw(in + i * kWidth + kPlane)), neg), keep = decay_of(side, neg);
+            const F4 beta = input4(widen4<T>(V::load_raw(in + i * kWidth + 2 * kPlane)));
+            m.H = fma4(beta, widen4<T>(V::load_raw(in + i * kWidth)), mul4(keep, m.H));
+            N = fma4(side, m.K, N);
+            m.K = mul4(keep, m.K);
             hl[i] = m.H;
             A[i] = m.K;
         }
@@ -809,29 +811,30 @@ scan_backward_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_con
                                            : zero4();
         };
 
-        F4 nd[S], beta[S];
-        typename V::Raw xr[S], dyr[S];
+        // the decays' sides (past the second barrier: the decays), e^-b, and what enters, beta x
+        F4 gate[S], input[S], u[S];
+        typename V::Raw dyr[S];
         const T *in = reinterpret_cast<const T *>(ring + it % G::kStages * G::kStage) + run * S * kWidth + quad * 4;
-#pragma unroll
-        for (int i = 0; i < S; ++i)
-            gates4(widen4<T>(V::load_raw(in + i * kWidth + kPlane)), widen4<T>(V::load_raw(in + i * kWidth + 2 * kPlane)),
-                   nd[i], beta[i]);
         Map h = identity();  // of this run, forward; with m in place of h.H, along the reverse scan
-        F4 N = all4(-0.f), m = zero4();
+        F4 N = all4(-0.f), m = zero4(), keep[S];
 #pragma unroll
         for (int i = 0; i < S; ++i) {
-            xr[i] = V::load_raw(in + i * kWidth);
+            F4 neg;
+            gate[i] = decay4<true>(widen4<T>(V::load_raw(in + i * kWidth + kPlane)), neg);
+            input[i] = input_exp4(widen4<T>(V::load_raw(in + i * kWidth + 2 * kPlane)));
+            keep[i] = decay_of(gate[i], neg);
             if (kMarked && (starts >> i & 1u)) h.H = initial(i);
-            h.H = fma4(beta[i], widen4<T>(xr[i]), left4(nd[i], h.H));
-            N = fma4(nd[i], h.K, N);
-            h.K = left4(nd[i], h.K);
+            u[i] = mul4(input_of(input[i]), widen4<T>(V::load_raw(in + i * kWidth)));
+            h.H = fma4(keep[i], h.H, u[i]);
+            N = fma4(gate[i], h.K, N);
+            h.K = mul4(keep[i], h.K);
         }
         h.K = left_of_run(N, h.K);
 #pragma unroll
         for (int i = S - 1; i >= 0; --i) {
             dyr[i] = V::load_raw(in + i * kWidth + 3 * kPlane);
             if (kMarked && (ends >> i & 1u)) m = final_gradient(i);
-            m = left4(nd[i], add4(widen4<T>(dyr[i]), m));
+            m = mul4(keep[i], add4(widen4<T>(dyr[i]), m));
         }
         if (warp == 0 && !known) sh->window.fetch(c, place - 1, cell, lane);  // in good time for look_back
         store_f4(&sh->K[run][quad * 4], h.K);
@@ -865,26 +868,37 @@ scan_backward_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_con
                 give_up(sh, c, kNoState, lane, a.status);
             sh->in[lane] = v;
         }
-        const Map m_warp = join<true, kMarked, kWarps - 1, 4>(&sh->K[3 + 4], &sh->M[4], warp_ends >> 1, kWarps - 1 - warp, quad);
         // meanwhile the others (and warp 0 after it) have the states before their tokens
         const Map h_warp = join<false, kMarked, kWarps - 1, 4>(&sh->K[3], &sh->H[3], warp_resets, warp, quad);
-        F4 hp[S];
+        F4 hd[S];  // what a token finds and forgets, -d h_{t-1}
         {
             F4 v = reset_before<false, kWarps>(warp_resets, warp) ? h_warp.H : h_warp.apply(h_in);
             v = reset_before<false, 4>(own_resets, rank) ? h_run.H : h_run.apply(v);
 #pragma unroll
             for (int i = 0; i < S; ++i) {
                 if (kMarked && (starts >> i & 1u)) v = initial(i);
-                hp[i] = v;
-                v = fma4(beta[i], widen4<T>(xr[i]), left4(nd[i], v));
+                const F4 neg = neg_of(gate[i]), side = gate[i];
+                hd[i] = mul4(v, minus_d_of(side, neg));
+                gate[i] = decay_of(side, neg);
+                v = fma4(gate[i], v, u[i]);
             }
+        }
+        // what the tokens after this run make of the gradient that reaches the tile
+        Map after_run = m_run;
+        bool ended = reset_before<true, 4>(own_ends, 3 - rank);
+        if (!ended) {
+            after_run = m_run.after(join<true, kMarked, kWarps - 1, 4>(&sh->K[3 + 4], &sh->M[4], warp_ends >> 1, kWarps - 1 - warp, quad));
+            ended = reset_before<true, kWarps>(warp_ends, kWarps - 1 - warp);
         }
         __syncthreads();
         if (*failed == kNoState) return false;
 
+        // beta comes from e^-b anew: kept since its first use, it would be 4 S registers more, and spills (362 us
+        // instead of 347 for both passes of 8 x 2048 x 4096 bf16)
+#pragma unroll
+        for (int i = 0; i < S; ++i) asm volatile("" : "+l"(input[i].p[0]), "+l"(input[i].p[1]));
         F4 v = load_f4(&sh->in[quad * 4]);
-        v = reset_before<true, kWarps>(warp_ends, kWarps - 1 - warp) ? m_warp.H : m_warp.apply(v);
-        v = reset_before<true, 4>(own_ends, 3 - rank) ? m_run.H : m_run.apply(v);
+        v = ended ? after_run.H : after_run.apply(v);
         const uint32_t all_starts = kMarked ? Slot<L>::bits(slot.starts, run) : 0u;
         const int count = kMarked ? slot.count - run * S : S;
         T *dxp = static_cast<T *>(a.dx) + (int64_t)(slot.t0 + run * S + S - 1) * a.dx_stride + ch;
@@ -892,12 +906,12 @@ scan_backward_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_con
 #pragma unroll
         for (int i = S - 1; i >= 0; --i) {
             if (kMarked && (ends >> i & 1u)) v = final_gradient(i);
-            const F4 lam = add4(widen4<T>(dyr[i]), v), dx = mul4(lam, beta[i]);
-            v = left4(nd[i], lam);
+            const F4 lam = add4(widen4<T>(dyr[i]), v), beta = input_of(input[i]), dx = mul4(lam, beta);
+            v = mul4(gate[i], lam);
             if (live && (!kMarked || i < count)) {
                 store_act4<T>(dxp, dx);
-                store_act4<T>(dap, mul4(mul4(v, hp[i]), nd[i]));
-                store_act4<T>(dap + a.channels, mul4(mul4(dx, widen4<T>(xr[i])), fma4(beta[i], all4(-1.f), all4(1.f))));
+                store_act4<T>(dap, mul4(v, hd[i]));
+                store_act4<T>(dap + a.channels, mul4(mul4(lam, u[i]), mul4(input[i], beta)));
             }
             dxp -= a.dx_stride;
             dap -= a.dab_stride;

@@ -49,9 +49,9 @@ __global__ void __launch_bounds__(kThreads) gated_step_kernel(const GatedStepArg
                 x[e] = silu(p[e]);
             }
         }
-        F4 nd, beta;
-        gates4(pack4(ga), pack4(gb), nd, beta);
-        unpack4(fma4(beta, pack4(x), left4(nd, pack4(hv))), hv);
+        F4 neg;
+        const F4 side = decay4<false>(pack4(ga), neg);
+        unpack4(fma4(input4(pack4(gb)), pack4(x), left4(side, neg, pack4(hv))), hv);
         Vec4<float>::store(h, hv);
         V::store((T *)a.y + s * a.y_stride + c, hv);
     }
