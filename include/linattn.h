@@ -355,7 +355,9 @@ int la_prefill_segmented(const uint64_t *h_state_ptrs, const void *q, const void
  *               stream starts from zero and its final state is not kept.
  * x             [total_tokens][x_stride] (dtype).
  * ab            [total_tokens][ab_stride] (dtype): a in columns 0 .. channels-1, b in the next ones.
- * y             [total_tokens][y_stride] (dtype; may not be x or ab).
+ * y             [total_tokens][y_stride] (dtype). Here and in the calls below an output may not
+ *               overlap an input or another output; columns of its own in a buffer that it shares
+ *               with them (rows at the same stride) are fine.
  * saved         NULL, or la_gated_scan_saved_bytes(...) bytes (16-byte aligned) that receive what
  *               the backward pass needs besides x and ab: the state every few tokens, and the
  *               states that the streams started from.
@@ -392,7 +394,7 @@ int la_gated_scan(const uint64_t *h_state_ptrs, const void *x, const void *ab, v
  * dh_final_ptrs DEVICE array of B pointers to fp32 [channels] gradients of the final states (read),
  *               or NULL for zero.
  * dx            [total_tokens][dx_stride] (dtype), out. dab [total_tokens][dab_stride] (dtype; da and
- *               db in the columns of a and b), out. Neither may be an input.
+ *               db in the columns of a and b), out.
  * dh0_ptrs      DEVICE array of B pointers to fp32 [channels] gradients of the initial states (out;
  *               no buffer of dh_final_ptrs), or NULL. A zero-length stream's dh0 is its dh_final.
  * workspace, errors and counts as for la_gated_scan. The same inputs give the same bits. */
@@ -411,7 +413,7 @@ int la_gated_scan_backward(const void *x, const void *ab, const void *saved, siz
  * conv_bias are not read); 1..4 as for la_conv1d_silu_prefill.
  * conv_state_ptrs, h_state_ptrs  DEVICE arrays of B pointers to [conv_kernel-1][channels] (dtype) and
  * [channels] (fp32) states, 16-byte aligned, advanced in place; no two streams share one.
- * x [B][x_stride], ab [B][ab_stride], y [B][y_stride] (y may not be x or ab).
+ * x [B][x_stride], ab [B][ab_stride], y [B][y_stride].
  * Count rule: 1 <= B <= max_streams. */
 int la_gated_scan_step(const uint64_t *conv_state_ptrs, const uint64_t *h_state_ptrs, const void *x,
                        const void *ab, const void *conv_w, const void *conv_bias, int conv_kernel,
@@ -426,7 +428,7 @@ int la_gated_scan_step(const uint64_t *conv_state_ptrs, const uint64_t *h_state_
  * x, w, bias        as in the forward call; dout [total_tokens][dout_stride] (dtype).
  * dstate_final_ptrs DEVICE array of B pointers to [kernel-1][channels] (dtype) gradients of the
  *                   states that the forward call left (read), or NULL for zero.
- * dx                [total_tokens][dx_stride] (dtype), out; may not be x or dout.
+ * dx                [total_tokens][dx_stride] (dtype), out.
  * dw, dbias         fp32 [channels][kernel] and [channels], out (16-byte aligned); summed in a fixed
  *                   order, so the same inputs give the same bits. dbias may be NULL.
  * dstate_ptrs       DEVICE array of B pointers to [kernel-1][channels] (dtype) gradients of the

@@ -180,6 +180,26 @@ int packed_common(const int32_t *cu_seqlens, int B, int total_tokens, int max_to
     return check_channels(channels, dtype);
 }
 
+// Rows of a matrix in memory, in bytes.
+struct Rows {
+    const void *p;
+    int64_t rows, width, stride;
+};
+Rows rows_of(const void *p, int64_t rows, int64_t cols, int64_t stride, int dtype) {
+    const int64_t e = dtype == LA_BF16 ? 2 : 4;
+    return Rows{p, rows, cols * e, stride * e};
+}
+// Whether two matrices may share memory: not where one ends before the other begins, nor where they are
+// different columns of one buffer (rows at the same stride; a single row goes with any).
+bool overlap(const Rows &a, const Rows &b) {
+    const uintptr_t pa = reinterpret_cast<uintptr_t>(a.p), pb = reinterpret_cast<uintptr_t>(b.p);
+    if (pa + (a.rows - 1) * a.stride + a.width <= pb || pb + (b.rows - 1) * b.stride + b.width <= pa) return false;
+    const int64_t stride = a.rows > 1 ? a.stride : b.stride;
+    if ((a.rows > 1 && b.rows > 1 && a.stride != b.stride) || (a.rows == 1 && b.rows == 1)) return true;
+    const int64_t at = pb >= pa ? (int64_t)((pb - pa) % stride) : (stride - (int64_t)((pa - pb) % stride)) % stride;
+    return at < a.width || at + b.width > stride;  // b's place in a's rows
+}
+
 int check_bytes(size_t bytes, size_t need, const char *name) {
     if (bytes < need)
         return fail(LA_ERR_ARG, "%s of %zu bytes is below the %zu required", name, bytes, need);
@@ -744,7 +764,10 @@ int la_gated_scan(const uint64_t *h_state_ptrs, const void *x, const void *ab, v
     LA_TRY(check_stride(x_stride, channels, dtype, "x_stride"));
     LA_TRY(check_stride(ab_stride, 2 * (int64_t)channels, dtype, "ab_stride"));
     LA_TRY(check_stride(y_stride, channels, dtype, "y_stride"));
-    if (y == x || y == ab) return fail(LA_ERR_ARG, "y may not alias x or ab");
+    const Rows out = rows_of(y, total_tokens, channels, y_stride, dtype);
+    if (overlap(out, rows_of(x, total_tokens, channels, x_stride, dtype)) ||
+        overlap(out, rows_of(ab, total_tokens, 2 * (int64_t)channels, ab_stride, dtype)))
+        return fail(LA_ERR_ARG, "y may not alias x or ab");
     if (saved) LA_TRY(check_bytes(saved_bytes, la_gated_scan_saved_bytes(B, total_tokens, channels, dtype), "saved"));
     LA_TRY(check_workspace(workspace, workspace_bytes,
                            la_gated_scan_workspace_bytes(B, total_tokens, channels, dtype)));
@@ -779,10 +802,15 @@ int la_gated_scan_backward(const void *x, const void *ab, const void *saved, siz
     LA_TRY(check_stride(dy_stride, channels, dtype, "dy_stride"));
     LA_TRY(check_stride(dx_stride, channels, dtype, "dx_stride"));
     LA_TRY(check_stride(dab_stride, 2 * (int64_t)channels, dtype, "dab_stride"));
-    for (const void *out : {static_cast<const void *>(dx), static_cast<const void *>(dab)})
-        if (out == x || out == ab || out == dy || out == saved)
+    const int64_t need = (int64_t)la_gated_scan_saved_bytes(B, total_tokens, channels, dtype);
+    const Rows outs[2] = {rows_of(dx, total_tokens, channels, dx_stride, dtype),
+                          rows_of(dab, total_tokens, 2 * (int64_t)channels, dab_stride, dtype)};
+    for (const Rows &out : outs)
+        if (overlap(out, rows_of(x, total_tokens, channels, x_stride, dtype)) ||
+            overlap(out, rows_of(ab, total_tokens, 2 * (int64_t)channels, ab_stride, dtype)) ||
+            overlap(out, rows_of(dy, total_tokens, channels, dy_stride, dtype)) || overlap(out, Rows{saved, 1, need, need}))
             return fail(LA_ERR_ARG, "dx and dab may not alias an input");
-    if (dx == dab) return fail(LA_ERR_ARG, "dx may not alias dab");
+    if (overlap(outs[0], outs[1])) return fail(LA_ERR_ARG, "dx may not alias dab");
     if (dh0_ptrs && dh0_ptrs == dh_final_ptrs)
         return fail(LA_ERR_ARG, "dh0_ptrs may not be dh_final_ptrs");
     LA_TRY(check_bytes(saved_bytes, la_gated_scan_saved_bytes(B, total_tokens, channels, dtype), "saved"));
@@ -825,7 +853,10 @@ int la_gated_scan_step(const uint64_t *conv_state_ptrs, const uint64_t *h_state_
     LA_TRY(check_stride(x_stride, channels, dtype, "x_stride"));
     LA_TRY(check_stride(ab_stride, 2 * (int64_t)channels, dtype, "ab_stride"));
     LA_TRY(check_stride(y_stride, channels, dtype, "y_stride"));
-    if (y == x || y == ab) return fail(LA_ERR_ARG, "y may not alias x or ab");
+    const Rows out = rows_of(y, B, channels, y_stride, dtype);
+    if (overlap(out, rows_of(x, B, channels, x_stride, dtype)) ||
+        overlap(out, rows_of(ab, B, 2 * (int64_t)channels, ab_stride, dtype)))
+        return fail(LA_ERR_ARG, "y may not alias x or ab");
     la::GatedStepArgs a{conv_state_ptrs, h_state_ptrs, x, ab, conv_w, conv_bias, conv_kernel, y, B,
                         channels, x_stride, ab_stride, y_stride, dtype};
     return launch_result([&] { return la::launch_gated_step(a, as_stream(stream)); }, "gated step launch");
@@ -853,7 +884,10 @@ int la_conv1d_silu_backward(const uint64_t *conv_state_ptrs, const void *x, cons
     LA_TRY(check_act_ptr(dw, "dw"));
     LA_TRY(check_act_ptr(dbias, "dbias", true));
     if (kernel > 1 && !conv_state_ptrs) return fail(LA_ERR_ARG, "conv_state_ptrs is NULL");
-    if (dx == dout) return fail(LA_ERR_ARG, "dx may not alias dout");
+    const Rows out = rows_of(dx, total_tokens, channels, dx_stride, dtype);
+    if (overlap(out, rows_of(x, total_tokens, channels, x_stride, dtype)) ||
+        overlap(out, rows_of(dout, total_tokens, channels, dout_stride, dtype)))
+        return fail(LA_ERR_ARG, "dx may not alias x or dout");
     if (dstate_ptrs && dstate_ptrs == dstate_final_ptrs)
         return fail(LA_ERR_ARG, "dstate_ptrs may not be dstate_final_ptrs");
     LA_TRY(check_workspace(workspace, workspace_bytes,
