@@ -451,7 +451,8 @@ int la_conv1d_silu_backward(const uint64_t *conv_state_ptrs, const void *x, cons
  * Projections of a few tokens with 4-bit weights: y[m][n] = sum_k x[m][k] W[n][k],
  *   W[n][k] = scales[n][k / group] (q(n, k) - 8),   q(n, k) in 0..15.
  * The decoding counterpart of la_gemm_bf16 ("split_prefill.rs", prefill_phase1_proj_batched).
- * x, y    bf16 [M][ldx], [M][ldy]; x and ldx aligned to 16 bytes; y may not overlap x.
+ * x, y    bf16 [M][ldx], [M][ldy]; x and ldx aligned to 16 bytes; y may not overlap x (as
+ *         above: columns of its own beside x in one buffer are fine).
  * q       [N][K/2] bytes, contiguous, 16-byte aligned: eight weights of a row to a little-endian
  *         32-bit word, weight 2i in bits 4i..4i+3 and weight 2i+1 in bits 16+4i..16+4i+3.
  * scales  bf16 [N][K/group], contiguous, 16-byte aligned.

@@ -916,9 +916,8 @@ int la_w4_matvec(const void *x, const void *q, const void *scales, void *y, int 
     if (!y || (reinterpret_cast<uintptr_t>(y) & 1u)) return fail(LA_ERR_ARG, "y is NULL or misaligned");
     LA_TRY(check_stride(ldx, K, LA_BF16, "ldx"));
     if (ldy < N) return fail(LA_ERR_ARG, "ldy (%lld) is smaller than N (%d)", (long long)ldy, N);
-    const char *xb = static_cast<const char *>(x), *xe = xb + ((M - 1) * ldx + K) * 2;
-    const char *yb = static_cast<const char *>(y), *ye = yb + ((M - 1) * ldy + N) * 2;
-    if (xb < ye && yb < xe) return fail(LA_ERR_ARG, "y may not overlap x");
+    if (overlap(rows_of(x, M, K, ldx, LA_BF16), rows_of(y, M, N, ldy, LA_BF16)))
+        return fail(LA_ERR_ARG, "y may not overlap x");
     la::W4Args a{x, q, scales, y, M, N, K, group, ldx, ldy};
     return launch_result([&] { return la::launch_w4_matvec(a, as_stream(stream)); }, "w4 matvec launch");
 }

@@ -70,3 +70,14 @@ def test_conv_backward(lib):  # noqa: F811
         assert all(conv(lib, dx=p) == ARG for p in hit) and conv(lib, dx=miss[0]) == CUDA
     assert conv(lib, x=A, dout=A + 128, dx=A + 256, xs=192, dos=192, dxs=192) == CUDA
     assert conv(lib, x=A, dout=A + 128, dx=A + 240, xs=192, dos=192, dxs=192) == ARG
+
+
+def test_products(lib):  # noqa: F811
+    side = dict(M=4, N=10, K=256, ldx=272, ldy=272)
+    assert matvec(lib, x=A, y=A + 512, **side) == CUDA  # x | y in rows of 272
+    assert matvec(lib, x=A + 32, y=A, **side) == CUDA   # y | x: ten outputs of two bytes before x
+    assert matvec(lib, x=A, y=A + 510, **side) == ARG and matvec(lib, x=A, y=A + 526, **side) == ARG
+    assert matvec(lib, x=A + 16, y=A, **side) == ARG
+    assert matvec(lib, x=A, y=A + 512, **{**side, "ldy": 280}) == ARG
+    assert matvec(lib, x=A, y=A + 512, M=1, N=10, K=256, ldx=256, ldy=10) == CUDA
+    assert matvec(lib, x=A, y=A + 510, M=1, N=10, K=256, ldx=256, ldy=10) == ARG

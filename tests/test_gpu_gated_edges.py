@@ -7,6 +7,7 @@ import numpy as np
 import pytest
 import torch
 
+import linear_attention_chunked_conv1d_gb300 as la
 from tests.helpers import f64
 from tests.test_gpu_gated_scan import backward, close, forward, gpu_pass, make
 
@@ -77,3 +78,21 @@ def test_gates_that_are_nan_stay_in_their_stream(cuda, dtype):
         if s in bad:
             assert bool(torch.isnan(got[0][rows, :8]).all())
             assert bool(torch.isfinite(got[0][rows, 8:16]).all())
+
+
+@pytest.mark.parametrize("M", [1, 7, 32])
+def test_products_into_columns_beside_their_rows(cuda, M):
+    """x | gap | y in one wide buffer: the products are those into a tensor of their own, the rest stays."""
+    N, K = 200, 256
+    g = torch.Generator().manual_seed(43)
+    r = lambda *s: torch.randn(*s, generator=g).to(torch.bfloat16).to(cuda)  # noqa: E731
+    q, s = la.w4_quantize((r(N, K) / 16).contiguous(), group=64)
+    wide = torch.full((M, K + N + 32), 5.0, dtype=torch.bfloat16, device=cuda)
+    x, y = wide[:, :K], wide[:, K + 16:K + 16 + N]
+    x.copy_(r(M, K))
+    want = la.w4_matvec(x.contiguous(), q, s)
+    before = x.clone()
+    la.w4_matvec(x, q, s, y)
+    torch.cuda.synchronize()
+    assert torch.equal(y, want) and torch.equal(x, before)
+    assert torch.all(wide[:, K:K + 16] == 5.0) and torch.all(wide[:, K + 16 + N:] == 5.0)
