@@ -155,15 +155,16 @@ class DecodeStep:
 
 
 def project(y, w, out=None, stream=None):
-    """y W^T for a linear layer's weight: bf16 [out][in], or the (q, scales) of w4_quantize (then at
-    most LA_W4_MAX_ROWS rows)."""
-    if isinstance(w, tuple):
-        return w4_matvec(y, *w, out, stream=stream)
-    return gemm_bf16(y, w, out, stream=stream)
+    """y W^T for a linear layer's weight: bf16 [out][in], or the pair (q, scales) of w4_quantize (then
+    at most LA_W4_MAX_ROWS rows)."""
+    if isinstance(w, torch.Tensor):
+        return gemm_bf16(y, w, out, stream=stream)
+    q, scales = w
+    return w4_matvec(y, q, scales, out, stream=stream)
 
 
 def _outputs(w) -> int:
-    return (w[0] if isinstance(w, tuple) else w).shape[0]
+    return (w if isinstance(w, torch.Tensor) else w[0]).shape[0]
 
 
 class Phase1:
