@@ -19,7 +19,7 @@ import math
 
 import torch
 
-from . import (conv1d_silu_backward, conv1d_silu_backward_workspace_bytes, conv1d_silu_l2_prefill,
+from . import (LA_W4_MAX_ROWS, conv1d_silu_backward, conv1d_silu_backward_workspace_bytes, conv1d_silu_l2_prefill,
                conv1d_silu_prefill, conv1d_silu_prefill_varlen, decode_step,
                decode_workspace_bytes, gate_activations, gated_scan, gated_scan_backward,
                gated_scan_saved_bytes, gated_scan_step, gated_scan_workspace_bytes,
@@ -321,12 +321,15 @@ class GatedPass:
 class GatedDecode:
     """Decode steps of a gated recurrent layer for B streams (one token each): row RMSNorm, one
     projection to x | a | b (3C outputs; bf16 weight or the 4-bit (q, scales) of w4_quantize),
-    conv1d + SiLU and the gated recurrence on the carried states, the projection back (w_out)."""
+    conv1d + SiLU and the gated recurrence on the carried states, the projection back (w_out). With a
+    4-bit weight B is at most LA_W4_MAX_ROWS: more streams take several objects, or bf16 weights."""
 
     def __init__(self, norm_w, w_in, w_out, conv_w, conv_bias, conv_state, h, *, eps=1e-6):
         self.norm_w, self.w_in, self.w_out, self.eps = norm_w, w_in, w_out, eps
         self.conv_w, self.conv_bias = conv_w, conv_bias
         self.B, self.C = h.shape
+        if self.B > LA_W4_MAX_ROWS and not all(isinstance(w, torch.Tensor) for w in (w_in, w_out)):
+            raise ValueError(f"{self.B} streams: 4-bit weights take at most {LA_W4_MAX_ROWS} rows")
         dev, bf16 = h.device, torch.bfloat16
         self.conv_ptrs = pointer_array(list(conv_state)) if conv_w.shape[1] > 1 else None
         self.h_ptrs = pointer_array(list(h))

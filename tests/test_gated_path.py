@@ -30,3 +30,22 @@ def test_a_pair_is_a_4_bit_weight_whatever_holds_it(calls, kind):
     assert [n for n, _ in calls] == ["w4_matvec", "gemm_bf16"]
     assert calls[0][1][1] is w[0] and calls[0][1][2] is w[1]
     assert path._outputs(w) == 24 and path._outputs(torch.zeros(7, 64)) == 7
+
+
+def decode(B=3, C=16, D=64, K=4, **kw):
+    a = dict(norm_w=torch.zeros(D, dtype=BF), w_in=torch.zeros(3 * C, D, dtype=BF), w_out=torch.zeros(D, C, dtype=BF),
+             conv_w=torch.zeros(C, K, dtype=BF), conv_bias=torch.zeros(C, dtype=BF),
+             conv_state=torch.zeros(B, K - 1, C, dtype=BF), h=torch.zeros(B, C))
+    a.update(kw)
+    return path.GatedDecode(**a)
+
+
+def test_decode_refuses_more_streams_than_4_bit_rows_when_it_is_made(calls):
+    C, D = 32, 64
+    most = path.LA_W4_MAX_ROWS
+    four = dict(w_in=quantized(3 * C, D), w_out=quantized(D, C))
+    decode(B=most, C=C, D=D, **four)
+    decode(B=most + 1, C=C, D=D)  # bf16 weights: any number
+    for given in (four, dict(w_in=four["w_in"]), dict(w_out=four["w_out"])):
+        with pytest.raises(ValueError, match="33 streams"):
+            decode(B=most + 1, C=C, D=D, **given)
