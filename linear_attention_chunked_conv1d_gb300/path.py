@@ -255,13 +255,25 @@ class StreamedPrefill:
         self.compute.wait_event(self.drained[1])
 
 
+def _fits(name, t, shape, dtype, dev, *, rows=False):
+    """Refuses a tensor that a gated layer's kernels would read or write past or misread. rows: the first
+    dimension may have any stride of whole 16 bytes; the rest is dense."""
+    if tuple(t.shape) != tuple(shape) or t.dtype != dtype or t.device != dev:
+        raise ValueError(f"{name}: {tuple(t.shape)} {t.dtype} on {t.device}, expected {tuple(shape)} {dtype} on {dev}")
+    dense = t[0] if rows and t.shape[0] else t
+    if not dense.is_contiguous() or t.data_ptr() % 16 or (dense is not t and t.shape[0] > 1
+                                                          and t.stride(0) * t.element_size() % 16):
+        raise ValueError(f"{name}: strides {t.stride()} at {t.data_ptr():#x}, expected dense "
+                         f"{'rows' if rows else 'values'} on 16-byte boundaries")
+
+
 class GatedPass:
     """Repeated passes of a gated recurrent layer (one state per channel) over one packed batch:
     conv1d + SiLU over the carried windows, then the gated scan from the carried states.
 
     `inputs` holds device tensors: x [T][C] (before the conv) and ab [T][2C] (gate rows a | b),
-    conv_w [C][K], conv_bias [C] or None, conv_state [B][K-1][C], h [B][C] (fp32, both contiguous),
-    cu_seqlens.
+    conv_w [C][K], conv_bias [C] or None, conv_state [B][K-1][C], h [B][C] (fp32; each stream's state
+    dense), cu_seqlens [B+1] (int32).
     forward() advances both states; with train=True it also keeps what backward() needs: the
     conv states as they were, and the scan's saved states. Outputs and gradients are the pass's own
     tensors, written again by the next call."""
@@ -270,7 +282,15 @@ class GatedPass:
         self.inp, self.train = inputs, train
         x, h, conv_state = inputs["x"], inputs["h"], inputs["conv_state"]
         (T, C), B, dev = x.shape, h.shape[0], x.device
-        K = inputs["conv_w"].shape[1]
+        K, dt = inputs["conv_w"].shape[1], x.dtype
+        _fits("x", x, (T, C), dt, dev, rows=True)
+        _fits("ab", inputs["ab"], (T, 2 * C), dt, dev, rows=True)
+        _fits("conv_w", inputs["conv_w"], (C, K), dt, dev)
+        if inputs["conv_bias"] is not None:
+            _fits("conv_bias", inputs["conv_bias"], (C,), dt, dev)
+        _fits("conv_state", conv_state, (B, K - 1, C), dt, dev, rows=True)
+        _fits("h", h, (B, C), torch.float32, dev, rows=True)
+        _fits("cu_seqlens", inputs["cu_seqlens"], (B + 1,), torch.int32, dev)
         self.u, self.y = torch.empty_like(x), torch.empty_like(x)
         self.h_ptrs = pointer_array(list(h))
         self.conv_ptrs = pointer_array(list(conv_state)) if K > 1 else None
@@ -331,6 +351,18 @@ class GatedDecode:
         if self.B > LA_W4_MAX_ROWS and not all(isinstance(w, torch.Tensor) for w in (w_in, w_out)):
             raise ValueError(f"{self.B} streams: 4-bit weights take at most {LA_W4_MAX_ROWS} rows")
         dev, bf16 = h.device, torch.bfloat16
+        D, K = norm_w.numel(), conv_w.shape[1]
+        _fits("norm_w", norm_w, (D,), bf16, dev)
+        _fits("conv_w", conv_w, (self.C, K), bf16, dev)
+        if conv_bias is not None:
+            _fits("conv_bias", conv_bias, (self.C,), bf16, dev)
+        _fits("conv_state", conv_state, (self.B, K - 1, self.C), bf16, dev, rows=True)
+        _fits("h", h, (self.B, self.C), torch.float32, dev, rows=True)
+        for name, w, outputs, inputs in (("w_in", w_in, 3 * self.C, D), ("w_out", w_out, None, self.C)):
+            if isinstance(w, torch.Tensor):
+                _fits(name, w, (outputs or w.shape[0], inputs), bf16, dev, rows=True)
+            elif (w[0].shape[0], 2 * w[0].shape[1]) != (outputs or w[0].shape[0], inputs):
+                raise ValueError(f"{name}: 4-bit weight of {w[0].shape[0]} x {2 * w[0].shape[1]}, expected {outputs} x {inputs}")
         self.conv_ptrs = pointer_array(list(conv_state)) if conv_w.shape[1] > 1 else None
         self.h_ptrs = pointer_array(list(h))
         self.normed = torch.empty(self.B, norm_w.numel(), dtype=bf16, device=dev)
@@ -339,6 +371,10 @@ class GatedDecode:
         self.out = torch.empty(self.B, _outputs(w_out), dtype=bf16, device=dev)
 
     def run(self, hidden, stream=None):
+        if (hidden.shape != self.normed.shape or hidden.dtype != self.normed.dtype
+                or hidden.device != self.normed.device or hidden.stride(1) != 1):
+            raise ValueError(f"hidden: {tuple(hidden.shape)} {hidden.dtype} on {hidden.device}, expected dense rows of "
+                             f"{tuple(self.normed.shape)} {self.normed.dtype} on {self.normed.device}")
         rmsnorm_rows(hidden, self.norm_w, self.normed, eps=self.eps, stream=stream)
         project(self.normed, self.w_in, self.rows, stream=stream)
         gated_scan_step(self.h_ptrs, self.rows[:, :self.C], self.rows[:, self.C:], self.y,
