@@ -296,6 +296,7 @@ class GatedPass:
         self.conv_ptrs = pointer_array(list(conv_state)) if K > 1 else None
         room = lambda n: torch.empty(n, dtype=torch.uint8, device=dev)  # noqa: E731
         self.workspace = room(gated_scan_workspace_bytes(B, T, C, x.dtype))
+        self.forwarded = False
         if train:
             self.saved = room(gated_scan_saved_bytes(B, T, C, x.dtype))
             self.conv_workspace = room(conv1d_silu_backward_workspace_bytes(B, T, C, K, x.dtype))
@@ -319,6 +320,7 @@ class GatedPass:
                                    bias=inp["conv_bias"], stream=stream)
         gated_scan(self.h_ptrs, self.u, inp["ab"], self.y, inp["cu_seqlens"],
                    saved=self.saved if self.train else None, workspace=self.workspace, stream=stream)
+        self.forwarded = True
         return self.y
 
     def backward(self, dy, *, dh_final_ptrs=None, dconv_final_ptrs=None, stream=None):
@@ -327,6 +329,8 @@ class GatedPass:
         gated_scan_backward and conv1d_silu_backward take them)."""
         if not self.train:
             raise RuntimeError("backward() needs GatedPass(..., train=True)")
+        if not self.forwarded:
+            raise RuntimeError("backward() needs a forward() before it")
         inp, g = self.inp, self.grads
         gated_scan_backward(self.u, inp["ab"], self.saved, dy, self.du, g["ab"], inp["cu_seqlens"],
                             dh_final_ptrs=dh_final_ptrs, dh0_ptrs=self.dh_ptrs,

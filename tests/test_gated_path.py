@@ -105,3 +105,14 @@ def test_pass_refuses_what_does_not_fit_when_it_is_made(calls):
                 dict(cu_seqlens=torch.zeros(B, dtype=torch.int32)), dict(x=torch.zeros(C, T).t())):
         with pytest.raises(ValueError, match=next(iter(bad))):
             path.GatedPass(inputs(**bad))
+
+
+def test_backward_needs_a_forward(calls):
+    """Before it there is nothing to go back through but what the buffers happen to hold."""
+    p, dy = path.GatedPass(inputs(), train=True), torch.zeros(10, 16)
+    with pytest.raises(RuntimeError, match="forward"):
+        p.backward(dy)
+    assert not calls
+    p.forward()
+    p.backward(dy)
+    assert [n for n, _ in calls][-2:] == ["gated_scan_backward", "conv1d_silu_backward"]
