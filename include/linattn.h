@@ -376,7 +376,8 @@ int la_prefill_segmented(const uint64_t *h_state_ptrs, const void *q, const void
  * nothing of a finite x. An infinite or NaN state, x or NaN gate makes its channel NaN or infinite
  * from there to the stream's end, and no other stream or channel.
  * States and the scan are fp32; y is rounded once. LA_F32 or LA_BF16; channels and strides multiples
- * of 16 bytes. Count rule: 1 <= total_tokens <= max_tokens, and at most 2^31 - 1024.
+ * of 16 bytes. Count rule: 1 <= total_tokens <= max_tokens, and at most 2^31 - 1024; channels at most
+ * 2^31 - 1024 (conv1d_silu_backward: 65535 * 512) and B at most 2^30 - 1, below too.
  * ------------------------------------------------------------------------------------------- */
 size_t la_gated_scan_workspace_bytes(int B, int total_tokens, int channels, int dtype);
 size_t la_gated_scan_saved_bytes(int B, int total_tokens, int channels, int dtype);

@@ -153,15 +153,18 @@ int conv_common(const void *x, const void *w, const void *bias, const void *out,
     return LA_OK;
 }
 
+// The kernels of the calls below add up to a tile to a token's, channel's, output's or input's 32-bit
+// number, and two streams' numbers in their searches.
+constexpr int kMaxCount = INT_MAX - 1023;
+constexpr int kMaxStreams = INT_MAX / 2;
+
 int check_channels(int channels, int dtype) {
     if (channels <= 0) return fail(LA_ERR_ARG, "channels must be positive (got %d)", channels);
     if (channels % vec_elems(dtype))
         return fail(LA_ERR_ARG, "channels (%d) is not a multiple of 16 bytes", channels);
+    if (channels > kMaxCount) return fail(LA_ERR_COUNT, "%d channels: the most are %d", channels, kMaxCount);
     return LA_OK;
 }
-
-// The kernels of the calls below add up to a tile to a token's, output's or input's 32-bit number.
-constexpr int kMaxCount = INT_MAX - 1023;
 
 // Counts, streams and channels of the calls over packed (cu_seqlens) or equal (NULL) streams.
 int packed_common(const int32_t *cu_seqlens, int B, int total_tokens, int max_tokens, int channels,
@@ -173,6 +176,7 @@ int packed_common(const int32_t *cu_seqlens, int B, int total_tokens, int max_to
         return fail(LA_ERR_COUNT, "call of %d tokens: the most are %d", total_tokens, kMaxCount);
     LA_TRY(check_dtype(dtype));
     if (B < 1) return fail(LA_ERR_ARG, "B must be >= 1 (got %d)", B);
+    if (B > kMaxStreams) return fail(LA_ERR_COUNT, "call of %d streams: the most are %d", B, kMaxStreams);
     if (!cu_seqlens && total_tokens % B)
         return fail(LA_ERR_ARG, "cu_seqlens NULL: total_tokens (%d) is not a multiple of B (%d)",
                     total_tokens, B);
@@ -837,6 +841,7 @@ int la_gated_scan_step(const uint64_t *conv_state_ptrs, const uint64_t *h_state_
     if (B < 1 || B > max_streams)
         return fail(LA_ERR_COUNT, "decode step of %d streams does not fit max_streams %d", B,
                     max_streams);
+    if (B > kMaxStreams) return fail(LA_ERR_COUNT, "decode step of %d streams: the most are %d", B, kMaxStreams);
     LA_TRY(check_dtype(dtype));
     if (conv_kernel < 0 || conv_kernel > 4)
         return fail(LA_ERR_UNSUPPORTED, "conv kernel %d outside the compiled 0..4", conv_kernel);
@@ -878,6 +883,8 @@ int la_conv1d_silu_backward(const uint64_t *conv_state_ptrs, const void *x, cons
     int T_each = 0;
     LA_TRY(packed_common(cu_seqlens, B, total_tokens, max_tokens, channels, dtype, &T_each));
     LA_TRY(conv_common(x, w, bias, dx, channels, kernel, x_stride, dx_stride, dtype));
+    if (channels > la::conv_backward_max_channels())
+        return fail(LA_ERR_COUNT, "%d channels: the most are %d", channels, la::conv_backward_max_channels());
     LA_TRY(check_act_ptr(w, "w"));
     LA_TRY(check_act_ptr(dout, "dout"));
     LA_TRY(check_stride(dout_stride, channels, dtype, "dout_stride"));

@@ -258,6 +258,8 @@ cudaError_t launch_k(const ConvBwdArgs &a, cudaStream_t st) {
 
 }  // namespace
 
+int conv_backward_max_channels() { return 65535 * 4 * kThreads; }  // blocks along a grid's y
+
 size_t conv_backward_workspace_bytes(int B, int total, int channels, int kernel, int) {
     // streams of equal lengths have no more runs than packed ones
     return ((size_t)total / run_rows(B, total, channels) + B) * (kernel + 1) * channels * sizeof(float);

@@ -220,6 +220,7 @@ struct ConvBwdArgs {
     void *workspace;
     int *status;
 };
+int conv_backward_max_channels();
 size_t conv_backward_workspace_bytes(int B, int total, int channels, int kernel, int dtype);
 cudaError_t launch_conv1d_silu_backward(const ConvBwdArgs &a, cudaStream_t st);
 
