@@ -584,7 +584,7 @@ def gated_scan_step(h_state_ptrs, x, ab, y, *, conv_state_ptrs=None, conv_w=None
             and h_state_ptrs is not None and h_state_ptrs.dtype is torch.int64
             and h_state_ptrs.numel() == B and h_state_ptrs.get_device() == dev
             and h_state_ptrs.is_contiguous()
-            and (K == 0 or (conv_w.dtype is dt and conv_w.shape[0] == C and conv_w.is_contiguous()
+            and (conv_w is None or (K > 0 and conv_w.dtype is dt and conv_w.shape[0] == C and conv_w.is_contiguous()
                             and conv_w.get_device() == dev
                             and (K == 1 or (conv_state_ptrs is not None
                                             and conv_state_ptrs.dtype is torch.int64
@@ -601,6 +601,8 @@ def gated_scan_step(h_state_ptrs, x, ab, y, *, conv_state_ptrs=None, conv_w=None
         _ptrs("h_state_ptrs", h_state_ptrs, B, dev)
         _ptrs("conv_state_ptrs", conv_state_ptrs, B, dev)
         if conv_w is not None:
+            if K == 0:
+                raise ValueError("conv_w has no taps: leave it out for a layer without a convolution")
             _dense("conv_w", conv_w, (C, K), dt, dev)
             if conv_bias is not None:
                 _dense("conv_bias", conv_bias, (C,), dt, dev)

@@ -96,3 +96,18 @@ def test_products_into_columns_beside_their_rows(cuda, M):
     torch.cuda.synchronize()
     assert torch.equal(y, want) and torch.equal(x, before)
     assert torch.all(wide[:, K:K + 16] == 5.0) and torch.all(wide[:, K + 16 + N:] == 5.0)
+
+
+def test_step_refuses_taps_that_are_none(cuda):
+    """conv_w [C][0] is no layer without a convolution: x would have entered without bias and SiLU."""
+    B, C = 2, 16
+    bf = dict(dtype=torch.bfloat16, device=cuda)
+    h, y = torch.zeros(B, C, device=cuda), torch.full((B, C), 5.0, **bf)
+    args = la.pointer_array(list(h)), torch.zeros(B, C, **bf), torch.zeros(B, 2 * C, **bf), y
+    with pytest.raises(ValueError, match="taps"):
+        la.gated_scan_step(*args, conv_w=torch.zeros(C, 0, **bf), conv_bias=torch.zeros(C, **bf))
+    torch.cuda.synchronize()
+    assert torch.all(y == 5.0)
+    la.gated_scan_step(*args)
+    torch.cuda.synchronize()
+    assert torch.all(y == 0.0)
