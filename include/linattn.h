@@ -457,7 +457,8 @@ int la_conv1d_silu_backward(const uint64_t *conv_state_ptrs, const void *x, cons
  * q       [N][K/2] bytes, contiguous, 16-byte aligned: eight weights of a row to a little-endian
  *         32-bit word, weight 2i in bits 4i..4i+3 and weight 2i+1 in bits 16+4i..16+4i+3.
  * scales  bf16 [N][K/group], contiguous, 16-byte aligned.
- * group   32, 64 or 128; K a multiple of it. Sums are fp32, y is rounded once, and the order of the
+ * group   32, 64 or 128; K a multiple of it. Sums are fp32 (a group's of x (q - 8) / 64 before its
+ *         scale: |x| under 2^123 cannot pass its range), y is rounded once, and the order of the
  *         sums does not depend on M: a row gives the same bits in any batch.
  * Count rule: 1 <= M <= LA_W4_MAX_ROWS; 1 <= N, K <= 2^31 - 1024. */
 #define LA_W4_MAX_ROWS 32

@@ -39,12 +39,17 @@ template <typename T> __device__ __forceinline__ void copy_row(void *to, const T
 
 // Tokens of a run: long ones read and write less for what runs share (K-1 rows at each end, the sums),
 // short ones make more blocks. The longest that still makes 1000 blocks (152 SMs have 608 at a time; a
-// fixed number of SMs, so that sums do not depend on the device). bf16, K = 4, runs of 384, 256, 192, 128
-// and 64 (*: taken), us:
-//   16384 x 6144, 8 streams    134  135 *126  131  140
-//   16384 x 4096, 8 streams    104   95  102  *93  101
-//   65536 x 2048, 32 streams   188 *173  175  180  205
-//   100003 x 8192, 32 streams *860  869  887  912 1028
+// fixed number of SMs, so that sums do not depend on the device). K = 4, runs of 384, 256, 192, 128, 96 and
+// 64 (*: taken), us:
+//   16384 x 6144, 8 streams, bf16    136  137 *127  133  136  143
+//   16384 x 4096, 8 streams, bf16    105   96  103  *92   98  102
+//   65536 x 2048, 32 streams, bf16   192 *176  177  183  190  208
+//   100003 x 8192, 32 streams, bf16 *861  869  890  914  949 1030
+//   8192 x 8192, 4 streams, bf16     104   95  101  *89   95   97
+//   32768 x 1024, 16 streams, bf16    77   58   61   59   64  *69
+//   16384 x 4096, 4 streams, fp32    151  151  144 *135  140  141
+//   40001 x 2000, 33 streams, fp32   203  179  175 *177  178  187
+// The best or within 2% of it, but for the few channels of 32768 x 1024, where longer runs are 20% better.
 __host__ __device__ inline int run_rows(int B, int total, int channels) {
     const int64_t cols = (channels / 4 + kThreads - 1) / kThreads;
     const auto blocks = [&](int rows) { return (total / rows + B) * cols; };

@@ -32,11 +32,12 @@
 //  - Blocks are persistent. Tiles come by TMA into a ring in shared memory and are worked on in
 //    registers, so a tile's place in the ring is free again, and the next copy under way, while the
 //    tile waits for its state.
-//  - Instructions are the next bound after HBM, and of these the special function unit's: channels go
-//    in packed pairs, and tiles without a start or an end of a stream (all but one in each stream)
+//  - To keep the instructions few (29 a (token, channel) forward, 65 backward) channels go in packed
+//    pairs, and tiles without a start or an end of a stream (all but one in each stream)
 //    take a path without tests for them.
-// Measured, bf16: 262,144 x 2048 in 64 streams 0.78 ms (5.5 TB/s of what has to move), one stream 65,536 x
-// 2048 0.235 ms (4.6 TB/s: it waits for its chains), both passes of 8 x 2048 x 4096 0.339 ms (4.3 TB/s).
+// Measured, bf16: 262,144 x 2048 in 64 streams 0.79 ms (5.4 TB/s of what has to move), one stream 65,536 x
+// 2048 0.237 ms (4.5 TB/s: it waits for its chains), both passes of 8 x 2048 x 4096 0.348 ms (4.2 TB/s: the
+// backward pass waits at its tiles' two barriers, 45% of its issue slots are used).
 #include <cuda.h>
 
 #include <type_traits>
