@@ -111,3 +111,27 @@ def test_step_refuses_taps_that_are_none(cuda):
     la.gated_scan_step(*args)
     torch.cuda.synchronize()
     assert torch.all(y == 0.0)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_nan_of_every_bit_set(cuda, dtype):
+    """The pattern by which a chain's word says that nobody has written it is a NaN, too: in states, inputs, gates
+    and gradients it comes out as a NaN, and no tile waits for it."""
+    lengths, C = [900, 256, 700], 72
+    inp = make(lengths, C, dtype, seed=44)
+    clean = gpu_pass(cuda, inp, lengths)
+    bits = torch.int32 if dtype == "f32" else torch.int16
+    chans = {"x": slice(0, 8), "h": slice(8, 16), "ab": slice(16, 24), "dy": slice(24, 32), "dfinal": slice(32, 40)}
+    for n, at in chans.items():
+        v = inp[n]
+        v[(slice(3, 4) if n in ("x", "ab") else slice(890, 891) if n == "dy" else slice(0, 1)), at] = float("nan")
+        v.view(torch.int32 if v.dtype == torch.float32 else bits)[torch.isnan(v)] = -1
+    y, h, dx, dab, dh0 = gpu_pass(cuda, inp, lengths)  # la_device_status() is 0
+    for at in (chans["x"], chans["h"], chans["ab"]):
+        assert bool(torch.isnan(y[3:900, at]).all()) and bool(torch.isnan(h[0, at]).all())
+    for at in (chans["dy"], chans["dfinal"]):
+        assert bool(torch.isnan(dx[:890, at]).all()) and bool(torch.isnan(dh0[0, at]).all())
+    rest = slice(40, C)
+    for got, want in zip((y, h, dx, dh0), (clean[0], clean[1], clean[2], clean[4])):
+        assert torch.equal(got[:, rest], want[:, rest])
+    assert torch.equal(y[900:], clean[0][900:]) and torch.equal(dx[900:], clean[2][900:])
