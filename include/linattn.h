@@ -471,6 +471,101 @@ int la_w4_matvec(const void *x, const void *q, const void *scales, void *y, int 
 int la_w4_quantize(const void *w, void *q, void *scales, int N, int K, int group, int64_t ldw,
                    uint64_t stream);
 
+/* ---------------------------------------------------------------------------------------------
+ * The dense half of a layer: layer norm, products with bias, activation and residual, the gated
+ * feed-forward block, each with its backward pass. They stand beside la_rmsnorm_rows and la_gemm_bf16
+ * ("split_prefill.rs", prefill_phase1_proj_batched); the pages have none of them.
+ *
+ * Shared by these calls: a matrix has dense rows at a stride that is a multiple of 16 bytes and starts on
+ * 16 bytes; any number of columns is fine, and what lies between a row's end and the next row is neither
+ * read nor written. An output may overlap no input and no other output, where nothing else is said;
+ * columns of its own in a buffer that it shares with them (rows at the same stride) are fine. Every
+ * result is summed in a fixed order: the same call on the same inputs gives the same bits. Infinities
+ * and NaN go where the formulas take them, in the rows (for weights' gradients: columns) they stand in.
+ * Counts are at least 1 and at most 2^31 - 1024 (LA_ERR_COUNT).
+ * ------------------------------------------------------------------------------------------- */
+
+/* Layer norm of rows: mean = sum x / width, rstd = 1 / sqrt(sum (x - mean)^2 / width + eps),
+ *   y = (x - mean) rstd w + b.
+ * x, y    [rows][ldx], [rows][ldy] (dtype; y may be x itself, at the same stride).
+ * w, b    [width] (dtype); b may be NULL.
+ * stats   fp32 [rows][2], mean and rstd of each row, for the backward pass (16-byte aligned); or NULL.
+ * Statistics and arithmetic are fp32, y is rounded once. LA_F32 or LA_BF16; width up to 8192, any number
+ * (else LA_ERR_UNSUPPORTED). */
+int la_layernorm_rows(const void *x, const void *w, const void *b, void *y, float *stats, int rows,
+                      int width, int64_t ldx, int64_t ldy, float eps, int dtype, uint64_t stream);
+
+/* Backward pass of la_layernorm_rows. With xh = (x - mean) rstd and u = dy w:
+ *   dx = rstd (u - mean(u) - xh mean(u xh)) + dskip,  dw = sum over rows of dy xh,  db = of dy.
+ * x, w, stats  as the forward call had them and left them.
+ * dy, dx  [rows][lddy], [rows][lddx] (dtype). dx may be dy or dskip itself, at the same stride.
+ * dskip   [rows][ldskip] (dtype), a gradient that reaches x past the norm, or NULL.
+ * dw, db  fp32 [width] (16-byte aligned); db may be NULL.
+ * workspace  la_layernorm_rows_backward_workspace_bytes(...) bytes (16-byte aligned), used by this call
+ *         alone until its work is done; calls in stream order may share one. */
+size_t la_layernorm_rows_backward_workspace_bytes(int rows, int width, int dtype);
+int la_layernorm_rows_backward(const void *x, const void *w, const float *stats, const void *dy,
+                               const void *dskip, void *dx, float *dw, float *db, int rows, int width,
+                               int64_t ldx, int64_t lddy, int64_t ldskip, int64_t lddx, int dtype,
+                               void *workspace, size_t workspace_bytes, uint64_t stream);
+
+/* Activations of the two calls below. */
+#define LA_ACT_NONE 0
+#define LA_ACT_RELU 1
+#define LA_ACT_GELU 2      /* z Phi(z), Phi the normal distribution function */
+#define LA_ACT_GELU_TANH 3 /* z (1 + tanh(sqrt(2 / pi) (z + 0.044715 z^3))) / 2 */
+#define LA_ACT_SILU 4
+
+/* Product with bias, activation and residual in its epilogue: z = x W^T + bias, y = act(z) + residual.
+ * x [M][ldx], w [N][ldw] (a linear layer's [out][in] weight), residual and y [M][ldr], [M][ldy], bias [N]:
+ * bf16; bias and residual may be NULL; y may be residual itself, at the same stride.
+ * saved   la_linear_saved_bytes(...) bytes (16-byte aligned) that receive z, in bf16, for the backward
+ *         pass; or NULL. No bytes are needed with LA_ACT_NONE.
+ * Tensor cores, fp32 accumulation; y is rounded once, from z as accumulated. */
+size_t la_linear_saved_bytes(int M, int N, int act);
+int la_linear(const void *x, const void *w, const void *bias, const void *residual, void *y,
+              void *saved, size_t saved_bytes, int M, int N, int K, int64_t ldx, int64_t ldw,
+              int64_t ldr, int64_t ldy, int act, uint64_t stream);
+
+/* Backward pass of la_linear. With dz = dy act'(z):  dx = dz W,  dw = dz^T x,  dbias = sum over rows of dz.
+ * (The residual's gradient is dy.) relu's derivative is 0 at 0.
+ * x, w, saved  as the forward call had them and left them (saved may be NULL with LA_ACT_NONE).
+ * dy [M][lddy], dx [M][lddx], dw [N][lddw], dbias [N]: bf16. dx, dw and dbias may each be NULL, not all.
+ * dz is rounded to bf16 where it enters the two products (it is the tensor cores' operand), not where it
+ * is summed to dbias; dx, dw and dbias are summed in fp32 and rounded once.
+ * workspace  la_linear_backward_workspace_bytes(...) bytes (16-byte aligned; may be NULL when that is 0). */
+size_t la_linear_backward_workspace_bytes(int M, int N, int K, int act);
+int la_linear_backward(const void *x, const void *w, const void *saved, size_t saved_bytes,
+                       const void *dy, void *dx, void *dw, void *dbias, int M, int N, int K,
+                       int64_t ldx, int64_t ldw, int64_t lddy, int64_t lddx, int64_t lddw, int act,
+                       void *workspace, size_t workspace_bytes, uint64_t stream);
+
+/* Gated feed-forward block, both projections, the activation and the product in one kernel:
+ *   h = act(x Wg^T) * (x Wu^T).
+ * x [M][ldx], w_gate [F][ldwg], w_up [F][ldwu] (halves of one packed weight are fine), h [M][ldh]: bf16.
+ * (The projection back is la_linear with the residual.)
+ * saved   la_gated_ffn_saved_bytes(...) bytes (16-byte aligned) that receive both products, in bf16, for
+ *         the backward pass; or NULL.
+ * h is rounded once, from the products as accumulated (fp32). */
+size_t la_gated_ffn_saved_bytes(int M, int F);
+int la_gated_ffn(const void *x, const void *w_gate, const void *w_up, void *h, void *saved,
+                 size_t saved_bytes, int M, int F, int K, int64_t ldx, int64_t ldwg, int64_t ldwu,
+                 int64_t ldh, int act, uint64_t stream);
+
+/* Backward pass of la_gated_ffn. With gate = x Wg^T and up = x Wu^T:
+ *   dgate = dh up act'(gate),  dup = dh act(gate),
+ *   dx = dgate Wg + dup Wu,  dw_gate = dgate^T x,  dw_up = dup^T x.
+ * x, w_gate, w_up, saved  as the forward call had them and left them.
+ * dh [M][lddh], dx [M][lddx], dw_gate [F][lddwg], dw_up [F][lddwu]: bf16. dx may be NULL, and dw_gate and
+ * dw_up (both or neither), not all. dgate and dup are rounded to bf16 (the tensor cores' operands).
+ * workspace  la_gated_ffn_backward_workspace_bytes(...) bytes (16-byte aligned). */
+size_t la_gated_ffn_backward_workspace_bytes(int M, int F, int K);
+int la_gated_ffn_backward(const void *x, const void *w_gate, const void *w_up, const void *saved,
+                          size_t saved_bytes, const void *dh, void *dx, void *dw_gate, void *dw_up,
+                          int M, int F, int K, int64_t ldx, int64_t ldwg, int64_t ldwu, int64_t lddh,
+                          int64_t lddx, int64_t lddwg, int64_t lddwu, int act, void *workspace,
+                          size_t workspace_bytes, uint64_t stream);
+
 #ifdef __cplusplus
 }
 #endif

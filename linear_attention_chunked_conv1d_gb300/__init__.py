@@ -25,6 +25,10 @@ __all__ = [
     "gated_scan", "gated_scan_backward", "gated_scan_step", "gated_scan_workspace_bytes",
     "gated_scan_saved_bytes", "conv1d_silu_backward", "conv1d_silu_backward_workspace_bytes",
     "w4_matvec", "w4_quantize", "LA_W4_MAX_ROWS",
+    "layernorm_rows", "layernorm_rows_backward", "layernorm_rows_backward_workspace_bytes",
+    "linear", "linear_saved_bytes", "linear_backward", "linear_backward_workspace_bytes",
+    "gated_ffn", "gated_ffn_saved_bytes", "gated_ffn_backward",
+    "gated_ffn_backward_workspace_bytes", "LA_ACTIVATIONS",
     "pointer_array", "library_path",
 ]
 
@@ -32,6 +36,8 @@ LA_OK, LA_ERR_ARG, LA_ERR_COUNT, LA_ERR_UNSUPPORTED, LA_ERR_CUDA = 0, 1, 2, 3, 4
 LA_F32, LA_BF16 = 0, 1
 LA_DEV_BAD_SEQLENS, LA_DEV_TIMEOUT = 1, 2
 LA_W4_MAX_ROWS = 32
+# activations of linear and gated_ffn (LA_ACT_*)
+LA_ACTIVATIONS = {"none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4}
 _CODES = {LA_ERR_ARG: "LA_ERR_ARG", LA_ERR_COUNT: "LA_ERR_COUNT",
           LA_ERR_UNSUPPORTED: "LA_ERR_UNSUPPORTED", LA_ERR_CUDA: "LA_ERR_CUDA"}
 
@@ -101,6 +107,24 @@ _SIGS = {
     "la_w4_matvec": ([_vp, _vp, _vp, _vp, _i32, _i32, _i32, _i32, _i64, _i64, _u64],
                      ctypes.c_int),
     "la_w4_quantize": ([_vp, _vp, _vp, _i32, _i32, _i32, _i64, _u64], ctypes.c_int),
+    "la_layernorm_rows": ([_vp, _vp, _vp, _vp, _vp, _i32, _i32, _i64, _i64, _f32, _i32, _u64],
+                          ctypes.c_int),
+    "la_layernorm_rows_backward_workspace_bytes": ([_i32, _i32, _i32], _sz),
+    "la_layernorm_rows_backward": ([_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i32, _i32, _i64, _i64,
+                                    _i64, _i64, _i32, _vp, _sz, _u64], ctypes.c_int),
+    "la_linear_saved_bytes": ([_i32, _i32, _i32], _sz),
+    "la_linear": ([_vp, _vp, _vp, _vp, _vp, _vp, _sz, _i32, _i32, _i32, _i64, _i64, _i64, _i64,
+                   _i32, _u64], ctypes.c_int),
+    "la_linear_backward_workspace_bytes": ([_i32, _i32, _i32, _i32], _sz),
+    "la_linear_backward": ([_vp, _vp, _vp, _sz, _vp, _vp, _vp, _vp, _i32, _i32, _i32, _i64, _i64,
+                            _i64, _i64, _i64, _i32, _vp, _sz, _u64], ctypes.c_int),
+    "la_gated_ffn_saved_bytes": ([_i32, _i32], _sz),
+    "la_gated_ffn": ([_vp, _vp, _vp, _vp, _vp, _sz, _i32, _i32, _i32, _i64, _i64, _i64, _i64, _i32,
+                      _u64], ctypes.c_int),
+    "la_gated_ffn_backward_workspace_bytes": ([_i32, _i32, _i32], _sz),
+    "la_gated_ffn_backward": ([_vp, _vp, _vp, _vp, _sz, _vp, _vp, _vp, _vp, _i32, _i32, _i32, _i64,
+                               _i64, _i64, _i64, _i64, _i64, _i64, _i32, _vp, _sz, _u64],
+                              ctypes.c_int),
 }
 
 _lib = None
@@ -696,3 +720,177 @@ def w4_matvec(x, q, scales, y=None, *, stream=None):
     _check(_load().la_w4_matvec(x.data_ptr(), q.data_ptr(), scales.data_ptr(), y.data_ptr(), M, N, K,
                                 K // groups, xs, ys, _stream_on(stream, dev)))
     return y
+
+
+def _act_code(act) -> int:
+    code = LA_ACTIVATIONS.get(act)
+    if code is None:
+        raise ValueError(f"activation {act!r}: one of {', '.join(LA_ACTIVATIONS)}")
+    return code
+
+
+def _vector(name, t, n, dtype, dev):
+    """The address of a contiguous vector, or None."""
+    return None if t is None else _dense(name, t, (n,), dtype, dev)
+
+
+def _rows_like(shape, dtype, device, stream):
+    """A new matrix on the stream of the call, whose rows start on 16 bytes."""
+    per = 16 // dtype.itemsize
+    ld = (shape[1] + per - 1) // per * per
+    if stream is None:
+        return torch.empty(shape[0], ld, dtype=dtype, device=device)[:, :shape[1]]
+    with _on_stream(stream):
+        return torch.empty(shape[0], ld, dtype=dtype, device=device)[:, :shape[1]]
+
+
+def layernorm_rows(x, w, b=None, y=None, *, stats=None, eps=1e-5, stream=None):
+    """y = (x - mean) / sqrt(var + eps) * w + b per row; x, y [rows][width] (fp32 or bf16; width up to
+    8192, rows on 16 bytes; y may be x, and defaults to a new tensor), w, b [width]. stats: fp32
+    [rows][2] that receives mean and 1 / sqrt(var + eps), when layernorm_rows_backward is to follow.
+    Returns y."""
+    dev = _on_gpu(x)
+    rows, width = x.shape
+    dt = x.dtype
+    code = _dtype_code(x)
+    if y is None:
+        y = _rows_like((rows, width), dt, x.device, stream)
+    _check(_load().la_layernorm_rows(
+        x.data_ptr(), _vector("w", w, width, dt, dev), _vector("b", b, width, dt, dev), y.data_ptr(),
+        None if stats is None else _dense("stats", stats, (rows, 2), torch.float32, dev), rows, width,
+        _matrix16("x", x, rows, width, dt, dev), _matrix16("y", y, rows, width, dt, dev), eps, code,
+        _stream_on(stream, dev)))
+    return y
+
+
+def _matrix16(name, t, rows, cols, dtype, dev) -> int:
+    """_matrix for calls whose rows start on 16 bytes: a single row goes with any stride."""
+    s = _matrix(name, t, rows, cols, dtype, dev)
+    return s if rows > 1 else (cols + 7) // 8 * 8
+
+
+def layernorm_rows_backward_workspace_bytes(rows, width, dtype) -> int:
+    """Bytes of workspace that layernorm_rows_backward needs."""
+    return int(_load().la_layernorm_rows_backward_workspace_bytes(rows, width, _dtype_arg(dtype)))
+
+
+def layernorm_rows_backward(x, w, stats, dy, dx, dw, db=None, *, dskip=None, workspace=None,
+                            stream=None) -> None:
+    """Gradients of layernorm_rows: dx [rows][width] (plus dskip [rows][width] where given: a gradient
+    that reaches x past the norm; dx may be dy or dskip), dw and db fp32 [width]. x, w and stats are
+    those of the forward call."""
+    dev = _on_gpu(x)
+    rows, width = x.shape
+    dt = x.dtype
+    ws, ws_bytes = _room("workspace", workspace, dev)
+    _check(_load().la_layernorm_rows_backward(
+        x.data_ptr(), _vector("w", w, width, dt, dev), _dense("stats", stats, (rows, 2), torch.float32, dev),
+        dy.data_ptr(), None if dskip is None else dskip.data_ptr(), dx.data_ptr(),
+        _vector("dw", dw, width, torch.float32, dev), _vector("db", db, width, torch.float32, dev), rows, width,
+        _matrix16("x", x, rows, width, dt, dev), _matrix16("dy", dy, rows, width, dt, dev),
+        0 if dskip is None else _matrix16("dskip", dskip, rows, width, dt, dev),
+        _matrix16("dx", dx, rows, width, dt, dev), _dtype_code(x), ws, ws_bytes, _stream_on(stream, dev)))
+
+
+def linear_saved_bytes(rows, outputs, act="none") -> int:
+    """Bytes of the buffer that linear fills for linear_backward (0 without an activation)."""
+    return int(_load().la_linear_saved_bytes(rows, outputs, _act_code(act)))
+
+
+def linear(x, w, y=None, *, bias=None, residual=None, act="none", saved=None, stream=None):
+    """y = act(x W^T + bias) + residual on the tensor cores (bf16, fp32 accumulation, one rounding).
+
+    x [M][K], w [N][K] (a linear layer's [out][in] weight), bias [N], residual and y [M][N] (y may be
+    residual, and defaults to a new tensor); any sizes, rows on 16 bytes. act: one of LA_ACTIVATIONS.
+    saved: a buffer of linear_saved_bytes(...) when linear_backward is to follow. Returns y."""
+    dev = _on_gpu(x)
+    M, K = x.shape
+    N = w.shape[0]
+    bf16 = torch.bfloat16
+    if y is None:
+        y = _rows_like((M, N), bf16, x.device, stream)
+    sv, sv_bytes = _room("saved", saved, dev)
+    _check(_load().la_linear(
+        x.data_ptr(), w.data_ptr(), _vector("bias", bias, N, bf16, dev),
+        None if residual is None else residual.data_ptr(), y.data_ptr(), sv, sv_bytes, M, N, K,
+        _matrix16("x", x, M, K, bf16, dev), _matrix16("w", w, N, K, bf16, dev),
+        0 if residual is None else _matrix16("residual", residual, M, N, bf16, dev),
+        _matrix16("y", y, M, N, bf16, dev), _act_code(act), _stream_on(stream, dev)))
+    return y
+
+
+def linear_backward_workspace_bytes(rows, outputs, inputs, act="none") -> int:
+    """Bytes of workspace that linear_backward needs."""
+    return int(_load().la_linear_backward_workspace_bytes(rows, outputs, inputs, _act_code(act)))
+
+
+def linear_backward(x, w, saved, dy, dx=None, dw=None, *, dbias=None, act="none", workspace=None,
+                    stream=None) -> None:
+    """Gradients of linear: dx [M][K], dw [N][K] and dbias [N] (bf16; those that are given) from dy
+    [M][N]; the residual's is dy itself. x, w, saved (None without an activation) and act are those of
+    the forward call."""
+    dev = _on_gpu(x)
+    M, K = x.shape
+    N = w.shape[0]
+    bf16 = torch.bfloat16
+    sv, sv_bytes = _room("saved", saved, dev)
+    ws, ws_bytes = _room("workspace", workspace, dev)
+    _check(_load().la_linear_backward(
+        x.data_ptr(), w.data_ptr(), sv, sv_bytes, dy.data_ptr(), None if dx is None else dx.data_ptr(),
+        None if dw is None else dw.data_ptr(), _vector("dbias", dbias, N, bf16, dev), M, N, K,
+        _matrix16("x", x, M, K, bf16, dev), _matrix16("w", w, N, K, bf16, dev),
+        _matrix16("dy", dy, M, N, bf16, dev), 0 if dx is None else _matrix16("dx", dx, M, K, bf16, dev),
+        0 if dw is None else _matrix16("dw", dw, N, K, bf16, dev), _act_code(act), ws, ws_bytes,
+        _stream_on(stream, dev)))
+
+
+def gated_ffn_saved_bytes(rows, hidden) -> int:
+    """Bytes of the buffer that gated_ffn fills for gated_ffn_backward."""
+    return int(_load().la_gated_ffn_saved_bytes(rows, hidden))
+
+
+def gated_ffn(x, w_gate, w_up, h=None, *, act="silu", saved=None, stream=None):
+    """h = act(x Wg^T) * (x Wu^T): both projections, the activation and the product in one kernel.
+
+    x [M][K], w_gate and w_up [F][K] (w[:F] and w[F:] of a packed weight are fine), h [M][F] (a new
+    tensor by default): bf16, any sizes, rows on 16 bytes. act: one of LA_ACTIVATIONS. saved: a buffer
+    of gated_ffn_saved_bytes(...) when gated_ffn_backward is to follow. The projection back is
+    linear(h, w_down, residual=...). Returns h."""
+    dev = _on_gpu(x)
+    M, K = x.shape
+    F = w_gate.shape[0]
+    bf16 = torch.bfloat16
+    if h is None:
+        h = _rows_like((M, F), bf16, x.device, stream)
+    sv, sv_bytes = _room("saved", saved, dev)
+    _check(_load().la_gated_ffn(
+        x.data_ptr(), w_gate.data_ptr(), w_up.data_ptr(), h.data_ptr(), sv, sv_bytes, M, F, K,
+        _matrix16("x", x, M, K, bf16, dev), _matrix16("w_gate", w_gate, F, K, bf16, dev),
+        _matrix16("w_up", w_up, F, K, bf16, dev), _matrix16("h", h, M, F, bf16, dev), _act_code(act),
+        _stream_on(stream, dev)))
+    return h
+
+
+def gated_ffn_backward_workspace_bytes(rows, hidden, inputs) -> int:
+    """Bytes of workspace that gated_ffn_backward needs."""
+    return int(_load().la_gated_ffn_backward_workspace_bytes(rows, hidden, inputs))
+
+
+def gated_ffn_backward(x, w_gate, w_up, saved, dh, dx=None, dw_gate=None, dw_up=None, *, act="silu",
+                       workspace=None, stream=None) -> None:
+    """Gradients of gated_ffn: dx [M][K] and/or dw_gate and dw_up [F][K] (bf16) from dh [M][F]. x, the
+    weights, saved and act are those of the forward call."""
+    dev = _on_gpu(x)
+    M, K = x.shape
+    F = w_gate.shape[0]
+    bf16 = torch.bfloat16
+    sv, sv_bytes = _room("saved", saved, dev)
+    ws, ws_bytes = _room("workspace", workspace, dev)
+    opt = lambda name, t, rows: (None, 0) if t is None else (  # noqa: E731
+        t.data_ptr(), _matrix16(name, t, rows, K, bf16, dev))
+    (pdx, lddx), (pg, lddg), (pu, lddu) = opt("dx", dx, M), opt("dw_gate", dw_gate, F), opt("dw_up", dw_up, F)
+    _check(_load().la_gated_ffn_backward(
+        x.data_ptr(), w_gate.data_ptr(), w_up.data_ptr(), sv, sv_bytes, dh.data_ptr(), pdx, pg, pu, M, F, K,
+        _matrix16("x", x, M, K, bf16, dev), _matrix16("w_gate", w_gate, F, K, bf16, dev),
+        _matrix16("w_up", w_up, F, K, bf16, dev), _matrix16("dh", dh, M, F, bf16, dev), lddx, lddg, lddu,
+        _act_code(act), ws, ws_bytes, _stream_on(stream, dev)))

@@ -204,6 +204,27 @@ bool overlap(const Rows &a, const Rows &b) {
     return at < a.width || at + b.width > stride;  // b's place in a's rows
 }
 
+// Whether two matrices are the same memory, row for row.
+bool same_rows(const Rows &a, const Rows &b) {
+    return a.p == b.p && a.rows == b.rows && a.width == b.width && (a.rows == 1 || a.stride == b.stride);
+}
+
+// Outputs may overlap neither inputs nor one another (null ones aside), but for the pairs (output, input)
+// that may be one and the same matrix.
+template <class F>
+int check_apart(const Rows *out, int n_out, const Rows *in, int n_in, F &&may_be_same, const char *names) {
+    for (int o = 0; o < n_out; ++o) {
+        if (!out[o].p || !out[o].width) continue;
+        for (int i = 0; i < n_in; ++i)
+            if (in[i].p && in[i].width && !(may_be_same(o, i) && same_rows(out[o], in[i])) && overlap(out[o], in[i]))
+                return fail(LA_ERR_ARG, "%s may not overlap an input", names);
+        for (int k = 0; k < o; ++k)
+            if (out[k].p && out[k].width && overlap(out[o], out[k]))
+                return fail(LA_ERR_ARG, "%s may not overlap one another", names);
+    }
+    return LA_OK;
+}
+
 int check_bytes(size_t bytes, size_t need, const char *name) {
     if (bytes < need)
         return fail(LA_ERR_ARG, "%s of %zu bytes is below the %zu required", name, bytes, need);
@@ -223,6 +244,28 @@ int w4_common(const void *q, const void *scales, int K, int group) {
     if (K % group) return fail(LA_ERR_ARG, "K (%d) is not a multiple of the group (%d)", K, group);
     LA_TRY(check_act_ptr(q, "q"));
     return check_act_ptr(scales, "scales");
+}
+
+// Columns of a buffer that the dense calls keep between forward and backward pass: whole 16 bytes of bf16.
+int64_t whole8(int n) { return ((int64_t)n + 7) / 8 * 8; }
+
+int layernorm_common(const void *x, const void *w, int rows, int width, int64_t ldx, int dtype) {
+    if (rows < 1 || rows > kMaxCount) return fail(LA_ERR_COUNT, "layer norm of %d rows (1..%d)", rows, kMaxCount);
+    LA_TRY(check_dtype(dtype));
+    if (width < 1 || width > la::layernorm_max_width())
+        return fail(LA_ERR_UNSUPPORTED, "width %d outside 1..%d", width, la::layernorm_max_width());
+    LA_TRY(check_act_ptr(x, "x"));
+    LA_TRY(check_act_ptr(w, "w"));
+    return check_stride(ldx, width, dtype, "ldx");
+}
+
+int dense_common(const void *x, int M, int N, int K, int64_t ldx, int act) {
+    if (M < 1 || N < 1 || K < 1 || M > kMaxCount || N > kMaxCount || K > kMaxCount)
+        return fail(LA_ERR_COUNT, "product of %d x %d x %d (1..%d each)", M, N, K, kMaxCount);
+    if ((int64_t)M * N > ((int64_t)1 << 48)) return fail(LA_ERR_COUNT, "product of %d x %d values: the most are 2^48", M, N);
+    if (act < LA_ACT_NONE || act > LA_ACT_SILU) return fail(LA_ERR_UNSUPPORTED, "activation %d", act);
+    LA_TRY(check_act_ptr(x, "x"));
+    return check_stride(ldx, K, LA_BF16, "ldx");
 }
 
 // Shared checks of the three recurrence calls.
@@ -271,6 +314,12 @@ int debug_stall() {
 int debug_stall_scan() {
     const char *v = getenv("LA_DEBUG_STALL");
     return v && !strcmp(v, "2") ? 2 : debug_stall();
+}
+
+int dense_status(la::DenseArgs *a) {
+    a->wait_ns = wait_limit_ns();
+    a->debug_stall = debug_stall();
+    return get_status(&a->status);
 }
 
 int run_recurrence(la::RecArgs &a, cudaStream_t st) {
@@ -937,6 +986,241 @@ int la_w4_quantize(const void *w, void *q, void *scales, int N, int K, int group
     LA_TRY(check_stride(ldw, K, LA_BF16, "ldw"));
     la::W4QuantArgs a{w, q, scales, N, K, group, ldw};
     return launch_result([&] { return la::launch_w4_quantize(a, as_stream(stream)); }, "w4 quantize launch");
+}
+
+size_t la_layernorm_rows_backward_workspace_bytes(int rows, int width, int dtype) {
+    if (rows < 1 || width < 1) return 0;
+    return la::layernorm_backward_workspace_bytes(rows, width, dtype);
+}
+
+int la_layernorm_rows(const void *x, const void *w, const void *b, void *y, float *stats, int rows, int width,
+                      int64_t ldx, int64_t ldy, float eps, int dtype, uint64_t stream) {
+    LA_TRY(layernorm_common(x, w, rows, width, ldx, dtype));
+    LA_TRY(check_act_ptr(b, "b", true));
+    LA_TRY(check_act_ptr(y, "y"));
+    LA_TRY(check_act_ptr(stats, "stats", true));
+    LA_TRY(check_stride(ldy, width, dtype, "ldy"));
+    if (!(eps >= 0.f)) return fail(LA_ERR_ARG, "eps must be >= 0");
+    const Rows out = rows_of(y, rows, width, ldy, dtype), sm = rows_of(stats, 1, 2 * (int64_t)rows, 2 * (int64_t)rows, LA_F32);
+    const Rows in[3] = {rows_of(x, rows, width, ldx, dtype), rows_of(w, 1, width, width, dtype), rows_of(b, 1, width, width, dtype)};
+    for (int i = 0; i < 3; ++i)
+        if (in[i].p && ((!(i == 0 && same_rows(out, in[0])) && overlap(out, in[i])) || (stats && overlap(sm, in[i]))))
+            return fail(LA_ERR_ARG, "y (but for x itself) and stats may not overlap an input");
+    if (stats && overlap(out, sm)) return fail(LA_ERR_ARG, "y may not overlap stats");
+    la::LayerNormArgs a{x, w, b, y, stats, rows, width, ldx, ldy, eps, dtype};
+    return launch_result([&] { return la::launch_layernorm(a, as_stream(stream)); }, "layernorm launch");
+}
+
+int la_layernorm_rows_backward(const void *x, const void *w, const float *stats, const void *dy, const void *dskip,
+                               void *dx, float *dw, float *db, int rows, int width, int64_t ldx, int64_t lddy,
+                               int64_t ldskip, int64_t lddx, int dtype, void *workspace, size_t workspace_bytes,
+                               uint64_t stream) {
+    LA_TRY(layernorm_common(x, w, rows, width, ldx, dtype));
+    LA_TRY(check_act_ptr(stats, "stats"));
+    LA_TRY(check_act_ptr(dy, "dy"));
+    LA_TRY(check_act_ptr(dskip, "dskip", true));
+    LA_TRY(check_act_ptr(dx, "dx"));
+    LA_TRY(check_act_ptr(dw, "dw"));
+    LA_TRY(check_act_ptr(db, "db", true));
+    LA_TRY(check_stride(lddy, width, dtype, "lddy"));
+    LA_TRY(check_stride(lddx, width, dtype, "lddx"));
+    if (dskip) LA_TRY(check_stride(ldskip, width, dtype, "ldskip"));
+    const size_t need = la_layernorm_rows_backward_workspace_bytes(rows, width, dtype);
+    LA_TRY(check_workspace(workspace, workspace_bytes, need));
+    const Rows in[5] = {rows_of(x, rows, width, ldx, dtype), rows_of(w, 1, width, width, dtype),
+                        rows_of(stats, 1, 2 * (int64_t)rows, 2 * (int64_t)rows, LA_F32),
+                        rows_of(dy, rows, width, lddy, dtype), rows_of(dskip, rows, width, ldskip, dtype)};
+    const Rows out[4] = {rows_of(dx, rows, width, lddx, dtype), rows_of(dw, 1, width, width, LA_F32),
+                         rows_of(db, 1, width, width, LA_F32), Rows{workspace, 1, (int64_t)need, (int64_t)need}};
+    LA_TRY(check_apart(out, 4, in, 5, [&](int o, int i) { return o == 0 && i >= 3; }, "dx, dw, db and the workspace"));
+    la::LayerNormBwdArgs a{x, w, stats, dy, dskip, dx, dw, db, rows, width, ldx, lddy, ldskip, lddx, dtype, workspace};
+    return launch_result([&] { return la::launch_layernorm_backward(a, as_stream(stream)); }, "layernorm backward launch");
+}
+
+size_t la_linear_saved_bytes(int M, int N, int act) {
+    if (M < 1 || N < 1 || act == LA_ACT_NONE) return 0;
+    return 2 * (size_t)M * whole8(N);
+}
+
+int la_linear(const void *x, const void *w, const void *bias, const void *residual, void *y, void *saved,
+              size_t saved_bytes, int M, int N, int K, int64_t ldx, int64_t ldw, int64_t ldr, int64_t ldy, int act,
+              uint64_t stream) {
+    LA_TRY(dense_common(x, M, N, K, ldx, act));
+    LA_TRY(check_act_ptr(w, "w"));
+    LA_TRY(check_act_ptr(bias, "bias", true));
+    LA_TRY(check_act_ptr(residual, "residual", true));
+    LA_TRY(check_act_ptr(y, "y"));
+    LA_TRY(check_act_ptr(saved, "saved", true));
+    LA_TRY(check_stride(ldw, K, LA_BF16, "ldw"));
+    LA_TRY(check_stride(ldy, N, LA_BF16, "ldy"));
+    if (residual) LA_TRY(check_stride(ldr, N, LA_BF16, "ldr"));
+    const size_t need = la_linear_saved_bytes(M, N, act);
+    if (!need) saved = nullptr;
+    if (saved) LA_TRY(check_bytes(saved_bytes, need, "saved"));
+    const Rows in[4] = {rows_of(x, M, K, ldx, LA_BF16), rows_of(w, N, K, ldw, LA_BF16), rows_of(bias, 1, N, N, LA_BF16),
+                        rows_of(residual, M, N, ldr, LA_BF16)};
+    const Rows out[2] = {rows_of(y, M, N, ldy, LA_BF16), Rows{saved, 1, (int64_t)need, (int64_t)need}};
+    LA_TRY(check_apart(out, 2, in, 4, [&](int o, int i) { return o == 0 && i == 3; }, "y and saved"));
+    la::DenseArgs a{};
+    a.kind = la::DENSE_LINEAR; a.count = 1;
+    a.a[0] = x; a.lda[0] = ldx; a.b[0] = w; a.ldb[0] = ldw; a.out[0] = y; a.ldo[0] = ldy;
+    a.M = M; a.N = N; a.K = K; a.bias = bias; a.residual = residual; a.ldr = ldr;
+    a.saved = saved; a.lds = whole8(N); a.act = act;
+    LA_TRY(dense_status(&a));
+    return launch_result([&] { return la::launch_dense(a, as_stream(stream)); }, "linear launch");
+}
+
+size_t la_linear_backward_workspace_bytes(int M, int N, int K, int act) {
+    if (M < 1 || N < 1 || K < 1) return 0;
+    return la_linear_saved_bytes(M, N, act) + la::linear_backward_partial_bytes(M, N);
+}
+
+int la_linear_backward(const void *x, const void *w, const void *saved, size_t saved_bytes, const void *dy, void *dx,
+                       void *dw, void *dbias, int M, int N, int K, int64_t ldx, int64_t ldw, int64_t lddy, int64_t lddx,
+                       int64_t lddw, int act, void *workspace, size_t workspace_bytes, uint64_t stream) {
+    LA_TRY(dense_common(x, M, N, K, ldx, act));
+    LA_TRY(check_act_ptr(w, "w"));
+    LA_TRY(check_act_ptr(dy, "dy"));
+    LA_TRY(check_act_ptr(dx, "dx", true));
+    LA_TRY(check_act_ptr(dw, "dw", true));
+    LA_TRY(check_act_ptr(dbias, "dbias", true));
+    if (!dx && !dw && !dbias) return fail(LA_ERR_ARG, "dx, dw and dbias are all NULL");
+    LA_TRY(check_stride(ldw, K, LA_BF16, "ldw"));
+    LA_TRY(check_stride(lddy, N, LA_BF16, "lddy"));
+    if (dx) LA_TRY(check_stride(lddx, K, LA_BF16, "lddx"));
+    if (dw) LA_TRY(check_stride(lddw, K, LA_BF16, "lddw"));
+    const size_t kept = la_linear_saved_bytes(M, N, act);
+    if (!kept) saved = nullptr;
+    if (kept) {
+        LA_TRY(check_act_ptr(saved, "saved"));
+        LA_TRY(check_bytes(saved_bytes, kept, "saved"));
+    }
+    const size_t need = la_linear_backward_workspace_bytes(M, N, K, act);
+    LA_TRY(check_workspace(workspace, workspace_bytes, need));
+    const Rows in[4] = {rows_of(x, M, K, ldx, LA_BF16), rows_of(w, N, K, ldw, LA_BF16),
+                        Rows{saved, 1, (int64_t)kept, (int64_t)kept}, rows_of(dy, M, N, lddy, LA_BF16)};
+    const Rows out[4] = {rows_of(dx, M, K, lddx, LA_BF16), rows_of(dw, N, K, lddw, LA_BF16),
+                         rows_of(dbias, 1, N, N, LA_BF16), Rows{workspace, 1, (int64_t)need, (int64_t)need}};
+    LA_TRY(check_apart(out, 4, in, 4, [](int, int) { return false; }, "dx, dw, dbias and the workspace"));
+    la::DenseArgs a{};
+    a.count = 1;
+    LA_TRY(dense_status(&a));
+    return launch_result([&] {
+        const void *dz = dy;
+        int64_t lddz = lddy;
+        if (kept || dbias) {
+            if (kept) {
+                dz = workspace;
+                lddz = whole8(N);
+            }
+            la::LinearGradArgs g{saved, dy, kept ? workspace : nullptr, dbias, reinterpret_cast<float *>(static_cast<char *>(workspace) + kept),
+                                 M, N, whole8(N), lddy, lddz, act};
+            const cudaError_t e = la::launch_linear_grad(g, as_stream(stream));
+            if (e != cudaSuccess) return e;
+        }
+        a.a[0] = dz; a.lda[0] = lddz;
+        if (dx) {
+            a.kind = la::DENSE_DX;
+            a.b[0] = w; a.ldb[0] = ldw; a.out[0] = dx; a.ldo[0] = lddx;
+            a.M = M; a.N = K; a.K = N;
+            const cudaError_t e = la::launch_dense(a, as_stream(stream));
+            if (e != cudaSuccess) return e;
+        }
+        if (!dw) return cudaSuccess;
+        a.kind = la::DENSE_DW;
+        a.b[0] = x; a.ldb[0] = ldx; a.out[0] = dw; a.ldo[0] = lddw;
+        a.M = N; a.N = K; a.K = M;
+        return la::launch_dense(a, as_stream(stream));
+    }, "linear backward launch");
+}
+
+size_t la_gated_ffn_saved_bytes(int M, int F) {
+    if (M < 1 || F < 1) return 0;
+    return 4 * (size_t)M * whole8(F);
+}
+
+int la_gated_ffn(const void *x, const void *w_gate, const void *w_up, void *h, void *saved, size_t saved_bytes, int M,
+                 int F, int K, int64_t ldx, int64_t ldwg, int64_t ldwu, int64_t ldh, int act, uint64_t stream) {
+    LA_TRY(dense_common(x, M, F, K, ldx, act));
+    LA_TRY(check_act_ptr(w_gate, "w_gate"));
+    LA_TRY(check_act_ptr(w_up, "w_up"));
+    LA_TRY(check_act_ptr(h, "h"));
+    LA_TRY(check_act_ptr(saved, "saved", true));
+    LA_TRY(check_stride(ldwg, K, LA_BF16, "ldwg"));
+    LA_TRY(check_stride(ldwu, K, LA_BF16, "ldwu"));
+    LA_TRY(check_stride(ldh, F, LA_BF16, "ldh"));
+    const size_t need = la_gated_ffn_saved_bytes(M, F);
+    if (saved) LA_TRY(check_bytes(saved_bytes, need, "saved"));
+    const Rows in[3] = {rows_of(x, M, K, ldx, LA_BF16), rows_of(w_gate, F, K, ldwg, LA_BF16), rows_of(w_up, F, K, ldwu, LA_BF16)};
+    const Rows out[2] = {rows_of(h, M, F, ldh, LA_BF16), Rows{saved, 1, (int64_t)need, (int64_t)need}};
+    LA_TRY(check_apart(out, 2, in, 3, [](int, int) { return false; }, "h and saved"));
+    la::DenseArgs a{};
+    a.kind = la::DENSE_GATED; a.count = 1;
+    a.a[0] = x; a.lda[0] = ldx; a.b[0] = w_gate; a.ldb[0] = ldwg; a.b[1] = w_up; a.ldb[1] = ldwu; a.out[0] = h; a.ldo[0] = ldh;
+    a.M = M; a.N = F; a.K = K; a.saved = saved; a.half = (int)whole8(F); a.lds = 2 * whole8(F); a.act = act;
+    LA_TRY(dense_status(&a));
+    return launch_result([&] { return la::launch_dense(a, as_stream(stream)); }, "gated ffn launch");
+}
+
+size_t la_gated_ffn_backward_workspace_bytes(int M, int F, int K) {
+    return K < 1 ? 0 : la_gated_ffn_saved_bytes(M, F);
+}
+
+int la_gated_ffn_backward(const void *x, const void *w_gate, const void *w_up, const void *saved, size_t saved_bytes,
+                          const void *dh, void *dx, void *dw_gate, void *dw_up, int M, int F, int K, int64_t ldx,
+                          int64_t ldwg, int64_t ldwu, int64_t lddh, int64_t lddx, int64_t lddwg, int64_t lddwu, int act,
+                          void *workspace, size_t workspace_bytes, uint64_t stream) {
+    LA_TRY(dense_common(x, M, F, K, ldx, act));
+    LA_TRY(check_act_ptr(w_gate, "w_gate"));
+    LA_TRY(check_act_ptr(w_up, "w_up"));
+    LA_TRY(check_act_ptr(saved, "saved"));
+    LA_TRY(check_act_ptr(dh, "dh"));
+    LA_TRY(check_act_ptr(dx, "dx", true));
+    LA_TRY(check_act_ptr(dw_gate, "dw_gate", true));
+    LA_TRY(check_act_ptr(dw_up, "dw_up", true));
+    if (!dw_gate != !dw_up) return fail(LA_ERR_ARG, "dw_gate and dw_up: both or neither");
+    if (!dx && !dw_gate) return fail(LA_ERR_ARG, "dx, dw_gate and dw_up are all NULL");
+    LA_TRY(check_stride(ldwg, K, LA_BF16, "ldwg"));
+    LA_TRY(check_stride(ldwu, K, LA_BF16, "ldwu"));
+    LA_TRY(check_stride(lddh, F, LA_BF16, "lddh"));
+    if (dx) LA_TRY(check_stride(lddx, K, LA_BF16, "lddx"));
+    if (dw_gate) {
+        LA_TRY(check_stride(lddwg, K, LA_BF16, "lddwg"));
+        LA_TRY(check_stride(lddwu, K, LA_BF16, "lddwu"));
+    }
+    const size_t kept = la_gated_ffn_saved_bytes(M, F), need = la_gated_ffn_backward_workspace_bytes(M, F, K);
+    LA_TRY(check_bytes(saved_bytes, kept, "saved"));
+    LA_TRY(check_workspace(workspace, workspace_bytes, need));
+    const Rows in[5] = {rows_of(x, M, K, ldx, LA_BF16), rows_of(w_gate, F, K, ldwg, LA_BF16), rows_of(w_up, F, K, ldwu, LA_BF16),
+                        Rows{saved, 1, (int64_t)kept, (int64_t)kept}, rows_of(dh, M, F, lddh, LA_BF16)};
+    const Rows out[4] = {rows_of(dx, M, K, lddx, LA_BF16), rows_of(dw_gate, F, K, lddwg, LA_BF16),
+                         rows_of(dw_up, F, K, lddwu, LA_BF16), Rows{workspace, 1, (int64_t)need, (int64_t)need}};
+    LA_TRY(check_apart(out, 4, in, 5, [](int, int) { return false; }, "dx, dw_gate, dw_up and the workspace"));
+    la::DenseArgs a{};
+    a.count = 2;
+    LA_TRY(dense_status(&a));
+    return launch_result([&] {
+        const int64_t half = whole8(F);
+        la::GatedGradArgs g{saved, dh, workspace, M, F, (int)half, lddh, act};
+        cudaError_t e = la::launch_gated_grad(g, as_stream(stream));
+        if (e != cudaSuccess) return e;
+        for (int i = 0; i < 2; ++i) {
+            a.a[i] = static_cast<const char *>(workspace) + i * half * 2;
+            a.lda[i] = 2 * half;
+        }
+        if (dx) {
+            a.kind = la::DENSE_DX;
+            a.b[0] = w_gate; a.ldb[0] = ldwg; a.b[1] = w_up; a.ldb[1] = ldwu; a.out[0] = dx; a.ldo[0] = lddx;
+            a.M = M; a.N = K; a.K = F;
+            e = la::launch_dense(a, as_stream(stream));
+            if (e != cudaSuccess) return e;
+        }
+        if (!dw_gate) return cudaSuccess;
+        a.kind = la::DENSE_DW;
+        a.b[0] = x; a.ldb[0] = ldx; a.out[0] = dw_gate; a.ldo[0] = lddwg; a.out[1] = dw_up; a.ldo[1] = lddwu;
+        a.M = F; a.N = K; a.K = M;
+        return la::launch_dense(a, as_stream(stream));
+    }, "gated ffn backward launch");
 }
 
 }  // extern "C"

@@ -1,0 +1,121 @@
+// The elementwise halves of the dense layers' backward passes: gradients before the activation, and the
+// bias's gradient.
+//
+//   linear:  dz = dy act'(z),  dbias = sum_rows dz
+//   gated:   dgate = dh up act'(gate),  dup = dh act(gate)
+//
+// Bound by memory: each value is read and written once. dz, dgate and dup are rounded to bf16, the type in
+// which the tensor cores take them; the bias's gradient is summed from dz before that rounding.
+#include "dense.cuh"
+#include "launch.h"
+#include "overlap.cuh"
+
+namespace la {
+
+namespace {
+
+using bf16 = __nv_bfloat16;
+constexpr int COLS = 256, WARPS = 8;  // a block: 32 lanes of 8 columns, eight rows at a time
+
+// dz may be null (act none: dz is dy); partial [gridDim.y][N] (or null): the sums of the block's rows.
+__global__ void __launch_bounds__(32 * WARPS)
+linear_grad_kernel(const bf16 *__restrict__ saved, const bf16 *__restrict__ dy, bf16 *__restrict__ dz,
+                   float *__restrict__ partial, int M, int N, int64_t lds, int64_t lddy, int64_t ldz, int act) {
+    __shared__ float sh[WARPS][COLS];
+    wait_for_previous();
+    const int c = blockIdx.x * COLS + threadIdx.x * 8;
+    float sum[8] = {};
+    if (c < N)
+        for (int64_t r = blockIdx.y * WARPS + threadIdx.y; r < M; r += (int64_t)gridDim.y * WARPS) {
+            float d[8];
+            load_piece(dy + r * lddy, c, N, d);
+            if (saved) {
+                float z[8];
+                load_piece(saved + r * lds, c, N, z);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) d[e] *= act_slope(z[e], act);
+                store_piece(dz + r * ldz, c, N, d);
+            }
+#pragma unroll
+            for (int e = 0; e < 8; ++e) sum[e] += d[e];
+        }
+    if (!partial) return;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) sh[threadIdx.y][threadIdx.x * 8 + e] = sum[e];
+    __syncthreads();
+    const int k = threadIdx.y * 32 + threadIdx.x;
+    float s = 0.f;
+#pragma unroll
+    for (int w = 0; w < WARPS; ++w) s += sh[w][k];
+    if (blockIdx.x * COLS + k < N) partial[(int64_t)blockIdx.y * N + blockIdx.x * COLS + k] = s;
+}
+
+__global__ void __launch_bounds__(32 * 16)
+bias_sum_kernel(const float *__restrict__ partial, int runs, int N, bf16 *__restrict__ dbias) {
+    __shared__ float sh[16][33];
+    wait_for_previous();
+    const int c = blockIdx.x * 32 + threadIdx.x;
+    float s = 0.f;
+    if (c < N)
+        for (int k = threadIdx.y; k < runs; k += 16) s += partial[(int64_t)k * N + c];
+    sh[threadIdx.y][threadIdx.x] = s;
+    __syncthreads();
+    if (threadIdx.y == 0 && c < N) {
+        s = 0.f;
+#pragma unroll
+        for (int k = 0; k < 16; ++k) s += sh[k][threadIdx.x];
+        dbias[c] = __float2bfloat16_rn(s);
+    }
+}
+
+// saved and d: [M][2 * half], gate in columns 0.., up from column half on.
+__global__ void __launch_bounds__(256)
+gated_grad_kernel(const bf16 *__restrict__ saved, const bf16 *__restrict__ dh, bf16 *__restrict__ d, int M, int F,
+                  int half, int64_t lddh, int act) {
+    wait_for_previous();
+    const int c = (blockIdx.x * 32 + threadIdx.x) * 8;
+    if (c >= F) return;
+    for (int64_t r = blockIdx.y * 8 + threadIdx.y; r < M; r += (int64_t)gridDim.y * 8) {
+        float gate[8], up[8], g[8];
+        const bf16 *s = saved + r * 2 * half;
+        bf16 *o = d + r * 2 * half;
+        load_piece(s, c, F, gate);
+        load_piece(s + half, c, F, up);
+        load_piece(dh + r * lddh, c, F, g);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            up[e] *= g[e] * act_slope(gate[e], act);
+            gate[e] = g[e] * act_value(gate[e], act);
+        }
+        store_piece(o, c, F, up);
+        store_piece(o + half, c, F, gate);
+    }
+}
+
+// Rows are shared out so that the grid has a few blocks for each SM.
+int row_runs(int M, int N) {
+    const int cols = (N + COLS - 1) / COLS, most = (M + WARPS - 1) / WARPS;
+    int runs = (152 * 6 + cols - 1) / cols;
+    return runs < most ? runs : most;
+}
+
+}  // namespace
+
+size_t linear_backward_partial_bytes(int M, int N) { return (size_t)row_runs(M, N) * N * sizeof(float); }
+
+cudaError_t launch_linear_grad(const LinearGradArgs &a, cudaStream_t st) {
+    const int runs = row_runs(a.M, a.N);
+    cudaError_t e = launch_overlapped(linear_grad_kernel, dim3((a.N + COLS - 1) / COLS, runs), dim3(32, WARPS), 0, 0, st,
+                                      (const bf16 *)a.saved, (const bf16 *)a.dy, (bf16 *)a.dz,
+                                      a.dbias ? a.partial : nullptr, a.M, a.N, a.lds, a.lddy, a.ldz, a.act);
+    if (e != cudaSuccess || !a.dbias) return e;
+    return launch_overlapped(bias_sum_kernel, dim3((a.N + 31) / 32), dim3(32, 16), 0, 0, st, (const float *)a.partial, runs,
+                             a.N, (bf16 *)a.dbias);
+}
+
+cudaError_t launch_gated_grad(const GatedGradArgs &a, cudaStream_t st) {
+    return launch_overlapped(gated_grad_kernel, dim3((a.F + COLS - 1) / COLS, row_runs(a.M, a.F)), dim3(32, 8), 0, 0, st,
+                             (const bf16 *)a.saved, (const bf16 *)a.dh, (bf16 *)a.d, a.M, a.F, a.half, a.lddh, a.act);
+}
+
+}  // namespace la

@@ -1,0 +1,275 @@
+// The matrix products of the dense layers' calls on the 5th-generation tensor cores, bf16 operands, fp32
+// accumulation in TMEM, one rounding of the result:
+//
+//   LINEAR  y  = act(x W^T + bias) + residual          x [M][K],  W [N][K]
+//   GATED   h  = act(x Wg^T) * (x Wu^T)                x [M][K],  Wg, Wu [N][K]
+//   DX      dx = sum_p dz_p W_p                        dz_p [M][K], W_p [K][N]      (p: one or two parts)
+//   DW      dW_i = dz_i^T x                            dz_i [K][M], x [K][N]        (i: one or two outputs)
+//
+// In DX the rows of W, in DW those of both operands run along the summed index: their tiles are taken as they
+// lie in memory (MN-major operands), nothing is transposed.
+#include <cuda.h>
+
+#include "dense.cuh"
+#include "launch.h"
+#include "tc.cuh"
+
+namespace la {
+
+namespace {
+
+constexpr int TM = 128, TN = 256, TK = 64, STAGES = 4;
+constexpr uint32_t A_BYTES = TM * TK * 2, B_BYTES = TN * TK * 2, STAGE_BYTES = A_BYTES + B_BYTES;
+constexpr uint32_t OFF_BAR = STAGES * STAGE_BYTES;
+constexpr size_t SMEM = OFF_BAR + 256 + 1024;  // barriers, alignment
+constexpr int THREADS = 192;
+constexpr uint64_t WAIT_NS = 2000000000ull;
+constexpr uint32_t SLEEP_NS = 1000000u;
+
+struct Maps {
+    CUtensorMap a[2], b[2];
+};
+
+struct Epilogue {
+    __nv_bfloat16 *out[2];
+    const __nv_bfloat16 *bias, *residual;
+    __nv_bfloat16 *saved;  // LINEAR: z [M][lds]; GATED: gate | up [M][2 * half]
+    int64_t ldo[2], ldr, lds;
+    int half, act;
+};
+
+__device__ __forceinline__ void mbar_arrive(uint64_t *bar) {
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(tc::smem_u32(bar)) : "memory");
+}
+
+// 16 columns from c on of a row with N columns.
+__device__ __forceinline__ void store16(__nv_bfloat16 *row, int c, int N, const float *v) {
+    if (c < N) store_piece(row, c, N, v);
+    if (c + 8 < N) store_piece(row, c + 8, N, v + 8);
+}
+__device__ __forceinline__ void load16(const __nv_bfloat16 *row, int c, int N, float *v) {
+    if (c < N) load_piece(row, c, N, v);
+    if (c + 8 < N) load_piece(row, c + 8, N, v + 8);
+}
+
+template <int KIND>
+__global__ void __launch_bounds__(THREADS, 1)
+dense_kernel(const __grid_constant__ Maps maps, const Epilogue ep, int M, int N, int K, int parts, int outs, int *status,
+             uint64_t wait_ns, int debug_stall) {
+    constexpr bool A_MN = KIND == DENSE_DW, B_MN = KIND == DENSE_DX || KIND == DENSE_DW;
+    constexpr int OUT_N = KIND == DENSE_GATED ? TN / 2 : TN;  // columns of the result a tile holds
+    extern __shared__ unsigned char smem_raw[];
+    unsigned char *sm = reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                                          ~static_cast<uintptr_t>(1023));
+    uint64_t *full = reinterpret_cast<uint64_t *>(sm + OFF_BAR);
+    uint64_t *empty = full + STAGES;
+    uint64_t *accf = empty + STAGES;
+    uint64_t *acce = accf + 2;
+    uint64_t *fin = acce + 2;
+    uint32_t *tmem_sh = reinterpret_cast<uint32_t *>(fin + 1);
+    volatile int *err = reinterpret_cast<volatile int *>(tmem_sh + 1);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < STAGES; ++s) {
+            tc::mbar_init(full + s, 1);
+            tc::mbar_init(empty + s, 1);
+        }
+        for (int b = 0; b < 2; ++b) {
+            tc::mbar_init(accf + b, 1);
+            tc::mbar_init(acce + b, 128);
+        }
+        tc::mbar_init(fin, 1);
+        *err = 0;
+        tc::fence_mbar_init();
+    }
+    if (warp == 1) {
+        tc::tmem_alloc(tmem_sh, 2 * TN);
+        tc::tmem_relinquish();
+    }
+    tc::fence_before_sync();
+    __syncthreads();
+    tc::fence_after_sync();
+    const uint32_t tm = *tmem_sh;
+    const int64_t mt = (M + TM - 1) / TM, nt = (N + OUT_N - 1) / OUT_N, ntiles = mt * nt * outs;
+    const int kp = (K + TK - 1) / TK, kb = kp * parts;
+    const uint32_t sbase = tc::smem_u32(sm);
+
+    if (warp == 0) {
+        if (tc::elect_one()) {
+            uint32_t it = 0;
+            for (int64_t tile = blockIdx.x; tile < ntiles && !*err; tile += gridDim.x) {
+                const int o = (int)(tile / (mt * nt));
+                const int m0 = (int)(tile % (mt * nt) / nt) * TM, n0 = (int)(tile % nt) * OUT_N;
+                for (int k = 0; k < kb; ++k, ++it) {
+                    const uint32_t s = it % STAGES, ph = (it / STAGES) & 1u;
+                    if (!tc::mbar_wait(empty + s, ph ^ 1u, wait_ns, SLEEP_NS) || *err) {
+                        *err = 1;
+                        break;
+                    }
+                    const int p = k / kp, k0 = (k - p * kp) * TK;
+                    const CUtensorMap *ma = &maps.a[KIND == DENSE_DW ? o : p], *mb = &maps.b[KIND == DENSE_DX ? p : 0];
+                    const uint32_t da = sbase + s * STAGE_BYTES, db = da + A_BYTES;
+                    tc::mbar_expect_tx(full + s, STAGE_BYTES);
+                    if (A_MN) {
+                        for (int i = 0; i < TM / 64; ++i) tc::tma_load_2d(da + i * 8192, ma, m0 + i * 64, k0, full + s);
+                    } else {
+                        tc::tma_load_2d(da, ma, k0, m0, full + s);
+                    }
+                    if (B_MN) {
+                        for (int i = 0; i < TN / 64; ++i) tc::tma_load_2d(db + i * 8192, mb, n0 + i * 64, k0, full + s);
+                    } else if (KIND == DENSE_GATED) {
+                        tc::tma_load_2d(db, mb, k0, n0, full + s);
+                        tc::tma_load_2d(db + B_BYTES / 2, &maps.b[1], k0, n0, full + s);
+                    } else {
+                        tc::tma_load_2d(db, mb, k0, n0, full + s);
+                        tc::tma_load_2d(db + B_BYTES / 2, mb, k0, n0 + 128, full + s);
+                    }
+                }
+            }
+            for (uint32_t s = 0; s < STAGES && s < it; ++s) {  // every copy has landed before the block exits
+                const uint32_t last = it - 1 - ((it - 1 - s) % STAGES);
+                if (!tc::mbar_wait(full + s, (last / STAGES) & 1u, WAIT_NS, SLEEP_NS)) *err = 1;
+            }
+        }
+    } else if (warp == 1) {
+        if (tc::elect_one()) {
+            constexpr uint32_t id = tc::idesc(TM, TN, tc::FMT_BF16, A_MN, B_MN);
+            uint32_t it = 0, tcnt = 0;
+            if (debug_stall && !tc::mbar_wait(fin, 0, wait_ns, SLEEP_NS)) *err = 1;
+            for (int64_t tile = blockIdx.x; tile < ntiles && !*err; tile += gridDim.x, ++tcnt) {
+                const uint32_t acc = tcnt & 1u, aph = (tcnt >> 1) & 1u;
+                if (!tc::mbar_wait(acce + acc, aph ^ 1u, wait_ns, SLEEP_NS)) {
+                    *err = 1;
+                    break;
+                }
+                tc::fence_after_sync();
+                const uint32_t d = tm + acc * TN;
+                bool ok = true;
+                for (int k = 0; k < kb; ++k, ++it) {
+                    const uint32_t s = it % STAGES, ph = (it / STAGES) & 1u;
+                    if (!tc::mbar_wait(full + s, ph, wait_ns, SLEEP_NS) || *err) {
+                        ok = false;
+                        break;
+                    }
+                    tc::fence_after_sync();
+                    const uint32_t a = sbase + s * STAGE_BYTES, b = a + A_BYTES;
+#pragma unroll
+                    for (uint32_t kk = 0; kk < TK / 16; ++kk)
+                        tc::mma_bf16_ss(d,
+                                        A_MN ? tc::sdesc_sw128_mn(a + kk * 2048u, 8192u, 1024u) : tc::sdesc_sw128(a + kk * 32u),
+                                        B_MN ? tc::sdesc_sw128_mn(b + kk * 2048u, 8192u, 1024u) : tc::sdesc_sw128(b + kk * 32u),
+                                        id, (k | kk) != 0);
+                    tc::mma_commit(empty + s);
+                }
+                if (!ok) {
+                    *err = 1;
+                    break;
+                }
+                tc::mma_commit(accf + acc);
+            }
+            tc::mma_commit(fin);
+            if (!tc::mbar_wait(fin, 0, WAIT_NS, SLEEP_NS)) *err = 1;
+        }
+    } else {
+        const uint32_t q = warp & 3;
+        uint32_t tcnt = 0;
+        for (int64_t tile = blockIdx.x; tile < ntiles; tile += gridDim.x, ++tcnt) {
+            if (__any_sync(0xffffffffu, *err != 0)) break;
+            const uint32_t acc = tcnt & 1u, aph = (tcnt >> 1) & 1u;
+            if (!__all_sync(0xffffffffu, tc::mbar_wait(accf + acc, aph, wait_ns, SLEEP_NS))) {
+                *err = 1;
+                break;
+            }
+            tc::fence_after_sync();
+            const int o = (int)(tile / (mt * nt));
+            const int m0 = (int)(tile % (mt * nt) / nt) * TM, n0 = (int)(tile % nt) * OUT_N;
+            const int row = m0 + 32 * (int)q + lane;
+#pragma unroll 1
+            for (int c = 0; c < OUT_N; c += 16) {
+                float v[16], u[16];
+                const int col = n0 + c;
+                tc::tmem_ld16(tc::tmem_addr(tm + acc * TN, 32 * q, c), v);
+                if (KIND == DENSE_GATED) tc::tmem_ld16(tc::tmem_addr(tm + acc * TN, 32 * q, c + TN / 2), u);
+                tc::tmem_wait_ld();
+                if (row >= M || col >= N) continue;
+                if (KIND == DENSE_LINEAR) {
+                    if (ep.bias) {
+                        load16(ep.bias, col, N, u);
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) v[e] += u[e];
+                    }
+                    if (ep.saved) store16(ep.saved + row * ep.lds, col, N, v);
+                    if (ep.act != LA_ACT_NONE)
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) v[e] = act_value(v[e], ep.act);
+                    if (ep.residual) {
+                        load16(ep.residual + row * ep.ldr, col, N, u);
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) v[e] += u[e];
+                    }
+                }
+                if (KIND == DENSE_GATED) {
+                    if (ep.saved) {
+                        store16(ep.saved + row * ep.lds, col, N, v);
+                        store16(ep.saved + row * ep.lds + ep.half, col, N, u);
+                    }
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) v[e] = act_value(v[e], ep.act) * u[e];
+                }
+                store16(ep.out[o] + row * ep.ldo[o], col, N, v);
+            }
+            tc::fence_before_sync();
+            mbar_arrive(acce + acc);
+        }
+    }
+    tc::fence_before_sync();
+    __syncthreads();
+    if (warp == 1) tc::tmem_dealloc(tm, 2 * TN);
+    if (*err && threadIdx.x == 0) raise_status(status, LA_DEV_TIMEOUT);
+}
+
+template <int KIND>
+cudaError_t launch(const DenseArgs &a, cudaStream_t st) {
+    constexpr bool A_MN = KIND == DENSE_DW, B_MN = KIND == DENSE_DX || KIND == DENSE_DW;
+    constexpr int OUT_N = KIND == DENSE_GATED ? TN / 2 : TN;
+    Maps maps;
+    for (int i = 0; i < 2; ++i) {
+        const int ia = KIND == DENSE_DX || KIND == DENSE_DW ? i : 0, ib = KIND == DENSE_DX || KIND == DENSE_GATED ? i : 0;
+        const int ja = ia < a.count ? ia : 0, jb = (KIND == DENSE_GATED || ib < a.count) ? ib : 0;
+        if (!(A_MN ? make_map_bf16_2d(&maps.a[i], a.a[ja], a.K, a.M, a.lda[ja], 64, TK, true)
+                   : make_map_bf16_2d(&maps.a[i], a.a[ja], a.M, a.K, a.lda[ja], TK, TM, true)) ||
+            !(B_MN ? make_map_bf16_2d(&maps.b[i], a.b[jb], a.K, a.N, a.ldb[jb], 64, TK, true)
+                   : make_map_bf16_2d(&maps.b[i], a.b[jb], a.N, a.K, a.ldb[jb], TK, 128, true)))
+            return cudaErrorInvalidValue;
+    }
+    Epilogue ep{};
+    for (int i = 0; i < 2; ++i) {
+        ep.out[i] = (__nv_bfloat16 *)a.out[i];
+        ep.ldo[i] = a.ldo[i];
+    }
+    ep.bias = (const __nv_bfloat16 *)a.bias; ep.residual = (const __nv_bfloat16 *)a.residual;
+    ep.saved = (__nv_bfloat16 *)a.saved; ep.ldr = a.ldr; ep.lds = a.lds; ep.half = a.half; ep.act = a.act;
+    const int parts = KIND == DENSE_DX ? a.count : 1, outs = KIND == DENSE_DW ? a.count : 1;
+    const int64_t ntiles = (int64_t)((a.M + TM - 1) / TM) * ((a.N + OUT_N - 1) / OUT_N) * outs;
+    int dev = 0, sms = 0;
+    cudaGetDevice(&dev);
+    cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    cudaError_t e = cudaFuncSetAttribute(dense_kernel<KIND>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SMEM);
+    if (e != cudaSuccess) return e;
+    dense_kernel<KIND><<<(int)(ntiles < sms ? ntiles : sms), THREADS, SMEM, st>>>(
+        maps, ep, a.M, a.N, a.K, parts, outs, a.status, a.wait_ns ? a.wait_ns : WAIT_NS, a.debug_stall);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_dense(const DenseArgs &a, cudaStream_t st) {
+    switch (a.kind) {
+        case DENSE_LINEAR: return launch<DENSE_LINEAR>(a, st);
+        case DENSE_GATED: return launch<DENSE_GATED>(a, st);
+        case DENSE_DX: return launch<DENSE_DX>(a, st);
+        default: return launch<DENSE_DW>(a, st);
+    }
+}
+
+}  // namespace la

@@ -241,6 +241,77 @@ struct W4QuantArgs {
 };
 cudaError_t launch_w4_quantize(const W4QuantArgs &a, cudaStream_t st);
 
+// Layer norm of rows (layernorm.cu): y = (x - mean) rstd w + b, stats [rows][2] = mean, rstd (or null).
+struct LayerNormArgs {
+    const void *x, *w, *b;
+    void *y;
+    float *stats;
+    int rows, width;
+    int64_t ldx, ldy;
+    float eps;
+    int dtype;
+};
+struct LayerNormBwdArgs {
+    const void *x, *w;
+    const float *stats;
+    const void *dy, *dskip;  // dskip: added to dx, or null
+    void *dx;
+    float *dw, *db;  // db may be null
+    int rows, width;
+    int64_t ldx, lddy, ldskip, lddx;
+    int dtype;
+    void *workspace;
+};
+cudaError_t launch_layernorm(const LayerNormArgs &a, cudaStream_t st);
+cudaError_t launch_layernorm_backward(const LayerNormBwdArgs &a, cudaStream_t st);
+int layernorm_max_width();
+size_t layernorm_backward_workspace_bytes(int rows, int width, int dtype);
+
+// The matrix products of the dense layers (dense_tc.cu), bf16:
+//   DENSE_LINEAR  out[0] [M][N] = act(a[0] [M][K] b[0] [N][K]^T + bias) + residual; saved: before act
+//   DENSE_GATED   out[0] [M][N] = act(a[0] b[0]^T) * (a[0] b[1]^T); saved [M][2 half]: both products
+//   DENSE_DX      out[0] [M][N] = sum over i < count of a[i] [M][K] b[i] [K][N]
+//   DENSE_DW      out[i] [M][N] = a[i] [K][M]^T b[0] [K][N], i < count
+enum { DENSE_LINEAR, DENSE_GATED, DENSE_DX, DENSE_DW };
+struct DenseArgs {
+    int kind, count;
+    const void *a[2], *b[2];
+    int64_t lda[2], ldb[2];
+    void *out[2];
+    int64_t ldo[2];
+    int M, N, K;
+    const void *bias, *residual;
+    void *saved;
+    int64_t ldr, lds;
+    int half, act;
+    int *status;
+    uint64_t wait_ns;  // limit of the kernel's bounded waits (0: the 2 s default)
+    int debug_stall;   // test knob: one wait on a barrier that nothing completes
+};
+cudaError_t launch_dense(const DenseArgs &a, cudaStream_t st);
+
+// Gradients before the activation (dense_grad.cu): dz = dy act'(saved), dbias = its column sums.
+// saved null: dz is dy and is not written.
+struct LinearGradArgs {
+    const void *saved, *dy;
+    void *dz, *dbias;
+    float *partial;
+    int M, N;
+    int64_t lds, lddy, ldz;
+    int act;
+};
+size_t linear_backward_partial_bytes(int M, int N);
+cudaError_t launch_linear_grad(const LinearGradArgs &a, cudaStream_t st);
+// d [M][2 half] = dh up act'(gate) | dh act(gate) from saved [M][2 half] = gate | up.
+struct GatedGradArgs {
+    const void *saved, *dh;
+    void *d;
+    int M, F, half;
+    int64_t lddh;
+    int act;
+};
+cudaError_t launch_gated_grad(const GatedGradArgs &a, cudaStream_t st);
+
 // As make_map_bf16_2d below, for elements of either activation type (LA_F32, LA_BF16).
 bool make_map_2d(void *map, const void *base, int dtype, int64_t rows, int64_t cols, int64_t ld,
                  uint32_t box_cols, uint32_t box_rows, bool swizzle128);
