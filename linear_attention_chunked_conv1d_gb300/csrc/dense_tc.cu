@@ -13,6 +13,7 @@
 #include <atomic>
 
 #include "dense.cuh"
+#include "dense_maps.cuh"
 #include "launch.h"
 #include "overlap.cuh"
 #include "tc.cuh"
@@ -29,18 +30,6 @@ constexpr int EPI_WARPS = 8, THREADS = 64 + 32 * EPI_WARPS;
 constexpr uint64_t WAIT_NS = 2000000000ull;
 constexpr uint32_t SLEEP_NS = 1000000u;
 constexpr int BAND = 8;  // tiles of rows that are walked together
-
-struct Maps {
-    CUtensorMap a[2], b[2];
-};
-
-struct Epilogue {
-    __nv_bfloat16 *out[2];
-    const __nv_bfloat16 *bias, *residual;
-    __nv_bfloat16 *saved;  // LINEAR: z [M][lds]; GATED: gate | up [M][2 * half]
-    int64_t ldo[2], ldr, lds;
-    int half, act;
-};
 
 // 16 columns from c on of a row with N columns.
 __device__ __forceinline__ void store16(__nv_bfloat16 *row, int c, int N, const float *v) {
@@ -294,22 +283,8 @@ cudaError_t launch(const DenseArgs &a, cudaStream_t st) {
     constexpr bool A_MN = KIND == DENSE_DW, B_MN = KIND == DENSE_DX || KIND == DENSE_DW;
     constexpr int OUT_N = KIND == DENSE_GATED ? TN / 2 : TN;
     Maps maps;
-    for (int i = 0; i < 2; ++i) {
-        const int ia = KIND == DENSE_DX || KIND == DENSE_DW ? i : 0, ib = KIND == DENSE_DX || KIND == DENSE_GATED ? i : 0;
-        const int ja = ia < a.count ? ia : 0, jb = (KIND == DENSE_GATED || ib < a.count) ? ib : 0;
-        if (!(A_MN ? make_map_bf16_2d(&maps.a[i], a.a[ja], a.K, a.M, a.lda[ja], 64, TK, true)
-                   : make_map_bf16_2d(&maps.a[i], a.a[ja], a.M, a.K, a.lda[ja], TK, 128, true)) ||
-            !(B_MN ? make_map_bf16_2d(&maps.b[i], a.b[jb], a.K, a.N, a.ldb[jb], 64, TK, true)
-                   : make_map_bf16_2d(&maps.b[i], a.b[jb], a.N, a.K, a.ldb[jb], TK, 128, true)))
-            return cudaErrorInvalidValue;
-    }
-    Epilogue ep{};
-    for (int i = 0; i < 2; ++i) {
-        ep.out[i] = (__nv_bfloat16 *)a.out[i];
-        ep.ldo[i] = a.ldo[i];
-    }
-    ep.bias = (const __nv_bfloat16 *)a.bias; ep.residual = (const __nv_bfloat16 *)a.residual;
-    ep.saved = (__nv_bfloat16 *)a.saved; ep.ldr = a.ldr; ep.lds = a.lds; ep.half = a.half; ep.act = a.act;
+    if (!make_maps(&maps, a, A_MN, B_MN, 128, 128)) return cudaErrorInvalidValue;
+    const Epilogue ep = make_epilogue(a);
     const int parts = KIND == DENSE_DX ? a.count : 1, outs = KIND == DENSE_DW ? a.count : 1;
     const int64_t ntiles = (int64_t)((a.M + TM - 1) / TM) * ((a.N + OUT_N - 1) / OUT_N) * outs;
     const int pairs = resident_pairs<KIND>();
@@ -320,6 +295,7 @@ cudaError_t launch(const DenseArgs &a, cudaStream_t st) {
 }  // namespace
 
 cudaError_t launch_dense(const DenseArgs &a, cudaStream_t st) {
+    if (dense_split_serves(a)) return launch_dense_split(a, st);
     switch (a.kind) {
         case DENSE_LINEAR: return launch<DENSE_LINEAR>(a, st);
         case DENSE_GATED: return launch<DENSE_GATED>(a, st);

@@ -289,6 +289,9 @@ struct DenseArgs {
     int debug_stall;   // test knob: one wait on a barrier that nothing completes
 };
 cudaError_t launch_dense(const DenseArgs &a, cudaStream_t st);
+// Those with few output tiles: the summed index split over a cluster's blocks (dense_split.cu).
+bool dense_split_serves(const DenseArgs &a);
+cudaError_t launch_dense_split(const DenseArgs &a, cudaStream_t st);
 
 // Gradients before the activation (dense_grad.cu): dz = dy act'(saved), dbias = its column sums.
 // saved null: dz is dy and is not written.
