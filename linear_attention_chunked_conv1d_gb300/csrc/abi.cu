@@ -322,6 +322,21 @@ int dense_status(la::DenseArgs *a) {
     return get_status(&a->status);
 }
 
+// dx = sum of dz_i W_i and dW_i = dz_i^T x, those that are asked for; a: the dz_i [M][N] and how many they are.
+cudaError_t launch_backward_products(const la::DenseArgs &a, const void *w0, int64_t ldw0, const void *w1, int64_t ldw1, void *dx,
+                                     int64_t lddx, const void *x, int64_t ldx, void *dw0, int64_t lddw0, void *dw1,
+                                     int64_t lddw1, int M, int N, int K, cudaStream_t st) {
+    la::DenseArgs gx = a, gw = a;
+    gx.kind = la::DENSE_DX;
+    gx.b[0] = w0; gx.ldb[0] = ldw0; gx.b[1] = w1; gx.ldb[1] = ldw1; gx.out[0] = dx; gx.ldo[0] = lddx;
+    gx.M = M; gx.N = K; gx.K = N;
+    gw.kind = la::DENSE_DW;
+    gw.b[0] = x; gw.ldb[0] = ldx; gw.out[0] = dw0; gw.ldo[0] = lddw0; gw.out[1] = dw1; gw.ldo[1] = lddw1;
+    gw.M = N; gw.N = K; gw.K = M;
+    if (dx && dw0) return la::launch_dense_pair(gx, gw, st);
+    return dx ? la::launch_dense(gx, st) : dw0 ? la::launch_dense(gw, st) : cudaSuccess;
+}
+
 int run_recurrence(la::RecArgs &a, cudaStream_t st) {
     LA_TRY(get_status(&a.status));
     a.wait_ns = wait_limit_ns();
@@ -1119,18 +1134,7 @@ int la_linear_backward(const void *x, const void *w, const void *saved, size_t s
             if (e != cudaSuccess) return e;
         }
         a.a[0] = dz; a.lda[0] = lddz;
-        if (dx) {
-            a.kind = la::DENSE_DX;
-            a.b[0] = w; a.ldb[0] = ldw; a.out[0] = dx; a.ldo[0] = lddx;
-            a.M = M; a.N = K; a.K = N;
-            const cudaError_t e = la::launch_dense(a, as_stream(stream));
-            if (e != cudaSuccess) return e;
-        }
-        if (!dw) return cudaSuccess;
-        a.kind = la::DENSE_DW;
-        a.b[0] = x; a.ldb[0] = ldx; a.out[0] = dw; a.ldo[0] = lddw;
-        a.M = N; a.N = K; a.K = M;
-        return la::launch_dense(a, as_stream(stream));
+        return launch_backward_products(a, w, ldw, nullptr, 0, dx, lddx, x, ldx, dw, lddw, nullptr, 0, M, N, K, as_stream(stream));
     }, "linear backward launch");
 }
 
@@ -1208,18 +1212,8 @@ int la_gated_ffn_backward(const void *x, const void *w_gate, const void *w_up, c
             a.a[i] = static_cast<const char *>(workspace) + i * half * 2;
             a.lda[i] = 2 * half;
         }
-        if (dx) {
-            a.kind = la::DENSE_DX;
-            a.b[0] = w_gate; a.ldb[0] = ldwg; a.b[1] = w_up; a.ldb[1] = ldwu; a.out[0] = dx; a.ldo[0] = lddx;
-            a.M = M; a.N = K; a.K = F;
-            e = la::launch_dense(a, as_stream(stream));
-            if (e != cudaSuccess) return e;
-        }
-        if (!dw_gate) return cudaSuccess;
-        a.kind = la::DENSE_DW;
-        a.b[0] = x; a.ldb[0] = ldx; a.out[0] = dw_gate; a.ldo[0] = lddwg; a.out[1] = dw_up; a.ldo[1] = lddwu;
-        a.M = F; a.N = K; a.K = M;
-        return la::launch_dense(a, as_stream(stream));
+        return launch_backward_products(a, w_gate, ldwg, w_up, ldwu, dx, lddx, x, ldx, dw_gate, lddwg, dw_up, lddwu, M, F, K,
+                                        as_stream(stream));
     }, "gated ffn backward launch");
 }
 

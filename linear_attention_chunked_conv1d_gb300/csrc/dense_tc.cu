@@ -8,6 +8,20 @@
 //
 // In DX the rows of W, in DW those of both operands run along the summed index: their tiles are taken as they
 // lie in memory (MN-major operands), nothing is transposed.
+//
+// A persistent, warp-specialised kernel; two blocks on neighbouring SMs form a pair (cta_group::2) that works on
+// one 256 x 256 tile: each holds 128 rows of A and half of B, so that an operand byte in shared memory serves
+// twice the multiply-adds of a single block's tile of 128 x 256.
+//  - warp 0 streams its block's halves (2 x 16 KB a stage of 64 summed indexes) through a ring of six stages by
+//    TMA; both blocks' copies complete on the leader's barrier;
+//  - warp 1 of the leader issues tcgen05.mma (M = 256, N = 256, K = 16) into one of two accumulators; GATED takes
+//    128 columns of each weight (one from each block), so that gate and up stand side by side in the accumulator;
+//  - warps 2-9 turn the other accumulator into the result meanwhile, 32 rows x 64 columns at a time, laid out in
+//    shared memory so that whole 128-byte lines go to memory.
+// Tiles are walked in bands of eight rows of tiles. DX and DW of one backward pass are one launch, the tiles with
+// the longer sums first: two launches would each leave SMs idle in their last round.
+// Every wait is bounded; on a timeout the blocks raise LA_DEV_TIMEOUT, stop issuing, let what is under way end,
+// free TMEM and return. Ragged edges come from TMA's zero fill; stores are guarded.
 #include <cuda.h>
 
 #include <atomic>
@@ -24,22 +38,24 @@ namespace {
 
 constexpr int TM = 256, TN = 256, TK = 64, STAGES = 6;  // a pair's tile; a block holds half of each operand
 constexpr uint32_t HALF_BYTES = 128 * TK * 2, STAGE_BYTES = 2 * HALF_BYTES;
-constexpr uint32_t OFF_BAR = STAGES * STAGE_BYTES;
-constexpr size_t SMEM = OFF_BAR + 256 + 1024;  // barriers, alignment
 constexpr int EPI_WARPS = 8, THREADS = 64 + 32 * EPI_WARPS;
+constexpr uint32_t OFF_OUT = STAGES * STAGE_BYTES;             // a warp's 32 rows of 128 bytes, for each epilogue warp
+constexpr uint32_t OFF_BAR = OFF_OUT + EPI_WARPS * 32 * 128;
+constexpr size_t SMEM = OFF_BAR + 256 + 1024;  // barriers, alignment
 constexpr uint64_t WAIT_NS = 2000000000ull;
 constexpr uint32_t SLEEP_NS = 1000000u;
 constexpr int BAND = 8;  // tiles of rows that are walked together
 
-// 16 columns from c on of a row with N columns.
-__device__ __forceinline__ void store16(__nv_bfloat16 *row, int c, int N, const float *v) {
-    if (c < N) store_piece(row, c, N, v);
-    if (c + 8 < N) store_piece(row, c + 8, N, v + 8);
-}
-__device__ __forceinline__ void load16(const __nv_bfloat16 *row, int c, int N, float *v) {
-    if (c < N) load_piece(row, c, N, v);
-    if (c + 8 < N) load_piece(row, c + 8, N, v + 8);
-}
+enum { LINEAR = DENSE_LINEAR, GATED = DENSE_GATED, BACKWARD };
+
+// One product of a launch (BACKWARD: up to two).
+struct Job {
+    int M, N, K, parts;
+    bool dw;  // BACKWARD: DW, else DX
+    int64_t mt, nt, tiles;
+};
+
+using bf16 = __nv_bfloat16;
 
 // Tile `t` of an output of mt x nt tiles: bands of BAND tiles of rows, column by column, so that the tiles
 // under way at one time share few rows and columns and find them in L2.
@@ -50,12 +66,74 @@ __device__ __forceinline__ void tile_place(int64_t t, int64_t mt, int64_t nt, in
     m = (int)(band * BAND + (r - n * high));
 }
 
+// A warp's 32 x 64 values on their way to or from memory: row r's 16-byte piece j lies at place j ^ (r % 8) of its
+// 128 bytes, so that neither a lane's own row nor eight lanes' pieces of one row meet in a bank.
+__device__ __forceinline__ uint4 &piece(uint4 *buf, int r, int j) { return buf[r * 8 + (j ^ (r & 7))]; }
+__device__ __forceinline__ uint4 pack8(const float *v) {
+    uint4 p;
+    Vec16<bf16>::store(reinterpret_cast<bf16 *>(&p), v);
+    return p;
+}
+// Rows row0.. (up to M) and columns col.. (up to N) of a matrix from the buffer, in whole lines.
+__device__ __forceinline__ void flush(uint4 *buf, bf16 *out, int64_t ld, int64_t row0, int M, int col, int N, int lane) {
+    __syncwarp();
+    const int j = lane & 7, c = col + j * 8;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const int r = i * 4 + (lane >> 3);
+        if (row0 + r < M && c < N) {
+            const uint4 v = piece(buf, r, j);
+            bf16 *dst = out + (row0 + r) * ld + c;
+            if (c + 8 <= N) {
+                *reinterpret_cast<uint4 *>(dst) = v;
+            } else {
+                const bf16 *e = reinterpret_cast<const bf16 *>(&v);
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                    if (c + k < N) dst[k] = e[k];
+            }
+        }
+    }
+    __syncwarp();
+}
+// The same of an input, first into registers (what lies outside stays as it is), then into the buffer.
+__device__ __forceinline__ void fetch(uint4 (&raw)[8], const bf16 *in, int64_t ld, int64_t row0, int M, int col, int N, int lane) {
+    const int c = col + (lane & 7) * 8;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const int r = i * 4 + (lane >> 3);
+        if (row0 + r < M && c < N) {
+            const bf16 *src = in + (row0 + r) * ld + c;
+            if (c + 8 <= N) {
+                raw[i] = *reinterpret_cast<const uint4 *>(src);
+            } else {
+                bf16 e[8];
+#pragma unroll
+                for (int k = 0; k < 8; ++k) e[k] = c + k < N ? src[k] : __float2bfloat16_rn(0.f);
+                memcpy(&raw[i], e, 16);
+            }
+        }
+    }
+}
+
+// The bias of 16 of the warp's columns, from c on, onto v: lane l has those of columns 4 l .. 4 l + 3.
+__device__ __forceinline__ void add_bias(float *v, const uint2 &bias, int c) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const uint32_t a = __shfl_sync(0xffffffffu, bias.x, c / 4 + i), b = __shfl_sync(0xffffffffu, bias.y, c / 4 + i);
+        v[4 * i] += __uint_as_float(a << 16);
+        v[4 * i + 1] += __uint_as_float(a & 0xFFFF0000u);
+        v[4 * i + 2] += __uint_as_float(b << 16);
+        v[4 * i + 3] += __uint_as_float(b & 0xFFFF0000u);
+    }
+}
+
 template <int KIND>
 __global__ void __launch_bounds__(THREADS, 1)
-dense_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Epilogue ep, int M, int N, int K, int parts, int outs, int *status,
-             uint64_t wait_ns, int debug_stall) {
-    constexpr bool A_MN = KIND == DENSE_DW, B_MN = KIND == DENSE_DX || KIND == DENSE_DW;
-    constexpr int OUT_N = KIND == DENSE_GATED ? TN / 2 : TN;  // columns of the result a tile holds
+dense_kernel(const __grid_constant__ Maps maps0, const __grid_constant__ Maps maps1, const __grid_constant__ Epilogue ep0,
+             const __grid_constant__ Epilogue ep1, const __grid_constant__ Job job0, const __grid_constant__ Job job1,
+             int *status, uint64_t wait_ns, int debug_stall) {
+    constexpr int OUT_N = KIND == GATED ? TN / 2 : TN;  // columns of the result a tile holds
     extern __shared__ unsigned char smem_raw[];
     unsigned char *sm = reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                                           ~static_cast<uintptr_t>(1023));
@@ -91,49 +169,53 @@ dense_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Epilogue
     tc::fence_after_sync();
     wait_for_previous();
     const uint32_t tm = *tmem_sh;
-    const int64_t mt = (M + TM - 1) / TM, nt = (N + OUT_N - 1) / OUT_N, per = mt * nt, ntiles = per * outs;
-    const int kp = (K + TK - 1) / TK;
-    const int64_t kb = (int64_t)kp * parts;
+    const int64_t ntiles = job0.tiles + (KIND == BACKWARD ? job1.tiles : 0);
     const int64_t first = blockIdx.x / 2, step = gridDim.x / 2;
     const uint32_t sbase = tc::smem_u32(sm);
 
     if (warp == 0) {
         if (tc::elect_one()) {
-            uint32_t it = 0;
-            uint64_t t_last = 0;
+            uint32_t s = 0, ph = 0, used = 0;
             for (int64_t tile = first; tile < ntiles && !*err; tile += step) {
-                const int o = (int)(tile / per);
+                const bool second = KIND == BACKWARD && tile >= job0.tiles;
+                const Job &job = second ? job1 : job0;
+                const Maps &maps = second ? maps1 : maps0;
+                const int64_t t = second ? tile - job0.tiles : tile, per = job.mt * job.nt;
+                const int o = (int)(t / per);
                 int m, n;
-                tile_place(tile - o * per, mt, nt, m, n);
+                tile_place(t - o * per, job.mt, job.nt, m, n);
                 const int m0 = m * TM + (int)rank * 128;
-                const int n0 = KIND == DENSE_GATED ? n * OUT_N : n * TN + (int)rank * 128;
-                const CUtensorMap *ma = &maps.a[KIND == DENSE_DW ? o : 0], *mb = &maps.b[KIND == DENSE_GATED ? rank : 0];
-                int k0 = 0;
-                for (int64_t k = 0; k < kb; ++k, ++it, k0 += TK) {
-                    const uint32_t s = it % STAGES, ph = (it / STAGES) & 1u;
-                    if (!tc::mbar_wait(empty + s, ph ^ 1u, wait_ns, SLEEP_NS) || *err) {
-                        *err = 1;
-                        break;
-                    }
-                    if (KIND == DENSE_DX && k == kp) {
+                const int n0 = KIND == GATED ? n * OUT_N : n * TN + (int)rank * 128;
+                const CUtensorMap *ma = &maps.a[KIND == BACKWARD && job.dw ? o : 0], *mb = &maps.b[KIND == GATED ? rank : 0];
+                const int kp = (job.K + TK - 1) / TK;
+                for (int p = 0; p < job.parts && !*err; ++p) {
+                    if (KIND == BACKWARD && p) {
                         ma = &maps.a[1];
                         mb = &maps.b[1];
-                        k0 = 0;
                     }
-                    const uint32_t da = sbase + s * STAGE_BYTES, db = da + HALF_BYTES;
-                    const uint32_t bar = tc::map_to_rank(tc::smem_u32(full + s), 0);
-                    if (rank == 0) tc::mbar_expect_tx(full + s, 2 * STAGE_BYTES);
-                    if (A_MN) {
-                        tc::tma_load_2d_pair(da, ma, m0, k0, bar);
-                        tc::tma_load_2d_pair(da + HALF_BYTES / 2, ma, m0 + 64, k0, bar);
-                    } else {
-                        tc::tma_load_2d_pair(da, ma, k0, m0, bar);
-                    }
-                    if (B_MN) {
-                        tc::tma_load_2d_pair(db, mb, n0, k0, bar);
-                        tc::tma_load_2d_pair(db + HALF_BYTES / 2, mb, n0 + 64, k0, bar);
-                    } else {
-                        tc::tma_load_2d_pair(db, mb, k0, n0, bar);
+                    int k0 = 0;
+                    for (int k = 0; k < kp; ++k, k0 += TK) {
+                        if (!tc::mbar_wait(empty + s, ph ^ 1u, wait_ns, SLEEP_NS) || *err) {
+                            *err = 1;
+                            break;
+                        }
+                        const uint32_t da = sbase + s * STAGE_BYTES, db = da + HALF_BYTES;
+                        const uint32_t bar = tc::map_to_rank(tc::smem_u32(full + s), 0);
+                        if (rank == 0) tc::mbar_expect_tx(full + s, 2 * STAGE_BYTES);
+                        if (KIND == BACKWARD && job.dw) {
+                            tc::tma_load_2d_pair(da, ma, m0, k0, bar);
+                            tc::tma_load_2d_pair(da + HALF_BYTES / 2, ma, m0 + 64, k0, bar);
+                        } else {
+                            tc::tma_load_2d_pair(da, ma, k0, m0, bar);
+                        }
+                        if (KIND == BACKWARD) {
+                            tc::tma_load_2d_pair(db, mb, n0, k0, bar);
+                            tc::tma_load_2d_pair(db + HALF_BYTES / 2, mb, n0 + 64, k0, bar);
+                        } else {
+                            tc::tma_load_2d_pair(db, mb, k0, n0, bar);
+                        }
+                        used |= 1u << s;
+                        if (++s == STAGES) s = 0, ph ^= 1u;
                     }
                 }
             }
@@ -141,21 +223,24 @@ dense_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Epilogue
             // own and the other block's. Where something went wrong the two may have stopped at different
             // stages; a copy takes microseconds, so each then gives its last ones a millisecond.
             if (*err) {
-                t_last = tc::globaltimer_ns();
-                while (tc::globaltimer_ns() - t_last < 1000000u) __nanosleep(1000);
+                const uint64_t t0 = tc::globaltimer_ns();
+                while (tc::globaltimer_ns() - t0 < 1000000u) __nanosleep(1000);
             } else if (rank == 0) {
-                for (uint32_t s = 0; s < STAGES && s < it; ++s) {
-                    const uint32_t last = it - 1 - ((it - 1 - s) % STAGES);
-                    if (!tc::mbar_wait(full + s, (last / STAGES) & 1u, WAIT_NS, SLEEP_NS)) *err = 1;
-                }
+                for (uint32_t i = 0; i < STAGES; ++i)  // stages before s were last filled in phase ph, the others in the one before
+                    if ((used >> i & 1u) && !tc::mbar_wait(full + i, i < s ? ph : ph ^ 1u, WAIT_NS, SLEEP_NS)) *err = 1;
             }
         }
     } else if (warp == 1) {
         if (rank == 0 && tc::elect_one()) {
-            constexpr uint32_t id = tc::idesc(TM, TN, tc::FMT_BF16, A_MN, B_MN);
-            uint32_t it = 0, tcnt = 0;
+            uint32_t s = 0, ph = 0, tcnt = 0;
             if (debug_stall && !tc::mbar_wait(fin, 0, wait_ns, SLEEP_NS)) *err = 1;
             for (int64_t tile = first; tile < ntiles && !*err; tile += step, ++tcnt) {
+                const bool second = KIND == BACKWARD && tile >= job0.tiles;
+                const Job &job = second ? job1 : job0;
+                const bool a_mn = KIND == BACKWARD && job.dw;
+                constexpr bool b_mn = KIND == BACKWARD;
+                const uint32_t id = tc::idesc(TM, TN, tc::FMT_BF16, a_mn, b_mn);
+                const int64_t kb = (int64_t)((job.K + TK - 1) / TK) * job.parts;
                 const uint32_t acc = tcnt & 1u, aph = (tcnt >> 1) & 1u;
                 if (!tc::mbar_wait(acce + acc, aph ^ 1u, wait_ns, SLEEP_NS)) {
                     *err = 1;
@@ -164,8 +249,7 @@ dense_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Epilogue
                 tc::fence_after_sync();
                 const uint32_t d = tm + acc * TN;
                 bool ok = true;
-                for (int64_t k = 0; k < kb; ++k, ++it) {
-                    const uint32_t s = it % STAGES, ph = (it / STAGES) & 1u;
+                for (int64_t k = 0; k < kb; ++k) {
                     if (!tc::mbar_wait(full + s, ph, wait_ns, SLEEP_NS) || *err) {
                         ok = false;
                         break;
@@ -175,10 +259,11 @@ dense_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Epilogue
 #pragma unroll
                     for (uint32_t kk = 0; kk < TK / 16; ++kk)
                         tc::mma_bf16_ss_pair(
-                            d, A_MN ? tc::sdesc_sw128_mn(a + kk * 2048u, 8192u, 1024u) : tc::sdesc_sw128(a + kk * 32u),
-                            B_MN ? tc::sdesc_sw128_mn(b + kk * 2048u, 8192u, 1024u) : tc::sdesc_sw128(b + kk * 32u), id,
+                            d, a_mn ? tc::sdesc_sw128_mn(a + kk * 2048u, 8192u, 1024u) : tc::sdesc_sw128(a + kk * 32u),
+                            b_mn ? tc::sdesc_sw128_mn(b + kk * 2048u, 8192u, 1024u) : tc::sdesc_sw128(b + kk * 32u), id,
                             (k | kk) != 0);
                     tc::mma_commit_pair(empty + s, 3);
+                    if (++s == STAGES) s = 0, ph ^= 1u;
                 }
                 if (!ok) {
                     *err = 1;
@@ -191,56 +276,123 @@ dense_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Epilogue
         }
     } else {
         const uint32_t q = warp & 3;
-        constexpr int COLS = OUT_N / (EPI_WARPS / 4);  // columns of a warp
+        constexpr int COLS = OUT_N / (EPI_WARPS / 4);  // columns of a warp: 128, GATED 64
         const int c_first = (warp - 2) / 4 * COLS;
-        const uint64_t acc_ns = wait_ns + kb * 1000;  // a tile takes as long as its summed index is
+        uint4 *buf = reinterpret_cast<uint4 *>(sm + OFF_OUT) + (warp - 2) * 256;
         uint32_t tcnt = 0;
         for (int64_t tile = first; tile < ntiles; tile += step, ++tcnt) {
+            // every decision to stop is made per warp: the TMEM loads below are warp-collective
             if (__any_sync(0xffffffffu, *err != 0)) break;
+            const bool second = KIND == BACKWARD && tile >= job0.tiles;
+            const Job &job = second ? job1 : job0;
+            const Epilogue &ep = second ? ep1 : ep0;
+            const int64_t t = second ? tile - job0.tiles : tile, per = job.mt * job.nt;
+            const int o = (int)(t / per);
+            int m, n;
+            tile_place(t - o * per, job.mt, job.nt, m, n);
+            const int M = job.M, N = job.N, n0 = n * OUT_N + c_first;
+            const int64_t row0 = (int64_t)m * TM + rank * 128 + 32 * q;
+            uint4 res[8];  // the residual's next 64 columns
+            uint2 bias = make_uint2(0u, 0u);  // the bias of columns 4 lane .. 4 lane + 3 of the warp's
+            if (KIND == LINEAR && ep.residual) fetch(res, ep.residual, ep.ldr, row0, M, n0, N, lane);
+            if (KIND == LINEAR && ep.bias) {
+                const int c = n0 + lane * 4;
+                if (c + 4 <= N) {
+                    bias = *reinterpret_cast<const uint2 *>(ep.bias + c);
+                } else if (c < N) {
+                    bf16 e[4];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) e[k] = c + k < N ? ep.bias[c + k] : __float2bfloat16_rn(0.f);
+                    memcpy(&bias, e, 8);
+                }
+            }
             const uint32_t acc = tcnt & 1u, aph = (tcnt >> 1) & 1u;
+            const uint64_t acc_ns = wait_ns + (uint64_t)((job.K + TK - 1) / TK) * job.parts * 1000;  // as long as the sum is
             if (!__all_sync(0xffffffffu, tc::mbar_wait(accf + acc, aph, acc_ns, SLEEP_NS))) {
                 *err = 1;
                 break;
             }
             tc::fence_after_sync();
-            const int o = (int)(tile / per);
-            int m, n;
-            tile_place(tile - o * per, mt, nt, m, n);
-            const int n0 = n * OUT_N;
-            const int64_t row = (int64_t)m * TM + rank * 128 + 32 * q + lane;
+            const uint32_t src = tc::tmem_addr(tm + acc * TN, 32 * q, c_first);
 #pragma unroll 1
-            for (int c = c_first; c < c_first + COLS; c += 16) {
-                float v[16], u[16];
+            for (int c = 0; c < COLS; c += 64) {
                 const int col = n0 + c;
-                tc::tmem_ld16(tc::tmem_addr(tm + acc * TN, 32 * q, c), v);
-                if (KIND == DENSE_GATED) tc::tmem_ld16(tc::tmem_addr(tm + acc * TN, 32 * q, c + TN / 2), u);
-                tc::tmem_wait_ld();
-                if (row >= M || col >= N) continue;
-                if (KIND == DENSE_LINEAR) {
-                    if (ep.bias) {
-                        load16(ep.bias, col, N, u);
-#pragma unroll
-                        for (int e = 0; e < 16; ++e) v[e] += u[e];
+                if (KIND == LINEAR) {
+                    if (ep.saved) {  // z goes out first, y is made of it in a second look at the accumulator
+#pragma unroll 1
+                        for (int j = 0; j < 8; j += 2) {
+                            float v[16];
+                            tc::tmem_ld16(src + c + j * 8, v);
+                            tc::tmem_wait_ld();
+                            if (ep.bias) add_bias(v, bias, c + j * 8);
+                            piece(buf, lane, j) = pack8(v);
+                            piece(buf, lane, j + 1) = pack8(v + 8);
+                        }
+                        flush(buf, ep.saved, ep.lds, row0, M, col, N, lane);
                     }
-                    if (ep.saved) store16(ep.saved + row * ep.lds, col, N, v);
-                    if (ep.act != LA_ACT_NONE)
-#pragma unroll
-                        for (int e = 0; e < 16; ++e) v[e] = act_value(v[e], ep.act);
                     if (ep.residual) {
-                        load16(ep.residual + row * ep.ldr, col, N, u);
 #pragma unroll
-                        for (int e = 0; e < 16; ++e) v[e] += u[e];
+                        for (int i = 0; i < 8; ++i) piece(buf, i * 4 + (lane >> 3), lane & 7) = res[i];
+                        if (c + 64 < COLS) fetch(res, ep.residual, ep.ldr, row0, M, col + 64, N, lane);
+                        __syncwarp();
                     }
-                }
-                if (KIND == DENSE_GATED) {
+#pragma unroll 1
+                    for (int j = 0; j < 8; j += 2) {
+                        float v[16];
+                        tc::tmem_ld16(src + c + j * 8, v);
+                        tc::tmem_wait_ld();
+                        if (ep.bias) add_bias(v, bias, c + j * 8);
+                        if (ep.act != LA_ACT_NONE) {
+#pragma unroll
+                            for (int e = 0; e < 16; ++e) v[e] = act_value(v[e], ep.act);
+                        }
+                        if (ep.residual) {
+                            float u[16];
+                            Vec16<bf16>::load(reinterpret_cast<bf16 *>(&piece(buf, lane, j)), u);
+                            Vec16<bf16>::load(reinterpret_cast<bf16 *>(&piece(buf, lane, j + 1)), u + 8);
+#pragma unroll
+                            for (int e = 0; e < 16; ++e) v[e] += u[e];
+                        }
+                        piece(buf, lane, j) = pack8(v);
+                        piece(buf, lane, j + 1) = pack8(v + 8);
+                    }
+                } else if (KIND == GATED) {
                     if (ep.saved) {
-                        store16(ep.saved + row * ep.lds, col, N, v);
-                        store16(ep.saved + row * ep.lds + ep.half, col, N, u);
+#pragma unroll 1
+                        for (int half = 0; half < 2; ++half) {
+#pragma unroll 1
+                            for (int j = 0; j < 8; j += 2) {
+                                float v[16];
+                                tc::tmem_ld16(src + half * (TN / 2) + j * 8, v);
+                                tc::tmem_wait_ld();
+                                piece(buf, lane, j) = pack8(v);
+                                piece(buf, lane, j + 1) = pack8(v + 8);
+                            }
+                            flush(buf, ep.saved + half * ep.half, ep.lds, row0, M, col, N, lane);
+                        }
                     }
+#pragma unroll 1
+                    for (int j = 0; j < 8; j += 2) {
+                        float v[16], u[16];
+                        tc::tmem_ld16(src + j * 8, v);
+                        tc::tmem_ld16(src + TN / 2 + j * 8, u);
+                        tc::tmem_wait_ld();
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) v[e] = act_value(v[e], ep.act) * u[e];
+                        for (int e = 0; e < 16; ++e) v[e] = act_value(v[e], ep.act) * u[e];
+                        piece(buf, lane, j) = pack8(v);
+                        piece(buf, lane, j + 1) = pack8(v + 8);
+                    }
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 8; j += 2) {
+                        float v[16];
+                        tc::tmem_ld16(src + c + j * 8, v);
+                        tc::tmem_wait_ld();
+                        piece(buf, lane, j) = pack8(v);
+                        piece(buf, lane, j + 1) = pack8(v + 8);
+                    }
                 }
-                store16(ep.out[o] + row * ep.ldo[o], col, N, v);
+                flush(buf, ep.out[o], ep.ldo[o], row0, M, col, N, lane);
             }
             tc::fence_before_sync();
             __syncwarp();
@@ -278,18 +430,27 @@ int resident_pairs() {
     return n;
 }
 
+Job make_job(const DenseArgs &a) {
+    const int out_n = a.kind == DENSE_GATED ? TN / 2 : TN;
+    Job j{a.M, a.N, a.K, a.kind == DENSE_DX ? a.count : 1, a.kind == DENSE_DW, 0, 0, 0};
+    j.mt = (a.M + TM - 1) / TM;
+    j.nt = (a.N + out_n - 1) / out_n;
+    j.tiles = j.mt * j.nt * (a.kind == DENSE_DW ? a.count : 1);
+    return j;
+}
+
+// One product, or (BACKWARD) two.
 template <int KIND>
-cudaError_t launch(const DenseArgs &a, cudaStream_t st) {
-    constexpr bool A_MN = KIND == DENSE_DW, B_MN = KIND == DENSE_DX || KIND == DENSE_DW;
-    constexpr int OUT_N = KIND == DENSE_GATED ? TN / 2 : TN;
-    Maps maps;
-    if (!make_maps(&maps, a, A_MN, B_MN, 128, 128)) return cudaErrorInvalidValue;
-    const Epilogue ep = make_epilogue(a);
-    const int parts = KIND == DENSE_DX ? a.count : 1, outs = KIND == DENSE_DW ? a.count : 1;
-    const int64_t ntiles = (int64_t)((a.M + TM - 1) / TM) * ((a.N + OUT_N - 1) / OUT_N) * outs;
-    const int pairs = resident_pairs<KIND>();
-    return launch_overlapped(dense_kernel<KIND>, dim3(2 * (int)(ntiles < pairs ? ntiles : pairs)), dim3(THREADS), SMEM, 2, st,
-                             maps, ep, a.M, a.N, a.K, parts, outs, a.status, a.wait_ns ? a.wait_ns : WAIT_NS, a.debug_stall);
+cudaError_t launch(const DenseArgs &a, const DenseArgs *b, cudaStream_t st) {
+    Maps maps[2];
+    const bool mn = KIND == BACKWARD;
+    if (!make_maps(&maps[0], a, a.kind == DENSE_DW, mn, 128, 128)) return cudaErrorInvalidValue;
+    if (b && !make_maps(&maps[1], *b, b->kind == DENSE_DW, mn, 128, 128)) return cudaErrorInvalidValue;
+    const Job j0 = make_job(a), j1 = b ? make_job(*b) : Job{};
+    const int64_t tiles = j0.tiles + j1.tiles, pairs = resident_pairs<KIND>();
+    return launch_overlapped(dense_kernel<KIND>, dim3(2 * (int)(tiles < pairs ? tiles : pairs)), dim3(THREADS), SMEM, 2, st, maps[0],
+                             b ? maps[1] : maps[0], make_epilogue(a), make_epilogue(b ? *b : a), j0, j1, a.status,
+                             a.wait_ns ? a.wait_ns : WAIT_NS, a.debug_stall);
 }
 
 }  // namespace
@@ -297,11 +458,19 @@ cudaError_t launch(const DenseArgs &a, cudaStream_t st) {
 cudaError_t launch_dense(const DenseArgs &a, cudaStream_t st) {
     if (dense_split_serves(a)) return launch_dense_split(a, st);
     switch (a.kind) {
-        case DENSE_LINEAR: return launch<DENSE_LINEAR>(a, st);
-        case DENSE_GATED: return launch<DENSE_GATED>(a, st);
-        case DENSE_DX: return launch<DENSE_DX>(a, st);
-        default: return launch<DENSE_DW>(a, st);
+        case DENSE_LINEAR: return launch<LINEAR>(a, nullptr, st);
+        case DENSE_GATED: return launch<GATED>(a, nullptr, st);
+        default: return launch<BACKWARD>(a, nullptr, st);
     }
+}
+
+cudaError_t launch_dense_pair(const DenseArgs &dx, const DenseArgs &dw, cudaStream_t st) {
+    if (dense_split_serves(dx) || dense_split_serves(dw)) {
+        const cudaError_t e = launch_dense(dx, st);
+        return e != cudaSuccess ? e : launch_dense(dw, st);
+    }
+    const bool dx_first = (int64_t)dx.K * dx.count >= dw.K;
+    return dx_first ? launch<BACKWARD>(dx, &dw, st) : launch<BACKWARD>(dw, &dx, st);
 }
 
 }  // namespace la

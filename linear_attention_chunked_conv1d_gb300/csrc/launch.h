@@ -289,6 +289,8 @@ struct DenseArgs {
     int debug_stall;   // test knob: one wait on a barrier that nothing completes
 };
 cudaError_t launch_dense(const DenseArgs &a, cudaStream_t st);
+// DENSE_DX and DENSE_DW of one backward pass (status, waits and knob: dx's).
+cudaError_t launch_dense_pair(const DenseArgs &dx, const DenseArgs &dw, cudaStream_t st);
 // Those with few output tiles: the summed index split over a cluster's blocks (dense_split.cu).
 bool dense_split_serves(const DenseArgs &a);
 cudaError_t launch_dense_split(const DenseArgs &a, cudaStream_t st);
