@@ -211,9 +211,7 @@ dense_split_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Ep
                 for (int e = 0; e < 4; ++e) v[e] += u[e];
             }
             if (ep.saved) store4(ep.saved + row * ep.lds, col, N, v);
-            if (ep.act != LA_ACT_NONE)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) v[e] = act_value(v[e], ep.act);
+            act_values(v, ep.act);
             if (ep.residual) {
                 load4(ep.residual + row * ep.ldr, col, N, u);
 #pragma unroll
@@ -225,8 +223,9 @@ dense_split_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Ep
                 store4(ep.saved + row * ep.lds, col, N, v);
                 store4(ep.saved + row * ep.lds + ep.half, col, N, u);
             }
+            act_values(v, ep.act);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) v[e] = act_value(v[e], ep.act) * u[e];
+            for (int e = 0; e < 4; ++e) v[e] *= u[e];
         }
         store4(ep.out[o] + row * ep.ldo[o], col, N, v);
     }

@@ -342,10 +342,7 @@ dense_kernel(const __grid_constant__ Maps maps0, const __grid_constant__ Maps ma
                         tc::tmem_ld16(src + c + j * 8, v);
                         tc::tmem_wait_ld();
                         if (ep.bias) add_bias(v, bias, c + j * 8);
-                        if (ep.act != LA_ACT_NONE) {
-#pragma unroll
-                            for (int e = 0; e < 16; ++e) v[e] = act_value(v[e], ep.act);
-                        }
+                        act_values(v, ep.act);
                         if (ep.residual) {
                             float u[16];
                             Vec16<bf16>::load(reinterpret_cast<bf16 *>(&piece(buf, lane, j)), u);
@@ -377,8 +374,9 @@ dense_kernel(const __grid_constant__ Maps maps0, const __grid_constant__ Maps ma
                         tc::tmem_ld16(src + j * 8, v);
                         tc::tmem_ld16(src + TN / 2 + j * 8, u);
                         tc::tmem_wait_ld();
+                        act_values(v, ep.act);
 #pragma unroll
-                        for (int e = 0; e < 16; ++e) v[e] = act_value(v[e], ep.act) * u[e];
+                        for (int e = 0; e < 16; ++e) v[e] *= u[e];
                         piece(buf, lane, j) = pack8(v);
                         piece(buf, lane, j + 1) = pack8(v + 8);
                     }

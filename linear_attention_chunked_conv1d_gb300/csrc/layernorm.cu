@@ -65,7 +65,6 @@ __device__ __forceinline__ void widen(const uint4 &v, uint64_t (&f)[4]) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) f[i] = pk2(__uint_as_float(u[i] << 16), __uint_as_float(u[i] & 0xFFFF0000u));
 }
-__device__ __forceinline__ uint64_t both(float x) { return pk2(x, x); }
 __device__ __forceinline__ float sum_of(uint64_t v) {
     float a, b;
     upk2(v, a, b);
