@@ -1,5 +1,7 @@
 // Activations of the dense layers' calls (la_linear, la_gated_ffn) and their derivatives, in fp32.
 #pragma once
+#include <type_traits>
+
 #include "common.cuh"
 
 namespace la {
@@ -44,48 +46,66 @@ __device__ __forceinline__ uint64_t normal2(uint64_t z, uint64_t &e) {
     return pk2(z0 < 0.f ? q0 : 1.f - q0, z1 < 0.f ? q1 : 1.f - q1);
 }
 
-// act(z) of a pair. GELU's tanh form is z logistic(2 c (z + a z^3)).
-__device__ __forceinline__ uint64_t act_value2(uint64_t z, int act) {
-    uint64_t e;
-    switch (act) {
-        case LA_ACT_RELU: return each(z, [](float v) { return v < 0.f ? 0.f : v; });  // NaN stays
-        case LA_ACT_GELU: return mul2(z, normal2(z, e));
-        case LA_ACT_GELU_TANH:
-            return mul2(z, logistic2(mul2(mul2(z, both(2.f * kGeluC)), fma2(mul2(z, both(kGeluA)), z, both(1.f)))));
-        case LA_ACT_SILU: return mul2(z, logistic2(z));
-        default: return z;
-    }
-}
-// act(z) and act'(z) of a pair. Where a factor of z meets one that has vanished, z is cut off first: 0 times
-// infinity would be NaN.
-__device__ __forceinline__ uint64_t act_both2(uint64_t z, int act, uint64_t &slope) {
+// act(z), and act'(z), of a pair. GELU's tanh form is z logistic(2 c (z + a z^3)). Where a factor of z meets one that has
+// vanished, z is cut off first: 0 times infinity would be NaN.
+template <int ACT>
+__device__ __forceinline__ uint64_t act_pair(uint64_t z, uint64_t &slope) {
     uint64_t s, e;
     const uint64_t c = each(z, [](float v) { return fminf(fmaxf(v, -200.f), 200.f); });
+    if constexpr (ACT == LA_ACT_RELU) {
+        slope = each(z, [](float v) { return v <= 0.f ? 0.f : 1.f; });
+        return each(z, [](float v) { return v < 0.f ? 0.f : v; });  // NaN stays
+    } else if constexpr (ACT == LA_ACT_GELU) {
+        s = normal2(z, e);
+        slope = fma2(mul2(c, both(kInvSqrt2Pi)), e, s);
+        return mul2(z, s);
+    } else if constexpr (ACT == LA_ACT_GELU_TANH) {
+        s = logistic2(mul2(mul2(z, both(2.f * kGeluC)), fma2(mul2(z, both(kGeluA)), z, both(1.f))));
+        const uint64_t rest = fma2(s, both(-1.f), both(1.f));
+        slope = fma2(mul2(c, mul2(s, rest)), fma2(mul2(c, both(6.f * kGeluC * kGeluA)), c, both(2.f * kGeluC)), s);
+        return mul2(z, s);
+    } else if constexpr (ACT == LA_ACT_SILU) {
+        s = logistic2(z);
+        slope = mul2(s, fma2(c, fma2(s, both(-1.f), both(1.f)), both(1.f)));
+        return mul2(z, s);
+    } else {
+        slope = both(1.f);
+        return z;
+    }
+}
+// f(integral_constant<int, act>): one branch around the values of a thread, so that their chains run side by side.
+template <class F>
+__device__ __forceinline__ void with_act(int act, F &&f) {
     switch (act) {
-        case LA_ACT_RELU:
-            slope = each(z, [](float v) { return v <= 0.f ? 0.f : 1.f; });
-            return each(z, [](float v) { return v < 0.f ? 0.f : v; });
-        case LA_ACT_GELU:
-            s = normal2(z, e);
-            slope = fma2(mul2(c, both(kInvSqrt2Pi)), e, s);
-            return mul2(z, s);
-        case LA_ACT_GELU_TANH: {
-            s = logistic2(mul2(mul2(z, both(2.f * kGeluC)), fma2(mul2(z, both(kGeluA)), z, both(1.f))));
-            const uint64_t rest = fma2(s, both(-1.f), both(1.f));
-            slope = fma2(mul2(c, mul2(s, rest)), fma2(mul2(c, both(6.f * kGeluC * kGeluA)), c, both(2.f * kGeluC)), s);
-            return mul2(z, s);
-        }
-        case LA_ACT_SILU:
-            s = logistic2(z);
-            slope = mul2(s, fma2(c, fma2(s, both(-1.f), both(1.f)), both(1.f)));
-            return mul2(z, s);
-        default: slope = both(1.f); return z;
+        case LA_ACT_RELU: f(std::integral_constant<int, LA_ACT_RELU>{}); break;
+        case LA_ACT_GELU: f(std::integral_constant<int, LA_ACT_GELU>{}); break;
+        case LA_ACT_GELU_TANH: f(std::integral_constant<int, LA_ACT_GELU_TANH>{}); break;
+        case LA_ACT_SILU: f(std::integral_constant<int, LA_ACT_SILU>{}); break;
+        default: f(std::integral_constant<int, LA_ACT_NONE>{}); break;
     }
 }
 template <int N>
 __device__ __forceinline__ void act_values(float (&v)[N], int act) {
+    if (act == LA_ACT_NONE) return;
+    with_act(act, [&](auto which) {
 #pragma unroll
-    for (int i = 0; i < N; i += 2) upk2(act_value2(pk2(v[i], v[i + 1]), act), v[i], v[i + 1]);
+        for (int i = 0; i < N; i += 2) {
+            uint64_t slope;
+            upk2(act_pair<which>(pk2(v[i], v[i + 1]), slope), v[i], v[i + 1]);
+        }
+    });
+}
+// value and slope of N values
+template <int N>
+__device__ __forceinline__ void act_slopes(float (&v)[N], float (&slope)[N], int act) {
+    with_act(act, [&](auto which) {
+#pragma unroll
+        for (int i = 0; i < N; i += 2) {
+            uint64_t s;
+            upk2(act_pair<which>(pk2(v[i], v[i + 1]), s), v[i], v[i + 1]);
+            upk2(s, slope[i], slope[i + 1]);
+        }
+    });
 }
 
 // N values (16 bytes) of a row from column c on, of which those at or past `width` read as zero; and the

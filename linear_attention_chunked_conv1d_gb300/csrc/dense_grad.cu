@@ -32,12 +32,10 @@ linear_grad_kernel(const bf16 *__restrict__ saved, const bf16 *__restrict__ dy, 
             if (saved) {
                 float z[8];
                 load_piece(saved + r * lds, c, N, z);
+                float slope[8];
+                act_slopes(z, slope, act);
 #pragma unroll
-                for (int e = 0; e < 8; e += 2) {
-                    uint64_t slope;
-                    act_both2(pk2(z[e], z[e + 1]), act, slope);
-                    upk2(mul2(pk2(d[e], d[e + 1]), slope), d[e], d[e + 1]);
-                }
+                for (int e = 0; e < 8; ++e) d[e] *= slope[e];
                 store_piece(dz + r * ldz, c, N, d);
             }
 #pragma unroll
@@ -86,12 +84,12 @@ gated_grad_kernel(const bf16 *__restrict__ saved, const bf16 *__restrict__ dh, b
         load_piece(s, c, F, gate);
         load_piece(s + half, c, F, up);
         load_piece(dh + r * lddh, c, F, g);
+        float slope[8];
+        act_slopes(gate, slope, act);
 #pragma unroll
-        for (int e = 0; e < 8; e += 2) {
-            uint64_t slope;
-            const uint64_t d = pk2(g[e], g[e + 1]), value = act_both2(pk2(gate[e], gate[e + 1]), act, slope);
-            upk2(mul2(mul2(pk2(up[e], up[e + 1]), d), slope), up[e], up[e + 1]);
-            upk2(mul2(value, d), gate[e], gate[e + 1]);
+        for (int e = 0; e < 8; ++e) {
+            up[e] *= g[e] * slope[e];
+            gate[e] *= g[e];
         }
         store_piece(o, c, F, up);
         store_piece(o + half, c, F, gate);

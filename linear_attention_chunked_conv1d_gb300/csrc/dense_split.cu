@@ -191,43 +191,54 @@ dense_split_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Ep
     const int f = nr * (int)rank / plan.split, l = nr * ((int)rank + 1) / plan.split;
     constexpr int LANES = OUT_P / 4, ROWS_AT = 32 / LANES;  // lanes and rows of a warp at one time
     const int c4 = lane % LANES * 4, col = p0 + c4;
-    for (int r = f + warp * ROWS_AT + lane / LANES; r < l && col < N && !*err; r += THREADS / 32 * ROWS_AT) {
-        const uint32_t at = rbase + (r * PT + c4) * 4;
-        float v[4] = {}, u[4] = {};
+    constexpr int AT = THREADS / 32 * ROWS_AT, U = 4;  // rows of the block at one time; how many times over
+    for (int first = f + warp * ROWS_AT + lane / LANES; first < l && col < N && !*err; first += U * AT) {
+        float v[U][4] = {}, u[U][4] = {}, res[U][4];
+        if (KIND == DENSE_LINEAR && ep.residual) {
+#pragma unroll
+            for (int i = 0; i < U; ++i)
+                if (first + i * AT < l) load4(ep.residual + (r0 + first + i * AT) * ep.ldr, col, N, res[i]);
+        }
+        float bias[4] = {};
+        if (KIND == DENSE_LINEAR && ep.bias) load4(ep.bias, col, N, bias);
         for (int k = 0; k < plan.split; ++k) {
-            const uint32_t src = plan.split > 1 ? tc::map_to_rank(at, k) : at;
-            const float4 t = ld_cluster(src);
-            v[0] += t.x; v[1] += t.y; v[2] += t.z; v[3] += t.w;
+            const uint32_t at = rbase + (first * PT + c4) * 4, src = plan.split > 1 ? tc::map_to_rank(at, k) : at;
+#pragma unroll
+            for (int i = 0; i < U; ++i)
+                if (first + i * AT < l) {
+                    const float4 t = ld_cluster(src + i * AT * PT * 4);
+                    v[i][0] += t.x; v[i][1] += t.y; v[i][2] += t.z; v[i][3] += t.w;
+                    if (KIND == DENSE_GATED) {
+                        const float4 t2 = ld_cluster(src + i * AT * PT * 4 + PT / 2 * 4);
+                        u[i][0] += t2.x; u[i][1] += t2.y; u[i][2] += t2.z; u[i][3] += t2.w;
+                    }
+                }
+        }
+#pragma unroll
+        for (int i = 0; i < U; ++i) {
+            if (first + i * AT >= l) break;
+            const int64_t row = r0 + first + i * AT;
+            if (KIND == DENSE_LINEAR) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) v[i][e] += bias[e];
+                if (ep.saved) store4(ep.saved + row * ep.lds, col, N, v[i]);
+                act_values(v[i], ep.act);
+                if (ep.residual) {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) v[i][e] += res[i][e];
+                }
+            }
             if (KIND == DENSE_GATED) {
-                const float4 t2 = ld_cluster(src + PT / 2 * 4);
-                u[0] += t2.x; u[1] += t2.y; u[2] += t2.z; u[3] += t2.w;
-            }
-        }
-        const int64_t row = r0 + r;
-        if (KIND == DENSE_LINEAR) {
-            if (ep.bias) {
-                load4(ep.bias, col, N, u);
+                if (ep.saved) {
+                    store4(ep.saved + row * ep.lds, col, N, v[i]);
+                    store4(ep.saved + row * ep.lds + ep.half, col, N, u[i]);
+                }
+                act_values(v[i], ep.act);
 #pragma unroll
-                for (int e = 0; e < 4; ++e) v[e] += u[e];
+                for (int e = 0; e < 4; ++e) v[i][e] *= u[i][e];
             }
-            if (ep.saved) store4(ep.saved + row * ep.lds, col, N, v);
-            act_values(v, ep.act);
-            if (ep.residual) {
-                load4(ep.residual + row * ep.ldr, col, N, u);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) v[e] += u[e];
-            }
+            store4(ep.out[o] + row * ep.ldo[o], col, N, v[i]);
         }
-        if (KIND == DENSE_GATED) {
-            if (ep.saved) {
-                store4(ep.saved + row * ep.lds, col, N, v);
-                store4(ep.saved + row * ep.lds + ep.half, col, N, u);
-            }
-            act_values(v, ep.act);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) v[e] *= u[e];
-        }
-        store4(ep.out[o] + row * ep.ldo[o], col, N, v);
     }
     if (plan.split > 1) tc::cluster_sync();  // the others have read this block's part
     if (*err && threadIdx.x == 0) raise_status(status, LA_DEV_TIMEOUT);

@@ -74,6 +74,11 @@ __device__ __forceinline__ uint4 pack8(const float *v) {
     Vec16<bf16>::store(reinterpret_cast<bf16 *>(&p), v);
     return p;
 }
+template <int V>
+__device__ __forceinline__ void put(uint4 *buf, int r, int j, const float (&v)[V]) {
+#pragma unroll
+    for (int i = 0; i < V / 8; ++i) piece(buf, r, j + i) = pack8(v + 8 * i);
+}
 // Rows row0.. (up to M) and columns col.. (up to N) of a matrix from the buffer, in whole lines.
 __device__ __forceinline__ void flush(uint4 *buf, bf16 *out, int64_t ld, int64_t row0, int M, int col, int N, int lane) {
     __syncwarp();
@@ -116,10 +121,10 @@ __device__ __forceinline__ void fetch(uint4 (&raw)[8], const bf16 *in, int64_t l
     }
 }
 
-// The bias of 16 of the warp's columns, from c on, onto v: lane l has those of columns 4 l .. 4 l + 3.
-__device__ __forceinline__ void add_bias(float *v, const uint2 &bias, int c) {
+// The bias of 32 of the warp's columns, from c on, onto v: lane l has those of columns 4 l .. 4 l + 3.
+__device__ __forceinline__ void add_bias(float (&v)[32], const uint2 &bias, int c) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < 8; ++i) {
         const uint32_t a = __shfl_sync(0xffffffffu, bias.x, c / 4 + i), b = __shfl_sync(0xffffffffu, bias.y, c / 4 + i);
         v[4 * i] += __uint_as_float(a << 16);
         v[4 * i + 1] += __uint_as_float(a & 0xFFFF0000u);
@@ -320,13 +325,13 @@ dense_kernel(const __grid_constant__ Maps maps0, const __grid_constant__ Maps ma
                 if (KIND == LINEAR) {
                     if (ep.saved) {  // z goes out first, y is made of it in a second look at the accumulator
 #pragma unroll 1
-                        for (int j = 0; j < 8; j += 2) {
-                            float v[16];
+                        for (int j = 0; j < 8; j += 4) {
+                            float v[32];
                             tc::tmem_ld16(src + c + j * 8, v);
+                            tc::tmem_ld16(src + c + j * 8 + 16, v + 16);
                             tc::tmem_wait_ld();
                             if (ep.bias) add_bias(v, bias, c + j * 8);
-                            piece(buf, lane, j) = pack8(v);
-                            piece(buf, lane, j + 1) = pack8(v + 8);
+                            put(buf, lane, j, v);
                         }
                         flush(buf, ep.saved, ep.lds, row0, M, col, N, lane);
                     }
@@ -337,33 +342,35 @@ dense_kernel(const __grid_constant__ Maps maps0, const __grid_constant__ Maps ma
                         __syncwarp();
                     }
 #pragma unroll 1
-                    for (int j = 0; j < 8; j += 2) {
-                        float v[16];
+                    for (int j = 0; j < 8; j += 4) {
+                        float v[32];
                         tc::tmem_ld16(src + c + j * 8, v);
+                        tc::tmem_ld16(src + c + j * 8 + 16, v + 16);
                         tc::tmem_wait_ld();
                         if (ep.bias) add_bias(v, bias, c + j * 8);
                         act_values(v, ep.act);
                         if (ep.residual) {
-                            float u[16];
-                            Vec16<bf16>::load(reinterpret_cast<bf16 *>(&piece(buf, lane, j)), u);
-                            Vec16<bf16>::load(reinterpret_cast<bf16 *>(&piece(buf, lane, j + 1)), u + 8);
 #pragma unroll
-                            for (int e = 0; e < 16; ++e) v[e] += u[e];
+                            for (int i = 0; i < 4; ++i) {
+                                float u[8];
+                                Vec16<bf16>::load(reinterpret_cast<bf16 *>(&piece(buf, lane, j + i)), u);
+#pragma unroll
+                                for (int e = 0; e < 8; ++e) v[8 * i + e] += u[e];
+                            }
                         }
-                        piece(buf, lane, j) = pack8(v);
-                        piece(buf, lane, j + 1) = pack8(v + 8);
+                        put(buf, lane, j, v);
                     }
                 } else if (KIND == GATED) {
                     if (ep.saved) {
 #pragma unroll 1
                         for (int half = 0; half < 2; ++half) {
-#pragma unroll 1
-                            for (int j = 0; j < 8; j += 2) {
-                                float v[16];
+#pragma unroll
+                            for (int j = 0; j < 8; j += 4) {
+                                float v[32];
                                 tc::tmem_ld16(src + half * (TN / 2) + j * 8, v);
+                                tc::tmem_ld16(src + half * (TN / 2) + j * 8 + 16, v + 16);
                                 tc::tmem_wait_ld();
-                                piece(buf, lane, j) = pack8(v);
-                                piece(buf, lane, j + 1) = pack8(v + 8);
+                                put(buf, lane, j, v);
                             }
                             flush(buf, ep.saved + half * ep.half, ep.lds, row0, M, col, N, lane);
                         }
@@ -377,17 +384,16 @@ dense_kernel(const __grid_constant__ Maps maps0, const __grid_constant__ Maps ma
                         act_values(v, ep.act);
 #pragma unroll
                         for (int e = 0; e < 16; ++e) v[e] *= u[e];
-                        piece(buf, lane, j) = pack8(v);
-                        piece(buf, lane, j + 1) = pack8(v + 8);
+                        put(buf, lane, j, v);
                     }
                 } else {
 #pragma unroll
-                    for (int j = 0; j < 8; j += 2) {
-                        float v[16];
+                    for (int j = 0; j < 8; j += 4) {
+                        float v[32];
                         tc::tmem_ld16(src + c + j * 8, v);
+                        tc::tmem_ld16(src + c + j * 8 + 16, v + 16);
                         tc::tmem_wait_ld();
-                        piece(buf, lane, j) = pack8(v);
-                        piece(buf, lane, j + 1) = pack8(v + 8);
+                        put(buf, lane, j, v);
                     }
                 }
                 flush(buf, ep.out[o], ep.ldo[o], row0, M, col, N, lane);
