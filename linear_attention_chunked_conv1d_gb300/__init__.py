@@ -749,17 +749,29 @@ def layernorm_rows(x, w, b=None, y=None, *, stats=None, eps=1e-5, stream=None):
     8192, rows on 16 bytes; y may be x, and defaults to a new tensor), w, b [width]. stats: fp32
     [rows][2] that receives mean and 1 / sqrt(var + eps), when layernorm_rows_backward is to follow.
     Returns y."""
-    dev = _on_gpu(x)
+    dev, dt = x.get_device(), x.dtype
     rows, width = x.shape
-    dt = x.dtype
-    code = _dtype_code(x)
     if y is None:
         y = _rows_like((rows, width), dt, x.device, stream)
+    (xs, x1), (ys, y1) = x.stride(), y.stride()
+    # As in gated_scan: one look at everything, and only where something is unusual the checks that say what.
+    if not (dev >= 0 and dev == _current_device() and x1 == y1 == 1 and y.shape == (rows, width)
+            and y.dtype is dt and y.get_device() == dev and w.dtype is dt and w.shape == (width,)
+            and w.is_contiguous() and w.get_device() == dev
+            and (b is None or (b.dtype is dt and b.shape == (width,) and b.is_contiguous() and b.get_device() == dev))
+            and (stats is None or (stats.dtype is torch.float32 and stats.shape == (rows, 2)
+                                   and stats.is_contiguous() and stats.get_device() == dev))):
+        _on_gpu(x)
+        xs, ys = _matrix16("x", x, rows, width, dt, dev), _matrix16("y", y, rows, width, dt, dev)
+        _dense("w", w, (width,), dt, dev)
+        _vector("b", b, width, dt, dev)
+        if stats is not None:
+            _dense("stats", stats, (rows, 2), torch.float32, dev)
+    if rows == 1:  # a single row's stride says nothing
+        xs = ys = (width + 7) // 8 * 8
     _check(_load().la_layernorm_rows(
-        x.data_ptr(), _vector("w", w, width, dt, dev), _vector("b", b, width, dt, dev), y.data_ptr(),
-        None if stats is None else _dense("stats", stats, (rows, 2), torch.float32, dev), rows, width,
-        _matrix16("x", x, rows, width, dt, dev), _matrix16("y", y, rows, width, dt, dev), eps, code,
-        _stream_on(stream, dev)))
+        x.data_ptr(), w.data_ptr(), None if b is None else b.data_ptr(), y.data_ptr(),
+        None if stats is None else stats.data_ptr(), rows, width, xs, ys, eps, _dtype_code(x), _stream_on(stream, dev)))
     return y
 
 
@@ -803,19 +815,39 @@ def linear(x, w, y=None, *, bias=None, residual=None, act="none", saved=None, st
     x [M][K], w [N][K] (a linear layer's [out][in] weight), bias [N], residual and y [M][N] (y may be
     residual, and defaults to a new tensor); any sizes, rows on 16 bytes. act: one of LA_ACTIVATIONS.
     saved: a buffer of linear_saved_bytes(...) when linear_backward is to follow. Returns y."""
-    dev = _on_gpu(x)
+    dev, bf16 = x.get_device(), torch.bfloat16
     M, K = x.shape
     N = w.shape[0]
-    bf16 = torch.bfloat16
     if y is None:
         y = _rows_like((M, N), bf16, x.device, stream)
-    sv, sv_bytes = _room("saved", saved, dev)
+    (xs, x1), (ws, w1), (ys, y1) = x.stride(), w.stride(), y.stride()
+    rs, r1 = (ys, 1) if residual is None else residual.stride()
+    # As in gated_scan: one look at everything, and only where something is unusual the checks that say what.
+    if not (dev >= 0 and dev == _current_device() and x.dtype is bf16 and w.dtype is bf16 and y.dtype is bf16
+            and w.shape == (N, K) and y.shape == (M, N) and x1 == w1 == y1 == r1 == 1
+            and w.get_device() == dev and y.get_device() == dev
+            and (residual is None or (residual.dtype is bf16 and residual.shape == (M, N)
+                                      and residual.get_device() == dev))
+            and (bias is None or (bias.dtype is bf16 and bias.shape == (N,) and bias.is_contiguous()
+                                  and bias.get_device() == dev))
+            and (saved is None or (saved.is_contiguous() and saved.get_device() == dev))):
+        _on_gpu(x)
+        xs, ws, ys = (_matrix16("x", x, M, K, bf16, dev), _matrix16("w", w, N, K, bf16, dev),
+                      _matrix16("y", y, M, N, bf16, dev))
+        rs = 0 if residual is None else _matrix16("residual", residual, M, N, bf16, dev)
+        _vector("bias", bias, N, bf16, dev)
+        _room("saved", saved, dev)
+    if M == 1:  # a single row's stride says nothing
+        xs, ys = (K + 7) // 8 * 8, (N + 7) // 8 * 8
+        rs = ys
+    if N == 1:
+        ws = (K + 7) // 8 * 8
+    code = LA_ACTIVATIONS.get(act)
     _check(_load().la_linear(
-        x.data_ptr(), w.data_ptr(), _vector("bias", bias, N, bf16, dev),
-        None if residual is None else residual.data_ptr(), y.data_ptr(), sv, sv_bytes, M, N, K,
-        _matrix16("x", x, M, K, bf16, dev), _matrix16("w", w, N, K, bf16, dev),
-        0 if residual is None else _matrix16("residual", residual, M, N, bf16, dev),
-        _matrix16("y", y, M, N, bf16, dev), _act_code(act), _stream_on(stream, dev)))
+        x.data_ptr(), w.data_ptr(), None if bias is None else bias.data_ptr(),
+        None if residual is None else residual.data_ptr(), y.data_ptr(), None if saved is None else saved.data_ptr(),
+        0 if saved is None else saved.numel() * saved.element_size(), M, N, K, xs, ws, rs, ys,
+        _act_code(act) if code is None else code, _stream_on(stream, dev)))
     return y
 
 
@@ -856,18 +888,31 @@ def gated_ffn(x, w_gate, w_up, h=None, *, act="silu", saved=None, stream=None):
     tensor by default): bf16, any sizes, rows on 16 bytes. act: one of LA_ACTIVATIONS. saved: a buffer
     of gated_ffn_saved_bytes(...) when gated_ffn_backward is to follow. The projection back is
     linear(h, w_down, residual=...). Returns h."""
-    dev = _on_gpu(x)
+    dev, bf16 = x.get_device(), torch.bfloat16
     M, K = x.shape
     F = w_gate.shape[0]
-    bf16 = torch.bfloat16
     if h is None:
         h = _rows_like((M, F), bf16, x.device, stream)
-    sv, sv_bytes = _room("saved", saved, dev)
+    (xs, x1), (gs, g1), (us, u1), (hs, h1) = x.stride(), w_gate.stride(), w_up.stride(), h.stride()
+    # As in gated_scan: one look at everything, and only where something is unusual the checks that say what.
+    if not (dev >= 0 and dev == _current_device() and x.dtype is bf16 and w_gate.dtype is bf16 and w_up.dtype is bf16
+            and h.dtype is bf16 and w_gate.shape == (F, K) and w_up.shape == (F, K) and h.shape == (M, F)
+            and x1 == g1 == u1 == h1 == 1 and w_gate.get_device() == dev
+            and w_up.get_device() == dev and h.get_device() == dev
+            and (saved is None or (saved.is_contiguous() and saved.get_device() == dev))):
+        _on_gpu(x)
+        xs, hs = _matrix16("x", x, M, K, bf16, dev), _matrix16("h", h, M, F, bf16, dev)
+        gs, us = _matrix16("w_gate", w_gate, F, K, bf16, dev), _matrix16("w_up", w_up, F, K, bf16, dev)
+        _room("saved", saved, dev)
+    if M == 1:  # a single row's stride says nothing
+        xs, hs = (K + 7) // 8 * 8, (F + 7) // 8 * 8
+    if F == 1:
+        gs = us = (K + 7) // 8 * 8
+    code = LA_ACTIVATIONS.get(act)
     _check(_load().la_gated_ffn(
-        x.data_ptr(), w_gate.data_ptr(), w_up.data_ptr(), h.data_ptr(), sv, sv_bytes, M, F, K,
-        _matrix16("x", x, M, K, bf16, dev), _matrix16("w_gate", w_gate, F, K, bf16, dev),
-        _matrix16("w_up", w_up, F, K, bf16, dev), _matrix16("h", h, M, F, bf16, dev), _act_code(act),
-        _stream_on(stream, dev)))
+        x.data_ptr(), w_gate.data_ptr(), w_up.data_ptr(), h.data_ptr(), None if saved is None else saved.data_ptr(),
+        0 if saved is None else saved.numel() * saved.element_size(), M, F, K, xs, gs, us, hs,
+        _act_code(act) if code is None else code, _stream_on(stream, dev)))
     return h
 
 

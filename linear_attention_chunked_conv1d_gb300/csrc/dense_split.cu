@@ -10,6 +10,7 @@
 // Operands as in dense_tc.cu, with the roles of rows and columns exchanged.
 #include <cuda.h>
 
+#include <atomic>
 #include <cmath>
 
 #include "dense.cuh"
@@ -79,6 +80,15 @@ dense_split_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Ep
     const uint32_t rows = plan.rows, cols = rows < 32 ? 32 : rows;  // TMEM columns
     const uint32_t stage_bytes = P_BYTES + rows * TK * 2;
     const uint32_t rank = plan.split > 1 ? tc::cluster_rank() : 0;
+    const int64_t tile = blockIdx.x / plan.split;
+    const int pt = (N + OUT_P - 1) / OUT_P;
+    const int64_t rt = (M + rows - 1) / rows, per = pt * rt;
+    const int o = (int)(tile / per);
+    const int p0 = (int)(tile % per % pt) * OUT_P;
+    const int64_t r0 = tile % per / pt * rows;
+    const int kp = (K + TK - 1) / TK;
+    const int64_t kb = (int64_t)kp * parts;
+    const int64_t k_first = kb * rank / plan.split, k_end = kb * (rank + 1) / plan.split;
     if (threadIdx.x == 0) {
         for (int s = 0; s < plan.stages; ++s) {
             tc::mbar_init(full + s, 1);
@@ -95,18 +105,12 @@ dense_split_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Ep
     tc::fence_before_sync();
     __syncthreads();
     tc::fence_after_sync();
+    launch_next();
     wait_for_previous();
     const uint32_t tm = *tmem_sh;
-    const int64_t tile = blockIdx.x / plan.split;
-    const int pt = (N + OUT_P - 1) / OUT_P;
-    const int64_t rt = (M + rows - 1) / rows, per = pt * rt;
-    const int o = (int)(tile / per);
-    const int p0 = (int)(tile % per % pt) * OUT_P;
-    const int64_t r0 = tile % per / pt * rows;
-    const int kp = (K + TK - 1) / TK;
-    const int64_t kb = (int64_t)kp * parts;
-    const int64_t k_first = kb * rank / plan.split, k_end = kb * (rank + 1) / plan.split;
     const uint32_t rbase = tc::smem_u32(ring);
+    const int nr = (int)(M - r0 < (int64_t)rows ? M - r0 : rows);  // the tile's rows, and those that this block finishes
+    const int f = nr * (int)rank / plan.split, l = nr * ((int)rank + 1) / plan.split;
 
     if (warp == 0) {
         if (tc::elect_one()) {
@@ -165,6 +169,11 @@ dense_split_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Ep
             tc::mma_commit(done);
             if (!tc::mbar_wait(done, 0, WAIT_NS + (k_end - k_first) * 1000, SLEEP_NS)) *err = 1;
         }
+    } else if (KIND == DENSE_LINEAR && ep.residual) {  // the residual's lines are on their way to L2 meanwhile
+        for (int i = threadIdx.x - 64; i < 2 * (l - f); i += THREADS - 64) {
+            const int col = p0 + i % 2 * 64;
+            if (col < N) asm volatile("prefetch.global.L2 [%0];" ::"l"(ep.residual + (r0 + f + i / 2) * ep.ldr + col));
+        }
     }
     __syncwarp();
     tc::fence_before_sync();
@@ -187,8 +196,6 @@ dense_split_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Ep
     if (plan.split > 1) tc::cluster_sync();
     else __syncthreads();
     if (warp == 1) tc::tmem_dealloc(tm, cols);
-    const int nr = (int)(M - r0 < (int64_t)rows ? M - r0 : rows);
-    const int f = nr * (int)rank / plan.split, l = nr * ((int)rank + 1) / plan.split;
     constexpr int LANES = OUT_P / 4, ROWS_AT = 32 / LANES;  // lanes and rows of a warp at one time
     const int c4 = lane % LANES * 4, col = p0 + c4;
     constexpr int AT = THREADS / 32 * ROWS_AT, U = 4;  // rows of the block at one time; how many times over
@@ -269,8 +276,15 @@ cudaError_t launch(const DenseArgs &a, cudaStream_t st) {
     const Epilogue ep = make_epilogue(a);
     const int parts = KIND == DENSE_DX ? a.count : 1, outs = KIND == DENSE_DW ? a.count : 1;
     const int64_t tiles = (int64_t)((a.N + out_cols(a) - 1) / out_cols(a)) * ((a.M + plan.rows - 1) / plan.rows) * outs;
-    cudaError_t e = cudaFuncSetAttribute(dense_split_kernel<KIND>, cudaFuncAttributeMaxDynamicSharedMemorySize, 113 * 1024);
+    static std::atomic<uint64_t> set;  // devices on which the kernel may have its shared memory
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
+    if (dev >= 64 || !(set.load(std::memory_order_relaxed) >> dev & 1)) {
+        e = cudaFuncSetAttribute(dense_split_kernel<KIND>, cudaFuncAttributeMaxDynamicSharedMemorySize, 113 * 1024);
+        if (e != cudaSuccess) return e;
+        if (dev < 64) set.fetch_or(1ull << dev);
+    }
     return launch_overlapped(dense_split_kernel<KIND>, dim3((unsigned)(tiles * plan.split)), dim3(THREADS), plan.smem,
                              plan.split > 1 ? plan.split : 0, st, maps, ep, plan, a.M, a.N, a.K, parts, a.status,
                              a.wait_ns ? a.wait_ns : WAIT_NS, a.debug_stall);
@@ -279,22 +293,24 @@ cudaError_t launch(const DenseArgs &a, cudaStream_t st) {
 }  // namespace
 
 // Which kernel a call takes: the one whose time is the shorter by what both were measured to take, in us:
-//   pairs (dense_tc.cu)  5 + 0.29 a stage of 64 summed indexes, for each time the tiles go round the 76 pairs,
-//                        and no less than 11 + bytes / 6 TB/s;
-//   this one             8 + operations / 1.2 PFLOP/s (tiles counted whole), no less than 6 + bytes / 6 TB/s.
-// Pairs and this kernel, M x N x K: linear 1 x 4096 x 4096 24.1 and 10.6, 128: 24.5 and 15.3, 512: 24.8 and 23.5,
-// 1024: 26.0 and 36.2; 1024 x 1024 x 8192 41.1 and 22.8; 2048 x 2048 x 2048 17.4 and 23.9; gated 32 x 8192 x 4096
-// 32.1 and 26.0, 256: 33.7 and 37.9; dx 256 x 8192 x 4096 40.7 and 24.2, 1024: 43.0 and 57.3; dw of 16384 rows,
-// 1024 x 1024: 74.2 and 35.9, of 1024 rows, 2048 x 2048: 12.1 and 16.1.
+//   pairs (dense_tc.cu)  5 + for each time the tiles go round the 76 pairs 0.29 a stage of 64 summed indexes and no less
+//                        than 3.2, the epilogue's; and no less than 7 + bytes / 6 TB/s;
+//   this one             2 + for each time the blocks go round the 304 places 6 and 0.41 a stage of 32 KB; and no less
+//                        than 6 + bytes / 6 TB/s.
+// Pairs and this kernel, M x N x K: linear 1 x 4096 x 4096 23.9 and 10.0, 128: 24.2 and 16.0, 512: 24.8 and 23.5,
+// 1024: 26.0 and 36.2; 1024 x 1024 x 8192 41.1 and 22.8; 2048 x 2048 x 2048 17.4 and 23.9; 777 x 5008 x 2048 24.6 and
+// 21.0, with bias, GELU and residual 29.5 and 30.5; 8192 x 8192 x 64 46.5 and 112; gated 32 x 8192 x 4096 29.5 and 25.5,
+// 256: 30.8 and 35.6; dx 256 x 8192 x 4096 40.7 and 24.2, 1024: 43.0 and 57.3; dw of 16384 rows, 1024 x 1024: 74.2 and
+// 35.9, of 1024 rows, 2048 x 2048: 12.1 and 16.1.
 bool dense_split_serves(const DenseArgs &a) {
     const Plan p = make_plan(a);
     const double twice = a.kind == DENSE_GATED ? 2 : 1, outs = a.kind == DENSE_DW ? a.count : 1, parts = a.kind == DENSE_DX ? a.count : 1;
-    const double M = a.M, N = a.N, K = a.K * parts;
-    const double bytes = 2 * (a.kind == DENSE_DW ? outs * (M * K + M * N) + K * N : M * K + twice * N * K + M * N);
-    const double tiles = ceil(M / 256) * ceil(N * twice / 256) * outs;
-    const double pairs = fmax(5 + 0.29 * parts * ceil(a.K / 64.) * ceil(tiles / 76), 11 + bytes * (1 / 6e6));
-    const double ops = 2 * ceil(M / p.rows) * p.rows * ceil(N * twice / PT) * PT * K * outs;
-    return tiles < 1e6 && fmax(8 + ops * (1 / 1.2e9), 6 + bytes * (1 / 6e6)) < pairs;
+    const double M = a.M, N = a.N * twice, K = a.K * parts, kb = ceil(a.K / 64.) * parts;
+    const double memory = 2 * (a.kind == DENSE_DW ? outs * (M * K + M * N) + K * N : M * K + N * K + M * a.N) * (1 / 6e6);
+    const double pairs = fmax(5 + ceil(ceil(M / 256) * ceil(N / 256) * outs / 76) * fmax(0.29 * kb, 3.2), 7 + memory);
+    const double blocks = ceil(M / p.rows) * ceil(N / PT) * outs * p.split;
+    const double stage = 0.41 * (P_BYTES + p.rows * TK * 2) / 32768;
+    return blocks < 1e6 && fmax(2 + ceil(blocks / 304) * (6 + stage * kb / p.split), 6 + memory) < pairs;
 }
 
 cudaError_t launch_dense_split(const DenseArgs &a, cudaStream_t st) {

@@ -13,6 +13,9 @@ namespace la {
 // a kernel that launch_overlapped starts calls it before it touches global memory.
 __device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
+// Lets the next kernel of the stream that waits so start its blocks where they fit beside this one's.
+__device__ __forceinline__ void launch_next() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
 // cluster: blocks of a cluster along x, or 0.
 template <class... Params, class... Args>
 cudaError_t launch_overlapped(void (*kernel)(Params...), dim3 grid, dim3 block, size_t smem, int cluster, cudaStream_t st,
