@@ -21,9 +21,12 @@ import torch
 
 from . import (LA_W4_MAX_ROWS, conv1d_silu_backward, conv1d_silu_backward_workspace_bytes, conv1d_silu_l2_prefill,
                conv1d_silu_prefill, conv1d_silu_prefill_varlen, decode_step,
-               decode_workspace_bytes, gate_activations, gated_scan, gated_scan_backward,
+               decode_workspace_bytes, gate_activations, gated_ffn, gated_ffn_backward,
+               gated_ffn_backward_workspace_bytes, gated_ffn_saved_bytes, gated_scan, gated_scan_backward,
                gated_scan_saved_bytes, gated_scan_step, gated_scan_workspace_bytes,
                gdn_prefill_batched, gdn_prefill_varlen, gemm_bf16, kda_prefill, l2norm_heads,
+               layernorm_rows, layernorm_rows_backward, layernorm_rows_backward_workspace_bytes, linear,
+               linear_backward, linear_backward_workspace_bytes,
                pointer_array, prefill_front, prefill_segmented, prefill_segmented_workspace_bytes,
                prefill_workspace_bytes, rmsnorm_rows, w4_matvec, _on_stream)
 
@@ -385,3 +388,57 @@ class GatedDecode:
                         conv_state_ptrs=self.conv_ptrs, conv_w=self.conv_w, conv_bias=self.conv_bias,
                         stream=stream)
         return project(self.y, self.w_out, self.out, stream=stream)
+
+
+class FeedForward:
+    """The feed-forward half of a layer over a fixed number of rows (the tokens of a packed batch, or one
+    for each of some streams): n = layernorm(x), h = act(n Wg^T) * (n Wu^T), y = h Wd^T + x.
+
+    norm_w, norm_b [D] (norm_b may be None), w_gate and w_up [F][D], w_down [D][F]: bf16. forward(x) takes
+    x [rows][D] and returns y; with train=True it also keeps what backward(dy) needs (x itself has to
+    stay as it is until then), which returns the gradients by name: x, norm_w and norm_b (fp32), w_gate,
+    w_up and w_down. Outputs and gradients are the object's own tensors, written again by the next call."""
+
+    def __init__(self, rows, norm_w, norm_b, w_gate, w_up, w_down, *, act="silu", eps=1e-5, train=False):
+        self.act, self.eps, self.train = act, eps, train
+        self.norm_w, self.norm_b, self.w_gate, self.w_up, self.w_down = norm_w, norm_b, w_gate, w_up, w_down
+        (F, D), dev, bf16 = w_gate.shape, w_gate.device, torch.bfloat16
+        for name, w, shape in (("norm_w", norm_w, (D,)), ("norm_b", norm_b, (D,)), ("w_gate", w_gate, (F, D)),
+                               ("w_up", w_up, (F, D)), ("w_down", w_down, (D, F))):
+            if w is not None and (tuple(w.shape) != shape or w.dtype != bf16 or w.device != dev):
+                raise ValueError(f"{name}: {tuple(w.shape)} {w.dtype} on {w.device}, expected {shape} {bf16} on {dev}")
+        matrix = lambda r, c: torch.empty(r, (c + 7) // 8 * 8, dtype=bf16, device=dev)[:, :c]  # noqa: E731
+        room = lambda n: torch.empty(n, dtype=torch.uint8, device=dev)  # noqa: E731
+        self.normed, self.h, self.y = matrix(rows, D), matrix(rows, F), matrix(rows, D)
+        self.x = self.stats = self.saved = None
+        if train:
+            self.stats = torch.empty(rows, 2, device=dev)
+            self.saved = room(gated_ffn_saved_bytes(rows, F))
+            self.dh, self.dnormed = matrix(rows, F), matrix(rows, D)
+            self.grads = dict(x=matrix(rows, D), norm_w=torch.empty(D, device=dev),
+                              norm_b=None if norm_b is None else torch.empty(D, device=dev), w_gate=matrix(F, D),
+                              w_up=matrix(F, D), w_down=matrix(D, F))
+            self.workspace = room(max(layernorm_rows_backward_workspace_bytes(rows, D, bf16),
+                                      gated_ffn_backward_workspace_bytes(rows, F, D),
+                                      linear_backward_workspace_bytes(rows, D, F)))
+
+    def forward(self, x, stream=None):
+        layernorm_rows(x, self.norm_w, self.norm_b, self.normed, stats=self.stats, eps=self.eps, stream=stream)
+        gated_ffn(self.normed, self.w_gate, self.w_up, self.h, act=self.act, saved=self.saved, stream=stream)
+        linear(self.h, self.w_down, self.y, residual=x, stream=stream)
+        self.x = x if self.train else None
+        return self.y
+
+    def backward(self, dy, stream=None):
+        """Gradients of the last forward()."""
+        if not self.train:
+            raise RuntimeError("backward() needs FeedForward(..., train=True)")
+        if self.x is None:
+            raise RuntimeError("backward() needs a forward() before it")
+        g, ws = self.grads, self.workspace
+        linear_backward(self.h, self.w_down, None, dy, self.dh, g["w_down"], workspace=ws, stream=stream)
+        gated_ffn_backward(self.normed, self.w_gate, self.w_up, self.saved, self.dh, self.dnormed, g["w_gate"],
+                           g["w_up"], act=self.act, workspace=ws, stream=stream)
+        layernorm_rows_backward(self.x, self.norm_w, self.stats, self.dnormed, g["x"], g["norm_w"], g["norm_b"],
+                                dskip=dy, workspace=ws, stream=stream)
+        return g

@@ -47,7 +47,8 @@ def untouched(t):
 def act64(z, act):
     return {"none": lambda: z, "relu": lambda: torch.clamp_min(z, 0), "silu": lambda: z * torch.sigmoid(z),
             "gelu": lambda: 0.5 * z * torch.erfc(-z / math.sqrt(2)),
-            "gelu_tanh": lambda: 0.5 * z * (1 + torch.tanh(math.sqrt(2 / math.pi) * (z + 0.044715 * z ** 3)))}[act]()
+            # (1 + tanh u) / 2 = 1 / (1 + e^-2u), which keeps the left tail that 1 + tanh u loses in 64 bits too
+            "gelu_tanh": lambda: z * torch.sigmoid(2 * math.sqrt(2 / math.pi) * (z + 0.044715 * z ** 3))}[act]()
 
 
 def slope64(z, act):

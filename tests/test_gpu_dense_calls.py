@@ -1,0 +1,313 @@
+"""The dense half's calls as programs make them: many tiles, long sums, far strides, shared buffers, other streams,
+captured graphs, values that are not finite, bounded waits, and the whole block (FeedForward) against 64 bits and
+against differences of its 64-bit form. Bounds are those of test_gpu_dense.py, or stated where they are used."""
+import math
+
+import pytest
+import torch
+
+import linear_attention_chunked_conv1d_gb300 as la
+from linear_attention_chunked_conv1d_gb300.path import FeedForward
+from tests.test_gpu_dense import F32, U, act64, case, check_gated, check_linear, close, gated_case, out_rows, room, rows
+
+pytestmark = pytest.mark.gpu
+BF16 = torch.bfloat16
+
+
+# tiles of 256 x 256 that go round the pairs more than once, with ragged edges; and sums that are split over blocks
+@pytest.mark.parametrize("m,n,k", [(1030, 4100, 136), (2500, 2600, 264), (4099, 2733, 65), (9000, 600, 520), (5000, 300, 2100), (130, 130, 8200)])
+def test_linear_many_tiles(cuda, m, n, k):
+    check_linear(case(cuda, m, n, k, m + n + k), "none")
+    check_linear(case(cuda, m, n, k, m + n + k + 1, residual=False), "gelu")
+
+
+@pytest.mark.parametrize("m,f,k", [(1030, 2100, 136), (2500, 1300, 264), (4099, 2733, 65), (9000, 300, 520), (5000, 150, 2100), (130, 130, 8200)])
+def test_gated_many_tiles(cuda, m, f, k):
+    check_gated(gated_case(cuda, m, f, k, m + f + k), "silu")
+
+
+@pytest.mark.parametrize("m", [1, 2, 15, 16, 17, 31, 32, 33, 63, 64, 65, 127, 128, 129])
+def test_rows_around_the_tiles(cuda, m):
+    check_linear(case(cuda, m, 392, 1100, m), "silu")
+    check_gated(gated_case(cuda, m, 197, 1100, m), "gelu_tanh")
+
+
+def test_far_strides(cuda):
+    """Rows 2^31 values apart: offsets pass 32 bits in x, residual and y, in dy and dx, and in a norm's rows."""
+    g = torch.Generator().manual_seed(1)
+    far = 2 ** 31
+    big = torch.empty(2 * far + 4096, dtype=BF16, device=cuda)
+    at = lambda o, r, c: big.as_strided((r, c), (far, 1), o)  # noqa: E731
+    m, n, k = 3, 72, 200
+    x, y, res, dy, dx = at(0, m, k), at(256, m, n), at(512, m, n), at(768, m, n), at(1024, m, k)
+    for t in (x, res, dy):
+        t.copy_(torch.randn(t.shape, generator=g).to(BF16))
+    w = (torch.randn(n, k, generator=g) / math.sqrt(k)).to(BF16).to(cuda)
+    dw = torch.empty_like(w)
+    want_y = la.linear(x.contiguous(), w, residual=res.contiguous())
+    want_dx, want_dw = torch.empty(m, k, dtype=BF16, device=cuda), torch.empty_like(w)
+    ws = room(la.linear_backward_workspace_bytes(m, n, k), cuda)
+    la.linear_backward(x.contiguous(), w, None, dy.contiguous(), want_dx, want_dw, workspace=ws)
+    assert torch.equal(la.linear(x, w, y, residual=res), want_y)
+    la.linear_backward(x, w, None, dy, dx, dw, workspace=ws)
+    assert torch.equal(dx, want_dx) and torch.equal(dw, want_dw)
+    nw = torch.ones(k, dtype=BF16, device=cuda)
+    assert torch.equal(la.layernorm_rows(x, nw, None, dx), la.layernorm_rows(x.contiguous(), nw))
+
+
+def test_shared_buffers(cuda):
+    """Halves of one packed weight and gradient, operands and results as columns of one buffer, y in the residual's
+    place; each as the call with buffers of their own."""
+    g = torch.Generator().manual_seed(2)
+    m, f, k = 700, 328, 264
+    x = rows((m, k), BF16, cuda, g)
+    w = rows((2 * f, k), BF16, cuda, g, 1 / math.sqrt(k))
+    dh = rows((m, f), BF16, cuda, g)
+    saved, ws = room(la.gated_ffn_saved_bytes(m, f), cuda), room(la.gated_ffn_backward_workspace_bytes(m, f, k), cuda)
+    h = la.gated_ffn(x, w[:f].clone(), w[f:].clone(), saved=saved)
+    dx, dg, du = (torch.empty(*s, dtype=BF16, device=cuda) for s in ((m, k), (f, k), (f, k)))
+    la.gated_ffn_backward(x, w[:f].clone(), w[f:].clone(), saved, dh, dx, dg, du, workspace=ws)
+    wide = torch.full((m, k + f + k + 16), 3.0, dtype=BF16, device=cuda)
+    x2, h2, dx2 = wide[:, :k], wide[:, k:k + f], wide[:, k + f:2 * k + f]
+    x2.copy_(x)
+    dw2 = torch.empty(2 * f, k, dtype=BF16, device=cuda)
+    la.gated_ffn(x2, w[:f], w[f:], h2, saved=saved)
+    la.gated_ffn_backward(x2, w[:f], w[f:], saved, dh, dx2, dw2[:f], dw2[f:], workspace=ws)
+    assert torch.equal(h2, h) and torch.equal(dx2, dx) and torch.equal(dw2[:f], dg) and torch.equal(dw2[f:], du)
+    assert bool((wide[:, 2 * k + f:] == 3.0).all())
+    for rows_ in (m, 5):  # tiles by pairs of blocks, and split sums
+        xs, wd, res = x[:rows_], w[:f], rows((rows_, f), BF16, cuda, g)
+        want = la.linear(xs, wd, residual=res, act="silu")
+        assert la.linear(xs, wd, res, residual=res, act="silu") is res and torch.equal(res, want)
+
+
+def test_same_bits_each_time(cuda):
+    """Sums are taken in a fixed order: every call, in whatever company, gives the same bits."""
+    c, d = gated_case(cuda, 2000, 700, 520, 3), case(cuda, 40, 500, 2000, 4)
+    first = None
+    for _ in range(5):
+        saved, ws = room(la.gated_ffn_saved_bytes(2000, 700), cuda), room(la.gated_ffn_backward_workspace_bytes(2000, 700, 520), cuda)
+        la.gated_ffn(c["x"], c["w"], c["w_up"], c["y"], saved=saved)
+        la.gated_ffn_backward(c["x"], c["w"], c["w_up"], saved, c["dy"], c["dx"], c["dw"], c["dw_up"], workspace=ws)
+        la.linear(d["x"], d["w"], d["y"], bias=d["bias"], act="gelu")
+        stats, dw, db = torch.empty(2000, 2, device=cuda), torch.empty(520, device=cuda), torch.empty(520, device=cuda)
+        nw = torch.ones(520, dtype=BF16, device=cuda)
+        la.layernorm_rows(c["x"], nw, stats=stats)
+        dn = torch.empty(2000, 520, dtype=BF16, device=cuda)
+        la.layernorm_rows_backward(c["x"], nw, stats, c["dx"], dn, dw, db,
+                                   workspace=room(la.layernorm_rows_backward_workspace_bytes(2000, 520, BF16), cuda))
+        got = [t.clone() for t in (c["y"], c["dx"], c["dw"], c["dw_up"], d["y"], dn, dw, db)]
+        assert first is None or all(torch.equal(a, b) for a, b in zip(first, got))
+        first = first or got
+
+
+def test_a_row_does_not_depend_on_its_batch_mates(cuda):
+    """Rows of NaN and infinities leave the other rows of y and dx as they are; a weight's row of NaN its column."""
+    for m in (12, 900):
+        c = gated_case(cuda, m, 300, 200, 5)
+        run = lambda: la.gated_ffn(c["x"], c["w"], c["w_up"]).clone()  # noqa: E731
+        good = run()
+        c["x"][3], c["x"][7, 5] = float("nan"), float("inf")
+        c["w"][11] = float("nan")
+        got = run()
+        keep_m, keep_n = [i for i in range(m) if i not in (3, 7)], [i for i in range(300) if i != 11]
+        assert torch.equal(got[keep_m][:, keep_n], good[keep_m][:, keep_n])
+        assert got[3].isnan().all() and got[:, 11].isnan().all()
+        assert not got[7][keep_n].isfinite().any()
+
+
+@pytest.mark.parametrize("act", ["relu", "gelu", "gelu_tanh", "silu"])
+def test_large_and_special_values_of_activations(cuda, act):
+    """z from -1e30 to 1e30 through a weight of 1 x 1: values and slopes go to their limits, never to NaN."""
+    z = torch.tensor([-1e30, -3e8, -1e4, -300, -90, -60, -20, -9, -5, -1, -0.1, -1e-3, -1e-30, 0.0, 1e-30, 1e-3, 0.1, 1, 5, 9, 20, 300, 1e4, 1e30])
+    x = z.to(BF16).reshape(-1, 1).to(cuda).expand(-1, 8).contiguous()[:, :1]
+    w = torch.ones(1, 8, dtype=BF16, device=cuda)[:, :1]
+    m = z.numel()
+    saved, dy, dx = room(la.linear_saved_bytes(m, 1, act), cuda), torch.ones(m, 8, dtype=BF16, device=cuda)[:, :1], torch.zeros(m, 8, dtype=BF16, device=cuda)[:, :1]
+    y = la.linear(x, w, act=act, saved=saved)
+    la.linear_backward(x, w, saved, dy, dx, act=act, workspace=room(la.linear_backward_workspace_bytes(m, 1, 1, act), cuda))
+    X = x.double().clamp(-1e9, 1e9) if act != "relu" else x.double()
+    X.requires_grad_()
+    ref = act64(X, act)
+    slope = torch.autograd.grad(ref.sum(), X)[0]
+    ref = torch.where(x.double() > 1e8, x.double(), ref.detach())
+    # 2^-17: the hardware's exponential and reciprocal, and an exponent z^2 / 2 rounded to 2^-24 of at most 2^6. The factor
+    # of z is a 32-bit number whose values below 2^-126 count as 0 (silu at -90: 90 e^-90 = 90 * 8.2e-40 with e^-90 < 2^-126
+    # = 1.2e-38), so what is lost of z times it is at most |z| 2^-126, where that is not past the range of z itself.
+    close(y, ref, U * ref.abs() + 2.0 ** -17 * ref.abs() + x.double().abs().clamp(max=200) * 2.0 ** -126 + 1e-38, "value")
+    if act == "relu":
+        slope = (x.double() > 0).double()
+    close(dx, slope, U * slope.abs() + 2.0 ** -20, "slope")
+
+
+def test_other_streams_and_two_at_once(cuda):
+    c, d = gated_case(cuda, 1500, 600, 520, 6), gated_case(cuda, 1500, 600, 520, 7)
+
+    def run(q, stream):
+        q["saved"], q["ws"] = room(la.gated_ffn_saved_bytes(1500, 600), cuda), room(la.gated_ffn_backward_workspace_bytes(1500, 600, 520), cuda)
+        torch.cuda.synchronize()
+        return lambda: (la.gated_ffn(q["x"], q["w"], q["w_up"], q["y"], saved=q["saved"], stream=stream),
+                        la.gated_ffn_backward(q["x"], q["w"], q["w_up"], q["saved"], q["dy"], q["dx"], q["dw"], q["dw_up"],
+                                              workspace=q["ws"], stream=stream))
+    names = ("y", "dx", "dw", "dw_up")
+    for q in (c, d):
+        run(q, None)()
+    want = [[q[n].clone() for n in names] for q in (c, d)]
+    torch.cuda.synchronize()
+    s, t = torch.cuda.Stream(), torch.cuda.Stream()
+    for q in (c, d):
+        for n in names:
+            q[n].zero_()
+    one, two = run(c, s), run(d, t.cuda_stream)
+    for _ in range(4):
+        one()
+        two()
+    torch.cuda.synchronize()
+    for q, ref in zip((c, d), want):
+        assert all(torch.equal(q[n], r) for n, r in zip(names, ref))
+    with torch.cuda.stream(s):  # a result made for the call belongs to the stream it runs on
+        y = la.linear(c["x"], c["w"])
+    z = la.linear(c["x"], c["w"], stream=s)
+    s.synchronize()
+    assert torch.equal(y, z)
+    assert la.device_status() == 0
+
+
+def test_captured_and_replayed(cuda):
+    """Forward and backward pass of the block in a graph, replayed with other inputs in the same places, between
+    eager calls that use the same workspace in stream order."""
+    g = torch.Generator().manual_seed(8)
+    m, D, F = 520, 264, 400
+    weights = [(torch.randn(*s, generator=g) * sd).to(BF16).to(cuda) for s, sd in
+               (((D,), 1.0), ((D,), 0.2), ((F, D), D ** -0.5), ((F, D), D ** -0.5), ((D, F), F ** -0.5))]
+    block = FeedForward(m, *weights, train=True)
+    x, dy = torch.empty(m, D, dtype=BF16, device=cuda), torch.empty(m, D, dtype=BF16, device=cuda)
+    inputs = [[torch.randn(m, D, generator=g).to(BF16).to(cuda) for _ in range(2)] for _ in range(3)]
+    keep = lambda: [block.y.clone()] + [t.clone() for t in block.grads.values()]  # noqa: E731
+    want = []
+    for a, b in inputs:
+        x.copy_(a), dy.copy_(b)
+        block.forward(x), block.backward(dy)
+        want.append(keep())
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        block.forward(x)
+        block.backward(dy)
+    for (a, b), ref in zip(inputs, want):
+        x.copy_(a), dy.copy_(b)
+        graph.replay()
+        assert all(torch.equal(p, q) for p, q in zip(keep(), ref))
+        block.forward(x), block.backward(dy)
+        assert all(torch.equal(p, q) for p, q in zip(keep(), ref))
+    assert la.device_status() == 0
+
+
+def test_the_wait_runs_out(cuda, monkeypatch):
+    """A block that waits for what never comes gives up, says so, and leaves the context usable: tiles by pairs of
+    blocks, and split sums."""
+    c, d = case(cuda, 1030, 2000, 264, 9), case(cuda, 8, 400, 2000, 10)
+    want = [la.linear(q["x"], q["w"]).clone() for q in (c, d)]
+    torch.cuda.synchronize()
+    assert la.device_status() == 0
+    monkeypatch.setenv("LA_WAIT_LIMIT_NS", "20000000")
+    for q in (c, d):
+        monkeypatch.setenv("LA_DEBUG_STALL", "1")
+        la.linear(q["x"], q["w"], q["y"])
+        assert la.device_status() & 2
+        monkeypatch.delenv("LA_DEBUG_STALL")
+    for q, ref in zip((c, d), want):
+        assert torch.equal(la.linear(q["x"], q["w"]), ref)
+    assert la.device_status() == 0
+
+
+# ---------------------------------------------------------------------------------- the whole block
+def block64(x, norm_w, norm_b, w_gate, w_up, w_down, act):
+    var, mean = torch.var_mean(x, 1, unbiased=False, keepdim=True)
+    n = (x - mean) / torch.sqrt(var + 1e-5) * norm_w + norm_b
+    return (act64(n @ w_gate.T, act) * (n @ w_up.T)) @ w_down.T + x
+
+
+@pytest.mark.parametrize("m,D,F,act", [(1, 64, 128, "silu"), (37, 200, 333, "gelu"), (600, 1000, 1500, "silu"), (3000, 264, 700, "gelu_tanh")])
+def test_feed_forward(cuda, m, D, F, act):
+    """y and every gradient against the 64-bit block, and every gradient against differences of it.
+
+    Norm-wise bounds: each of the roundings on the way (n, gate, up, h, y; dh, dgate, dup, dn, dx) moves its values by
+    at most U of themselves, that is a relative U in norm, and passes on through products and norms whose gain in
+    norm is at most 4 here (weights of unit gain, |act'| <= 1.13, norm weights around 1). Ten of them: 40 U, taken as
+    if none cancelled."""
+    g = torch.Generator().manual_seed(m + D)
+    shapes = ((m, D), (D,), (D,), (F, D), (F, D), (D, F))
+    scales = (1.0, 0.2, 0.2, D ** -0.5, D ** -0.5, F ** -0.5)
+    t = [(torch.randn(*s, generator=g) * sd + (1.0 if i == 1 else 0.0)).to(BF16).to(cuda) for i, (s, sd) in enumerate(zip(shapes, scales))]
+    t = [rows_like(v) if v.dim() == 2 else v for v in t]
+    dy = rows((m, D), BF16, cuda, g)
+    block = FeedForward(m, *t[1:], act=act, train=True)
+    y = block.forward(t[0]).clone()
+    grads = block.backward(dy)
+    torch.cuda.synchronize()
+    assert la.device_status() == 0
+    leaves = [v.double().requires_grad_() for v in t]
+    ref = block64(*leaves, act)
+    want = torch.autograd.grad(ref, leaves, dy.double())
+    near = lambda a, b: float((a.double() - b).norm() / b.norm())  # noqa: E731
+    assert near(y, ref.detach()) <= 40 * U
+    names = ("x", "norm_w", "norm_b", "w_gate", "w_up", "w_down")
+    for name, w in zip(names, want):
+        assert near(grads[name], w) <= 40 * U, (name, near(grads[name], w))
+    # differences: (L(p + e d) - L(p - e d)) / 2 e = <gradient, d> + O(e^2); e = 1e-4 leaves 1e-7 of third derivatives of
+    # order 10 and 1e-11 of rounding in 64 bits, next to 40 U of the gradient's norm times d's
+    loss = lambda *p: (block64(*p, act) * dy.double()).sum()  # noqa: E731
+    with torch.no_grad():
+        for i, name in enumerate(names):
+            base = [v.double() for v in t]
+            d = torch.randn(base[i].shape, generator=g, dtype=torch.float64).to(cuda) * base[i].abs().mean()
+            up, down = [list(base) for _ in range(2)]
+            up[i], down[i] = base[i] + 1e-4 * d, base[i] - 1e-4 * d
+            slope = float(loss(*up) - loss(*down)) / 2e-4
+            got = float((grads[name].double() * d).sum())
+            assert abs(got - slope) <= 40 * U * float(want[i].norm() * d.norm()) + 1e-6 * abs(slope), name
+
+
+def rows_like(v):
+    out = out_rows(v.shape, v.dtype, v.device)
+    out.copy_(v)
+    return out
+
+
+def test_feed_forward_rows_one_by_one(cuda):
+    """A decode step of some streams gives what one pass over the same rows gives, to the last places of fp32 sums."""
+    g = torch.Generator().manual_seed(11)
+    D, F, m = 512, 1000, 300
+    t = [(torch.randn(*s, generator=g) * sd).to(BF16).to(cuda) for s, sd in
+         (((D,), 1.0), ((F, D), D ** -0.5), ((F, D), D ** -0.5), ((D, F), F ** -0.5))]
+    x = torch.randn(m, D, generator=g).to(BF16).to(cuda)
+    many = FeedForward(m, t[0], None, *t[1:]).forward(x)
+    step = FeedForward(4, t[0], None, *t[1:])
+    for i in range(0, m, 60):
+        got = step.forward(x[i:i + 4])
+        # h is rounded once in each; a sum at the edge of a step may round the other way: one step of h, U |h| |Wd| a term
+        near = float((got.double() - many[i:i + 4].double()).norm() / many[i:i + 4].double().norm())
+        assert near <= 4 * U
+
+
+def test_feed_forward_refusals(cuda):
+    w = lambda *s: torch.zeros(*s, dtype=BF16, device=cuda)  # noqa: E731
+    with pytest.raises(ValueError, match="w_down"):
+        FeedForward(4, w(64), None, w(128, 64), w(128, 64), w(128, 64))
+    block = FeedForward(4, w(64), None, w(128, 64), w(128, 64), w(64, 128))
+    with pytest.raises(RuntimeError, match="train"):
+        block.backward(w(4, 64))
+    with pytest.raises(RuntimeError, match="forward"):
+        FeedForward(4, w(64), None, w(128, 64), w(128, 64), w(64, 128), train=True).backward(w(4, 64))
+    with pytest.raises(ValueError, match="y"):
+        block.forward(w(5, 64))
+    for bad in (w(4, 64).float(), w(4, 63)):
+        with pytest.raises((TypeError, ValueError)):
+            block.forward(bad)
+    with pytest.raises(TypeError):
+        la.linear(w(4, 64), w(8, 64), bias=torch.zeros(8, device=cuda))
+    with pytest.raises(la.LinAttnError, match="16 bytes"):
+        la.linear(w(4, 64), w(8, 64), residual=w(4, 9)[:, :8])
+    with pytest.raises(la.LinAttnError, match="workspace"):
+        la.linear_backward(w(4, 64), w(8, 64), None, w(4, 8), w(4, 64))
