@@ -544,8 +544,8 @@ int la_linear_backward(const void *x, const void *w, const void *saved, size_t s
  *   h = act(x Wg^T) * (x Wu^T).
  * x [M][ldx], w_gate [F][ldwg], w_up [F][ldwu] (halves of one packed weight are fine), h [M][ldh]: bf16.
  * (The projection back is la_linear with the residual.)
- * saved   la_gated_ffn_saved_bytes(...) bytes (16-byte aligned) that receive both products, in bf16, for
- *         the backward pass; or NULL.
+ * saved   la_gated_ffn_saved_bytes(...) bytes (16-byte aligned) that receive both products, in 24 bits,
+ *         for the backward pass; or NULL.
  * h is rounded once, from the products as accumulated (fp32). */
 size_t la_gated_ffn_saved_bytes(int M, int F);
 int la_gated_ffn(const void *x, const void *w_gate, const void *w_up, void *h, void *saved,

@@ -1140,7 +1140,7 @@ int la_linear_backward(const void *x, const void *w, const void *saved, size_t s
 
 size_t la_gated_ffn_saved_bytes(int M, int F) {
     if (M < 1 || F < 1) return 0;
-    return 4 * (size_t)M * whole8(F);
+    return 6 * (size_t)M * whole8(F);
 }
 
 int la_gated_ffn(const void *x, const void *w_gate, const void *w_up, void *h, void *saved, size_t saved_bytes, int M,
@@ -1167,7 +1167,7 @@ int la_gated_ffn(const void *x, const void *w_gate, const void *w_up, void *h, v
 }
 
 size_t la_gated_ffn_backward_workspace_bytes(int M, int F, int K) {
-    return K < 1 ? 0 : la_gated_ffn_saved_bytes(M, F);
+    return M < 1 || F < 1 || K < 1 ? 0 : 4 * (size_t)M * whole8(F);
 }
 
 int la_gated_ffn_backward(const void *x, const void *w_gate, const void *w_up, const void *saved, size_t saved_bytes,

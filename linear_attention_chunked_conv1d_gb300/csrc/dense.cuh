@@ -108,6 +108,24 @@ __device__ __forceinline__ void act_slopes(float (&v)[N], float (&slope)[N], int
     });
 }
 
+// Values kept between forward and backward pass in 24 bits: fp32 without its last eight fraction bits, the upper 16
+// bits in one plane and the next eight in another. (Relative error below 2^-15, and no rounding that could carry a NaN's
+// pattern over.)
+__device__ __forceinline__ uint32_t upper2(float a, float b) { return __byte_perm(__float_as_uint(a), __float_as_uint(b), 0x7632); }
+__device__ __forceinline__ uint32_t lower4(float a, float b, float c, float d) {
+    return __byte_perm(__byte_perm(__float_as_uint(a), __float_as_uint(b), 0x51), __byte_perm(__float_as_uint(c), __float_as_uint(d), 0x51), 0x5410);
+}
+__device__ __forceinline__ uint4 upper8(const float *v) {
+    return make_uint4(upper2(v[0], v[1]), upper2(v[2], v[3]), upper2(v[4], v[5]), upper2(v[6], v[7]));
+}
+__device__ __forceinline__ uint2 lower8(const float *v) { return make_uint2(lower4(v[0], v[1], v[2], v[3]), lower4(v[4], v[5], v[6], v[7])); }
+__device__ __forceinline__ void joined8(const uint4 &upper, const uint2 &lower, float (&v)[8]) {
+    const uint32_t u[4] = {upper.x, upper.y, upper.z, upper.w}, l[2] = {lower.x, lower.y};
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        v[i] = __uint_as_float((i % 2 ? u[i / 2] & 0xFFFF0000u : u[i / 2] << 16) | (l[i / 4] >> i % 4 * 8 & 0xFFu) << 8);
+}
+
 // N values (16 bytes) of a row from column c on, of which those at or past `width` read as zero; and the
 // store of those before it. Rows start on 16 bytes, so only a row's last piece is taken by elements.
 template <class T>

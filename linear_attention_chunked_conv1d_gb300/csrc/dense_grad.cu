@@ -70,29 +70,30 @@ bias_sum_kernel(const float *__restrict__ partial, int runs, int N, bf16 *__rest
     }
 }
 
-// saved and d: [M][2 * half], gate in columns 0.., up from column half on.
+// d: [M][2 * half], gate in columns 0.., up from column half on; saved: the same in 24 bits, one plane of 16 and one of 8.
 __global__ void __launch_bounds__(256)
-gated_grad_kernel(const bf16 *__restrict__ saved, const bf16 *__restrict__ dh, bf16 *__restrict__ d, int M, int F,
+gated_grad_kernel(const uint8_t *__restrict__ saved, const bf16 *__restrict__ dh, bf16 *__restrict__ d, int M, int F,
                   int half, int64_t lddh, int act) {
     wait_for_previous();
     const int c = (blockIdx.x * 32 + threadIdx.x) * 8;
     if (c >= F) return;
+    const uint8_t *lower = saved + (int64_t)M * 4 * half;
     for (int64_t r = blockIdx.y * 8 + threadIdx.y; r < M; r += (int64_t)gridDim.y * 8) {
-        float gate[8], up[8], g[8];
-        const bf16 *s = saved + r * 2 * half;
-        bf16 *o = d + r * 2 * half;
-        load_piece(s, c, F, gate);
-        load_piece(s + half, c, F, up);
+        float gate[8], up[8], g[8], slope[8];
+        const int64_t at = r * 2 * half + c;  // whole pieces: the buffers' rows are
+        const uint4 gu = *reinterpret_cast<const uint4 *>(saved + 2 * at), uu = *reinterpret_cast<const uint4 *>(saved + 2 * (at + half));
+        const uint2 gl = *reinterpret_cast<const uint2 *>(lower + at), ul = *reinterpret_cast<const uint2 *>(lower + at + half);
         load_piece(dh + r * lddh, c, F, g);
-        float slope[8];
+        joined8(gu, gl, gate);
+        joined8(uu, ul, up);
         act_slopes(gate, slope, act);
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
             up[e] *= g[e] * slope[e];
             gate[e] *= g[e];
         }
-        store_piece(o, c, F, up);
-        store_piece(o + half, c, F, gate);
+        Vec16<bf16>::store(d + at, up);
+        Vec16<bf16>::store(d + at + half, gate);
     }
 }
 
@@ -119,7 +120,7 @@ cudaError_t launch_linear_grad(const LinearGradArgs &a, cudaStream_t st) {
 
 cudaError_t launch_gated_grad(const GatedGradArgs &a, cudaStream_t st) {
     return launch_overlapped(gated_grad_kernel, dim3((a.F + COLS - 1) / COLS, row_runs(a.M, a.F)), dim3(32, 8), 0, 0, st,
-                             (const bf16 *)a.saved, (const bf16 *)a.dh, (bf16 *)a.d, a.M, a.F, a.half, a.lddh, a.act);
+                             (const uint8_t *)a.saved, (const bf16 *)a.dh, (bf16 *)a.d, a.M, a.F, a.half, a.lddh, a.act);
 }
 
 }  // namespace la

@@ -14,7 +14,8 @@ struct Maps {
 struct Epilogue {
     __nv_bfloat16 *out[2];
     const __nv_bfloat16 *bias, *residual;
-    __nv_bfloat16 *saved;  // LINEAR: z [M][lds]; GATED: gate | up [M][2 * half]
+    __nv_bfloat16 *saved;  // LINEAR: z [M][lds]; GATED: upper 16 bits of gate | up [M][lds], up from column half on
+    uint8_t *lower;        // GATED: the next eight bits, laid out the same
     int64_t ldo[2], ldr, lds;
     int half, act;
 };
@@ -44,6 +45,7 @@ inline Epilogue make_epilogue(const DenseArgs &a) {
     ep.bias = (const __nv_bfloat16 *)a.bias;
     ep.residual = (const __nv_bfloat16 *)a.residual;
     ep.saved = (__nv_bfloat16 *)a.saved;
+    ep.lower = (uint8_t *)a.saved + 2 * (int64_t)a.M * a.lds;
     ep.ldr = a.ldr;
     ep.lds = a.lds;
     ep.half = a.half;

@@ -61,6 +61,12 @@ __device__ __forceinline__ void store4(__nv_bfloat16 *row, int c, int N, const f
     }
 }
 
+// Four values of gate or up for the backward pass (whole pieces: the buffer's rows are).
+__device__ __forceinline__ void keep4(const Epilogue &ep, int64_t row, int64_t c, const float *v) {
+    *reinterpret_cast<uint2 *>(ep.saved + row * ep.lds + c) = make_uint2(upper2(v[0], v[1]), upper2(v[2], v[3]));
+    *reinterpret_cast<uint32_t *>(ep.lower + row * ep.lds + c) = lower4(v[0], v[1], v[2], v[3]);
+}
+
 template <int KIND>
 __global__ void __launch_bounds__(THREADS, 2)
 dense_split_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Epilogue ep, const Plan plan, int M, int N, int K,
@@ -237,8 +243,8 @@ dense_split_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Ep
             }
             if (KIND == DENSE_GATED) {
                 if (ep.saved) {
-                    store4(ep.saved + row * ep.lds, col, N, v[i]);
-                    store4(ep.saved + row * ep.lds + ep.half, col, N, u[i]);
+                    keep4(ep, row, col, v[i]);
+                    keep4(ep, row, col + ep.half, u[i]);
                 }
                 act_values(v[i], ep.act);
 #pragma unroll

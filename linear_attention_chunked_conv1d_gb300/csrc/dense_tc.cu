@@ -101,6 +101,19 @@ __device__ __forceinline__ void flush(uint4 *buf, bf16 *out, int64_t ld, int64_t
     }
     __syncwarp();
 }
+// The same of a matrix of bytes, from each lane's row.
+__device__ __forceinline__ void flush_bytes(uint2 *buf, const uint2 (&mine)[8], uint8_t *out, int64_t ld, int64_t row0, int M, int col, int N, int lane) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) buf[lane * 8 + (j ^ (lane & 7))] = mine[j];
+    __syncwarp();
+    const int j = lane & 7, c = col + j * 8;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const int r = i * 4 + (lane >> 3);
+        if (row0 + r < M && c < N) *reinterpret_cast<uint2 *>(out + (row0 + r) * ld + c) = buf[r * 8 + (j ^ (r & 7))];
+    }
+    __syncwarp();
+}
 // The same of an input, first into registers (what lies outside stays as it is), then into the buffer.
 __device__ __forceinline__ void fetch(uint4 (&raw)[8], const bf16 *in, int64_t ld, int64_t row0, int M, int col, int N, int lane) {
     const int c = col + (lane & 7) * 8;
@@ -364,15 +377,21 @@ dense_kernel(const __grid_constant__ Maps maps0, const __grid_constant__ Maps ma
                     if (ep.saved) {
 #pragma unroll 1
                         for (int half = 0; half < 2; ++half) {
+                            uint2 lower[8];
 #pragma unroll
                             for (int j = 0; j < 8; j += 4) {
                                 float v[32];
                                 tc::tmem_ld16(src + half * (TN / 2) + j * 8, v);
                                 tc::tmem_ld16(src + half * (TN / 2) + j * 8 + 16, v + 16);
                                 tc::tmem_wait_ld();
-                                put(buf, lane, j, v);
+#pragma unroll
+                                for (int i = 0; i < 4; ++i) {
+                                    piece(buf, lane, j + i) = upper8(v + 8 * i);
+                                    lower[j + i] = lower8(v + 8 * i);
+                                }
                             }
                             flush(buf, ep.saved + half * ep.half, ep.lds, row0, M, col, N, lane);
+                            flush_bytes(reinterpret_cast<uint2 *>(buf), lower, ep.lower + half * ep.half, ep.lds, row0, M, col, N, lane);
                         }
                     }
 #pragma unroll 1

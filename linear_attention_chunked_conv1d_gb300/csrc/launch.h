@@ -269,7 +269,7 @@ size_t layernorm_backward_workspace_bytes(int rows, int width, int dtype);
 
 // The matrix products of the dense layers (dense_tc.cu), bf16:
 //   DENSE_LINEAR  out[0] [M][N] = act(a[0] [M][K] b[0] [N][K]^T + bias) + residual; saved: before act
-//   DENSE_GATED   out[0] [M][N] = act(a[0] b[0]^T) * (a[0] b[1]^T); saved [M][2 half]: both products
+//   DENSE_GATED   out[0] [M][N] = act(a[0] b[0]^T) * (a[0] b[1]^T); saved: both products, [M][2 half] in 16 + 8 bits
 //   DENSE_DX      out[0] [M][N] = sum over i < count of a[i] [M][K] b[i] [K][N]
 //   DENSE_DW      out[i] [M][N] = a[i] [K][M]^T b[0] [K][N], i < count
 enum { DENSE_LINEAR, DENSE_GATED, DENSE_DX, DENSE_DW };
@@ -307,7 +307,7 @@ struct LinearGradArgs {
 };
 size_t linear_backward_partial_bytes(int M, int N);
 cudaError_t launch_linear_grad(const LinearGradArgs &a, cudaStream_t st);
-// d [M][2 half] = dh up act'(gate) | dh act(gate) from saved [M][2 half] = gate | up.
+// d [M][2 half] = dh up act'(gate) | dh act(gate) from saved (as DENSE_GATED leaves it).
 struct GatedGradArgs {
     const void *saved, *dh;
     void *d;

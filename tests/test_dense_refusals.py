@@ -187,7 +187,7 @@ def test_ffn_backward(lib):
 
 def test_sizes_of_buffers(lib):
     assert lib.linear_saved_bytes(10, 60, "gelu") == 10 * 64 * 2 and lib.linear_saved_bytes(10, 60) == 0
-    assert lib.gated_ffn_saved_bytes(10, 61) == 10 * 128 * 2 and lib.gated_ffn_backward_workspace_bytes(10, 61, 7) == 10 * 128 * 2
+    assert lib.gated_ffn_saved_bytes(10, 61) == 10 * 128 * 3 and lib.gated_ffn_backward_workspace_bytes(10, 61, 7) == 10 * 128 * 2
     for call in (lib._load().la_linear_saved_bytes, lib._load().la_layernorm_rows_backward_workspace_bytes):
         assert call(0, 5, 1) == 0 and call(5, 0, 1) == 0
     assert lib._load().la_gated_ffn_saved_bytes(0, 5) == 0 and lib._load().la_linear_backward_workspace_bytes(5, 5, 0, 1) == 0
