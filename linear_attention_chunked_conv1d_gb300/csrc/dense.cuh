@@ -1,5 +1,6 @@
 // Activations of the dense layers' calls (la_linear, la_gated_ffn) and their derivatives, in fp32.
 #pragma once
+#include <cstring>
 #include <type_traits>
 
 #include "common.cuh"
@@ -108,6 +109,22 @@ __device__ __forceinline__ void act_slopes(float (&v)[N], float (&slope)[N], int
     });
 }
 
+template <class T> constexpr int kPiece = Vec16<T>::N;  // values of 16 bytes
+
+// 16 bytes of a row from column c on, what lies at or past `width` as zero bytes; and its values in fp32.
+template <class T>
+__device__ __forceinline__ uint4 load_raw(const T *row, int c, int width) {
+    uint4 v = make_uint4(0u, 0u, 0u, 0u);
+    if (c + kPiece<T> <= width) {
+        v = *reinterpret_cast<const uint4 *>(row + c);
+    } else if (c < width) {
+        T e[kPiece<T>];
+#pragma unroll
+        for (int i = 0; i < kPiece<T>; ++i) e[i] = c + i < width ? row[c + i] : from_f<T>(0.f);
+        memcpy(&v, e, 16);
+    }
+    return v;
+}
 // Values kept between forward and backward pass in 24 bits: fp32 without its last eight fraction bits, the upper 16
 // bits in one plane and the next eight in another. (Relative error below 2^-15, and no rounding that could carry a NaN's
 // pattern over.)

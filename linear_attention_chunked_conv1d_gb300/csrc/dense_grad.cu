@@ -15,10 +15,10 @@ namespace la {
 namespace {
 
 using bf16 = __nv_bfloat16;
-constexpr int COLS = 256, WARPS = 8;  // a block: 32 lanes of 8 columns, eight rows at a time
+constexpr int COLS = 256, WARPS = 8, ROWS = 2;  // a block: 32 lanes of 8 columns, eight warps of a row at a time, twice
 
 // dz may be null (act none: dz is dy); partial [gridDim.y][N] (or null): the sums of the block's rows.
-__global__ void __launch_bounds__(32 * WARPS)
+__global__ void __launch_bounds__(32 * WARPS, 4)
 linear_grad_kernel(const bf16 *__restrict__ saved, const bf16 *__restrict__ dy, bf16 *__restrict__ dz,
                    float *__restrict__ partial, int M, int N, int64_t lds, int64_t lddy, int64_t ldz, int act) {
     __shared__ float sh[WARPS][COLS];
@@ -26,20 +26,31 @@ linear_grad_kernel(const bf16 *__restrict__ saved, const bf16 *__restrict__ dy, 
     const int c = blockIdx.x * COLS + threadIdx.x * 8;
     float sum[8] = {};
     if (c < N)
-        for (int64_t r = blockIdx.y * WARPS + threadIdx.y; r < M; r += (int64_t)gridDim.y * WARPS) {
-            float d[8];
-            load_piece(dy + r * lddy, c, N, d);
-            if (saved) {
-                float z[8];
-                load_piece(saved + r * lds, c, N, z);
-                float slope[8];
-                act_slopes(z, slope, act);
+        for (int64_t first = blockIdx.y * WARPS + threadIdx.y; first < M; first += (int64_t)gridDim.y * WARPS * ROWS) {
+            uint4 dr[ROWS], zr[ROWS];
 #pragma unroll
-                for (int e = 0; e < 8; ++e) d[e] *= slope[e];
-                store_piece(dz + r * ldz, c, N, d);
+            for (int i = 0; i < ROWS; ++i) {  // several rows' loads are under way at one time
+                const int64_t r = first + (int64_t)i * gridDim.y * WARPS;
+                if (r >= M) continue;
+                dr[i] = load_raw(dy + r * lddy, c, N);
+                if (saved) zr[i] = *reinterpret_cast<const uint4 *>(saved + r * lds + c);  // whole pieces: the buffer's rows are
             }
 #pragma unroll
-            for (int e = 0; e < 8; ++e) sum[e] += d[e];
+            for (int i = 0; i < ROWS; ++i) {
+                const int64_t r = first + (int64_t)i * gridDim.y * WARPS;
+                if (r >= M) break;
+                float d[8], z[8], slope[8];
+                Vec16<bf16>::load(reinterpret_cast<const bf16 *>(&dr[i]), d);
+                if (saved) {
+                    Vec16<bf16>::load(reinterpret_cast<const bf16 *>(&zr[i]), z);
+                    act_slopes(z, slope, act);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) d[e] *= slope[e];
+                    Vec16<bf16>::store(dz + r * ldz + c, d);
+                }
+#pragma unroll
+                for (int e = 0; e < 8; ++e) sum[e] += d[e];
+            }
         }
     if (!partial) return;
 #pragma unroll
@@ -97,19 +108,19 @@ gated_grad_kernel(const uint8_t *__restrict__ saved, const bf16 *__restrict__ dh
     }
 }
 
-// Rows are shared out so that the grid has a few blocks for each SM.
-int row_runs(int M, int N) {
+// Rows are shared out so that the grid has `held` blocks for each SM.
+int row_runs(int M, int N, int held) {
     const int cols = (N + COLS - 1) / COLS, most = (M + WARPS - 1) / WARPS;
-    int runs = (152 * 6 + cols - 1) / cols;
-    return runs < most ? runs : most;
+    int runs = 152 * held / cols;
+    return runs < 1 ? 1 : runs < most ? runs : most;
 }
 
 }  // namespace
 
-size_t linear_backward_partial_bytes(int M, int N) { return (size_t)row_runs(M, N) * N * sizeof(float); }
+size_t linear_backward_partial_bytes(int M, int N) { return (size_t)row_runs(M, N, 4) * N * sizeof(float); }
 
 cudaError_t launch_linear_grad(const LinearGradArgs &a, cudaStream_t st) {
-    const int runs = row_runs(a.M, a.N);
+    const int runs = row_runs(a.M, a.N, 4);
     cudaError_t e = launch_overlapped(linear_grad_kernel, dim3((a.N + COLS - 1) / COLS, runs), dim3(32, WARPS), 0, 0, st,
                                       (const bf16 *)a.saved, (const bf16 *)a.dy, (bf16 *)a.dz,
                                       a.dbias ? a.partial : nullptr, a.M, a.N, a.lds, a.lddy, a.ldz, a.act);
@@ -119,7 +130,7 @@ cudaError_t launch_linear_grad(const LinearGradArgs &a, cudaStream_t st) {
 }
 
 cudaError_t launch_gated_grad(const GatedGradArgs &a, cudaStream_t st) {
-    return launch_overlapped(gated_grad_kernel, dim3((a.F + COLS - 1) / COLS, row_runs(a.M, a.F)), dim3(32, 8), 0, 0, st,
+    return launch_overlapped(gated_grad_kernel, dim3((a.F + COLS - 1) / COLS, row_runs(a.M, a.F, 6)), dim3(32, 8), 0, 0, st,
                              (const uint8_t *)a.saved, (const bf16 *)a.dh, (bf16 *)a.d, a.M, a.F, a.half, a.lddh, a.act);
 }
 
