@@ -791,17 +791,36 @@ def layernorm_rows_backward(x, w, stats, dy, dx, dw, db=None, *, dskip=None, wor
     """Gradients of layernorm_rows: dx [rows][width] (plus dskip [rows][width] where given: a gradient
     that reaches x past the norm; dx may be dy or dskip), dw and db fp32 [width]. x, w and stats are
     those of the forward call."""
-    dev = _on_gpu(x)
+    dev, dt = x.get_device(), x.dtype
     rows, width = x.shape
-    dt = x.dtype
-    ws, ws_bytes = _room("workspace", workspace, dev)
+    (xs, x1), (ys, y1), (ds, d1) = x.stride(), dy.stride(), dx.stride()
+    ss, s1 = (ds, 1) if dskip is None else dskip.stride()
+    f32 = torch.float32
+    # As in gated_scan: one look at everything, and only where something is unusual the checks that say what.
+    if not (dev >= 0 and dev == _current_device() and x1 == y1 == d1 == s1 == 1 and dy.dtype is dt and dx.dtype is dt
+            and dy.shape == (rows, width) and dx.shape == (rows, width) and dy.get_device() == dev
+            and dx.get_device() == dev and w.dtype is dt and w.shape == (width,) and w.is_contiguous()
+            and w.get_device() == dev and stats.dtype is f32 and stats.shape == (rows, 2) and stats.is_contiguous()
+            and stats.get_device() == dev and dw.dtype is f32 and dw.shape == (width,) and dw.is_contiguous()
+            and dw.get_device() == dev
+            and (db is None or (db.dtype is f32 and db.shape == (width,) and db.is_contiguous() and db.get_device() == dev))
+            and (dskip is None or (dskip.dtype is dt and dskip.shape == (rows, width) and dskip.get_device() == dev))
+            and workspace is not None and workspace.is_contiguous() and workspace.get_device() == dev):
+        _on_gpu(x)
+        xs, ys, ds = (_matrix16(name, t, rows, width, dt, dev) for name, t in (("x", x), ("dy", dy), ("dx", dx)))
+        ss = 0 if dskip is None else _matrix16("dskip", dskip, rows, width, dt, dev)
+        _dense("w", w, (width,), dt, dev)
+        _dense("stats", stats, (rows, 2), f32, dev)
+        _dense("dw", dw, (width,), f32, dev)
+        _vector("db", db, width, f32, dev)
+        _room("workspace", workspace, dev)
+    if rows == 1:  # a single row's stride says nothing
+        xs = ys = ds = ss = (width + 7) // 8 * 8
     _check(_load().la_layernorm_rows_backward(
-        x.data_ptr(), _vector("w", w, width, dt, dev), _dense("stats", stats, (rows, 2), torch.float32, dev),
-        dy.data_ptr(), None if dskip is None else dskip.data_ptr(), dx.data_ptr(),
-        _vector("dw", dw, width, torch.float32, dev), _vector("db", db, width, torch.float32, dev), rows, width,
-        _matrix16("x", x, rows, width, dt, dev), _matrix16("dy", dy, rows, width, dt, dev),
-        0 if dskip is None else _matrix16("dskip", dskip, rows, width, dt, dev),
-        _matrix16("dx", dx, rows, width, dt, dev), _dtype_code(x), ws, ws_bytes, _stream_on(stream, dev)))
+        x.data_ptr(), w.data_ptr(), stats.data_ptr(), dy.data_ptr(), None if dskip is None else dskip.data_ptr(),
+        dx.data_ptr(), dw.data_ptr(), None if db is None else db.data_ptr(), rows, width, xs, ys, ss, ds, _dtype_code(x),
+        None if workspace is None else workspace.data_ptr(),
+        0 if workspace is None else workspace.numel() * workspace.element_size(), _stream_on(stream, dev)))
 
 
 def linear_saved_bytes(rows, outputs, act="none") -> int:
@@ -861,19 +880,41 @@ def linear_backward(x, w, saved, dy, dx=None, dw=None, *, dbias=None, act="none"
     """Gradients of linear: dx [M][K], dw [N][K] and dbias [N] (bf16; those that are given) from dy
     [M][N]; the residual's is dy itself. x, w, saved (None without an activation) and act are those of
     the forward call."""
-    dev = _on_gpu(x)
+    dev, bf16 = x.get_device(), torch.bfloat16
     M, K = x.shape
     N = w.shape[0]
-    bf16 = torch.bfloat16
-    sv, sv_bytes = _room("saved", saved, dev)
-    ws, ws_bytes = _room("workspace", workspace, dev)
+    (xs, x1), (ws, w1), (ys, y1) = x.stride(), w.stride(), dy.stride()
+    ds, d1 = (xs, 1) if dx is None else dx.stride()
+    gs, g1 = (ws, 1) if dw is None else dw.stride()
+    # As in gated_scan: one look at everything, and only where something is unusual the checks that say what.
+    if not (dev >= 0 and dev == _current_device() and x1 == w1 == y1 == d1 == g1 == 1 and x.dtype is bf16
+            and w.dtype is bf16 and dy.dtype is bf16 and w.shape == (N, K) and dy.shape == (M, N)
+            and w.get_device() == dev and dy.get_device() == dev
+            and (dx is None or (dx.dtype is bf16 and dx.shape == (M, K) and dx.get_device() == dev))
+            and (dw is None or (dw.dtype is bf16 and dw.shape == (N, K) and dw.get_device() == dev))
+            and (dbias is None or (dbias.dtype is bf16 and dbias.shape == (N,) and dbias.is_contiguous()
+                                   and dbias.get_device() == dev))
+            and (saved is None or (saved.is_contiguous() and saved.get_device() == dev))
+            and (workspace is None or (workspace.is_contiguous() and workspace.get_device() == dev))):
+        _on_gpu(x)
+        xs, ws, ys = (_matrix16("x", x, M, K, bf16, dev), _matrix16("w", w, N, K, bf16, dev),
+                      _matrix16("dy", dy, M, N, bf16, dev))
+        ds = 0 if dx is None else _matrix16("dx", dx, M, K, bf16, dev)
+        gs = 0 if dw is None else _matrix16("dw", dw, N, K, bf16, dev)
+        _vector("dbias", dbias, N, bf16, dev)
+        _room("saved", saved, dev)
+        _room("workspace", workspace, dev)
+    if M == 1:  # a single row's stride says nothing
+        xs = ds = (K + 7) // 8 * 8
+        ys = (N + 7) // 8 * 8
+    if N == 1:
+        ws = gs = (K + 7) // 8 * 8
     _check(_load().la_linear_backward(
-        x.data_ptr(), w.data_ptr(), sv, sv_bytes, dy.data_ptr(), None if dx is None else dx.data_ptr(),
-        None if dw is None else dw.data_ptr(), _vector("dbias", dbias, N, bf16, dev), M, N, K,
-        _matrix16("x", x, M, K, bf16, dev), _matrix16("w", w, N, K, bf16, dev),
-        _matrix16("dy", dy, M, N, bf16, dev), 0 if dx is None else _matrix16("dx", dx, M, K, bf16, dev),
-        0 if dw is None else _matrix16("dw", dw, N, K, bf16, dev), _act_code(act), ws, ws_bytes,
-        _stream_on(stream, dev)))
+        x.data_ptr(), w.data_ptr(), None if saved is None else saved.data_ptr(),
+        0 if saved is None else saved.numel() * saved.element_size(), dy.data_ptr(), None if dx is None else dx.data_ptr(),
+        None if dw is None else dw.data_ptr(), None if dbias is None else dbias.data_ptr(), M, N, K, xs, ws, ys, ds, gs,
+        _act_code(act), None if workspace is None else workspace.data_ptr(),
+        0 if workspace is None else workspace.numel() * workspace.element_size(), _stream_on(stream, dev)))
 
 
 def gated_ffn_saved_bytes(rows, hidden) -> int:
@@ -925,17 +966,39 @@ def gated_ffn_backward(x, w_gate, w_up, saved, dh, dx=None, dw_gate=None, dw_up=
                        workspace=None, stream=None) -> None:
     """Gradients of gated_ffn: dx [M][K] and/or dw_gate and dw_up [F][K] (bf16) from dh [M][F]. x, the
     weights, saved and act are those of the forward call."""
-    dev = _on_gpu(x)
+    dev, bf16 = x.get_device(), torch.bfloat16
     M, K = x.shape
     F = w_gate.shape[0]
-    bf16 = torch.bfloat16
-    sv, sv_bytes = _room("saved", saved, dev)
-    ws, ws_bytes = _room("workspace", workspace, dev)
-    opt = lambda name, t, rows: (None, 0) if t is None else (  # noqa: E731
-        t.data_ptr(), _matrix16(name, t, rows, K, bf16, dev))
-    (pdx, lddx), (pg, lddg), (pu, lddu) = opt("dx", dx, M), opt("dw_gate", dw_gate, F), opt("dw_up", dw_up, F)
+    (xs, x1), (gs, g1), (us, u1), (hs, h1) = x.stride(), w_gate.stride(), w_up.stride(), dh.stride()
+    ds, d1 = (xs, 1) if dx is None else dx.stride()
+    (dgs, dg1), (dus, du1) = ((gs, 1), (us, 1)) if dw_gate is None or dw_up is None else (dw_gate.stride(), dw_up.stride())
+    # As in gated_scan: one look at everything, and only where something is unusual the checks that say what.
+    if not (dev >= 0 and dev == _current_device() and x1 == g1 == u1 == h1 == d1 == dg1 == du1 == 1 and x.dtype is bf16
+            and w_gate.dtype is bf16 and w_up.dtype is bf16 and dh.dtype is bf16 and w_gate.shape == (F, K)
+            and w_up.shape == (F, K) and dh.shape == (M, F) and w_gate.get_device() == dev
+            and w_up.get_device() == dev and dh.get_device() == dev
+            and (dx is None or (dx.dtype is bf16 and dx.shape == (M, K) and dx.get_device() == dev))
+            and ((dw_gate is None and dw_up is None)
+                 or (dw_gate is not None and dw_up is not None and dw_gate.dtype is bf16 and dw_up.dtype is bf16
+                     and dw_gate.shape == (F, K) and dw_up.shape == (F, K) and dw_gate.get_device() == dev
+                     and dw_up.get_device() == dev))
+            and saved is not None and saved.is_contiguous() and saved.get_device() == dev
+            and workspace is not None and workspace.is_contiguous() and workspace.get_device() == dev):
+        _on_gpu(x)
+        xs, hs = _matrix16("x", x, M, K, bf16, dev), _matrix16("dh", dh, M, F, bf16, dev)
+        gs, us = _matrix16("w_gate", w_gate, F, K, bf16, dev), _matrix16("w_up", w_up, F, K, bf16, dev)
+        ds, dgs, dus = (0 if t is None else _matrix16(name, t, r, K, bf16, dev)
+                        for name, t, r in (("dx", dx, M), ("dw_gate", dw_gate, F), ("dw_up", dw_up, F)))
+        _room("saved", saved, dev)
+        _room("workspace", workspace, dev)
+    if M == 1:  # a single row's stride says nothing
+        xs = ds = (K + 7) // 8 * 8
+        hs = (F + 7) // 8 * 8
+    if F == 1:
+        gs = us = dgs = dus = (K + 7) // 8 * 8
     _check(_load().la_gated_ffn_backward(
-        x.data_ptr(), w_gate.data_ptr(), w_up.data_ptr(), sv, sv_bytes, dh.data_ptr(), pdx, pg, pu, M, F, K,
-        _matrix16("x", x, M, K, bf16, dev), _matrix16("w_gate", w_gate, F, K, bf16, dev),
-        _matrix16("w_up", w_up, F, K, bf16, dev), _matrix16("dh", dh, M, F, bf16, dev), lddx, lddg, lddu,
-        _act_code(act), ws, ws_bytes, _stream_on(stream, dev)))
+        x.data_ptr(), w_gate.data_ptr(), w_up.data_ptr(), None if saved is None else saved.data_ptr(),
+        0 if saved is None else saved.numel() * saved.element_size(), dh.data_ptr(), None if dx is None else dx.data_ptr(),
+        None if dw_gate is None else dw_gate.data_ptr(), None if dw_up is None else dw_up.data_ptr(), M, F, K, xs, gs, us, hs,
+        ds, dgs, dus, _act_code(act), None if workspace is None else workspace.data_ptr(),
+        0 if workspace is None else workspace.numel() * workspace.element_size(), _stream_on(stream, dev)))

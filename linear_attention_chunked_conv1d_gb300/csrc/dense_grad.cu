@@ -17,10 +17,11 @@ namespace {
 using bf16 = __nv_bfloat16;
 constexpr int COLS = 256, WARPS = 8, ROWS = 2;  // a block: 32 lanes of 8 columns, eight warps of a row at a time, twice
 
-// dz may be null (act none: dz is dy); partial [gridDim.y][N] (or null): the sums of the block's rows.
+// dz may be null (act none: dz is dy); partial [gridDim.y][N] (or null): the sums of the block's rows; where there
+// is one block to a column, its sums are the gradient.
 __global__ void __launch_bounds__(32 * WARPS, 4)
 linear_grad_kernel(const bf16 *__restrict__ saved, const bf16 *__restrict__ dy, bf16 *__restrict__ dz,
-                   float *__restrict__ partial, int M, int N, int64_t lds, int64_t lddy, int64_t ldz, int act) {
+                   float *__restrict__ partial, bf16 *__restrict__ dbias, int M, int N, int64_t lds, int64_t lddy, int64_t ldz, int act) {
     __shared__ float sh[WARPS][COLS];
     wait_for_previous();
     const int c = blockIdx.x * COLS + threadIdx.x * 8;
@@ -52,7 +53,7 @@ linear_grad_kernel(const bf16 *__restrict__ saved, const bf16 *__restrict__ dy, 
                 for (int e = 0; e < 8; ++e) sum[e] += d[e];
             }
         }
-    if (!partial) return;
+    if (!dbias) return;
 #pragma unroll
     for (int e = 0; e < 8; ++e) sh[threadIdx.y][threadIdx.x * 8 + e] = sum[e];
     __syncthreads();
@@ -60,7 +61,9 @@ linear_grad_kernel(const bf16 *__restrict__ saved, const bf16 *__restrict__ dy, 
     float s = 0.f;
 #pragma unroll
     for (int w = 0; w < WARPS; ++w) s += sh[w][k];
-    if (blockIdx.x * COLS + k < N) partial[(int64_t)blockIdx.y * N + blockIdx.x * COLS + k] = s;
+    const int at = blockIdx.x * COLS + k;
+    if (at < N && gridDim.y == 1) dbias[at] = __float2bfloat16_rn(s);
+    else if (at < N) partial[(int64_t)blockIdx.y * N + at] = s;
 }
 
 __global__ void __launch_bounds__(32 * 16)
@@ -108,8 +111,10 @@ gated_grad_kernel(const uint8_t *__restrict__ saved, const bf16 *__restrict__ dh
     }
 }
 
-// Rows are shared out so that the grid has `held` blocks for each SM.
+// Rows are shared out so that the grid has `held` blocks for each SM; a few rows stay in one block (a second launch,
+// for the blocks' sums, takes as long as eight rows a warp).
 int row_runs(int M, int N, int held) {
+    if (M <= 8 * WARPS) return 1;
     const int cols = (N + COLS - 1) / COLS, most = (M + WARPS - 1) / WARPS;
     int runs = 152 * held / cols;
     return runs < 1 ? 1 : runs < most ? runs : most;
@@ -123,8 +128,8 @@ cudaError_t launch_linear_grad(const LinearGradArgs &a, cudaStream_t st) {
     const int runs = row_runs(a.M, a.N, 4);
     cudaError_t e = launch_overlapped(linear_grad_kernel, dim3((a.N + COLS - 1) / COLS, runs), dim3(32, WARPS), 0, 0, st,
                                       (const bf16 *)a.saved, (const bf16 *)a.dy, (bf16 *)a.dz,
-                                      a.dbias ? a.partial : nullptr, a.M, a.N, a.lds, a.lddy, a.ldz, a.act);
-    if (e != cudaSuccess || !a.dbias) return e;
+                                      a.partial, (bf16 *)a.dbias, a.M, a.N, a.lds, a.lddy, a.ldz, a.act);
+    if (e != cudaSuccess || !a.dbias || runs == 1) return e;
     return launch_overlapped(bias_sum_kernel, dim3((a.N + 31) / 32), dim3(32, 16), 0, 0, st, (const float *)a.partial, runs,
                              a.N, (bf16 *)a.dbias);
 }

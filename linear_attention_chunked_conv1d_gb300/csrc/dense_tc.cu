@@ -25,6 +25,7 @@
 #include <cuda.h>
 
 #include <atomic>
+#include <cmath>
 
 #include "dense.cuh"
 #include "dense_maps.cuh"
@@ -479,7 +480,7 @@ cudaError_t launch(const DenseArgs &a, const DenseArgs *b, cudaStream_t st) {
 }  // namespace
 
 cudaError_t launch_dense(const DenseArgs &a, cudaStream_t st) {
-    if (dense_split_serves(a)) return launch_dense_split(a, st);
+    if (dense_split_us(a, nullptr) < dense_pairs_us(a, nullptr)) return launch_dense_split(a, nullptr, st);
     switch (a.kind) {
         case DENSE_LINEAR: return launch<LINEAR>(a, nullptr, st);
         case DENSE_GATED: return launch<GATED>(a, nullptr, st);
@@ -488,12 +489,15 @@ cudaError_t launch_dense(const DenseArgs &a, cudaStream_t st) {
 }
 
 cudaError_t launch_dense_pair(const DenseArgs &dx, const DenseArgs &dw, cudaStream_t st) {
-    if (dense_split_serves(dx) || dense_split_serves(dw)) {
+    const double pairs = dense_pairs_us(dx, &dw), split = dense_split_us(dx, &dw);
+    const double apart = fmin(dense_pairs_us(dx, nullptr), dense_split_us(dx, nullptr)) + fmin(dense_pairs_us(dw, nullptr), dense_split_us(dw, nullptr));
+    if (apart < fmin(pairs, split)) {
         const cudaError_t e = launch_dense(dx, st);
         return e != cudaSuccess ? e : launch_dense(dw, st);
     }
-    const bool dx_first = (int64_t)dx.K * dx.count >= dw.K;
-    return dx_first ? launch<BACKWARD>(dx, &dw, st) : launch<BACKWARD>(dw, &dx, st);
+    const bool dx_first = (int64_t)dx.K * dx.count >= dw.K;  // the longer sums first
+    const DenseArgs &a = dx_first ? dx : dw, &b = dx_first ? dw : dx;
+    return split < pairs ? launch_dense_split(a, &b, st) : launch<BACKWARD>(a, &b, st);
 }
 
 }  // namespace la

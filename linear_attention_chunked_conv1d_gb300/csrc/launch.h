@@ -292,8 +292,10 @@ cudaError_t launch_dense(const DenseArgs &a, cudaStream_t st);
 // DENSE_DX and DENSE_DW of one backward pass (status, waits and knob: dx's).
 cudaError_t launch_dense_pair(const DenseArgs &dx, const DenseArgs &dw, cudaStream_t st);
 // Those with few output tiles: the summed index split over a cluster's blocks (dense_split.cu).
-bool dense_split_serves(const DenseArgs &a);
-cudaError_t launch_dense_split(const DenseArgs &a, cudaStream_t st);
+// b: another product of the same backward pass, or null.
+cudaError_t launch_dense_split(const DenseArgs &a, const DenseArgs *b, cudaStream_t st);
+double dense_pairs_us(const DenseArgs &a, const DenseArgs *b);
+double dense_split_us(const DenseArgs &a, const DenseArgs *b);
 
 // Gradients before the activation (dense_grad.cu): dz = dy act'(saved), dbias = its column sums.
 // saved null: dz is dy and is not written.

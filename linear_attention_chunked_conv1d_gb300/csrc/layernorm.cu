@@ -168,13 +168,13 @@ __device__ __forceinline__ void copy_piece(void *dst, const T *row, int c, int w
                  : "memory");
 }
 
-// partial [gridDim.x][2][width]: a block's sums of dy xh and of dy. Rows come DEPTH ahead through a ring in
+// partial [gridDim.x][2][width]: a block's sums of dy xh and of dy; a single block's are dw and db. Rows come DEPTH ahead through a ring in
 // shared memory to which each thread copies its own columns, so that nothing but the row's two sums is shared.
 constexpr int depth(int bufs, int p, int threads) { return 3 * bufs * p * threads * 16 > 220 * 1024 ? 2 : 3; }
 template <class T, int TPR, int P, bool SKIP>
 __global__ void __launch_bounds__(block_threads(TPR), TPR > 128 ? 1 : TPR == 64 ? 4 : 3)
 layernorm_backward_kernel(const T *__restrict__ x, const T *__restrict__ w, const float2 *__restrict__ stats, const T *dy,
-                          const T *dskip, T *dx, float *__restrict__ partial, int rows, int width, int64_t ldx, int64_t lddy,
+                          const T *dskip, T *dx, float *__restrict__ partial, float *__restrict__ dw, float *__restrict__ db, int rows, int width, int64_t ldx, int64_t lddy,
                           int64_t ldskip, int64_t lddx) {
     constexpr int N = kPiece<T>, H = N / 2, G = block_threads(TPR) / TPR, BUFS = SKIP ? 3 : 2;
     constexpr int DEPTH = depth(BUFS, P, block_threads(TPR));
@@ -249,7 +249,8 @@ layernorm_backward_kernel(const T *__restrict__ x, const T *__restrict__ w, cons
         st = next;
         stage = stage == DEPTH - 1 ? 0 : stage + 1;
     }
-    float *out = partial + (int64_t)blockIdx.x * 2 * width;
+    float *out_w = gridDim.x == 1 ? dw : partial + (int64_t)blockIdx.x * 2 * width;
+    float *out_b = gridDim.x == 1 ? db : out_w + width;
     float fw[P][N], fb[P][N];
 #pragma unroll
     for (int i = 0; i < P; ++i)
@@ -275,7 +276,8 @@ layernorm_backward_kernel(const T *__restrict__ x, const T *__restrict__ w, cons
             float s = 0.f;
 #pragma unroll
             for (int k = 0; k < G; ++k) s += cross[k * 2 * width + c];
-            out[c] = s;
+            if (c < width) out_w[c] = s;
+            else if (out_b) out_b[c - width] = s;
         }
     } else {
 #pragma unroll
@@ -284,8 +286,8 @@ layernorm_backward_kernel(const T *__restrict__ x, const T *__restrict__ w, cons
             for (int e = 0; e < N; ++e) {
                 const int c = (t + i * TPR) * N + e;
                 if (c < width) {
-                    out[c] = fw[i][e];
-                    out[width + c] = fb[i][e];
+                    out_w[c] = fw[i][e];
+                    if (out_b) out_b[c] = fb[i][e];
                 }
             }
     }
@@ -358,6 +360,7 @@ constexpr int MOST_BLOCKS = 152 * 4;
 int backward_blocks(int rows, int groups, int threads, size_t smem) {
     const int room = (int)(227 * 1024 / (smem + 1024 + 256)), held = threads == 64 ? 4 : threads == 128 ? 3 : 1;
     const int most = 152 * (room < 1 ? 1 : room < held ? room : held);
+    if (rows <= 8 * groups) return 1;  // and no second launch
     const int need = (int)(((int64_t)rows + 4 * groups - 1) / (4 * groups));
     return need < most ? need : most;
 }
@@ -383,12 +386,12 @@ cudaError_t backward(const LayerNormBwdArgs &a, cudaStream_t st) {
             const cudaError_t set = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
             if (set != cudaSuccess) return set;
             return launch_overlapped(kernel, dim3(blocks), dim3(block_threads(TPR)), smem, 0, st, (const T *)a.x, (const T *)a.w,
-                                     (const float2 *)a.stats, (const T *)a.dy, (const T *)a.dskip, (T *)a.dx, (float *)a.workspace,
+                                     (const float2 *)a.stats, (const T *)a.dy, (const T *)a.dskip, (T *)a.dx, (float *)a.workspace, a.dw, a.db,
                                      a.rows, a.width, a.ldx, a.lddy, a.ldskip, a.lddx);
         };
         return a.dskip ? launch(layernorm_backward_kernel<T, TPR, P, true>, 3) : launch(layernorm_backward_kernel<T, TPR, P, false>, 2);
     });
-    if (e != cudaSuccess) return e;
+    if (e != cudaSuccess || blocks == 1) return e;
     return launch_overlapped(layernorm_sums_kernel, dim3((2 * a.width + 31) / 32), dim3(32, SUM_Y), 0, 0, st,
                              (const float *)a.workspace, blocks, a.width, a.dw, a.db);
 }
