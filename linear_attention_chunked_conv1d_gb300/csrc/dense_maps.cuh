@@ -25,14 +25,16 @@ struct Epilogue {
 inline bool make_maps(Maps *maps, const DenseArgs &a, bool a_mn, bool b_mn, uint32_t box_a, uint32_t box_b) {
     const int na = a.kind == DENSE_DX || a.kind == DENSE_DW ? a.count : 1;
     const int nb = a.kind == DENSE_GATED ? 2 : a.kind == DENSE_DX ? a.count : 1;
-    for (int i = 0; i < 2; ++i) {
-        const int ia = i < na ? i : 0, ib = i < nb ? i : 0;
-        if (!(a_mn ? make_map_bf16_2d(&maps->a[i], a.a[ia], a.K, a.M, a.lda[ia], 64, 64, true)
-                   : make_map_bf16_2d(&maps->a[i], a.a[ia], a.M, a.K, a.lda[ia], 64, box_a, true)) ||
-            !(b_mn ? make_map_bf16_2d(&maps->b[i], a.b[ib], a.K, a.N, a.ldb[ib], 64, 64, true)
-                   : make_map_bf16_2d(&maps->b[i], a.b[ib], a.N, a.K, a.ldb[ib], 64, box_b, true)))
+    for (int i = 0; i < na; ++i)
+        if (!(a_mn ? make_map_bf16_2d(&maps->a[i], a.a[i], a.K, a.M, a.lda[i], 64, 64, true)
+                   : make_map_bf16_2d(&maps->a[i], a.a[i], a.M, a.K, a.lda[i], 64, box_a, true)))
             return false;
-    }
+    for (int i = 0; i < nb; ++i)
+        if (!(b_mn ? make_map_bf16_2d(&maps->b[i], a.b[i], a.K, a.N, a.ldb[i], 64, 64, true)
+                   : make_map_bf16_2d(&maps->b[i], a.b[i], a.N, a.K, a.ldb[i], 64, box_b, true)))
+            return false;
+    if (na == 1) maps->a[1] = maps->a[0];
+    if (nb == 1) maps->b[1] = maps->b[0];
     return true;
 }
 

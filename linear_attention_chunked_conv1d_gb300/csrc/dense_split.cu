@@ -25,7 +25,7 @@ namespace {
 
 constexpr int PT = 128, TK = 64;  // columns of the result, summed indexes of a stage
 constexpr uint32_t P_BYTES = PT * TK * 2;
-constexpr int THREADS = 192, MAX_STAGES = 8;
+constexpr int THREADS = 256, MAX_STAGES = 8;
 constexpr uint64_t WAIT_NS = 2000000000ull;
 constexpr uint32_t SLEEP_NS = 1000000u;
 
@@ -199,20 +199,18 @@ dense_split_kernel(const __grid_constant__ Maps maps0, const __grid_constant__ M
     tc::fence_after_sync();
     // the block's part of the tile, [rows][128 lanes] fp32
     float *part = reinterpret_cast<float *>(ring);
-    if (warp >= 2) {
-        const uint32_t q = warp & 3;
+    const uint32_t q = warp & 3;  // the warp's TMEM lanes; its columns are every other 16
 #pragma unroll 1
-        for (uint32_t c = 0; c < rows; c += 16) {
-            float v[16] = {};
-            if (k_first < k_end) {  // a short sum may leave some blocks nothing
-                tc::tmem_ld16(tc::tmem_addr(tm, 32 * q, c), v);
-                tc::tmem_wait_ld();
-            }
-#pragma unroll
-            for (int e = 0; e < 16; ++e) part[(c + e) * PT + 32 * q + lane] = v[e];
+    for (uint32_t c = warp / 4 * 16; c < rows; c += 32) {
+        float v[16] = {};
+        if (k_first < k_end) {  // a short sum may leave some blocks nothing
+            tc::tmem_ld16(tc::tmem_addr(tm, 32 * q, c), v);
+            tc::tmem_wait_ld();
         }
-        tc::fence_before_sync();
+#pragma unroll
+        for (int e = 0; e < 16; ++e) part[(c + e) * PT + 32 * q + lane] = v[e];
     }
+    tc::fence_before_sync();
     if (split > 1) tc::cluster_sync();
     else __syncthreads();
     if (warp == 1) tc::tmem_dealloc(tm, cols);
@@ -337,7 +335,7 @@ double rounds(double a, double n, double b, double m, double places) {
 //                        than 6 + bytes / 6 TB/s.
 // Pairs and this kernel as measured, M x N x K: linear 1 x 4096 x 4096 23.9 and 10.0, 128: 24.2 and 16.0, 512: 24.8 and
 // 23.5, 1024: 26.0 and 36.2; 1024 x 1024 x 8192 41.1 and 22.8; 2048 x 2048 x 2048 17.4 and 23.9; 777 x 5008 x 2048 24.6
-// and 21.0, with bias, GELU and residual 29.5 and 30.5; 8192 x 8192 x 64 46.5 and 112; gated 32 x 8192 x 4096 29.5 and
+// and 20.0, with bias, GELU and residual 29.5 and 27.3; 8192 x 8192 x 64 46.5 and 112; gated 32 x 8192 x 4096 29.5 and
 // 25.5, 256: 30.8 and 35.6; dx 256 x 8192 x 4096 40.7 and 24.2, 1024: 43.0 and 57.3; dw of 16384 rows, 1024 x 1024: 74.2
 // and 35.9, of 1024 rows, 2048 x 2048: 12.1 and 16.1.
 double dense_pairs_us(const DenseArgs &a, const DenseArgs *b) {
