@@ -190,12 +190,15 @@ dense_kernel(const __grid_constant__ Maps maps0, const __grid_constant__ Maps ma
     const uint32_t tm = *tmem_sh;
     const int64_t ntiles = job0.tiles + (KIND == BACKWARD ? job1.tiles : 0);
     const int64_t first = blockIdx.x / 2, step = gridDim.x / 2;
+    // Every round of tiles but the first goes to the pairs from the last to the first: where the first pairs had the longer
+    // sums, the last ones have an incomplete round's.
+    auto later_tile = [&](int64_t round) { return round * step + (step - 1 - first); };
     const uint32_t sbase = tc::smem_u32(sm);
 
     if (warp == 0) {
         if (tc::elect_one()) {
             uint32_t s = 0, ph = 0, used = 0;
-            for (int64_t tile = first; tile < ntiles && !*err; tile += step) {
+            for (int64_t tile = first, round = 0; tile < ntiles && !*err; tile = later_tile(++round)) {
                 const bool second = KIND == BACKWARD && tile >= job0.tiles;
                 const Job &job = second ? job1 : job0;
                 const Maps &maps = second ? maps1 : maps0;
@@ -253,7 +256,7 @@ dense_kernel(const __grid_constant__ Maps maps0, const __grid_constant__ Maps ma
         if (rank == 0 && tc::elect_one()) {
             uint32_t s = 0, ph = 0, tcnt = 0;
             if (debug_stall && !tc::mbar_wait(fin, 0, wait_ns, SLEEP_NS)) *err = 1;
-            for (int64_t tile = first; tile < ntiles && !*err; tile += step, ++tcnt) {
+            for (int64_t tile = first; tile < ntiles && !*err; tile = later_tile(++tcnt)) {
                 const bool second = KIND == BACKWARD && tile >= job0.tiles;
                 const Job &job = second ? job1 : job0;
                 const bool a_mn = KIND == BACKWARD && job.dw;
@@ -299,7 +302,7 @@ dense_kernel(const __grid_constant__ Maps maps0, const __grid_constant__ Maps ma
         const int c_first = (warp - 2) / 4 * COLS;
         uint4 *buf = reinterpret_cast<uint4 *>(sm + OFF_OUT) + (warp - 2) * 256;
         uint32_t tcnt = 0;
-        for (int64_t tile = first; tile < ntiles; tile += step, ++tcnt) {
+        for (int64_t tile = first; tile < ntiles; tile = later_tile(++tcnt)) {
             // every decision to stop is made per warp: the TMEM loads below are warp-collective
             if (__any_sync(0xffffffffu, *err != 0)) break;
             const bool second = KIND == BACKWARD && tile >= job0.tiles;
