@@ -319,38 +319,42 @@ double memory_us(const DenseArgs &a) {
                                                                            : M * K + (a.kind == DENSE_GATED ? 2 : 1) * N * K + M * N;
     return values * (2 / 6e6);
 }
-// n things of a and m of b, side by side in `places`.
-double rounds(double a, double n, double b, double m, double places) {
-    const double longest = m > 0 && b > a ? b : a, all = n + m;
-    if (all <= places) return longest;
-    return m > 0 ? fmax(longest, (a * n + b * m) / places) + longest / 2 : a * ceil(n / places);
+// n things that take a and m that take b, side by side in `places`; the rest of a last round takes `last` of its time
+// where it fills no more than half the places.
+double rounds(double a, double n, double b, double m, double places, double last) {
+    const double longest = m > 0 && b > a ? b : a, all = n + m, rest = all - places * floor(all / places);
+    const double tail = rest == 0 ? 0 : 2 * rest <= places ? last : 1;
+    if (all <= places) return longest * tail + (tail == 0 ? longest : 0);
+    return m > 0 ? fmax(longest, (a * n + b * m) / places) + longest / 2 : a * (floor(n / places) + tail);
 }
 
 }  // namespace
 
 // What a product, or two in one launch, take by either kernel, in us, as far as sizes say:
 //   pairs (dense_tc.cu)  5 + for each time the tiles go round the 76 pairs 0.29 a stage of 64 summed indexes and no less
-//                        than 3.2, the epilogue's; and no less than 7 + bytes / 6 TB/s;
-//   this one             2 + for each time the blocks go round the 304 places 6 and 0.41 a stage of 32 KB; and no less
-//                        than 6 + bytes / 6 TB/s.
-// Pairs and this kernel as measured, M x N x K: linear 1 x 4096 x 4096 23.9 and 10.0, 128: 24.2 and 16.0, 512: 24.8 and
-// 23.5, 1024: 26.0 and 36.2; 1024 x 1024 x 8192 41.1 and 22.8; 2048 x 2048 x 2048 17.4 and 23.9; 777 x 5008 x 2048 24.6
-// and 20.0, with bias, GELU and residual 29.5 and 27.3; 8192 x 8192 x 64 46.5 and 112; gated 32 x 8192 x 4096 29.5 and
-// 25.5, 256: 30.8 and 35.6; dx 256 x 8192 x 4096 40.7 and 24.2, 1024: 43.0 and 57.3; dw of 16384 rows, 1024 x 1024: 74.2
-// and 35.9, of 1024 rows, 2048 x 2048: 12.1 and 16.1.
+//                        than 3.2, the epilogue's (0.7 of it for a round of halves); and no less than 7 + bytes / 6 TB/s;
+//   this one             2 + for each time the blocks go round the 304 places 3, 0.04 a row of the tile and 0.41 a stage
+//                        of 32 KB; and no less than 6 + bytes / 6 TB/s.
+// Pairs and this kernel as measured, M x N x K: linear 1 x 4096 x 4096 23.9 and 10.0, 256: 20.0 and 17.3, 512: 20.5 and
+// 21.4, 1024: 26.0 and 36.2; 256 x 2048 x 2048 12.5 and 13.4; 300 x 1000 x 1000 10.7 and 11.4; 1024 x 1024 x 8192 32.1 and
+// 23.3; 777 x 5008 x 2048 22.7 and 20.2, with bias, GELU and residual 27.6 and 27.9; 8192 x 8192 x 64 46.5 and 112; gated
+// 32 x 8192 x 4096 29.5 and 25.5, 128: 29.5 and 28.9, 256: 30.8 and 35.6; dx 512 x 4096 x 4096 19.9 and 20.6; dw of 16384
+// rows, 1024 x 1024: 57.1 and 36.0, of 4096 rows: 18.5 and 16.3, of 1024 rows: 8.5 and 10.8.
 double dense_pairs_us(const DenseArgs &a, const DenseArgs *b) {
     auto tiles = [](const DenseArgs &q) {
         return ceil(q.M / 256.) * ceil(q.N * (q.kind == DENSE_GATED ? 2. : 1.) / 256) * (q.kind == DENSE_DW ? q.count : 1);
     };
     auto time = [](const DenseArgs &q) { return fmax(0.29 * ceil(q.K / 64.) * (q.kind == DENSE_DX ? q.count : 1), 3.2); };
-    return fmax(5 + rounds(time(a), tiles(a), b ? time(*b) : 0, b ? tiles(*b) : 0, 76), 7 + memory_us(a) + (b ? memory_us(*b) : 0));
+    return fmax(5 + rounds(time(a), tiles(a), b ? time(*b) : 0, b ? tiles(*b) : 0, 76, 0.7),
+                7 + memory_us(a) + (b ? memory_us(*b) : 0));
 }
 double dense_split_us(const DenseArgs &a, const DenseArgs *b) {
     const Job j0 = make_job(a), j1 = b ? make_job(*b) : Job{};
     if (j0.tiles + j1.tiles > 1000000) return 1e30;
     const double s = choose_split(j0, b ? &j1 : nullptr);
-    auto time = [&](const Job &j) { return 6 + 0.41 / 32768 * (P_BYTES + j.rows * TK * 2) * ceil(stages_of(j) / s); };
-    return fmax(2 + rounds(time(j0), j0.tiles * s, b ? time(j1) : 0, j1.tiles * s, PLACES), 6 + memory_us(a) + (b ? memory_us(*b) : 0));
+    auto time = [&](const Job &j) { return 3 + 0.04 * j.rows + 0.41 / 32768 * (P_BYTES + j.rows * TK * 2) * ceil(stages_of(j) / s); };
+    return fmax(2 + rounds(time(j0), j0.tiles * s, b ? time(j1) : 0, j1.tiles * s, PLACES, 1),
+                6 + memory_us(a) + (b ? memory_us(*b) : 0));
 }
 
 cudaError_t launch_dense_split(const DenseArgs &a, const DenseArgs *b, cudaStream_t st) {

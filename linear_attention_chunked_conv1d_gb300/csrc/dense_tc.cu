@@ -18,7 +18,8 @@
 //    128 columns of each weight (one from each block), so that gate and up stand side by side in the accumulator;
 //  - warps 2-9 turn the other accumulator into the result meanwhile, 32 rows x 64 columns at a time, laid out in
 //    shared memory so that whole 128-byte lines go to memory.
-// Tiles are walked in bands of eight rows of tiles. DX and DW of one backward pass are one launch, the tiles with
+// Tiles are walked in bands of eight rows of tiles; those of a round that would leave half the pairs without any are cut
+// in halves of 128 columns (512 x 4096 x 4096: 24.5 -> 20.5 us, 1024 x 2048 x 2048: 15.9 -> 13.0). DX and DW of one backward pass are one launch, the tiles with
 // the longer sums first: two launches would each leave SMs idle in their last round.
 // Every wait is bounded; on a timeout the blocks raise LA_DEV_TIMEOUT, stop issuing, let what is under way end,
 // free TMEM and return. Ragged edges come from TMA's zero fill; stores are guarded.
@@ -60,11 +61,32 @@ using bf16 = __nv_bfloat16;
 
 // Tile `t` of an output of mt x nt tiles: bands of BAND tiles of rows, column by column, so that the tiles
 // under way at one time share few rows and columns and find them in L2.
-__device__ __forceinline__ void tile_place(int64_t t, int64_t mt, int64_t nt, int &m, int &n) {
+__device__ __forceinline__ void place_in_bands(int64_t t, int64_t mt, int64_t nt, int &m, int &n) {
     const int64_t band = t / (BAND * nt), r = t - band * BAND * nt;
     const int64_t high = mt - band * BAND < BAND ? mt - band * BAND : BAND;
     n = (int)(r / high);
     m = (int)(band * BAND + (r - n * high));
+}
+
+// What a pair works on at one time: a tile, or, of those from tile number `whole` on, half of its columns.
+struct Unit {
+    bool second;     // of the launch's second product
+    int o, m, n;     // output (DW), place of the tile
+    bool cut;        // half a tile:
+    int half;        // the first or the second
+};
+__device__ __forceinline__ Unit unit_at(int64_t u, int64_t whole, const Job &job0, const Job &job1) {
+    Unit q;
+    q.cut = u >= whole;
+    q.half = q.cut ? (int)((u - whole) & 1) : 0;
+    int64_t t = q.cut ? whole + ((u - whole) >> 1) : u;
+    q.second = t >= job0.tiles;
+    if (q.second) t -= job0.tiles;
+    const Job &job = q.second ? job1 : job0;
+    const int64_t per = job.mt * job.nt;
+    q.o = (int)(t / per);
+    place_in_bands(t - q.o * per, job.mt, job.nt, q.m, q.n);
+    return q;
 }
 
 // A warp's 32 x 64 values on their way to or from memory: row r's 16-byte piece j lies at place j ^ (r % 8) of its
@@ -151,7 +173,7 @@ template <int KIND>
 __global__ void __launch_bounds__(THREADS, 1)
 dense_kernel(const __grid_constant__ Maps maps0, const __grid_constant__ Maps maps1, const __grid_constant__ Epilogue ep0,
              const __grid_constant__ Epilogue ep1, const __grid_constant__ Job job0, const __grid_constant__ Job job1,
-             int *status, uint64_t wait_ns, int debug_stall) {
+             int64_t whole, int64_t units, int *status, uint64_t wait_ns, int debug_stall) {
     constexpr int OUT_N = KIND == GATED ? TN / 2 : TN;  // columns of the result a tile holds
     extern __shared__ unsigned char smem_raw[];
     unsigned char *sm = reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -188,27 +210,23 @@ dense_kernel(const __grid_constant__ Maps maps0, const __grid_constant__ Maps ma
     tc::fence_after_sync();
     wait_for_previous();
     const uint32_t tm = *tmem_sh;
-    const int64_t ntiles = job0.tiles + (KIND == BACKWARD ? job1.tiles : 0);
     const int64_t first = blockIdx.x / 2, step = gridDim.x / 2;
-    // Every round of tiles but the first goes to the pairs from the last to the first: where the first pairs had the longer
-    // sums, the last ones have an incomplete round's.
-    auto later_tile = [&](int64_t round) { return round * step + (step - 1 - first); };
+    // Every round but the first goes to the pairs from the last to the first: where the first pairs had the longer sums,
+    // the last ones have an incomplete round's.
+    auto later = [&](int64_t round) { return round * step + (step - 1 - first); };
     const uint32_t sbase = tc::smem_u32(sm);
 
     if (warp == 0) {
         if (tc::elect_one()) {
             uint32_t s = 0, ph = 0, used = 0;
-            for (int64_t tile = first, round = 0; tile < ntiles && !*err; tile = later_tile(++round)) {
-                const bool second = KIND == BACKWARD && tile >= job0.tiles;
-                const Job &job = second ? job1 : job0;
-                const Maps &maps = second ? maps1 : maps0;
-                const int64_t t = second ? tile - job0.tiles : tile, per = job.mt * job.nt;
-                const int o = (int)(t / per);
-                int m, n;
-                tile_place(t - o * per, job.mt, job.nt, m, n);
-                const int m0 = m * TM + (int)rank * 128;
-                const int n0 = KIND == GATED ? n * OUT_N : n * TN + (int)rank * 128;
-                const CUtensorMap *ma = &maps.a[KIND == BACKWARD && job.dw ? o : 0], *mb = &maps.b[KIND == GATED ? rank : 0];
+            for (int64_t u = first, round = 0; u < units && !*err; u = later(++round)) {
+                const Unit unit = unit_at(u, whole, job0, job1);
+                const Job &job = KIND == BACKWARD && unit.second ? job1 : job0;
+                const Maps &maps = KIND == BACKWARD && unit.second ? maps1 : maps0;
+                const int m0 = unit.m * TM + (int)rank * 128, share = unit.cut ? 64 : 128;  // rows of B in a block
+                const int n0 = unit.n * OUT_N + unit.half * (OUT_N / 2) + (KIND == GATED ? 0 : (int)rank * share);
+                const uint32_t bytes = 2 * (HALF_BYTES + share * TK * 2);
+                const CUtensorMap *ma = &maps.a[KIND == BACKWARD && job.dw ? unit.o : 0], *mb = &maps.b[KIND == GATED ? rank : 0];
                 const int kp = (job.K + TK - 1) / TK;
                 for (int p = 0; p < job.parts && !*err; ++p) {
                     if (KIND == BACKWARD && p) {
@@ -223,19 +241,15 @@ dense_kernel(const __grid_constant__ Maps maps0, const __grid_constant__ Maps ma
                         }
                         const uint32_t da = sbase + s * STAGE_BYTES, db = da + HALF_BYTES;
                         const uint32_t bar = tc::map_to_rank(tc::smem_u32(full + s), 0);
-                        if (rank == 0) tc::mbar_expect_tx(full + s, 2 * STAGE_BYTES);
+                        if (rank == 0) tc::mbar_expect_tx(full + s, bytes);
                         if (KIND == BACKWARD && job.dw) {
                             tc::tma_load_2d_pair(da, ma, m0, k0, bar);
                             tc::tma_load_2d_pair(da + HALF_BYTES / 2, ma, m0 + 64, k0, bar);
                         } else {
                             tc::tma_load_2d_pair(da, ma, k0, m0, bar);
                         }
-                        if (KIND == BACKWARD) {
-                            tc::tma_load_2d_pair(db, mb, n0, k0, bar);
-                            tc::tma_load_2d_pair(db + HALF_BYTES / 2, mb, n0 + 64, k0, bar);
-                        } else {
-                            tc::tma_load_2d_pair(db, mb, k0, n0, bar);
-                        }
+                        for (int i = 0; i < share; i += 64)
+                            tc::tma_load_2d_pair(db + i * TK * 2, mb, KIND == BACKWARD ? n0 + i : k0, KIND == BACKWARD ? k0 : n0 + i, bar);
                         used |= 1u << s;
                         if (++s == STAGES) s = 0, ph ^= 1u;
                     }
@@ -256,12 +270,12 @@ dense_kernel(const __grid_constant__ Maps maps0, const __grid_constant__ Maps ma
         if (rank == 0 && tc::elect_one()) {
             uint32_t s = 0, ph = 0, tcnt = 0;
             if (debug_stall && !tc::mbar_wait(fin, 0, wait_ns, SLEEP_NS)) *err = 1;
-            for (int64_t tile = first; tile < ntiles && !*err; tile = later_tile(++tcnt)) {
-                const bool second = KIND == BACKWARD && tile >= job0.tiles;
-                const Job &job = second ? job1 : job0;
+            for (int64_t u = first; u < units && !*err; u = later(++tcnt)) {
+                const Unit unit = unit_at(u, whole, job0, job1);
+                const Job &job = KIND == BACKWARD && unit.second ? job1 : job0;
                 const bool a_mn = KIND == BACKWARD && job.dw;
                 constexpr bool b_mn = KIND == BACKWARD;
-                const uint32_t id = tc::idesc(TM, TN, tc::FMT_BF16, a_mn, b_mn);
+                const uint32_t id = tc::idesc(TM, unit.cut ? TN / 2 : TN, tc::FMT_BF16, a_mn, b_mn);
                 const int64_t kb = (int64_t)((job.K + TK - 1) / TK) * job.parts;
                 const uint32_t acc = tcnt & 1u, aph = (tcnt >> 1) & 1u;
                 if (!tc::mbar_wait(acce + acc, aph ^ 1u, wait_ns, SLEEP_NS)) {
@@ -298,22 +312,19 @@ dense_kernel(const __grid_constant__ Maps maps0, const __grid_constant__ Maps ma
         }
     } else {
         const uint32_t q = warp & 3;
-        constexpr int COLS = OUT_N / (EPI_WARPS / 4);  // columns of a warp: 128, GATED 64
-        const int c_first = (warp - 2) / 4 * COLS;
         uint4 *buf = reinterpret_cast<uint4 *>(sm + OFF_OUT) + (warp - 2) * 256;
         uint32_t tcnt = 0;
-        for (int64_t tile = first; tile < ntiles; tile = later_tile(++tcnt)) {
+        for (int64_t u = first; u < units; u = later(++tcnt)) {
             // every decision to stop is made per warp: the TMEM loads below are warp-collective
             if (__any_sync(0xffffffffu, *err != 0)) break;
-            const bool second = KIND == BACKWARD && tile >= job0.tiles;
-            const Job &job = second ? job1 : job0;
-            const Epilogue &ep = second ? ep1 : ep0;
-            const int64_t t = second ? tile - job0.tiles : tile, per = job.mt * job.nt;
-            const int o = (int)(t / per);
-            int m, n;
-            tile_place(t - o * per, job.mt, job.nt, m, n);
-            const int M = job.M, N = job.N, n0 = n * OUT_N + c_first;
-            const int64_t row0 = (int64_t)m * TM + rank * 128 + 32 * q;
+            const Unit unit = unit_at(u, whole, job0, job1);
+            const Job &job = KIND == BACKWARD && unit.second ? job1 : job0;
+            const Epilogue &ep = KIND == BACKWARD && unit.second ? ep1 : ep0;
+            // A warp has 128 columns of a tile (half a tile, GATED: 64); of half a GATED tile the first four warps have all.
+            const int wide = unit.cut ? OUT_N / 2 : OUT_N, cols = wide / 2 < 64 ? (warp < 6 ? 64 : 0) : wide / 2;
+            const int c_first = (warp - 2) / 4 * (wide / 2), up_at = unit.cut ? TN / 4 : TN / 2;
+            const int M = job.M, N = job.N, o = unit.o, n0 = unit.n * OUT_N + unit.half * (OUT_N / 2) + c_first;
+            const int64_t row0 = (int64_t)unit.m * TM + rank * 128 + 32 * q;
             uint4 res[8];  // the residual's next 64 columns
             uint2 bias = make_uint2(0u, 0u);  // the bias of columns 4 lane .. 4 lane + 3 of the warp's
             if (KIND == LINEAR && ep.residual) fetch(res, ep.residual, ep.ldr, row0, M, n0, N, lane);
@@ -337,7 +348,7 @@ dense_kernel(const __grid_constant__ Maps maps0, const __grid_constant__ Maps ma
             tc::fence_after_sync();
             const uint32_t src = tc::tmem_addr(tm + acc * TN, 32 * q, c_first);
 #pragma unroll 1
-            for (int c = 0; c < COLS; c += 64) {
+            for (int c = 0; c < cols; c += 64) {
                 const int col = n0 + c;
                 if (KIND == LINEAR) {
                     if (ep.saved) {  // z goes out first, y is made of it in a second look at the accumulator
@@ -355,7 +366,7 @@ dense_kernel(const __grid_constant__ Maps maps0, const __grid_constant__ Maps ma
                     if (ep.residual) {
 #pragma unroll
                         for (int i = 0; i < 8; ++i) piece(buf, i * 4 + (lane >> 3), lane & 7) = res[i];
-                        if (c + 64 < COLS) fetch(res, ep.residual, ep.ldr, row0, M, col + 64, N, lane);
+                        if (c + 64 < cols) fetch(res, ep.residual, ep.ldr, row0, M, col + 64, N, lane);
                         __syncwarp();
                     }
 #pragma unroll 1
@@ -385,8 +396,8 @@ dense_kernel(const __grid_constant__ Maps maps0, const __grid_constant__ Maps ma
 #pragma unroll
                             for (int j = 0; j < 8; j += 4) {
                                 float v[32];
-                                tc::tmem_ld16(src + half * (TN / 2) + j * 8, v);
-                                tc::tmem_ld16(src + half * (TN / 2) + j * 8 + 16, v + 16);
+                                tc::tmem_ld16(src + half * up_at + j * 8, v);
+                                tc::tmem_ld16(src + half * up_at + j * 8 + 16, v + 16);
                                 tc::tmem_wait_ld();
 #pragma unroll
                                 for (int i = 0; i < 4; ++i) {
@@ -402,7 +413,7 @@ dense_kernel(const __grid_constant__ Maps maps0, const __grid_constant__ Maps ma
                     for (int j = 0; j < 8; j += 2) {
                         float v[16], u[16];
                         tc::tmem_ld16(src + j * 8, v);
-                        tc::tmem_ld16(src + TN / 2 + j * 8, u);
+                        tc::tmem_ld16(src + up_at + j * 8, u);
                         tc::tmem_wait_ld();
                         act_values(v, ep.act);
 #pragma unroll
@@ -471,12 +482,14 @@ template <int KIND>
 cudaError_t launch(const DenseArgs &a, const DenseArgs *b, cudaStream_t st) {
     Maps maps[2];
     const bool mn = KIND == BACKWARD;
-    if (!make_maps(&maps[0], a, a.kind == DENSE_DW, mn, 128, 128)) return cudaErrorInvalidValue;
-    if (b && !make_maps(&maps[1], *b, b->kind == DENSE_DW, mn, 128, 128)) return cudaErrorInvalidValue;
+    if (!make_maps(&maps[0], a, a.kind == DENSE_DW, mn, 128, 64)) return cudaErrorInvalidValue;
+    if (b && !make_maps(&maps[1], *b, b->kind == DENSE_DW, mn, 128, 64)) return cudaErrorInvalidValue;
     const Job j0 = make_job(a), j1 = b ? make_job(*b) : Job{};
-    const int64_t tiles = j0.tiles + j1.tiles, pairs = resident_pairs<KIND>();
-    return launch_overlapped(dense_kernel<KIND>, dim3(2 * (int)(tiles < pairs ? tiles : pairs)), dim3(THREADS), SMEM, 2, st, maps[0],
-                             b ? maps[1] : maps[0], make_epilogue(a), make_epilogue(b ? *b : a), j0, j1, a.status,
+    // the tiles of an incomplete round are cut in halves where there are pairs for them
+    const int64_t tiles = j0.tiles + j1.tiles, pairs = resident_pairs<KIND>(), rest = tiles % pairs;
+    const int64_t whole = 2 * rest <= pairs ? tiles - rest : tiles, units = whole + 2 * (tiles - whole);
+    return launch_overlapped(dense_kernel<KIND>, dim3(2 * (int)(units < pairs ? units : pairs)), dim3(THREADS), SMEM, 2, st, maps[0],
+                             b ? maps[1] : maps[0], make_epilogue(a), make_epilogue(b ? *b : a), j0, j1, whole, units, a.status,
                              a.wait_ns ? a.wait_ns : WAIT_NS, a.debug_stall);
 }
 
