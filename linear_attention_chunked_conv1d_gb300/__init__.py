@@ -722,6 +722,9 @@ def w4_matvec(x, q, scales, y=None, *, stream=None):
     return y
 
 
+_BF16, _F32 = torch.bfloat16, torch.float32
+
+
 def _act_code(act) -> int:
     code = LA_ACTIVATIONS.get(act)
     if code is None:
@@ -759,7 +762,7 @@ def layernorm_rows(x, w, b=None, y=None, *, stats=None, eps=1e-5, stream=None):
             and y.dtype is dt and y.get_device() == dev and w.dtype is dt and w.shape == (width,)
             and w.is_contiguous() and w.get_device() == dev
             and (b is None or (b.dtype is dt and b.shape == (width,) and b.is_contiguous() and b.get_device() == dev))
-            and (stats is None or (stats.dtype is torch.float32 and stats.shape == (rows, 2)
+            and (stats is None or (stats.dtype is _F32 and stats.shape == (rows, 2)
                                    and stats.is_contiguous() and stats.get_device() == dev))):
         _on_gpu(x)
         xs, ys = _matrix16("x", x, rows, width, dt, dev), _matrix16("y", y, rows, width, dt, dev)
@@ -769,9 +772,12 @@ def layernorm_rows(x, w, b=None, y=None, *, stats=None, eps=1e-5, stream=None):
             _dense("stats", stats, (rows, 2), torch.float32, dev)
     if rows == 1:  # a single row's stride says nothing
         xs = ys = (width + 7) // 8 * 8
-    _check(_load().la_layernorm_rows(
+    rc = (_lib or _load()).la_layernorm_rows(
         x.data_ptr(), w.data_ptr(), None if b is None else b.data_ptr(), y.data_ptr(),
-        None if stats is None else stats.data_ptr(), rows, width, xs, ys, eps, _dtype_code(x), _stream_on(stream, dev)))
+        None if stats is None else stats.data_ptr(), rows, width, xs, ys, eps, LA_BF16 if dt is _BF16 else _dtype_code(x),
+        _current_stream(dev) if stream is None and _current_stream is not None else _stream(stream))
+    if rc:
+        _check(rc)
     return y
 
 
@@ -795,7 +801,7 @@ def layernorm_rows_backward(x, w, stats, dy, dx, dw, db=None, *, dskip=None, wor
     rows, width = x.shape
     (xs, x1), (ys, y1), (ds, d1) = x.stride(), dy.stride(), dx.stride()
     ss, s1 = (ds, 1) if dskip is None else dskip.stride()
-    f32 = torch.float32
+    f32 = _F32
     # As in gated_scan: one look at everything, and only where something is unusual the checks that say what.
     if not (dev >= 0 and dev == _current_device() and x1 == y1 == d1 == s1 == 1 and dy.dtype is dt and dx.dtype is dt
             and dy.shape == (rows, width) and dx.shape == (rows, width) and dy.get_device() == dev
@@ -816,11 +822,14 @@ def layernorm_rows_backward(x, w, stats, dy, dx, dw, db=None, *, dskip=None, wor
         _room("workspace", workspace, dev)
     if rows == 1:  # a single row's stride says nothing
         xs = ys = ds = ss = (width + 7) // 8 * 8
-    _check(_load().la_layernorm_rows_backward(
+    rc = (_lib or _load()).la_layernorm_rows_backward(
         x.data_ptr(), w.data_ptr(), stats.data_ptr(), dy.data_ptr(), None if dskip is None else dskip.data_ptr(),
-        dx.data_ptr(), dw.data_ptr(), None if db is None else db.data_ptr(), rows, width, xs, ys, ss, ds, _dtype_code(x),
+        dx.data_ptr(), dw.data_ptr(), None if db is None else db.data_ptr(), rows, width, xs, ys, ss, ds, LA_BF16 if dt is _BF16 else _dtype_code(x),
         None if workspace is None else workspace.data_ptr(),
-        0 if workspace is None else workspace.numel() * workspace.element_size(), _stream_on(stream, dev)))
+        0 if workspace is None else workspace.numel() * workspace.element_size(),
+        _current_stream(dev) if stream is None and _current_stream is not None else _stream(stream))
+    if rc:
+        _check(rc)
 
 
 def linear_saved_bytes(rows, outputs, act="none") -> int:
@@ -834,7 +843,7 @@ def linear(x, w, y=None, *, bias=None, residual=None, act="none", saved=None, st
     x [M][K], w [N][K] (a linear layer's [out][in] weight), bias [N], residual and y [M][N] (y may be
     residual, and defaults to a new tensor); any sizes, rows on 16 bytes. act: one of LA_ACTIVATIONS.
     saved: a buffer of linear_saved_bytes(...) when linear_backward is to follow. Returns y."""
-    dev, bf16 = x.get_device(), torch.bfloat16
+    dev, bf16 = x.get_device(), _BF16
     M, K = x.shape
     N = w.shape[0]
     if y is None:
@@ -862,11 +871,16 @@ def linear(x, w, y=None, *, bias=None, residual=None, act="none", saved=None, st
     if N == 1:
         ws = (K + 7) // 8 * 8
     code = LA_ACTIVATIONS.get(act)
-    _check(_load().la_linear(
+    if code is None:
+        _act_code(act)  # says what there is
+    rc = (_lib or _load()).la_linear(
         x.data_ptr(), w.data_ptr(), None if bias is None else bias.data_ptr(),
         None if residual is None else residual.data_ptr(), y.data_ptr(), None if saved is None else saved.data_ptr(),
         0 if saved is None else saved.numel() * saved.element_size(), M, N, K, xs, ws, rs, ys,
-        _act_code(act) if code is None else code, _stream_on(stream, dev)))
+        code,
+        _current_stream(dev) if stream is None and _current_stream is not None else _stream(stream))
+    if rc:
+        _check(rc)
     return y
 
 
@@ -880,7 +894,7 @@ def linear_backward(x, w, saved, dy, dx=None, dw=None, *, dbias=None, act="none"
     """Gradients of linear: dx [M][K], dw [N][K] and dbias [N] (bf16; those that are given) from dy
     [M][N]; the residual's is dy itself. x, w, saved (None without an activation) and act are those of
     the forward call."""
-    dev, bf16 = x.get_device(), torch.bfloat16
+    dev, bf16 = x.get_device(), _BF16
     M, K = x.shape
     N = w.shape[0]
     (xs, x1), (ws, w1), (ys, y1) = x.stride(), w.stride(), dy.stride()
@@ -909,12 +923,18 @@ def linear_backward(x, w, saved, dy, dx=None, dw=None, *, dbias=None, act="none"
         ys = (N + 7) // 8 * 8
     if N == 1:
         ws = gs = (K + 7) // 8 * 8
-    _check(_load().la_linear_backward(
+    code = LA_ACTIVATIONS.get(act)
+    if code is None:
+        _act_code(act)  # says what there is
+    rc = (_lib or _load()).la_linear_backward(
         x.data_ptr(), w.data_ptr(), None if saved is None else saved.data_ptr(),
         0 if saved is None else saved.numel() * saved.element_size(), dy.data_ptr(), None if dx is None else dx.data_ptr(),
         None if dw is None else dw.data_ptr(), None if dbias is None else dbias.data_ptr(), M, N, K, xs, ws, ys, ds, gs,
-        _act_code(act), None if workspace is None else workspace.data_ptr(),
-        0 if workspace is None else workspace.numel() * workspace.element_size(), _stream_on(stream, dev)))
+        code, None if workspace is None else workspace.data_ptr(),
+        0 if workspace is None else workspace.numel() * workspace.element_size(),
+        _current_stream(dev) if stream is None and _current_stream is not None else _stream(stream))
+    if rc:
+        _check(rc)
 
 
 def gated_ffn_saved_bytes(rows, hidden) -> int:
@@ -929,7 +949,7 @@ def gated_ffn(x, w_gate, w_up, h=None, *, act="silu", saved=None, stream=None):
     tensor by default): bf16, any sizes, rows on 16 bytes. act: one of LA_ACTIVATIONS. saved: a buffer
     of gated_ffn_saved_bytes(...) when gated_ffn_backward is to follow. The projection back is
     linear(h, w_down, residual=...). Returns h."""
-    dev, bf16 = x.get_device(), torch.bfloat16
+    dev, bf16 = x.get_device(), _BF16
     M, K = x.shape
     F = w_gate.shape[0]
     if h is None:
@@ -950,10 +970,15 @@ def gated_ffn(x, w_gate, w_up, h=None, *, act="silu", saved=None, stream=None):
     if F == 1:
         gs = us = (K + 7) // 8 * 8
     code = LA_ACTIVATIONS.get(act)
-    _check(_load().la_gated_ffn(
+    if code is None:
+        _act_code(act)  # says what there is
+    rc = (_lib or _load()).la_gated_ffn(
         x.data_ptr(), w_gate.data_ptr(), w_up.data_ptr(), h.data_ptr(), None if saved is None else saved.data_ptr(),
         0 if saved is None else saved.numel() * saved.element_size(), M, F, K, xs, gs, us, hs,
-        _act_code(act) if code is None else code, _stream_on(stream, dev)))
+        code,
+        _current_stream(dev) if stream is None and _current_stream is not None else _stream(stream))
+    if rc:
+        _check(rc)
     return h
 
 
@@ -966,7 +991,7 @@ def gated_ffn_backward(x, w_gate, w_up, saved, dh, dx=None, dw_gate=None, dw_up=
                        workspace=None, stream=None) -> None:
     """Gradients of gated_ffn: dx [M][K] and/or dw_gate and dw_up [F][K] (bf16) from dh [M][F]. x, the
     weights, saved and act are those of the forward call."""
-    dev, bf16 = x.get_device(), torch.bfloat16
+    dev, bf16 = x.get_device(), _BF16
     M, K = x.shape
     F = w_gate.shape[0]
     (xs, x1), (gs, g1), (us, u1), (hs, h1) = x.stride(), w_gate.stride(), w_up.stride(), dh.stride()
@@ -996,9 +1021,15 @@ def gated_ffn_backward(x, w_gate, w_up, saved, dh, dx=None, dw_gate=None, dw_up=
         hs = (F + 7) // 8 * 8
     if F == 1:
         gs = us = dgs = dus = (K + 7) // 8 * 8
-    _check(_load().la_gated_ffn_backward(
+    code = LA_ACTIVATIONS.get(act)
+    if code is None:
+        _act_code(act)  # says what there is
+    rc = (_lib or _load()).la_gated_ffn_backward(
         x.data_ptr(), w_gate.data_ptr(), w_up.data_ptr(), None if saved is None else saved.data_ptr(),
         0 if saved is None else saved.numel() * saved.element_size(), dh.data_ptr(), None if dx is None else dx.data_ptr(),
         None if dw_gate is None else dw_gate.data_ptr(), None if dw_up is None else dw_up.data_ptr(), M, F, K, xs, gs, us, hs,
         ds, dgs, dus, _act_code(act), None if workspace is None else workspace.data_ptr(),
-        0 if workspace is None else workspace.numel() * workspace.element_size(), _stream_on(stream, dev)))
+        0 if workspace is None else workspace.numel() * workspace.element_size(),
+        _current_stream(dev) if stream is None and _current_stream is not None else _stream(stream))
+    if rc:
+        _check(rc)

@@ -21,21 +21,22 @@ namespace la {
 
 namespace {
 
-// The pieces of a thread, TPR apart. Where whole pieces make up the row the loads need no branches, and all of
-// them are under way at one time.
+// The pieces of a thread, TPR apart. Whole pieces are loaded without branches, so that all of them are under way at
+// one time; then the one that a row may end in.
 template <class T, int TPR, int P>
 __device__ __forceinline__ void load_row(uint4 (&raw)[P], const T *row, int t, int width) {
     constexpr int N = kPiece<T>;
-    if (width % N == 0) {
 #pragma unroll
-        for (int i = 0; i < P; ++i) {
-            const int c = (t + i * TPR) * N;
-            raw[i] = make_uint4(0u, 0u, 0u, 0u);
-            if (c < width) raw[i] = *reinterpret_cast<const uint4 *>(row + c);
-        }
-    } else {
+    for (int i = 0; i < P; ++i) {
+        const int c = (t + i * TPR) * N;
+        raw[i] = make_uint4(0u, 0u, 0u, 0u);
+        if (c + N <= width) raw[i] = *reinterpret_cast<const uint4 *>(row + c);
+    }
+    if (width % N == 0) return;
 #pragma unroll
-        for (int i = 0; i < P; ++i) raw[i] = load_raw(row, (t + i * TPR) * N, width);
+    for (int i = 0; i < P; ++i) {
+        const int c = (t + i * TPR) * N;
+        if (c < width && c + N > width) raw[i] = load_raw(row, c, width);
     }
 }
 // The values of 16 bytes in fp32, as packed pairs (the arithmetic below is on pairs: half the instructions, of
