@@ -477,10 +477,13 @@ int la_w4_quantize(const void *w, void *q, void *scales, int N, int K, int group
  * ("split_prefill.rs", prefill_phase1_proj_batched); the pages have none of them.
  *
  * Shared by these calls: a matrix has dense rows at a stride that is a multiple of 16 bytes and starts on
- * 16 bytes; any number of columns is fine, and what lies between a row's end and the next row is neither
+ * 16 bytes, and so do vectors and buffers; any number of columns is fine, and what lies between a row's end and the next row is neither
  * read nor written. An output may overlap no input and no other output, where nothing else is said;
  * columns of its own in a buffer that it shares with them (rows at the same stride) are fine. Every
- * result is summed in a fixed order: the same call on the same inputs gives the same bits. Infinities
+ * result is summed in an order that depends on the sizes alone: the same call on the same inputs gives the
+ * same bits (a row may differ in its last place from one batch size to another). A workspace is used by its
+ * call alone until its work is done; calls in stream order may share one, calls (and captured graphs) that
+ * may overlap on the GPU need one each, and so for saved buffers. None need be initialised. Infinities
  * and NaN go where the formulas take them, in the rows (for weights' gradients: columns) they stand in.
  * Counts are at least 1 and at most 2^31 - 1024 (LA_ERR_COUNT).
  * ------------------------------------------------------------------------------------------- */
@@ -501,8 +504,7 @@ int la_layernorm_rows(const void *x, const void *w, const void *b, void *y, floa
  * dy, dx  [rows][lddy], [rows][lddx] (dtype). dx may be dy or dskip itself, at the same stride.
  * dskip   [rows][ldskip] (dtype), a gradient that reaches x past the norm, or NULL.
  * dw, db  fp32 [width] (16-byte aligned); db may be NULL.
- * workspace  la_layernorm_rows_backward_workspace_bytes(...) bytes (16-byte aligned), used by this call
- *         alone until its work is done; calls in stream order may share one. */
+ * workspace  la_layernorm_rows_backward_workspace_bytes(...) bytes (16-byte aligned). */
 size_t la_layernorm_rows_backward_workspace_bytes(int rows, int width, int dtype);
 int la_layernorm_rows_backward(const void *x, const void *w, const float *stats, const void *dy,
                                const void *dskip, void *dx, float *dw, float *db, int rows, int width,

@@ -255,15 +255,15 @@ dense_kernel(const __grid_constant__ Maps maps0, const __grid_constant__ Maps ma
                     }
                 }
             }
-            // Every copy has landed before the blocks exit: the leader waits for the last one of each stage, its
-            // own and the other block's. Where something went wrong the two may have stopped at different
-            // stages; a copy takes microseconds, so each then gives its last ones a millisecond.
+            // Before the blocks exit, each waits until the MMAs have read its last copies: they have landed then, and the
+            // leader's arrivals have reached the other block's barriers. Where something went wrong the two may have
+            // stopped at different stages; a copy takes microseconds, so each then gives its last ones a millisecond.
             if (*err) {
                 const uint64_t t0 = tc::globaltimer_ns();
                 while (tc::globaltimer_ns() - t0 < 1000000u) __nanosleep(1000);
-            } else if (rank == 0) {
+            } else {
                 for (uint32_t i = 0; i < STAGES; ++i)  // stages before s were last filled in phase ph, the others in the one before
-                    if ((used >> i & 1u) && !tc::mbar_wait(full + i, i < s ? ph : ph ^ 1u, WAIT_NS, SLEEP_NS)) *err = 1;
+                    if ((used >> i & 1u) && !tc::mbar_wait(empty + i, i < s ? ph : ph ^ 1u, wait_ns, SLEEP_NS)) *err = 1;
             }
         }
     } else if (warp == 1) {

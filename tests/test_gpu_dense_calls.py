@@ -81,6 +81,90 @@ def test_shared_buffers(cuda):
         assert la.linear(xs, wd, res, residual=res, act="silu") is res and torch.equal(res, want)
 
 
+@pytest.mark.parametrize("m,n,k,act", [(700, 520, 264, "gelu"), (5, 520, 264, "none"), (70, 40, 1000, "silu"), (3000, 1100, 264, "none")])
+def test_gradients_that_are_asked_for(cuda, m, n, k, act):
+    """Any of dx, dw and dbias alone, or two of them, as all three together."""
+    c = case(cuda, m, n, k, 21)
+    saved = room(la.linear_saved_bytes(m, n, act), cuda) if act != "none" else None
+    ws = room(la.linear_backward_workspace_bytes(m, n, k, act), cuda)
+    la.linear(c["x"], c["w"], bias=c["bias"], act=act, saved=saved)
+    la.linear_backward(c["x"], c["w"], saved, c["dy"], c["dx"], c["dw"], dbias=c["dbias"], act=act, workspace=ws)
+    want = [c[q].double() for q in ("dx", "dw", "dbias")]
+    for which in range(1, 7):
+        got = [torch.full_like(c[q], 7.0, memory_format=torch.preserve_format) if which >> i & 1 else None for i, q in enumerate(("dx", "dw", "dbias"))]
+        la.linear_backward(c["x"], c["w"], saved, c["dy"], got[0], got[1], dbias=got[2], act=act, workspace=ws)
+        for g, w in zip(got, want):
+            # one launch or two may split a sum differently: last places of fp32 sums, then one rounding
+            assert g is None or float((g.double() - w).norm()) <= 2 * U * float(w.norm())
+    f = gated_case(cuda, m, n, k, 22)
+    saved, ws = room(la.gated_ffn_saved_bytes(m, n), cuda), room(la.gated_ffn_backward_workspace_bytes(m, n, k), cuda)
+    la.gated_ffn(f["x"], f["w"], f["w_up"], saved=saved)
+    la.gated_ffn_backward(f["x"], f["w"], f["w_up"], saved, f["dy"], f["dx"], f["dw"], f["dw_up"], workspace=ws)
+    want = [f[q].double() for q in ("dx", "dw", "dw_up")]
+    for q in ("dx", "dw", "dw_up"):
+        f[q].fill_(7.0)
+    la.gated_ffn_backward(f["x"], f["w"], f["w_up"], saved, f["dy"], f["dx"], workspace=ws)
+    la.gated_ffn_backward(f["x"], f["w"], f["w_up"], saved, f["dy"], None, f["dw"], f["dw_up"], workspace=ws)
+    for q, w in zip(("dx", "dw", "dw_up"), want):
+        assert float((f[q].double() - w).norm()) <= 2 * U * float(w.norm())
+
+
+def test_one_row_one_column_and_one_of_each(cuda):
+    """A single row goes with any stride, its own width's among them, and so does a weight of one output."""
+    g = torch.Generator().manual_seed(23)
+    x = torch.randn(1, 77, generator=g).to(BF16).to(cuda)
+    w = torch.randn(30, 80, generator=g).to(BF16).to(cuda)[:, :77]
+    y = torch.empty(1, 30, dtype=BF16, device=cuda)
+    ref = x.double() @ w.double().T
+    bound = U * ref.abs() + 64 * F32 * (x.double().abs() @ w.double().abs().T)
+    close(la.linear(x, w, y), ref, bound, "y")
+    one = torch.randn(1, 77, generator=g).to(BF16).to(cuda)
+    out = torch.empty(1, 1, dtype=BF16, device=cuda)
+    ref = x.double() @ one.double().T
+    close(la.linear(x, one, out), ref, U * ref.abs() + 64 * F32 * (x.double().abs() @ one.double().abs().T), "1 x 1")
+    dx, dw = torch.empty_like(x), torch.empty_like(one)
+    dy = torch.ones(1, 1, dtype=BF16, device=cuda)
+    la.linear_backward(x, one, None, dy, dx, dw, workspace=room(la.linear_backward_workspace_bytes(1, 1, 77), cuda))
+    assert torch.equal(dx, one) and torch.equal(dw, x)
+    h = la.gated_ffn(x, one, one)
+    a = ref * torch.sigmoid(ref) * ref
+    close(h, a, U * a.abs() + 1e-4 * a.abs().clamp(min=1e-3), "h")  # 64 2^-24 of sums of 77 terms, three times over: 1e-5 of them
+    st = torch.empty(1, 2, device=cuda)
+    assert la.layernorm_rows(x, torch.ones(77, dtype=BF16, device=cuda), stats=st).shape == (1, 77)
+
+
+def test_first_calls_of_a_process_inside_a_capture(cuda):
+    """Nothing is set up by a first call that a capture would not allow."""
+    import subprocess
+    import sys
+    code = """
+import torch
+import linear_attention_chunked_conv1d_gb300 as la
+b = torch.bfloat16
+x, w, u = (torch.randn(2000, 512, device="cuda").to(b) for _ in range(3))
+n, o, s, h, dx = torch.ones(512, device="cuda").to(b), torch.empty_like(x), torch.empty(2000, 2000, device="cuda", dtype=b), torch.empty(2000, 2000, device="cuda", dtype=b), torch.empty_like(x)
+few, ws = torch.empty(3, 2000, device="cuda", dtype=b), torch.empty(la.linear_backward_workspace_bytes(2000, 2000, 512), device="cuda", dtype=torch.uint8)
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    la.layernorm_rows(x, n, y=o)
+    la.linear(o, w, s)
+    la.gated_ffn(o, w, u, h)
+    la.linear(o[:3], w, few)
+    la.linear_backward(o, w, None, h, dx, workspace=ws)
+for t in (o, s, h, few, dx):
+    t.zero_()
+g.replay()
+torch.cuda.synchronize()
+got = [t.clone() for t in (o, s, h, few, dx)]
+la.layernorm_rows(x, n, y=o), la.linear(o, w, s), la.gated_ffn(o, w, u, h), la.linear(o[:3], w, few), la.linear_backward(o, w, None, h, dx, workspace=ws)
+assert la.device_status() == 0 and all(torch.equal(p, q) for p, q in zip(got, (o, s, h, few, dx)))
+print("captured")
+"""
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "captured" in r.stdout, r.stderr[-2000:]
+
+
 def test_same_bits_each_time(cuda):
     """Sums are taken in a fixed order: every call, in whatever company, gives the same bits."""
     c, d = gated_case(cuda, 2000, 700, 520, 3), case(cuda, 40, 500, 2000, 4)
