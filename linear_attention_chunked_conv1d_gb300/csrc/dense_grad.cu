@@ -9,6 +9,7 @@
 #include "dense.cuh"
 #include "launch.h"
 #include "overlap.cuh"
+#include "tc.cuh"
 
 namespace la {
 
@@ -17,12 +18,12 @@ namespace {
 using bf16 = __nv_bfloat16;
 constexpr int COLS = 256, WARPS = 8, ROWS = 2;  // a block: 32 lanes of 8 columns, eight warps of a row at a time, twice
 
-// dz may be null (act none: dz is dy); partial [gridDim.y][N] (or null): the sums of the block's rows; where there
-// is one block to a column, its sums are the gradient.
+// dz may be null (act none: dz is dy). The sums of a block's rows go to partial [gridDim.y][N]; where the blocks of the
+// same columns are one cluster (along y) or one block, they add them up, each of some columns, to dbias.
 __global__ void __launch_bounds__(32 * WARPS, 4)
 linear_grad_kernel(const bf16 *__restrict__ saved, const bf16 *__restrict__ dy, bf16 *__restrict__ dz,
-                   float *__restrict__ partial, bf16 *__restrict__ dbias, int M, int N, int64_t lds, int64_t lddy, int64_t ldz, int act) {
-    __shared__ float sh[WARPS][COLS];
+                   float *__restrict__ partial, bf16 *__restrict__ dbias, int M, int N, int64_t lds, int64_t lddy, int64_t ldz, int act, int cluster) {
+    __shared__ float sh[WARPS][COLS], mine[COLS];
     wait_for_previous();
     const int c = blockIdx.x * COLS + threadIdx.x * 8;
     float sum[8] = {};
@@ -62,8 +63,22 @@ linear_grad_kernel(const bf16 *__restrict__ saved, const bf16 *__restrict__ dy, 
 #pragma unroll
     for (int w = 0; w < WARPS; ++w) s += sh[w][k];
     const int at = blockIdx.x * COLS + k;
-    if (at < N && gridDim.y == 1) dbias[at] = __float2bfloat16_rn(s);
-    else if (at < N) partial[(int64_t)blockIdx.y * N + at] = s;
+    if (gridDim.y > 1 && cluster == 1) {
+        if (at < N) partial[(int64_t)blockIdx.y * N + at] = s;
+        return;
+    }
+    if (cluster > 1) {
+        mine[k] = s;
+        tc::cluster_sync();
+        if (k % cluster == (int)tc::cluster_rank()) {
+            s = 0.f;
+            for (int i = 0; i < cluster; ++i) s += tc::ld_shared_cluster(tc::map_to_rank(tc::smem_u32(mine + k), i));
+            if (at < N) dbias[at] = __float2bfloat16_rn(s);
+        }
+        tc::cluster_sync();  // the others have read this block's
+    } else if (at < N) {
+        dbias[at] = __float2bfloat16_rn(s);
+    }
 }
 
 __global__ void __launch_bounds__(32 * 16)
@@ -111,13 +126,11 @@ gated_grad_kernel(const uint8_t *__restrict__ saved, const bf16 *__restrict__ dh
     }
 }
 
-// Rows are shared out so that the grid has `held` blocks for each SM; a few rows stay in one block (a second launch,
-// for the blocks' sums, takes as long as eight rows a warp).
+// Rows are shared out so that the grid has `held` blocks for each SM, or 64 rows a block where that is fewer.
 int row_runs(int M, int N, int held) {
-    if (M <= 8 * WARPS) return 1;
-    const int cols = (N + COLS - 1) / COLS, most = (M + WARPS - 1) / WARPS;
-    int runs = 152 * held / cols;
-    return runs < 1 ? 1 : runs < most ? runs : most;
+    const int cols = (N + COLS - 1) / COLS, most = (int)(((int64_t)M + 8 * WARPS - 1) / (8 * WARPS));
+    const int runs = 152 * held / cols < 1 ? 1 : 152 * held / cols;
+    return runs < most ? runs : most;
 }
 
 }  // namespace
@@ -125,11 +138,12 @@ int row_runs(int M, int N, int held) {
 size_t linear_backward_partial_bytes(int M, int N) { return (size_t)row_runs(M, N, 4) * N * sizeof(float); }
 
 cudaError_t launch_linear_grad(const LinearGradArgs &a, cudaStream_t st) {
-    const int runs = row_runs(a.M, a.N, 4);
-    cudaError_t e = launch_overlapped(linear_grad_kernel, dim3((a.N + COLS - 1) / COLS, runs), dim3(32, WARPS), 0, 0, st,
-                                      (const bf16 *)a.saved, (const bf16 *)a.dy, (bf16 *)a.dz,
-                                      a.partial, (bf16 *)a.dbias, a.M, a.N, a.lds, a.lddy, a.ldz, a.act);
-    if (e != cudaSuccess || !a.dbias || runs == 1) return e;
+    // up to eight blocks to a column are one cluster, which needs no second launch for its sums
+    const int runs = row_runs(a.M, a.N, 4), cluster = a.dbias && runs <= 8 ? runs : 1;
+    cudaError_t e = launch_overlapped(linear_grad_kernel, dim3((a.N + COLS - 1) / COLS, runs), dim3(32, WARPS), 0,
+                                      dim3(cluster > 1 ? 1 : 0, cluster, 1), st, (const bf16 *)a.saved, (const bf16 *)a.dy, (bf16 *)a.dz,
+                                      a.partial, (bf16 *)a.dbias, a.M, a.N, a.lds, a.lddy, a.ldz, a.act, cluster);
+    if (e != cudaSuccess || !a.dbias || runs == cluster) return e;
     return launch_overlapped(bias_sum_kernel, dim3((a.N + 31) / 32), dim3(32, 16), 0, 0, st, (const float *)a.partial, runs,
                              a.N, (bf16 *)a.dbias);
 }

@@ -10,12 +10,14 @@
 // cancels where a row's mean is large). In the backward pass a block takes every gridDim-th row and its
 // threads keep the sums over rows of their own columns in registers; what the blocks have is added up
 // in the blocks' order by a second launch, so the gradients are the same bits in every run.
+#include <atomic>
 #include <cstring>
 #include <type_traits>
 
 #include "dense.cuh"
 #include "launch.h"
 #include "overlap.cuh"
+#include "tc.cuh"
 
 namespace la {
 
@@ -169,13 +171,16 @@ __device__ __forceinline__ void copy_piece(void *dst, const T *row, int c, int w
                  : "memory");
 }
 
-// partial [gridDim.x][2][width]: a block's sums of dy xh and of dy; a single block's are dw and db. Rows come DEPTH ahead through a ring in
-// shared memory to which each thread copies its own columns, so that nothing but the row's two sums is shared.
+// partial [clusters][2][width]: a cluster's sums of dy xh and of dy; a single cluster's are dw and db. Rows come DEPTH ahead
+// through a ring in shared memory to which each thread copies its own columns, so that nothing but the row's two sums
+// is shared. At the end the blocks of a cluster (as many as `cluster`) add up what they have, each a share of the columns.
+constexpr int CLUSTER = 8;
 constexpr int depth(int bufs, int p, int threads) { return 3 * bufs * p * threads * 16 > 220 * 1024 ? 2 : 3; }
 template <class T, int TPR, int P, bool SKIP>
 __global__ void __launch_bounds__(block_threads(TPR), TPR > 128 ? 1 : TPR == 64 ? 4 : 3)
 layernorm_backward_kernel(const T *__restrict__ x, const T *__restrict__ w, const float2 *__restrict__ stats, const T *dy,
-                          const T *dskip, T *dx, float *__restrict__ partial, float *__restrict__ dw, float *__restrict__ db, int rows, int width, int64_t ldx, int64_t lddy,
+                          const T *dskip, T *dx, float *__restrict__ partial,
+                          float *__restrict__ dw, float *__restrict__ db, int rows, int width, int cluster, int64_t ldx, int64_t lddy,
                           int64_t ldskip, int64_t lddx) {
     constexpr int N = kPiece<T>, H = N / 2, G = block_threads(TPR) / TPR, BUFS = SKIP ? 3 : 2;
     constexpr int DEPTH = depth(BUFS, P, block_threads(TPR));
@@ -250,51 +255,63 @@ layernorm_backward_kernel(const T *__restrict__ x, const T *__restrict__ w, cons
         st = next;
         stage = stage == DEPTH - 1 ? 0 : stage + 1;
     }
-    float *out_w = gridDim.x == 1 ? dw : partial + (int64_t)blockIdx.x * 2 * width;
-    float *out_b = gridDim.x == 1 ? db : out_w + width;
-    float fw[P][N], fb[P][N];
-#pragma unroll
-    for (int i = 0; i < P; ++i)
-#pragma unroll
-        for (int e = 0; e < H; ++e) {
-            upk2(aw[i][e], fw[i][2 * e], fw[i][2 * e + 1]);
-            upk2(ab[i][e], fb[i][2 * e], fb[i][2 * e + 1]);
-        }
-    if constexpr (G > 1) {
-        float *cross = reinterpret_cast<float *>(ring + DEPTH * BUFS * P * block_threads(TPR));
+    // what the block has: c, then the sums of columns c and c + 1
+    auto each_pair = [&](auto &&f) {
 #pragma unroll
         for (int i = 0; i < P; ++i)
 #pragma unroll
-            for (int e = 0; e < N; ++e) {
-                const int c = (t + i * TPR) * N + e;
-                if (c < width) {
-                    cross[(g * 2) * width + c] = fw[i][e];
-                    cross[(g * 2 + 1) * width + c] = fb[i][e];
-                }
+            for (int e = 0; e < H; ++e) {
+                float w0, w1, b0, b1;
+                upk2(aw[i][e], w0, w1);
+                upk2(ab[i][e], b0, b1);
+                f((t + i * TPR) * N + 2 * e, w0, w1, b0, b1);
             }
+    };
+    const bool whole = gridDim.x == cluster;
+    float *out_w = whole ? dw : partial + (int64_t)(blockIdx.x / cluster) * 2 * width, *out_b = whole ? db : out_w + width;
+    if (G == 1 && cluster == 1) {
+        each_pair([&](int c, float w0, float w1, float b0, float b1) {
+            if (c < width) out_w[c] = w0;
+            if (c + 1 < width) out_w[c + 1] = w1;
+            if (out_b && c < width) out_b[c] = b0;
+            if (out_b && c + 1 < width) out_b[c + 1] = b1;
+        });
+        return;
+    }
+    float *mine = reinterpret_cast<float *>(G > 1 ? ring + DEPTH * BUFS * P * block_threads(TPR) : ring);  // [G][2][width]
+    __syncthreads();  // the ring has been read
+    each_pair([&](int c, float w0, float w1, float b0, float b1) {
+        float *m = mine + g * 2 * width;
+        if (c < width) m[c] = w0, m[width + c] = b0;
+        if (c + 1 < width) m[c + 1] = w1, m[width + c + 1] = b1;
+    });
+    if constexpr (G > 1) {
         __syncthreads();
         for (int c = threadIdx.x; c < 2 * width; c += blockDim.x) {
             float s = 0.f;
 #pragma unroll
-            for (int k = 0; k < G; ++k) s += cross[k * 2 * width + c];
-            if (c < width) out_w[c] = s;
+            for (int k = 0; k < G; ++k) s += mine[k * 2 * width + c];
+            if (cluster > 1) mine[c] = s;
+            else if (c < width) out_w[c] = s;
             else if (out_b) out_b[c - width] = s;
         }
-    } else {
-#pragma unroll
-        for (int i = 0; i < P; ++i)
-#pragma unroll
-            for (int e = 0; e < N; ++e) {
-                const int c = (t + i * TPR) * N + e;
-                if (c < width) {
-                    out_w[c] = fw[i][e];
-                    if (out_b) out_b[c] = fb[i][e];
-                }
-            }
+        if (cluster == 1) return;
     }
+    const uint32_t rank = tc::cluster_rank(), at = tc::smem_u32(mine);
+    tc::cluster_sync();
+    for (int c = rank * blockDim.x + threadIdx.x; c < 2 * width; c += cluster * blockDim.x) {
+        float v[CLUSTER], s = 0.f;
+#pragma unroll
+        for (int k = 0; k < CLUSTER; ++k) v[k] = k < cluster ? tc::ld_shared_cluster(tc::map_to_rank(at + c * 4, k)) : 0.f;
+#pragma unroll
+        for (int k = 0; k < CLUSTER; ++k) s += v[k];
+        if (c < width) out_w[c] = s;
+        else if (out_b) out_b[c - width] = s;
+    }
+    tc::cluster_sync();  // the others have read this block's
 }
 
-// dw and db from the blocks' sums [blocks][2][width], added up in the blocks' order.
+// dw and db from the clusters' sums [blocks][2][width], added up in their order.
 constexpr int SUM_Y = 32;
 __global__ void __launch_bounds__(32 * SUM_Y)
 layernorm_sums_kernel(const float *__restrict__ partial, int blocks, int width, float *__restrict__ dw,
@@ -355,15 +372,77 @@ cudaError_t with_backward_shape(int width, F &&f) {
     return f(Int<512>{}, Int<Q / 2>{});
 }
 
-// Blocks of the backward pass: as many as the SMs' shared memory (and, for three, registers) holds, and no
-// more than leave each group of threads four rows (a block's sums are 8 bytes a column, its rows' values six).
-constexpr int MOST_BLOCKS = 152 * 4;
-int backward_blocks(int rows, int groups, int threads, size_t smem) {
-    const int room = (int)(227 * 1024 / (smem + 1024 + 256)), held = threads == 64 ? 4 : threads == 128 ? 3 : 1;
-    const int most = 152 * (room < 1 ? 1 : room < held ? room : held);
-    if (rows <= 8 * groups) return 1;  // and no second launch
-    const int need = (int)(((int64_t)rows + 4 * groups - 1) / (4 * groups));
-    return need < most ? need : most;
+// Blocks of the backward pass: as many as are resident (looked up once a device), and no more than leave each group of
+// threads four rows (a block's sums are 8 bytes a column, its rows' values six). What the blocks have is added up
+//  - in one cluster of up to eight, where that leaves a group no more than eight rows: no second launch;
+//  - in clusters of four, then by a second launch, where the blocks' sums are 12 MB or more and clusters leave next
+//    to no SM idle (16384 x 4096 bf16: 80 us without clusters, 74 with; 32768 x 2048, 10 MB: 78 and 80; fp32 16384 x 4096,
+//    where clusters find 288 places of 304: 124 and 137);
+//  - by the second launch alone.
+constexpr int MOST_BLOCKS = 152 * 4, BIG_CLUSTER = 4;
+constexpr size_t CLUSTER_BYTES = 12 << 20;
+
+struct Resident {
+    int blocks, in_clusters;  // at one time, without clusters and in clusters of four
+};
+template <class K>
+cudaError_t look_up_resident(K kernel, int threads, size_t smem, Resident *r) {
+    int dev = 0, sms = 0, per = 0, clusters = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per, kernel, threads, smem);
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1] = {};
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = BIG_CLUSTER;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.gridDim = dim3(BIG_CLUSTER);
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (e == cudaSuccess) e = cudaOccupancyMaxActiveClusters(&clusters, kernel, &cfg);
+    const int b = per < 1 ? 1 : sms * per, c = clusters * BIG_CLUSTER;
+    r->blocks = b < MOST_BLOCKS ? b : MOST_BLOCKS;
+    r->in_clusters = c < MOST_BLOCKS ? c : MOST_BLOCKS;
+    return e;
+}
+
+template <class T, int TPR, int P, bool SKIP>
+cudaError_t launch_backward(const LayerNormBwdArgs &a, cudaStream_t st, int *sums) {
+    constexpr int G = block_threads(TPR) / TPR, BT = block_threads(TPR), BUFS = SKIP ? 3 : 2;
+    constexpr size_t RING = (size_t)depth(BUFS, P, BT) * BUFS * P * BT * 16;
+    constexpr size_t MOST_SMEM = RING + (G > 1 ? (size_t)G * 2 * TPR * P * kPiece<T> * 4 : 0);  // at the shape's widest
+    auto kernel = layernorm_backward_kernel<T, TPR, P, SKIP>;
+    static std::atomic<uint64_t> known[64];  // a Resident
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    Resident r;
+    const uint64_t have = dev < 64 ? known[dev].load(std::memory_order_relaxed) : 0;
+    if (have) {
+        memcpy(&r, &have, sizeof r);
+    } else {
+        e = look_up_resident(kernel, BT, MOST_SMEM, &r);
+        if (e != cudaSuccess) return e;
+        uint64_t keep;
+        memcpy(&keep, &r, sizeof r);
+        if (dev < 64) known[dev].store(keep, std::memory_order_relaxed);
+    }
+    const int need = (int)(((int64_t)a.rows + 4 * G - 1) / (4 * G));
+    int blocks = need < r.blocks ? need : r.blocks, cluster = 1;
+    if (a.rows <= 64 * G) {
+        blocks = cluster = (a.rows + G - 1) / G < CLUSTER ? (a.rows + G - 1) / G : CLUSTER;
+    } else if ((size_t)blocks * 8 * a.width >= CLUSTER_BYTES && r.in_clusters * 20 >= blocks * 19) {
+        cluster = BIG_CLUSTER;
+        blocks = (blocks < r.in_clusters ? blocks : r.in_clusters) / BIG_CLUSTER * BIG_CLUSTER;
+    }
+    *sums = blocks / cluster;
+    const size_t smem = RING + (G > 1 ? (size_t)G * 2 * a.width * 4 : 0);
+    return launch_overlapped(kernel, dim3(blocks), dim3(BT), smem, cluster > 1 ? cluster : 0, st, (const T *)a.x,
+                             (const T *)a.w, (const float2 *)a.stats, (const T *)a.dy, (const T *)a.dskip, (T *)a.dx,
+                             (float *)a.workspace, a.dw, a.db, a.rows, a.width, cluster, a.ldx, a.lddy, a.ldskip, a.lddx);
 }
 
 template <class T>
@@ -378,23 +457,13 @@ cudaError_t forward(const LayerNormArgs &a, cudaStream_t st) {
 
 template <class T>
 cudaError_t backward(const LayerNormBwdArgs &a, cudaStream_t st) {
-    int blocks = 0;
-    cudaError_t e = with_backward_shape<T>(a.width, [&](auto tpr, auto p) {
-        constexpr int TPR = tpr, P = p, G = block_threads(TPR) / TPR;
-        auto launch = [&](auto kernel, int bufs) {
-            const size_t smem = (size_t)depth(bufs, P, block_threads(TPR)) * bufs * P * block_threads(TPR) * 16 + (G > 1 ? (size_t)G * 2 * a.width * 4 : 0);
-            blocks = backward_blocks(a.rows, G, block_threads(TPR), smem);
-            const cudaError_t set = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-            if (set != cudaSuccess) return set;
-            return launch_overlapped(kernel, dim3(blocks), dim3(block_threads(TPR)), smem, 0, st, (const T *)a.x, (const T *)a.w,
-                                     (const float2 *)a.stats, (const T *)a.dy, (const T *)a.dskip, (T *)a.dx, (float *)a.workspace, a.dw, a.db,
-                                     a.rows, a.width, a.ldx, a.lddy, a.ldskip, a.lddx);
-        };
-        return a.dskip ? launch(layernorm_backward_kernel<T, TPR, P, true>, 3) : launch(layernorm_backward_kernel<T, TPR, P, false>, 2);
+    int sums = 0;
+    const cudaError_t e = with_backward_shape<T>(a.width, [&](auto tpr, auto p) {
+        return a.dskip ? launch_backward<T, tpr, p, true>(a, st, &sums) : launch_backward<T, tpr, p, false>(a, st, &sums);
     });
-    if (e != cudaSuccess || blocks == 1) return e;
+    if (e != cudaSuccess || sums == 1) return e;
     return launch_overlapped(layernorm_sums_kernel, dim3((2 * a.width + 31) / 32), dim3(32, SUM_Y), 0, 0, st,
-                             (const float *)a.workspace, blocks, a.width, a.dw, a.db);
+                             (const float *)a.workspace, sums, a.width, a.dw, a.db);
 }
 
 }  // namespace
