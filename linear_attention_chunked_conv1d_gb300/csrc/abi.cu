@@ -1161,7 +1161,8 @@ int la_gated_ffn(const void *x, const void *w_gate, const void *w_up, void *h, v
     la::DenseArgs a{};
     a.kind = la::DENSE_GATED; a.count = 1;
     a.a[0] = x; a.lda[0] = ldx; a.b[0] = w_gate; a.ldb[0] = ldwg; a.b[1] = w_up; a.ldb[1] = ldwu; a.out[0] = h; a.ldo[0] = ldh;
-    a.M = M; a.N = F; a.K = K; a.saved = saved; a.half = (int)whole8(F); a.lds = 2 * whole8(F); a.act = act;
+    a.M = M; a.N = F; a.K = K; a.half = (int)whole8(F); a.lds = 2 * whole8(F); a.act = act;
+    a.saved = saved; a.lower = saved ? static_cast<char *>(saved) + 2 * M * a.lds : nullptr;
     LA_TRY(dense_status(&a));
     return launch_result([&] { return la::launch_dense(a, as_stream(stream)); }, "gated ffn launch");
 }

@@ -47,7 +47,7 @@ inline Epilogue make_epilogue(const DenseArgs &a) {
     ep.bias = (const __nv_bfloat16 *)a.bias;
     ep.residual = (const __nv_bfloat16 *)a.residual;
     ep.saved = (__nv_bfloat16 *)a.saved;
-    ep.lower = (uint8_t *)a.saved + 2 * (int64_t)a.M * a.lds;
+    ep.lower = (uint8_t *)a.lower;
     ep.ldr = a.ldr;
     ep.lds = a.lds;
     ep.half = a.half;

@@ -75,7 +75,7 @@ template <int KIND>
 __global__ void __launch_bounds__(THREADS, 2)
 dense_split_kernel(const __grid_constant__ Maps maps0, const __grid_constant__ Maps maps1, const __grid_constant__ Epilogue ep0,
                    const __grid_constant__ Epilogue ep1, const __grid_constant__ Job job0, const __grid_constant__ Job job1,
-                   int split, int *status, uint64_t wait_ns, int debug_stall) {
+                   int split, int beside, int *status, uint64_t wait_ns, int debug_stall) {
     constexpr bool P_MN = KIND == BACKWARD;
     constexpr int OUT_P = KIND == GATED ? PT / 2 : PT;  // columns of the result a tile holds
     extern __shared__ unsigned char smem_raw[];
@@ -124,7 +124,7 @@ dense_split_kernel(const __grid_constant__ Maps maps0, const __grid_constant__ M
     __syncthreads();
     tc::fence_after_sync();
     launch_next();
-    wait_for_previous();
+    if (beside != 2) wait_for_previous();  // else the kernel ahead has waited, and this one's rows are not that one's
     const uint32_t tm = *tmem_sh;
     const uint32_t rbase = tc::smem_u32(ring);
     const int nr = (int)(M - r0 < (int64_t)rows ? M - r0 : rows);  // the tile's rows, and those that this block finishes
@@ -266,6 +266,7 @@ dense_split_kernel(const __grid_constant__ Maps maps0, const __grid_constant__ M
         }
     }
     if (split > 1) tc::cluster_sync();  // the others have read this block's part
+    if (beside == 2) wait_for_previous();  // who waits for this kernel waits for the one ahead too
     if (*err && threadIdx.x == 0) raise_status(status, LA_DEV_TIMEOUT);
 }
 
@@ -284,9 +285,9 @@ Job make_job(const DenseArgs &a) {
 int64_t stages_of(const Job &j) { return (int64_t)((j.K + TK - 1) / TK) * j.parts; }
 
 // Blocks of a cluster: as many as there are places for, each with four stages or more of the longer sum.
-int choose_split(const Job &a, const Job *b) {
+int choose_split(const Job &a, const Job *b, int places) {
     const int64_t tiles = a.tiles + (b ? b->tiles : 0), kb = b && stages_of(*b) > stages_of(a) ? stages_of(*b) : stages_of(a);
-    int64_t s = PLACES / tiles;
+    int64_t s = places / tiles;
     if (s > kb / 4) s = kb / 4;
     return s < 1 ? 1 : s > 8 ? 8 : (int)s;
 }
@@ -294,7 +295,7 @@ int choose_split(const Job &a, const Job *b) {
 template <int KIND>
 cudaError_t launch(const DenseArgs &a, const DenseArgs *b, cudaStream_t st) {
     const Job j0 = make_job(a), j1 = b ? make_job(*b) : Job{};
-    const int split = choose_split(j0, b ? &j1 : nullptr);
+    const int split = choose_split(j0, b ? &j1 : nullptr, a.places ? a.places : PLACES);
     Maps maps[2];
     if (!make_maps(&maps[0], a, j0.dw, KIND == BACKWARD, j0.rows, 64) || (b && !make_maps(&maps[1], *b, j1.dw, KIND == BACKWARD, j1.rows, 64)))
         return cudaErrorInvalidValue;
@@ -309,7 +310,7 @@ cudaError_t launch(const DenseArgs &a, const DenseArgs *b, cudaStream_t st) {
     }
     return launch_overlapped(dense_split_kernel<KIND>, dim3((unsigned)((j0.tiles + j1.tiles) * split)), dim3(THREADS), ROOM + 2048,
                              split > 1 ? split : 0, st, maps[0], b ? maps[1] : maps[0], make_epilogue(a), make_epilogue(b ? *b : a), j0,
-                             j1, split, a.status, a.wait_ns ? a.wait_ns : WAIT_NS, a.debug_stall);
+                             j1, split, a.beside, a.status, a.wait_ns ? a.wait_ns : WAIT_NS, a.debug_stall);
 }
 
 // What the operands and results of a product weigh, in us at 6 TB/s.
@@ -351,9 +352,10 @@ double dense_pairs_us(const DenseArgs &a, const DenseArgs *b) {
 double dense_split_us(const DenseArgs &a, const DenseArgs *b) {
     const Job j0 = make_job(a), j1 = b ? make_job(*b) : Job{};
     if (j0.tiles + j1.tiles > 1000000) return 1e30;
-    const double s = choose_split(j0, b ? &j1 : nullptr);
+    const int places = a.places ? a.places : PLACES;
+    const double s = choose_split(j0, b ? &j1 : nullptr, places);
     auto time = [&](const Job &j) { return 3 + 0.04 * j.rows + 0.41 / 32768 * (P_BYTES + j.rows * TK * 2) * ceil(stages_of(j) / s); };
-    return fmax(2 + rounds(time(j0), j0.tiles * s, b ? time(j1) : 0, j1.tiles * s, PLACES, 1),
+    return fmax(2 + rounds(time(j0), j0.tiles * s, b ? time(j1) : 0, j1.tiles * s, places, 1),
                 6 + memory_us(a) + (b ? memory_us(*b) : 0));
 }
 

@@ -173,7 +173,7 @@ template <int KIND>
 __global__ void __launch_bounds__(THREADS, 1)
 dense_kernel(const __grid_constant__ Maps maps0, const __grid_constant__ Maps maps1, const __grid_constant__ Epilogue ep0,
              const __grid_constant__ Epilogue ep1, const __grid_constant__ Job job0, const __grid_constant__ Job job1,
-             int64_t whole, int64_t units, int *status, uint64_t wait_ns, int debug_stall) {
+             int64_t whole, int64_t units, int beside, int *status, uint64_t wait_ns, int debug_stall) {
     constexpr int OUT_N = KIND == GATED ? TN / 2 : TN;  // columns of the result a tile holds
     extern __shared__ unsigned char smem_raw[];
     unsigned char *sm = reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -209,6 +209,7 @@ dense_kernel(const __grid_constant__ Maps maps0, const __grid_constant__ Maps ma
     tc::cluster_sync();
     tc::fence_after_sync();
     wait_for_previous();
+    if (beside) launch_next();  // what came before is complete: the call's other kernel need not wait for it
     const uint32_t tm = *tmem_sh;
     const int64_t first = blockIdx.x / 2, step = gridDim.x / 2;
     // Every round but the first goes to the pairs from the last to the first: where the first pairs had the longer sums,
@@ -489,19 +490,58 @@ cudaError_t launch(const DenseArgs &a, const DenseArgs *b, cudaStream_t st) {
     const int64_t tiles = j0.tiles + j1.tiles, pairs = resident_pairs<KIND>(), rest = tiles % pairs;
     const int64_t whole = 2 * rest <= pairs ? tiles - rest : tiles, units = whole + 2 * (tiles - whole);
     return launch_overlapped(dense_kernel<KIND>, dim3(2 * (int)(units < pairs ? units : pairs)), dim3(THREADS), SMEM, 2, st, maps[0],
-                             b ? maps[1] : maps[0], make_epilogue(a), make_epilogue(b ? *b : a), j0, j1, whole, units, a.status,
+                             b ? maps[1] : maps[0], make_epilogue(a), make_epilogue(b ? *b : a), j0, j1, whole, units, a.beside, a.status,
                              a.wait_ns ? a.wait_ns : WAIT_NS, a.debug_stall);
 }
 
 }  // namespace
 
-cudaError_t launch_dense(const DenseArgs &a, cudaStream_t st) {
-    if (dense_split_us(a, nullptr) < dense_pairs_us(a, nullptr)) return launch_dense_split(a, nullptr, st);
+namespace {
+
+cudaError_t launch_pairs(const DenseArgs &a, cudaStream_t st) {
     switch (a.kind) {
         case DENSE_LINEAR: return launch<LINEAR>(a, nullptr, st);
         case DENSE_GATED: return launch<GATED>(a, nullptr, st);
         default: return launch<BACKWARD>(a, nullptr, st);
     }
+}
+
+// A call's rows from `row` on.
+DenseArgs rows_from(const DenseArgs &a, int row) {
+    DenseArgs r = a;
+    auto on = [&](const void *p, int64_t ld, int size) { return p ? static_cast<const char *>(p) + row * ld * size : nullptr; };
+    for (int i = 0; i < 2; ++i) r.a[i] = on(a.a[i], a.lda[i], 2);
+    r.out[0] = const_cast<char *>(on(a.out[0], a.ldo[0], 2));
+    r.residual = on(a.residual, a.ldr, 2);
+    r.saved = const_cast<char *>(on(a.saved, a.lds, 2));
+    r.lower = const_cast<char *>(on(a.lower, a.lds, 1));
+    r.M = a.M - row;
+    return r;
+}
+
+}  // namespace
+
+cudaError_t launch_dense(const DenseArgs &a, cudaStream_t st) {
+    const double pairs = dense_pairs_us(a, nullptr), split = dense_split_us(a, nullptr);
+    // A few rows past whole tiles would take tiles of their own, and with them part of another round. Where the whole
+    // tiles leave pairs without work, the other kernel takes those rows there, beside this one's last round. (777 x 5001 x
+    // 2048: 60 tiles on 76 pairs and 9 rows, 22.3 us in 80 tiles, 17.7 so; with bias, GELU and residual 27.0 and 22.2;
+    // 1030 x 8192 x 2048: 31.8 and 27.5; where little is to be gained it may be lost: 1040 x 2048 x 2048 16.0 and 19.5.)
+    const int rest = a.M % TM;
+    if (a.kind != DENSE_DW && a.M > TM && rest && rest <= 64) {
+        DenseArgs main = a, other = rows_from(a, a.M - rest);
+        main.M = a.M - rest;
+        const int64_t last = make_job(main).tiles % 76, idle = last ? 76 - (2 * last <= 76 ? 2 * last : last) : 0;
+        other.places = (int)idle * 4;
+        // the other kernel starts some 4 us after this one
+        if (idle >= 8 && fmax(dense_pairs_us(main, nullptr) + 1.5, 4 + dense_split_us(other, nullptr)) + 2 < fmin(pairs, split)) {
+            main.beside = 1;
+            other.beside = 2;
+            const cudaError_t e = launch_pairs(main, st);
+            return e != cudaSuccess ? e : launch_dense_split(other, nullptr, st);
+        }
+    }
+    return split < pairs ? launch_dense_split(a, nullptr, st) : launch_pairs(a, st);
 }
 
 cudaError_t launch_dense_pair(const DenseArgs &dx, const DenseArgs &dw, cudaStream_t st) {

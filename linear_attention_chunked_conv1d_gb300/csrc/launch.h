@@ -281,9 +281,11 @@ struct DenseArgs {
     int64_t ldo[2];
     int M, N, K;
     const void *bias, *residual;
-    void *saved;
+    void *saved, *lower;  // lower: DENSE_GATED's 8-bit plane
     int64_t ldr, lds;
     int half, act;
+    int beside;  // two kernels of one call side by side: 1, another follows; 2, this is the other (set by launch_dense)
+    int places;  // blocks that there is room for (0: the whole GPU)
     int *status;
     uint64_t wait_ns;  // limit of the kernel's bounded waits (0: the 2 s default)
     int debug_stall;   // test knob: one wait on a barrier that nothing completes

@@ -32,6 +32,50 @@ def test_rows_around_the_tiles(cuda, m):
     check_gated(gated_case(cuda, m, 197, 1100, m), "gelu_tanh")
 
 
+@pytest.mark.parametrize("m,n,k", [(777, 5001, 2048), (1030, 8192, 2048), (777, 2048, 5001), (257, 2000, 520), (1281, 3000, 136), (513, 392, 2100), (4099, 4500, 72)])
+def test_a_few_rows_past_whole_tiles(cuda, m, n, k):
+    """The rows past the last whole tile may be another kernel's, beside the first one's last round: between calls that
+    write what it reads and read what it writes, with nothing of the one's rows missing or touched by the other."""
+    c = case(cuda, m, n, k, m)
+    check_linear(c, "gelu")
+    check_linear(case(cuda, m, n, k, m + 1, bias=False, residual=False), "none")
+    g = gated_case(cuda, m, n, k, m + 2)
+    check_gated(g, "silu")
+    want = c["dx"].double()  # of the call that makes dw too
+    c["dx"].fill_(7.0)
+    saved = room(la.linear_saved_bytes(m, n, "gelu"), cuda)
+    la.linear(c["x"], c["w"], bias=c["bias"], act="gelu", saved=saved)
+    la.linear_backward(c["x"], c["w"], saved, c["dy"], c["dx"], act="gelu", workspace=room(la.linear_backward_workspace_bytes(m, n, k, "gelu"), cuda))
+    assert float((c["dx"].double() - want).norm()) <= 2 * U * float(want.norm())  # one rounding each
+    # in the residual's place
+    res = rows_like(c["residual"])
+    assert torch.equal(la.linear(c["x"], c["w"], res, bias=c["bias"], residual=res, act="gelu"), la.linear(c["x"], c["w"], bias=c["bias"], residual=c["residual"], act="gelu"))
+    # a chain on one stream, eager and replayed: x is written by the call before, y read by the next and written again
+    w2 = (torch.randn(k, n, device=cuda) / math.sqrt(n)).to(BF16)
+    if n % 8 or k % 8:
+        w2 = rows_like(w2)
+    x0, x1, y, z = rows_like(c["x"]), rows_like(c["x"]), out_rows((m, n), BF16, cuda), out_rows((m, k), BF16, cuda)
+
+    def chain():
+        x1.copy_(x0)
+        for _ in range(3):
+            la.linear(x1, c["w"], y, bias=c["bias"], act="silu")
+            la.linear(y, w2, z)
+            la.layernorm_rows(z, torch.ones(k, dtype=BF16, device=cuda), y=x1)
+        return x1.clone()
+    cur = x0
+    for _ in range(3):
+        a = la.linear(cur, c["w"], bias=c["bias"], act="silu")
+        torch.cuda.synchronize()
+        b = la.linear(a, w2)
+        torch.cuda.synchronize()
+        cur = la.layernorm_rows(b, torch.ones(k, dtype=BF16, device=cuda))
+        torch.cuda.synchronize()
+    for _ in range(5):
+        assert torch.equal(chain(), cur)
+    assert la.device_status() == 0
+
+
 def test_far_strides(cuda):
     """Rows 2^31 values apart: offsets pass 32 bits in x, residual and y, in dy and dx, and in a norm's rows."""
     g = torch.Generator().manual_seed(1)
