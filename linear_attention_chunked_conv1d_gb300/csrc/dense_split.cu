@@ -284,12 +284,42 @@ Job make_job(const DenseArgs &a) {
 }
 int64_t stages_of(const Job &j) { return (int64_t)((j.K + TK - 1) / TK) * j.parts; }
 
+// Clusters of s blocks (2..8) that are resident at one time: the SMs of a GPC hold whole clusters only, so some sizes leave
+// many places empty. The runtime's answer counts a block an SM (15 clusters of 7 or 8, 23 of 6, 28, 36, 46, 76 of 2); two
+// are there (40 clusters of 7 take two rounds, 13.5 us for 8.7 in clusters of 6; 32 of 8 and 94 of 3 take one, so a little
+// more than twice the answer fits). Looked up once a device (the three kernels take the same room).
+int resident_clusters(int s) {
+    static std::atomic<int> known[64][9];
+    int dev = 0, n = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return PLACES / s;
+    n = known[dev][s].load(std::memory_order_relaxed);
+    if (n) return n;
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1] = {};
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = s;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.gridDim = dim3(s);
+    cfg.blockDim = dim3(THREADS);
+    cfg.dynamicSmemBytes = ROOM + 2048;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cudaFuncSetAttribute(dense_split_kernel<LINEAR>, cudaFuncAttributeMaxDynamicSharedMemorySize, ROOM + 2048) != cudaSuccess ||
+        cudaOccupancyMaxActiveClusters(&n, dense_split_kernel<LINEAR>, &cfg) != cudaSuccess || n < 1)
+        return PLACES / s;
+    n = n * 2 * 107 / 100;
+    known[dev][s].store(n, std::memory_order_relaxed);
+    return n;
+}
+
 // Blocks of a cluster: as many as there are places for, each with four stages or more of the longer sum.
 int choose_split(const Job &a, const Job *b, int places) {
     const int64_t tiles = a.tiles + (b ? b->tiles : 0), kb = b && stages_of(*b) > stages_of(a) ? stages_of(*b) : stages_of(a);
     int64_t s = places / tiles;
     if (s > kb / 4) s = kb / 4;
-    return s < 1 ? 1 : s > 8 ? 8 : (int)s;
+    if (s > 8) s = 8;
+    while (s > 1 && resident_clusters((int)s) < tiles) --s;
+    return s < 1 ? 1 : (int)s;
 }
 
 template <int KIND>
