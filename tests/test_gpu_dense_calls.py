@@ -73,6 +73,25 @@ def test_a_few_rows_past_whole_tiles(cuda, m, n, k):
         torch.cuda.synchronize()
     for _ in range(5):
         assert torch.equal(chain(), cur)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = chain()
+    for _ in range(5):
+        out.zero_()
+        graph.replay()
+        assert torch.equal(out, cur)
+    # two chains at once, on streams of their own
+    u, v = torch.cuda.Stream(), torch.cuda.Stream()
+    ends = [torch.empty(m, (k + 7) // 8 * 8, dtype=BF16, device=cuda)[:, :k] for _ in range(2)]
+    mids = [out_rows((m, n), BF16, cuda) for _ in range(2)]
+    torch.cuda.synchronize()
+    for _ in range(6):
+        for st, mid, end in zip((u, v), mids, ends):
+            la.linear(x0, c["w"], mid, bias=c["bias"], act="silu", stream=st)
+            la.linear(mid, w2, end, stream=st)
+    torch.cuda.synchronize()
+    first = la.linear(la.linear(x0, c["w"], bias=c["bias"], act="silu"), w2)
+    assert all(torch.equal(end, first) for end in ends)
     assert la.device_status() == 0
 
 
@@ -334,17 +353,17 @@ def test_captured_and_replayed(cuda):
 def test_the_wait_runs_out(cuda, monkeypatch):
     """A block that waits for what never comes gives up, says so, and leaves the context usable: tiles by pairs of
     blocks, and split sums."""
-    c, d = case(cuda, 1030, 2000, 264, 9), case(cuda, 8, 400, 2000, 10)
-    want = [la.linear(q["x"], q["w"]).clone() for q in (c, d)]
+    c, d, f = case(cuda, 1030, 2000, 264, 9), case(cuda, 8, 400, 2000, 10), case(cuda, 777, 5001, 2048, 11)
+    want = [la.linear(q["x"], q["w"]).clone() for q in (c, d, f)]
     torch.cuda.synchronize()
     assert la.device_status() == 0
     monkeypatch.setenv("LA_WAIT_LIMIT_NS", "20000000")
-    for q in (c, d):
+    for q in (c, d, f):
         monkeypatch.setenv("LA_DEBUG_STALL", "1")
         la.linear(q["x"], q["w"], q["y"])
         assert la.device_status() & 2
         monkeypatch.delenv("LA_DEBUG_STALL")
-    for q, ref in zip((c, d), want):
+    for q, ref in zip((c, d, f), want):
         assert torch.equal(la.linear(q["x"], q["w"]), ref)
     assert la.device_status() == 0
 
