@@ -248,6 +248,11 @@ int w4_common(const void *q, const void *scales, int K, int group) {
 
 // Columns of a buffer that the dense calls keep between forward and backward pass: whole 16 bytes of bf16.
 int64_t whole8(int n) { return ((int64_t)n + 7) / 8 * 8; }
+size_t whole16(size_t bytes) { return (bytes + 15) / 16 * 16; }
+// Where in a workspace, from `used` bytes on, dW's partial sums lie; null where there are none.
+float *dw_partial(void *workspace, size_t used, size_t bytes) {
+    return bytes > used ? reinterpret_cast<float *>(static_cast<char *>(workspace) + used) : nullptr;
+}
 
 int layernorm_common(const void *x, const void *w, int rows, int width, int64_t ldx, int dtype) {
     if (rows < 1 || rows > kMaxCount) return fail(LA_ERR_COUNT, "layer norm of %d rows (1..%d)", rows, kMaxCount);
@@ -1087,7 +1092,7 @@ int la_linear(const void *x, const void *w, const void *bias, const void *residu
 
 size_t la_linear_backward_workspace_bytes(int M, int N, int K, int act) {
     if (M < 1 || N < 1 || K < 1) return 0;
-    return la_linear_saved_bytes(M, N, act) + la::linear_backward_partial_bytes(M, N);
+    return la_linear_saved_bytes(M, N, act) + whole16(la::linear_backward_partial_bytes(M, N)) + la::dense_dw_partial_bytes(M, N, K, 1);
 }
 
 int la_linear_backward(const void *x, const void *w, const void *saved, size_t saved_bytes, const void *dy, void *dx,
@@ -1134,6 +1139,7 @@ int la_linear_backward(const void *x, const void *w, const void *saved, size_t s
             if (e != cudaSuccess) return e;
         }
         a.a[0] = dz; a.lda[0] = lddz;
+        a.partial = dw_partial(workspace, kept + whole16(la::linear_backward_partial_bytes(M, N)), need);
         return launch_backward_products(a, w, ldw, nullptr, 0, dx, lddx, x, ldx, dw, lddw, nullptr, 0, M, N, K, as_stream(stream));
     }, "linear backward launch");
 }
@@ -1168,7 +1174,7 @@ int la_gated_ffn(const void *x, const void *w_gate, const void *w_up, void *h, v
 }
 
 size_t la_gated_ffn_backward_workspace_bytes(int M, int F, int K) {
-    return M < 1 || F < 1 || K < 1 ? 0 : 4 * (size_t)M * whole8(F);
+    return M < 1 || F < 1 || K < 1 ? 0 : 4 * (size_t)M * whole8(F) + la::dense_dw_partial_bytes(M, F, K, 2);
 }
 
 int la_gated_ffn_backward(const void *x, const void *w_gate, const void *w_up, const void *saved, size_t saved_bytes,
@@ -1213,6 +1219,7 @@ int la_gated_ffn_backward(const void *x, const void *w_gate, const void *w_up, c
             a.a[i] = static_cast<const char *>(workspace) + i * half * 2;
             a.lda[i] = 2 * half;
         }
+        a.partial = dw_partial(workspace, 4 * (size_t)M * half, need);
         return launch_backward_products(a, w_gate, ldwg, w_up, ldwu, dx, lddx, x, ldx, dw_gate, lddwg, dw_up, lddwu, M, F, K,
                                         as_stream(stream));
     }, "gated ffn backward launch");

@@ -18,6 +18,8 @@ struct Epilogue {
     uint8_t *lower;        // GATED: the next eight bits, laid out the same
     int64_t ldo[2], ldr, lds;
     int half, act;
+    float *partial;  // DW split: [out][part][M][ldp] fp32
+    int64_t ldp;
 };
 
 // Tensor maps of a call's operands. An operand that runs along the summed index is read in boxes of 64 of its
@@ -52,6 +54,8 @@ inline Epilogue make_epilogue(const DenseArgs &a) {
     ep.lds = a.lds;
     ep.half = a.half;
     ep.act = a.act;
+    ep.partial = a.partial;
+    ep.ldp = ((int64_t)a.N + 7) / 8 * 8;
     return ep;
 }
 

@@ -373,13 +373,16 @@ double rounds(double a, double n, double b, double m, double places, double last
 // 23.3; 777 x 5008 x 2048 22.7 and 20.2, with bias, GELU and residual 27.6 and 27.9; 8192 x 8192 x 64 46.5 and 112; gated
 // 32 x 8192 x 4096 29.5 and 25.5, 128: 29.5 and 28.9, 256: 30.8 and 35.6; dx 512 x 4096 x 4096 19.9 and 20.6; dw of 16384
 // rows, 1024 x 1024: 57.1 and 36.0, of 4096 rows: 18.5 and 16.3, of 1024 rows: 8.5 and 10.8.
+//   Parts of dW's sum (split) add a launch of 4 us and their values, written and read at 4 TB/s.
 double dense_pairs_us(const DenseArgs &a, const DenseArgs *b) {
-    auto tiles = [](const DenseArgs &q) {
-        return ceil(q.M / 256.) * ceil(q.N * (q.kind == DENSE_GATED ? 2. : 1.) / 256) * (q.kind == DENSE_DW ? q.count : 1);
+    auto parts = [](const DenseArgs &q) { return q.kind == DENSE_DW && q.split > 1 ? q.split : 1.; };
+    auto tiles = [&](const DenseArgs &q) {
+        return ceil(q.M / 256.) * ceil(q.N * (q.kind == DENSE_GATED ? 2. : 1.) / 256) * (q.kind == DENSE_DW ? q.count : 1) * parts(q);
     };
-    auto time = [](const DenseArgs &q) { return fmax(0.29 * ceil(q.K / 64.) * (q.kind == DENSE_DX ? q.count : 1), 3.2); };
+    auto time = [&](const DenseArgs &q) { return fmax(0.29 * ceil(ceil(q.K / 64.) / parts(q)) * (q.kind == DENSE_DX ? q.count : 1), 3.2); };
+    auto join = [&](const DenseArgs &q) { return parts(q) > 1 ? 4 + parts(q) * q.count * q.M * (double)q.N * (8 / 4e6) : 0; };
     return fmax(5 + rounds(time(a), tiles(a), b ? time(*b) : 0, b ? tiles(*b) : 0, 76, 0.7),
-                7 + memory_us(a) + (b ? memory_us(*b) : 0));
+                7 + memory_us(a) + (b ? memory_us(*b) : 0)) + join(a) + (b ? join(*b) : 0);
 }
 double dense_split_us(const DenseArgs &a, const DenseArgs *b) {
     const Job j0 = make_job(a), j1 = b ? make_job(*b) : Job{};

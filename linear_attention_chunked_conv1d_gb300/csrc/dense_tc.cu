@@ -56,7 +56,8 @@ enum { LINEAR = DENSE_LINEAR, GATED = DENSE_GATED, BACKWARD };
 struct Job {
     int M, N, K, parts;
     bool dw;  // BACKWARD: DW, else DX
-    int64_t mt, nt, tiles;
+    int split;  // DW: parts of a long sum that are units of their own and are joined afterwards
+    int64_t mt, nt, tiles;  // tiles: times parts
 };
 
 using bf16 = __nv_bfloat16;
@@ -74,6 +75,7 @@ __device__ __forceinline__ void place_in_bands(int64_t t, int64_t mt, int64_t nt
 struct Unit {
     bool second;     // of the launch's second product
     int o, m, n;     // output (DW), place of the tile
+    int part;        // of the sum
     bool cut;        // half a tile:
     int half;        // the first or the second
 };
@@ -85,10 +87,19 @@ __device__ __forceinline__ Unit unit_at(int64_t u, int64_t whole, const Job &job
     q.second = t >= job0.tiles;
     if (q.second) t -= job0.tiles;
     const Job &job = q.second ? job1 : job0;
+    q.part = job.split > 1 ? (int)(t % job.split) : 0;
+    if (job.split > 1) t /= job.split;
     const int64_t per = job.mt * job.nt;
     q.o = (int)(t / per);
     place_in_bands(t - q.o * per, job.mt, job.nt, q.m, q.n);
     return q;
+}
+
+// The stages of 64 summed indexes that a unit adds up (of each of DX's parts), from first to end.
+__device__ __forceinline__ void stages_of(const Job &job, const Unit &unit, int &first, int &end) {
+    const int64_t all = (job.K + TK - 1) / TK;
+    first = (int)(all * unit.part / job.split);
+    end = (int)(all * (unit.part + 1) / job.split);
 }
 
 // A warp's 32 x 64 values on their way to or from memory: row r's 16-byte piece j lies at place j ^ (r % 8) of its
@@ -136,6 +147,17 @@ __device__ __forceinline__ void flush_bytes(uint2 *buf, const uint2 (&mine)[8], 
     for (int i = 0; i < 8; ++i) {
         const int r = i * 4 + (lane >> 3);
         if (row0 + r < M && c < N) *reinterpret_cast<uint2 *>(out + (row0 + r) * ld + c) = buf[r * 8 + (j ^ (r & 7))];
+    }
+    __syncwarp();
+}
+// Rows of 32 floats (whole pieces up to ld, which is a multiple of 8).
+__device__ __forceinline__ void flush_floats(uint4 *buf, float *out, int64_t ld, int64_t row0, int M, int col, int lane) {
+    __syncwarp();
+    const int j = lane & 7, c = col + j * 4;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const int r = i * 4 + (lane >> 3);
+        if (row0 + r < M && c < ld) *reinterpret_cast<uint4 *>(out + (row0 + r) * ld + c) = piece(buf, r, j);
     }
     __syncwarp();
 }
@@ -230,14 +252,15 @@ dense_kernel(const __grid_constant__ Maps maps0, const __grid_constant__ Maps ma
                 const int n0 = unit.n * OUT_N + unit.half * (OUT_N / 2) + (KIND == GATED ? 0 : (int)rank * share);
                 const uint32_t bytes = 2 * (HALF_BYTES + share * TK * 2);
                 const CUtensorMap *ma = &maps.a[KIND == BACKWARD && job.dw ? unit.o : 0], *mb = &maps.b[KIND == GATED ? rank : 0];
-                const int kp = (job.K + TK - 1) / TK;
+                int k_first, k_end;
+                stages_of(job, unit, k_first, k_end);
                 for (int p = 0; p < job.parts && !*err; ++p) {
                     if (KIND == BACKWARD && p) {
                         ma = &maps.a[1];
                         mb = &maps.b[1];
                     }
-                    int k0 = 0;
-                    for (int k = 0; k < kp; ++k, k0 += TK) {
+                    int k0 = k_first * TK;
+                    for (int k = k_first; k < k_end; ++k, k0 += TK) {
                         if (!tc::mbar_wait(empty + s, ph ^ 1u, wait_ns, SLEEP_NS) || *err) {
                             *err = 1;
                             break;
@@ -279,7 +302,9 @@ dense_kernel(const __grid_constant__ Maps maps0, const __grid_constant__ Maps ma
                 const bool a_mn = KIND == BACKWARD && job.dw;
                 constexpr bool b_mn = KIND == BACKWARD;
                 const uint32_t id = tc::idesc(TM, unit.cut ? TN / 2 : TN, tc::FMT_BF16, a_mn, b_mn);
-                const int64_t kb = (int64_t)((job.K + TK - 1) / TK) * job.parts;
+                int k_first, k_end;
+                stages_of(job, unit, k_first, k_end);
+                const int64_t kb = (int64_t)(k_end - k_first) * job.parts;
                 const uint32_t acc = tcnt & 1u, aph = (tcnt >> 1) & 1u;
                 if (!tc::mbar_wait(acce + acc, aph ^ 1u, wait_ns, SLEEP_NS)) {
                     *err = 1;
@@ -350,8 +375,23 @@ dense_kernel(const __grid_constant__ Maps maps0, const __grid_constant__ Maps ma
             }
             tc::fence_after_sync();
             const uint32_t src = tc::tmem_addr(tm + acc * TN, 32 * q, c_first);
+            if (KIND == BACKWARD && job.split > 1) {  // a part of the sum, in fp32
+                float *part = ep.partial + ((int64_t)o * job.split + unit.part) * M * ep.ldp;
 #pragma unroll 1
-            for (int c = 0; c < cols; c += 64) {
+                for (int c = 0; c < cols; c += 32) {
+                    float v[32];
+                    tc::tmem_ld16(src + c, v);
+                    tc::tmem_ld16(src + c + 16, v + 16);
+                    tc::tmem_wait_ld();
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        piece(buf, lane, j) = make_uint4(__float_as_uint(v[4 * j]), __float_as_uint(v[4 * j + 1]),
+                                                         __float_as_uint(v[4 * j + 2]), __float_as_uint(v[4 * j + 3]));
+                    flush_floats(buf, part, ep.ldp, row0, M, n0 + c, lane);
+                }
+            }
+#pragma unroll 1
+            for (int c = KIND == BACKWARD && job.split > 1 ? cols : 0; c < cols; c += 64) {
                 const int col = n0 + c;
                 if (KIND == LINEAR) {
                     if (ep.saved) {  // z goes out first, y is made of it in a second look at the accumulator
@@ -447,6 +487,27 @@ dense_kernel(const __grid_constant__ Maps maps0, const __grid_constant__ Maps ma
     if (*err && threadIdx.x == 0) raise_status(status, LA_DEV_TIMEOUT);
 }
 
+// dW from the parts of its sum, [split][M][ldp] fp32, added up in their order.
+__global__ void __launch_bounds__(256)
+dense_join_kernel(const float *__restrict__ partial, bf16 *__restrict__ out, int M, int N, int split, int64_t ldp, int64_t ldo) {
+    wait_for_previous();
+    const int c = (blockIdx.x * 32 + threadIdx.x) * 8;
+    if (c >= N) return;
+    for (int64_t r = blockIdx.y * 8 + threadIdx.y; r < M; r += (int64_t)gridDim.y * 8) {
+        float v[8] = {};
+#pragma unroll 4
+        for (int s = 0; s < split; ++s) {
+            const float *p = partial + ((int64_t)s * M + r) * ldp + c;
+            float t[8];
+            Vec16<float>::load(p, t);
+            Vec16<float>::load(p + 4, t + 4);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] += t[e];
+        }
+        store_piece(out + r * ldo, c, N, v);
+    }
+}
+
 // Pairs that are resident at one time (looked up once a device).
 template <int KIND>
 int resident_pairs() {
@@ -473,10 +534,10 @@ int resident_pairs() {
 
 Job make_job(const DenseArgs &a) {
     const int out_n = a.kind == DENSE_GATED ? TN / 2 : TN;
-    Job j{a.M, a.N, a.K, a.kind == DENSE_DX ? a.count : 1, a.kind == DENSE_DW, 0, 0, 0};
+    Job j{a.M, a.N, a.K, a.kind == DENSE_DX ? a.count : 1, a.kind == DENSE_DW, a.split > 1 ? a.split : 1, 0, 0, 0};
     j.mt = (a.M + TM - 1) / TM;
     j.nt = (a.N + out_n - 1) / out_n;
-    j.tiles = j.mt * j.nt * (a.kind == DENSE_DW ? a.count : 1);
+    j.tiles = j.mt * j.nt * (a.kind == DENSE_DW ? a.count : 1) * j.split;
     return j;
 }
 
@@ -487,13 +548,25 @@ cudaError_t launch(const DenseArgs &a, const DenseArgs *b, cudaStream_t st) {
     const bool mn = KIND == BACKWARD;
     if (!make_maps(&maps[0], a, a.kind == DENSE_DW, mn, 128, 64)) return cudaErrorInvalidValue;
     if (b && !make_maps(&maps[1], *b, b->kind == DENSE_DW, mn, 128, 64)) return cudaErrorInvalidValue;
-    const Job j0 = make_job(a), j1 = b ? make_job(*b) : Job{};
+    const Job j0 = make_job(a), j1 = b ? make_job(*b) : Job{0, 0, 0, 1, false, 1, 0, 0, 0};
     // the tiles of an incomplete round are cut in halves where there are pairs for them
     const int64_t tiles = j0.tiles + j1.tiles, pairs = resident_pairs<KIND>(), rest = tiles % pairs;
     const int64_t whole = 2 * rest <= pairs ? tiles - rest : tiles, units = whole + 2 * (tiles - whole);
-    return launch_overlapped(dense_kernel<KIND>, dim3(2 * (int)(units < pairs ? units : pairs)), dim3(THREADS), SMEM, 2, st, maps[0],
-                             b ? maps[1] : maps[0], make_epilogue(a), make_epilogue(b ? *b : a), j0, j1, whole, units, a.beside, a.status,
-                             a.wait_ns ? a.wait_ns : WAIT_NS, a.debug_stall);
+    const cudaError_t e = launch_overlapped(
+        dense_kernel<KIND>, dim3(2 * (int)(units < pairs ? units : pairs)), dim3(THREADS), SMEM, 2, st, maps[0], b ? maps[1] : maps[0],
+        make_epilogue(a), make_epilogue(b ? *b : a), j0, j1, whole, units, a.beside, a.status, a.wait_ns ? a.wait_ns : WAIT_NS,
+        a.debug_stall);
+    const DenseArgs &w = b && b->split > 1 ? *b : a;
+    if (e != cudaSuccess || w.split <= 1) return e;
+    const Epilogue ep = make_epilogue(w);
+    const int cols = (w.N + 255) / 256, runs = (w.M + 7) / 8, most = 152 * 6 / cols < 1 ? 1 : 152 * 6 / cols;
+    for (int o = 0; o < w.count; ++o) {
+        const cudaError_t j = launch_overlapped(dense_join_kernel, dim3(cols, runs < most ? runs : most), dim3(32, 8), 0, 0, st,
+                                                (const float *)(ep.partial + (int64_t)o * w.split * w.M * ep.ldp), ep.out[o], w.M, w.N,
+                                                w.split, ep.ldp, ep.ldo[o]);
+        if (j != cudaSuccess) return j;
+    }
+    return cudaSuccess;
 }
 
 }  // namespace
@@ -523,7 +596,37 @@ DenseArgs rows_from(const DenseArgs &a, int row) {
 
 }  // namespace
 
-cudaError_t launch_dense(const DenseArgs &a, cudaStream_t st) {
+// Parts of dW's long sum. Few tiles of many rows' sums (16384 rows, 1024 x 1024: 16 tiles of 256 stages) would keep few
+// pairs busy; parts of them are units of their own, as many as make the sum of the model's times the least.
+namespace {
+
+int choose_dw_split(const DenseArgs &dw, const DenseArgs *dx) {
+    DenseArgs q = dw;
+    q.split = 1;
+    double best = dense_pairs_us(q, dx) - 2;  // worth a second launch
+    int s = 1;
+    for (int k = 2; k <= 8; ++k) {
+        q.split = k;
+        if ((q.K + TK - 1) / TK < 8 * k) break;
+        const double t = dense_pairs_us(q, dx);
+        if (t < best) best = t, s = k;
+    }
+    return s;
+}
+
+}  // namespace
+
+size_t dense_dw_partial_bytes(int rows, int M, int N, int count) {
+    DenseArgs dw{}, dx{};
+    dw.kind = DENSE_DW; dw.count = count; dw.M = M; dw.N = N; dw.K = rows;
+    dx.kind = DENSE_DX; dx.count = count; dx.M = rows; dx.N = N; dx.K = M;
+    const int with = choose_dw_split(dw, &dx), alone = choose_dw_split(dw, nullptr), s = with > alone ? with : alone;
+    return s > 1 ? (size_t)count * s * M * (((size_t)N + 7) / 8 * 8) * sizeof(float) : 0;
+}
+
+cudaError_t launch_dense(const DenseArgs &args, cudaStream_t st) {
+    DenseArgs a = args;
+    a.split = a.kind == DENSE_DW && a.partial ? choose_dw_split(a, nullptr) : 1;
     const double pairs = dense_pairs_us(a, nullptr), split = dense_split_us(a, nullptr);
     // A few rows past whole tiles would take tiles of their own, and with them part of another round. Where the whole
     // tiles leave pairs without work, the other kernel takes those rows there, beside this one's last round. (777 x 5001 x
@@ -546,16 +649,21 @@ cudaError_t launch_dense(const DenseArgs &a, cudaStream_t st) {
     return split < pairs ? launch_dense_split(a, nullptr, st) : launch_pairs(a, st);
 }
 
-cudaError_t launch_dense_pair(const DenseArgs &dx, const DenseArgs &dw, cudaStream_t st) {
-    const double pairs = dense_pairs_us(dx, &dw), split = dense_split_us(dx, &dw);
-    const double apart = fmin(dense_pairs_us(dx, nullptr), dense_split_us(dx, nullptr)) + fmin(dense_pairs_us(dw, nullptr), dense_split_us(dw, nullptr));
+cudaError_t launch_dense_pair(const DenseArgs &dx, const DenseArgs &dw_args, cudaStream_t st) {
+    DenseArgs dw = dw_args, alone = dw_args;
+    dw.split = dw.partial ? choose_dw_split(dw, &dx) : 1;
+    alone.split = dw.partial ? choose_dw_split(dw, nullptr) : 1;
+    const double pairs = dense_pairs_us(dw, &dx), split = dense_split_us(dx, &dw);
+    const double apart = fmin(dense_pairs_us(dx, nullptr), dense_split_us(dx, nullptr)) + fmin(dense_pairs_us(alone, nullptr), dense_split_us(dw, nullptr));
     if (apart < fmin(pairs, split)) {
         const cudaError_t e = launch_dense(dx, st);
-        return e != cudaSuccess ? e : launch_dense(dw, st);
+        return e != cudaSuccess ? e : launch_dense(dw_args, st);
     }
-    const bool dx_first = (int64_t)dx.K * dx.count >= dw.K;  // the longer sums first
+    const bool by_split = split < pairs;
+    if (by_split) dw.split = 1;
+    const bool dx_first = (int64_t)dx.K * dx.count * dw.split >= dw.K;  // the longer sums first
     const DenseArgs &a = dx_first ? dx : dw, &b = dx_first ? dw : dx;
-    return split < pairs ? launch_dense_split(a, &b, st) : launch<BACKWARD>(a, &b, st);
+    return by_split ? launch_dense_split(a, &b, st) : launch<BACKWARD>(a, &b, st);
 }
 
 }  // namespace la

@@ -286,11 +286,15 @@ struct DenseArgs {
     int half, act;
     int beside;  // two kernels of one call side by side: 1, another follows; 2, this is the other (set by launch_dense)
     int places;  // blocks that there is room for (0: the whole GPU)
+    float *partial;  // DENSE_DW: dense_dw_partial_bytes(...) bytes, or null
+    int split;       // DENSE_DW: parts of the sum that go there and are joined (set by the launch; 0 or 1: none)
     int *status;
     uint64_t wait_ns;  // limit of the kernel's bounded waits (0: the 2 s default)
     int debug_stall;   // test knob: one wait on a barrier that nothing completes
 };
 cudaError_t launch_dense(const DenseArgs &a, cudaStream_t st);
+// What DENSE_DW's partial sums may take: `rows` summed, `count` outputs [M][N], next to DENSE_DX or not.
+size_t dense_dw_partial_bytes(int rows, int M, int N, int count);
 // DENSE_DX and DENSE_DW of one backward pass (status, waits and knob: dx's).
 cudaError_t launch_dense_pair(const DenseArgs &dx, const DenseArgs &dw, cudaStream_t st);
 // Those with few output tiles: the summed index split over a cluster's blocks (dense_split.cu).

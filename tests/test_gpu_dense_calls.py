@@ -95,6 +95,27 @@ def test_a_few_rows_past_whole_tiles(cuda, m, n, k):
     assert la.device_status() == 0
 
 
+@pytest.mark.parametrize("m,n,k", [(16384, 520, 392), (30001, 257, 264), (8192, 256, 256), (12000, 1001, 513), (40000, 8, 72)])
+def test_long_sums_of_small_weights(cuda, m, n, k):
+    """dw's sum over many rows in parts that are joined, next to dx and alone, the same bits each time; the workspace
+    starts as NaN and what the parts do not reach is not read."""
+    c = case(cuda, m, n, k, m)
+    check_linear(c, "gelu")
+    check_gated(gated_case(cuda, m, n, k, m + 1), "silu")
+    nan = lambda b: torch.full((b // 4 + 4,), float("nan"), device=cuda).view(torch.uint8)  # noqa: E731
+    ref = c["dy"].double().T @ c["x"].double()
+    mag = c["dy"].double().abs().T @ c["x"].double().abs()
+    got = []
+    for dx in (None, c["dx"], None):
+        c["dw"].fill_(7.0)
+        la.linear_backward(c["x"], c["w"], None, c["dy"], dx, c["dw"], workspace=nan(la.linear_backward_workspace_bytes(m, n, k)))
+        # sums of m terms in parts of at least 512, each in fp32: (m / 8) 2^-24 of the terms is far more than their order adds
+        close(c["dw"], ref, U * ref.abs() + max(64, m / 8) * F32 * mag, "dw")
+        got.append(c["dw"].clone())
+    assert torch.equal(got[0], got[2])
+    assert la.device_status() == 0
+
+
 def test_far_strides(cuda):
     """Rows 2^31 values apart: offsets pass 32 bits in x, residual and y, in dy and dx, and in a norm's rows."""
     g = torch.Generator().manual_seed(1)
