@@ -20,7 +20,8 @@
 //    shared memory so that whole 128-byte lines go to memory.
 // Tiles are walked in bands of eight rows of tiles; those of a round that would leave half the pairs without any are cut
 // in halves of 128 columns (512 x 4096 x 4096: 24.5 -> 20.5 us, 1024 x 2048 x 2048: 15.9 -> 13.0). DX and DW of one backward pass are one launch, the tiles with
-// the longer sums first: two launches would each leave SMs idle in their last round.
+// the longer sums first: two launches would each leave SMs idle in their last round. A long sum of few tiles of DW is cut
+// in parts, which go to the workspace in fp32 and are joined in their order.
 // 8192 x 8192 x 2048 takes 146 us (1.88 PFLOP/s, tensor pipe 95% in the backward pass, 81% where an epilogue keeps z or gate
 // and up); back to back, large products are held at 1.6 to 1.75 PFLOP/s by the power limit.
 // Every wait is bounded; on a timeout the blocks raise LA_DEV_TIMEOUT, stop issuing, let what is under way end,
@@ -597,7 +598,8 @@ DenseArgs rows_from(const DenseArgs &a, int row) {
 }  // namespace
 
 // Parts of dW's long sum. Few tiles of many rows' sums (16384 rows, 1024 x 1024: 16 tiles of 256 stages) would keep few
-// pairs busy; parts of them are units of their own, as many as make the sum of the model's times the least.
+// pairs busy; parts of them are units of their own, as many as make the model's time the least. (dx and dw of 16384 rows,
+// 1024 x 1024: 64.4 us in one part, 52.6 so; 8192 rows, 1000 x 1000: 55.9 and 42.8; dw of 65,536 rows: 115.9 and 83.4.)
 namespace {
 
 int choose_dw_split(const DenseArgs &dw, const DenseArgs *dx) {
