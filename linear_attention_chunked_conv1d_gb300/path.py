@@ -405,8 +405,8 @@ class FeedForward:
         (F, D), dev, bf16 = w_gate.shape, w_gate.device, torch.bfloat16
         for name, w, shape in (("norm_w", norm_w, (D,)), ("norm_b", norm_b, (D,)), ("w_gate", w_gate, (F, D)),
                                ("w_up", w_up, (F, D)), ("w_down", w_down, (D, F))):
-            if w is not None and (tuple(w.shape) != shape or w.dtype != bf16 or w.device != dev):
-                raise ValueError(f"{name}: {tuple(w.shape)} {w.dtype} on {w.device}, expected {shape} {bf16} on {dev}")
+            if w is not None:
+                _fits(name, w, shape, bf16, dev, rows=len(shape) == 2)
         matrix = lambda r, c: torch.empty(r, (c + 7) // 8 * 8, dtype=bf16, device=dev)[:, :c]  # noqa: E731
         room = lambda n: torch.empty(n, dtype=torch.uint8, device=dev)  # noqa: E731
         self.normed, self.h, self.y = matrix(rows, D), matrix(rows, F), matrix(rows, D)

@@ -461,8 +461,11 @@ def test_feed_forward_rows_one_by_one(cuda):
 
 def test_feed_forward_refusals(cuda):
     w = lambda *s: torch.zeros(*s, dtype=BF16, device=cuda)  # noqa: E731
-    with pytest.raises(ValueError, match="w_down"):
-        FeedForward(4, w(64), None, w(128, 64), w(128, 64), w(128, 64))
+    for name, bad in (("w_down", dict(w_down=w(128, 64))), ("w_up", dict(w_up=w(128, 64).float())), ("w_gate", dict(w_gate=w(64, 128).t())),
+                      ("w_gate", dict(w_gate=w(128, 67)[:, :64])), ("norm_w", dict(norm_w=w(128)[::2])), ("norm_b", dict(norm_b=w(65)[1:])),
+                      ("w_up", dict(w_up=torch.zeros(128, 64, dtype=BF16)))):
+        with pytest.raises(ValueError, match=name):
+            FeedForward(4, **(dict(norm_w=w(64), norm_b=None, w_gate=w(128, 64), w_up=w(128, 64), w_down=w(64, 128)) | bad))
     block = FeedForward(4, w(64), None, w(128, 64), w(128, 64), w(64, 128))
     with pytest.raises(RuntimeError, match="train"):
         block.backward(w(4, 64))
