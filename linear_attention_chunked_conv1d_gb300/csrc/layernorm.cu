@@ -475,7 +475,7 @@ cudaError_t launch_layernorm(const LayerNormArgs &a, cudaStream_t st) {
 cudaError_t launch_layernorm_backward(const LayerNormBwdArgs &a, cudaStream_t st) {
     return a.dtype == LA_BF16 ? backward<__nv_bfloat16>(a, st) : backward<float>(a, st);
 }
-int layernorm_max_width() { return 8192; }  // the backward pass: 256 threads of 32 columns
+int layernorm_max_width() { return 8192; }  // the backward pass: 512 threads of 16 columns
 size_t layernorm_backward_workspace_bytes(int rows, int width, int) {
     return (size_t)(rows < MOST_BLOCKS ? rows : MOST_BLOCKS) * 2 * width * sizeof(float);
 }
