@@ -249,6 +249,11 @@ int w4_common(const void *q, const void *scales, int K, int group) {
 // Columns of a buffer that the dense calls keep between forward and backward pass: whole 16 bytes of bf16.
 int64_t whole8(int n) { return ((int64_t)n + 7) / 8 * 8; }
 size_t whole16(size_t bytes) { return (bytes + 15) / 16 * 16; }
+// gate | up, the gated block's products, as its buffers hold them: [M][2 whole8(F)]. The kept buffer has their upper 16 bits
+// in one plane and the next eight in another, right behind it; the workspace of the backward pass begins with their gradients.
+// Rows times columns pass 32 bits.
+size_t gated_values(int M, int F) { return (size_t)M * 2 * whole8(F); }
+size_t gated_lower_at(int M, int F) { return 2 * gated_values(M, F); }
 // Where in a workspace, from `used` bytes on, dW's partial sums lie; null where there are none.
 float *dw_partial(void *workspace, size_t used, size_t bytes) {
     return bytes > used ? reinterpret_cast<float *>(static_cast<char *>(workspace) + used) : nullptr;
@@ -1146,7 +1151,7 @@ int la_linear_backward(const void *x, const void *w, const void *saved, size_t s
 
 size_t la_gated_ffn_saved_bytes(int M, int F) {
     if (M < 1 || F < 1) return 0;
-    return 6 * (size_t)M * whole8(F);
+    return 3 * gated_values(M, F);
 }
 
 int la_gated_ffn(const void *x, const void *w_gate, const void *w_up, void *h, void *saved, size_t saved_bytes, int M,
@@ -1168,13 +1173,13 @@ int la_gated_ffn(const void *x, const void *w_gate, const void *w_up, void *h, v
     a.kind = la::DENSE_GATED; a.count = 1;
     a.a[0] = x; a.lda[0] = ldx; a.b[0] = w_gate; a.ldb[0] = ldwg; a.b[1] = w_up; a.ldb[1] = ldwu; a.out[0] = h; a.ldo[0] = ldh;
     a.M = M; a.N = F; a.K = K; a.half = (int)whole8(F); a.lds = 2 * whole8(F); a.act = act;
-    a.saved = saved; a.lower = saved ? static_cast<char *>(saved) + 2 * M * a.lds : nullptr;
+    a.saved = saved; a.lower = saved ? static_cast<char *>(saved) + gated_lower_at(M, F) : nullptr;
     LA_TRY(dense_status(&a));
     return launch_result([&] { return la::launch_dense(a, as_stream(stream)); }, "gated ffn launch");
 }
 
 size_t la_gated_ffn_backward_workspace_bytes(int M, int F, int K) {
-    return M < 1 || F < 1 || K < 1 ? 0 : 4 * (size_t)M * whole8(F) + la::dense_dw_partial_bytes(M, F, K, 2);
+    return M < 1 || F < 1 || K < 1 ? 0 : 2 * gated_values(M, F) + la::dense_dw_partial_bytes(M, F, K, 2);
 }
 
 int la_gated_ffn_backward(const void *x, const void *w_gate, const void *w_up, const void *saved, size_t saved_bytes,
@@ -1212,14 +1217,14 @@ int la_gated_ffn_backward(const void *x, const void *w_gate, const void *w_up, c
     LA_TRY(dense_status(&a));
     return launch_result([&] {
         const int64_t half = whole8(F);
-        la::GatedGradArgs g{saved, dh, workspace, M, F, (int)half, lddh, act};
+        la::GatedGradArgs g{saved, static_cast<const char *>(saved) + gated_lower_at(M, F), dh, workspace, M, F, (int)half, lddh, act};
         cudaError_t e = la::launch_gated_grad(g, as_stream(stream));
         if (e != cudaSuccess) return e;
         for (int i = 0; i < 2; ++i) {
             a.a[i] = static_cast<const char *>(workspace) + i * half * 2;
             a.lda[i] = 2 * half;
         }
-        a.partial = dw_partial(workspace, 4 * (size_t)M * half, need);
+        a.partial = dw_partial(workspace, 2 * gated_values(M, F), need);
         return launch_backward_products(a, w_gate, ldwg, w_up, ldwu, dx, lddx, x, ldx, dw_gate, lddwg, dw_up, lddwu, M, F, K,
                                         as_stream(stream));
     }, "gated ffn backward launch");

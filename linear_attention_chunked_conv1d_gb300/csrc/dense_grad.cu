@@ -102,12 +102,11 @@ bias_sum_kernel(const float *__restrict__ partial, int runs, int N, bf16 *__rest
 
 // d: [M][2 * half], gate in columns 0.., up from column half on; saved: the same in 24 bits, one plane of 16 and one of 8.
 __global__ void __launch_bounds__(256)
-gated_grad_kernel(const uint8_t *__restrict__ saved, const bf16 *__restrict__ dh, bf16 *__restrict__ d, int M, int F,
-                  int half, int64_t lddh, int act) {
+gated_grad_kernel(const uint8_t *__restrict__ saved, const uint8_t *__restrict__ lower, const bf16 *__restrict__ dh,
+                  bf16 *__restrict__ d, int M, int F, int half, int64_t lddh, int act) {
     wait_for_previous();
     const int c = (blockIdx.x * 32 + threadIdx.x) * 8;
     if (c >= F) return;
-    const uint8_t *lower = saved + (int64_t)M * 4 * half;
     for (int64_t r = blockIdx.y * 8 + threadIdx.y; r < M; r += (int64_t)gridDim.y * 8) {
         float gate[8], up[8], g[8], slope[8];
         const int64_t at = r * 2 * half + c;  // whole pieces: the buffers' rows are
@@ -151,7 +150,7 @@ cudaError_t launch_linear_grad(const LinearGradArgs &a, cudaStream_t st) {
 
 cudaError_t launch_gated_grad(const GatedGradArgs &a, cudaStream_t st) {
     return launch_overlapped(gated_grad_kernel, dim3((a.F + COLS - 1) / COLS, row_runs(a.M, a.F, 6)), dim3(32, 8), 0, 0, st,
-                             (const uint8_t *)a.saved, (const bf16 *)a.dh, (bf16 *)a.d, a.M, a.F, a.half, a.lddh, a.act);
+                             (const uint8_t *)a.saved, (const uint8_t *)a.lower, (const bf16 *)a.dh, (bf16 *)a.d, a.M, a.F, a.half, a.lddh, a.act);
 }
 
 }  // namespace la

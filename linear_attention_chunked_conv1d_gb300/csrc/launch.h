@@ -317,7 +317,7 @@ size_t linear_backward_partial_bytes(int M, int N);
 cudaError_t launch_linear_grad(const LinearGradArgs &a, cudaStream_t st);
 // d [M][2 half] = dh up act'(gate) | dh act(gate) from saved (as DENSE_GATED leaves it).
 struct GatedGradArgs {
-    const void *saved, *dh;
+    const void *saved, *lower, *dh;  // lower: the plane of eight bits
     void *d;
     int M, F, half;
     int64_t lddh;
