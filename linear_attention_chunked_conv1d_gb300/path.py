@@ -270,6 +270,19 @@ def _fits(name, t, shape, dtype, dev, *, rows=False):
                          f"{'rows' if rows else 'values'} on 16-byte boundaries")
 
 
+def _span(t):
+    """The addresses from a tensor's first byte to its end."""
+    return t.data_ptr(), t.data_ptr() + (sum((n - 1) * s for n, s in zip(t.shape, t.stride())) + 1) * t.element_size()
+
+
+def _apart(name, t, spans):
+    """Refuses a tensor that shares memory with buffers (their _span) that are written while it is still needed."""
+    first, end = _span(t)
+    for b, e in spans:
+        if first < e and b < end:
+            raise ValueError(f"{name} shares memory with a buffer of the object's own that is written before {name} was last read")
+
+
 class GatedPass:
     """Repeated passes of a gated recurrent layer (one state per channel) over one packed batch:
     conv1d + SiLU over the carried windows, then the gated scan from the carried states.
@@ -397,7 +410,9 @@ class FeedForward:
     norm_w, norm_b [D] (norm_b may be None), w_gate and w_up [F][D], w_down [D][F]: bf16. forward(x) takes
     x [rows][D] and returns y; with train=True it also keeps what backward(dy) needs (x itself has to
     stay as it is until then), which returns the gradients by name: x, norm_w and norm_b (fp32), w_gate,
-    w_up and w_down. Outputs and gradients are the object's own tensors, written again by the next call."""
+    w_up and w_down. Outputs and gradients are the object's own tensors, written again by the next call.
+    x may be y without train, and dy x's gradient; any tensor of the object's own that it writes while it
+    still has to read x or dy is refused in their places."""
 
     def __init__(self, rows, norm_w, norm_b, w_gate, w_up, w_down, *, act="silu", eps=1e-5, train=False):
         self.act, self.eps, self.train = act, eps, train
@@ -411,6 +426,9 @@ class FeedForward:
         room = lambda n: torch.empty(n, dtype=torch.uint8, device=dev)  # noqa: E731
         self.normed, self.h, self.y = matrix(rows, D), matrix(rows, F), matrix(rows, D)
         self.x = self.stats = self.saved = None
+        # what is written before x (with train: in backward()) and dy are read for the last time; the norm may write x's
+        # gradient in dy's place, and linear y in x's
+        self.before_x, self.before_dy = [_span(self.normed), _span(self.h)], []
         if train:
             self.stats = torch.empty(rows, 2, device=dev)
             self.saved = room(gated_ffn_saved_bytes(rows, F))
@@ -421,8 +439,12 @@ class FeedForward:
             self.workspace = room(max(layernorm_rows_backward_workspace_bytes(rows, D, bf16),
                                       gated_ffn_backward_workspace_bytes(rows, F, D),
                                       linear_backward_workspace_bytes(rows, D, F)))
+            self.before_dy = [_span(t) for t in (self.dh, self.dnormed, self.workspace, *self.grads.values())
+                              if t is not None and t is not self.grads["x"]]
+            self.before_x += [_span(t) for t in (self.y, self.stats, self.saved, self.grads["x"])] + self.before_dy
 
     def forward(self, x, stream=None):
+        _apart("x", x, self.before_x)
         layernorm_rows(x, self.norm_w, self.norm_b, self.normed, stats=self.stats, eps=self.eps, stream=stream)
         gated_ffn(self.normed, self.w_gate, self.w_up, self.h, act=self.act, saved=self.saved, stream=stream)
         linear(self.h, self.w_down, self.y, residual=x, stream=stream)
@@ -436,6 +458,7 @@ class FeedForward:
         if self.x is None:
             raise RuntimeError("backward() needs a forward() before it")
         g, ws = self.grads, self.workspace
+        _apart("dy", dy, self.before_dy)
         linear_backward(self.h, self.w_down, None, dy, self.dh, g["w_down"], workspace=ws, stream=stream)
         gated_ffn_backward(self.normed, self.w_gate, self.w_up, self.saved, self.dh, self.dnormed, g["w_gate"],
                            g["w_up"], act=self.act, workspace=ws, stream=stream)
