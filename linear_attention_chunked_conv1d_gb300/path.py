@@ -445,6 +445,7 @@ class FeedForward:
 
     def forward(self, x, stream=None):
         _apart("x", x, self.before_x)
+        self.x = None  # a call that is refused on the way leaves buffers of two passes
         layernorm_rows(x, self.norm_w, self.norm_b, self.normed, stats=self.stats, eps=self.eps, stream=stream)
         gated_ffn(self.normed, self.w_gate, self.w_up, self.h, act=self.act, saved=self.saved, stream=stream)
         linear(self.h, self.w_down, self.y, residual=x, stream=stream)
@@ -456,7 +457,7 @@ class FeedForward:
         if not self.train:
             raise RuntimeError("backward() needs FeedForward(..., train=True)")
         if self.x is None:
-            raise RuntimeError("backward() needs a forward() before it")
+            raise RuntimeError("backward() needs a forward() before it that went through")
         g, ws = self.grads, self.workspace
         _apart("dy", dy, self.before_dy)
         linear_backward(self.h, self.w_down, None, dy, self.dh, g["w_down"], workspace=ws, stream=stream)

@@ -64,6 +64,28 @@ def test_dy_is_not_written_before_it_was_last_read(calls):
     q.backward(torch.zeros(ROWS, D, dtype=BF))
 
 
+@pytest.mark.parametrize("refused", KERNELS[:3])
+def test_backward_after_a_forward_that_was_refused(calls, monkeypatch, refused):
+    """The calls before the refused one have written over what the last whole pass kept: its gradients cannot be had."""
+    t, x = block(True), torch.zeros(ROWS, D, dtype=BF)
+    t.forward(x)
+    t.backward(x.clone())
+
+    def refuse(*a, **k):
+        raise ValueError("refused")
+    with monkeypatch.context() as m:
+        m.setattr(path, refused, refuse)
+        with pytest.raises(ValueError, match="refused"):
+            t.forward(torch.ones(ROWS, D, dtype=BF))
+    del calls[:]
+    with pytest.raises(RuntimeError, match="forward"):
+        t.backward(x.clone())
+    assert not calls
+    t.forward(x)
+    t.backward(x.clone())
+    assert calls == list(KERNELS)
+
+
 @pytest.mark.gpu
 def test_the_places_that_are_taken_give_the_same_bits(cuda):
     """x in y's place without train, and dy in the place of x's gradient, as with tensors of their own."""
