@@ -126,7 +126,8 @@ dense_split_kernel(const __grid_constant__ Maps maps0, const __grid_constant__ M
     __syncthreads();
     tc::fence_after_sync();
     launch_next();
-    if (beside != 2) wait_for_previous();  // else the kernel ahead has waited, and this one's rows are not that one's
+    if (beside == 2) start_beside();  // the kernel ahead has waited, and this one's rows are not that one's
+    else wait_for_previous();
     const uint32_t tm = *tmem_sh;
     const uint32_t rbase = tc::smem_u32(ring);
     const int nr = (int)(M - r0 < (int64_t)rows ? M - r0 : rows);  // the tile's rows, and those that this block finishes
@@ -135,6 +136,7 @@ dense_split_kernel(const __grid_constant__ Maps maps0, const __grid_constant__ M
     if (warp == 0) {
         if (tc::elect_one()) {
             uint32_t s = 0, ph = 0, issued = 0;
+            if (beside == 2) beside_tma();
             for (int64_t k = k_first; k < k_end; ++k) {
                 if (!tc::mbar_wait(empty + s, ph ^ 1u, wait_ns, SLEEP_NS) || *err) {
                     *err = 1;
@@ -268,7 +270,7 @@ dense_split_kernel(const __grid_constant__ Maps maps0, const __grid_constant__ M
         }
     }
     if (split > 1) tc::cluster_sync();  // the others have read this block's part
-    if (beside == 2) wait_for_previous();  // who waits for this kernel waits for the one ahead too
+    if (beside == 2) end_beside();
     if (*err && threadIdx.x == 0) raise_status(status, LA_DEV_TIMEOUT);
 }
 

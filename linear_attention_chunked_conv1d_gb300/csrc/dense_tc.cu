@@ -234,8 +234,8 @@ dense_kernel(const __grid_constant__ Maps maps0, const __grid_constant__ Maps ma
     __syncthreads();
     tc::cluster_sync();
     tc::fence_after_sync();
-    wait_for_previous();
-    if (beside) launch_next();  // what came before is complete: the call's other kernel need not wait for it
+    if (beside) wait_and_let_beside();  // the call's other kernel, beside this one's last round
+    else wait_for_previous();
     const uint32_t tm = *tmem_sh;
     const int64_t first = blockIdx.x / 2, step = gridDim.x / 2;
     // Every round but the first goes to the pairs from the last to the first: where the first pairs had the longer sums,
