@@ -25,9 +25,10 @@ __device__ __forceinline__ uint64_t logistic2(uint64_t y) {
     return each(add2(e, both(1.f)), [](float t) { return rcp_approx(t); });
 }
 // Phi(z), the normal distribution function, and e = exp(-z^2 / 2). For z < 0 it is erfc(x) / 2 with x = |z| / sqrt 2 and
-// erfc(x) = e^(-x^2) t Q(t), t = 1 / (1 + 0.375 x), Q the polynomial of degree 6 whose largest relative error over
-// 0 <= x <= 10 is the least, 6.2e-7 (a linear program over 400 Chebyshev points). So the left tail keeps its
-// relative accuracy: within 8e-6 to z = -12, all of it from rounding z^2. (8192 x 8192 outputs of 2048 summed indexes with
+// erfc(x) = e^(-x^2) t Q(t), t = 1 / (1 + 0.375 x), Q a polynomial of degree 6 fitted by a linear program to the least
+// relative error at 400 Chebyshev points of 0 <= x <= 10. Its largest relative error over that range is 6.8e-7 (6.2e-7 at
+// the points themselves), 1.1e-6 with t and Q in fp32. So the left tail keeps its relative accuracy: within 8e-6 to
+// z = -12, most of it from rounding z^2. (8192 x 8192 outputs of 2048 summed indexes with
 // bias, GELU and residual: 228 us with erfcf, 210 with this, value by value; 169 with a thread's values side by side.)
 __device__ __forceinline__ uint64_t normal2(uint64_t z, uint64_t &e) {
     e = each(mul2(mul2(z, both(-0.5f * kLog2e)), z), [](float t) { return ex2_approx(t); });
