@@ -535,7 +535,8 @@ int la_linear(const void *x, const void *w, const void *bias, const void *residu
  * dy [M][lddy], dx [M][lddx], dw [N][lddw], dbias [N]: bf16. dx, dw and dbias may each be NULL, not all.
  * dz is rounded to bf16 where it enters the two products (it is the tensor cores' operand), not where it
  * is summed to dbias; dx, dw and dbias are summed in fp32 and rounded once.
- * workspace  la_linear_backward_workspace_bytes(...) bytes (16-byte aligned; may be NULL when that is 0). */
+ * workspace  la_linear_backward_workspace_bytes(...) bytes (16-byte aligned): never 0, and wanted whichever gradients
+ *         are asked for, so that one buffer serves all of a program's calls of these sizes. */
 size_t la_linear_backward_workspace_bytes(int M, int N, int K, int act);
 int la_linear_backward(const void *x, const void *w, const void *saved, size_t saved_bytes,
                        const void *dy, void *dx, void *dw, void *dbias, int M, int N, int K,

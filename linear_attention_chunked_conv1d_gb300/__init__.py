@@ -885,7 +885,7 @@ def linear(x, w, y=None, *, bias=None, residual=None, act="none", saved=None, st
 
 
 def linear_backward_workspace_bytes(rows, outputs, inputs, act="none") -> int:
-    """Bytes of workspace that linear_backward needs."""
+    """Bytes of workspace that linear_backward needs, whichever gradients it is asked for (never 0)."""
     return int(_load().la_linear_backward_workspace_bytes(rows, outputs, inputs, _act_code(act)))
 
 
@@ -893,7 +893,7 @@ def linear_backward(x, w, saved, dy, dx=None, dw=None, *, dbias=None, act="none"
                     stream=None) -> None:
     """Gradients of linear: dx [M][K], dw [N][K] and dbias [N] (bf16; those that are given) from dy
     [M][N]; the residual's is dy itself. x, w, saved (None without an activation) and act are those of
-    the forward call."""
+    the forward call. workspace: a buffer of linear_backward_workspace_bytes(...), which every call needs."""
     dev, bf16 = x.get_device(), _BF16
     M, K = x.shape
     N = w.shape[0]
