@@ -288,10 +288,14 @@ Job make_job(const DenseArgs &a) {
 }
 int64_t stages_of(const Job &j) { return (int64_t)((j.K + TK - 1) / TK) * j.parts; }
 
+// Never launched: what the runtime is asked about in place of the kernels above, of which it counts one block an SM, as they
+// take tensor memory. Two are there: 128 of 512 columns, 128 registers for each of 256 threads and 112 KB leave room for both.
+__global__ void __launch_bounds__(THREADS, 2) places_kernel() {}
+
 // Clusters of s blocks (2..8) that are resident at one time: the SMs of a GPC hold whole clusters only, so some sizes leave
-// many places empty. The runtime's answer counts a block an SM (15 clusters of 7 or 8, 23 of 6, 28, 36, 46, 76 of 2); two
-// are there (40 clusters of 7 take two rounds, 13.5 us for 8.7 in clusters of 6; 32 of 8 and 94 of 3 take one, so a little
-// more than twice the answer fits). Looked up once a device (the three kernels take the same room).
+// many places empty (36 clusters of 8, 38 of 7, 46 of 6, 58, 74, 97, 152 of 2). One more takes another round: 49 tiles of one row,
+// 2048 summed, 12.3 us in clusters of 6 and 7.8 of 5; 59 tiles 13.7 of 5 and 8.8 of 4; 75 tiles 16.6 of 4 and 10.6 of 3; 98
+// tiles 18.4 of 3 and 13.3 of 2. Looked up once a device.
 int resident_clusters(int s) {
     static std::atomic<int> known[64][9];
     int dev = 0, n = 0;
@@ -308,10 +312,9 @@ int resident_clusters(int s) {
     cfg.dynamicSmemBytes = ROOM + 2048;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    if (cudaFuncSetAttribute(dense_split_kernel<LINEAR>, cudaFuncAttributeMaxDynamicSharedMemorySize, ROOM + 2048) != cudaSuccess ||
-        cudaOccupancyMaxActiveClusters(&n, dense_split_kernel<LINEAR>, &cfg) != cudaSuccess || n < 1)
+    if (cudaFuncSetAttribute(places_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, ROOM + 2048) != cudaSuccess ||
+        cudaOccupancyMaxActiveClusters(&n, places_kernel, &cfg) != cudaSuccess || n < 1)
         return PLACES / s;
-    n = n * 2 * 107 / 100;
     known[dev][s].store(n, std::memory_order_relaxed);
     return n;
 }
