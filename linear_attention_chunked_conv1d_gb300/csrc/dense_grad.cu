@@ -129,7 +129,7 @@ gated_grad_kernel(const uint8_t *__restrict__ saved, const uint8_t *__restrict__
 // Rows are shared out so that the grid has `held` blocks for each SM, or 64 rows a block where that is fewer.
 int row_runs(int M, int N, int held) {
     const int cols = (N + COLS - 1) / COLS, most = (int)(((int64_t)M + 8 * WARPS - 1) / (8 * WARPS));
-    const int runs = 152 * held / cols < 1 ? 1 : 152 * held / cols;
+    const int runs = SMS * held / cols < 1 ? 1 : SMS * held / cols;
     return runs < most ? runs : most;
 }
 

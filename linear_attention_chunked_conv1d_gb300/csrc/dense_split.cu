@@ -275,7 +275,7 @@ dense_split_kernel(const __grid_constant__ Maps maps0, const __grid_constant__ M
 }
 
 constexpr uint32_t ROOM = 110 * 1024;  // a block's ring: two blocks fit an SM
-constexpr int PLACES = 304;
+constexpr int PLACES = 2 * SMS;
 
 Job make_job(const DenseArgs &a) {
     const int64_t out = a.kind == DENSE_GATED ? PT / 2 : PT;
@@ -386,7 +386,7 @@ double dense_pairs_us(const DenseArgs &a, const DenseArgs *b) {
     };
     auto time = [&](const DenseArgs &q) { return fmax(0.29 * ceil(ceil(q.K / 64.) / parts(q)) * (q.kind == DENSE_DX ? q.count : 1), 3.2); };
     auto join = [&](const DenseArgs &q) { return parts(q) > 1 ? 4 + parts(q) * q.count * q.M * (double)q.N * (8 / 4e6) : 0; };
-    return fmax(5 + rounds(time(a), tiles(a), b ? time(*b) : 0, b ? tiles(*b) : 0, 76, 0.7),
+    return fmax(5 + rounds(time(a), tiles(a), b ? time(*b) : 0, b ? tiles(*b) : 0, PAIRS, 0.7),
                 7 + memory_us(a) + (b ? memory_us(*b) : 0)) + join(a) + (b ? join(*b) : 0);
 }
 double dense_split_us(const DenseArgs &a, const DenseArgs *b) {

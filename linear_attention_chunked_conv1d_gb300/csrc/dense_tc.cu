@@ -561,7 +561,7 @@ cudaError_t launch(const DenseArgs &a, const DenseArgs *b, cudaStream_t st) {
     const DenseArgs &w = b && b->split > 1 ? *b : a;
     if (e != cudaSuccess || w.split <= 1) return e;
     const Epilogue ep = make_epilogue(w);
-    const int cols = (w.N + 255) / 256, runs = (w.M + 7) / 8, most = 152 * 6 / cols < 1 ? 1 : 152 * 6 / cols;
+    const int cols = (w.N + 255) / 256, runs = (w.M + 7) / 8, most = SMS * 6 / cols < 1 ? 1 : SMS * 6 / cols;
     for (int o = 0; o < w.count; ++o) {
         const cudaError_t j = launch_overlapped(dense_join_kernel, dim3(cols, runs < most ? runs : most), dim3(32, 8), 0, 0, st,
                                                 (const float *)(ep.partial + (int64_t)o * w.split * w.M * ep.ldp), ep.out[o], w.M, w.N,
@@ -639,7 +639,7 @@ cudaError_t launch_dense(const DenseArgs &args, cudaStream_t st) {
     if (a.kind != DENSE_DW && a.M > TM && rest && rest <= 64) {
         DenseArgs main = a, other = rows_from(a, a.M - rest);
         main.M = a.M - rest;
-        const int64_t last = make_job(main).tiles % 76, idle = last ? 76 - (2 * last <= 76 ? 2 * last : last) : 0;
+        const int64_t last = make_job(main).tiles % PAIRS, idle = last ? PAIRS - (2 * last <= PAIRS ? 2 * last : last) : 0;
         other.places = (int)idle * 4;
         // the other kernel starts some 4 us after this one
         if (idle >= 8 && fmax(dense_pairs_us(main, nullptr) + 1.5, 4 + dense_split_us(other, nullptr)) + 2 < fmin(pairs, split)) {

@@ -241,6 +241,11 @@ struct W4QuantArgs {
 };
 cudaError_t launch_w4_quantize(const W4QuantArgs &a, cudaStream_t st);
 
+// The GB300's SMs, and the pairs of them that dense_tc.cu's blocks take: for the rules that choose a kernel, a tile's cut or
+// the blocks of a sum, which are fitted to this chip. What a launch relies on (blocks that are resident at one time) is
+// asked of the runtime.
+constexpr int SMS = 152, PAIRS = SMS / 2;
+
 // Layer norm of rows (layernorm.cu): y = (x - mean) rstd w + b, stats [rows][2] = mean, rstd (or null).
 struct LayerNormArgs {
     const void *x, *w, *b;

@@ -380,7 +380,7 @@ cudaError_t with_backward_shape(int width, F &&f) {
 //    to no SM idle (16384 x 4096 bf16: 80 us without clusters, 74 with; 32768 x 2048, 10 MB: 78 and 80; fp32 16384 x 4096,
 //    where clusters find 288 places of 304: 124 and 137);
 //  - by the second launch alone.
-constexpr int MOST_BLOCKS = 152 * 4, BIG_CLUSTER = 4;
+constexpr int MOST_BLOCKS = SMS * 4, BIG_CLUSTER = 4;
 constexpr size_t CLUSTER_BYTES = 12 << 20;
 
 struct Resident {
