@@ -503,7 +503,8 @@ int la_layernorm_rows(const void *x, const void *w, const void *b, void *y, floa
  * x, w, stats  as the forward call had them and left them.
  * dy, dx  [rows][lddy], [rows][lddx] (dtype). dx may be dy or dskip itself, at the same stride.
  * dskip   [rows][ldskip] (dtype), a gradient that reaches x past the norm, or NULL.
- * dw, db  fp32 [width] (16-byte aligned); db may be NULL.
+ * dw, db  fp32 [width] (16-byte aligned); db may be NULL. Sums in fp32, in a thread one row after another, then over threads
+ *         and blocks (held by tests to 64 x 2^-24 of the sum of their absolute terms).
  * workspace  la_layernorm_rows_backward_workspace_bytes(...) bytes (16-byte aligned). */
 size_t la_layernorm_rows_backward_workspace_bytes(int rows, int width, int dtype);
 int la_layernorm_rows_backward(const void *x, const void *w, const float *stats, const void *dy,

@@ -7,7 +7,9 @@
 //    out in its shared memory, and each adds up a share of the rows over the cluster through distributed shared
 //    memory, in the blocks' order, with the epilogue;
 //  - two blocks fit an SM, so that one's copies run under the other's prologue and epilogue.
-// 1 x 8192 x 2048 takes 9.4 us in a row of calls (33.6 MB; 2.8 of them launching 256 blocks, 1.6 the cluster's sums),
+// 1 x 8192 x 2048 takes 9.3 us in a row of calls (33.6 MB; alone, the last of 256 blocks starts 1.3 us after the first, and
+// of a block's time 1.0 are its barriers and tensor memory, 2.3 its first copy, 3.2 the way from there to its last MMA, 1.4 the
+// cluster's meeting, 1.3 the sums and its leave),
 // gated 32 x 8192 x 4096 25 us (5.4 TB/s), gated 1 x 16384 x 4096 42 us (6.3 TB/s).
 // Operands as in dense_tc.cu, with the roles of rows and columns exchanged.
 #include <cuda.h>
