@@ -23,7 +23,7 @@ BF16 = torch.bfloat16
 
 
 def act64(z, act):
-    return {"none": lambda: z, "relu": lambda: torch.clamp_min(z, 0), "silu": lambda: z * torch.sigmoid(z),
+    return {"none": lambda: z, "relu": lambda: torch.relu(z), "silu": lambda: z * torch.sigmoid(z),
             "gelu": lambda: 0.5 * z * torch.erfc(-z / math.sqrt(2)),
             "gelu_tanh": lambda: z * torch.sigmoid(2 * math.sqrt(2 / math.pi) * (z + 0.044715 * z ** 3))}[act]()
 
