@@ -1,6 +1,6 @@
 // The dense calls of the C ABI with their launches replaced (the linker's --wrap): prints where in the buffers of a
 // call the kernels would be sent. Host only: the addresses are made up, nothing is launched or dereferenced.
-//   driver M F   ->  gated block: bytes from `saved` to the lower plane that the forward call would write, and to the
+//   places M F   ->  gated block: bytes from `saved` to the lower plane that the forward call would write, and to the
 //                    one that the backward call would read
 #include <cstdio>
 #include <cstdlib>
