@@ -1028,7 +1028,7 @@ def gated_ffn_backward(x, w_gate, w_up, saved, dh, dx=None, dw_gate=None, dw_up=
         x.data_ptr(), w_gate.data_ptr(), w_up.data_ptr(), None if saved is None else saved.data_ptr(),
         0 if saved is None else saved.numel() * saved.element_size(), dh.data_ptr(), None if dx is None else dx.data_ptr(),
         None if dw_gate is None else dw_gate.data_ptr(), None if dw_up is None else dw_up.data_ptr(), M, F, K, xs, gs, us, hs,
-        ds, dgs, dus, _act_code(act), None if workspace is None else workspace.data_ptr(),
+        ds, dgs, dus, code, None if workspace is None else workspace.data_ptr(),
         0 if workspace is None else workspace.numel() * workspace.element_size(),
         _current_stream(dev) if stream is None and _current_stream is not None else _stream(stream))
     if rc:

@@ -16,6 +16,8 @@ def places(built_lib, tmp_path_factory):
     from linear_attention_chunked_conv1d_gb300 import build
     out = str(tmp_path_factory.mktemp("dense_args") / "places")
     objects = [os.path.join(build.BUILD_DIR, os.path.basename(s)[:-3] + ".o") for s in build.sources()]
+    if not all(os.path.exists(o) for o in objects):  # of a library that was built elsewhere
+        build.build(force=True)
     subprocess.run([build._nvcc(), *build.ARCH, "-std=c++17", "-I", build.INCLUDE, "-I", build.CSRC, "-o", out,
                     os.path.join(HERE, "dense_args", "places.cu"), *objects, "-lcudart_static",
                     *[a for w in WRAPPED for a in ("-Xlinker", f"--wrap={w}")]], check=True)
