@@ -321,13 +321,16 @@ int resident_clusters(int s) {
     return n;
 }
 
-// Blocks of a cluster: as many as there are places for, each with four stages or more of the longer sum.
+// Blocks of a cluster: as many as there are places for, each with four stages or more of the longer sum. Not seven, though: one
+// row, 37 and 38 tiles of 8192 summed take 17.1 and 17.4 us in sevens, 16.5 and 16.7 in sixes, of 4096 10.7 and 11.1 to 10.5 and
+// 10.8; of 1792 to 2048, where four stages a block allow no more than seven, 4 to 39 tiles are the same in both.
 int choose_split(const Job &a, const Job *b, int places) {
     const int64_t tiles = a.tiles + (b ? b->tiles : 0), kb = b && stages_of(*b) > stages_of(a) ? stages_of(*b) : stages_of(a);
     int64_t s = places / tiles;
     if (s > kb / 4) s = kb / 4;
     if (s > 8) s = 8;
     while (s > 1 && resident_clusters((int)s) < tiles) --s;
+    if (s == 7) s = 6;
     return s < 1 ? 1 : (int)s;
 }
 
